@@ -50,7 +50,8 @@ typedef enum {
     W4A16_ERR_MISALIGNED = 3,        /* a pointer is not 16-byte aligned */
     W4A16_ERR_CUDA = 4,              /* the CUDA runtime refused a launch or query */
     W4A16_ERR_DEVICE_TIMEOUT = 5,    /* a kernel gave up a bounded wait (reported by w4a16_device_status) */
-    W4A16_ERR_BOUNDS = 6             /* a kernel index check failed: the debug-bounds build only (see below) */
+    W4A16_ERR_BOUNDS = 6             /* a kernel index check failed: the debug-bounds build (see below), and in every
+                                        build a slot, position or page of a w4a16_kv4 call that does not exist */
 } w4a16_status;
 
 /* Which kernel family runs a GEMM. */
@@ -276,6 +277,109 @@ int w4a16_quantize_gemm_w4a8(const uint16_t* x, int8_t* xq, uint16_t* xq_f16, fl
 
 /* The automatic plan of w4a16_gemm_w4a8 for this shape (host only). */
 int w4a16_plan_for_w4a8(int M, int N, int K, int group, w4a16_plan* out);
+
+/*
+ * ---- Between the qkv product and the output projection: the key/value cache in 4 bits.
+ *
+ * (The pages' full-attention layers keep their keys and values in a paged pool, 4 key/value heads of
+ * 256 ("Qwen3.8-27B at 764, 1,035 and 1,623 tok/s", section "What one more stream costs"); 4-bit values
+ * are named there for one engine, without a format. The format below is this library's own.)
+ *
+ * A cache holds num_pages pages of page_tokens tokens, each with kv_heads keys and values of head_dim
+ * elements. A token's place is its slot, page * page_tokens + offset; a sequence's tokens lie in the
+ * pages that its row of a block table names. Per 64 consecutive elements of a key or value, in binary32:
+ *   scale = fp16_rne((max - min) / 15), code = rne((x - min) / scale) in 0..15 (0 where scale is 0),
+ *   and the stored value is x' = min + code * scale (min is one of the fp16 x).
+ * 0.5625 bytes an element. The order of the bytes is opaque; w4a16_kv4_append writes it,
+ * w4a16_kv4_load and w4a16_kv4_attention read it. Nothing is read from slots that were never written,
+ * beyond bytes that are then discarded: the pages need no initialisation.
+ *
+ * Supported: head_dim 64, 128, 256; page_tokens a power of two, 16..4096; num_pages * page_tokens < 2^31;
+ * kv_heads <= 256; heads (of queries) a multiple of kv_heads, heads <= 1024; pages 16-byte aligned.
+ */
+typedef struct {
+    void* pages;     /* device memory, w4a16_kv4_cache_bytes */
+    int num_pages;
+    int page_tokens;
+    int kv_heads;
+    int head_dim;
+} w4a16_kv4_cache;
+
+/* Bytes of the pages; 0 for an unsupported shape. */
+size_t w4a16_kv4_cache_bytes(int num_pages, int page_tokens, int kv_heads, int head_dim);
+
+/*
+ * One pass over the rows of a fused qkv product: norms and rotation of each head, queries written out,
+ * keys and values stored in the cache.
+ *   qkv:       fp16 [M] rows of (heads + 2 kv_heads) * head_dim elements (query, key, value heads), rows
+ *              qkv_stride elements apart (a multiple of 8)
+ *   q_out:     fp16 [M][heads][head_dim], written in full; NULL when heads is 0 (rows of keys and values)
+ *   slots:     int32 [M]; a negative slot stores nothing (a padding row); no slot twice
+ *   positions: int32 [M], rows of the rotation table; NULL when rope is NULL
+ *   rope:      fp32 [rope_positions][rot]: rot/2 cosines, then rot/2 sines; NULL: no rotation. The first
+ *              rot elements of each query and key head are rotated, in pairs (i, i + rot/2), or
+ *              (2i, 2i + 1) when adjacent is 1. rot % 16 == 0, rot <= head_dim.
+ *   q_norm, k_norm: fp16 [head_dim], or NULL for none: y = (x * (1 / sqrt(mean(x^2) + eps))) * w before
+ *              the rotation. Values are not normed or rotated.
+ * Queries and keys are rounded once to fp16, after the rotation; the code of a key is decided on that.
+ * All of it is defined to the bit (binary32, no fused multiply-add, squares added 8 neighbours in turn
+ * and then in pairs of neighbouring sums). x must be finite. A position outside the table makes the row's
+ * queries 0 and stores nothing, a slot outside the cache stores nothing; both set W4A16_ERR_BOUNDS in the
+ * device status word. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA.
+ */
+int w4a16_kv4_append(const uint16_t* qkv, int64_t qkv_stride, int heads, uint16_t* q_out, const w4a16_kv4_cache* cache,
+                     const int32_t* slots, const int32_t* positions, const float* rope, int rope_positions, int rot,
+                     int adjacent, const uint16_t* q_norm, const uint16_t* k_norm, float eps, int M, void* stream);
+
+/* The stored values of n slots: k, v fp16 [n][kv_heads][head_dim], fp16_rne(min + code * scale). A
+ * negative slot gives zeros; so does one outside the cache, with W4A16_ERR_BOUNDS in the status word. */
+int w4a16_kv4_load(const w4a16_kv4_cache* cache, const int32_t* slots, uint16_t* k, uint16_t* v, int n, void* stream);
+
+/* Bytes of device memory that w4a16_kv4_attention needs beside its operands, the same for every batch;
+ * 0 for an unsupported head size. To be zeroed once, before its first use; every call leaves it ready
+ * for the next. Calls that may run at the same time need one each. */
+size_t w4a16_kv4_attention_workspace_bytes(int head_dim);
+
+/*
+ * out = softmax(scale * q . k'^T) . v' over the cached tokens of each sequence, k' and v' unrounded.
+ *   q:           fp16 [M][heads][head_dim], rows q_stride elements apart (a multiple of 8); head h
+ *                attends with key/value head h / (heads / kv_heads)
+ *   block_table: int32 [B][max_pages], page j of sequence b holds its tokens j * page_tokens and on
+ *   kv_len:      int32 [B], cached tokens of each sequence (0 is allowed)
+ *   q_start:     int32 [B + 1], not decreasing, within 0..M: sequence b's queries are rows
+ *                q_start[b] .. q_start[b+1]-1 of q, and, when causal is 1, the last of its cached tokens:
+ *                query i of n sees tokens 0 .. kv_len - n + i. When causal is 0 it sees all kv_len.
+ *   max_q_len:   an upper bound of q_start[b+1] - q_start[b] (it chooses the kernel, not the result)
+ *   out:         fp16 [M][heads][head_dim]; rows of no sequence are left as they are
+ *   lse:         NULL, or fp32 [M][heads]: log(sum(exp(scale q k'))) (-inf for a query that sees nothing)
+ * A query that sees no token gives 0. All lengths are read on the device: a captured graph may be
+ * replayed with other contents. fp32 scores, softmax and sums; repeats are bit-identical. A page outside
+ * the cache, a kv_len or q_start outside its range is cut off (its tokens are not seen) and sets
+ * W4A16_ERR_BOUNDS in the device status word. B, M <= 2^20. Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
+ * MISALIGNED, CUDA.
+ */
+int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4a16_kv4_cache* cache,
+                        const int32_t* block_table, int max_pages, const int32_t* kv_len, const int32_t* q_start,
+                        int B, int M, int max_q_len, int causal, float scale, uint16_t* out, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---- After the output head: one token per row of fp16 logits, by a given uniform random number.
+ * Tokens in the order of their logits, ties by lower index; NaN and -inf are never chosen.
+ *   w = exp((l - l_max) / T) in binary32 (1 where l = l_max), W = rne(2^40 w), masses are sums of W
+ *   kept: the first top_k (all where top_k <= 0); of those, a token whose preceding mass is below
+ *         floor(floor(2^24 top_p) * mass / 2^24) (all where top_p >= 1); with w >= min_p (all where
+ *         min_p <= 0); the first token always
+ *   the token is the first kept one whose running mass exceeds floor(floor(2^24 u) * kept mass / 2^24).
+ * temperature <= 0: the first token. A row with nothing but masked logits gives token -1.
+ *   logits: fp16 [M] rows of V, stride elements apart (2-byte aligned: any part of a wider row)
+ *   temperature, top_p, min_p, u: fp32 [M]; top_k: int32 [M] (device). All but u may be NULL (1, all,
+ *           1, 0).
+ *   tokens: int32 [M]; probs: fp32 [M] or NULL, the probability with which the token was chosen.
+ * V <= 1,000,000, M <= 65,536. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA.
+ */
+int w4a16_sample(const uint16_t* logits, int64_t stride, int M, int V, const float* temperature, const int32_t* top_k,
+                 const float* top_p, const float* min_p, const float* u, int32_t* tokens, float* probs, void* stream);
 
 /* Describes the last GEMM this process launched (path, tile, split, grid) into buf (NUL
  * terminated, truncated to len). Host only. Returns W4A16_OK or INVALID_ARG. */

@@ -1,0 +1,391 @@
+"""The paged 4-bit cache on the GPU: append and load bit for bit against a binary32 statement, attention
+against 64 bits under a bound derived from its roundings, and what may go wrong around both: pages that
+end inside a tile, empty sequences and rows, rows beyond the length, unwritten memory, padding rows,
+places that do not exist, other streams, graphs, long offsets."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import kv4_ref as ref
+from gpu_util import lib
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def W():
+    return lib()
+
+
+def cuda(x, dtype=None):
+    return torch.from_numpy(np.ascontiguousarray(x)).cuda() if dtype is None else torch.tensor(x, dtype=dtype).cuda()
+
+
+def ok(W):
+    torch.cuda.synchronize()
+    st = W.w4a16_device_status()
+    assert st == W.OK, W.status_string(st)
+
+
+def table(positions, rot):
+    a = np.arange(positions)[:, None] * (1.0 / 10000.0 ** (np.arange(0, rot, 2) / rot))[None, :]
+    return np.concatenate([np.cos(a), np.sin(a)], axis=1).astype(np.float32)
+
+
+def awkward(rng, M, heads, D):
+    """Rows as a product gives them, and rows where storage can go wrong."""
+    x = (rng.normal(size=(M, heads, D)) * np.exp(0.7 * rng.normal(size=(heads, D)))).astype(np.float16)
+    x[0, -1] = 0                                                   # nothing to scale
+    x[0, 0, :64] = np.float16(3.25)                                # one value
+    x[-1, -1, :64] = (np.arange(64) % 16 - 5).astype(np.float16)    # exact codes
+    x[-1, 0, :64] = (np.arange(64) % 31 / 2).astype(np.float16)     # ties
+    x[M // 2, -1, -64:] = np.float16(6e-8)                         # subnormal
+    x[M // 2, -1, -1] = np.float16(-6e-8)
+    x[M // 2, 0, 5] = np.float16(30000)                            # one large element
+    return x.reshape(M, heads * D)
+
+
+APPEND = [(1, 20, 4, 256, 64, False, True, 16), (3, 40, 8, 128, 128, True, False, 32), (65, 8, 8, 64, 32, False, True, 64),
+          (17, 6, 2, 128, 48, False, True, 16), (5, 3, 1, 256, 256, True, True, 4096), (130, 5, 1, 64, 0, False, False, 16),
+          (33, 2, 2, 256, 16, True, False, 128)]
+
+
+@pytest.mark.parametrize("M,H,KV,D,rot,adjacent,normed,page", APPEND)
+def test_append_and_load_match_the_definition_bit_for_bit(W, M, H, KV, D, rot, adjacent, normed, page):
+    rng = np.random.default_rng(M * 1000 + D + rot)
+    qkv = awkward(rng, M, H + 2 * KV, D)
+    pad = 24
+    wide = np.full((M, qkv.shape[1] + pad), np.nan, np.float16)  # rows of a wider buffer
+    wide[:, :qkv.shape[1]] = qkv
+    pages = M // page + 3
+    cache = W.KV4Cache(pages, page, KV, D)
+    cache.pages.fill_(0xFF)
+    slots = rng.permutation(pages * page)[:M].astype(np.int32)
+    pos = rng.integers(0, 500, M).astype(np.int32)
+    rope = table(500, rot) if rot else None
+    qn = (1 + 0.3 * rng.normal(size=D)).astype(np.float16) if normed else None
+    kn = (1 + 0.3 * rng.normal(size=D)).astype(np.float16) if normed else None
+    q = W.kv4_append(cuda(wide)[:, :qkv.shape[1]], cache, cuda(slots), heads=H,
+                     positions=cuda(pos) if rot else None, rope=cuda(rope) if rot else None, adjacent=adjacent,
+                     q_norm=cuda(qn) if normed else None, k_norm=cuda(kn) if normed else None, eps=1e-5)
+    k, v = W.kv4_load(cache, cuda(slots))
+    ok(W)
+    qr, kr, vr = ref.append(qkv, H, KV, D, rope, pos, adjacent, qn, kn, 1e-5)
+    assert np.array_equal(q.cpu().numpy().view(np.uint16) & 0x7FFF, qr.view(np.uint16) & 0x7FFF)
+    assert np.array_equal(q.cpu().numpy(), qr)  # (signs of zero aside)
+    assert np.array_equal(k.cpu().numpy(), kr.astype(np.float32).astype(np.float16))
+    assert np.array_equal(v.cpu().numpy(), vr.astype(np.float32).astype(np.float16))
+
+
+def test_append_keys_and_values_alone(W):
+    rng = np.random.default_rng(5)
+    kv = awkward(rng, 9, 6, 128)
+    cache = W.KV4Cache(2, 16, 3, 128)
+    slots = cuda(np.arange(9, dtype=np.int32) + 12)  # across a page's end
+    assert W.kv4_append(cuda(kv), cache, slots, heads=0) is None
+    k, v = W.kv4_load(cache, slots)
+    ok(W)
+    _, kr, vr = ref.append(kv, 0, 3, 128)
+    assert np.array_equal(k.cpu().numpy(), kr.astype(np.float16)) and np.array_equal(v.cpu().numpy(), vr.astype(np.float16))
+
+
+def test_append_leaves_other_tokens_alone_and_skips_padding(W):
+    rng = np.random.default_rng(6)
+    a, b = awkward(rng, 32, 4, 64), awkward(rng, 5, 4, 64)
+    cache = W.KV4Cache(2, 16, 2, 64)
+    every = cuda(np.arange(32, dtype=np.int32))
+    W.kv4_append(cuda(a), cache, every, heads=0)
+    W.kv4_append(cuda(b), cache, cuda(np.array([3, -1, 16, -5, 31], np.int32)), heads=0)
+    k, v = W.kv4_load(cache, every)
+    nothing = W.kv4_load(cache, cuda(np.array([-1, -7], np.int32)))
+    ok(W)
+    a[[3, 16, 31]] = b[[0, 2, 4]]
+    _, kr, vr = ref.append(a, 0, 2, 64)
+    assert np.array_equal(k.cpu().numpy(), kr.astype(np.float16)) and np.array_equal(v.cpu().numpy(), vr.astype(np.float16))
+    assert all(int(t.abs().sum()) == 0 for t in nothing)
+
+
+def test_places_that_do_not_exist_are_reported_and_store_nothing(W):
+    rng = np.random.default_rng(7)
+    x = awkward(rng, 3, 4, 64)
+    cache = W.KV4Cache(2, 16, 1, 64)
+    every = cuda(np.arange(32, dtype=np.int32))
+    W.kv4_append(cuda(awkward(rng, 32, 2, 64)), cache, every, heads=0)
+    before = cache.pages.clone()
+    rope = cuda(table(10, 32))
+    good = cuda(np.array([1, 2, 3], np.int32))
+    W.kv4_append(cuda(x), cache, cuda(np.array([32, 2 ** 31 - 1, -1], np.int32)), heads=2)
+    torch.cuda.synchronize()
+    assert W.w4a16_device_status() == W.ERR_BOUNDS and torch.equal(cache.pages, before)
+    q = W.kv4_append(cuda(x), cache, good, heads=2, rope=rope, positions=cuda(np.array([10, -1, 2 ** 31 - 1], np.int32)))
+    torch.cuda.synchronize()
+    assert W.w4a16_device_status() == W.ERR_BOUNDS and torch.equal(cache.pages, before)
+    assert int(q.abs().sum()) == 0
+    k, v = W.kv4_load(cache, cuda(np.array([32, 2 ** 31 - 1], np.int32)))
+    torch.cuda.synchronize()
+    assert W.w4a16_device_status() == W.ERR_BOUNDS and int(k.abs().sum()) == 0 and int(v.abs().sum()) == 0
+    ok(W)  # taken: the next call starts clean
+
+
+# ------------------------------------------------------------------------------------ attention
+class Batch:
+    """Sequences of given lengths in pages of random order; memory that no token was written to holds NaN
+    parameters."""
+
+    def __init__(self, W, seed, lens, q_lens, H, KV, D, page, spare=2, gain=1.0):
+        rng = np.random.default_rng(seed)
+        need = [-(-n // page) for n in lens]
+        self.cache = W.KV4Cache(sum(need) + spare, page, KV, D)
+        self.cache.pages.fill_(0xFF)
+        order = rng.permutation(sum(need) + spare)
+        self.table = np.full((len(lens), max(max(need), 1)), -1, np.int32)
+        self.keys, self.values, at = [], [], 0
+        for b, n in enumerate(lens):
+            self.table[b, :need[b]] = order[at:at + need[b]]
+            at += need[b]
+            k = (rng.normal(size=(n, KV, D)) * np.exp(0.3 * rng.normal(size=(KV, D)))).astype(np.float16)
+            v = (gain * (rng.normal(size=(n, KV, D)) + rng.normal(size=(KV, D)))).astype(np.float16)
+            self.keys.append(ref.store(k))
+            self.values.append(ref.store(v))
+            if n:
+                t = np.arange(n)
+                slots = self.table[b, t // page] * page + t % page
+                W.kv4_append(cuda(np.concatenate([k, v], axis=1).reshape(n, -1)), self.cache,
+                             cuda(slots.astype(np.int32)), heads=0)
+        self.q_lens, self.lens = q_lens, lens
+        self.q = (1.5 * rng.normal(size=(sum(q_lens), H, D))).astype(np.float16)
+        self.start = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+        self.work = W.kv4_attention_workspace(self.cache)
+
+    def args(self):
+        return dict(block_table=cuda(self.table), kv_len=cuda(np.array(self.lens, np.int32)), q_start=cuda(self.start),
+                    max_q_len=max(1, max(self.q_lens)), workspace=self.work)
+
+    def want(self, scale, causal=True):
+        return ref.attention(self.q, self.keys, self.values, self.q_lens, scale, causal)
+
+
+def close(got, want, bound, what=""):
+    err = np.abs(got.float().cpu().numpy().astype(np.float64) - want)
+    assert np.isfinite(err).all(), f"{what}: not finite"
+    worst = float((err / np.maximum(bound, 1e-30)).max())
+    assert (err <= bound).all(), f"{what}: worst error / bound {worst:.3f}"
+    return worst
+
+
+ATTENTION = [
+    # lens, q_lens, H, KV, D, page
+    ([1], [1], 20, 4, 256, 16),
+    ([777], [1], 20, 4, 256, 16),
+    ([15, 16, 17, 0, 1, 33], [1, 1, 1, 1, 1, 1], 8, 8, 64, 16),
+    ([64, 65, 300, 2], [1, 1, 1, 1], 40, 8, 128, 64),
+    ([130, 31, 16], [3, 16, 16], 10, 2, 256, 32),
+    ([40, 3, 0, 100], [7, 5, 2, 0], 9, 3, 128, 16),          # more queries than tokens: rows that see nothing
+    ([513], [2], 16, 1, 128, 128),                           # 16 query heads on one key head
+    ([200, 90], [33, 70], 5, 1, 256, 64),
+    ([260, 400], [129, 31], 14, 2, 64, 16),
+    ([350], [200], 4, 2, 128, 4096),                         # a page longer than the sequence
+    ([2500], [1], 24, 4, 256, 32),
+    ([700], [150], 20, 4, 256, 64),
+]
+
+
+@pytest.mark.parametrize("lens,q_lens,H,KV,D,page", ATTENTION, ids=[f"case{i}" for i in range(len(ATTENTION))])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_matches_64_bits(W, lens, q_lens, H, KV, D, page, causal):
+    b = Batch(W, len(lens) * 100 + D + page, lens, q_lens, H, KV, D, page)
+    lse = torch.full((sum(q_lens), H), 7.0, device="cuda")
+    out = W.kv4_attention(cuda(b.q), b.cache, lse=lse, causal=causal, **b.args())
+    ok(W)
+    want, want_lse, bound = b.want(D ** -0.5, causal)
+    close(out, want, bound)
+    got = lse.cpu().numpy().astype(np.float64)
+    empty = np.isneginf(want_lse)
+    assert np.array_equal(np.isneginf(got), empty)
+    # an absolute error of the scores is one of their logarithm: at most 2^-11 sum|q k'| scale + 2^-18
+    tol = 2.0 ** -11 * D ** -0.5 * 6.0 * np.abs(b.q.astype(np.float64)).sum(-1) + 2.0 ** -18
+    assert (np.abs(got[~empty] - want_lse[~empty]) <= tol[~empty]).all()
+    assert int(b.work[:256].sum()) == 0  # the workspace is ready for the next call
+
+
+def test_attention_with_rows_of_a_wider_buffer_and_another_scale(W):
+    b = Batch(W, 11, [90, 20], [4, 1], 6, 2, 128, 16)
+    wide = np.full((5, 6 * 128 + 40), np.nan, np.float16)
+    wide[:, :768] = b.q.reshape(5, -1)
+    out = W.kv4_attention(cuda(wide)[:, :768].unflatten(1, (6, 128)), b.cache, scale=0.3, **b.args())
+    ok(W)
+    want, _, bound = b.want(0.3)
+    close(out, want, bound)
+
+
+@pytest.mark.parametrize("gain", [1e-4, 300.0])
+def test_attention_of_small_and_large_values(W, gain):
+    # values near fp16's smallest normal numbers and far above one: products p * scale keep their bits
+    b = Batch(W, 12, [333, 40], [1, 9], 20, 4, 256, 16, gain=gain)
+    out = W.kv4_attention(cuda(b.q), b.cache, **b.args())
+    ok(W)
+    want, _, bound = b.want(1 / 16)
+    close(out, want, bound + 2.0 ** -25)
+
+
+def test_attention_of_one_dominant_token(W):
+    # a key that the query points at: every other weight is below fp16's range of the products
+    b = Batch(W, 13, [400], [1], 4, 4, 64, 16)
+    q = b.q.copy()
+    for h in range(4):
+        q[0, h] = (4 * b.keys[0][170, h]).astype(np.float16)
+    b.q = q
+    out = W.kv4_attention(cuda(q), b.cache, scale=1.0, **b.args())
+    ok(W)
+    want, _, bound = b.want(1.0)
+    close(out, want, bound)
+
+
+def test_attention_of_equal_keys_is_the_mean_of_the_values(W):
+    n, KV, D = 100, 2, 128
+    rng = np.random.default_rng(14)
+    k = np.tile((np.arange(D) % 16).astype(np.float16), (n, KV, 1))
+    v = rng.integers(0, 16, size=(n, KV, D)).astype(np.float16)
+    v[..., 0::64], v[..., 1::64] = 0, 15  # scale 1: values are stored exactly
+    cache = W.KV4Cache(7, 16, KV, D)
+    slots = cuda(np.arange(n, dtype=np.int32))
+    W.kv4_append(cuda(np.concatenate([k, v], axis=1).reshape(n, -1)), cache, slots, heads=0)
+    out = W.kv4_attention(cuda(rng.normal(size=(1, KV, D)).astype(np.float16)), cache, cuda(np.arange(7, dtype=np.int32)[None]),
+                          cuda(np.array([n], np.int32)), cuda(np.array([0, 1], np.int32)), 1, W.kv4_attention_workspace(cache))
+    ok(W)
+    mean = v.astype(np.float64).mean(0)
+    assert (np.abs(out[0].float().cpu().numpy() - mean) <= 2.0 ** -10 * 2 * mean + 1e-6).all()
+
+
+def test_attention_repeats_bit_for_bit_and_on_another_stream(W):
+    b = Batch(W, 15, [3000, 1200, 50], [1, 1, 1], 20, 4, 256, 32)
+    q, args = cuda(b.q), b.args()
+    a = W.kv4_attention(q, b.cache, **args)
+    again = W.kv4_attention(q, b.cache, **args)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = W.kv4_attention(q, b.cache, stream=s, **args)
+    ok(W)
+    assert torch.equal(a.view(torch.int16), again.view(torch.int16))
+    assert torch.equal(a.view(torch.int16), other.view(torch.int16))
+    want, _, bound = b.want(1 / 16)
+    close(a, want, bound)
+
+
+def test_a_captured_step_replays_with_other_lengths(W):
+    H, KV, D, page = 10, 2, 128, 16
+    b = Batch(W, 16, [70, 200], [1, 1], H, KV, D, page)
+    q, args = cuda(b.q), b.args()
+    out = torch.empty((2, H, D), dtype=torch.float16, device="cuda")
+    W.kv4_attention(q, b.cache, out=out, **args)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            W.kv4_attention(q, b.cache, out=out, **args)
+    for lens in ([70, 200], [1, 17], [0, 199]):
+        args["kv_len"].copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        ok(W)
+        want, _, bound = ref.attention(b.q, [k[:n] for k, n in zip(b.keys, lens)], [v[:n] for v, n in zip(b.values, lens)],
+                                       [1, 1], D ** -0.5)
+        close(out, want, bound, str(lens))
+
+
+def test_pages_and_lengths_that_do_not_exist_are_cut_off(W):
+    b = Batch(W, 17, [64, 64], [1, 1], 4, 2, 64, 16)
+    args = b.args()
+    args["kv_len"] = cuda(np.array([64, 1000], np.int32))  # longer than the table's row: its 64 tokens
+    out = W.kv4_attention(cuda(b.q), b.cache, **args)
+    torch.cuda.synchronize()
+    assert W.w4a16_device_status() == W.ERR_BOUNDS
+    want, _, bound = b.want(0.125)
+    close(out, want, bound)
+    for bad in (-1, 10 ** 6):
+        t = b.table.copy()
+        t[0, 2] = bad  # tokens 32..47 of the first sequence
+        args = b.args()
+        args["block_table"] = cuda(t)
+        out = W.kv4_attention(cuda(b.q), b.cache, **args)
+        torch.cuda.synchronize()
+        assert W.w4a16_device_status() == W.ERR_BOUNDS
+        left = np.r_[0:32, 48:64]
+        want, _, bound = ref.attention(b.q, [b.keys[0][left], b.keys[1]], [b.values[0][left], b.values[1]], [1, 1], 0.125)
+        close(out, want, bound)
+    args = b.args()
+    args["q_start"] = cuda(np.array([0, 1, 90], np.int32))  # more rows than q has
+    out = W.kv4_attention(cuda(b.q), b.cache, causal=False, **args)
+    torch.cuda.synchronize()
+    assert W.w4a16_device_status() == W.ERR_BOUNDS
+    want, _, bound = b.want(0.125, causal=False)
+    close(out, want, bound)
+    ok(W)
+
+
+def test_rows_of_no_sequence_are_left_alone(W):
+    b = Batch(W, 18, [20, 30], [2, 2], 4, 2, 64, 16)
+    out = torch.full((4, 4, 64), 5.0, dtype=torch.float16, device="cuda")
+    args = b.args()
+    args["q_start"] = cuda(np.array([1, 2, 3], np.int32))
+    W.kv4_attention(cuda(b.q), b.cache, out=out, **args)
+    ok(W)
+    assert bool((out[0] == 5).all()) and bool((out[3] == 5).all())
+    want, _, bound = ref.attention(b.q[1:3], b.keys, b.values, [1, 1], 0.125)
+    close(out[1:3], want, bound)
+
+
+def test_offsets_beyond_32_bits(W):
+    # the last pages of a cache of 4.8 GB
+    KV, D, page = 4, 256, 64
+    cache = W.KV4Cache(65000, page, KV, D)
+    assert cache.pages.numel() > 2 ** 32
+    rng = np.random.default_rng(19)
+    n = 100
+    x = awkward(rng, n, 2 * KV, D)
+    x = np.clip(x, -20, 20)
+    pages = np.array([[64999, 64990]], np.int32)
+    t = np.arange(n)
+    slots = cuda((pages[0, t // page] * page + t % page).astype(np.int32))
+    W.kv4_append(cuda(x), cache, slots, heads=0)
+    k, v = W.kv4_load(cache, slots)
+    q = rng.normal(size=(1, KV, D)).astype(np.float16)
+    out = W.kv4_attention(cuda(q), cache, cuda(pages), cuda(np.array([n], np.int32)), cuda(np.array([0, 1], np.int32)), 1,
+                          W.kv4_attention_workspace(cache))
+    ok(W)
+    _, kr, vr = ref.append(x, 0, KV, D)
+    assert np.array_equal(k.cpu().numpy(), kr.astype(np.float32).astype(np.float16))
+    assert np.array_equal(v.cpu().numpy(), vr.astype(np.float32).astype(np.float16))
+    want, _, bound = ref.attention(q, [kr], [vr], [1], 1 / 16)
+    close(out, want, bound)
+
+
+def test_the_index_checking_build_runs_clean(W):
+    import ctypes
+
+    D_ = W.load_debug_bounds()
+    b = Batch(W, 20, [100, 17, 0], [1, 20, 1], 6, 2, 128, 16)
+    s = torch.cuda.current_stream().cuda_stream
+    args = b.args()
+    q = cuda(b.q)
+    out = torch.empty_like(q)
+    assert D_.w4a16_kv4_attention(q.data_ptr(), q.stride(0), 6, ctypes.byref(b.cache.desc), args["block_table"].data_ptr(),
+                                  args["block_table"].shape[1], args["kv_len"].data_ptr(), args["q_start"].data_ptr(), 3, 22,
+                                  20, 1, 128 ** -0.5, out.data_ptr(), None, b.work.data_ptr(), b.work.numel(), s) == 0
+    x = cuda(awkward(np.random.default_rng(3), 4, 10, 128))
+    cache = W.KV4Cache(1, 16, 2, 128)
+    slots = cuda(np.array([15, 0, 3, 8], np.int32))
+    qq = torch.empty((4, 6, 128), dtype=torch.float16, device="cuda")
+    kv = torch.empty((2, 4, 2, 128), dtype=torch.float16, device="cuda")
+    assert D_.w4a16_kv4_append(x.data_ptr(), 1280, 6, qq.data_ptr(), ctypes.byref(cache.desc), slots.data_ptr(), None, None,
+                               0, 0, 0, None, None, 0.0, 4, s) == 0
+    assert D_.w4a16_kv4_load(ctypes.byref(cache.desc), slots.data_ptr(), kv[0].data_ptr(), kv[1].data_ptr(), 4, s) == 0
+    torch.cuda.synchronize()
+    assert D_.w4a16_device_status(s) == W.OK
+    normal = W.kv4_attention(q, b.cache, **args)
+    k, v = W.kv4_load(cache, slots)
+    ok(W)
+    assert torch.equal(out.view(torch.int16), normal.view(torch.int16))
+    assert torch.equal(kv[0], k) and torch.equal(kv[1], v)

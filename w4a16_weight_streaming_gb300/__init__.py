@@ -40,7 +40,8 @@ EXPORTED = [
     "w4a16_silu_mul", "w4a16_debug_bounds", "w4a16_repacked_nvfp4_scales_bytes", "w4a16_repack_nvfp4",
     "w4a16_unrepack_nvfp4", "w4a16_gemm_nvfp4", "w4a16_gemm_nvfp4_ex", "w4a16_plan_for_nvfp4",
     "w4a16_quantize_x_int8", "w4a16_gemm_w4a8", "w4a16_gemm_w4a8_ex", "w4a16_plan_for_w4a8",
-    "w4a16_quantize_gemm_w4a8",
+    "w4a16_quantize_gemm_w4a8", "w4a16_kv4_cache_bytes", "w4a16_kv4_append", "w4a16_kv4_load",
+    "w4a16_kv4_attention_workspace_bytes", "w4a16_kv4_attention", "w4a16_sample",
 ]
 
 
@@ -54,6 +55,13 @@ class Plan(ctypes.Structure):
 
     def as_dict(self):
         return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class KV4Desc(ctypes.Structure):
+    """Mirror of ``w4a16_kv4_cache``: the pages' address and the cache's shape."""
+
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_tokens", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
 
 
 class W4A16Error(RuntimeError):
@@ -117,6 +125,19 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.w4a16_quantize_gemm_w4a8.argtypes = [P, P, P, P, P, P, P, I, I, I, I, ctypes.POINTER(Plan), P]
     lib.w4a16_plan_for_w4a8.restype = I
     lib.w4a16_plan_for_w4a8.argtypes = [I, I, I, I, ctypes.POINTER(Plan)]
+    L, C = ctypes.c_int64, ctypes.POINTER(KV4Desc)
+    lib.w4a16_kv4_cache_bytes.restype = S
+    lib.w4a16_kv4_cache_bytes.argtypes = [I, I, I, I]
+    lib.w4a16_kv4_append.restype = I
+    lib.w4a16_kv4_append.argtypes = [P, L, I, P, C, P, P, P, I, I, I, P, P, F, I, P]
+    lib.w4a16_kv4_load.restype = I
+    lib.w4a16_kv4_load.argtypes = [C, P, P, P, I, P]
+    lib.w4a16_kv4_attention_workspace_bytes.restype = S
+    lib.w4a16_kv4_attention_workspace_bytes.argtypes = [I]
+    lib.w4a16_kv4_attention.restype = I
+    lib.w4a16_kv4_attention.argtypes = [P, L, I, C, P, I, P, P, I, I, I, I, F, P, P, P, S, P]
+    lib.w4a16_sample.restype = I
+    lib.w4a16_sample.argtypes = [P, L, I, I, P, P, P, P, P, P, P, P]
     return lib
 
 
@@ -411,3 +432,168 @@ def quantize_gemm_w4a8(x: torch.Tensor, qweight_r: torch.Tensor, scales_r: torch
                                     sx.data_ptr(), qweight_r.data_ptr(), scales_r.data_ptr(), y.data_ptr(), M, N, K,
                                     group, plan, _stream_handle(stream)), "w4a16_quantize_gemm_w4a8")
     return y, out
+
+
+# ------------------------------------------------------------------------------ 4-bit paged key/value cache
+def w4a16_kv4_cache_bytes(num_pages: int, page_tokens: int, kv_heads: int, head_dim: int) -> int:
+    return lib.w4a16_kv4_cache_bytes(num_pages, page_tokens, kv_heads, head_dim)
+
+
+def w4a16_kv4_append(qkv: int, qkv_stride: int, heads: int, q_out: int | None, cache: KV4Desc, slots: int,
+                     positions: int | None, rope: int | None, rope_positions: int, rot: int, adjacent: int,
+                     q_norm: int | None, k_norm: int | None, eps: float, M: int, stream: int | None) -> int:
+    return lib.w4a16_kv4_append(qkv, qkv_stride, heads, q_out, ctypes.byref(cache), slots, positions, rope,
+                                rope_positions, rot, adjacent, q_norm, k_norm, eps, M, stream)
+
+
+def w4a16_kv4_load(cache: KV4Desc, slots: int, k: int, v: int, n: int, stream: int | None) -> int:
+    return lib.w4a16_kv4_load(ctypes.byref(cache), slots, k, v, n, stream)
+
+
+def w4a16_kv4_attention_workspace_bytes(head_dim: int) -> int:
+    return lib.w4a16_kv4_attention_workspace_bytes(head_dim)
+
+
+def w4a16_kv4_attention(q: int, q_stride: int, heads: int, cache: KV4Desc, block_table: int, max_pages: int,
+                        kv_len: int, q_start: int, B: int, M: int, max_q_len: int, causal: int, scale: float,
+                        out: int, lse: int | None, workspace: int, workspace_bytes: int, stream: int | None) -> int:
+    return lib.w4a16_kv4_attention(q, q_stride, heads, ctypes.byref(cache), block_table, max_pages, kv_len, q_start,
+                                   B, M, max_q_len, causal, scale, out, lse, workspace, workspace_bytes, stream)
+
+
+def w4a16_sample(logits: int, stride: int, M: int, V: int, temperature: int | None, top_k: int | None,
+                 top_p: int | None, min_p: int | None, u: int, tokens: int, probs: int | None,
+                 stream: int | None) -> int:
+    return lib.w4a16_sample(logits, stride, M, V, temperature, top_k, top_p, min_p, u, tokens, probs, stream)
+
+
+def _ptr(t: torch.Tensor | None) -> int | None:
+    return t.data_ptr() if t is not None else None
+
+
+def _want(where: str, **tensors):
+    """Every given tensor on the GPU, of the dtype and shape asked for (None in the shape: any), rows dense."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda or t.dtype != dtype or t.dim() != len(shape) or \
+                any(want is not None and have != want for have, want in zip(t.shape, shape)):
+            raise ValueError(f"{where}: {name} must be a CUDA {dtype} tensor of shape "
+                             f"{tuple('any' if s is None else s for s in shape)}, not {t.dtype} {tuple(t.shape)}")
+        step = 1
+        for i in range(t.dim() - 1, 0, -1):
+            if t.shape[i] != 1 and t.stride(i) != step:
+                raise ValueError(f"{where}: {name} must be contiguous within a row")
+            step *= t.shape[i]
+        if t.dim() == 1 and t.shape[0] > 1 and t.stride(0) != 1:
+            raise ValueError(f"{where}: {name} must be contiguous")
+
+
+def _dense(where: str, **tensors):
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+
+
+class KV4Cache:
+    """Keys and values in 4 bits (0.5625 bytes an element), in pages of `page_tokens` tokens. A token's
+    slot is page * page_tokens + its offset in the page; which pages a sequence has is the caller's."""
+
+    def __init__(self, num_pages: int, page_tokens: int, kv_heads: int, head_dim: int, device="cuda"):
+        n = w4a16_kv4_cache_bytes(num_pages, page_tokens, kv_heads, head_dim)
+        if n == 0:
+            raise W4A16Error(ERR_UNSUPPORTED_SHAPE, "KV4Cache")
+        self.num_pages, self.page_tokens, self.kv_heads, self.head_dim = num_pages, page_tokens, kv_heads, head_dim
+        self.pages = torch.empty(n, dtype=torch.uint8, device=device)
+        self.desc = KV4Desc(self.pages.data_ptr(), num_pages, page_tokens, kv_heads, head_dim)
+
+
+def kv4_append(qkv: torch.Tensor, cache: KV4Cache, slots: torch.Tensor, heads: int, positions=None, rope=None,
+               adjacent: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6, q: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor | None:
+    """Norms and rotation of the heads of qkv [M, (heads + 2 kv_heads) head_dim] (float16), keys and values
+    stored at `slots` (int32 [M], negative: not stored); returns the queries [M, heads, head_dim] (None for
+    heads = 0). rope float32 [positions, rot]: rot/2 cosines, rot/2 sines; positions int32 [M]."""
+    M, D = qkv.shape[0], cache.head_dim
+    _want("kv4_append", qkv=(qkv, torch.float16, (None, (heads + 2 * cache.kv_heads) * D)),
+          slots=(slots, torch.int32, (M,)), positions=(positions, torch.int32, (M,)),
+          rope=(rope, torch.float32, (None, None)), q_norm=(q_norm, torch.float16, (D,)),
+          k_norm=(k_norm, torch.float16, (D,)), q=(q, torch.float16, (M, heads, D)))
+    _dense("kv4_append", rope=rope, q=q)
+    if q is None and heads > 0:
+        with torch.cuda.stream(stream):
+            q = torch.empty((M, heads, D), dtype=torch.float16, device=qkv.device)
+    _check(w4a16_kv4_append(qkv.data_ptr(), qkv.stride(0), heads, _ptr(q) if heads > 0 else None, cache.desc,
+                            slots.data_ptr(), _ptr(positions), _ptr(rope), rope.shape[0] if rope is not None else 0,
+                            rope.shape[1] if rope is not None else 0, int(adjacent), _ptr(q_norm), _ptr(k_norm), eps,
+                            M, _stream_handle(stream)), "w4a16_kv4_append")
+    return q if heads > 0 else None
+
+
+def kv4_load(cache: KV4Cache, slots: torch.Tensor, out=None, stream=None):
+    """The stored values at `slots` (int32 [n]): keys and values, float16 [n, kv_heads, head_dim] each."""
+    n = slots.shape[0]
+    shape = (n, cache.kv_heads, cache.head_dim)
+    if out is None:
+        with torch.cuda.stream(stream):
+            out = (torch.empty(shape, dtype=torch.float16, device=slots.device),
+                   torch.empty(shape, dtype=torch.float16, device=slots.device))
+    k, v = out
+    _want("kv4_load", slots=(slots, torch.int32, (n,)), k=(k, torch.float16, shape), v=(v, torch.float16, shape))
+    _dense("kv4_load", k=k, v=v)
+    _check(w4a16_kv4_load(cache.desc, slots.data_ptr(), k.data_ptr(), v.data_ptr(), n, _stream_handle(stream)),
+           "w4a16_kv4_load")
+    return k, v
+
+
+def kv4_attention_workspace(cache: KV4Cache) -> torch.Tensor:
+    """Device memory for kv4_attention calls on `cache` (or on any cache of its head size) that follow one
+    another on one stream; calls that may overlap need one each."""
+    return torch.zeros(w4a16_kv4_attention_workspace_bytes(cache.head_dim), dtype=torch.uint8,
+                       device=cache.pages.device)
+
+
+def kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, kv_len: torch.Tensor,
+                  q_start: torch.Tensor, max_q_len: int, workspace: torch.Tensor, scale: float | None = None,
+                  causal: bool = True, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """Attention of q [M, heads, head_dim] (float16) over the cached tokens of B sequences: block_table
+    int32 [B, pages], kv_len int32 [B], q_start int32 [B + 1] (sequence b's rows of q). Queries are the last
+    tokens of their sequence (causal) or see all of them. scale: 1 / sqrt(head_dim) when None."""
+    M, heads, D = q.shape
+    B = kv_len.shape[0]
+    _want("kv4_attention", q=(q, torch.float16, (None, None, cache.head_dim)),
+          block_table=(block_table, torch.int32, (B, None)), kv_len=(kv_len, torch.int32, (B,)),
+          q_start=(q_start, torch.int32, (B + 1,)), workspace=(workspace, torch.uint8, (None,)),
+          out=(out, torch.float16, (M, heads, D)), lse=(lse, torch.float32, (M, heads)))
+    _dense("kv4_attention", block_table=block_table, out=out, lse=lse)
+    if out is None:
+        with torch.cuda.stream(stream):
+            out = torch.empty((M, heads, D), dtype=torch.float16, device=q.device)
+    _check(w4a16_kv4_attention(q.data_ptr(), q.stride(0), heads, cache.desc, block_table.data_ptr(),
+                               block_table.shape[1], kv_len.data_ptr(), q_start.data_ptr(), B, M, max_q_len,
+                               int(causal), D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse),
+                               workspace.data_ptr(), workspace.numel(), _stream_handle(stream)),
+           "w4a16_kv4_attention")
+    return out
+
+
+# ------------------------------------------------------------------------------ sampling
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None, out=None,
+           stream=None):
+    """One token per row of logits [M, V] (float16, rows of any stride) by the uniform numbers u [M]:
+    (tokens int32 [M], probs float32 [M]). temperature, top_p, min_p float32 [M], top_k int32 [M], or None."""
+    M, V = logits.shape
+    if out is None:
+        with torch.cuda.stream(stream):
+            out = (torch.empty(M, dtype=torch.int32, device=logits.device),
+                   torch.empty(M, dtype=torch.float32, device=logits.device))
+    tokens, probs = out
+    f = torch.float32
+    _want("sample", logits=(logits, torch.float16, (None, None)), u=(u, f, (M,)), temperature=(temperature, f, (M,)),
+          top_k=(top_k, torch.int32, (M,)), top_p=(top_p, f, (M,)), min_p=(min_p, f, (M,)),
+          tokens=(tokens, torch.int32, (M,)), probs=(probs, f, (M,)))
+    _check(w4a16_sample(logits.data_ptr(), logits.stride(0), M, V, _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                        _ptr(min_p), u.data_ptr(), tokens.data_ptr(), _ptr(probs), _stream_handle(stream)),
+           "w4a16_sample")
+    return tokens, probs

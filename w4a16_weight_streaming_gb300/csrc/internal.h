@@ -91,4 +91,70 @@ cudaError_t launch_gemv_w4a8(const int8_t* xq, const float* sx, const uint32_t* 
 cudaError_t launch_silu_mul(const uint16_t* gu, uint16_t* act, int M, int I, int sm_count, cudaStream_t s,
                             unsigned* status);
 
+// ---- the paged 4-bit key/value cache (kv4.cu, kv4_attn.cu); mirrors w4a16_kv4_cache.
+struct Kv4Cache {
+    void* pages;
+    int num_pages;
+    int page_tokens;  // a power of two, >= 16
+    int kv_heads;
+    int head_dim;  // 64, 128, 256
+};
+
+struct Kv4AppendParams {
+    const uint16_t* qkv;
+    int64_t qkv_stride;
+    uint16_t* q_out;
+    const int32_t* slots;
+    const int32_t* positions;
+    const float* rope;
+    int rope_positions;
+    int rot;
+    int adjacent;
+    const uint16_t* q_norm;
+    const uint16_t* k_norm;
+    float eps;
+    int M;
+    int heads;
+};
+cudaError_t launch_kv4_append(const Kv4AppendParams& p, const Kv4Cache& c, cudaStream_t s, unsigned* status);
+cudaError_t launch_kv4_load(const Kv4Cache& c, const int32_t* slots, uint16_t* k, uint16_t* v, int n, cudaStream_t s,
+                            unsigned* status);
+
+struct Kv4AttnParams {
+    const uint16_t* q;
+    int64_t q_stride;
+    const int32_t* block_table;
+    const int32_t* kv_len;
+    const int32_t* q_start;
+    uint16_t* out;
+    float* lse;
+    void* workspace;
+    int B;
+    int M;
+    int heads;
+    int max_pages;
+    int max_q_len;
+    int causal;
+    float scale;
+};
+size_t kv4_attention_workspace(int head_dim);  // bytes; the same for every batch
+cudaError_t launch_kv4_attention(const Kv4AttnParams& p, const Kv4Cache& c, int sm_count, cudaStream_t s,
+                                 unsigned* status);
+
+// ---- sample.cu
+struct SampleParams {
+    const uint16_t* logits;
+    int64_t stride;
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    const float* u;
+    int32_t* tokens;
+    float* probs;
+    int M;
+    int V;
+};
+cudaError_t launch_sample(const SampleParams& p, cudaStream_t s, unsigned* status);
+
 }  // namespace w4a16

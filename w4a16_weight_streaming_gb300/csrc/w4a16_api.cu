@@ -615,7 +615,7 @@ int launch_gemm(const Choice& ch, const uint16_t* x, const void* qweight_r, cons
 
 extern "C" {
 
-int w4a16_version(void) { return 300; }
+int w4a16_version(void) { return 400; }
 
 int w4a16_debug_bounds(void) {
 #ifdef W4A16_DEBUG_BOUNDS
@@ -633,7 +633,7 @@ const char* w4a16_status_string(int code) {
         case W4A16_ERR_MISALIGNED: return "W4A16_ERR_MISALIGNED: a pointer is not 16-byte aligned";
         case W4A16_ERR_CUDA: return "W4A16_ERR_CUDA: the CUDA runtime refused the call";
         case W4A16_ERR_DEVICE_TIMEOUT: return "W4A16_ERR_DEVICE_TIMEOUT: a kernel gave up a bounded wait";
-        case W4A16_ERR_BOUNDS: return "W4A16_ERR_BOUNDS: a kernel index check failed (debug-bounds build)";
+        case W4A16_ERR_BOUNDS: return "W4A16_ERR_BOUNDS: a kernel index check failed (debug-bounds build), or a slot, position or page does not exist";
         default: return "W4A16_ERR_UNKNOWN";
     }
 }
@@ -948,6 +948,187 @@ int w4a16_silu_mul(const uint16_t* gu, uint16_t* act, int M, int I, void* stream
         return W4A16_ERR_CUDA;
     }
     return W4A16_OK;
+}
+
+// ---- the 4-bit paged key/value cache
+namespace {
+
+using namespace w4a16;
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int check_kv4_shape(int num_pages, int page_tokens, int kv_heads, int head_dim) {
+    if (num_pages <= 0 || page_tokens <= 0 || kv_heads <= 0 || head_dim <= 0) return W4A16_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (page_tokens < 16 || page_tokens > 4096 || (page_tokens & (page_tokens - 1)) != 0)
+        return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (kv_heads > 256 || static_cast<int64_t>(num_pages) * page_tokens >= (1LL << 31))
+        return W4A16_ERR_UNSUPPORTED_SHAPE;
+    return W4A16_OK;
+}
+
+size_t kv4_bytes(int num_pages, int page_tokens, int kv_heads, int head_dim) {
+    return static_cast<size_t>(num_pages) * page_tokens * kv_heads * head_dim / 8 * 9;
+}
+
+int check_kv4_cache(const w4a16_kv4_cache* c, Kv4Cache* out) {
+    if (!c || !c->pages) return W4A16_ERR_INVALID_ARG;
+    const int rc = check_kv4_shape(c->num_pages, c->page_tokens, c->kv_heads, c->head_dim);
+    if (rc != W4A16_OK) return rc;
+    if (!aligned16(c->pages)) return W4A16_ERR_MISALIGNED;
+    *out = Kv4Cache{c->pages, c->num_pages, c->page_tokens, c->kv_heads, c->head_dim};
+    return W4A16_OK;
+}
+
+size_t kv4_cache_size(const Kv4Cache& c) { return kv4_bytes(c.num_pages, c.page_tokens, c.kv_heads, c.head_dim); }
+
+// Bytes from the first element of the first row to the last of the last, rows `stride` elements apart.
+size_t rows_bytes(int M, int64_t stride, int64_t width, size_t element) {
+    return (static_cast<size_t>(M - 1) * static_cast<size_t>(stride) + static_cast<size_t>(width)) * element;
+}
+
+int launched(cudaError_t e) {
+    if (e == cudaSuccess) return W4A16_OK;
+    cudaGetLastError();
+    return W4A16_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t w4a16_kv4_cache_bytes(int num_pages, int page_tokens, int kv_heads, int head_dim) {
+    if (check_kv4_shape(num_pages, page_tokens, kv_heads, head_dim) != W4A16_OK) return 0;
+    return kv4_bytes(num_pages, page_tokens, kv_heads, head_dim);
+}
+
+int w4a16_kv4_append(const uint16_t* qkv, int64_t qkv_stride, int heads, uint16_t* q_out, const w4a16_kv4_cache* cache,
+                     const int32_t* slots, const int32_t* positions, const float* rope, int rope_positions, int rot,
+                     int adjacent, const uint16_t* q_norm, const uint16_t* k_norm, float eps, int M, void* stream) {
+    if (!qkv || !slots || M <= 0 || heads < 0 || (heads > 0 && !q_out)) return W4A16_ERR_INVALID_ARG;
+    if (rope && (!positions || rope_positions <= 0 || rot <= 0)) return W4A16_ERR_INVALID_ARG;
+    if (adjacent != 0 && adjacent != 1) return W4A16_ERR_INVALID_ARG;
+    if ((q_norm || k_norm) && !(eps >= 0.f && std::isfinite(eps))) return W4A16_ERR_INVALID_ARG;
+    Kv4Cache c;
+    const int rc = check_kv4_cache(cache, &c);
+    if (rc != W4A16_OK) return rc;
+    if (M > (1 << 20) || heads > 1024 || heads % c.kv_heads != 0) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    const int64_t width = static_cast<int64_t>(heads + 2 * c.kv_heads) * c.head_dim;
+    if (qkv_stride < width && M > 1) return W4A16_ERR_INVALID_ARG;
+    if (qkv_stride % 8 != 0 || qkv_stride > (1LL << 32)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (rope && (rot % 16 != 0 || rot > c.head_dim)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(rope) || !aligned16(q_norm) || !aligned16(k_norm) ||
+        !aligned4(slots) || !aligned4(positions))
+        return W4A16_ERR_MISALIGNED;
+    const size_t in_b = rows_bytes(M, qkv_stride, width, 2), kv_b = kv4_cache_size(c);
+    const size_t out_b = static_cast<size_t>(M) * heads * c.head_dim * 2, row_b = static_cast<size_t>(M) * 4;
+    if (overlaps(qkv, in_b, c.pages, kv_b) || overlaps(slots, row_b, c.pages, kv_b)) return W4A16_ERR_INVALID_ARG;
+    if (heads > 0 && (overlaps(qkv, in_b, q_out, out_b) || overlaps(q_out, out_b, c.pages, kv_b) ||
+                      overlaps(slots, row_b, q_out, out_b) || (positions && overlaps(positions, row_b, q_out, out_b))))
+        return W4A16_ERR_INVALID_ARG;
+    if (is_host_pointer(qkv) || is_host_pointer(c.pages) || is_host_pointer(slots) ||
+        (heads > 0 && is_host_pointer(q_out)) || (rope && (is_host_pointer(rope) || is_host_pointer(positions))) ||
+        (q_norm && is_host_pointer(q_norm)) || (k_norm && is_host_pointer(k_norm)))
+        return W4A16_ERR_INVALID_ARG;
+    DeviceInfo d;
+    if (!device_info(&d)) return W4A16_ERR_CUDA;
+    Kv4AppendParams p = {qkv,   qkv_stride, q_out,    slots,  positions, rope, rope_positions,
+                         rope ? rot : 0, adjacent, q_norm, k_norm, eps, M, heads};
+    return launched(launch_kv4_append(p, c, static_cast<cudaStream_t>(stream), d.status));
+}
+
+int w4a16_kv4_load(const w4a16_kv4_cache* cache, const int32_t* slots, uint16_t* k, uint16_t* v, int n, void* stream) {
+    if (!slots || !k || !v || n <= 0) return W4A16_ERR_INVALID_ARG;
+    Kv4Cache c;
+    const int rc = check_kv4_cache(cache, &c);
+    if (rc != W4A16_OK) return rc;
+    if (n > (1 << 24)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(k) || !aligned16(v) || !aligned4(slots)) return W4A16_ERR_MISALIGNED;
+    const size_t b = static_cast<size_t>(n) * c.kv_heads * c.head_dim * 2, kv_b = kv4_cache_size(c);
+    const size_t row_b = static_cast<size_t>(n) * 4;
+    if (overlaps(k, b, v, b) || overlaps(k, b, c.pages, kv_b) || overlaps(v, b, c.pages, kv_b) ||
+        overlaps(slots, row_b, k, b) || overlaps(slots, row_b, v, b))
+        return W4A16_ERR_INVALID_ARG;
+    if (is_host_pointer(slots) || is_host_pointer(k) || is_host_pointer(v) || is_host_pointer(c.pages))
+        return W4A16_ERR_INVALID_ARG;
+    DeviceInfo d;
+    if (!device_info(&d)) return W4A16_ERR_CUDA;
+    return launched(launch_kv4_load(c, slots, k, v, n, static_cast<cudaStream_t>(stream), d.status));
+}
+
+size_t w4a16_kv4_attention_workspace_bytes(int head_dim) {
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+    return kv4_attention_workspace(head_dim);
+}
+
+int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4a16_kv4_cache* cache,
+                        const int32_t* block_table, int max_pages, const int32_t* kv_len, const int32_t* q_start,
+                        int B, int M, int max_q_len, int causal, float scale, uint16_t* out, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+    if (!q || !block_table || !kv_len || !q_start || !out || !workspace) return W4A16_ERR_INVALID_ARG;
+    if (heads <= 0 || max_pages <= 0 || B <= 0 || M <= 0 || max_q_len <= 0) return W4A16_ERR_INVALID_ARG;
+    if ((causal != 0 && causal != 1) || !std::isfinite(scale)) return W4A16_ERR_INVALID_ARG;
+    Kv4Cache c;
+    const int rc = check_kv4_cache(cache, &c);
+    if (rc != W4A16_OK) return rc;
+    if (heads > 1024 || heads % c.kv_heads != 0 || B > (1 << 20) || M > (1 << 20)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<int64_t>(max_pages) * c.page_tokens >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    const int64_t width = static_cast<int64_t>(heads) * c.head_dim;
+    if (q_stride < width && M > 1) return W4A16_ERR_INVALID_ARG;
+    if (q_stride % 8 != 0 || q_stride > (1LL << 32)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (workspace_bytes < kv4_attention_workspace(c.head_dim)) return W4A16_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned4(lse) || !aligned4(block_table) ||
+        !aligned4(kv_len) || !aligned4(q_start))
+        return W4A16_ERR_MISALIGNED;
+    struct Buffer {
+        const void* p;
+        size_t n;
+    };
+    const size_t out_b = static_cast<size_t>(M) * width * 2;
+    const Buffer written[3] = {{out, out_b}, {workspace, workspace_bytes}, {lse, static_cast<size_t>(M) * heads * 4}};
+    const Buffer read[5] = {{q, rows_bytes(M, q_stride, width, 2)},
+                            {c.pages, kv4_cache_size(c)},
+                            {block_table, static_cast<size_t>(B) * max_pages * 4},
+                            {kv_len, static_cast<size_t>(B) * 4},
+                            {q_start, (static_cast<size_t>(B) + 1) * 4}};
+    for (int i = 0; i < 3; ++i) {
+        if (!written[i].p) continue;
+        if (is_host_pointer(written[i].p)) return W4A16_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(written[i].p, written[i].n, written[j].p, written[j].n)) return W4A16_ERR_INVALID_ARG;
+        for (const Buffer& r : read)
+            if (overlaps(written[i].p, written[i].n, r.p, r.n)) return W4A16_ERR_INVALID_ARG;
+    }
+    for (const Buffer& r : read)
+        if (is_host_pointer(r.p)) return W4A16_ERR_INVALID_ARG;
+    DeviceInfo d;
+    if (!device_info(&d)) return W4A16_ERR_CUDA;
+    Kv4AttnParams p = {q, q_stride, block_table, kv_len, q_start, out, lse, workspace, B, M, heads, max_pages,
+                       max_q_len, causal, scale};
+    return launched(launch_kv4_attention(p, c, d.sm_count, static_cast<cudaStream_t>(stream), d.status));
+}
+
+int w4a16_sample(const uint16_t* logits, int64_t stride, int M, int V, const float* temperature, const int32_t* top_k,
+                 const float* top_p, const float* min_p, const float* u, int32_t* tokens, float* probs, void* stream) {
+    if (!logits || !u || !tokens || M <= 0 || V <= 0 || (stride < V && M > 1)) return W4A16_ERR_INVALID_ARG;
+    if (M > 65536 || V > 1000000 || stride > (1LL << 32)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if ((reinterpret_cast<uintptr_t>(logits) & 1u) != 0 || !aligned4(temperature) || !aligned4(top_k) ||
+        !aligned4(top_p) || !aligned4(min_p) || !aligned4(u) || !aligned4(tokens) || !aligned4(probs))
+        return W4A16_ERR_MISALIGNED;
+    const size_t in_b = rows_bytes(M, stride, V, 2), row_b = static_cast<size_t>(M) * 4;
+    const void* read[6] = {logits, temperature, top_k, top_p, min_p, u};
+    const void* written[2] = {tokens, probs};
+    if (probs && overlaps(tokens, row_b, probs, row_b)) return W4A16_ERR_INVALID_ARG;
+    for (int i = 0; i < 6; ++i) {
+        if (!read[i]) continue;
+        if (is_host_pointer(read[i])) return W4A16_ERR_INVALID_ARG;
+        for (const void* w : written)
+            if (w && overlaps(read[i], i == 0 ? in_b : row_b, w, row_b)) return W4A16_ERR_INVALID_ARG;
+    }
+    for (const void* w : written)
+        if (w && is_host_pointer(w)) return W4A16_ERR_INVALID_ARG;
+    DeviceInfo d;
+    if (!device_info(&d)) return W4A16_ERR_CUDA;
+    SampleParams p = {logits, stride, temperature, top_k, top_p, min_p, u, tokens, probs, M, V};
+    return launched(launch_sample(p, static_cast<cudaStream_t>(stream), d.status));
 }
 
 int w4a16_last_dispatch(char* buf, size_t len) {
