@@ -138,8 +138,7 @@ struct Kv4AttnParams {
     float scale;
 };
 size_t kv4_attention_workspace(int head_dim);  // bytes; the same for every batch
-cudaError_t launch_kv4_attention(const Kv4AttnParams& p, const Kv4Cache& c, int sm_count, cudaStream_t s,
-                                 unsigned* status);
+cudaError_t launch_kv4_attention(const Kv4AttnParams& p, const Kv4Cache& c, const LaunchCtx& ctx);
 
 // ---- sample.cu
 struct SampleParams {

@@ -1103,7 +1103,12 @@ int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4
     if (!device_info(&d)) return W4A16_ERR_CUDA;
     Kv4AttnParams p = {q, q_stride, block_table, kv_len, q_start, out, lse, workspace, B, M, heads, max_pages,
                        max_q_len, causal, scale};
-    return launched(launch_kv4_attention(p, c, d.sm_count, static_cast<cudaStream_t>(stream), d.status));
+    LaunchCtx ctx;
+    ctx.stream = static_cast<cudaStream_t>(stream);
+    ctx.status = d.status;
+    ctx.timeout_ns = g_timeout_ns.load();
+    ctx.sm_count = d.sm_count;
+    return launched(launch_kv4_attention(p, c, ctx));
 }
 
 int w4a16_sample(const uint16_t* logits, int64_t stride, int M, int V, const float* temperature, const int32_t* top_k,
