@@ -7,8 +7,8 @@
 //   scores  S^T[16 tokens][8 rows]   = K codes [16 x D] . Q^T[D x 8]
 //   output  O^T[D][8 rows]          += V codes^T [D x 16] . P[16 x 8]
 // The codes go into the instruction as they are: a nibble in the low bits of an fp16 is the subnormal
-// code * 2^-24, exact, so a pair of operands costs one AND (the nibbles one place up are 16 times that;
-// for keys they have an accumulator of their own, for values they are other rows of the output). The
+// code * 2^-24, exact, so a pair of operands costs one AND. (The nibbles one place up count 16 times: for
+// keys their elements of q are divided by 16, for values they are other rows of the output.) The
 // parameters come in around the products, in fp32, per token t and group y of 64 elements:
 //   S_t  = sum_y scale_ty (sum_d q_d code_td) + min_ty (sum_d q_d)
 //   O_d  = sum_t (P_t scale_ty) code_td + sum_t P_t min_ty
@@ -52,6 +52,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// c = A . B
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
@@ -124,7 +135,8 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
     extern __shared__ __align__(128) uint8_t smem[];
     float* s_max = reinterpret_cast<float*>(smem + C::kData + NW * S * 8);  // [NW][8]
     float* s_sum = s_max + NW * kRows;
-    int64_t* s_plan = reinterpret_cast<int64_t*>(s_sum + NW * kRows);  // run length, offset in the first sequence
+    float* s_row = s_sum + NW * kRows;  // maximum and sum of the unit's rows
+    int64_t* s_plan = reinterpret_cast<int64_t*>(s_row + 2 * kRows);  // run length, offset in the first sequence
     int* s_first = reinterpret_cast<int*>(s_plan + 4);
     int* s_abort = s_first + 1;
     int* s_last = s_first + 2;
@@ -191,6 +203,7 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
     int64_t left = s_plan[0], off = s_plan[1], seq_at = s_plan[3];
     const int64_t per = s_plan[2];
     uint32_t phase = 0;  // one bit per ring stage
+    const uint64_t policy = policy_evict_first();
 
     for (int b = *s_first; left > 0 && b < p.B;) {
         const Seq sq = seq_of(p, cache, b);
@@ -215,49 +228,45 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
         const int t1e = min(t1, (lim_max + kKv4Tile - 1) / kKv4Tile);
         const int mine = max(0, (t1e - t0 - warp + NW - 1) / NW);  // tiles of this warp: t0 + warp + NW i
 
-        // ---- the ring: page numbers of 32 of the warp's tiles at a time, one bulk copy a tile
-        int page_of = -1;
-        auto fetch_pages = [&](int i0) {
+        // ---- the ring: where 32 of the warp's tiles at a time lie (one a lane), one bulk copy a tile
+        int64_t tile_at = -1;
+        uint32_t there = 0;  // tiles in the ring whose page exists, by stage
+        auto locate = [&](int i0) {
             const int tile = t0 + warp + NW * (i0 + lane);
-            page_of = -1;
+            tile_at = -1;
             if (tile < t1e) {
-                page_of = p.block_table[static_cast<int64_t>(b) * p.max_pages + (tile * kKv4Tile >> cache.page_shift)];
-                if (page_of < 0 || page_of >= cache.num_pages) {
+                const int tok = tile * kKv4Tile;
+                const int page = p.block_table[static_cast<int64_t>(b) * p.max_pages + (tok >> cache.page_shift)];
+                if (page >= 0 && page < cache.num_pages) {
+                    tile_at = cache.tile_offset<D>(page, kvh, tok & ((1 << cache.page_shift) - 1));
+                    if (!in_bounds(tile_at >= 0 && tile_at + C::kTile <= cache.bytes<D>(), status)) tile_at = -1;
+                } else {
                     record_error(status, kErrBounds);
-                    page_of = -1;
                 }
             }
         };
-        uint32_t there = 0;  // tiles in the ring whose page exists, by stage
-        auto issue = [&](int i) {
-            if ((i & 31) == 0) fetch_pages(i);
-            const int page = __shfl_sync(0xffffffffu, page_of, i & 31);
-            const int st = i % S;
-            const int tile = t0 + warp + NW * i;
-            bool ok = page >= 0;
-            int64_t from = 0;
-            if (ok) {
-                from = cache.tile_offset<D>(page, kvh, tile * kKv4Tile & ((1 << cache.page_shift) - 1));
-                ok = in_bounds(from >= 0 && from + C::kTile <= cache.bytes<D>(), status);
-            }
-            there = ok ? there | (1u << st) : there & ~(1u << st);
-            if (ok && lane == 0) {
+        auto issue = [&](int i, int st) {
+            if ((i & 31) == 0) locate(i);
+            const int64_t from = __shfl_sync(0xffffffffu, tile_at, i & 31);
+            there = from >= 0 ? there | (1u << st) : there & ~(1u << st);
+            if (from >= 0 && lane == 0) {
                 mbar_arrive_expect_tx(bars + 8 * st, C::kTile);
-                bulk_g2s(ring + st * C::kTile, cache.pages + from, C::kTile, bars + 8 * st, policy_evict_first());
+                bulk_g2s(ring + st * C::kTile, cache.pages + from, C::kTile, bars + 8 * st, policy);
             }
         };
-        for (int i = 0; i < min(S, mine); ++i) issue(i);
+        for (int i = 0; i < min(S, mine); ++i) issue(i, i);
 
-        // ---- Q^T fragments (row g of the unit), and the sums of q over each group for rows 2t, 2t + 1
-        uint32_t q[G][2][4];
-        float qs0[G], qs1[G];
+        // ---- Q^T fragments (row g of the unit), times a power of two that brings the row's largest element
+        // to 2^8 .. 2^9: the odd pairs, whose codes count 16 times, are divided by 16 without loss. Then the
+        // sums of q over each group, as two fp16 numbers: what the keys' minimums are multiplied by.
+        uint32_t q[G][2][4], qsum[2] = {0, 0};
+        float row0, row1;  // of rows 2t, 2t + 1: what takes a score in code units to powers of two
         {
             const int pos = (rt * kRows + g) / grp, hd = (rt * kRows + g) % grp;
             const uint16_t* src = p.q + (sq.q0 + pos) * p.q_stride + static_cast<int64_t>(kvh * grp + hd) * D;
-            const float c1 = p.scale * 1.4426950408889634f;
+            float big = 0.f;
 #pragma unroll
-            for (int y = 0; y < G; ++y) {
-                float sum = 0.f;
+            for (int y = 0; y < G; ++y)
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     uint4 v = make_uint4(0, 0, 0, 0);
@@ -267,15 +276,42 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
                     q[y][w][2] = v.z;
                     q[y][w][3] = v.w;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sum += lo_f(q[y][w][i]) + hi_f(q[y][w][i]);
+                    for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(lo_f(q[y][w][i])), fabsf(hi_f(q[y][w][i]))));
                 }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                qs0[y] = __shfl_sync(0xffffffffu, sum, 8 * t) * c1;
-                qs1[y] = __shfl_sync(0xffffffffu, sum, 8 * t + 4) * c1;
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            const int e = big > 0.f && big < INFINITY ? 8 - (static_cast<int>(__float_as_uint(big) >> 23) - 127) : 0;
+            const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+            float sum[G];
+#pragma unroll
+            for (int y = 0; y < G; ++y) {
+                sum[y] = 0.f;
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float a = lo_f(q[y][w][i]) * up, c = hi_f(q[y][w][i]) * up;
+                        sum[y] += a + c;
+                        const float k = (i & 1) ? 0.0625f : 1.f;
+                        q[y][w][i] = pack_h2(a * k, c * k);
+                    }
+                sum[y] += __shfl_xor_sync(0xffffffffu, sum[y], 1);
+                sum[y] += __shfl_xor_sync(0xffffffffu, sum[y], 2);
             }
+            // as the B operand of 16 columns: groups 0 .. G-1 rounded, and in columns 4 .. what is left
+            if (G == 1) {
+                const float r = __half2float(__float2half_rn(sum[0]));
+                if ((t & 1) == 0) qsum[0] = pack_h2(t == 0 ? sum[0] : sum[0] - r, 0.f);
+            } else {
+                const bool second = G == 4 && (t & 1);
+                const float a = second ? sum[G > 2 ? 2 : 0] : sum[0], c = second ? sum[G > 2 ? 3 : 0] : sum[G > 1 ? 1 : 0];
+                const float ra = a - __half2float(__float2half_rn(a)), rc = c - __half2float(__float2half_rn(c));
+                if (G == 4 || (t & 1) == 0) qsum[0] = t < 2 ? pack_h2(a, c) : pack_h2(ra, rc);
+            }
+            const float c1 = p.scale * (1.4426950408889634f * 16777216.f) / up;  // scale log2(e) 2^24
+            row0 = __shfl_sync(0xffffffffu, c1, 8 * t);
+            row1 = __shfl_sync(0xffffffffu, c1, 8 * t + 4);
         }
-        const float c0 = p.scale * (1.4426950408889634f * 16777216.f);  // scale log2(e) 2^24
         float o[4 * G][4], om[G][2];
 #pragma unroll
         for (int i = 0; i < 4 * G; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -284,8 +320,7 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         float vmul = 1.f, vcap = 0.f;  // P scale is taken times vmul = 2^e; scales up to vcap fit
 
-        for (int i = 0; i < mine; ++i) {
-            const int st = i % S;
+        for (int i = 0, st = 0; i < mine; ++i, st = st + 1 == S ? 0 : st + 1) {
             const bool have = (there >> st) & 1u;
             const uint32_t tile_s = ring + st * C::kTile;
             if (have) {
@@ -312,21 +347,37 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
                             for (int y = 0; y < G; ++y) kp[h][y] = vp[h][y] = 0;
                         }
                 }
-                // scores of tokens g, g + 8 (s[0..1], s[2..3]) and rows 2t, 2t + 1, in powers of two
-                float s[4] = {0.f, 0.f, 0.f, 0.f};
-                auto group_scores = [&](int y, uint32_t a_w0, uint32_t b_w0, uint32_t a_w1, uint32_t b_w1) {
-                    float x[4] = {0.f, 0.f, 0.f, 0.f}, z[4] = {0.f, 0.f, 0.f, 0.f};
-                    constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
-                    mma16816(x, a_w0 & kLow, b_w0 & kLow, (a_w0 >> 8) & kLow, (b_w0 >> 8) & kLow, q[y][0][0], q[y][0][2]);
-                    mma16816(z, a_w0 & kHigh, b_w0 & kHigh, (a_w0 >> 8) & kHigh, (b_w0 >> 8) & kHigh, q[y][0][1], q[y][0][3]);
-                    mma16816(x, a_w1 & kLow, b_w1 & kLow, (a_w1 >> 8) & kLow, (b_w1 >> 8) & kLow, q[y][1][0], q[y][1][2]);
-                    mma16816(z, a_w1 & kHigh, b_w1 & kHigh, (a_w1 >> 8) & kHigh, (b_w1 >> 8) & kHigh, q[y][1][1], q[y][1][3]);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float sc = lo_f(kp[h][y]) * c0, mn = hi_f(kp[h][y]);
-                        s[2 * h] = fmaf(sc, fmaf(z[2 * h], 0.0625f, x[2 * h]), fmaf(mn, qs0[y], s[2 * h]));
-                        s[2 * h + 1] = fmaf(sc, fmaf(z[2 * h + 1], 0.0625f, x[2 * h + 1]), fmaf(mn, qs1[y], s[2 * h + 1]));
+                // scores of tokens g, g + 8 (s[0..1], s[2..3]) and rows 2t, 2t + 1
+                float s[4];
+                {
+                    // minimums of the groups that this lane's columns of the A operand stand for
+                    uint32_t ka, kb;
+                    if constexpr (G == 4) {
+                        ka = __byte_perm((t & 1) ? kp[0][2] : kp[0][0], (t & 1) ? kp[0][3] : kp[0][1], 0x7632);
+                        kb = __byte_perm((t & 1) ? kp[1][2] : kp[1][0], (t & 1) ? kp[1][3] : kp[1][1], 0x7632);
+                    } else if constexpr (G == 2) {
+                        ka = __byte_perm(kp[0][0], kp[0][1], 0x7632);
+                        kb = __byte_perm(kp[1][0], kp[1][1], 0x7632);
+                    } else {
+                        ka = kp[0][0] >> 16;
+                        kb = kp[1][0] >> 16;
                     }
+                    mma16816_first(s, ka, kb, 0u, 0u, qsum[0], 0u);
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[x] *= 5.9604644775390625e-8f;  // 2^-24: the unit of the codes
+                auto group_scores = [&](int y, uint32_t a_w0, uint32_t b_w0, uint32_t a_w1, uint32_t b_w1) {
+                    float x[4];
+                    constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
+                    mma16816_first(x, a_w0 & kLow, b_w0 & kLow, (a_w0 >> 8) & kLow, (b_w0 >> 8) & kLow, q[y][0][0], q[y][0][2]);
+                    mma16816(x, a_w0 & kHigh, b_w0 & kHigh, (a_w0 >> 8) & kHigh, (b_w0 >> 8) & kHigh, q[y][0][1], q[y][0][3]);
+                    mma16816(x, a_w1 & kLow, b_w1 & kLow, (a_w1 >> 8) & kLow, (b_w1 >> 8) & kLow, q[y][1][0], q[y][1][2]);
+                    mma16816(x, a_w1 & kHigh, b_w1 & kHigh, (a_w1 >> 8) & kHigh, (b_w1 >> 8) & kHigh, q[y][1][1], q[y][1][3]);
+                    const float sa = lo_f(kp[0][y]), sb = lo_f(kp[1][y]);
+                    s[0] = fmaf(sa, x[0], s[0]);
+                    s[1] = fmaf(sa, x[1], s[1]);
+                    s[2] = fmaf(sb, x[2], s[2]);
+                    s[3] = fmaf(sb, x[3], s[3]);
                 };
                 if constexpr (G == 1) {
                     const uint2 a = lds64(tile_s + lane * 8), c = lds64(tile_s + (32 + lane) * 8);
@@ -340,13 +391,18 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
                         group_scores(2 * j + 1, a.z, c.z, a.w, c.w);
                     }
                 }
+                s[0] *= row0;
+                s[1] *= row1;
+                s[2] *= row0;
+                s[3] *= row1;
                 if (edge) {
                     if (tok + g >= lim0) s[0] = -INFINITY;
                     if (tok + g >= lim1) s[1] = -INFINITY;
                     if (tok + g + 8 >= lim0) s[2] = -INFINITY;
                     if (tok + g + 8 >= lim1) s[3] = -INFINITY;
                 }
-                // a new maximum (or a scale that would not fit) anywhere in the warp: rescale what is summed
+                // P may grow to 2^8 before the reference moves: most tiles rescale nothing. A score above that
+                // (or a scale that would not fit) anywhere in the warp: take the new maximum, rescale the sums.
                 __half2 big = __hmax2(*reinterpret_cast<const __half2*>(&vp[0][0]), *reinterpret_cast<const __half2*>(&vp[1][0]));
 #pragma unroll
                 for (int y = 1; y < G; ++y) {
@@ -354,7 +410,7 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
                     big = __hmax2(big, *reinterpret_cast<const __half2*>(&vp[1][y]));
                 }
                 float top = __low2float(big);
-                if (__any_sync(0xffffffffu, s[0] > m0 || s[2] > m0 || s[1] > m1 || s[3] > m1 || top > vcap)) {
+                if (__any_sync(0xffffffffu, fmaxf(s[0], s[2]) > m0 + 8.f || fmaxf(s[1], s[3]) > m1 + 8.f || top > vcap)) {
                     float n0 = fmaxf(m0, fmaxf(s[0], s[2])), n1 = fmaxf(m1, fmaxf(s[1], s[3]));
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) {
@@ -373,13 +429,13 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
                         om[y][1] *= r1;
                     }
                     if (top > vcap) {
-                        // the largest scale becomes 2^8 .. 2^9: 7 bits of room above, 22 below to fp16's
-                        // smallest normal number; never less than 2^-1, with which every finite scale fits
-                        const int e = max(8 - (static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127), -1);
+                        // the largest scale becomes 1 .. 2: 2^8 P times scales up to 2^7 of it fit in fp16. Never
+                        // less than 2^-9, with which every finite scale does
+                        const int e = max(-(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127), -9);
                         const float to = __uint_as_float(static_cast<uint32_t>(min(e, 100) + 127) << 23);
                         const float f = to / vmul;
                         vmul = to;
-                        vcap = 32768.f / to;
+                        vcap = 127.f / to;
                         r0 *= f;
                         r1 *= f;
                     }
@@ -412,15 +468,16 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const uint32_t a0 = w[x] & 0x000F000Fu, a1 = w[x] & 0x00F000F0u;
-                        const uint32_t a2 = (w[x] >> 8) & 0x000F000Fu, a3 = (w[x] >> 8) & 0x00F000F0u;
+                        // rows g: the low codes; rows g + 8: low + 16 high (the low ones are taken off at the end)
+                        const uint32_t a1 = w[x] & 0x00FF00FFu, a3 = __byte_perm(w[x], 0u, 0x4341);
+                        const uint32_t a0 = w[x] & 0x000F000Fu, a2 = a3 & 0x000F000Fu;
                         mma16816(o[4 * y + x], a0, a1, a2, a3, b0, b1);
                         mma16816(o[4 * y + x], a0, a1, a2, a3, e0, e1);
                     }
                 }
             }
             __syncwarp();
-            if (i + S < mine) issue(i + S);
+            if (i + S < mine) issue(i + S, st);
         }
 
         // ---- join the warps: rows relative to the CTA's maximum, summed in warp order
@@ -455,44 +512,56 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
                 const int d = 16 * x + g, y = x / 4;
                 part[2 * t * C::kPitch + d] = fmaf(o[x][0], k0, om[y][0] * f0);
                 part[(2 * t + 1) * C::kPitch + d] = fmaf(o[x][1], k1, om[y][1] * f1);
-                part[2 * t * C::kPitch + d + 8] = fmaf(o[x][2], k0 * 0.0625f, om[y][0] * f0);
-                part[(2 * t + 1) * C::kPitch + d + 8] = fmaf(o[x][3], k1 * 0.0625f, om[y][1] * f1);
+                part[2 * t * C::kPitch + d + 8] = fmaf(o[x][2] - o[x][0], k0 * 0.0625f, om[y][0] * f0);
+                part[(2 * t + 1) * C::kPitch + d + 8] = fmaf(o[x][3] - o[x][1], k1 * 0.0625f, om[y][1] * f1);
             }
+        }
+        if (tid < kRows) {  // the CTA's maximum and sum of each row
+            float top = -INFINITY, total = 0.f;
+            for (int w = 0; w < NW; ++w) top = fmaxf(top, s_max[w * kRows + tid]);
+            for (int w = 0; w < NW; ++w) {
+                const float m = s_max[w * kRows + tid];
+                total += m == -INFINITY ? 0.f : s_sum[w * kRows + tid] * ex2(m - top);
+            }
+            s_row[tid] = top;
+            s_row[kRows + tid] = total;
         }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == sq.tiles;
         const int64_t unit_at = seq_at + static_cast<int64_t>(unit) * sq.tiles;  // its place in the work list
         const int cta0 = static_cast<int>(unit_at / per), cta1 = static_cast<int>((unit_at + sq.tiles - 1) / per);
         float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kCounterBytes);
-        float* my_part = parts + static_cast<int64_t>(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * C::kPart;
-        auto finish = [&](int r, int d, float sum, float total, float top) {
+        auto part_of = [&](int c) { return parts + static_cast<int64_t>(2 * c + (c == cta0 ? 1 : 0)) * C::kPart; };
+        auto finish = [&](int r, int d, float4 v, float total, float top) {
             const int pos = (rt * kRows + r) / grp, hd = (rt * kRows + r) % grp;
             const int64_t at = static_cast<int64_t>(sq.q0 + pos) * p.heads + kvh * grp + hd;
-            p.out[at * D + d] = __half_as_ushort(__float2half_rn(total > 0.f ? sum / total : 0.f));
+            const float f = total > 0.f ? 1.f / total : 0.f;
+            const __half2 h0 = __floats2half2_rn(v.x * f, v.y * f), h1 = __floats2half2_rn(v.z * f, v.w * f);
+            *reinterpret_cast<uint2*>(p.out + at * D + d) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
             if (d == 0 && p.lse != nullptr)
                 p.lse[at] = total > 0.f ? 0.6931471805599453f * (top + log2f(total)) : -INFINITY;
         };
-        for (int x = tid; x < rows * D; x += C::kThreads) {
+        float* mine_out = part_of(blockIdx.x);
+        for (int x = 4 * tid; x < rows * D; x += 4 * C::kThreads) {
             const int r = x / D, d = x - r * D;
-            float sum = 0.f, total = 0.f, top = -INFINITY;
-            for (int w = 0; w < NW; ++w) top = fmaxf(top, s_max[w * kRows + r]);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
             for (int w = 0; w < NW; ++w) {
-                sum += reinterpret_cast<float*>(smem)[(w * kRows + r) * C::kPitch + d];
-                const float m = s_max[w * kRows + r];
-                total += m == -INFINITY ? 0.f : s_sum[w * kRows + r] * ex2(m - top);
+                const float4 a = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + (w * kRows + r) * C::kPitch + d);
+                v.x += a.x;
+                v.y += a.y;
+                v.z += a.z;
+                v.w += a.w;
             }
-            if (whole) {
-                finish(r, d, sum, total, top);
-            } else {
-                __stcg(my_part + 2 * kRows + x, sum);
-                if (d == 0) {
-                    __stcg(my_part + r, top);
-                    __stcg(my_part + kRows + r, total);
-                }
-            }
+            if (whole)
+                finish(r, d, v, s_row[kRows + r], s_row[r]);
+            else
+                __stcg(reinterpret_cast<float4*>(mine_out + 2 * kRows + x), v);
         }
         if (!whole) {
             // ---- the last CTA of the unit to arrive adds its parts in CTA order
+            if (tid < 2 * kRows) __stcg(mine_out + tid, s_row[tid]);
             unsigned* counter = static_cast<unsigned*>(p.workspace) + cta0;
             __threadfence();
             __syncthreads();
@@ -504,19 +573,40 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
             __syncthreads();
             if (*s_last) {
                 __threadfence();
-                for (int x = tid; x < rows * D; x += C::kThreads) {
-                    const int r = x / D, d = x - r * D;
-                    float sum = 0.f, total = 0.f, top = -INFINITY;
-                    for (int c = cta0; c <= cta1; ++c)
-                        top = fmaxf(top, __ldcg(parts + static_cast<int64_t>(2 * c + (c == cta0 ? 1 : 0)) * C::kPart + r));
-                    for (int c = cta0; c <= cta1; ++c) {
-                        const float* part = parts + static_cast<int64_t>(2 * c + (c == cta0 ? 1 : 0)) * C::kPart;
-                        const float m = __ldcg(part + r);
+                const int n = cta1 - cta0 + 1;
+                float* s_f = reinterpret_cast<float*>(smem);  // [n][8]: what each part is scaled by
+                if (warp < kRows) {  // a warp per row
+                    float top = -INFINITY, total = 0.f;
+                    for (int c = lane; c < n; c += 32) top = fmaxf(top, __ldcg(part_of(cta0 + c) + warp));
+#pragma unroll
+                    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    for (int c = lane; c < n; c += 32) {
+                        const float m = __ldcg(part_of(cta0 + c) + warp);
                         const float f = m == -INFINITY ? 0.f : ex2(m - top);
-                        sum = fmaf(__ldcg(part + 2 * kRows + x), f, sum);
-                        total = fmaf(__ldcg(part + kRows + r), f, total);
+                        s_f[c * kRows + warp] = f;
+                        total = fmaf(__ldcg(part_of(cta0 + c) + kRows + warp), f, total);
                     }
-                    finish(r, d, sum, total, top);
+#pragma unroll
+                    for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+                    if (lane == 0) {
+                        s_row[warp] = top;
+                        s_row[kRows + warp] = total;
+                    }
+                }
+                __syncthreads();
+                for (int x = 4 * tid; x < rows * D; x += 4 * C::kThreads) {
+                    const int r = x / D, d = x - r * D;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int c = 0; c < n; ++c) {
+                        const float4 a = __ldcg(reinterpret_cast<const float4*>(part_of(cta0 + c) + 2 * kRows + x));
+                        const float f = s_f[c * kRows + r];
+                        v.x = fmaf(a.x, f, v.x);
+                        v.y = fmaf(a.y, f, v.y);
+                        v.z = fmaf(a.z, f, v.z);
+                        v.w = fmaf(a.w, f, v.w);
+                    }
+                    finish(r, d, v, s_row[kRows + r], s_row[r]);
                 }
             }
         }
