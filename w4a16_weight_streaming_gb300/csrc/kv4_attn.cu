@@ -16,11 +16,13 @@
 // codes' part and the minimums' part of a value cancel where the value is small, so one rounding of P_t
 // scale_ty would be off by 2^-11 of the group's whole range. A power of two keeps both normal.
 //
-// Work is a list of (sequence, 8 rows, key/value head, 16-token tile); every CTA takes an equal run of
+// Work is a list of (sequence, 8 rows, key/value head, 16-token tile); every CTA takes an equal share of
 // it, whatever the lengths, and its warps take the run's tiles in turn, each with a running maximum and
 // sum of its own, so that no warp waits for another inside a run. A tile is one bulk copy into the
 // warp's own ring in shared memory. Runs that end inside a row group leave their part in the workspace;
 // the CTA that arrives last there adds the parts in CTA order.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -28,23 +30,32 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kRows = 8;  // query rows of one work unit
+constexpr int kRows = 8;       // query rows of one work unit
+// What the start and end of a unit in a CTA cost, in tiles (narrow shape, 64 sequences of 512 .. 8192 tokens
+// and 8 key/value heads of 128: 93.7 us without it, the CTAs with short sequences last)
+constexpr int kUnitCost = 20;
 
-template <int D>
+// The kernel in two shapes, the same registers and ring bytes on an SM. Wide: one CTA, for few work units
+// (every CTA then has one run inside one unit, and few parts are left to add). Narrow: 3 or 4 CTAs of 4
+// warps, for many units: the start and end of one CTA's run (page numbers, queries, first copies; joining
+// the warps, writing) are hidden by the others' tiles.
+template <int D, bool Narrow>
 struct Decode {
-    static constexpr int kWarps = D == 256 ? 12 : 16;
-    static constexpr int kStages = D == 256 ? 3 : D == 128 ? 4 : 6;
+    static constexpr int kCtas = !Narrow ? 1 : D == 256 ? 3 : 4;
+    static constexpr int kWarps = Narrow ? 4 : D == 256 ? 12 : 16;
+    static constexpr int kStages = D == 256 ? 3 : D == 128 ? 5 : 8;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kTile = Kv4<D>::kTileBytes;
     static constexpr int kRing = kWarps * kStages * kTile;
     static constexpr int kPitch = D + 4;  // floats between rows of a warp's part: conflict-free stores
     static constexpr int kJoin = kWarps * kRows * kPitch * 4;
     static constexpr int kData = kRing > kJoin ? kRing : kJoin;
-    static constexpr int kSmem = kData + kWarps * kStages * 8 + kWarps * kRows * 8 + 256;
+    static constexpr int kQ = D / 64 * 1024 + 256;  // queries as operands, their sums, the rows' units
+    static constexpr int kSmem = kData + kQ + kWarps * kStages * 8 + kWarps * kRows * 8 + 256;
     static constexpr int kPart = kRows * (D + 2);  // floats of one workspace part: m, l, then rows
 };
 
-constexpr int kMaxCtas = 256;
+constexpr int kMaxCtas = 640;
 constexpr size_t kCounterBytes = kMaxCtas * 4;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -126,14 +137,18 @@ __device__ __forceinline__ Seq seq_of(const Kv4AttnParams& p, const Kv4View& c, 
     return s;
 }
 
-template <int D>
-__global__ void __launch_bounds__(Decode<D>::kThreads, 1)
+template <int D, bool Narrow>
+__global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>::kCtas)
     kv4_decode_kernel(const Kv4AttnParams p, const Kv4View cache, uint64_t timeout_ns, unsigned* status) {
-    using C = Decode<D>;
+    using C = Decode<D, Narrow>;
     using T = Kv4<D>;
     constexpr int G = T::kGroups, NW = C::kWarps, S = C::kStages;
+    constexpr int kBatch = Narrow ? 4 : 13;  // parts read at a time by the CTA that adds them
     extern __shared__ __align__(128) uint8_t smem[];
-    float* s_max = reinterpret_cast<float*>(smem + C::kData + NW * S * 8);  // [NW][8]
+    uint4* s_q = reinterpret_cast<uint4*>(smem + C::kData);  // [G][2][32 lanes]
+    uint32_t* s_qsum = reinterpret_cast<uint32_t*>(s_q + G * 2 * 32);
+    float* s_unit = reinterpret_cast<float*>(s_qsum + 32);
+    float* s_max = reinterpret_cast<float*>(smem + C::kData + C::kQ + NW * S * 8);  // [NW][8]
     float* s_sum = s_max + NW * kRows;
     float* s_row = s_sum + NW * kRows;  // maximum and sum of the unit's rows
     int64_t* s_plan = reinterpret_cast<int64_t*>(s_row + 2 * kRows);  // run length, offset in the first sequence
@@ -142,7 +157,7 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
     int* s_last = s_first + 2;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * S * C::kTile;
-    const uint32_t bars = smem_u32(smem + C::kData) + warp * S * 8;
+    const uint32_t bars = smem_u32(smem + C::kData + C::kQ) + warp * S * 8;
     const int grp = p.heads / cache.kv_heads;
 
     if (lane == 0)
@@ -155,26 +170,47 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
     // ---- this CTA's run of the work list
     if (warp == 0) {
         int64_t total = 0;
+        int units = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             int64_t c = 0;
+            int n = 0;
             if (b0 + lane < p.B) {
                 const Seq s = seq_of(p, cache, b0 + lane);
-                c = static_cast<int64_t>(s.units) * s.tiles;
+                c = static_cast<int64_t>(s.units) * (s.tiles + kUnitCost);
+                n = min(s.units, kMaxCtas);
                 if (s.bad && blockIdx.x == 0) record_error(status, kErrBounds);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
             total += c;
+            units = min(kMaxCtas, units + __reduce_add_sync(0xffffffffu, n));
         }
-        const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(NW));
-        const int64_t w0 = min(total, per * blockIdx.x), w1 = min(total, w0 + per);
+        // Few units: each is cut into equal chunks, one a CTA, the chunk size the smallest of 32 candidates
+        // with which there are CTAs enough (twice the mean is, when half the CTAs suffice for the units); at
+        // least 4 tiles a warp, since adding the parts of a unit takes as long as 5 or so. Otherwise equal
+        // runs that may begin and end inside a unit.
+        const int grid = static_cast<int>(gridDim.x);
+        const bool chunked = 2 * units <= grid;
+        int64_t per = max((total + grid - 1) / grid, static_cast<int64_t>(chunked ? 4 * NW : NW + kUnitCost));
+        if (chunked) {
+            const int mine = static_cast<int>(min(per + (per * lane + 30) / 31, static_cast<int64_t>(1 << 30)));
+            int items = 0;
+            for (int b = 0; b < p.B; ++b) {
+                const Seq s = seq_of(p, cache, b);
+                items += s.units * ((s.tiles + mine - 1) / mine);
+            }
+            const uint32_t fits = __ballot_sync(0xffffffffu, items <= grid);
+            per = __shfl_sync(0xffffffffu, mine, fits ? __ffs(fits) - 1 : 31);
+        }
+        // where the run (its first tile, or this CTA's chunk) lies
+        const int64_t w0 = chunked ? blockIdx.x : min(total, per * blockIdx.x), w1 = min(total, w0 + per);
         int64_t at = 0;
         int first = p.B;
-        for (int b0 = 0; b0 < p.B && w0 < w1; b0 += 32) {
+        for (int b0 = 0; b0 < p.B && (chunked || w0 < w1); b0 += 32) {
             int64_t c = 0;
             if (b0 + lane < p.B) {
                 const Seq s = seq_of(p, cache, b0 + lane);
-                c = static_cast<int64_t>(s.units) * s.tiles;
+                c = static_cast<int64_t>(s.units) * (chunked ? (s.tiles + per - 1) / per : s.tiles + kUnitCost);
             }
             int64_t upto = c;
 #pragma unroll
@@ -192,31 +228,52 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
             at += __shfl_sync(0xffffffffu, upto, 31);
         }
         if (lane == 0) {
-            s_plan[0] = w1 - w0;
+            s_plan[0] = chunked ? (first < p.B ? 1 : 0) : w1 - w0;
             s_plan[1] = w0 - at;
             s_plan[2] = per;
             s_plan[3] = at;  // work list position of the first sequence
-            *s_first = first;
+            s_first[0] = first;
+            s_first[3] = chunked;
         }
     }
     __syncthreads();
     int64_t left = s_plan[0], off = s_plan[1], seq_at = s_plan[3];
     const int64_t per = s_plan[2];
+    const bool chunked = s_first[3] != 0;
     uint32_t phase = 0;  // one bit per ring stage
     const uint64_t policy = policy_evict_first();
 
     for (int b = *s_first; left > 0 && b < p.B;) {
         const Seq sq = seq_of(p, cache, b);
-        const int64_t cost = static_cast<int64_t>(sq.units) * sq.tiles;
-        if (off >= cost) {
-            off -= cost;  // a sequence without rows
-            seq_at += cost;
-            ++b;
-            continue;
+        int unit, t0, t1, cta0, cta1;  // tiles t0 .. t1-1 of the unit, whose parts come from CTAs cta0 .. cta1
+        if (chunked) {
+            const int chunks = static_cast<int>((sq.tiles + per - 1) / per), size = (sq.tiles + chunks - 1) / chunks;
+            unit = static_cast<int>(off) / chunks;
+            const int chunk = static_cast<int>(off) - unit * chunks;
+            t0 = chunk * size;
+            t1 = min(sq.tiles, t0 + size);
+            cta0 = static_cast<int>(blockIdx.x) - chunk;
+            cta1 = cta0 + (sq.tiles + size - 1) / size - 1;
+            if (t0 >= t1) break;  // equal chunks came out one fewer
+        } else {
+            const int64_t each = sq.tiles + kUnitCost, cost = sq.units * each;
+            if (off >= cost) {
+                off -= cost;  // a sequence without rows, or done
+                seq_at += cost;
+                ++b;
+                continue;
+            }
+            unit = static_cast<int>(off / each);
+            const int64_t in_unit = off - unit * each, to = min(each, in_unit + left);
+            t0 = static_cast<int>(max(static_cast<int64_t>(0), in_unit - kUnitCost));
+            t1 = static_cast<int>(max(static_cast<int64_t>(0), to - kUnitCost));
+            off += to - in_unit;
+            left -= to - in_unit;
+            if (t0 == t1) continue;
+            const int64_t unit_at = seq_at + unit * each;  // its place in the work list
+            cta0 = static_cast<int>((unit_at + kUnitCost) / per);
+            cta1 = static_cast<int>((unit_at + each - 1) / per);
         }
-        const int unit = static_cast<int>(off / sq.tiles);
-        const int t0 = static_cast<int>(off - static_cast<int64_t>(unit) * sq.tiles);
-        const int t1 = static_cast<int>(min(static_cast<int64_t>(sq.tiles), t0 + left));
         const int kvh = unit / sq.row_groups, rt = unit - kvh * sq.row_groups;
         const int rows = min(kRows, sq.q_len * grp - rt * kRows);
         // tokens that a row sees; rows of this unit beyond the sequence's see as many as the last
@@ -254,29 +311,32 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
                 bulk_g2s(ring + st * C::kTile, cache.pages + from, C::kTile, bars + 8 * st, policy);
             }
         };
-        for (int i = 0; i < min(S, mine); ++i) issue(i, i);
-
-        // ---- Q^T fragments (row g of the unit), times a power of two that brings the row's largest element
-        // to 2^8 .. 2^9: the odd pairs, whose codes count 16 times, are divided by 16 without loss. Then the
-        // sums of q over each group, as two fp16 numbers: what the keys' minimums are multiplied by.
-        uint32_t q[G][2][4], qsum[2] = {0, 0};
-        float row0, row1;  // of rows 2t, 2t + 1: what takes a score in code units to powers of two
-        {
+        // ---- Q^T as the B operand (row g of the unit), times a power of two that brings the row's largest
+        // element to 2^8 .. 2^9: the odd pairs, whose codes count 16 times, are divided by 16 without loss.
+        // Then the sums of q over each group, as two fp16 numbers: what the keys' minimums are multiplied by.
+        // One warp makes them for all.
+        uint4 raw[G][2];
+        if (warp == 0) {
             const int pos = (rt * kRows + g) / grp, hd = (rt * kRows + g) % grp;
             const uint16_t* src = p.q + (sq.q0 + pos) * p.q_stride + static_cast<int64_t>(kvh * grp + hd) * D;
+#pragma unroll
+            for (int y = 0; y < G; ++y)
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+                    raw[y][w] = g < rows ? *reinterpret_cast<const uint4*>(src + y * kKv4Group + 16 * t + 8 * w)
+                                         : make_uint4(0, 0, 0, 0);
+        }
+        // (the first copies are on their way before the queries are used)
+        for (int i = 0; i < min(S, mine); ++i) issue(i, i);
+        if (warp == 0) {
             float big = 0.f;
 #pragma unroll
             for (int y = 0; y < G; ++y)
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (g < rows) v = *reinterpret_cast<const uint4*>(src + y * kKv4Group + 16 * t + 8 * w);
-                    q[y][w][0] = v.x;
-                    q[y][w][1] = v.y;
-                    q[y][w][2] = v.z;
-                    q[y][w][3] = v.w;
+                    const uint32_t v[4] = {raw[y][w].x, raw[y][w].y, raw[y][w].z, raw[y][w].w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(lo_f(q[y][w][i])), fabsf(hi_f(q[y][w][i]))));
+                    for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(lo_f(v[i])), fabsf(hi_f(v[i]))));
                 }
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -287,31 +347,39 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
             for (int y = 0; y < G; ++y) {
                 sum[y] = 0.f;
 #pragma unroll
-                for (int w = 0; w < 2; ++w)
+                for (int w = 0; w < 2; ++w) {
+                    uint32_t v[4] = {raw[y][w].x, raw[y][w].y, raw[y][w].z, raw[y][w].w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float a = lo_f(q[y][w][i]) * up, c = hi_f(q[y][w][i]) * up;
+                        const float a = lo_f(v[i]) * up, c = hi_f(v[i]) * up;
                         sum[y] += a + c;
                         const float k = (i & 1) ? 0.0625f : 1.f;
-                        q[y][w][i] = pack_h2(a * k, c * k);
+                        v[i] = pack_h2(a * k, c * k);
                     }
+                    s_q[(y * 2 + w) * 32 + lane] = make_uint4(v[0], v[2], v[1], v[3]);
+                }
                 sum[y] += __shfl_xor_sync(0xffffffffu, sum[y], 1);
                 sum[y] += __shfl_xor_sync(0xffffffffu, sum[y], 2);
             }
-            // as the B operand of 16 columns: groups 0 .. G-1 rounded, and in columns 4 .. what is left
+            // columns 0 .. G-1 of the operand: the sums rounded; columns 4 ..: what is left
+            uint32_t v = 0;
             if (G == 1) {
                 const float r = __half2float(__float2half_rn(sum[0]));
-                if ((t & 1) == 0) qsum[0] = pack_h2(t == 0 ? sum[0] : sum[0] - r, 0.f);
+                if ((t & 1) == 0) v = pack_h2(t == 0 ? sum[0] : sum[0] - r, 0.f);
             } else {
                 const bool second = G == 4 && (t & 1);
                 const float a = second ? sum[G > 2 ? 2 : 0] : sum[0], c = second ? sum[G > 2 ? 3 : 0] : sum[G > 1 ? 1 : 0];
                 const float ra = a - __half2float(__float2half_rn(a)), rc = c - __half2float(__float2half_rn(c));
-                if (G == 4 || (t & 1) == 0) qsum[0] = t < 2 ? pack_h2(a, c) : pack_h2(ra, rc);
+                if (G == 4 || (t & 1) == 0) v = t < 2 ? pack_h2(a, c) : pack_h2(ra, rc);
             }
-            const float c1 = p.scale * (1.4426950408889634f * 16777216.f) / up;  // scale log2(e) 2^24
-            row0 = __shfl_sync(0xffffffffu, c1, 8 * t);
-            row1 = __shfl_sync(0xffffffffu, c1, 8 * t + 4);
+            s_qsum[lane] = v;
+            if (t == 0) s_unit[g] = p.scale * (1.4426950408889634f * 16777216.f) / up;  // scale log2(e) 2^24
         }
+        __syncthreads();
+        const uint32_t qsum = s_qsum[lane];
+        // what takes a score of rows 2t, 2t + 1 in code units to powers of two
+        const float row0 = s_unit[2 * t], row1 = s_unit[2 * t + 1];
+        const uint32_t q_s = smem_u32(s_q) + lane * 16;
         float o[4 * G][4], om[G][2];
 #pragma unroll
         for (int i = 0; i < 4 * G; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -362,17 +430,18 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
                         ka = kp[0][0] >> 16;
                         kb = kp[1][0] >> 16;
                     }
-                    mma16816_first(s, ka, kb, 0u, 0u, qsum[0], 0u);
+                    mma16816_first(s, ka, kb, 0u, 0u, qsum, 0u);
                 }
 #pragma unroll
                 for (int x = 0; x < 4; ++x) s[x] *= 5.9604644775390625e-8f;  // 2^-24: the unit of the codes
                 auto group_scores = [&](int y, uint32_t a_w0, uint32_t b_w0, uint32_t a_w1, uint32_t b_w1) {
                     float x[4];
                     constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
-                    mma16816_first(x, a_w0 & kLow, b_w0 & kLow, (a_w0 >> 8) & kLow, (b_w0 >> 8) & kLow, q[y][0][0], q[y][0][2]);
-                    mma16816(x, a_w0 & kHigh, b_w0 & kHigh, (a_w0 >> 8) & kHigh, (b_w0 >> 8) & kHigh, q[y][0][1], q[y][0][3]);
-                    mma16816(x, a_w1 & kLow, b_w1 & kLow, (a_w1 >> 8) & kLow, (b_w1 >> 8) & kLow, q[y][1][0], q[y][1][2]);
-                    mma16816(x, a_w1 & kHigh, b_w1 & kHigh, (a_w1 >> 8) & kHigh, (b_w1 >> 8) & kHigh, q[y][1][1], q[y][1][3]);
+                    const uint4 q0 = lds128(q_s + (2 * y) * 512), q1 = lds128(q_s + (2 * y + 1) * 512);
+                    mma16816_first(x, a_w0 & kLow, b_w0 & kLow, (a_w0 >> 8) & kLow, (b_w0 >> 8) & kLow, q0.x, q0.y);
+                    mma16816(x, a_w0 & kHigh, b_w0 & kHigh, (a_w0 >> 8) & kHigh, (b_w0 >> 8) & kHigh, q0.z, q0.w);
+                    mma16816(x, a_w1 & kLow, b_w1 & kLow, (a_w1 >> 8) & kLow, (b_w1 >> 8) & kLow, q1.x, q1.y);
+                    mma16816(x, a_w1 & kHigh, b_w1 & kHigh, (a_w1 >> 8) & kHigh, (b_w1 >> 8) & kHigh, q1.z, q1.w);
                     const float sa = lo_f(kp[0][y]), sb = lo_f(kp[1][y]);
                     s[0] = fmaf(sa, x[0], s[0]);
                     s[1] = fmaf(sa, x[1], s[1]);
@@ -528,8 +597,6 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
         }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == sq.tiles;
-        const int64_t unit_at = seq_at + static_cast<int64_t>(unit) * sq.tiles;  // its place in the work list
-        const int cta0 = static_cast<int>(unit_at / per), cta1 = static_cast<int>((unit_at + sq.tiles - 1) / per);
         float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kCounterBytes);
         auto part_of = [&](int c) { return parts + static_cast<int64_t>(2 * c + (c == cta0 ? 1 : 0)) * C::kPart; };
         auto finish = [&](int r, int d, float4 v, float total, float top) {
@@ -575,64 +642,94 @@ __global__ void __launch_bounds__(Decode<D>::kThreads, 1)
                 __threadfence();
                 const int n = cta1 - cta0 + 1;
                 float* s_f = reinterpret_cast<float*>(smem);  // [n][8]: what each part is scaled by
-                if (warp < kRows) {  // a warp per row
-                    float top = -INFINITY, total = 0.f;
-                    for (int c = lane; c < n; c += 32) top = fmaxf(top, __ldcg(part_of(cta0 + c) + warp));
+                for (int r = warp; r < rows; r += NW) {  // a warp per row; 64 parts' numbers in one round of loads
+                    float top = -INFINITY, total = 0.f, m[2], l[2];
+                    for (int c = lane; c < n; c += 64) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) m[k] = c + 32 * k < n ? __ldcg(part_of(cta0 + c + 32 * k) + r) : -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) l[k] = c + 32 * k < n ? __ldcg(part_of(cta0 + c + 32 * k) + kRows + r) : 0.f;
+                        const float was = top;
+                        top = fmaxf(top, fmaxf(m[0], m[1]));
+                        total = was == top ? total : total * ex2(was - top);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            if (c + 32 * k < n) s_f[(c + 32 * k) * kRows + r] = m[k];
+                            total += m[k] == -INFINITY ? 0.f : l[k] * ex2(m[k] - top);
+                        }
+                    }
+                    const float mine_top = top;
 #pragma unroll
                     for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    for (int c = lane; c < n; c += 32) {
-                        const float m = __ldcg(part_of(cta0 + c) + warp);
-                        const float f = m == -INFINITY ? 0.f : ex2(m - top);
-                        s_f[c * kRows + warp] = f;
-                        total = fmaf(__ldcg(part_of(cta0 + c) + kRows + warp), f, total);
-                    }
+                    total = mine_top == -INFINITY ? 0.f : total * ex2(mine_top - top);
 #pragma unroll
                     for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+                    for (int c = lane; c < n; c += 32) {
+                        const float m0 = s_f[c * kRows + r];
+                        s_f[c * kRows + r] = m0 == -INFINITY ? 0.f : ex2(m0 - top);
+                    }
                     if (lane == 0) {
-                        s_row[warp] = top;
-                        s_row[kRows + warp] = total;
+                        s_row[r] = top;
+                        s_row[kRows + r] = total;
                     }
                 }
-                __syncthreads();
-                for (int x = 4 * tid; x < rows * D; x += 4 * C::kThreads) {
-                    const int r = x / D, d = x - r * D;
+                bool ready = false;
+                for (int x = 4 * tid; x < rows * D || !ready; x += 4 * C::kThreads) {
+                    const int r = min(x / D, rows - 1), d = x - x / D * D;
+                    const bool live = x < rows * D;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int c = 0; c < n; ++c) {
-                        const float4 a = __ldcg(reinterpret_cast<const float4*>(part_of(cta0 + c) + 2 * kRows + x));
-                        const float f = s_f[c * kRows + r];
-                        v.x = fmaf(a.x, f, v.x);
-                        v.y = fmaf(a.y, f, v.y);
-                        v.z = fmaf(a.z, f, v.z);
-                        v.w = fmaf(a.w, f, v.w);
+                    for (int c = 0; c < n; c += kBatch) {
+                        float4 a[kBatch];
+#pragma unroll
+                        for (int k = 0; k < kBatch; ++k)
+                            a[k] = live && c + k < n
+                                       ? __ldcg(reinterpret_cast<const float4*>(part_of(cta0 + c + k) + 2 * kRows + x))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (!ready) __syncthreads();  // the factors, while the first parts are on their way
+                        ready = true;
+#pragma unroll
+                        for (int k = 0; k < kBatch; ++k) {
+                            const float f = c + k < n ? s_f[(c + k) * kRows + r] : 0.f;
+                            v.x = fmaf(a[k].x, f, v.x);
+                            v.y = fmaf(a[k].y, f, v.y);
+                            v.z = fmaf(a[k].z, f, v.z);
+                            v.w = fmaf(a[k].w, f, v.w);
+                        }
                     }
-                    finish(r, d, v, s_row[kRows + r], s_row[r]);
+                    if (live) finish(r, d, v, s_row[kRows + r], s_row[r]);
                 }
             }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring is written by copies again
         __syncthreads();
-        off += t1 - t0;
-        left -= t1 - t0;
+        if (chunked) break;
     }
 }
 
-template <int D>
+template <int D, bool Narrow>
 cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, const LaunchCtx& ctx) {
-    cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Decode<D>::kSmem);
+    using C = Decode<D, Narrow>;
+    cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<D, Narrow>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctx.sm_count < kMaxCtas ? ctx.sm_count : kMaxCtas), 1, 1);
-    cfg.blockDim = dim3(Decode<D>::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = Decode<D>::kSmem;
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min(ctx.sm_count * C::kCtas, kMaxCtas)), 1, 1);
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = ctx.stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<D>, p, v, ctx.timeout_ns, ctx.status);
+    return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<D, Narrow>, p, v, ctx.timeout_ns, ctx.status);
+}
+
+template <int D>
+cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, const LaunchCtx& ctx) {
+    const int grp = p.heads / v.kv_heads;
+    const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * grp;
+    const int64_t units = std::min<int64_t>(p.B, p.M) * v.kv_heads * ((rows + kRows - 1) / kRows);
+    return 2 * units <= ctx.sm_count ? launch_decode<D, false>(p, v, ctx) : launch_decode<D, true>(p, v, ctx);
 }
 
 }  // namespace
