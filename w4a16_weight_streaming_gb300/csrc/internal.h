@@ -154,6 +154,6 @@ struct SampleParams {
     int M;
     int V;
 };
-cudaError_t launch_sample(const SampleParams& p, cudaStream_t s, unsigned* status);
+cudaError_t launch_sample(const SampleParams& p, int sm_count, cudaStream_t s);
 
 }  // namespace w4a16

@@ -1133,7 +1133,7 @@ int w4a16_sample(const uint16_t* logits, int64_t stride, int M, int V, const flo
     DeviceInfo d;
     if (!device_info(&d)) return W4A16_ERR_CUDA;
     SampleParams p = {logits, stride, temperature, top_k, top_p, min_p, u, tokens, probs, M, V};
-    return launched(launch_sample(p, static_cast<cudaStream_t>(stream), d.status));
+    return launched(launch_sample(p, d.sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 int w4a16_last_dispatch(char* buf, size_t len) {
