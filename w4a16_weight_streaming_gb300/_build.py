@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(PKG, "libw4a16.so")
 DEBUG_LIB_PATH = os.path.join(PKG, "libw4a16_debug.so")
 
 SOURCES = ["w4a16_api.cu", "repack.cu", "gemv.cu", "tc_gemm.cu", "act.cu", "w4a8.cu", "kv4.cu", "kv4_attn.cu",
-           "sample.cu"]
+           "kv4_prompt.cu", "sample.cu"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "kv4.cuh"), os.path.join(CSRC, "internal.h"), os.path.join(INCLUDE, "w4a16.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]

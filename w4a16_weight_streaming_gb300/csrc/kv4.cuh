@@ -17,6 +17,8 @@
 //     no two tokens share a byte, and tokens may be stored in any order without read-modify-write.
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include "common.cuh"
 
 namespace w4a16 {
@@ -68,5 +70,12 @@ struct Kv4View {
         return (static_cast<int64_t>(num_pages) * kv_heads << (page_shift - 4)) * Kv4<D>::kTileBytes;
     }
 };
+
+// ---- kv4_prompt.cu: the tcgen05 kernel for many query rows a sequence.
+struct Kv4AttnParams;
+struct LaunchCtx;
+constexpr int kKv4MaxPromptCtas = 160;
+size_t kv4_prompt_workspace(int head_dim);
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4View& v, int head_dim, const LaunchCtx& ctx);
 
 }  // namespace w4a16

@@ -56,7 +56,9 @@ struct Decode {
 };
 
 constexpr int kMaxCtas = 640;
-constexpr size_t kCounterBytes = kMaxCtas * 4;
+constexpr int kDecodeRows = 16;  // query rows a key/value head of a sequence, above which the tcgen05 kernel is taken
+constexpr size_t kCounterBytes = 4096;
+static_assert(kMaxCtas * 4 <= kCounterBytes, "a counter a CTA");
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -735,7 +737,8 @@ cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, const Launch
 }  // namespace
 
 size_t kv4_attention_workspace(int head_dim) {
-    return (kCounterBytes + static_cast<size_t>(2 * kMaxCtas) * kRows * (head_dim + 2) * 4 + 15) / 16 * 16;
+    return std::max(kv4_prompt_workspace(head_dim),
+                    kCounterBytes + static_cast<size_t>(2 * kMaxCtas) * kRows * (head_dim + 2) * 4);
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, const Kv4Cache& c, const LaunchCtx& ctx) {
@@ -745,6 +748,8 @@ cudaError_t launch_kv4_attention(const Kv4AttnParams& p, const Kv4Cache& c, cons
     v.page_shift = 0;
     while ((1 << v.page_shift) < c.page_tokens) ++v.page_shift;
     v.kv_heads = c.kv_heads;
+    const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / c.kv_heads);
+    if (rows > kDecodeRows) return launch_kv4_prompt(p, v, c.head_dim, ctx);
     switch (c.head_dim) {
         case 64: return launch_decode<64>(p, v, ctx);
         case 128: return launch_decode<128>(p, v, ctx);

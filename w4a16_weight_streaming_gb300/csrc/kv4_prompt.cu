@@ -1,0 +1,704 @@
+// Attention over the 4-bit paged key/value cache for many query rows a sequence (prompt chunks, verify
+// steps of several positions): o = softmax(scale q k'^T) v' on the tcgen05 tensor cores.
+//
+// A work unit is 128 query rows of one key/value head of one sequence (row r: query r / group, head
+// r % group, so that every head that shares the keys uses one read of them) against the sequence's tokens,
+// 64 at a time:
+//   S[128][64]  = Q[128][D] . K'[64][D]^T      A = Q in TMEM, B = K' in shared memory
+//   O[128][D]  += P[128][64] . V'[64][D]       A = P in TMEM (over S), B = V'^T in shared memory
+// K' and V' are the stored values rounded to fp16 once (fma(code, scale, min)), written by dequantisation
+// warps in the matrix instruction's 128-byte-swizzled layouts straight from the cache's lane order: a K
+// word is 16 bytes of one token's row, a V word four pairs of tokens in rows of elements. With Q in TMEM a
+// tile reads 64 KB of operands from shared memory for 1077 cycles of tensor work (D = 256), which leaves
+// room for the dequantised stores; with Q in shared memory it would be 128 KB.
+//
+// Warps: 0-3 softmax, a row a thread (the running maximum moves, and O is rescaled in TMEM, only when a
+// score exceeds it by 2^8); 4-11 dequantise, a 16-token quarter of the tile's keys or values each; 12
+// fetches the cache's tiles by bulk copies; 13 issues S, 14 issues PV (one thread issues an instruction
+// every 45-55 cycles, too few for the 16 of S and the 4 of PV). K', V' and S/P are double-buffered: S of
+// tile i + 1 and the dequantisation of i + 2 run beside the softmax of i.
+//
+// Work is a list of (unit, tile); every CTA takes an equal run. Units that a run's end cuts leave parts
+// (maximum, sum, unnormalised rows) in the workspace; the CTA that arrives last adds them in CTA order.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "kv4.cuh"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kRows = 128;     // query rows of a unit
+constexpr int kTok = 64;       // tokens of a tile
+constexpr int kSub = kTok / kKv4Tile;
+constexpr int kUnitCost = 6;   // what the start and end of a unit cost, in tiles
+constexpr int kMinRun = 12;    // tiles; fewer make more parts than they save
+constexpr int kWarps = 15;
+constexpr int kThreads = kWarps * 32;
+constexpr int kProducer = 12, kIssueS = 13;  // (14: PV)
+constexpr int kNotes = 16;     // tiles whose page validity is kept
+
+template <int D>
+struct Prompt {
+    static constexpr int kRaw = kSub * Kv4<D>::kTileBytes;
+    static constexpr int kRawStages = D == 256 ? 3 : 4;
+    static constexpr int kBuf = kTok * D * 2;  // one K' or V' buffer
+    static constexpr int kOffV = 2 * kBuf;
+    static constexpr int kOffRaw = 4 * kBuf;
+    static constexpr int kOffBars = kOffRaw + kRawStages * kRaw;
+    static constexpr int kBars = 2 * kRawStages + 2 * 5 + 1;
+    static constexpr int kOffMisc = kOffBars + kBars * 8;
+    static constexpr int kSmem = kOffMisc + 256 + 1024;  // + alignment
+    static constexpr uint32_t kColS = D, kColQ = D + 2 * kTok;
+    static constexpr uint32_t kCols = D == 64 ? 256 : 512;
+    static constexpr int kPart = kRows * (D + 2);  // floats of one workspace part: m, l, then [D / 4][128] float4
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 32 consecutive TMEM columns of a warp's 32 lanes
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t a) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+
+// The codes of a word as fp16 pairs, exact: out[i] = (nibble i, nibble i + 4).
+__device__ __forceinline__ void codes(uint32_t w, uint32_t (&out)[4]) {
+    constexpr uint32_t kMagic = 0x64006400u, kNeg1024 = 0xE400E400u, kSixteenth = 0x2C002C00u, kNeg64 = 0xD400D400u;
+    const uint32_t hi = w >> 8;
+    out[0] = hadd2(and_or(w, 0x000F000Fu, kMagic), kNeg1024);
+    out[1] = hfma2(and_or(w, 0x00F000F0u, kMagic), kSixteenth, kNeg64);
+    out[2] = hadd2(and_or(hi, 0x000F000Fu, kMagic), kNeg1024);
+    out[3] = hfma2(and_or(hi, 0x00F000F0u, kMagic), kSixteenth, kNeg64);
+}
+
+template <int G>
+__device__ __forceinline__ void lds_params(uint32_t addr, uint32_t (&p)[G]) {
+    if constexpr (G == 4) {
+        const uint4 v = lds128(addr);
+        p[0] = v.x;
+        p[1] = v.y;
+        p[2] = v.z;
+        p[3] = v.w;
+    } else if constexpr (G == 2) {
+        const uint2 v = lds64(addr);
+        p[0] = v.x;
+        p[1] = v.y;
+    } else {
+        p[0] = lds32(addr);
+    }
+}
+
+struct PromptSeq {
+    int q0, q_len, n, grp, row_tiles;
+    bool bad;
+    // tokens that query row r (within the sequence) sees
+    __device__ __forceinline__ int seen(int r, int causal) const {
+        return causal ? max(0, n - (q_len - 1 - r / grp)) : n;
+    }
+    // tiles of a row tile (its last row sees most); at least one, so that empty rows are written
+    __device__ __forceinline__ int tiles(int rt, int causal) const {
+        const int last = min(q_len * grp, (rt + 1) * kRows) - 1;
+        return max(1, (seen(last, causal) + kTok - 1) / kTok);
+    }
+    // work of one key/value head
+    __device__ __forceinline__ int64_t cost(int causal) const {
+        if (!causal) return static_cast<int64_t>(row_tiles) * (tiles(0, 0) + kUnitCost);
+        int64_t c = 0;
+        for (int rt = 0; rt < row_tiles; ++rt) c += tiles(rt, 1) + kUnitCost;
+        return c;
+    }
+};
+
+__device__ __forceinline__ PromptSeq seq_of(const Kv4AttnParams& p, const Kv4View& c, int b) {
+    PromptSeq s;
+    const int q0 = p.q_start[b], q1 = p.q_start[b + 1], n = p.kv_len[b];
+    s.q0 = min(max(q0, 0), p.M);
+    const int end = min(max(q1, s.q0), p.M);
+    s.q_len = end - s.q0;
+    s.n = min(max(n, 0), p.max_pages << c.page_shift);
+    s.bad = s.q0 != q0 || end != q1 || s.n != n;
+    s.grp = p.heads / c.kv_heads;
+    s.row_tiles = (s.q_len * s.grp + kRows - 1) / kRows;
+    return s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv4_prompt_kernel(const Kv4AttnParams p, const Kv4View cache, uint64_t timeout_ns, unsigned* status) {
+    using C = Prompt<D>;
+    using T = Kv4<D>;
+    constexpr int G = T::kGroups, R = C::kRawStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
+    int* s_misc = reinterpret_cast<int*>(smem + C::kOffMisc);
+    int* s_abort = s_misc;
+    int* s_last = s_misc + 1;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_misc + 2);
+    int* s_first = s_misc + 3;
+    int64_t* s_plan = reinterpret_cast<int64_t*>(s_misc + 4);      // run begin, end, length; first sequence's place
+    uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_misc + 12);  // [kNotes]: valid tokens of each quarter, a byte each
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t bars = base + C::kOffBars;
+    auto raw_full = [&](int s) { return bars + 8 * s; };
+    auto raw_empty = [&](int s) { return bars + 8 * (R + s); };
+    auto k_full = [&](int s) { return bars + 8 * (2 * R + s); };
+    auto v_full = [&](int s) { return bars + 8 * (2 * R + 2 + s); };
+    auto s_full = [&](int s) { return bars + 8 * (2 * R + 4 + s); };   // S in TMEM, K' free
+    auto p_full = [&](int s) { return bars + 8 * (2 * R + 6 + s); };
+    auto pv_done = [&](int s) { return bars + 8 * (2 * R + 8 + s); };  // O updated, V' and S/P free
+    const uint32_t q_full = bars + 8 * (2 * R + 10);
+    auto wait = [&](uint32_t bar, uint32_t parity) { return warp_spin(bar, parity, s_abort, timeout_ns, status); };
+
+    if (warp == kProducer) {
+        if (lane == 0) {
+            for (int i = 0; i < R; ++i) {
+                mbar_init(raw_full(i), 1);
+                mbar_init(raw_empty(i), 8);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(k_full(i), 4);
+                mbar_init(v_full(i), 4);
+                mbar_init(s_full(i), 1);
+                mbar_init(p_full(i), 4);
+                mbar_init(pv_done(i), 1);
+            }
+            mbar_init(q_full, 4);
+            *s_abort = 0;
+            fence_barrier_init();
+        }
+        __syncwarp();
+        tmem_alloc(smem_u32(s_tmem), C::kCols);
+        tmem_relinquish();
+    }
+    griddep_wait();
+
+    // ---- this CTA's run of the work list
+    if (warp == 0) {
+        int64_t total = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int64_t c = 0;
+            if (b0 + lane < p.B) {
+                const PromptSeq s = seq_of(p, cache, b0 + lane);
+                c = s.cost(p.causal) * cache.kv_heads;
+                if (s.bad && blockIdx.x == 0) record_error(status, kErrBounds);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+            total += c;
+        }
+        const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinRun + kUnitCost));
+        const int64_t w0 = min(total, per * blockIdx.x), w1 = min(total, w0 + per);
+        int64_t at = 0;
+        int first = p.B;
+        for (int b0 = 0; b0 < p.B && w0 < w1; b0 += 32) {
+            int64_t c = 0;
+            if (b0 + lane < p.B) c = seq_of(p, cache, b0 + lane).cost(p.causal) * cache.kv_heads;
+            int64_t upto = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, at + upto > w0);
+            if (hit != 0) {
+                const int l = __ffs(hit) - 1;
+                first = b0 + l;
+                at += __shfl_sync(0xffffffffu, upto - c, l);
+                break;
+            }
+            at += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        if (lane == 0) {
+            s_plan[0] = w0;
+            s_plan[1] = w1;
+            s_plan[2] = per;
+            s_plan[3] = at;
+            *s_first = first;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_launch_dependents();  // (after the allocation: the next grid's cannot come before it)
+    const uint32_t tmem = *s_tmem;
+    const int64_t w0 = s_plan[0], w1 = s_plan[1], per = s_plan[2];
+    int64_t at = s_plan[3];  // work list position of the current unit
+    uint32_t done = 0;       // tiles of earlier segments
+    uint32_t segment = 0;
+
+    for (int b = *s_first, kvh = 0, rt = 0; at < w1 && b < p.B;) {
+        const PromptSeq sq = seq_of(p, cache, b);
+        if (rt >= sq.row_tiles) {
+            rt = 0;
+            if (++kvh >= cache.kv_heads || sq.row_tiles == 0) {
+                kvh = 0;
+                ++b;
+            }
+            continue;
+        }
+        if (rt == 0) {  // whole heads before the run
+            const int64_t head_cost = sq.cost(p.causal);
+            if (at + head_cost <= w0) {
+                at += head_cost;
+                rt = sq.row_tiles;
+                continue;
+            }
+        }
+        const int tiles = sq.tiles(rt, p.causal);
+        const int64_t unit_at = at, each = tiles + kUnitCost;
+        const int row0 = rt * kRows;
+        const int t0 = static_cast<int>(min(static_cast<int64_t>(tiles), max(static_cast<int64_t>(0), w0 - unit_at - kUnitCost)));
+        const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), max(static_cast<int64_t>(0), w1 - unit_at - kUnitCost)));
+        at += each;
+        ++rt;
+        if (t0 >= t1) continue;
+        const int nt = t1 - t0;
+        const int cta0 = static_cast<int>((unit_at + kUnitCost) / per), cta1 = static_cast<int>((unit_at + each - 1) / per);
+        const int rows = min(kRows, sq.q_len * sq.grp - row0);
+        const bool whole = t0 == 0 && t1 == tiles;
+
+        if (warp < 4) {
+            // ================= softmax: row `r` of the unit
+            const int r = warp * 32 + lane;
+            const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);  // this warp's 32 lanes
+            const bool idle = warp * 32 >= rows;
+            const int pos = (row0 + min(r, rows - 1)) / sq.grp, hd = (row0 + min(r, rows - 1)) % sq.grp;
+            const int64_t q_row = sq.q0 + pos;
+            const int head = kvh * sq.grp + hd;
+            {
+                const uint16_t* src = p.q + q_row * p.q_stride + static_cast<int64_t>(head) * D;
+                const uint32_t sign = p.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (r < rows) x = *reinterpret_cast<const uint4*>(src + c * 64 + i * 8);
+                        v[4 * i] = x.x ^ sign;
+                        v[4 * i + 1] = x.y ^ sign;
+                        v[4 * i + 2] = x.z ^ sign;
+                        v[4 * i + 3] = x.w ^ sign;
+                    }
+                    tmem_st<32>(lanes + C::kColQ + 32 * c, v);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+            }
+            const float c1 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
+            const int lim = sq.seen(row0 + min(r, rows - 1), p.causal);
+            const int lim_min = sq.seen(row0 + min(warp * 32, rows - 1), p.causal);
+            float m = -INFINITY, l = 0.f;
+            bool ok = true;
+            for (int i = 0; i < nt && ok; ++i) {
+                const uint32_t it = done + i, buf = it & 1, ph = (it >> 1) & 1;
+                ok = wait(s_full(buf), ph);
+                if (!ok) break;
+                if (!idle) {
+                    tc_fence_after();
+                    float s[2][32];
+                    tmem_ld32(lanes + C::kColS + buf * kTok, s[0]);
+                    tmem_ld32(lanes + C::kColS + buf * kTok + 32, s[1]);
+                    tmem_wait_ld();
+                    const int tok = (t0 + i) * kTok;
+                    const uint32_t valid = s_valid[it % kNotes];
+                    if (tok + kTok > lim_min || valid != 0x10101010u) {
+#pragma unroll
+                        for (int j = 0; j < kTok; ++j) {
+                            const int there = static_cast<int>((valid >> (8 * (j / 16))) & 255u);
+                            if (tok + j >= lim || (j & 15) >= there) s[j / 32][j % 32] = -INFINITY;
+                        }
+                    }
+                    float mx = s[0][0];
+#pragma unroll
+                    for (int j = 1; j < kTok; ++j) mx = fmaxf(mx, s[j / 32][j % 32]);
+                    mx *= c1;
+                    if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+                        const float now = fmaxf(m, mx), f = m == now ? 1.f : ex2(m - now);
+                        m = now;
+                        l *= f;
+                        if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                            const uint32_t before = it - 1;
+                            ok = wait(pv_done(before & 1), (before >> 1) & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                float v[32];
+                                tmem_ld32(lanes + c, v);
+                                tmem_wait_ld();
+                                uint32_t u[32];
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(v[j] * f);
+                                tmem_st<32>(lanes + c, u);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float sub = m == -INFINITY ? 0.f : m;
+                    uint32_t pk[32];
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float a = ex2(fmaf(s[j / 16][2 * j % 32], c1, -sub)), e = ex2(fmaf(s[j / 16][2 * j % 32 + 1], c1, -sub));
+                        sum += a + e;
+                        const __half2 h = __floats2half2_rn(a, e);
+                        pk[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    l += sum;
+                    tmem_st<32>(lanes + C::kColS + buf * kTok, pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(buf));
+            }
+            // ---- the unit's rows, or this CTA's part of them
+            if (ok) {
+                const uint32_t end = done + nt - 1;
+                ok = wait(pv_done(end & 1), (end >> 1) & 1);
+            }
+            if (ok && !idle) {
+                tc_fence_after();
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + 4096) +
+                              static_cast<int64_t>(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * C::kPart;
+                uint16_t* out = p.out + (q_row * p.heads + head) * D;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float v[32];
+                    tmem_ld32(lanes + c, v);
+                    tmem_wait_ld();
+                    if (whole) {
+                        if (r < rows) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t h[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const __half2 x = __floats2half2_rn(l > 0.f ? v[8 * j + 2 * k] * inv : 0.f,
+                                                                        l > 0.f ? v[8 * j + 2 * k + 1] * inv : 0.f);
+                                    h[k] = *reinterpret_cast<const uint32_t*>(&x);
+                                }
+                                *reinterpret_cast<uint4*>(out + c + 8 * j) = make_uint4(h[0], h[1], h[2], h[3]);
+                            }
+                        }
+                    } else if (r < rows) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            __stcg(reinterpret_cast<float4*>(part + 2 * kRows) + (c / 4 + j) * kRows + r,
+                                   make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+                    }
+                }
+                if (r < rows) {
+                    if (!whole) {
+                        __stcg(part + r, m);
+                        __stcg(part + kRows + r, l);
+                    } else if (p.lse != nullptr) {
+                        p.lse[q_row * p.heads + head] = l > 0.f ? 0.6931471805599453f * (m + log2f(l)) : -INFINITY;
+                    }
+                }
+                tc_fence_before();
+            }
+        } else if (warp < kProducer) {
+            // ================= dequantise: keys (warps 4-7) or values (8-11) of quarter `sub`
+            const int sub = warp & 3;
+            const bool is_k = warp < 8;
+            const int g = lane >> 2, t = lane & 3;
+            for (int i = 0; i < nt; ++i) {
+                const uint32_t it = done + i, st = it % R, buf = it & 1, use = it >> 1;
+                if (!wait(raw_full(st), (it / R) & 1)) break;
+                if (!wait(is_k ? s_full(buf) : pv_done(buf), (use & 1) ^ 1)) break;
+                const uint32_t tile = base + C::kOffRaw + st * C::kRaw + sub * T::kTileBytes;
+                const int there = static_cast<int>((s_valid[it % kNotes] >> (8 * sub)) & 255u);
+                if (is_k) {
+                    uint32_t sc[2][G], mn[2][G];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pr[G];
+                        lds_params<G>(tile + T::kKParams + (8 * h + g) * G * 4, pr);
+#pragma unroll
+                        for (int y = 0; y < G; ++y) {
+                            if (8 * h + g >= there) pr[y] = 0;
+                            sc[h][y] = __byte_perm(pr[y], 0, 0x1010);
+                            mn[h][y] = __byte_perm(pr[y], 0, 0x3232);
+                        }
+                    }
+                    const uint32_t to = base + buf * C::kBuf;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = sub * 16 + 8 * h + g;
+                        const uint32_t row_at = to + row * 128;
+                        auto put = [&](int y, int w, uint32_t word) {
+                            uint32_t q[4];
+                            codes(word, q);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) q[x] = hfma2(q[x], sc[h][y], mn[h][y]);
+                            sts128(row_at + y * (kTok * 128) + (((2 * t + w) ^ (row & 7)) << 4), q[0], q[1], q[2], q[3]);
+                        };
+                        if constexpr (G == 1) {
+                            const uint2 v = lds64(tile + (h * 32 + lane) * 8);
+                            put(0, 0, v.x);
+                            put(0, 1, v.y);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < G / 2; ++j) {
+                                const uint4 v = lds128(tile + ((2 * j + h) * 32 + lane) * 16);
+                                put(2 * j, 0, v.x);
+                                put(2 * j, 1, v.y);
+                                put(2 * j + 1, 0, v.z);
+                                put(2 * j + 1, 1, v.w);
+                            }
+                        }
+                    }
+                } else {
+                    uint32_t pr[4][G];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int token = 2 * t + (k & 1) + 8 * (k >> 1);
+                        lds_params<G>(tile + T::kVParams + token * G * 4, pr[k]);
+                        if (token >= there) {
+#pragma unroll
+                            for (int y = 0; y < G; ++y) pr[k][y] = 0;
+                        }
+                    }
+                    const uint32_t to = base + C::kOffV + buf * C::kBuf + t * 4;
+#pragma unroll
+                    for (int y = 0; y < G; ++y) {
+                        const uint32_t sa = __byte_perm(pr[0][y], pr[1][y], 0x5410), ma = __byte_perm(pr[0][y], pr[1][y], 0x7632);
+                        const uint32_t sb = __byte_perm(pr[2][y], pr[3][y], 0x5410), mb = __byte_perm(pr[2][y], pr[3][y], 0x7632);
+                        const uint4 v = lds128(tile + T::kV + y * 512 + lane * 16);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t q[4];
+                            codes(w[x], q);
+                            const uint32_t row = to + (64 * y + 16 * x + g) * 128;
+                            const uint32_t c0 = ((2 * sub) ^ g) << 4, c8 = ((2 * sub + 1) ^ g) << 4;
+                            sts32(row + c0, hfma2(q[0], sa, ma));
+                            sts32(row + 1024 + c0, hfma2(q[1], sa, ma));
+                            sts32(row + c8, hfma2(q[2], sb, mb));
+                            sts32(row + 1024 + c8, hfma2(q[3], sb, mb));
+                        }
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(is_k ? k_full(buf) : v_full(buf));
+                    mbar_arrive(raw_empty(st));
+                }
+            }
+        } else if (warp == kProducer) {
+            // ================= fetch: four 16-token tiles a stage, page numbers of 8 stages at a time
+            const uint64_t policy = policy_evict_last();
+            int64_t from = -1;
+            int there = 0;
+            for (int i = 0; i < nt; ++i) {
+                const uint32_t it = done + i, st = it % R;
+                if ((i & 7) == 0) {
+                    const int tok = (t0 + i) * kTok + lane * kKv4Tile;
+                    there = max(0, min(kKv4Tile, sq.n - tok));
+                    from = -1;
+                    if (there > 0 && i + lane / kSub < nt) {
+                        const int page = p.block_table[static_cast<int64_t>(b) * p.max_pages + (tok >> cache.page_shift)];
+                        if (page >= 0 && page < cache.num_pages) {
+                            from = cache.tile_offset<D>(page, kvh, tok & ((1 << cache.page_shift) - 1));
+                            if (!in_bounds(from >= 0 && from + T::kTileBytes <= cache.bytes<D>(), status)) from = -1;
+                        } else {
+                            record_error(status, kErrBounds);
+                        }
+                    }
+                }
+                if (!wait(raw_empty(st), ((it / R) & 1) ^ 1)) break;
+                const bool mine = lane / kSub == (i & 7) && from >= 0;
+                const uint32_t have = __ballot_sync(0xffffffffu, mine);
+                uint32_t note = lane / kSub == (i & 7) && from >= 0 ? static_cast<uint32_t>(there) << (8 * (lane % kSub)) : 0u;
+                note = __reduce_or_sync(0xffffffffu, note);
+                if (lane == 0) {
+                    s_valid[it % kNotes] = note;
+                    mbar_arrive_expect_tx(raw_full(st), static_cast<uint32_t>(__popc(have)) * T::kTileBytes);
+                }
+                __syncwarp();
+                if (mine)
+                    bulk_g2s(base + C::kOffRaw + st * C::kRaw + (lane % kSub) * T::kTileBytes, cache.pages + from, T::kTileBytes,
+                             raw_full(st), policy);
+            }
+        } else if (warp == kIssueS) {
+            // ================= S = Q . K'^T
+            constexpr uint32_t idesc = idesc_f16_f32(128, kTok);
+            bool ok = wait(q_full, segment & 1);
+            for (int i = 0; i < nt && ok; ++i) {
+                const uint32_t it = done + i, buf = it & 1, use = it >> 1;
+                ok = wait(k_full(buf), use & 1) && wait(pv_done(buf), (use & 1) ^ 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t desc = smem_desc_sw128(base + buf * C::kBuf + (k / 4) * (kTok * 128)) + (k & 3) * 2;
+                        umma_f16_ts(tmem + C::kColS + buf * kTok, tmem + C::kColQ + 8 * k, desc, idesc, k > 0);
+                    }
+                    umma_commit(s_full(buf));
+                }
+                __syncwarp();
+            }
+        } else {
+            // ================= O += P . V'
+            constexpr uint32_t idesc = idesc_f16_f32(128, D);
+            for (int i = 0; i < nt; ++i) {
+                const uint32_t it = done + i, buf = it & 1, use = it >> 1;
+                if (!wait(v_full(buf), use & 1) || !wait(p_full(buf), use & 1)) break;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < kTok / 16; ++k) {
+                        const uint64_t desc = smem_desc_sw128(base + C::kOffV + buf * C::kBuf) + k * 2;
+                        umma_f16_ts(tmem, tmem + C::kColS + buf * kTok + 8 * k, desc, idesc, i > 0 || k > 0);
+                    }
+                    umma_commit(pv_done(buf));
+                }
+                __syncwarp();
+            }
+        }
+        done += nt;
+        ++segment;
+
+        if (!whole) {
+            // ---- the last CTA of the unit to arrive adds its parts in CTA order
+            float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + 4096);
+            auto part_of = [&](int c) { return parts + static_cast<int64_t>(2 * c + (c == cta0 ? 1 : 0)) * C::kPart; };
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                unsigned* counter = static_cast<unsigned*>(p.workspace) + cta0;
+                const unsigned before = atomicAdd(counter, 1u);
+                *s_last = before == static_cast<unsigned>(cta1 - cta0);
+                if (*s_last) *counter = 0;
+            }
+            __syncthreads();
+            if (*s_last && !*s_abort) {
+                __threadfence();
+                // threads in groups of 128: a row each, columns of four in turn
+                const int r = tid & (kRows - 1), first = tid / kRows, step = 3;
+                if (first < step && r < rows) {
+                    float top = -INFINITY, total = 0.f;
+                    for (int c = cta0; c <= cta1; ++c) top = fmaxf(top, __ldcg(part_of(c) + r));
+                    for (int c = cta0; c <= cta1; ++c) {
+                        const float m = __ldcg(part_of(c) + r);
+                        total += m == -INFINITY ? 0.f : __ldcg(part_of(c) + kRows + r) * ex2(m - top);
+                    }
+                    const int pos = (row0 + r) / sq.grp, hd = (row0 + r) % sq.grp;
+                    const int64_t at_out = (static_cast<int64_t>(sq.q0 + pos) * p.heads + kvh * sq.grp + hd);
+                    const float inv = total > 0.f ? 1.f / total : 0.f;
+                    for (int c4 = first; c4 < D / 4; c4 += 4 * step) {
+                        float4 v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int c = cta0; c <= cta1; ++c) {
+                            const float m = __ldcg(part_of(c) + r);
+                            const float f = m == -INFINITY ? 0.f : ex2(m - top);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (c4 + k * step >= D / 4) break;
+                                const float4 a = __ldcg(reinterpret_cast<const float4*>(part_of(c) + 2 * kRows) + (c4 + k * step) * kRows + r);
+                                if (m == -INFINITY) continue;  // (its sums are of nothing)
+                                v[k].x = fmaf(a.x, f, v[k].x);
+                                v[k].y = fmaf(a.y, f, v[k].y);
+                                v[k].z = fmaf(a.z, f, v[k].z);
+                                v[k].w = fmaf(a.w, f, v[k].w);
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (c4 + k * step >= D / 4) break;
+                            const __half2 h0 = __floats2half2_rn(v[k].x * inv, v[k].y * inv), h1 = __floats2half2_rn(v[k].z * inv, v[k].w * inv);
+                            *reinterpret_cast<uint2*>(p.out + at_out * D + 4 * (c4 + k * step)) =
+                                make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+                        }
+                    }
+                    if (first == 0 && p.lse != nullptr)
+                        p.lse[at_out] = total > 0.f ? 0.6931471805599453f * (top + log2f(total)) : -INFINITY;
+                }
+            }
+        }
+        __syncthreads();  // Q, O and the barriers' phases belong to the next segment from here on
+        if (*s_abort) break;
+    }
+    if (*s_abort) {  // copies still under way land before the memory is given back (bounded)
+        for (int i = 0; i < R; ++i)
+            for (int n = 0; n < 65536 && !mbar_test_wait(raw_full(i), 0) && !mbar_test_wait(raw_full(i), 1); ++n) {
+            }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kProducer) tmem_dealloc(tmem, C::kCols);
+}
+
+template <int D>
+cudaError_t launch_prompt(const Kv4AttnParams& p, const Kv4View& v, const LaunchCtx& ctx) {
+    using C = Prompt<D>;
+    cudaError_t e = cudaFuncSetAttribute(kv4_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min(ctx.sm_count, kKv4MaxPromptCtas)), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_prompt_kernel<D>, p, v, ctx.timeout_ns, ctx.status);
+}
+
+}  // namespace
+
+size_t kv4_prompt_workspace(int head_dim) {
+    return 4096 + static_cast<size_t>(2 * kKv4MaxPromptCtas) * kRows * (head_dim + 2) * 4;
+}
+
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4View& v, int head_dim, const LaunchCtx& ctx) {
+    switch (head_dim) {
+        case 64: return launch_prompt<64>(p, v, ctx);
+        case 128: return launch_prompt<128>(p, v, ctx);
+        default: return launch_prompt<256>(p, v, ctx);
+    }
+}
+
+}  // namespace w4a16
