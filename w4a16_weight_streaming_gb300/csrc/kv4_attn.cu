@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
             const bool have = (there >> st) & 1u;
             const uint32_t tile_s = ring + st * C::kTile;
             if (have) {
-                if (!warp_spin(bars + 8 * st, (phase >> st) & 1u, s_abort, timeout_ns, status)) {
+                if (!warp_suspend(bars + 8 * st, (phase >> st) & 1u, s_abort, timeout_ns, status)) {
                     // give up: let the copies in flight land (bounded) before their memory is used again
                     for (int k = 0; k < S; ++k)
                         for (int n = 0; n < 65536 && !mbar_test_wait(bars + 8 * k, (phase >> k) & 1u); ++n) {

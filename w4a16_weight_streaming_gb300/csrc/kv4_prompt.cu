@@ -12,10 +12,10 @@
 // tile reads 64 KB of operands from shared memory for 1077 cycles of tensor work (D = 256), which leaves
 // room for the dequantised stores; with Q in shared memory it would be 128 KB.
 //
-// Warps: 0-3 softmax, a row a thread (the running maximum moves, and O is rescaled in TMEM, only when a
-// score exceeds it by 2^8); 4-11 dequantise, a 16-token quarter of the tile's keys or values each; 12
-// fetches the cache's tiles by bulk copies; 13 issues S, 14 issues PV (one thread issues an instruction
-// every 45-55 cycles, too few for the 16 of S and the 4 of PV). K', V' and S/P are double-buffered: S of
+// Warps: 0-7 softmax, half a row a thread (the running maximum moves, and O is rescaled in TMEM, only when
+// a score exceeds it by 2^8; the two warps of 32 rows meet at a barrier once a tile); 8-23 dequantise, half
+// of a 16-token quarter of the tile's keys or values each; 24 fetches the cache's tiles by bulk copies; 25
+// issues S, 26 issues PV. K', V' and S/P are double-buffered: S of
 // tile i + 1 and the dequantisation of i + 2 run beside the softmax of i.
 //
 // Work is a list of (unit, tile); every CTA takes an equal run. Units that a run's end cuts leave parts
@@ -34,9 +34,10 @@ constexpr int kTok = 64;       // tokens of a tile
 constexpr int kSub = kTok / kKv4Tile;
 constexpr int kUnitCost = 6;   // what the start and end of a unit cost, in tiles
 constexpr int kMinRun = 12;    // tiles; fewer make more parts than they save
-constexpr int kWarps = 15;
+constexpr int kDequant = 8;    // first warp of each role (softmax: 0)
+constexpr int kProducer = 24, kIssueS = 25;
+constexpr int kWarps = 27;     // (26: PV)
 constexpr int kThreads = kWarps * 32;
-constexpr int kProducer = 12, kIssueS = 13;  // (14: PV)
 constexpr int kNotes = 16;     // tiles whose page validity is kept
 
 template <int D>
@@ -49,11 +50,20 @@ struct Prompt {
     static constexpr int kOffBars = kOffRaw + kRawStages * kRaw;
     static constexpr int kBars = 2 * kRawStages + 2 * 5 + 1;
     static constexpr int kOffMisc = kOffBars + kBars * 8;
-    static constexpr int kSmem = kOffMisc + 256 + 1024;  // + alignment
+    static constexpr int kSmem = kOffMisc + 256 + 2 * kRows * 4 + 1024;  // + alignment
     static constexpr uint32_t kColS = D, kColQ = D + 2 * kTok;
     static constexpr uint32_t kCols = D == 64 ? 256 : 512;
     static constexpr int kPart = kRows * (D + 2);  // floats of one workspace part: m, l, then [D / 4][128] float4
 };
+
+// One lane of a converged warp, in a form from which the compiler sees that a single thread runs what it
+// guards: a tcgen05.mma of 64 columns is then issued every 32-42 cycles (its execution time), against 64-80
+// under a comparison of the lane number.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 r;\n\telect.sync r|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -72,6 +82,25 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
           "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(taddr)
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+// Whether the predicate holds for any of the 64 threads that meet at named barrier `id`.
+__device__ __forceinline__ bool any_of_64(int id, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\tbarrier.red.or.pred po, %2, 64, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+        : "=r"(r)
+        : "r"(pred ? 1u : 0u), "r"(id)
+        : "memory");
+    return r != 0;
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -130,12 +159,18 @@ struct PromptSeq {
         const int last = min(q_len * grp, (rt + 1) * kRows) - 1;
         return max(1, (seen(last, causal) + kTok - 1) / kTok);
     }
-    // work of one key/value head
-    __device__ __forceinline__ int64_t cost(int causal) const {
-        if (!causal) return static_cast<int64_t>(row_tiles) * (tiles(0, 0) + kUnitCost);
-        int64_t c = 0;
-        for (int rt = 0; rt < row_tiles; ++rt) c += tiles(rt, 1) + kUnitCost;
-        return c;
+    // The work list's unit is 1 / grp of a token: row tile rt takes a fixed cost, then no less than its
+    // tokens, grows by kRows from one row tile to the next (causal), and so has a sum in closed form. Its
+    // tile t begins at fixed() + t * grp * kTok.
+    __device__ __forceinline__ int64_t fixed() const { return static_cast<int64_t>(grp) * kTok * kUnitCost; }
+    __device__ __forceinline__ int64_t flat(int causal) const {
+        return fixed() + static_cast<int64_t>(grp) * (causal ? max(n - q_len, 0) + 1 : max(n, 1));
+    }
+    __device__ __forceinline__ int64_t length(int rt, int causal) const {
+        return flat(causal) + (causal ? static_cast<int64_t>(rt + 1) * kRows : 0);
+    }
+    __device__ __forceinline__ int64_t before(int rt, int causal) const {  // of row tiles 0 .. rt-1 of one head
+        return rt * flat(causal) + (causal ? static_cast<int64_t>(rt) * (rt + 1) / 2 * kRows : 0);
     }
 };
 
@@ -168,7 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* s_first = s_misc + 3;
     int64_t* s_plan = reinterpret_cast<int64_t*>(s_misc + 4);      // run begin, end, length; first sequence's place
     uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_misc + 12);  // [kNotes]: valid tokens of each quarter, a byte each
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float* s_half = reinterpret_cast<float*>(smem + C::kOffMisc + 256);  // [2][128]: what two halves of a row exchange
+    volatile int* s_left = s_misc + 32;  // [8]: softmax warps whose wait ran out
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t bars = base + C::kOffBars;
     auto raw_full = [&](int s) { return bars + 8 * s; };
     auto raw_empty = [&](int s) { return bars + 8 * (R + s); };
@@ -178,22 +215,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto p_full = [&](int s) { return bars + 8 * (2 * R + 6 + s); };
     auto pv_done = [&](int s) { return bars + 8 * (2 * R + 8 + s); };  // O updated, V' and S/P free
     const uint32_t q_full = bars + 8 * (2 * R + 10);
-    auto wait = [&](uint32_t bar, uint32_t parity) { return warp_spin(bar, parity, s_abort, timeout_ns, status); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return warp_suspend(bar, parity, s_abort, timeout_ns, status); };
 
     if (warp == kProducer) {
         if (lane == 0) {
             for (int i = 0; i < R; ++i) {
                 mbar_init(raw_full(i), 1);
-                mbar_init(raw_empty(i), 8);
+                mbar_init(raw_empty(i), 16);
             }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(k_full(i), 4);
-                mbar_init(v_full(i), 4);
+                mbar_init(k_full(i), 8);
+                mbar_init(v_full(i), 8);
                 mbar_init(s_full(i), 1);
-                mbar_init(p_full(i), 4);
+                mbar_init(p_full(i), 8);
                 mbar_init(pv_done(i), 1);
             }
-            mbar_init(q_full, 4);
+            mbar_init(q_full, 8);
             *s_abort = 0;
             fence_barrier_init();
         }
@@ -210,20 +247,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             int64_t c = 0;
             if (b0 + lane < p.B) {
                 const PromptSeq s = seq_of(p, cache, b0 + lane);
-                c = s.cost(p.causal) * cache.kv_heads;
+                c = s.before(s.row_tiles, p.causal) * cache.kv_heads;
                 if (s.bad && blockIdx.x == 0) record_error(status, kErrBounds);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
             total += c;
         }
-        const int64_t per = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinRun + kUnitCost));
+        const int64_t per = max((total + gridDim.x - 1) / gridDim.x,
+                                static_cast<int64_t>(kMinRun + kUnitCost) * kTok * (p.heads / cache.kv_heads));
         const int64_t w0 = min(total, per * blockIdx.x), w1 = min(total, w0 + per);
         int64_t at = 0;
         int first = p.B;
         for (int b0 = 0; b0 < p.B && w0 < w1; b0 += 32) {
             int64_t c = 0;
-            if (b0 + lane < p.B) c = seq_of(p, cache, b0 + lane).cost(p.causal) * cache.kv_heads;
+            if (b0 + lane < p.B) {
+                const PromptSeq s = seq_of(p, cache, b0 + lane);
+                c = s.before(s.row_tiles, p.causal) * cache.kv_heads;
+            }
             int64_t upto = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -240,11 +281,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             at += __shfl_sync(0xffffffffu, upto, 31);
         }
         if (lane == 0) {
+            int kvh = 0, rt = 0;
+            if (first < p.B) {  // the unit that the run begins in
+                const PromptSeq s = seq_of(p, cache, first);
+                const int64_t head = s.before(s.row_tiles, p.causal);
+                kvh = static_cast<int>((w0 - at) / head);
+                at += kvh * head;
+                int hi = s.row_tiles - 1;
+                while (rt < hi) {
+                    const int mid = (rt + hi + 1) / 2;
+                    if (at + s.before(mid, p.causal) <= w0) rt = mid;
+                    else hi = mid - 1;
+                }
+                at += s.before(rt, p.causal);
+            }
             s_plan[0] = w0;
             s_plan[1] = w1;
             s_plan[2] = per;
             s_plan[3] = at;
-            *s_first = first;
+            s_first[0] = first;
+            s_first[8 + kNotes + 1] = kvh;
+            s_first[8 + kNotes + 2] = rt;
         }
     }
     tc_fence_before();
@@ -254,64 +311,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *s_tmem;
     const int64_t w0 = s_plan[0], w1 = s_plan[1], per = s_plan[2];
     int64_t at = s_plan[3];  // work list position of the current unit
+    int b = s_first[0], kvh = s_first[8 + kNotes + 1], rt = s_first[8 + kNotes + 2];
     uint32_t done = 0;       // tiles of earlier segments
     uint32_t segment = 0;
+    PromptSeq sq = {};
+    if (b < p.B) sq = seq_of(p, cache, b);
 
-    for (int b = *s_first, kvh = 0, rt = 0; at < w1 && b < p.B;) {
-        const PromptSeq sq = seq_of(p, cache, b);
+    while (at < w1 && b < p.B) {
         if (rt >= sq.row_tiles) {
             rt = 0;
             if (++kvh >= cache.kv_heads || sq.row_tiles == 0) {
                 kvh = 0;
-                ++b;
+                if (++b < p.B) sq = seq_of(p, cache, b);
             }
             continue;
         }
-        if (rt == 0) {  // whole heads before the run
-            const int64_t head_cost = sq.cost(p.causal);
-            if (at + head_cost <= w0) {
-                at += head_cost;
-                rt = sq.row_tiles;
-                continue;
-            }
-        }
-        const int tiles = sq.tiles(rt, p.causal);
-        const int64_t unit_at = at, each = tiles + kUnitCost;
-        const int row0 = rt * kRows;
-        const int t0 = static_cast<int>(min(static_cast<int64_t>(tiles), max(static_cast<int64_t>(0), w0 - unit_at - kUnitCost)));
-        const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), max(static_cast<int64_t>(0), w1 - unit_at - kUnitCost)));
-        at += each;
+        // tiles of the unit whose places lie in the run
+        const int tiles = sq.tiles(rt, p.causal), row0 = rt * kRows;
+        const int64_t first_at = at + sq.fixed(), each = static_cast<int64_t>(sq.grp) * kTok;
+        const int t0 = static_cast<int>(min(static_cast<int64_t>(tiles), (max(w0 - first_at, static_cast<int64_t>(0)) + each - 1) / each));
+        const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), (max(w1 - first_at, static_cast<int64_t>(0)) + each - 1) / each));
+        at += sq.length(rt, p.causal);
         ++rt;
         if (t0 >= t1) continue;
         const int nt = t1 - t0;
-        const int cta0 = static_cast<int>((unit_at + kUnitCost) / per), cta1 = static_cast<int>((unit_at + each - 1) / per);
+        const int cta0 = static_cast<int>(first_at / per), cta1 = static_cast<int>((first_at + (tiles - 1) * each) / per);
         const int rows = min(kRows, sq.q_len * sq.grp - row0);
         const bool whole = t0 == 0 && t1 == tiles;
 
-        if (warp < 4) {
-            // ================= softmax: row `r` of the unit
-            const int r = warp * 32 + lane;
-            const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);  // this warp's 32 lanes
-            const bool idle = warp * 32 >= rows;
-            const int pos = (row0 + min(r, rows - 1)) / sq.grp, hd = (row0 + min(r, rows - 1)) % sq.grp;
+        if (warp < kDequant) {
+            // ================= softmax: half `hf` of row `r` of the unit
+            const int quad = warp & 3, hf = warp >> 2, r = quad * 32 + lane;
+            const uint32_t lanes = tmem + (static_cast<uint32_t>(quad) << 21);  // this warp's 32 lanes
+            const bool idle = quad * 32 >= rows;
+            const int in_seq = row0 + min(r, rows - 1), pos = in_seq / sq.grp, hd = in_seq - pos * sq.grp;
             const int64_t q_row = sq.q0 + pos;
             const int head = kvh * sq.grp + hd;
             {
-                const uint16_t* src = p.q + q_row * p.q_stride + static_cast<int64_t>(head) * D;
+                const uint16_t* src = p.q + q_row * p.q_stride + static_cast<int64_t>(head) * D + hf * (D / 2);
                 const uint32_t sign = p.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
-                    uint32_t v[32];
+                    uint32_t v[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         uint4 x = make_uint4(0, 0, 0, 0);
-                        if (r < rows) x = *reinterpret_cast<const uint4*>(src + c * 64 + i * 8);
+                        if (r < rows) x = *reinterpret_cast<const uint4*>(src + c * 32 + i * 8);
                         v[4 * i] = x.x ^ sign;
                         v[4 * i + 1] = x.y ^ sign;
                         v[4 * i + 2] = x.z ^ sign;
                         v[4 * i + 3] = x.w ^ sign;
                     }
-                    tmem_st<32>(lanes + C::kColQ + 32 * c, v);
+                    tmem_st<16>(lanes + C::kColQ + hf * (D / 4) + 16 * c, v);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -319,67 +370,72 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(q_full);
             }
             const float c1 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
-            const int lim = sq.seen(row0 + min(r, rows - 1), p.causal);
-            const int lim_min = sq.seen(row0 + min(warp * 32, rows - 1), p.causal);
+            const int lim = sq.seen(in_seq, p.causal);
+            const int lim_min = sq.seen(row0 + min(quad * 32, rows - 1), p.causal);
             float m = -INFINITY, l = 0.f;
             bool ok = true;
-            for (int i = 0; i < nt && ok; ++i) {
+            for (int i = 0; i < nt; ++i) {
                 const uint32_t it = done + i, buf = it & 1, ph = (it >> 1) & 1;
-                ok = wait(s_full(buf), ph);
-                if (!ok) break;
+                // (a warp whose wait ran out goes on to the barrier, where the two agree to leave)
+                ok = ok && wait(s_full(buf), ph);
+                if (idle && !ok) break;
                 if (!idle) {
                     tc_fence_after();
-                    float s[2][32];
-                    tmem_ld32(lanes + C::kColS + buf * kTok, s[0]);
-                    tmem_ld32(lanes + C::kColS + buf * kTok + 32, s[1]);
+                    float s[32];
+                    tmem_ld32(lanes + C::kColS + buf * kTok + hf * 32, s);
                     tmem_wait_ld();
-                    const int tok = (t0 + i) * kTok;
-                    const uint32_t valid = s_valid[it % kNotes];
-                    if (tok + kTok > lim_min || valid != 0x10101010u) {
+                    const int tok = (t0 + i) * kTok + hf * 32;
+                    const uint32_t valid = (s_valid[it % kNotes] >> (16 * hf)) & 0xFFFFu;
+                    if (tok + 32 > lim_min || valid != 0x1010u) {
 #pragma unroll
-                        for (int j = 0; j < kTok; ++j) {
+                        for (int j = 0; j < 32; ++j) {
                             const int there = static_cast<int>((valid >> (8 * (j / 16))) & 255u);
-                            if (tok + j >= lim || (j & 15) >= there) s[j / 32][j % 32] = -INFINITY;
+                            if (tok + j >= lim || (j & 15) >= there) s[j] = -INFINITY;
                         }
                     }
-                    float mx = s[0][0];
+                    float mx = s[0];
 #pragma unroll
-                    for (int j = 1; j < kTok; ++j) mx = fmaxf(mx, s[j / 32][j % 32]);
+                    for (int j = 1; j < 32; ++j) mx = fmaxf(mx, s[j]);
                     mx *= c1;
-                    if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-                        const float now = fmaxf(m, mx), f = m == now ? 1.f : ex2(m - now);
+                    // both halves have read S from here on: P may take its place
+                    if (any_of_64(1 + quad, mx > m + 8.f || !ok)) {
+                        s_half[hf * kRows + r] = mx;
+                        if (lane == 0) s_left[warp] = !ok;
+                        named_sync(1 + quad, 64);
+                        const bool leave = s_left[quad] || s_left[quad + 4];
+                        const float now = fmaxf(m, fmaxf(mx, s_half[(hf ^ 1) * kRows + r])), f = m == now ? 1.f : ex2(m - now);
                         m = now;
                         l *= f;
                         if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
                             const uint32_t before = it - 1;
-                            ok = wait(pv_done(before & 1), (before >> 1) & 1);
-                            if (!ok) break;
+                            ok = ok && wait(pv_done(before & 1), (before >> 1) & 1);
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                float v[32];
-                                tmem_ld32(lanes + c, v);
+                            for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 16) {
+                                uint32_t v[16];
+                                tmem_ld16(lanes + c, v);
                                 tmem_wait_ld();
-                                uint32_t u[32];
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(v[j] * f);
-                                tmem_st<32>(lanes + c, u);
+                                for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+                                tmem_st<16>(lanes + c, v);
                             }
                             tmem_wait_st();
                         }
+                        named_sync(1 + quad, 64);  // s_half may be written again
+                        if (leave) break;
                     }
                     const float sub = m == -INFINITY ? 0.f : m;
-                    uint32_t pk[32];
+                    uint32_t pk[16];
                     float sum = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float a = ex2(fmaf(s[j / 16][2 * j % 32], c1, -sub)), e = ex2(fmaf(s[j / 16][2 * j % 32 + 1], c1, -sub));
+                    for (int j = 0; j < 16; ++j) {
+                        const float a = ex2(fmaf(s[2 * j], c1, -sub)), e = ex2(fmaf(s[2 * j + 1], c1, -sub));
                         sum += a + e;
                         const __half2 h = __floats2half2_rn(a, e);
                         pk[j] = *reinterpret_cast<const uint32_t*>(&h);
                     }
                     l += sum;
-                    tmem_st<32>(lanes + C::kColS + buf * kTok, pk);
+                    tmem_st<16>(lanes + C::kColS + buf * kTok + hf * 16, pk);
                     tmem_wait_st();
                     tc_fence_before();
                 }
@@ -391,6 +447,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t end = done + nt - 1;
                 ok = wait(pv_done(end & 1), (end >> 1) & 1);
             }
+            if (!idle) {
+                s_half[hf * kRows + r] = l;
+                named_sync(1 + quad, 64);
+                l += s_half[(hf ^ 1) * kRows + r];
+                named_sync(1 + quad, 64);
+            }
             if (ok && !idle) {
                 tc_fence_after();
                 const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -398,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                               static_cast<int64_t>(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * C::kPart;
                 uint16_t* out = p.out + (q_row * p.heads + head) * D;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
                     float v[32];
                     tmem_ld32(lanes + c, v);
                     tmem_wait_ld();
@@ -423,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
                     }
                 }
-                if (r < rows) {
+                if (r < rows && hf == 0) {
                     if (!whole) {
                         __stcg(part + r, m);
                         __stcg(part + kRows + r, l);
@@ -434,9 +496,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
             }
         } else if (warp < kProducer) {
-            // ================= dequantise: keys (warps 4-7) or values (8-11) of quarter `sub`
-            const int sub = warp & 3;
-            const bool is_k = warp < 8;
+            // ================= dequantise: half `part` of the keys or values of quarter `sub`
+            const int dw = warp - kDequant, sub = dw & 3, part = (dw >> 2) & 1;
+            const bool is_k = dw < 8;
             const int g = lane >> 2, t = lane & 3;
             for (int i = 0; i < nt; ++i) {
                 const uint32_t it = done + i, st = it % R, buf = it & 1, use = it >> 1;
@@ -445,46 +507,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t tile = base + C::kOffRaw + st * C::kRaw + sub * T::kTileBytes;
                 const int there = static_cast<int>((s_valid[it % kNotes] >> (8 * sub)) & 255u);
                 if (is_k) {
-                    uint32_t sc[2][G], mn[2][G];
+                    // tokens 8 part + g
+                    const int h = part, row = sub * 16 + 8 * h + g;
+                    uint32_t pr[G], sc[G], mn[G];
+                    lds_params<G>(tile + T::kKParams + (8 * h + g) * G * 4, pr);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t pr[G];
-                        lds_params<G>(tile + T::kKParams + (8 * h + g) * G * 4, pr);
-#pragma unroll
-                        for (int y = 0; y < G; ++y) {
-                            if (8 * h + g >= there) pr[y] = 0;
-                            sc[h][y] = __byte_perm(pr[y], 0, 0x1010);
-                            mn[h][y] = __byte_perm(pr[y], 0, 0x3232);
-                        }
+                    for (int y = 0; y < G; ++y) {
+                        if (8 * h + g >= there) pr[y] = 0;
+                        sc[y] = __byte_perm(pr[y], 0, 0x1010);
+                        mn[y] = __byte_perm(pr[y], 0, 0x3232);
                     }
-                    const uint32_t to = base + buf * C::kBuf;
+                    const uint32_t row_at = base + buf * C::kBuf + row * 128;
+                    auto put = [&](int y, int w, uint32_t word) {
+                        uint32_t q[4];
+                        codes(word, q);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int row = sub * 16 + 8 * h + g;
-                        const uint32_t row_at = to + row * 128;
-                        auto put = [&](int y, int w, uint32_t word) {
-                            uint32_t q[4];
-                            codes(word, q);
+                        for (int x = 0; x < 4; ++x) q[x] = hfma2(q[x], sc[y], mn[y]);
+                        sts128(row_at + y * (kTok * 128) + (((2 * t + w) ^ (row & 7)) << 4), q[0], q[1], q[2], q[3]);
+                    };
+                    if constexpr (G == 1) {
+                        const uint2 v = lds64(tile + (h * 32 + lane) * 8);
+                        put(0, 0, v.x);
+                        put(0, 1, v.y);
+                    } else {
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) q[x] = hfma2(q[x], sc[h][y], mn[h][y]);
-                            sts128(row_at + y * (kTok * 128) + (((2 * t + w) ^ (row & 7)) << 4), q[0], q[1], q[2], q[3]);
-                        };
-                        if constexpr (G == 1) {
-                            const uint2 v = lds64(tile + (h * 32 + lane) * 8);
-                            put(0, 0, v.x);
-                            put(0, 1, v.y);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < G / 2; ++j) {
-                                const uint4 v = lds128(tile + ((2 * j + h) * 32 + lane) * 16);
-                                put(2 * j, 0, v.x);
-                                put(2 * j, 1, v.y);
-                                put(2 * j + 1, 0, v.z);
-                                put(2 * j + 1, 1, v.w);
-                            }
+                        for (int j = 0; j < G / 2; ++j) {
+                            const uint4 v = lds128(tile + ((2 * j + h) * 32 + lane) * 16);
+                            put(2 * j, 0, v.x);
+                            put(2 * j, 1, v.y);
+                            put(2 * j + 1, 0, v.z);
+                            put(2 * j + 1, 1, v.w);
                         }
                     }
                 } else {
+                    // groups part * G / 2 .. of all 16 tokens (one group: half of its words)
                     uint32_t pr[4][G];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -496,18 +552,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const uint32_t to = base + C::kOffV + buf * C::kBuf + t * 4;
+                    const uint32_t c0 = ((2 * sub) ^ g) << 4, c8 = ((2 * sub + 1) ^ g) << 4;
+                    constexpr int kY = G > 1 ? G / 2 : 1, kX = G > 1 ? 4 : 2;
 #pragma unroll
-                    for (int y = 0; y < G; ++y) {
-                        const uint32_t sa = __byte_perm(pr[0][y], pr[1][y], 0x5410), ma = __byte_perm(pr[0][y], pr[1][y], 0x7632);
-                        const uint32_t sb = __byte_perm(pr[2][y], pr[3][y], 0x5410), mb = __byte_perm(pr[2][y], pr[3][y], 0x7632);
+                    for (int yy = 0; yy < kY; ++yy) {
+                        const int y = G > 1 ? part * kY + yy : 0;
+                        uint32_t u[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) u[k] = G > 1 && part ? pr[k][G > 1 ? G / 2 + yy : 0] : pr[k][yy];
+                        const uint32_t sa = __byte_perm(u[0], u[1], 0x5410), ma = __byte_perm(u[0], u[1], 0x7632);
+                        const uint32_t sb = __byte_perm(u[2], u[3], 0x5410), mb = __byte_perm(u[2], u[3], 0x7632);
                         const uint4 v = lds128(tile + T::kV + y * 512 + lane * 16);
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
+                        for (int xx = 0; xx < kX; ++xx) {
+                            const int x = G > 1 ? xx : 2 * part + xx;
                             uint32_t q[4];
-                            codes(w[x], q);
+                            codes(G > 1 ? w[xx] : (part ? w[2 + (xx & 1)] : w[xx & 1]), q);
                             const uint32_t row = to + (64 * y + 16 * x + g) * 128;
-                            const uint32_t c0 = ((2 * sub) ^ g) << 4, c8 = ((2 * sub + 1) ^ g) << 4;
                             sts32(row + c0, hfma2(q[0], sa, ma));
                             sts32(row + 1024 + c0, hfma2(q[1], sa, ma));
                             sts32(row + c8, hfma2(q[2], sb, mb));
@@ -566,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait(k_full(buf), use & 1) && wait(pv_done(buf), (use & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint64_t desc = smem_desc_sw128(base + buf * C::kBuf + (k / 4) * (kTok * 128)) + (k & 3) * 2;
@@ -583,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t it = done + i, buf = it & 1, use = it >> 1;
                 if (!wait(v_full(buf), use & 1) || !wait(p_full(buf), use & 1)) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k) {
                         const uint64_t desc = smem_desc_sw128(base + C::kOffV + buf * C::kBuf) + k * 2;
@@ -612,45 +674,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncthreads();
             if (*s_last && !*s_abort) {
                 __threadfence();
-                // threads in groups of 128: a row each, columns of four in turn
-                const int r = tid & (kRows - 1), first = tid / kRows, step = 3;
-                if (first < step && r < rows) {
+                // A thread has a row and 16 of its elements at a time, from two parts in one round of loads.
+                const int n = cta1 - cta0 + 1, r = tid & (kRows - 1);
+                constexpr int kGroups = kThreads / kRows;
+                if (tid < kGroups * kRows && r < rows) {
                     float top = -INFINITY, total = 0.f;
-                    for (int c = cta0; c <= cta1; ++c) top = fmaxf(top, __ldcg(part_of(c) + r));
-                    for (int c = cta0; c <= cta1; ++c) {
-                        const float m = __ldcg(part_of(c) + r);
-                        total += m == -INFINITY ? 0.f : __ldcg(part_of(c) + kRows + r) * ex2(m - top);
+                    for (int c = 0; c < n; ++c) top = fmaxf(top, __ldcg(part_of(cta0 + c) + r));
+                    for (int c = 0; c < n; ++c) {
+                        const float m = __ldcg(part_of(cta0 + c) + r);
+                        total += m == -INFINITY ? 0.f : __ldcg(part_of(cta0 + c) + kRows + r) * ex2(m - top);
                     }
-                    const int pos = (row0 + r) / sq.grp, hd = (row0 + r) % sq.grp;
-                    const int64_t at_out = (static_cast<int64_t>(sq.q0 + pos) * p.heads + kvh * sq.grp + hd);
+                    const int in_seq = row0 + r, pos = in_seq / sq.grp, hd = in_seq - pos * sq.grp;
+                    const int64_t at_out = static_cast<int64_t>(sq.q0 + pos) * p.heads + kvh * sq.grp + hd;
                     const float inv = total > 0.f ? 1.f / total : 0.f;
-                    for (int c4 = first; c4 < D / 4; c4 += 4 * step) {
+                    for (int c4 = tid / kRows * 4; c4 < D / 4; c4 += kGroups * 4) {
                         float4 v[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int c = cta0; c <= cta1; ++c) {
-                            const float m = __ldcg(part_of(c) + r);
-                            const float f = m == -INFINITY ? 0.f : ex2(m - top);
+                        for (int c = 0; c < n; c += 2) {
+                            float f[2];
+                            float4 a[2][4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if (c4 + k * step >= D / 4) break;
-                                const float4 a = __ldcg(reinterpret_cast<const float4*>(part_of(c) + 2 * kRows) + (c4 + k * step) * kRows + r);
-                                if (m == -INFINITY) continue;  // (its sums are of nothing)
-                                v[k].x = fmaf(a.x, f, v[k].x);
-                                v[k].y = fmaf(a.y, f, v[k].y);
-                                v[k].z = fmaf(a.z, f, v[k].z);
-                                v[k].w = fmaf(a.w, f, v[k].w);
+                            for (int h = 0; h < 2; ++h) {
+                                const float* from = part_of(cta0 + min(c + h, n - 1));
+                                const float m = __ldcg(from + r);
+                                f[h] = m == -INFINITY || c + h >= n ? 0.f : ex2(m - top);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    a[h][k] = __ldcg(reinterpret_cast<const float4*>(from + 2 * kRows) + (c4 + k) * kRows + r);
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (f[h] == 0.f) continue;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    v[k].x = fmaf(a[h][k].x, f[h], v[k].x);
+                                    v[k].y = fmaf(a[h][k].y, f[h], v[k].y);
+                                    v[k].z = fmaf(a[h][k].z, f[h], v[k].z);
+                                    v[k].w = fmaf(a[h][k].w, f[h], v[k].w);
+                                }
                             }
                         }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (c4 + k * step >= D / 4) break;
+                        for (int k = 0; k < 4; k += 2) {
                             const __half2 h0 = __floats2half2_rn(v[k].x * inv, v[k].y * inv), h1 = __floats2half2_rn(v[k].z * inv, v[k].w * inv);
-                            *reinterpret_cast<uint2*>(p.out + at_out * D + 4 * (c4 + k * step)) =
-                                make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+                            const __half2 h2 = __floats2half2_rn(v[k + 1].x * inv, v[k + 1].y * inv);
+                            const __half2 h3 = __floats2half2_rn(v[k + 1].z * inv, v[k + 1].w * inv);
+                            *reinterpret_cast<uint4*>(p.out + at_out * D + 4 * (c4 + k)) =
+                                make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
+                                           *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
                         }
                     }
-                    if (first == 0 && p.lse != nullptr)
+                    if (tid < kRows && p.lse != nullptr)
                         p.lse[at_out] = total > 0.f ? 0.6931471805599453f * (top + log2f(total)) : -INFINITY;
                 }
             }
