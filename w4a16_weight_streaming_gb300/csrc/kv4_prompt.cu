@@ -12,11 +12,13 @@
 // tile reads 64 KB of operands from shared memory for 1077 cycles of tensor work (D = 256), which leaves
 // room for the dequantised stores; with Q in shared memory it would be 128 KB.
 //
-// Warps: 0-7 softmax, half a row a thread (the running maximum moves, and O is rescaled in TMEM, only when
-// a score exceeds it by 2^8; the two warps of 32 rows meet at a barrier once a tile); 8-23 dequantise, half
-// of a 16-token quarter of the tile's keys or values each; 24 fetches the cache's tiles by bulk copies; 25
-// issues S, 26 issues PV. K', V' and S/P are double-buffered: S of
-// tile i + 1 and the dequantisation of i + 2 run beside the softmax of i.
+// Warps: 0-15 softmax, a quarter of a row a thread (the four warps of 32 rows meet at a barrier once a tile;
+// the row's reference moves, and O is rescaled in TMEM, only when a score exceeds it by 2^8); 16-23
+// dequantise a 16-token quarter of the tile's keys or values each; 24 fetches the cache's tiles by bulk
+// copies; 25 issues S, 26 issues PV. K', V' and S/P are double-buffered. What bounds a tile is the circle
+// S -> softmax -> PV -> S of its S/P buffer, so the softmax is spread over many warps for its latency
+// (a row in one thread: 283 us, in two 179, in four less; two groups of one-thread rows taking the even and
+// the odd tiles: 186).
 //
 // Work is a list of (unit, tile); every CTA takes an equal run. Units that a run's end cuts leave parts
 // (maximum, sum, unnormalised rows) in the workspace; the CTA that arrives last adds them in CTA order.
@@ -34,7 +36,7 @@ constexpr int kTok = 64;       // tokens of a tile
 constexpr int kSub = kTok / kKv4Tile;
 constexpr int kUnitCost = 6;   // what the start and end of a unit cost, in tiles
 constexpr int kMinRun = 12;    // tiles; fewer make more parts than they save
-constexpr int kDequant = 8;    // first warp of each role (softmax: 0)
+constexpr int kDequant = 16;   // first warp of each role (softmax: 0)
 constexpr int kProducer = 24, kIssueS = 25;
 constexpr int kWarps = 27;     // (26: PV)
 constexpr int kThreads = kWarps * 32;
@@ -50,7 +52,7 @@ struct Prompt {
     static constexpr int kOffBars = kOffRaw + kRawStages * kRaw;
     static constexpr int kBars = 2 * kRawStages + 2 * 5 + 1;
     static constexpr int kOffMisc = kOffBars + kBars * 8;
-    static constexpr int kSmem = kOffMisc + 256 + 2 * kRows * 4 + 1024;  // + alignment
+    static constexpr int kSmem = kOffMisc + 256 + 4 * kRows * 4 + 1024;  // + alignment
     static constexpr uint32_t kColS = D, kColQ = D + 2 * kTok;
     static constexpr uint32_t kCols = D == 64 ? 256 : 512;
     static constexpr int kPart = kRows * (D + 2);  // floats of one workspace part: m, l, then [D / 4][128] float4
@@ -71,19 +73,7 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
-// 32 consecutive TMEM columns of a warp's 32 lanes
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
-          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
-          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
-
+// Consecutive TMEM columns of a warp's 32 lanes
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -92,22 +82,54 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr)
         : "memory");
 }
-// Whether the predicate holds for any of the 64 threads that meet at named barrier `id`.
-__device__ __forceinline__ bool any_of_64(int id, bool pred) {
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// Whether the predicate holds for any of the 128 threads that meet at named barrier `id`.
+__device__ __forceinline__ bool any_of_128(int id, bool pred) {
     uint32_t r;
     asm volatile(
-        "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\tbarrier.red.or.pred po, %2, 64, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+        "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\tbarrier.red.or.pred po, %2, 128, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
         : "=r"(r)
         : "r"(pred ? 1u : 0u), "r"(id)
         : "memory");
     return r != 0;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// pairs of fp32 numbers
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// Four 8 x 8 matrices of fp16 from a warp's fragments (lane 4 g + t: row g, columns 2t, 2t + 1) to rows of
+// 16 bytes; lane l gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ void sts32(uint32_t addr, uint32_t a) {
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     uint32_t v;
@@ -203,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* s_first = s_misc + 3;
     int64_t* s_plan = reinterpret_cast<int64_t*>(s_misc + 4);      // run begin, end, length; first sequence's place
     uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_misc + 12);  // [kNotes]: valid tokens of each quarter, a byte each
-    float* s_half = reinterpret_cast<float*>(smem + C::kOffMisc + 256);  // [2][128]: what two halves of a row exchange
-    volatile int* s_left = s_misc + 32;  // [8]: softmax warps whose wait ran out
+    float* s_part = reinterpret_cast<float*>(smem + C::kOffMisc + 256);  // [4][128]: what the quarters of a row exchange
+    volatile int* s_left = s_misc + 32;  // [16]: softmax warps whose wait ran out
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t bars = base + C::kOffBars;
     auto raw_full = [&](int s) { return bars + 8 * s; };
@@ -221,16 +243,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             for (int i = 0; i < R; ++i) {
                 mbar_init(raw_full(i), 1);
-                mbar_init(raw_empty(i), 16);
+                mbar_init(raw_empty(i), 8);
             }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(k_full(i), 8);
-                mbar_init(v_full(i), 8);
+                mbar_init(k_full(i), 4);
+                mbar_init(v_full(i), 4);
                 mbar_init(s_full(i), 1);
-                mbar_init(p_full(i), 8);
+                mbar_init(p_full(i), 16);
                 mbar_init(pv_done(i), 1);
             }
-            mbar_init(q_full, 8);
+            mbar_init(q_full, 16);
             *s_abort = 0;
             fence_barrier_init();
         }
@@ -340,29 +362,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = t0 == 0 && t1 == tiles;
 
         if (warp < kDequant) {
-            // ================= softmax: half `hf` of row `r` of the unit
-            const int quad = warp & 3, hf = warp >> 2, r = quad * 32 + lane;
+            // ================= softmax: quarter `part` of row `r` of the unit
+            const int quad = warp & 3, part = warp >> 2, r = quad * 32 + lane;
             const uint32_t lanes = tmem + (static_cast<uint32_t>(quad) << 21);  // this warp's 32 lanes
             const bool idle = quad * 32 >= rows;
             const int in_seq = row0 + min(r, rows - 1), pos = in_seq / sq.grp, hd = in_seq - pos * sq.grp;
             const int64_t q_row = sq.q0 + pos;
             const int head = kvh * sq.grp + hd;
             {
-                const uint16_t* src = p.q + q_row * p.q_stride + static_cast<int64_t>(head) * D + hf * (D / 2);
+                const uint16_t* src = p.q + q_row * p.q_stride + static_cast<int64_t>(head) * D + part * (D / 4);
                 const uint32_t sign = p.scale < 0.f ? 0x80008000u : 0u;
+                uint4 x[D / 32];
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    x[c] = make_uint4(0, 0, 0, 0);
+                    if (r < rows) x[c] = *reinterpret_cast<const uint4*>(src + c * 8);
+                }
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
-                    uint32_t v[16];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (r < rows) x = *reinterpret_cast<const uint4*>(src + c * 32 + i * 8);
-                        v[4 * i] = x.x ^ sign;
-                        v[4 * i + 1] = x.y ^ sign;
-                        v[4 * i + 2] = x.z ^ sign;
-                        v[4 * i + 3] = x.w ^ sign;
-                    }
-                    tmem_st<16>(lanes + C::kColQ + hf * (D / 4) + 16 * c, v);
+                    const uint32_t v[8] = {x[2 * c].x ^ sign,     x[2 * c].y ^ sign,     x[2 * c].z ^ sign,     x[2 * c].w ^ sign,
+                                           x[2 * c + 1].x ^ sign, x[2 * c + 1].y ^ sign, x[2 * c + 1].z ^ sign, x[2 * c + 1].w ^ sign};
+                    tmem_st8(lanes + C::kColQ + part * (D / 8) + 8 * c, v);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -372,38 +392,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float c1 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
             const int lim = sq.seen(in_seq, p.causal);
             const int lim_min = sq.seen(row0 + min(quad * 32, rows - 1), p.causal);
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f;  // the row's reference, and this quarter's sum
             bool ok = true;
             for (int i = 0; i < nt; ++i) {
                 const uint32_t it = done + i, buf = it & 1, ph = (it >> 1) & 1;
-                // (a warp whose wait ran out goes on to the barrier, where the two agree to leave)
+                // (a warp whose wait ran out goes on to the barrier, where the four agree to leave)
                 ok = ok && wait(s_full(buf), ph);
                 if (idle && !ok) break;
                 if (!idle) {
                     tc_fence_after();
-                    float s[32];
-                    tmem_ld32(lanes + C::kColS + buf * kTok + hf * 32, s);
+                    const uint32_t from = lanes + C::kColS + buf * kTok;
+                    uint32_t s[16];
+                    tmem_ld16(from + part * 16, s);
                     tmem_wait_ld();
-                    const int tok = (t0 + i) * kTok + hf * 32;
-                    const uint32_t valid = (s_valid[it % kNotes] >> (16 * hf)) & 0xFFFFu;
-                    if (tok + 32 > lim_min || valid != 0x1010u) {
+                    const int tok = (t0 + i) * kTok + part * 16;
+                    const int there = static_cast<int>((s_valid[it % kNotes] >> (8 * part)) & 255u);
+                    if (tok + 16 > lim_min || there != 16) {
+                        const int most = min(there, lim - tok);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int there = static_cast<int>((valid >> (8 * (j / 16))) & 255u);
-                            if (tok + j >= lim || (j & 15) >= there) s[j] = -INFINITY;
-                        }
+                        for (int j = 0; j < 16; ++j)
+                            if (j >= most) s[j] = 0xFF800000u;  // -inf
                     }
-                    float mx = s[0];
+                    float mx = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])), my = fmaxf(__uint_as_float(s[2]), __uint_as_float(s[3]));
 #pragma unroll
-                    for (int j = 1; j < 32; ++j) mx = fmaxf(mx, s[j]);
-                    mx *= c1;
-                    // both halves have read S from here on: P may take its place
-                    if (any_of_64(1 + quad, mx > m + 8.f || !ok)) {
-                        s_half[hf * kRows + r] = mx;
+                    for (int j = 4; j < 16; j += 4) {
+                        mx = max3(mx, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+                        my = max3(my, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+                    }
+                    mx = fmaxf(mx, my) * c1;
+                    // all quarters have read S from here on: P may take its place
+                    if (any_of_128(1 + quad, mx > m + 8.f || !ok)) {
+                        s_part[part * kRows + r] = mx;
                         if (lane == 0) s_left[warp] = !ok;
-                        named_sync(1 + quad, 64);
-                        const bool leave = s_left[quad] || s_left[quad + 4];
-                        const float now = fmaxf(m, fmaxf(mx, s_half[(hf ^ 1) * kRows + r])), f = m == now ? 1.f : ex2(m - now);
+                        named_sync(1 + quad, 128);
+                        const bool leave = s_left[quad] || s_left[quad + 4] || s_left[quad + 8] || s_left[quad + 12];
+                        const float now = max3(max3(m, s_part[r], s_part[kRows + r]), s_part[2 * kRows + r], s_part[3 * kRows + r]);
+                        const float f = m == now ? 1.f : ex2(m - now);
                         m = now;
                         l *= f;
                         if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
@@ -411,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = ok && wait(pv_done(before & 1), (before >> 1) & 1);
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 16) {
+                            for (int c = part * (D / 4); c < (part + 1) * (D / 4); c += 16) {
                                 uint32_t v[16];
                                 tmem_ld16(lanes + c, v);
                                 tmem_wait_ld();
@@ -421,74 +445,79 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             tmem_wait_st();
                         }
-                        named_sync(1 + quad, 64);  // s_half may be written again
+                        named_sync(1 + quad, 128);  // s_part may be written again
                         if (leave) break;
                     }
                     const float sub = m == -INFINITY ? 0.f : m;
-                    uint32_t pk[16];
-                    float sum = 0.f;
+                    uint32_t pk[8];
+                    uint64_t sum = 0;  // two fp32 sums
+                    const uint64_t c2 = pair(c1, c1), sub2 = pair(-sub, -sub);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float a = ex2(fmaf(s[2 * j], c1, -sub)), e = ex2(fmaf(s[2 * j + 1], c1, -sub));
-                        sum += a + e;
-                        const __half2 h = __floats2half2_rn(a, e);
-                        pk[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    for (int j = 0; j < 8; ++j) {
+                        float a, e;
+                        unpair(fma2(pair(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, sub2), a, e);
+                        a = ex2(a);
+                        e = ex2(e);
+                        sum = add2(sum, pair(a, e));
+                        const __half2 x = __floats2half2_rn(a, e);
+                        pk[j] = *reinterpret_cast<const uint32_t*>(&x);
                     }
-                    l += sum;
-                    tmem_st<16>(lanes + C::kColS + buf * kTok + hf * 16, pk);
+                    float a, e;
+                    unpair(sum, a, e);
+                    l += a + e;
+                    tmem_st8(from + part * 8, pk);
                     tmem_wait_st();
                     tc_fence_before();
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full(buf));
             }
-            // ---- the unit's rows, or this CTA's part of them
+            // ---- the unit's rows, or this CTA's part of them: a quarter of the elements each
             if (ok) {
                 const uint32_t end = done + nt - 1;
                 ok = wait(pv_done(end & 1), (end >> 1) & 1);
             }
             if (!idle) {
-                s_half[hf * kRows + r] = l;
-                named_sync(1 + quad, 64);
-                l += s_half[(hf ^ 1) * kRows + r];
-                named_sync(1 + quad, 64);
+                s_part[part * kRows + r] = l;
+                named_sync(1 + quad, 128);
+                l = (s_part[r] + s_part[kRows + r]) + (s_part[2 * kRows + r] + s_part[3 * kRows + r]);
+                named_sync(1 + quad, 128);
             }
             if (ok && !idle) {
                 tc_fence_after();
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-                float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + 4096) +
-                              static_cast<int64_t>(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * C::kPart;
+                float* dst = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + 4096) +
+                             static_cast<int64_t>(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * C::kPart;
                 uint16_t* out = p.out + (q_row * p.heads + head) * D;
 #pragma unroll 1
-                for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
-                    float v[32];
-                    tmem_ld32(lanes + c, v);
+                for (int c = part * (D / 4); c < (part + 1) * (D / 4); c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(lanes + c, v);
                     tmem_wait_ld();
+                    if (r >= rows) continue;
                     if (whole) {
-                        if (r < rows) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t h[4];
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t h[4];
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const __half2 x = __floats2half2_rn(l > 0.f ? v[8 * j + 2 * k] * inv : 0.f,
-                                                                        l > 0.f ? v[8 * j + 2 * k + 1] * inv : 0.f);
-                                    h[k] = *reinterpret_cast<const uint32_t*>(&x);
-                                }
-                                *reinterpret_cast<uint4*>(out + c + 8 * j) = make_uint4(h[0], h[1], h[2], h[3]);
+                            for (int k = 0; k < 4; ++k) {
+                                const __half2 x = __floats2half2_rn(l > 0.f ? __uint_as_float(v[8 * j + 2 * k]) * inv : 0.f,
+                                                                    l > 0.f ? __uint_as_float(v[8 * j + 2 * k + 1]) * inv : 0.f);
+                                h[k] = *reinterpret_cast<const uint32_t*>(&x);
                             }
+                            *reinterpret_cast<uint4*>(out + c + 8 * j) = make_uint4(h[0], h[1], h[2], h[3]);
                         }
-                    } else if (r < rows) {
+                    } else {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            __stcg(reinterpret_cast<float4*>(part + 2 * kRows) + (c / 4 + j) * kRows + r,
-                                   make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+                        for (int j = 0; j < 4; ++j)
+                            __stcg(reinterpret_cast<uint4*>(dst + 2 * kRows) + (c / 4 + j) * kRows + r,
+                                   make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
                     }
                 }
-                if (r < rows && hf == 0) {
+                if (r < rows && part == 0) {
                     if (!whole) {
-                        __stcg(part + r, m);
-                        __stcg(part + kRows + r, l);
+                        __stcg(dst + r, m);
+                        __stcg(dst + kRows + r, l);
                     } else if (p.lse != nullptr) {
                         p.lse[q_row * p.heads + head] = l > 0.f ? 0.6931471805599453f * (m + log2f(l)) : -INFINITY;
                     }
@@ -496,84 +525,82 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
             }
         } else if (warp < kProducer) {
-            // ================= dequantise: half `part` of the keys or values of quarter `sub`
-            const int dw = warp - kDequant, sub = dw & 3, part = (dw >> 2) & 1;
-            const bool is_k = dw < 8;
+            // ================= dequantise: keys or values of quarter `sub`
+            const int dw = warp - kDequant, sub = dw & 3;
+            const bool is_k = dw < 4;
             const int g = lane >> 2, t = lane & 3;
+            const uint32_t to_k0 = base + (sub * 16 + g) * 128;  // the row of token g
+            // the 16 bytes that this lane addresses of the four 8 x 8 matrices of a V word: matrix lane / 8 (rows
+            // 8 (m & 1) on, tokens 8 (m / 2) on), row lane % 8
+            const uint32_t to_v0 = base + C::kOffV + (((lane >> 3) & 1) * 8 + (lane & 7)) * 128 +
+                                   (((2 * sub + (lane >> 4)) ^ (lane & 7)) << 4);
             for (int i = 0; i < nt; ++i) {
                 const uint32_t it = done + i, st = it % R, buf = it & 1, use = it >> 1;
+                const uint32_t to_k = to_k0 + buf * C::kBuf, to_v = to_v0 + buf * C::kBuf;
                 if (!wait(raw_full(st), (it / R) & 1)) break;
-                if (!wait(is_k ? s_full(buf) : pv_done(buf), (use & 1) ^ 1)) break;
                 const uint32_t tile = base + C::kOffRaw + st * C::kRaw + sub * T::kTileBytes;
                 const int there = static_cast<int>((s_valid[it % kNotes] >> (8 * sub)) & 255u);
+                if (!wait(is_k ? s_full(buf) : pv_done(buf), (use & 1) ^ 1)) break;
                 if (is_k) {
-                    // tokens 8 part + g
-                    const int h = part, row = sub * 16 + 8 * h + g;
-                    uint32_t pr[G], sc[G], mn[G];
-                    lds_params<G>(tile + T::kKParams + (8 * h + g) * G * 4, pr);
 #pragma unroll
-                    for (int y = 0; y < G; ++y) {
-                        if (8 * h + g >= there) pr[y] = 0;
-                        sc[y] = __byte_perm(pr[y], 0, 0x1010);
-                        mn[y] = __byte_perm(pr[y], 0, 0x3232);
-                    }
-                    const uint32_t row_at = base + buf * C::kBuf + row * 128;
-                    auto put = [&](int y, int w, uint32_t word) {
-                        uint32_t q[4];
-                        codes(word, q);
+                    for (int h = 0; h < 2; ++h) {  // tokens 8 h + g
+                        uint32_t pr[G], sc[G], mn[G];
+                        lds_params<G>(tile + T::kKParams + (8 * h + g) * G * 4, pr);
+                        if (there < 16) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) q[x] = hfma2(q[x], sc[y], mn[y]);
-                        sts128(row_at + y * (kTok * 128) + (((2 * t + w) ^ (row & 7)) << 4), q[0], q[1], q[2], q[3]);
-                    };
-                    if constexpr (G == 1) {
-                        const uint2 v = lds64(tile + (h * 32 + lane) * 8);
-                        put(0, 0, v.x);
-                        put(0, 1, v.y);
-                    } else {
+                            for (int y = 0; y < G; ++y)
+                                if (8 * h + g >= there) pr[y] = 0;
+                        }
 #pragma unroll
-                        for (int j = 0; j < G / 2; ++j) {
-                            const uint4 v = lds128(tile + ((2 * j + h) * 32 + lane) * 16);
-                            put(2 * j, 0, v.x);
-                            put(2 * j, 1, v.y);
-                            put(2 * j + 1, 0, v.z);
-                            put(2 * j + 1, 1, v.w);
+                        for (int y = 0; y < G; ++y) {
+                            sc[y] = __byte_perm(pr[y], 0, 0x1010);
+                            mn[y] = __byte_perm(pr[y], 0, 0x3232);
+                        }
+                        auto put = [&](int y, int w, uint32_t word) {
+                            uint32_t q[4];
+                            codes(word, q);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) q[x] = hfma2(q[x], sc[y], mn[y]);
+                            sts128(to_k + h * 1024 + y * (kTok * 128) + (((2 * t + w) ^ g) << 4), q[0], q[1], q[2], q[3]);
+                        };
+                        if constexpr (G == 1) {
+                            const uint2 v = lds64(tile + (h * 32 + lane) * 8);
+                            put(0, 0, v.x);
+                            put(0, 1, v.y);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < G / 2; ++j) {
+                                const uint4 v = lds128(tile + ((2 * j + h) * 32 + lane) * 16);
+                                put(2 * j, 0, v.x);
+                                put(2 * j, 1, v.y);
+                                put(2 * j + 1, 0, v.z);
+                                put(2 * j + 1, 1, v.w);
+                            }
                         }
                     }
                 } else {
-                    // groups part * G / 2 .. of all 16 tokens (one group: half of its words)
                     uint32_t pr[4][G];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int token = 2 * t + (k & 1) + 8 * (k >> 1);
                         lds_params<G>(tile + T::kVParams + token * G * 4, pr[k]);
-                        if (token >= there) {
+                        if (there < 16 && token >= there) {
 #pragma unroll
                             for (int y = 0; y < G; ++y) pr[k][y] = 0;
                         }
                     }
-                    const uint32_t to = base + C::kOffV + buf * C::kBuf + t * 4;
-                    const uint32_t c0 = ((2 * sub) ^ g) << 4, c8 = ((2 * sub + 1) ^ g) << 4;
-                    constexpr int kY = G > 1 ? G / 2 : 1, kX = G > 1 ? 4 : 2;
 #pragma unroll
-                    for (int yy = 0; yy < kY; ++yy) {
-                        const int y = G > 1 ? part * kY + yy : 0;
-                        uint32_t u[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) u[k] = G > 1 && part ? pr[k][G > 1 ? G / 2 + yy : 0] : pr[k][yy];
-                        const uint32_t sa = __byte_perm(u[0], u[1], 0x5410), ma = __byte_perm(u[0], u[1], 0x7632);
-                        const uint32_t sb = __byte_perm(u[2], u[3], 0x5410), mb = __byte_perm(u[2], u[3], 0x7632);
+                    for (int y = 0; y < G; ++y) {
+                        const uint32_t sa = __byte_perm(pr[0][y], pr[1][y], 0x5410), ma = __byte_perm(pr[0][y], pr[1][y], 0x7632);
+                        const uint32_t sb = __byte_perm(pr[2][y], pr[3][y], 0x5410), mb = __byte_perm(pr[2][y], pr[3][y], 0x7632);
                         const uint4 v = lds128(tile + T::kV + y * 512 + lane * 16);
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int xx = 0; xx < kX; ++xx) {
-                            const int x = G > 1 ? xx : 2 * part + xx;
+                        for (int x = 0; x < 4; ++x) {
                             uint32_t q[4];
-                            codes(G > 1 ? w[xx] : (part ? w[2 + (xx & 1)] : w[xx & 1]), q);
-                            const uint32_t row = to + (64 * y + 16 * x + g) * 128;
-                            sts32(row + c0, hfma2(q[0], sa, ma));
-                            sts32(row + 1024 + c0, hfma2(q[1], sa, ma));
-                            sts32(row + c8, hfma2(q[2], sb, mb));
-                            sts32(row + 1024 + c8, hfma2(q[3], sb, mb));
+                            codes(w[x], q);
+                            stmatrix4(to_v + (64 * y + 16 * x) * 128, hfma2(q[0], sa, ma), hfma2(q[1], sa, ma), hfma2(q[2], sb, mb),
+                                      hfma2(q[3], sb, mb));
                         }
                     }
                 }
