@@ -471,14 +471,13 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return t.data_ptr() if t is not None else None
 
 
-def _want(ok: bool, where: str, what: str):
-    if not ok:
-        raise ValueError(f"{where}: {what}")
+def _refuse(where: str, what: str):
+    raise ValueError(f"{where}: {what}")
 
 
 def _vec(t: torch.Tensor | None, dtype: torch.dtype, n: int) -> bool:
     """None, or a contiguous CUDA vector of n elements of `dtype`."""
-    return t is None or (t.dtype is dtype and t.is_cuda and t.shape == (n,) and t.is_contiguous())
+    return t is None or (t.dtype is dtype and t.is_cuda and t.numel() == n and t.dim() == 1 and t.is_contiguous())
 
 
 def _dense(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple) -> bool:
@@ -504,6 +503,7 @@ class KV4Cache:
         self.num_pages, self.page_tokens, self.kv_heads, self.head_dim = num_pages, page_tokens, kv_heads, head_dim
         self.pages = torch.empty(n, dtype=torch.uint8, device=device)
         self.desc = KV4Desc(self.pages.data_ptr(), num_pages, page_tokens, kv_heads, head_dim)
+        self.ref = ctypes.byref(self.desc)
 
 
 def kv4_append(qkv: torch.Tensor, cache: KV4Cache, slots: torch.Tensor, heads: int, positions=None, rope=None,
@@ -512,27 +512,34 @@ def kv4_append(qkv: torch.Tensor, cache: KV4Cache, slots: torch.Tensor, heads: i
     """Norms and rotation of the heads of qkv [M, (heads + 2 kv_heads) head_dim] (float16), keys and values
     stored at `slots` (int32 [M], negative: not stored); returns the queries [M, heads, head_dim] (None for
     heads = 0). rope float32 [positions, rot]: rot/2 cosines, rot/2 sines; positions int32 [M]."""
-    D, H = cache.head_dim, heads + 2 * cache.kv_heads
-    half, rot = torch.float16, rope.shape[-1] if rope is not None else 0
-    _want(qkv.dim() == 2 and qkv.dtype is half and qkv.is_cuda and qkv.shape[1] == H * D and qkv.stride(1) == 1,
-          "kv4_append", "qkv must be a CUDA float16 tensor [M, (heads + 2 kv_heads) head_dim], dense in a row")
+    half, D = torch.float16, cache.head_dim
+    if not (qkv.dtype is half and qkv.is_cuda and qkv.dim() == 2 and qkv.shape[1] == (heads + 2 * cache.kv_heads) * D
+            and qkv.stride(1) == 1):
+        _refuse("kv4_append", "qkv must be a CUDA float16 tensor [M, (heads + 2 kv_heads) head_dim], dense in a row")
     M = qkv.shape[0]
-    _want(_vec(slots, torch.int32, M) and _vec(positions, torch.int32, M), "kv4_append",
-          "slots and positions must be CUDA int32 vectors of M elements")
-    _want(rope is None or (rope.dim() == 2 and _dense(rope, torch.float32, (rope.shape[0], rot))), "kv4_append",
-          "rope must be a contiguous CUDA float32 tensor [positions, rot]")
-    _want(_vec(q_norm, half, D) and _vec(k_norm, half, D), "kv4_append",
-          "q_norm and k_norm must be CUDA float16 vectors of head_dim elements")
+    if not (_vec(slots, torch.int32, M) and _vec(positions, torch.int32, M)):
+        _refuse("kv4_append", "slots and positions must be CUDA int32 vectors of M elements")
+    rope_p = norm_q = norm_k = q_p = None
+    rows = rot = 0
+    if rope is not None:
+        if not (rope.dtype is torch.float32 and rope.is_cuda and rope.dim() == 2 and rope.is_contiguous()):
+            _refuse("kv4_append", "rope must be a contiguous CUDA float32 tensor [positions, rot]")
+        rows, rot = rope.shape
+        rope_p = rope.data_ptr()
+    if q_norm is not None or k_norm is not None:
+        if not (_vec(q_norm, half, D) and _vec(k_norm, half, D)):
+            _refuse("kv4_append", "q_norm and k_norm must be CUDA float16 vectors of head_dim elements")
+        norm_q, norm_k = _ptr(q_norm), _ptr(k_norm)
     if heads > 0:
         if q is None:
             q = _new((M, heads, D), half, qkv.device, stream)
-        else:
-            _want(_dense(q, half, (M, heads, D)), "kv4_append",
-                  "q must be a contiguous CUDA float16 tensor [M, heads, head_dim]")
-    _check(w4a16_kv4_append(qkv.data_ptr(), qkv.stride(0), heads, q.data_ptr() if heads > 0 else None, cache.desc,
-                            slots.data_ptr(), _ptr(positions), _ptr(rope), rope.shape[0] if rope is not None else 0,
-                            rot, int(adjacent), _ptr(q_norm), _ptr(k_norm), eps, M, _stream_handle(stream)),
-           "w4a16_kv4_append")
+        elif not _dense(q, half, (M, heads, D)):
+            _refuse("kv4_append", "q must be a contiguous CUDA float16 tensor [M, heads, head_dim]")
+        q_p = q.data_ptr()
+    rc = lib.w4a16_kv4_append(qkv.data_ptr(), qkv.stride(0), heads, q_p, cache.ref, slots.data_ptr(), _ptr(positions),
+                              rope_p, rows, rot, int(adjacent), norm_q, norm_k, eps, M, _stream_handle(stream))
+    if rc != OK:
+        raise W4A16Error(rc, "w4a16_kv4_append")
     return q if heads > 0 else None
 
 
@@ -540,15 +547,17 @@ def kv4_load(cache: KV4Cache, slots: torch.Tensor, out=None, stream=None):
     """The stored values at `slots` (int32 [n]): keys and values, float16 [n, kv_heads, head_dim] each."""
     n = slots.shape[0]
     shape = (n, cache.kv_heads, cache.head_dim)
-    _want(_vec(slots, torch.int32, n), "kv4_load", "slots must be a CUDA int32 vector")
+    if not _vec(slots, torch.int32, n):
+        _refuse("kv4_load", "slots must be a CUDA int32 vector")
     if out is None:
-        k, v = (_new(shape, torch.float16, slots.device, stream) for _ in range(2))
+        k, v = _new(shape, torch.float16, slots.device, stream), _new(shape, torch.float16, slots.device, stream)
     else:
         k, v = out
-        _want(_dense(k, torch.float16, shape) and _dense(v, torch.float16, shape), "kv4_load",
-              "out must be two contiguous CUDA float16 tensors [n, kv_heads, head_dim]")
-    _check(w4a16_kv4_load(cache.desc, slots.data_ptr(), k.data_ptr(), v.data_ptr(), n, _stream_handle(stream)),
-           "w4a16_kv4_load")
+        if not (_dense(k, torch.float16, shape) and _dense(v, torch.float16, shape)):
+            _refuse("kv4_load", "out must be two contiguous CUDA float16 tensors [n, kv_heads, head_dim]")
+    rc = lib.w4a16_kv4_load(cache.ref, slots.data_ptr(), k.data_ptr(), v.data_ptr(), n, _stream_handle(stream))
+    if rc != OK:
+        raise W4A16Error(rc, "w4a16_kv4_load")
     return k, v
 
 
@@ -566,29 +575,30 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, k
     """Attention of q [M, heads, head_dim] (float16) over the cached tokens of B sequences: block_table
     int32 [B, pages], kv_len int32 [B], q_start int32 [B + 1] (sequence b's rows of q). Queries are the last
     tokens of their sequence (causal) or see all of them. scale: 1 / sqrt(head_dim) when None."""
-    half, i32 = torch.float16, torch.int32
-    _want(q.dim() == 3 and q.dtype is half and q.is_cuda and q.shape[2] == cache.head_dim and
-          q.stride()[1:] == (q.shape[2], 1), "kv4_attention",
-          "q must be a CUDA float16 tensor [M, heads, head_dim], dense in a row")
-    M, heads, D = q.shape
+    half, i32, D = torch.float16, torch.int32, cache.head_dim
+    if not (q.dtype is half and q.is_cuda and q.dim() == 3 and q.shape[2] == D and q.stride()[1:] == (D, 1)):
+        _refuse("kv4_attention", "q must be a CUDA float16 tensor [M, heads, head_dim], dense in a row")
+    M, heads = q.shape[0], q.shape[1]
     B = kv_len.shape[0]
-    _want(_vec(kv_len, i32, B) and _vec(q_start, i32, B + 1), "kv4_attention",
-          "kv_len and q_start must be CUDA int32 vectors of B and B + 1 elements")
-    _want(block_table.dim() == 2 and _dense(block_table, i32, (B, block_table.shape[1])), "kv4_attention",
-          "block_table must be a contiguous CUDA int32 tensor [B, pages]")
-    _want(workspace.dtype is torch.uint8 and workspace.is_cuda and workspace.is_contiguous(), "kv4_attention",
-          "workspace must come from kv4_attention_workspace")
-    _want(_dense(lse, torch.float32, (M, heads)), "kv4_attention", "lse must be a contiguous CUDA float32 [M, heads]")
+    if not (_vec(kv_len, i32, B) and _vec(q_start, i32, B + 1)):
+        _refuse("kv4_attention", "kv_len and q_start must be CUDA int32 vectors of B and B + 1 elements")
+    if not (block_table.dtype is i32 and block_table.is_cuda and block_table.dim() == 2 and block_table.shape[0] == B
+            and block_table.is_contiguous()):
+        _refuse("kv4_attention", "block_table must be a contiguous CUDA int32 tensor [B, pages]")
+    if not (workspace.dtype is torch.uint8 and workspace.is_cuda and workspace.is_contiguous()):
+        _refuse("kv4_attention", "workspace must come from kv4_attention_workspace")
+    if not _dense(lse, torch.float32, (M, heads)):
+        _refuse("kv4_attention", "lse must be a contiguous CUDA float32 tensor [M, heads]")
     if out is None:
         out = _new((M, heads, D), half, q.device, stream)
-    else:
-        _want(_dense(out, half, (M, heads, D)), "kv4_attention",
-              "out must be a contiguous CUDA float16 tensor [M, heads, head_dim]")
-    _check(w4a16_kv4_attention(q.data_ptr(), q.stride(0), heads, cache.desc, block_table.data_ptr(),
-                               block_table.shape[1], kv_len.data_ptr(), q_start.data_ptr(), B, M, max_q_len,
-                               int(causal), D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse),
-                               workspace.data_ptr(), workspace.numel(), _stream_handle(stream)),
-           "w4a16_kv4_attention")
+    elif not _dense(out, half, (M, heads, D)):
+        _refuse("kv4_attention", "out must be a contiguous CUDA float16 tensor [M, heads, head_dim]")
+    rc = lib.w4a16_kv4_attention(q.data_ptr(), q.stride(0), heads, cache.ref, block_table.data_ptr(),
+                                 block_table.shape[1], kv_len.data_ptr(), q_start.data_ptr(), B, M, max_q_len,
+                                 int(causal), D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse),
+                                 workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
+    if rc != OK:
+        raise W4A16Error(rc, "w4a16_kv4_attention")
     return out
 
 
@@ -598,19 +608,20 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     """One token per row of logits [M, V] (float16, rows of any stride) by the uniform numbers u [M]:
     (tokens int32 [M], probs float32 [M]). temperature, top_p, min_p float32 [M], top_k int32 [M], or None."""
     f = torch.float32
-    _want(logits.dim() == 2 and logits.dtype is torch.float16 and logits.is_cuda and logits.stride(1) == 1, "sample",
-          "logits must be a CUDA float16 tensor [M, V], dense in a row")
+    if not (logits.dtype is torch.float16 and logits.is_cuda and logits.dim() == 2 and logits.stride(1) == 1):
+        _refuse("sample", "logits must be a CUDA float16 tensor [M, V], dense in a row")
     M, V = logits.shape
-    _want(_vec(u, f, M) and _vec(temperature, f, M) and _vec(top_k, torch.int32, M) and _vec(top_p, f, M) and
-          _vec(min_p, f, M), "sample",
-          "u, temperature, top_p, min_p must be CUDA float32 vectors, top_k an int32 one, of M elements")
+    if not (_vec(u, f, M) and _vec(temperature, f, M) and _vec(top_k, torch.int32, M) and _vec(top_p, f, M)
+            and _vec(min_p, f, M)):
+        _refuse("sample", "u, temperature, top_p, min_p must be CUDA float32 vectors, top_k an int32 one, of M elements")
     if out is None:
         tokens, probs = _new(M, torch.int32, logits.device, stream), _new(M, f, logits.device, stream)
     else:
         tokens, probs = out
-        _want(_vec(tokens, torch.int32, M) and _vec(probs, f, M), "sample",
-              "out must be a CUDA int32 and a float32 vector of M elements")
-    _check(w4a16_sample(logits.data_ptr(), logits.stride(0), M, V, _ptr(temperature), _ptr(top_k), _ptr(top_p),
-                        _ptr(min_p), u.data_ptr(), tokens.data_ptr(), _ptr(probs), _stream_handle(stream)),
-           "w4a16_sample")
+        if not (_vec(tokens, torch.int32, M) and _vec(probs, f, M)):
+            _refuse("sample", "out must be a CUDA int32 and a float32 vector of M elements")
+    rc = lib.w4a16_sample(logits.data_ptr(), logits.stride(0), M, V, _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                          _ptr(min_p), u.data_ptr(), tokens.data_ptr(), _ptr(probs), _stream_handle(stream))
+    if rc != OK:
+        raise W4A16Error(rc, "w4a16_sample")
     return tokens, probs
