@@ -159,8 +159,14 @@ class Batch:
         self.start = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
         self.work = W.kv4_attention_workspace(self.cache)
 
-    def args(self):
-        return dict(block_table=cuda(self.table), kv_len=cuda(np.array(self.lens, np.int32)), q_start=cuda(self.start),
+    def args(self, wide=False):
+        """wide: a block table for far longer sequences (its columns beyond theirs name no page), as it is
+        allocated once for all lengths; of several query rows it makes the tcgen05 kernel the choice."""
+        table = self.table
+        if wide:
+            table = np.full((table.shape[0], table.shape[1] + 2 ** 20 // self.cache.page_tokens), -1, np.int32)
+            table[:, : self.table.shape[1]] = self.table
+        return dict(block_table=cuda(table), kv_len=cuda(np.array(self.lens, np.int32)), q_start=cuda(self.start),
                     max_q_len=max(1, max(self.q_lens)), workspace=self.work)
 
     def want(self, scale, causal=True):
@@ -189,15 +195,19 @@ ATTENTION = [
     ([350], [200], 4, 2, 128, 4096),                         # a page longer than the sequence
     ([2500], [1], 24, 4, 256, 32),
     ([700], [150], 20, 4, 256, 64),
+    ([5000], [40], 8, 2, 64, 16),                            # many pages, parts of a unit from several CTAs
+    ([3000, 64, 63, 1], [26, 64, 63, 1], 20, 4, 256, 16),    # whole prompts: the first rows see a token or two
+    ([900] * 12, [17] * 12, 4, 1, 128, 64),
 ]
 
 
 @pytest.mark.parametrize("lens,q_lens,H,KV,D,page", ATTENTION, ids=[f"case{i}" for i in range(len(ATTENTION))])
+@pytest.mark.parametrize("wide", [False, True], ids=["short", "wide"])
 @pytest.mark.parametrize("causal", [True, False])
-def test_attention_matches_64_bits(W, lens, q_lens, H, KV, D, page, causal):
+def test_attention_matches_64_bits(W, lens, q_lens, H, KV, D, page, causal, wide):
     b = Batch(W, len(lens) * 100 + D + page, lens, q_lens, H, KV, D, page)
     lse = torch.full((sum(q_lens), H), 7.0, device="cuda")
-    out = W.kv4_attention(cuda(b.q), b.cache, lse=lse, causal=causal, **b.args())
+    out = W.kv4_attention(cuda(b.q), b.cache, lse=lse, causal=causal, **b.args(wide))
     ok(W)
     want, want_lse, bound = b.want(D ** -0.5, causal)
     close(out, want, bound)
@@ -220,11 +230,12 @@ def test_attention_with_rows_of_a_wider_buffer_and_another_scale(W):
     close(out, want, bound)
 
 
+@pytest.mark.parametrize("wide", [False, True], ids=["short", "wide"])
 @pytest.mark.parametrize("gain", [1e-4, 300.0])
-def test_attention_of_small_and_large_values(W, gain):
+def test_attention_of_small_and_large_values(W, gain, wide):
     # values near fp16's smallest normal numbers and far above one: products p * scale keep their bits
     b = Batch(W, 12, [333, 40], [1, 9], 20, 4, 256, 16, gain=gain)
-    out = W.kv4_attention(cuda(b.q), b.cache, **b.args())
+    out = W.kv4_attention(cuda(b.q), b.cache, **b.args(wide))
     ok(W)
     want, _, bound = b.want(1 / 16)
     close(out, want, bound + 2.0 ** -25)
@@ -259,9 +270,10 @@ def test_attention_of_equal_keys_is_the_mean_of_the_values(W):
     assert (np.abs(out[0].float().cpu().numpy() - mean) <= 2.0 ** -10 * 2 * mean + 1e-6).all()
 
 
-def test_attention_repeats_bit_for_bit_and_on_another_stream(W):
-    b = Batch(W, 15, [3000, 1200, 50], [1, 1, 1], 20, 4, 256, 32)
-    q, args = cuda(b.q), b.args()
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [40, 1, 17]], ids=["one", "several"])
+def test_attention_repeats_bit_for_bit_and_on_another_stream(W, q_lens):
+    b = Batch(W, 15, [3000, 1200, 50], q_lens, 20, 4, 256, 32)
+    q, args = cuda(b.q), b.args(wide=True)
     a = W.kv4_attention(q, b.cache, **args)
     again = W.kv4_attention(q, b.cache, **args)
     s = torch.cuda.Stream()
@@ -272,6 +284,16 @@ def test_attention_repeats_bit_for_bit_and_on_another_stream(W):
     assert torch.equal(a.view(torch.int16), other.view(torch.int16))
     want, _, bound = b.want(1 / 16)
     close(a, want, bound)
+
+
+def test_attention_with_negative_and_zero_scale(W):
+    b = Batch(W, 21, [100, 300], [1, 30], 4, 2, 128, 16)
+    for wide in (False, True):
+        for scale in (-0.1, 0.0):
+            out = W.kv4_attention(cuda(b.q), b.cache, scale=scale, **b.args(wide))
+            ok(W)
+            want, _, bound = b.want(scale)
+            close(out, want, bound, f"{scale} {wide}")
 
 
 def test_a_captured_step_replays_with_other_lengths(W):
@@ -293,6 +315,18 @@ def test_a_captured_step_replays_with_other_lengths(W):
         want, _, bound = ref.attention(b.q, [k[:n] for k, n in zip(b.keys, lens)], [v[:n] for v, n in zip(b.values, lens)],
                                        [1, 1], D ** -0.5)
         close(out, want, bound, str(lens))
+
+
+def test_pages_that_do_not_exist_many_rows(W):
+    b = Batch(W, 22, [200, 64], [50, 30], 4, 2, 64, 16)
+    b.table[0, 2], b.table[0, 7] = -1, 10 ** 6  # tokens 32..47 and 112..127 of the first sequence
+    out = W.kv4_attention(cuda(b.q), b.cache, causal=False, **b.args(wide=True))
+    torch.cuda.synchronize()
+    assert W.w4a16_device_status() == W.ERR_BOUNDS
+    left = np.r_[0:32, 48:112, 128:200]
+    want, _, bound = ref.attention(b.q, [b.keys[0][left], b.keys[1]], [b.values[0][left], b.values[1]], [50, 30], 0.125, False)
+    close(out, want, bound)
+    ok(W)
 
 
 def test_pages_and_lengths_that_do_not_exist_are_cut_off(W):
@@ -362,13 +396,14 @@ def test_offsets_beyond_32_bits(W):
     close(out, want, bound)
 
 
-def test_the_index_checking_build_runs_clean(W):
+@pytest.mark.parametrize("wide", [False, True], ids=["short", "wide"])
+def test_the_index_checking_build_runs_clean(W, wide):
     import ctypes
 
     D_ = W.load_debug_bounds()
     b = Batch(W, 20, [100, 17, 0], [1, 20, 1], 6, 2, 128, 16)
     s = torch.cuda.current_stream().cuda_stream
-    args = b.args()
+    args = b.args(wide)
     q = cuda(b.q)
     out = torch.empty_like(q)
     assert D_.w4a16_kv4_attention(q.data_ptr(), q.stride(0), 6, ctypes.byref(b.cache.desc), args["block_table"].data_ptr(),

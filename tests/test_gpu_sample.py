@@ -43,7 +43,9 @@ def peaked(rng, M, V, std=2.0):
 SETTINGS = [dict(), dict(temperature=0.6, top_k=20, top_p=0.95), dict(temperature=1.3, top_p=0.8), dict(min_p=0.05),
             dict(temperature=0.7, top_k=50, min_p=0.02), dict(top_k=1000, top_p=0.5, min_p=0.001), dict(top_k=3),
             dict(temperature=5.0), dict(top_p=0.01), dict(top_p=0.0), dict(min_p=1.0), dict(min_p=2.0),
-            dict(top_k=10 ** 9, top_p=1.0, min_p=0.0)]
+            dict(top_k=10 ** 9, top_p=1.0, min_p=0.0), dict(top_k=400), dict(top_k=700, top_p=0.9), dict(top_k=6000, top_p=0.99),
+            dict(temperature=50.0), dict(temperature=50.0, top_p=0.7), dict(temperature=0.02), dict(temperature=3.0, min_p=1e-6),
+            dict(temperature=50.0, min_p=0.9), dict(top_k=5, min_p=1e-9), dict(temperature=1e30)]
 
 
 @pytest.mark.parametrize("kw", SETTINGS, ids=[str(i) for i in range(len(SETTINGS))])
@@ -157,6 +159,34 @@ def test_settings_of_each_row_and_the_batch_do_not_matter_to_another(W):
         assert a[0] == tokens[r] and b[0] == probs[r]
         s = Sampled(x[r], float(u[r]), float(t[r]), int(k[r]), float(p[r]), float(m[r]))
         assert s.check(tokens[r], probs[r])
+
+
+@pytest.mark.parametrize("shape", ["negative", "narrow", "two_levels", "many_top", "steep"])
+def test_rows_of_unusual_shape(W, shape):
+    rng = np.random.default_rng(9)
+    M, V = 7, 40000
+    x = {"negative": lambda: -30 + 2 * rng.normal(size=(M, V)),           # every logit below 0
+         "narrow": lambda: 1e-3 * rng.normal(size=(M, V)),                # all weights nearly equal
+         "two_levels": lambda: np.where(rng.random((M, V)) < 0.5, 3.0, -3.0),
+         "many_top": lambda: np.where(rng.random((M, V)) < 0.2, 5.0, rng.normal(size=(M, V))),  # 8000 equal best
+         "steep": lambda: -np.arange(V)[None, :] / 500.0 + rng.normal(size=(M, V)) * 1e-2}[shape]().astype(np.float16)
+    u = rng.random(M).astype(np.float32)
+    for kw in (dict(), dict(top_p=0.6), dict(top_k=37), dict(min_p=0.3), dict(temperature=0.5, top_k=5000, top_p=0.9)):
+        tokens, probs = draw(W, x, u, **kw)
+        for r in range(M):
+            s = Sampled(x[r], float(u[r]), **kw)
+            assert s.check(tokens[r], probs[r]), (shape, kw, r, tokens[r], probs[r])
+
+
+@pytest.mark.parametrize("M", [1, 2, 40, 300])
+def test_a_row_does_not_depend_on_the_batch(W, M):
+    rng = np.random.default_rng(10)
+    V = 50000
+    row = peaked(rng, 1, V)
+    for kw in (dict(temperature=0.7, top_k=30), dict(top_p=0.9), dict(temperature=2.5), dict(min_p=0.01)):
+        one = draw(W, row, [0.37], **kw)
+        many = draw(W, np.repeat(row, M, axis=0), [0.37] * M, **kw)
+        assert (many[0] == one[0][0]).all() and (many[1] == one[1][0]).all()
 
 
 def test_uniform_numbers_cover_the_distribution(W):

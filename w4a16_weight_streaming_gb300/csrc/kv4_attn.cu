@@ -56,7 +56,6 @@ struct Decode {
 };
 
 constexpr int kMaxCtas = 640;
-constexpr int kDecodeRows = 16;  // query rows a key/value head of a sequence, above which the tcgen05 kernel is taken
 constexpr size_t kCounterBytes = 4096;
 static_assert(kMaxCtas * 4 <= kCounterBytes, "a counter a CTA");
 
@@ -726,12 +725,33 @@ cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, const Launch
     return cudaLaunchKernelEx(&cfg, kv4_decode_kernel<D, Narrow>, p, v, ctx.timeout_ns, ctx.status);
 }
 
+// Wide where half the SMs suffice for the work units, narrow otherwise.
 template <int D>
 cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, const LaunchCtx& ctx) {
     const int grp = p.heads / v.kv_heads;
     const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * grp;
     const int64_t units = std::min<int64_t>(p.B, p.M) * v.kv_heads * ((rows + kRows - 1) / kRows);
     return 2 * units <= ctx.sm_count ? launch_decode<D, false>(p, v, ctx) : launch_decode<D, true>(p, v, ctx);
+}
+
+// This kernel takes a pass over a sequence's tokens for every 8 query rows, the tcgen05 kernel one for every
+// 128, but starts and ends slower. Fitted to 1, 16 and 64 sequences of 777 .. 16384 tokens with 1 .. 120 rows
+// a key/value head, in us on 152 SMs: a start, and so much a 16-token tile of 8 rows (here) or a 64-token
+// tile of 128 rows (there). Both sides, measured: 16 sequences of 4096 and 4 heads of 256, 10 rows 47.3 | 46.7,
+// 20 rows 63.6 | 47.5; 8 heads of 128, 20 rows 61.1 | 59.6, 25 rows 77.7 | 60.4; 16 heads of 64, 24 rows
+// 74.2 | 93.2; one sequence of 16384, heads of 256, 40 rows 31.5 | 49.2, 80 rows 57.4 | 52.4. The lengths are
+// on the device: the block table's width stands for them.
+bool decode_is_faster(const Kv4AttnParams& p, const Kv4Cache& c) {
+    const double start_here = c.head_dim == 256 ? 11.5 : c.head_dim == 128 ? 9.0 : 8.0;
+    const double start_there = c.head_dim == 256 ? 28.0 : c.head_dim == 128 ? 24.5 : 20.0;
+    const double tile_here = c.head_dim == 256 ? 0.142 : c.head_dim == 128 ? 0.081 : 0.053;
+    const double tile_there = c.head_dim == 256 ? 1.05 : c.head_dim == 128 ? 0.86 : 0.79;
+    const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / c.kv_heads);
+    const double heads = static_cast<double>(std::min(p.B, p.M)) * c.kv_heads;
+    const double tokens = static_cast<double>(p.max_pages) * c.page_tokens;
+    const double here = start_here + tile_here / 152 * heads * static_cast<double>((rows + kRows - 1) / kRows) * (tokens / kKv4Tile);
+    const double there = start_there + tile_there / 152 * heads * static_cast<double>((rows + 127) / 128) * (tokens / 64);
+    return here <= there;
 }
 
 }  // namespace
@@ -748,8 +768,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnParams& p, const Kv4Cache& c, cons
     v.page_shift = 0;
     while ((1 << v.page_shift) < c.page_tokens) ++v.page_shift;
     v.kv_heads = c.kv_heads;
-    const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / c.kv_heads);
-    if (rows > kDecodeRows) return launch_kv4_prompt(p, v, c.head_dim, ctx);
+    if (!decode_is_faster(p, c)) return launch_kv4_prompt(p, v, c.head_dim, ctx);
     switch (c.head_dim) {
         case 64: return launch_decode<64>(p, v, ctx);
         case 128: return launch_decode<128>(p, v, ctx);
