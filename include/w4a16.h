@@ -341,7 +341,7 @@ int w4a16_kv4_load(const w4a16_kv4_cache* cache, const int32_t* slots, uint16_t*
 size_t w4a16_kv4_attention_workspace_bytes(int head_dim);
 
 /*
- * out = softmax(scale * q . k'^T) . v' over the cached tokens of each sequence, k' and v' unrounded.
+ * out = softmax(scale * q . k'^T) . v' over the cached tokens of each sequence.
  *   q:           fp16 [M][heads][head_dim], rows q_stride elements apart (a multiple of 8); head h
  *                attends with key/value head h / (heads / kv_heads)
  *   block_table: int32 [B][max_pages], page j of sequence b holds its tokens j * page_tokens and on
@@ -349,13 +349,16 @@ size_t w4a16_kv4_attention_workspace_bytes(int head_dim);
  *   q_start:     int32 [B + 1], not decreasing, within 0..M: sequence b's queries are rows
  *                q_start[b] .. q_start[b+1]-1 of q, and, when causal is 1, the last of its cached tokens:
  *                query i of n sees tokens 0 .. kv_len - n + i. When causal is 0 it sees all kv_len.
- *   max_q_len:   an upper bound of q_start[b+1] - q_start[b] (it chooses the kernel, not the result)
+ *   max_q_len:   an upper bound of q_start[b+1] - q_start[b] (it bears on the choice of the kernel only)
  *   out:         fp16 [M][heads][head_dim]; rows of no sequence are left as they are
  *   lse:         NULL, or fp32 [M][heads]: log(sum(exp(scale q k'))) (-inf for a query that sees nothing)
  * A query that sees no token gives 0. All lengths are read on the device: a captured graph may be
  * replayed with other contents. fp32 scores, softmax and sums; repeats are bit-identical. A page outside
  * the cache, a kv_len or q_start outside its range is cut off (its tokens are not seen) and sets
- * W4A16_ERR_BOUNDS in the device status word. B, M <= 2^20. Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
+ * W4A16_ERR_BOUNDS in the device status word. B, M <= 2^20, M * heads <= 2^28,
+ * max_pages * page_tokens < 2^31. Two kernels (8 query rows a key/value head at a time on mma, exact codes;
+ * 128 at a time on tcgen05, k', v' and the weights rounded to fp16): the choice is by max_q_len, B and the
+ * block table's width. Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
  * MISALIGNED, CUDA.
  */
 int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4a16_kv4_cache* cache,

@@ -154,6 +154,6 @@ struct SampleParams {
     int M;
     int V;
 };
-cudaError_t launch_sample(const SampleParams& p, int sm_count, cudaStream_t s);
+cudaError_t launch_sample(const SampleParams& p, int sm_count, cudaStream_t s, unsigned* status);
 
 }  // namespace w4a16

@@ -76,7 +76,10 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a, uns
     const bool is_k = !is_q && head < a.heads + a.cache.kv_heads;
 
     uint4 raw = make_uint4(0, 0, 0, 0);
-    if (live) raw = *reinterpret_cast<const uint4*>(a.qkv + m * a.qkv_stride + static_cast<int64_t>(head) * D + d0);
+    if (live && in_bounds(m * a.qkv_stride + static_cast<int64_t>(head) * D + d0 + 8 <=
+                              static_cast<int64_t>(a.M - 1) * a.qkv_stride + static_cast<int64_t>(per_row) * D,
+                          status))
+        raw = *reinterpret_cast<const uint4*>(a.qkv + m * a.qkv_stride + static_cast<int64_t>(head) * D + d0);
     float x[8];
     unpack8(raw, x);
 
@@ -147,7 +150,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a, uns
     if (is_q) {
         if (live) {
             if (!ok) packed = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(a.q_out + (m * a.heads + head) * D + d0) = packed;
+            if (in_bounds((m * a.heads + head) * D + d0 + 8 <= static_cast<int64_t>(a.M) * a.heads * D, status))
+                *reinterpret_cast<uint4*>(a.q_out + (m * a.heads + head) * D + d0) = packed;
         }
     }
     // ---- keys and values: the fp16 values above, in 4 bits (query lanes run along for the exchanges)
@@ -253,7 +257,8 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(const Kv4View cache, cons
         }
     }
     uint16_t* out = is_k ? k : v;
-    *reinterpret_cast<uint4*>(out + (row * cache.kv_heads + head) * D + d0) = pack8(x);
+    if (in_bounds((row * cache.kv_heads + head) * D + d0 + 8 <= static_cast<int64_t>(n) * cache.kv_heads * D, status))
+        *reinterpret_cast<uint4*>(out + (row * cache.kv_heads + head) * D + d0) = pack8(x);
 }
 
 template <typename F, typename... A>

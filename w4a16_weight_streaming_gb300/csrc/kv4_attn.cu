@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
         auto locate = [&](int i0) {
             const int tile = t0 + warp + NW * (i0 + lane);
             tile_at = -1;
-            if (tile < t1e) {
+            if (tile < t1e && in_bounds((tile * kKv4Tile >> cache.page_shift) < p.max_pages, status)) {
                 const int tok = tile * kKv4Tile;
                 const int page = p.block_table[static_cast<int64_t>(b) * p.max_pages + (tok >> cache.page_shift)];
                 if (page >= 0 && page < cache.num_pages) {
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
             for (int y = 0; y < G; ++y)
 #pragma unroll
                 for (int w = 0; w < 2; ++w)
-                    raw[y][w] = g < rows ? *reinterpret_cast<const uint4*>(src + y * kKv4Group + 16 * t + 8 * w)
+                    raw[y][w] = g < rows && in_bounds(sq.q0 + pos < p.M, status) ? *reinterpret_cast<const uint4*>(src + y * kKv4Group + 16 * t + 8 * w)
                                          : make_uint4(0, 0, 0, 0);
         }
         // (the first copies are on their way before the queries are used)
@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
         auto finish = [&](int r, int d, float4 v, float total, float top) {
             const int pos = (rt * kRows + r) / grp, hd = (rt * kRows + r) % grp;
             const int64_t at = static_cast<int64_t>(sq.q0 + pos) * p.heads + kvh * grp + hd;
+            if (!in_bounds(at < static_cast<int64_t>(p.M) * p.heads && d + 4 <= D, status)) return;
             const float f = total > 0.f ? 1.f / total : 0.f;
             const __half2 h0 = __floats2half2_rn(v.x * f, v.y * f), h1 = __floats2half2_rn(v.z * f, v.w * f);
             *reinterpret_cast<uint2*>(p.out + at * D + d) =
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
             }
             if (whole)
                 finish(r, d, v, s_row[kRows + r], s_row[r]);
-            else
+            else if (in_bounds(blockIdx.x < kMaxCtas && 2 * kRows + x + 4 <= C::kPart, status))
                 __stcg(reinterpret_cast<float4*>(mine_out + 2 * kRows + x), v);
         }
         if (!whole) {

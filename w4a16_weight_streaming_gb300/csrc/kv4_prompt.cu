@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     x[c] = make_uint4(0, 0, 0, 0);
-                    if (r < rows) x[c] = *reinterpret_cast<const uint4*>(src + c * 8);
+                    if (r < rows && in_bounds(q_row < p.M, status)) x[c] = *reinterpret_cast<const uint4*>(src + c * 8);
                 }
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t v[16];
                     tmem_ld16(lanes + c, v);
                     tmem_wait_ld();
-                    if (r >= rows) continue;
+                    if (r >= rows || !in_bounds(q_row < p.M && blockIdx.x < kKv4MaxPromptCtas, status)) continue;
                     if (whole) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int tok = (t0 + i) * kTok + lane * kKv4Tile;
                     there = max(0, min(kKv4Tile, sq.n - tok));
                     from = -1;
-                    if (there > 0 && i + lane / kSub < nt) {
+                    if (there > 0 && i + lane / kSub < nt && in_bounds((tok >> cache.page_shift) < p.max_pages, status)) {
                         const int page = p.block_table[static_cast<int64_t>(b) * p.max_pages + (tok >> cache.page_shift)];
                         if (page >= 0 && page < cache.num_pages) {
                             from = cache.tile_offset<D>(page, kvh, tok & ((1 << cache.page_shift) - 1));
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // A thread has a row and 16 of its elements at a time, from two parts in one round of loads.
                 const int n = cta1 - cta0 + 1, r = tid & (kRows - 1);
                 constexpr int kGroups = kThreads / kRows;
-                if (tid < kGroups * kRows && r < rows) {
+                if (tid < kGroups * kRows && r < rows && in_bounds(cta1 < kKv4MaxPromptCtas, status)) {
                     float top = -INFINITY, total = 0.f;
                     for (int c = 0; c < n; ++c) top = fmaxf(top, __ldcg(part_of(cta0 + c) + r));
                     for (int c = 0; c < n; ++c) {

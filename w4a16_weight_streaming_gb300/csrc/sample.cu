@@ -14,7 +14,7 @@
 // at most 65,536 values and equal logits have equal weights, so a row is described by how often each value
 // occurs, and its weight is computed once a value.
 //
-// Window: the first kernel counts the 8192 values below the largest logit (8 octaves), one shared-memory
+// Window: the first kernel counts the 4096 values below the largest logit (4 octaves), one shared-memory
 // atomic each, after a first pass that finds the largest. Where the mass of all tokens is asked for, the
 // weights of those below the window are added up directly. A row is one CTA or a thread-block cluster
 // whose counts are added up in rank 0. Draws and cuts below the window are left to the second kernel.
@@ -135,7 +135,8 @@ __device__ __forceinline__ Fine fine_of(int bin, uint32_t sums, int C, uint32_t 
 }
 
 // ---------------------------------------------------------------------------------------- window
-constexpr int kWindow = 8192;      // values counted below (and with) the largest
+constexpr int kWindowThreads = 256;
+constexpr int kWindow = 4096;      // values counted below (and with) the largest, 16 a thread
 constexpr int kUndone = -2;        // token of a row that is left to the counting kernel
 constexpr int kVectors = 4;        // vectors of 8 logits a thread loads at a time
 constexpr float kSmallWeight = 7.62939453125e-6f;  // 2^-17: 2^40 times less is below 2^23, exact in an fp32
@@ -146,10 +147,10 @@ struct WindowShared {
     uint32_t cut_at;           // a thread's answer
     unsigned long long cut_mass;
     unsigned long long tail;   // rank 0: mass below the window
-    uint32_t warp_key[kThreads / 32];
-    uint32_t warp_count[kThreads / 32];
-    unsigned long long warp_mass[kThreads / 32];
-    unsigned long long warp_tail[kThreads / 32];
+    uint32_t warp_key[16];
+    uint32_t warp_count[16];
+    unsigned long long warp_mass[16];
+    unsigned long long warp_tail[16];
     uint32_t pick_key, pick_index, pick_rank;
 };
 // counts, positions and weights of the window's values, largest first
@@ -174,6 +175,7 @@ __device__ __forceinline__ void add_dsmem_u64(uint32_t addr, unsigned long long 
 
 // Where the `index`-th (from 0, in index order) occurrence of `key` is in elements begin .. end-1 of a
 // row: written to *token by the thread that finds it. All threads of the CTA; scratch: 1024 words.
+template <int kThreads>
 __device__ __forceinline__ void find_occurrence(const uint16_t* src, int begin, int end, uint32_t key, uint32_t index,
                                                 uint32_t* scratch, int32_t* token) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -201,7 +203,7 @@ __device__ __forceinline__ void find_occurrence(const uint16_t* src, int begin, 
             bits |= (key_of(w[j] & 0xFFFFu) == key ? 1u << (2 * j) : 0u) | (key_of(w[j] >> 16) == key ? 2u << (2 * j) : 0u);
         return bits;
     };
-    // a warp's share in rounds of 128 vectors, at most 64 of them (V <= 1,000,000): how many in each
+    // a warp's share in rounds of 128 vectors (V <= 1,000,000: at most 62, or 123 with 8 warps): how many in each
     __syncthreads();
     uint32_t count = 0;
     for (int v = v0, round = 0; v < v1; v += 128, ++round) {
@@ -212,7 +214,7 @@ __device__ __forceinline__ void find_occurrence(const uint16_t* src, int begin, 
 #pragma unroll
         for (int k = 0; k < 4; ++k) n += __popc(bits_of(x[k]));
         n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0) scratch[warp * 64 + round] = count;
+        if (lane == 0) scratch[warp * (32768 / kThreads) + round] = count;
         count += n;
     }
     __syncwarp();
@@ -223,8 +225,8 @@ __device__ __forceinline__ void find_occurrence(const uint16_t* src, int begin, 
     for (int i = 0; i < warp; ++i) before += totals[i];
     if (index < before || index >= before + count) return;
     int round = 0;
-    while (v0 + 128 * (round + 1) < v1 && before + scratch[warp * 64 + round + 1] <= index) ++round;
-    before += scratch[warp * 64 + round];
+    while (v0 + 128 * (round + 1) < v1 && before + scratch[warp * (32768 / kThreads) + round + 1] <= index) ++round;
+    before += scratch[warp * (32768 / kThreads) + round];
     uint4 x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] = fetch(v0 + 128 * round + 32 * k + lane);
@@ -244,11 +246,12 @@ __device__ __forceinline__ void find_occurrence(const uint16_t* src, int begin, 
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kWindowThreads, 4)
     sample_window_kernel(const uint16_t* __restrict__ logits, int64_t stride, int V, int slice,
                          const float* __restrict__ temperature, const int32_t* __restrict__ top_k,
                          const float* __restrict__ top_p, const float* __restrict__ min_p, const float* __restrict__ u,
-                         int32_t* __restrict__ tokens, float* __restrict__ probs, int C) {
+                         int32_t* __restrict__ tokens, float* __restrict__ probs, int C, unsigned* status) {
+    constexpr int kThreads = kWindowThreads;
     extern __shared__ __align__(16) uint8_t smem[];
     WindowShared& sh = *reinterpret_cast<WindowShared*>(smem);
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem + 1024);
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto load = [&](int i0) {
 #pragma unroll
         for (int k = 0; k < kVectors; ++k)
-            v[k] = i0 + k * kThreads < vectors
+            v[k] = i0 + k * kThreads < vectors && in_bounds(first + 8 * (i0 + k * kThreads) + 8 <= V, status)
                        ? *reinterpret_cast<const uint4*>(aligned + 8 * static_cast<int64_t>(i0 + k * kThreads))
                        : make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);
     };
@@ -659,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         return;
     }
     // (a sparse row's is looked for by rank 0 in the whole row: equal logits among its few likely tokens)
-    find_occurrence(src, sparse ? 0 : begin, sparse ? V : end, key, sh.pick_index, reinterpret_cast<uint32_t*>(weights), tokens + row);
+    find_occurrence<kThreads>(src, sparse ? 0 : begin, sparse ? V : end, key, sh.pick_index, reinterpret_cast<uint32_t*>(weights), tokens + row);
 }
 
 // -------------------------------------------------------------------------------------- counting
@@ -676,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sample_kernel(const uint16_t* __restrict__ logits, int64_t stride, int V, int slice,
                   const float* __restrict__ temperature, const int32_t* __restrict__ top_k,
                   const float* __restrict__ top_p, const float* __restrict__ min_p, const float* __restrict__ u,
-                  int32_t* __restrict__ tokens, float* __restrict__ probs, int C) {
+                  int32_t* __restrict__ tokens, float* __restrict__ probs, int C, unsigned* status) {
     extern __shared__ __align__(16) uint8_t smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem);
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem + 1024);  // two 16-bit counters a word
@@ -714,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4 v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (i0 + k * kThreads < vectors)
+            if (i0 + k * kThreads < vectors && in_bounds(first + 8 * (i0 + k * kThreads) + 8 <= V, status))
                 v[k] = *reinterpret_cast<const uint4*>(src + first + 8 * static_cast<int64_t>(i0 + k * kThreads));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -936,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (sh.pick_owner != static_cast<int>(rank)) return;
 
     // ---- the owner finds occurrence pick_index of the value in its slice, in index order
-    find_occurrence(src, begin, end, sh.pick_key, sh.pick_index, sums, tokens + row);
+    find_occurrence<kThreads>(src, begin, end, sh.pick_key, sh.pick_index, sums, tokens + row);
 }
 
 }  // namespace
@@ -944,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 namespace {
 
 template <typename F>
-cudaError_t launch_rows(F* f, const SampleParams& p, int C, size_t smem, cudaStream_t s) {
+cudaError_t launch_rows(F* f, const SampleParams& p, int C, int threads, size_t smem, cudaStream_t s, unsigned* status) {
     const int slice = ((p.V + C - 1) / C + 7) / 8 * 8;
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -954,7 +957,7 @@ cudaError_t launch_rows(F* f, const SampleParams& p, int C, size_t smem, cudaStr
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.M) * C), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -967,23 +970,24 @@ cudaError_t launch_rows(F* f, const SampleParams& p, int C, size_t smem, cudaStr
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, f, p.logits, p.stride, p.V, slice, p.temperature, p.top_k, p.top_p, p.min_p, p.u,
-                              p.tokens, p.probs, C);
+                              p.tokens, p.probs, C, status);
 }
 
 }  // namespace
 
-cudaError_t launch_sample(const SampleParams& p, int sm_count, cudaStream_t s) {
-    // Window: two CTAs an SM. Few rows are spread over up to 16 CTAs, more over up to 8 (clusters of 16
-    // leave SMs idle: 16 rows of 248,320 took 37 us with 16, 25 with 8), many over as many as make three
-    // rounds (256 rows: 258 us with 1, 172 with 2, 175 with 4).
+cudaError_t launch_sample(const SampleParams& p, int sm_count, cudaStream_t s, unsigned* status) {
+    // Window: 256 threads, four CTAs an SM (with 512 and two, and 8192 values: 256 rows of 248,320 153 us
+    // against 139, 33 mixed rows of 32,003 26.7 against 24.4). Few rows are spread over up to 16 CTAs (1 row
+    // 12.4 us, with 8 14.4), more over up to 8 (16 rows 12.5, with 16 13.4), many over as many as make two
+    // rounds (256 rows: 216 with 1, 167 with 2, 139 with 4, 149 with 8).
     int C = p.M <= 8 ? 16 : 8;
-    while (C > 1 && static_cast<int64_t>(p.M) * C * 10 > 34LL * sm_count) C /= 2;
-    cudaError_t e = launch_rows(sample_window_kernel, p, C, kWindowSmem, s);
+    while (C > 1 && static_cast<int64_t>(p.M) * C > 7LL * sm_count) C /= 2;
+    cudaError_t e = launch_rows(sample_window_kernel, p, C, kWindowThreads, kWindowSmem, s, status);
     if (e != cudaSuccess) return e;
     // Counting: one CTA an SM; enough a row that each counts fewer than 65,536 values.
     C = p.M <= 9 ? 16 : p.M <= 18 ? 8 : 4;
     while (C < 16 && (p.V + C - 1) / C > 65528) C *= 2;
-    return launch_rows(sample_kernel, p, C, kSmemBytes, s);
+    return launch_rows(sample_kernel, p, C, kThreads, kSmemBytes, s, status);
 }
 
 }  // namespace w4a16

@@ -1071,6 +1071,7 @@ int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4
     if (rc != W4A16_OK) return rc;
     if (heads > 1024 || heads % c.kv_heads != 0 || B > (1 << 20) || M > (1 << 20)) return W4A16_ERR_UNSUPPORTED_SHAPE;
     if (static_cast<int64_t>(max_pages) * c.page_tokens >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<int64_t>(M) * heads > (1LL << 28)) return W4A16_ERR_UNSUPPORTED_SHAPE;
     const int64_t width = static_cast<int64_t>(heads) * c.head_dim;
     if (q_stride < width && M > 1) return W4A16_ERR_INVALID_ARG;
     if (q_stride % 8 != 0 || q_stride > (1LL << 32)) return W4A16_ERR_UNSUPPORTED_SHAPE;
@@ -1133,7 +1134,7 @@ int w4a16_sample(const uint16_t* logits, int64_t stride, int M, int V, const flo
     DeviceInfo d;
     if (!device_info(&d)) return W4A16_ERR_CUDA;
     SampleParams p = {logits, stride, temperature, top_k, top_p, min_p, u, tokens, probs, M, V};
-    return launched(launch_sample(p, d.sm_count, static_cast<cudaStream_t>(stream)));
+    return launched(launch_sample(p, d.sm_count, static_cast<cudaStream_t>(stream), d.status));
 }
 
 int w4a16_last_dispatch(char* buf, size_t len) {
