@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a, uns
                 *reinterpret_cast<uint4*>(a.q_out + (m * a.heads + head) * D + d0) = packed;
         }
     }
-    // ---- keys and values: the fp16 values above, in 4 bits (query lanes run along for the exchanges)
+    if (__all_sync(0xffffffffu, is_q || !live)) return;
+    // ---- keys and values: the fp16 values above, in 4 bits (query lanes of a mixed warp run along)
     unpack8(packed, x);
     float lo = x[0], hi = x[0];
 #pragma unroll
@@ -169,10 +170,14 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a, uns
     }
     const __half scale = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
     const float sf = __half2float(scale);
+    // (x - min) / scale, correctly rounded: a quotient by the rounded reciprocal and one correction (Markstein
+    // 1990), 3 instructions an element instead of a division each
+    const float inv_sf = sf > 0.f ? __frcp_rn(sf) : 0.f;
     uint32_t code[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float c = sf > 0.f ? rintf(__fdiv_rn(__fsub_rn(x[i], lo), sf)) : 0.f;
+        const float a = __fsub_rn(x[i], lo), quotient = __fmul_rn(a, inv_sf);
+        const float c = rintf(__fmaf_rn(__fmaf_rn(-quotient, sf, a), inv_sf, quotient));
         code[i] = static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f));
     }
     uint32_t seq = 0;  // code i in nibble i
