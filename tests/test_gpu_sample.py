@@ -45,7 +45,8 @@ SETTINGS = [dict(), dict(temperature=0.6, top_k=20, top_p=0.95), dict(temperatur
             dict(temperature=5.0), dict(top_p=0.01), dict(top_p=0.0), dict(min_p=1.0), dict(min_p=2.0),
             dict(top_k=10 ** 9, top_p=1.0, min_p=0.0), dict(top_k=400), dict(top_k=700, top_p=0.9), dict(top_k=6000, top_p=0.99),
             dict(temperature=50.0), dict(temperature=50.0, top_p=0.7), dict(temperature=0.02), dict(temperature=3.0, min_p=1e-6),
-            dict(temperature=50.0, min_p=0.9), dict(top_k=5, min_p=1e-9), dict(temperature=1e30)]
+            dict(temperature=50.0, min_p=0.9), dict(top_k=5, min_p=1e-9), dict(temperature=1e30), dict(temperature=np.inf),
+            dict(temperature=np.inf, top_p=0.6), dict(temperature=1e-44, top_p=0.9)]
 
 
 @pytest.mark.parametrize("kw", SETTINGS, ids=[str(i) for i in range(len(SETTINGS))])

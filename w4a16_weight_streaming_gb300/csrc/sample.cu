@@ -23,6 +23,8 @@
 // CTA's slice is below 65,536 elements). Each CTA then adds up the cluster's counts of its share of the
 // values and folds them into coarse bins of 32 values, count and mass. Every decision is a search in the
 // 2048 prefix sums followed by a look at the 32 values of one bin.
+#include <cfloat>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(kWindowThreads, 4)
     Softmax sm;
     sm.kmax = kmax;
     sm.vmax = value_of(kmax);
-    sm.temp = greedy ? 1.f : t;
+    sm.temp = greedy ? 1.f : fminf(t, FLT_MAX);  // (infinite: every weight is 1, as with the largest)
 
     // ---- the window: unmasked values of the kWindow up to kmax, no lower than the cuts look
     uint32_t bottom = kmax >= kWindow + kMaskedKey ? kmax - kWindow + 1 : kMaskedKey + 1;
@@ -748,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.vmax = value_of(kmax);
     const float t = temperature != nullptr ? temperature[row] : 1.f;
     const bool greedy = t <= 0.f;
-    sm.temp = greedy ? 1.f : t;
+    sm.temp = greedy ? 1.f : fminf(t, FLT_MAX);  // (infinite: every weight is 1, as with the largest)
 
     // ---- the cluster's counts of this CTA's bins, a quarter of a bin a thread; their count and mass go to
     // rank 0. Values whose weight is 0 are left out (every cut among them leaves the masses as they are).
