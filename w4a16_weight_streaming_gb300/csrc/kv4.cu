@@ -5,8 +5,14 @@
 //   - the sum of squares of a head's norm is 8 additions in a lane and log2(D / 8) exchanges,
 //   - the rotation's partner element is in the same lane (adjacent pairs) or one exchange away (halves),
 //   - the minimum and maximum of the 64 elements that share a scale are 3 exchanges among 8 lanes,
-// and one pass takes a row from the product's output to rotated queries and stored codes. Bound by
-// latency for decode rows (a load, three short exchange chains, a store), by memory for prompt chunks.
+// and one pass takes a row from the product's output to rotated queries and stored codes. A decode row is
+// bound by latency (a load, three short exchange chains, a store), a prompt chunk by instruction issue: the
+// exact arithmetic below is some 200 instructions a warp for 256 elements. Rows are the grid's first
+// dimension, so no thread divides (1024 rows 15.2 us with one index over rows and heads, 13.0 so).
+//
+// Measured with the reading kernel behind it, on one GB300, the data in L2: 1 row of 20 + 2 x 4 heads of 256
+// 3.7 us the pair, 64 rows of 40 + 2 x 8 heads of 128 4.2 us, 1024 rows of 20 + 2 x 4 heads of 256 13.0 us (32
+// MB in and out: 2.5 TB/s, 0.36 of the copy bandwidth).
 //
 // The codes are decisions, so everything before them is defined to the bit, in binary32 without fused
 // multiply-adds: squares added 8 neighbours in turn, then sums of neighbours in pairs;
@@ -67,11 +73,10 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a, uns
     const int l = lane % L;
     const int d0 = l * 8;
     const int per_row = a.heads + 2 * a.cache.kv_heads;
-    const int64_t items = static_cast<int64_t>(a.M) * per_row;
-    const int64_t item = blockIdx.x * static_cast<int64_t>(256 / L) + threadIdx.x / L;
-    const bool live = item < items;  // every lane takes part in the exchanges
-    const int64_t m = live ? item / per_row : 0;
-    const int head = live ? static_cast<int>(item - m * per_row) : 0;
+    const int64_t m = blockIdx.x;
+    const int slot_head = static_cast<int>((blockIdx.y * blockDim.x + threadIdx.x) / L);
+    const bool live = slot_head < per_row;  // every lane takes part in the exchanges
+    const int head = live ? slot_head : 0;
     const bool is_q = head < a.heads;
     const bool is_k = !is_q && head < a.heads + a.cache.kv_heads;
 
@@ -80,11 +85,16 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a, uns
                               static_cast<int64_t>(a.M - 1) * a.qkv_stride + static_cast<int64_t>(per_row) * D,
                           status))
         raw = *reinterpret_cast<const uint4*>(a.qkv + m * a.qkv_stride + static_cast<int64_t>(head) * D + d0);
+    // what the row and its position bring, asked for with the row itself
+    const uint16_t* norm = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
+    uint4 norm_raw = make_uint4(0, 0, 0, 0);
+    if (norm != nullptr) norm_raw = *reinterpret_cast<const uint4*>(norm + d0);
+    const int position = a.rope != nullptr ? a.positions[m] : 0;
+    const int64_t slot = is_q ? -1 : a.slots[m];
     float x[8];
     unpack8(raw, x);
 
     bool ok = live;
-    const uint16_t* norm = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
     // A warp's lanes may belong to heads of different kinds (D < 256): all take part in the exchanges.
     float s = __fmul_rn(x[0], x[0]);
 #pragma unroll
@@ -92,15 +102,16 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a, uns
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
     if (norm != nullptr) {
-        const float inv = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(s, static_cast<float>(D)), a.eps)));
+        // (s / D and 1 / sqrt, rounded as the divisions are)
+        const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(s, 1.f / D), a.eps)));
         float w[8];
-        unpack8(*reinterpret_cast<const uint4*>(norm + d0), w);
+        unpack8(norm_raw, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], inv), w[i]);
     }
     int pos = 0;
     if (a.rope != nullptr && live) {
-        pos = a.positions[m];
+        pos = position;
         if (pos < 0 || pos >= a.rope_positions) {  // no such row of the table: nothing is stored
             if (l == 0) record_error(status, kErrBounds);
             ok = false;
@@ -186,7 +197,6 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a, uns
     const uint32_t other = __shfl_xor_sync(0xffffffffu, seq, 1);
     if (is_q || !ok) return;
 
-    const int64_t slot = a.slots[m];
     if (slot < 0) return;  // a padding row: nothing is stored
     if (slot >= a.cache.slots()) {
         if (l == 0) record_error(status, kErrBounds);
@@ -230,10 +240,9 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(const Kv4View cache, cons
     constexpr int L = D / 8;
     using T = Kv4<D>;
     const int d0 = static_cast<int>(threadIdx.x % L) * 8;
-    const int64_t item = blockIdx.x * static_cast<int64_t>(256 / L) + threadIdx.x / L;
-    if (item >= 2LL * n * cache.kv_heads) return;
-    const int64_t row = item / (2 * cache.kv_heads);
-    const int r = static_cast<int>(item - row * (2 * cache.kv_heads));
+    const int64_t row = blockIdx.x;
+    const int r = static_cast<int>((blockIdx.y * blockDim.x + threadIdx.x) / L);
+    if (r >= 2 * cache.kv_heads) return;
     const bool is_k = r < cache.kv_heads;
     const int head = is_k ? r : r - cache.kv_heads;
     const int64_t slot = slots[row];
@@ -267,11 +276,12 @@ __global__ void __launch_bounds__(256) kv4_load_kernel(const Kv4View cache, cons
 }
 
 template <typename F, typename... A>
-cudaError_t launch_pdl(F* f, int64_t blocks, int threads, size_t smem, cudaStream_t s, A... args) {
+cudaError_t launch_rows(F* f, int rows, int heads, int lanes, cudaStream_t s, A... args) {
+    // a grid row of CTAs a token, its heads dealt evenly to as few CTAs of up to 256 threads as hold them
+    const int parts = (heads * lanes + 255) / 256, threads = ((heads + parts - 1) / parts * lanes + 31) / 32 * 32;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(rows), static_cast<unsigned>(parts), 1);
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -310,26 +320,21 @@ cudaError_t launch_kv4_append(const Kv4AppendParams& p, const Kv4Cache& c, cudaS
     a.eps = p.eps;
     a.M = p.M;
     a.heads = p.heads;
-    const int64_t items = static_cast<int64_t>(p.M) * (p.heads + 2 * c.kv_heads);
-    const int64_t per = 256 / (c.head_dim / 8);
-    const int64_t blocks = (items + per - 1) / per;
+    const int heads = p.heads + 2 * c.kv_heads;
     switch (c.head_dim) {
-        case 64: return launch_pdl(kv4_append_kernel<64>, blocks, 256, 0, s, a, status);
-        case 128: return launch_pdl(kv4_append_kernel<128>, blocks, 256, 0, s, a, status);
-        default: return launch_pdl(kv4_append_kernel<256>, blocks, 256, 0, s, a, status);
+        case 64: return launch_rows(kv4_append_kernel<64>, p.M, heads, 8, s, a, status);
+        case 128: return launch_rows(kv4_append_kernel<128>, p.M, heads, 16, s, a, status);
+        default: return launch_rows(kv4_append_kernel<256>, p.M, heads, 32, s, a, status);
     }
 }
 
 cudaError_t launch_kv4_load(const Kv4Cache& c, const int32_t* slots, uint16_t* k, uint16_t* v, int n, cudaStream_t s,
                             unsigned* status) {
-    const int64_t items = 2LL * n * c.kv_heads;
-    const int64_t per = 256 / (c.head_dim / 8);
-    const int64_t blocks = (items + per - 1) / per;
     const Kv4View w = view(c);
     switch (c.head_dim) {
-        case 64: return launch_pdl(kv4_load_kernel<64>, blocks, 256, 0, s, w, slots, k, v, n, status);
-        case 128: return launch_pdl(kv4_load_kernel<128>, blocks, 256, 0, s, w, slots, k, v, n, status);
-        default: return launch_pdl(kv4_load_kernel<256>, blocks, 256, 0, s, w, slots, k, v, n, status);
+        case 64: return launch_rows(kv4_load_kernel<64>, n, 2 * c.kv_heads, 8, s, w, slots, k, v, n, status);
+        case 128: return launch_rows(kv4_load_kernel<128>, n, 2 * c.kv_heads, 16, s, w, slots, k, v, n, status);
+        default: return launch_rows(kv4_load_kernel<256>, n, 2 * c.kv_heads, 32, s, w, slots, k, v, n, status);
     }
 }
 
