@@ -80,15 +80,13 @@ __device__ __forceinline__ bool warp_suspend(uint32_t bar, uint32_t parity, vola
     const uint64_t t0 = global_timer_ns();
     for (uint32_t spin = 1;; ++spin) {
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if ((spin & 31u) == 0u) {
-            bool over = *abort_flag != 0;
-            if (!over && global_timer_ns() - t0 > timeout_ns) {
-                record_error(status, kErrTimeout);
-                *abort_flag = 1;
-                over = true;
-            }
-            if (__any_sync(0xffffffffu, over)) return false;
+        bool over = *abort_flag != 0;
+        if (!over && (spin & 31u) == 0u && global_timer_ns() - t0 > timeout_ns) {
+            record_error(status, kErrTimeout);
+            *abort_flag = 1;
+            over = true;
         }
+        if (__any_sync(0xffffffffu, over)) return false;
     }
 }
 

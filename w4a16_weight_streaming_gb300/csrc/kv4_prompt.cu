@@ -48,11 +48,13 @@ struct Prompt {
     static constexpr int kRawStages = D == 256 ? 3 : 4;
     static constexpr int kBuf = kTok * D * 2;  // one K' or V' buffer
     static constexpr int kOffV = 2 * kBuf;
-    static constexpr int kOffRaw = 4 * kBuf;
+    static constexpr int kFactors = kKv4MaxPromptCtas * kRows * 4;  // what each part is scaled by, over K' and V'
+    static constexpr int kOffRaw = 4 * kBuf > kFactors ? 4 * kBuf : kFactors;
     static constexpr int kOffBars = kOffRaw + kRawStages * kRaw;
-    static constexpr int kBars = 2 * kRawStages + 2 * 5 + 1;
+    static constexpr int kBars = 2 * kRawStages + 2 * 5 + 3;
     static constexpr int kOffMisc = kOffBars + kBars * 8;
-    static constexpr int kSmem = kOffMisc + 256 + 4 * kRows * 4 + 1024;  // + alignment
+    static constexpr int kJoin = (2 * (kThreads / kRows) + 1) * kRows * 4;
+    static constexpr int kSmem = kOffMisc + 256 + kJoin + 1024;  // + alignment
     static constexpr uint32_t kColS = D, kColQ = D + 2 * kTok;
     static constexpr uint32_t kCols = D == 64 ? 256 : 512;
     static constexpr int kPart = kRows * (D + 2);  // floats of one workspace part: m, l, then [D / 4][128] float4
@@ -171,7 +173,7 @@ __device__ __forceinline__ void lds_params(uint32_t addr, uint32_t (&p)[G]) {
 
 struct PromptSeq {
     int q0, q_len, n, grp, row_tiles;
-    bool bad;
+    bool bad;  // (24 bytes)
     // tokens that query row r (within the sequence) sees
     __device__ __forceinline__ int seen(int r, int causal) const {
         return causal ? max(0, n - (q_len - 1 - r / grp)) : n;
@@ -226,6 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t* s_plan = reinterpret_cast<int64_t*>(s_misc + 4);      // run begin, end, length; first sequence's place
     uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_misc + 12);  // [kNotes]: valid tokens of each quarter, a byte each
     float* s_part = reinterpret_cast<float*>(smem + C::kOffMisc + 256);  // [4][128]: what the quarters of a row exchange
+    float* s_join = s_part;  // [13][128]: what the threads that add a unit's parts exchange
+    PromptSeq* s_seq = reinterpret_cast<PromptSeq*>(s_misc + 48);  // the sequence that the run begins in
     volatile int* s_left = s_misc + 32;  // [16]: softmax warps whose wait ran out
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t bars = base + C::kOffBars;
@@ -237,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto p_full = [&](int s) { return bars + 8 * (2 * R + 6 + s); };
     auto pv_done = [&](int s) { return bars + 8 * (2 * R + 8 + s); };  // O updated, V' and S/P free
     const uint32_t q_full = bars + 8 * (2 * R + 10);
+    auto drained = [&](int i) { return bars + 8 * (2 * R + 11 + i); };  // the issuers' instructions, after a wait ran out
     auto wait = [&](uint32_t bar, uint32_t parity) { return warp_suspend(bar, parity, s_abort, timeout_ns, status); };
 
     if (warp == kProducer) {
@@ -253,6 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(pv_done(i), 1);
             }
             mbar_init(q_full, 16);
+            mbar_init(drained(0), 1);
+            mbar_init(drained(1), 1);
             *s_abort = 0;
             fence_barrier_init();
         }
@@ -264,14 +271,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---- this CTA's run of the work list
     if (warp == 0) {
-        int64_t total = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            int64_t c = 0;
+        int64_t total = 0, cost = 0;  // cost: of sequence b0 + lane, kept for the search where there are no more than 32
+        PromptSeq seq = {};
+        auto read = [&](int b0) {
+            cost = 0;
             if (b0 + lane < p.B) {
-                const PromptSeq s = seq_of(p, cache, b0 + lane);
-                c = s.before(s.row_tiles, p.causal) * cache.kv_heads;
-                if (s.bad && blockIdx.x == 0) record_error(status, kErrBounds);
+                seq = seq_of(p, cache, b0 + lane);
+                cost = seq.before(seq.row_tiles, p.causal) * cache.kv_heads;
             }
+        };
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            read(b0);
+            if (b0 + lane < p.B && seq.bad && blockIdx.x == 0) record_error(status, kErrBounds);
+            int64_t c = cost;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
             total += c;
@@ -282,12 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t at = 0;
         int first = p.B;
         for (int b0 = 0; b0 < p.B && w0 < w1; b0 += 32) {
-            int64_t c = 0;
-            if (b0 + lane < p.B) {
-                const PromptSeq s = seq_of(p, cache, b0 + lane);
-                c = s.before(s.row_tiles, p.causal) * cache.kv_heads;
-            }
-            int64_t upto = c;
+            if (p.B > 32) read(b0);
+            int64_t upto = cost;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
@@ -297,15 +305,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (hit != 0) {
                 const int l = __ffs(hit) - 1;
                 first = b0 + l;
-                at += __shfl_sync(0xffffffffu, upto - c, l);
+                at += __shfl_sync(0xffffffffu, upto - cost, l);
                 break;
             }
             at += __shfl_sync(0xffffffffu, upto, 31);
         }
-        if (lane == 0) {
+        if (lane == (first < p.B ? first & 31 : 0)) {
             int kvh = 0, rt = 0;
             if (first < p.B) {  // the unit that the run begins in
-                const PromptSeq s = seq_of(p, cache, first);
+                const PromptSeq& s = seq;
                 const int64_t head = s.before(s.row_tiles, p.causal);
                 kvh = static_cast<int>((w0 - at) / head);
                 at += kvh * head;
@@ -324,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             s_first[0] = first;
             s_first[8 + kNotes + 1] = kvh;
             s_first[8 + kNotes + 2] = rt;
+            *s_seq = seq;
         }
     }
     tc_fence_before();
@@ -336,8 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int b = s_first[0], kvh = s_first[8 + kNotes + 1], rt = s_first[8 + kNotes + 2];
     uint32_t done = 0;       // tiles of earlier segments
     uint32_t segment = 0;
+    uint32_t issued = 0;     // tiles that the fetching warp has asked for
     PromptSeq sq = {};
-    if (b < p.B) sq = seq_of(p, cache, b);
+    if (b < p.B) sq = *s_seq;
 
     while (at < w1 && b < p.B) {
         if (rt >= sq.row_tiles) {
@@ -645,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (mine)
                     bulk_g2s(base + C::kOffRaw + st * C::kRaw + (lane % kSub) * T::kTileBytes, cache.pages + from, T::kTileBytes,
                              raw_full(st), policy);
+                issued = it + 1;
             }
         } else if (warp == kIssueS) {
             // ================= S = Q . K'^T
@@ -701,69 +712,105 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncthreads();
             if (*s_last && !*s_abort) {
                 __threadfence();
-                // A thread has a row and 16 of its elements at a time, from two parts in one round of loads.
-                const int n = cta1 - cta0 + 1, r = tid & (kRows - 1);
+                // What each part's rows are scaled by: six groups of threads, every sixth part each. (K' and V'
+                // are not in use: all their products are done.)
                 constexpr int kGroups = kThreads / kRows;
-                if (tid < kGroups * kRows && r < rows && in_bounds(cta1 < kKv4MaxPromptCtas, status)) {
-                    float top = -INFINITY, total = 0.f;
-                    for (int c = 0; c < n; ++c) top = fmaxf(top, __ldcg(part_of(cta0 + c) + r));
-                    for (int c = 0; c < n; ++c) {
-                        const float m = __ldcg(part_of(cta0 + c) + r);
-                        total += m == -INFINITY ? 0.f : __ldcg(part_of(cta0 + c) + kRows + r) * ex2(m - top);
+                const int n = min(cta1, kKv4MaxPromptCtas - 1) - cta0 + 1;
+                float* s_f = reinterpret_cast<float*>(smem);  // [n][128]
+                // 8 elements of a row a thread, from four parts in one round of loads (the first one's before
+                // the factors are known)
+                const int items = rows * (D / 8);
+                float4 a[4][2];
+                auto load = [&](int x, int c) {
+                    const int c8 = x / rows, r = x - c8 * rows;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const float4* from = reinterpret_cast<const float4*>(part_of(cta0 + min(c + h, n - 1)) + 2 * kRows) + r;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            a[h][k] = x < items && c + h < n ? __ldcg(from + (2 * c8 + k) * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                };
+                load(tid, 0);
+                {
+                    const int grp = tid / kRows, r = min(tid & (kRows - 1), rows - 1);
+                    float top = -INFINITY, total = 0.f, l = 0.f;
+                    if (grp < kGroups) {
+                        if (grp < n) l = __ldcg(part_of(cta0 + grp) + kRows + r);
+                        for (int c = grp; c < n; c += kGroups) {
+                            const float m = __ldcg(part_of(cta0 + c) + r);
+                            s_f[c * kRows + (tid & (kRows - 1))] = m;
+                            top = fmaxf(top, m);
+                        }
+                        s_join[tid] = top;
+                    }
+                    __syncthreads();
+                    if (grp < kGroups) {
+                        for (int i = 0; i < kGroups; ++i) top = fmaxf(top, s_join[i * kRows + (tid & (kRows - 1))]);
+                        for (int c = grp; c < n; c += kGroups) {
+                            const float m = s_f[c * kRows + (tid & (kRows - 1))];
+                            const float f = m == -INFINITY ? 0.f : ex2(m - top);
+                            s_f[c * kRows + (tid & (kRows - 1))] = f;
+                            total += (c == grp ? l : __ldcg(part_of(cta0 + c) + kRows + r)) * f;
+                        }
+                        s_join[(kGroups + grp) * kRows + (tid & (kRows - 1))] = total;
+                    }
+                    __syncthreads();
+                    if (tid < kRows) {
+                        total = 0.f;
+                        for (int i = 0; i < kGroups; ++i) total += s_join[(kGroups + i) * kRows + tid];
+                        s_join[2 * kGroups * kRows + tid] = total > 0.f ? 1.f / total : 0.f;
+                        if (p.lse != nullptr && tid < rows) {
+                            const int in_seq = row0 + tid, pos = in_seq / sq.grp, hd = in_seq - pos * sq.grp;
+                            p.lse[static_cast<int64_t>(sq.q0 + pos) * p.heads + kvh * sq.grp + hd] =
+                                total > 0.f ? 0.6931471805599453f * (top + log2f(total)) : -INFINITY;
+                        }
+                    }
+                    __syncthreads();
+                }
+                for (int x = tid; x < items; x += kThreads) {
+                    const int c8 = x / rows, r = x - c8 * rows;
+                    float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+                    for (int c = 0; c < n; c += 4) {
+                        if (x != tid || c != 0) load(x, c);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const float f = c + h < n ? s_f[(c + h) * kRows + r] : 0.f;
+                            if (f == 0.f) continue;  // (a part that saw nothing may hold anything)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                v[k].x = fmaf(a[h][k].x, f, v[k].x);
+                                v[k].y = fmaf(a[h][k].y, f, v[k].y);
+                                v[k].z = fmaf(a[h][k].z, f, v[k].z);
+                                v[k].w = fmaf(a[h][k].w, f, v[k].w);
+                            }
+                        }
                     }
                     const int in_seq = row0 + r, pos = in_seq / sq.grp, hd = in_seq - pos * sq.grp;
                     const int64_t at_out = static_cast<int64_t>(sq.q0 + pos) * p.heads + kvh * sq.grp + hd;
-                    const float inv = total > 0.f ? 1.f / total : 0.f;
-                    for (int c4 = tid / kRows * 4; c4 < D / 4; c4 += kGroups * 4) {
-                        float4 v[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int c = 0; c < n; c += 2) {
-                            float f[2];
-                            float4 a[2][4];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float* from = part_of(cta0 + min(c + h, n - 1));
-                                const float m = __ldcg(from + r);
-                                f[h] = m == -INFINITY || c + h >= n ? 0.f : ex2(m - top);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    a[h][k] = __ldcg(reinterpret_cast<const float4*>(from + 2 * kRows) + (c4 + k) * kRows + r);
-                            }
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (f[h] == 0.f) continue;
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    v[k].x = fmaf(a[h][k].x, f[h], v[k].x);
-                                    v[k].y = fmaf(a[h][k].y, f[h], v[k].y);
-                                    v[k].z = fmaf(a[h][k].z, f[h], v[k].z);
-                                    v[k].w = fmaf(a[h][k].w, f[h], v[k].w);
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; k += 2) {
-                            const __half2 h0 = __floats2half2_rn(v[k].x * inv, v[k].y * inv), h1 = __floats2half2_rn(v[k].z * inv, v[k].w * inv);
-                            const __half2 h2 = __floats2half2_rn(v[k + 1].x * inv, v[k + 1].y * inv);
-                            const __half2 h3 = __floats2half2_rn(v[k + 1].z * inv, v[k + 1].w * inv);
-                            *reinterpret_cast<uint4*>(p.out + at_out * D + 4 * (c4 + k)) =
-                                make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
-                                           *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
-                        }
-                    }
-                    if (tid < kRows && p.lse != nullptr)
-                        p.lse[at_out] = total > 0.f ? 0.6931471805599453f * (top + log2f(total)) : -INFINITY;
+                    const float inv = s_join[2 * kGroups * kRows + r];
+                    const __half2 h0 = __floats2half2_rn(v[0].x * inv, v[0].y * inv), h1 = __floats2half2_rn(v[0].z * inv, v[0].w * inv);
+                    const __half2 h2 = __floats2half2_rn(v[1].x * inv, v[1].y * inv), h3 = __floats2half2_rn(v[1].z * inv, v[1].w * inv);
+                    *reinterpret_cast<uint4*>(p.out + at_out * D + 8 * c8) =
+                        make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
+                                   *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
                 }
             }
         }
         __syncthreads();  // Q, O and the barriers' phases belong to the next segment from here on
         if (*s_abort) break;
     }
-    if (*s_abort) {  // copies still under way land before the memory is given back (bounded)
-        for (int i = 0; i < R; ++i)
-            for (int n = 0; n < 65536 && !mbar_test_wait(raw_full(i), 0) && !mbar_test_wait(raw_full(i), 1); ++n) {
+    if (*s_abort) {  // what is under way ends before the memory is given back (bounded)
+        if (warp == kProducer) {
+            for (uint32_t it = issued < R ? 0 : issued - R; it < issued; ++it)
+                for (int n = 0; n < 65536 && !mbar_test_wait(raw_full(it % R), (it / R) & 1); ++n) {
+                }
+        } else if (warp >= kIssueS) {
+            const uint32_t bar = drained(warp - kIssueS);
+            if (elect_one()) umma_commit(bar);
+            for (int n = 0; n < 65536 && !mbar_test_wait(bar, 0); ++n) {
             }
+        }
     }
     tc_fence_before();
     __syncthreads();
