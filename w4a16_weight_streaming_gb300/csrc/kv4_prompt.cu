@@ -21,7 +21,9 @@
 // the odd tiles: 186).
 //
 // Work is a list of (unit, tile); every CTA takes an equal run. Units that a run's end cuts leave parts
-// (maximum, sum, unnormalised rows) in the workspace; the CTA that arrives last adds them in CTA order.
+// (maximum, sum, unnormalised rows) in the workspace; the CTA that arrives last adds them, in CTA order, to
+// what it still has in TMEM. (Added from memory, its own part among them: 169 us for the chunk above, 163 so.
+// An SM reads parts at 45 to 60 GB/s, however many loads are under way.)
 #include <algorithm>
 
 #include "common.cuh"
@@ -34,12 +36,15 @@ namespace {
 constexpr int kRows = 128;     // query rows of a unit
 constexpr int kTok = 64;       // tokens of a tile
 constexpr int kSub = kTok / kKv4Tile;
-constexpr int kUnitCost = 6;   // what the start and end of a unit cost, in tiles
+// What the start and end of a unit cost, in tiles (prompt chunk of 1024 x 20 heads behind 8192 tokens: 164.9 us
+// with 6, 162.5 with 8, 163.3 with 10)
+constexpr int kUnitCost = 8;
 constexpr int kMinRun = 12;    // tiles; fewer make more parts than they save
 constexpr int kDequant = 16;   // first warp of each role (softmax: 0)
 constexpr int kProducer = 24, kIssueS = 25;
 constexpr int kWarps = 27;     // (26: PV)
 constexpr int kThreads = kWarps * 32;
+constexpr int kJoinInPlace = 8;  // most parts of a unit that its last CTA adds to its own in TMEM
 constexpr int kNotes = 16;     // tiles whose page validity is kept
 
 template <int D>
@@ -48,12 +53,14 @@ struct Prompt {
     static constexpr int kRawStages = D == 256 ? 3 : 4;
     static constexpr int kBuf = kTok * D * 2;  // one K' or V' buffer
     static constexpr int kOffV = 2 * kBuf;
-    static constexpr int kFactors = kKv4MaxPromptCtas * kRows * 4;  // what each part is scaled by, over K' and V'
-    static constexpr int kOffRaw = 4 * kBuf > kFactors ? 4 * kBuf : kFactors;
+    // (where the tiles are, a unit's parts are added: four slots or more of 16 elements of a part for every
+    // softmax thread, or what up to kKv4MaxPromptCtas parts are scaled by, under the raw tiles)
+    static constexpr int kOffRaw = 4 * 64 * kDequant * 32;
+    static_assert(4 * kBuf <= kOffRaw && kKv4MaxPromptCtas * kRows * 4 <= kOffRaw, "");
     static constexpr int kOffBars = kOffRaw + kRawStages * kRaw;
     static constexpr int kBars = 2 * kRawStages + 2 * 5 + 3;
     static constexpr int kOffMisc = kOffBars + kBars * 8;
-    static constexpr int kJoin = (2 * (kThreads / kRows) + 1) * kRows * 4;
+    static constexpr int kJoin = (kJoinInPlace + 1) * kRows * 4;
     static constexpr int kSmem = kOffMisc + 256 + kJoin + 1024;  // + alignment
     static constexpr uint32_t kColS = D, kColQ = D + 2 * kTok;
     static constexpr uint32_t kCols = D == 64 ? 256 : 512;
@@ -154,6 +161,15 @@ __device__ __forceinline__ void codes(uint32_t w, uint32_t (&out)[4]) {
     out[3] = hfma2(and_or(hi, 0x00F000F0u, kMagic), kSixteenth, kNeg64);
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_acquire(const unsigned* p) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 template <int G>
 __device__ __forceinline__ void lds_params(uint32_t addr, uint32_t (&p)[G]) {
     if constexpr (G == 4) {
@@ -225,10 +241,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* s_last = s_misc + 1;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_misc + 2);
     int* s_first = s_misc + 3;
+    int* s_joined = s_misc + 30;
     int64_t* s_plan = reinterpret_cast<int64_t*>(s_misc + 4);      // run begin, end, length; first sequence's place
     uint32_t* s_valid = reinterpret_cast<uint32_t*>(s_misc + 12);  // [kNotes]: valid tokens of each quarter, a byte each
     float* s_part = reinterpret_cast<float*>(smem + C::kOffMisc + 256);  // [4][128]: what the quarters of a row exchange
-    float* s_join = s_part;  // [13][128]: what the threads that add a unit's parts exchange
+    float* s_join = s_part;  // [kJoinInPlace + 1][128]: what the threads that add a unit's parts exchange
     PromptSeq* s_seq = reinterpret_cast<PromptSeq*>(s_misc + 48);  // the sequence that the run begins in
     volatile int* s_left = s_misc + 32;  // [16]: softmax warps whose wait ran out
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -348,6 +365,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t issued = 0;     // tiles that the fetching warp has asked for
     PromptSeq sq = {};
     if (b < p.B) sq = *s_seq;
+
+    // CTA c's part of the unit that begins in CTA cta0
+    auto part_of = [&](int cta0, int c) {
+        return reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + 4096) + static_cast<int64_t>(2 * c + (c == cta0 ? 1 : 0)) * C::kPart;
+    };
 
     while (at < w1 && b < p.B) {
         if (rt >= sq.row_tiles) {
@@ -482,7 +504,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full(buf));
             }
-            // ---- the unit's rows, or this CTA's part of them: a quarter of the elements each
+            // ---- the unit's rows, or this CTA's part of them: a quarter of the elements each. The last CTA adds
+            // the others' parts to its own in TMEM, which is not written where they are all there by now.
+            const int n = cta1 - cta0 + 1, own = static_cast<int>(blockIdx.x) - cta0;
+            bool join = false;
+            if (!whole) {
+                if (tid == 0) {
+                    unsigned* counter = static_cast<unsigned*>(p.workspace) + cta0;
+                    const bool there = n <= kJoinInPlace && ld_acquire(counter) == static_cast<unsigned>(n - 1);
+                    if (there) *counter = 0;
+                    *s_joined = there;
+                    *s_last = 0;
+                }
+                named_sync(5, kDequant * 32);
+                join = *s_joined;
+            }
             if (ok) {
                 const uint32_t end = done + nt - 1;
                 ok = wait(pv_done(end & 1), (end >> 1) & 1);
@@ -491,9 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s_part[part * kRows + r] = l;
                 named_sync(1 + quad, 128);
                 l = (s_part[r] + s_part[kRows + r]) + (s_part[2 * kRows + r] + s_part[3 * kRows + r]);
-                named_sync(1 + quad, 128);
+                ok = !any_of_128(1 + quad, !ok);  // (the four leave together)
             }
-            if (ok && !idle) {
+            if (ok && !idle && !join) {
                 tc_fence_after();
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 float* dst = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + 4096) +
@@ -530,6 +566,112 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __stcg(dst + kRows + r, l);
                     } else if (p.lse != nullptr) {
                         p.lse[q_row * p.heads + head] = l > 0.f ? 0.6931471805599453f * (m + log2f(l)) : -INFINITY;
+                    }
+                }
+                tc_fence_before();
+            }
+            if (!whole && !join) {  // this CTA's part is written: whether it was the last
+                __threadfence();
+                named_sync(5, kDequant * 32);
+                if (tid == 0) {
+                    unsigned* counter = static_cast<unsigned*>(p.workspace) + cta0;
+                    *s_last = atomicAdd(counter, 1u) == static_cast<unsigned>(n - 1);
+                    if (*s_last) *counter = 0;
+                }
+                named_sync(5, kDequant * 32);
+                join = *s_last && n <= kJoinInPlace;
+            }
+            if (join && ok && !idle) {
+                __threadfence();
+                // The others' elements come through four slots of shared memory (K' and V' are not in use), 16
+                // elements of one part a thread in each, every thread its own; parts in CTA order.
+                constexpr int kChunks = D / 64, kSlot = 64 * kDequant * 32;
+                const int rr = min(r, rows - 1);
+                const uint32_t slots = base + tid * 16;
+                const float4* rest = reinterpret_cast<const float4*>(part_of(cta0, cta0) + 2 * kRows) + part * (D / 16) * kRows + rr;
+                int to_come = r < rows ? kChunks * (n - 1) : 0, next = own == 0, at_chunk = 0;
+                uint32_t to_slot = slots;
+                auto fetch = [&]() {  // part `next` of the next chunk
+                    if (to_come > 0) {
+                        // (the parts of the unit's other CTAs: every second one from the first's neighbour on)
+                        const float4* from = rest + (next == 0 ? 0 : (2 * next - 1) * (C::kPart / 4)) + at_chunk;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) cp_async16(to_slot + k * (kSlot / 4), from + k * kRows);
+                        --to_come;
+                        to_slot = to_slot == slots + 3 * kSlot ? slots : to_slot + kSlot;
+                        next += next + 1 == own ? 2 : 1;
+                        if (next >= n) {
+                            next = own == 0;
+                            at_chunk += 4 * kRows;
+                        }
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                };
+                for (int j = 0; j < 4; ++j) fetch();
+                if (part == 0) {  // the row's factors and sum
+                    float mm[kJoinInPlace], ll[kJoinInPlace], top = -INFINITY, total = 0.f;
+#pragma unroll
+                    for (int c = 0; c < kJoinInPlace; ++c) {
+                        const float* from = part_of(cta0, cta0 + min(c, n - 1)) + rr;
+                        mm[c] = c == own ? m : c < n ? __ldcg(from) : -INFINITY;
+                        ll[c] = c == own ? l : c < n ? __ldcg(from + kRows) : 0.f;
+                        top = fmaxf(top, mm[c]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < kJoinInPlace; ++c) {
+                        const float f = mm[c] == -INFINITY ? 0.f : ex2(mm[c] - top);
+                        total = fmaf(ll[c], f, total);
+                        if (c < n) s_join[c * kRows + r] = f;
+                    }
+                    s_join[kJoinInPlace * kRows + r] = total > 0.f ? 1.f / total : 0.f;
+                    if (r < rows && p.lse != nullptr)
+                        p.lse[q_row * p.heads + head] = total > 0.f ? 0.6931471805599453f * (top + log2f(total)) : -INFINITY;
+                }
+                named_sync(1 + quad, 128);
+                tc_fence_after();
+                const float inv = s_join[kJoinInPlace * kRows + r];
+                uint16_t* out = p.out + (q_row * p.heads + head) * D + part * (D / 4);
+                uint32_t slot = slots;
+#pragma unroll 1
+                for (int chunk = 0; chunk < kChunks; ++chunk) {
+                    uint32_t v[16];
+                    float sum[16];
+                    tmem_ld16(lanes + part * (D / 4) + 16 * chunk, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+                    for (int c = 0; c < n; ++c) {
+                        const float f = s_join[c * kRows + r];
+                        if (c != own) {
+                            asm volatile("cp.async.wait_group 3;" ::: "memory");
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint4 a = lds128(slot + k * (kSlot / 4));
+                                if (f != 0.f) {  // (a part that saw nothing may hold anything)
+                                    sum[4 * k] = fmaf(__uint_as_float(a.x), f, sum[4 * k]);
+                                    sum[4 * k + 1] = fmaf(__uint_as_float(a.y), f, sum[4 * k + 1]);
+                                    sum[4 * k + 2] = fmaf(__uint_as_float(a.z), f, sum[4 * k + 2]);
+                                    sum[4 * k + 3] = fmaf(__uint_as_float(a.w), f, sum[4 * k + 3]);
+                                }
+                            }
+                            slot = slot == slots + 3 * kSlot ? slots : slot + kSlot;
+                            fetch();
+                        } else if (f != 0.f) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) sum[e] = fmaf(__uint_as_float(v[e]), f, sum[e]);
+                        }
+                    }
+                    if (r < rows && in_bounds(q_row < p.M, status)) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __half2 x = __floats2half2_rn(sum[8 * k + 2 * e] * inv, sum[8 * k + 2 * e + 1] * inv);
+                                h[e] = *reinterpret_cast<const uint32_t*>(&x);
+                            }
+                            *reinterpret_cast<uint4*>(out + 16 * chunk + 8 * k) = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
                     }
                 }
                 tc_fence_before();
@@ -697,18 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         done += nt;
         ++segment;
 
-        if (!whole) {
-            // ---- the last CTA of the unit to arrive adds its parts in CTA order
-            float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + 4096);
-            auto part_of = [&](int c) { return parts + static_cast<int64_t>(2 * c + (c == cta0 ? 1 : 0)) * C::kPart; };
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                unsigned* counter = static_cast<unsigned*>(p.workspace) + cta0;
-                const unsigned before = atomicAdd(counter, 1u);
-                *s_last = before == static_cast<unsigned>(cta1 - cta0);
-                if (*s_last) *counter = 0;
-            }
+        if (cta1 - cta0 >= kJoinInPlace) {
+            // ---- more parts than that: all threads of the last CTA add them from memory, in the same order
             __syncthreads();
             if (*s_last && !*s_abort) {
                 __threadfence();
@@ -725,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int c8 = x / rows, r = x - c8 * rows;
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
-                        const float4* from = reinterpret_cast<const float4*>(part_of(cta0 + min(c + h, n - 1)) + 2 * kRows) + r;
+                        const float4* from = reinterpret_cast<const float4*>(part_of(cta0, cta0 + min(c + h, n - 1)) + 2 * kRows) + r;
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
                             a[h][k] = x < items && c + h < n ? __ldcg(from + (2 * c8 + k) * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -734,11 +866,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load(tid, 0);
                 {
                     const int grp = tid / kRows, r = min(tid & (kRows - 1), rows - 1);
-                    float top = -INFINITY, total = 0.f, l = 0.f;
+                    float top = -INFINITY;
                     if (grp < kGroups) {
-                        if (grp < n) l = __ldcg(part_of(cta0 + grp) + kRows + r);
                         for (int c = grp; c < n; c += kGroups) {
-                            const float m = __ldcg(part_of(cta0 + c) + r);
+                            const float m = __ldcg(part_of(cta0, cta0 + c) + r);
                             s_f[c * kRows + (tid & (kRows - 1))] = m;
                             top = fmaxf(top, m);
                         }
@@ -751,15 +882,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float m = s_f[c * kRows + (tid & (kRows - 1))];
                             const float f = m == -INFINITY ? 0.f : ex2(m - top);
                             s_f[c * kRows + (tid & (kRows - 1))] = f;
-                            total += (c == grp ? l : __ldcg(part_of(cta0 + c) + kRows + r)) * f;
                         }
-                        s_join[(kGroups + grp) * kRows + (tid & (kRows - 1))] = total;
                     }
                     __syncthreads();
                     if (tid < kRows) {
-                        total = 0.f;
-                        for (int i = 0; i < kGroups; ++i) total += s_join[(kGroups + i) * kRows + tid];
-                        s_join[2 * kGroups * kRows + tid] = total > 0.f ? 1.f / total : 0.f;
+                        float total = 0.f;
+                        for (int c = 0; c < n; c += 4) {
+                            float l[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) l[k] = c + k < n ? __ldcg(part_of(cta0, cta0 + c + k) + kRows + r) : 0.f;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) total = c + k < n ? fmaf(l[k], s_f[(c + k) * kRows + tid], total) : total;
+                        }
+                        s_join[kJoinInPlace * kRows + tid] = total > 0.f ? 1.f / total : 0.f;
                         if (p.lse != nullptr && tid < rows) {
                             const int in_seq = row0 + tid, pos = in_seq / sq.grp, hd = in_seq - pos * sq.grp;
                             p.lse[static_cast<int64_t>(sq.q0 + pos) * p.heads + kvh * sq.grp + hd] =
@@ -788,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int in_seq = row0 + r, pos = in_seq / sq.grp, hd = in_seq - pos * sq.grp;
                     const int64_t at_out = static_cast<int64_t>(sq.q0 + pos) * p.heads + kvh * sq.grp + hd;
-                    const float inv = s_join[2 * kGroups * kRows + r];
+                    const float inv = s_join[kJoinInPlace * kRows + r];
                     const __half2 h0 = __floats2half2_rn(v[0].x * inv, v[0].y * inv), h1 = __floats2half2_rn(v[0].z * inv, v[0].w * inv);
                     const __half2 h2 = __floats2half2_rn(v[1].x * inv, v[1].y * inv), h3 = __floats2half2_rn(v[1].z * inv, v[1].w * inv);
                     *reinterpret_cast<uint4*>(p.out + at_out * D + 8 * c8) =
