@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
     int* s_first = reinterpret_cast<int*>(s_plan + 4);
     int* s_abort = s_first + 1;
     int* s_last = s_first + 2;
+    Seq* s_seq = reinterpret_cast<Seq*>(s_first + 4);  // sequence *s_first
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * S * C::kTile;
     const uint32_t bars = smem_u32(smem + C::kData + C::kQ) + warp * S * 8;
@@ -172,15 +173,16 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
     if (warp == 0) {
         int64_t total = 0;
         int units = 0;
+        Seq seq = {};  // sequence b0 + lane; 32 or fewer are read once (each trip to memory is 0.6 us)
+        auto read = [&](int b0) {
+            seq = Seq{};
+            if (b0 + lane < p.B) seq = seq_of(p, cache, b0 + lane);
+        };
         for (int b0 = 0; b0 < p.B; b0 += 32) {
-            int64_t c = 0;
-            int n = 0;
-            if (b0 + lane < p.B) {
-                const Seq s = seq_of(p, cache, b0 + lane);
-                c = static_cast<int64_t>(s.units) * (s.tiles + kUnitCost);
-                n = min(s.units, kMaxCtas);
-                if (s.bad && blockIdx.x == 0) record_error(status, kErrBounds);
-            }
+            read(b0);
+            if (seq.bad && blockIdx.x == 0) record_error(status, kErrBounds);
+            int64_t c = static_cast<int64_t>(seq.units) * (seq.tiles + kUnitCost);
+            const int n = min(seq.units, kMaxCtas);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
             total += c;
@@ -196,9 +198,12 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
         if (chunked) {
             const int mine = static_cast<int>(min(per + (per * lane + 30) / 31, static_cast<int64_t>(1 << 30)));
             int items = 0;
-            for (int b = 0; b < p.B; ++b) {
-                const Seq s = seq_of(p, cache, b);
-                items += s.units * ((s.tiles + mine - 1) / mine);
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                if (p.B > 32) read(b0);
+                for (int l = 0; l < min(32, p.B - b0); ++l) {
+                    const int n = __shfl_sync(0xffffffffu, seq.units, l), tiles = __shfl_sync(0xffffffffu, seq.tiles, l);
+                    items += n * ((tiles + mine - 1) / mine);
+                }
             }
             const uint32_t fits = __ballot_sync(0xffffffffu, items <= grid);
             per = __shfl_sync(0xffffffffu, mine, fits ? __ffs(fits) - 1 : 31);
@@ -208,11 +213,8 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
         int64_t at = 0;
         int first = p.B;
         for (int b0 = 0; b0 < p.B && (chunked || w0 < w1); b0 += 32) {
-            int64_t c = 0;
-            if (b0 + lane < p.B) {
-                const Seq s = seq_of(p, cache, b0 + lane);
-                c = static_cast<int64_t>(s.units) * (chunked ? (s.tiles + per - 1) / per : s.tiles + kUnitCost);
-            }
+            if (p.B > 32) read(b0);
+            const int64_t c = static_cast<int64_t>(seq.units) * (chunked ? (seq.tiles + per - 1) / per : seq.tiles + kUnitCost);
             int64_t upto = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -228,7 +230,8 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
             }
             at += __shfl_sync(0xffffffffu, upto, 31);
         }
-        if (lane == 0) {
+        if (lane == (first < p.B ? first & 31 : 0)) {
+            *s_seq = seq;
             s_plan[0] = chunked ? (first < p.B ? 1 : 0) : w1 - w0;
             s_plan[1] = w0 - at;
             s_plan[2] = per;
@@ -244,8 +247,9 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
     uint32_t phase = 0;  // one bit per ring stage
     const uint64_t policy = policy_evict_first();
 
-    for (int b = *s_first; left > 0 && b < p.B;) {
-        const Seq sq = seq_of(p, cache, b);
+    const int first = *s_first;
+    for (int b = first; left > 0 && b < p.B;) {
+        const Seq sq = b == first ? *s_seq : seq_of(p, cache, b);
         int unit, t0, t1, cta0, cta1;  // tiles t0 .. t1-1 of the unit, whose parts come from CTAs cta0 .. cta1
         if (chunked) {
             const int chunks = static_cast<int>((sq.tiles + per - 1) / per), size = (sq.tiles + chunks - 1) / chunks;
