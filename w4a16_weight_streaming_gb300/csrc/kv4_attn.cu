@@ -21,6 +21,13 @@
 // sum of its own, so that no warp waits for another inside a run. A tile is one bulk copy into the
 // warp's own ring in shared memory. Runs that end inside a row group leave their part in the workspace;
 // the CTA that arrives last there adds the parts in CTA order.
+//
+// Measured on one GB300: one sequence of 131,072 tokens, 20 heads on 4 of 256, 41.3 us (151 MB, 3.7 TB/s, 0.54 of
+// the copy bandwidth); 64 sequences of up to 8192 tokens, 40 heads on 8 of 128, 79.1 us (304 MB, 3.8 TB/s, 0.57);
+// one sequence of 777 tokens 12.8 us, which is the kernel's start (4 us), its tiles, and the adding of parts (5
+// us). A tile is 380 warp instructions for D = 128 and 610 for 256; with the 16 warps that the registers leave room
+// for an SM issues 2.2 of 4 a cycle, its ALU busy half of the time: the issue of dependent instructions bounds
+// the long calls, not memory.
 #include <algorithm>
 
 #include "common.cuh"
@@ -742,15 +749,16 @@ cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, const Launch
 // This kernel takes a pass over a sequence's tokens for every 8 query rows, the tcgen05 kernel one for every
 // 128, but starts and ends slower. Fitted to 1, 16 and 64 sequences of 777 .. 16384 tokens with 1 .. 120 rows
 // a key/value head, in us on 152 SMs: a start, and so much a 16-token tile of 8 rows (here) or a 64-token
-// tile of 128 rows (there). Both sides, measured: 16 sequences of 4096 and 4 heads of 256, 10 rows 47.3 | 46.7,
-// 20 rows 63.6 | 47.5; 8 heads of 128, 20 rows 61.1 | 59.6, 25 rows 77.7 | 60.4; 16 heads of 64, 24 rows
-// 74.2 | 93.2; one sequence of 16384, heads of 256, 40 rows 31.5 | 49.2, 80 rows 57.4 | 52.4. The lengths are
-// on the device: the block table's width stands for them.
+// tile of 128 rows (there). Both sides, measured: 16 sequences of 4096 and 4 heads of 256, 5 rows 27.9 | 43.3,
+// 10 rows 47.0 | 43.3, 20 rows 63.2 | 43.4; 8 heads of 128, 10 rows 47.9 | 57.6, 20 rows 61.3 | 57.8; 16 heads
+// of 64, 20 rows 73.1 | 94.6, 40 rows 115.2 | 94.5; one sequence of 16384, heads of 256, 40 rows 31.6 | 37.7, 80
+// rows 57.1 | 43.8. The choice costs 0.5 % over the better of the two on average, 20 % at most (1000 tokens, where
+// both take 20 to 35 us). The lengths are on the device: the block table's width stands for them.
 bool decode_is_faster(const Kv4AttnParams& p, const Kv4Cache& c) {
-    const double start_here = c.head_dim == 256 ? 11.5 : c.head_dim == 128 ? 9.0 : 8.0;
-    const double start_there = c.head_dim == 256 ? 28.0 : c.head_dim == 128 ? 24.5 : 20.0;
-    const double tile_here = c.head_dim == 256 ? 0.142 : c.head_dim == 128 ? 0.081 : 0.053;
-    const double tile_there = c.head_dim == 256 ? 1.05 : c.head_dim == 128 ? 0.86 : 0.79;
+    const double start_here = c.head_dim == 256 ? 13.1 : c.head_dim == 128 ? 10.7 : 8.8;
+    const double start_there = c.head_dim == 256 ? 28.6 : c.head_dim == 128 ? 22.2 : 18.7;
+    const double tile_here = c.head_dim == 256 ? 0.145 : c.head_dim == 128 ? 0.080 : 0.054;
+    const double tile_there = c.head_dim == 256 ? 0.82 : c.head_dim == 128 ? 0.73 : 0.70;
     const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / c.kv_heads);
     const double heads = static_cast<double>(std::min(p.B, p.M)) * c.kv_heads;
     const double tokens = static_cast<double>(p.max_pages) * c.page_tokens;

@@ -24,6 +24,11 @@
 // (maximum, sum, unnormalised rows) in the workspace; the CTA that arrives last adds them, in CTA order, to
 // what it still has in TMEM. (Added from memory, its own part among them: 169 us for the chunk above, 163 so.
 // An SM reads parts at 45 to 60 GB/s, however many loads are under way.)
+//
+// Measured on one GB300: 1024 queries of 20 heads (4 of 256) behind 8192 tokens 162.6 us (183 GFLOP, 1,125 TFLOP/s,
+// 0.59 of the bf16 rate); 16 sequences of 1070 .. 8005 tokens with 8 .. 16 queries each 46.8 us (73.6 MB). A tile
+// of 64 tokens takes 1.05 us with full rows, of which its matrix instructions fill 0.55; 6000 warp instructions
+// at 2.8 a cycle are the rest: issue bounds the chunk, the dequantisation above all.
 #include <algorithm>
 
 #include "common.cuh"

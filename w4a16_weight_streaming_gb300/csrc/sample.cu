@@ -23,6 +23,12 @@
 // CTA's slice is below 65,536 elements). Each CTA then adds up the cluster's counts of its share of the
 // values and folds them into coarse bins of 32 values, count and mass. Every decision is a search in the
 // 2048 prefix sums followed by a look at the 32 values of one bin.
+//
+// Measured on one GB300, vocabulary 248,320: 1 row with top-k 20 and top-p 12.3 us, 16 rows with min-p 13.0 us:
+// latency, of two short passes and the barriers behind them. 256 rows with top-p alone 138 us (127 MB, 0.92
+// TB/s): the issue of 44 instructions a logit, most of them for the exponentials of those below the window (35
+// us) and the counts (22 us). 33 rows of 32,003 with settings of their own 24 us, rows of the second kernel
+// among them.
 #include <cfloat>
 
 #include "common.cuh"
