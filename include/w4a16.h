@@ -337,7 +337,8 @@ int w4a16_kv4_load(const w4a16_kv4_cache* cache, const int32_t* slots, uint16_t*
 
 /* Bytes of device memory that w4a16_kv4_attention needs beside its operands, the same for every batch;
  * 0 for an unsupported head size. To be zeroed once, before its first use; every call leaves it ready
- * for the next. Calls that may run at the same time need one each. */
+ * for the next (after a W4A16_ERR_DEVICE_TIMEOUT zero it again). Calls that may run at the same time
+ * need one each. */
 size_t w4a16_kv4_attention_workspace_bytes(int head_dim);
 
 /*

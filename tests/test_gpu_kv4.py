@@ -286,6 +286,25 @@ def test_attention_repeats_bit_for_bit_and_on_another_stream(W, q_lens):
     close(a, want, bound)
 
 
+@pytest.mark.parametrize("lens,q_lens,H,KV,D", [([14000], [3], 8, 1, 64), ([16000], [26], 5, 1, 256), ([12000], [17], 16, 2, 128),
+                                                ([5000, 4100, 70], [40, 9, 26], 10, 2, 256)],
+                         ids=["many64", "many256", "many128", "several"])
+def test_parts_of_long_units_are_added_alike_whoever_is_last(W, lens, q_lens, H, KV, D):
+    """One unit's tokens in the hands of up to a dozen CTAs, which finish in any order."""
+    b = Batch(W, 16, lens, q_lens, H, KV, D, 64)
+    q, args = cuda(b.q), b.args(wide=True)
+    lse = torch.empty((sum(q_lens), H), device="cuda")
+    a = W.kv4_attention(q, b.cache, lse=lse, **args)
+    for _ in range(25):
+        lse_again = torch.empty_like(lse)
+        again = W.kv4_attention(q, b.cache, lse=lse_again, **args)
+        assert torch.equal(a.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse_again)
+    ok(W)
+    want, _, bound = b.want(D ** -0.5)
+    close(a, want, bound)
+    assert int(b.work[:4096].sum()) == 0
+
+
 def test_attention_with_negative_and_zero_scale(W):
     b = Batch(W, 21, [100, 300], [1, 30], 4, 2, 128, 16)
     for wide in (False, True):
