@@ -24,7 +24,7 @@
 //
 // Measured on one GB300: one sequence of 131,072 tokens, 20 heads on 4 of 256, 41.3 us (151 MB, 3.7 TB/s, 0.54 of
 // the copy bandwidth); 64 sequences of up to 8192 tokens, 40 heads on 8 of 128, 79.1 us (304 MB, 3.8 TB/s, 0.57);
-// one sequence of 777 tokens 12.8 us, which is the kernel's start (4 us), its tiles, and the adding of parts (5
+// one sequence of 777 tokens 10.1 us, which is the kernel's start (4 us), a few tiles, and the adding of parts (3
 // us). A tile is 380 warp instructions for D = 128 and 610 for 256; with the 16 warps that the registers leave room
 // for an SM issues 2.2 of 4 a cycle, its ALU busy half of the time: the issue of dependent instructions bounds
 // the long calls, not memory.
@@ -52,6 +52,7 @@ struct Decode {
     static constexpr int kWarps = Narrow ? 4 : D == 256 ? 12 : 16;
     static constexpr int kStages = D == 256 ? 3 : D == 128 ? 5 : 8;
     static constexpr int kThreads = kWarps * 32;
+    static constexpr int kWhole = kWarps * (D == 256 ? 2 : D == 128 ? 3 : 4);
     static constexpr int kTile = Kv4<D>::kTileBytes;
     static constexpr int kRing = kWarps * kStages * kTile;
     static constexpr int kPitch = D + 4;  // floats between rows of a warp's part: conflict-free stores
@@ -177,6 +178,7 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
     griddep_wait();
 
     // ---- this CTA's run of the work list
+    auto chunks_of = [](int tiles, int size) { return tiles <= C::kWhole ? 1 : (tiles + size - 1) / size; };
     if (warp == 0) {
         int64_t total = 0;
         int units = 0;
@@ -196,12 +198,13 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
             units = min(kMaxCtas, units + __reduce_add_sync(0xffffffffu, n));
         }
         // Few units: each is cut into equal chunks, one a CTA, the chunk size the smallest of 32 candidates
-        // with which there are CTAs enough (twice the mean is, when half the CTAs suffice for the units); at
-        // least 4 tiles a warp, since adding the parts of a unit takes as long as 5 or so. Otherwise equal
-        // runs that may begin and end inside a unit.
+        // with which there are CTAs enough (twice the mean is, when half the CTAs suffice for the units); a
+        // tile a warp at least (one sequence of 2000 tokens, 4 heads of 256: 11.0 us, with two 12.2, with four
+        // 15.0). Adding the parts takes 3 us, a tile 1.3 (256), 0.8 (128) or 0.5 (64): a unit of up to kWhole
+        // tiles is left whole. Otherwise equal runs that may begin and end inside a unit.
         const int grid = static_cast<int>(gridDim.x);
         const bool chunked = 2 * units <= grid;
-        int64_t per = max((total + grid - 1) / grid, static_cast<int64_t>(chunked ? 4 * NW : NW + kUnitCost));
+        int64_t per = max((total + grid - 1) / grid, static_cast<int64_t>(chunked ? NW : NW + kUnitCost));
         if (chunked) {
             const int mine = static_cast<int>(min(per + (per * lane + 30) / 31, static_cast<int64_t>(1 << 30)));
             int items = 0;
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
                 if (p.B > 32) read(b0);
                 for (int l = 0; l < min(32, p.B - b0); ++l) {
                     const int n = __shfl_sync(0xffffffffu, seq.units, l), tiles = __shfl_sync(0xffffffffu, seq.tiles, l);
-                    items += n * ((tiles + mine - 1) / mine);
+                    items += n * chunks_of(tiles, mine);
                 }
             }
             const uint32_t fits = __ballot_sync(0xffffffffu, items <= grid);
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
         int first = p.B;
         for (int b0 = 0; b0 < p.B && (chunked || w0 < w1); b0 += 32) {
             if (p.B > 32) read(b0);
-            const int64_t c = static_cast<int64_t>(seq.units) * (chunked ? (seq.tiles + per - 1) / per : seq.tiles + kUnitCost);
+            const int64_t c = static_cast<int64_t>(seq.units) * (chunked ? chunks_of(seq.tiles, static_cast<int>(per)) : seq.tiles + kUnitCost);
             int64_t upto = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
         const Seq sq = b == first ? *s_seq : seq_of(p, cache, b);
         int unit, t0, t1, cta0, cta1;  // tiles t0 .. t1-1 of the unit, whose parts come from CTAs cta0 .. cta1
         if (chunked) {
-            const int chunks = static_cast<int>((sq.tiles + per - 1) / per), size = (sq.tiles + chunks - 1) / chunks;
+            const int chunks = chunks_of(sq.tiles, static_cast<int>(per)), size = (sq.tiles + chunks - 1) / chunks;
             unit = static_cast<int>(off) / chunks;
             const int chunk = static_cast<int>(off) - unit * chunks;
             t0 = chunk * size;
