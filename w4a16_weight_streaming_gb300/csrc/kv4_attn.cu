@@ -752,16 +752,16 @@ cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, const Launch
 // This kernel takes a pass over a sequence's tokens for every 8 query rows, the tcgen05 kernel one for every
 // 128, but starts and ends slower. Fitted to 1, 16 and 64 sequences of 777 .. 16384 tokens with 1 .. 120 rows
 // a key/value head, in us on 152 SMs: a start, and so much a 16-token tile of 8 rows (here) or a 64-token
-// tile of 128 rows (there). Both sides, measured: 16 sequences of 4096 and 4 heads of 256, 5 rows 27.9 | 43.3,
-// 10 rows 47.0 | 43.3, 20 rows 63.2 | 43.4; 8 heads of 128, 10 rows 47.9 | 57.6, 20 rows 61.3 | 57.8; 16 heads
-// of 64, 20 rows 73.1 | 94.6, 40 rows 115.2 | 94.5; one sequence of 16384, heads of 256, 40 rows 31.6 | 37.7, 80
-// rows 57.1 | 43.8. The choice costs 0.5 % over the better of the two on average, 20 % at most (1000 tokens, where
-// both take 20 to 35 us). The lengths are on the device: the block table's width stands for them.
+// tile of 128 rows (there). Both sides, measured: 16 sequences of 4096 and 4 heads of 256, 5 rows 28.9 | 43.1,
+// 10 rows 47.9 | 43.1, 20 rows 64.0 | 43.2; 8 heads of 128, 10 rows 48.7 | 57.5, 20 rows 61.0 | 57.5; 16 heads of
+// 64, 20 rows 73.2 | 94.4, 40 rows 115.5 | 94.3; one sequence of 16384, heads of 256, 40 rows 31.5 | 34.4, 80 rows
+// 57.3 | 41.4. The choice costs 0.3 % over the better of the two on average, 17 % at most (1000 tokens, where both
+// take 20 to 35 us). The lengths are on the device: the block table's width stands for them.
 bool decode_is_faster(const Kv4AttnParams& p, const Kv4Cache& c) {
-    const double start_here = c.head_dim == 256 ? 13.1 : c.head_dim == 128 ? 10.7 : 8.8;
-    const double start_there = c.head_dim == 256 ? 28.6 : c.head_dim == 128 ? 22.2 : 18.7;
-    const double tile_here = c.head_dim == 256 ? 0.145 : c.head_dim == 128 ? 0.080 : 0.054;
-    const double tile_there = c.head_dim == 256 ? 0.82 : c.head_dim == 128 ? 0.73 : 0.70;
+    const double start_here = c.head_dim == 256 ? 11.2 : c.head_dim == 128 ? 10.0 : 8.5;
+    const double start_there = c.head_dim == 256 ? 26.3 : c.head_dim == 128 ? 19.3 : 16.1;
+    const double tile_here = c.head_dim == 256 ? 0.162 : c.head_dim == 128 ? 0.087 : 0.053;
+    const double tile_there = c.head_dim == 256 ? 0.73 : c.head_dim == 128 ? 0.69 : 0.74;
     const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / c.kv_heads);
     const double heads = static_cast<double>(std::min(p.B, p.M)) * c.kv_heads;
     const double tokens = static_cast<double>(p.max_pages) * c.page_tokens;

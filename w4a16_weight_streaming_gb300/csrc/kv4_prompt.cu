@@ -44,7 +44,9 @@ constexpr int kSub = kTok / kKv4Tile;
 // What the start and end of a unit cost, in tiles (prompt chunk of 1024 x 20 heads behind 8192 tokens: 164.9 us
 // with 6, 162.5 with 8, 163.3 with 10)
 constexpr int kUnitCost = 8;
-constexpr int kMinRun = 12;    // tiles; fewer make more parts than they save
+// Fewest tiles of a run: less makes more parts than it saves (24 queries of 20 heads behind 4096 tokens, 4 heads of
+// 256: 32.2 us with 4, 34.8 with 8, 37.3 with 12; behind 16384 53.4, 50.0, 50.9)
+constexpr int kMinRun = 6;
 constexpr int kDequant = 16;   // first warp of each role (softmax: 0)
 constexpr int kProducer = 24, kIssueS = 25;
 constexpr int kWarps = 27;     // (26: PV)
