@@ -203,27 +203,33 @@ __device__ __forceinline__ void find_occurrence(const uint16_t* src, int begin, 
                                        : (w[j / 2] & 0xFFFF0000u) | src[i + j];
         return make_uint4(w[0], w[1], w[2], w[3]);
     };
+    // compared as numbers: +0 and -0 are one value, NaN is none
+    const __half2 value = __float2half2_rn(value_of(key));
+    auto equal = [&](uint32_t w) { return __heq2(*reinterpret_cast<const __half2*>(&w), value); };  // 1 or 0
     auto bits_of = [&](const uint4& x) -> uint32_t {  // a bit for each of the vector's elements with the value
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
         uint32_t bits = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            bits |= (key_of(w[j] & 0xFFFFu) == key ? 1u << (2 * j) : 0u) | (key_of(w[j] >> 16) == key ? 2u << (2 * j) : 0u);
+        for (int j = 0; j < 4; ++j) {
+            const __half2 e = equal(w[j]);
+            bits |= (__low2float(e) != 0.f ? 1u << (2 * j) : 0u) | (__high2float(e) != 0.f ? 2u << (2 * j) : 0u);
+        }
         return bits;
     };
-    // a warp's share in rounds of 128 vectors (V <= 1,000,000: at most 62, or 123 with 8 warps): how many in each
+    // a warp's share in rounds of 256 vectors (V <= 1,000,000: at most 62): how many in each
+    constexpr int kRound = 8;
     __syncthreads();
     uint32_t count = 0;
-    for (int v = v0, round = 0; v < v1; v += 128, ++round) {
-        uint4 x[4];
+    for (int v = v0, round = 0; v < v1; v += 32 * kRound, ++round) {
+        uint4 x[kRound];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = fetch(v + 32 * k + lane);
-        uint32_t n = 0;
+        for (int k = 0; k < kRound; ++k) x[k] = fetch(v + 32 * k + lane);
+        __half2 n = __float2half2_rn(0.f);  // (32 of each half at most)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) n += __popc(bits_of(x[k]));
-        n = __reduce_add_sync(0xffffffffu, n);
+        for (int k = 0; k < kRound; ++k)
+            n = __hadd2(n, __hadd2(__hadd2(equal(x[k].x), equal(x[k].y)), __hadd2(equal(x[k].z), equal(x[k].w))));
         if (lane == 0) scratch[warp * (32768 / kThreads) + round] = count;
-        count += n;
+        count += __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(__low2float(n) + __high2float(n)));
     }
     __syncwarp();
     __shared__ uint32_t totals[kThreads / 32];
@@ -233,13 +239,13 @@ __device__ __forceinline__ void find_occurrence(const uint16_t* src, int begin, 
     for (int i = 0; i < warp; ++i) before += totals[i];
     if (index < before || index >= before + count) return;
     int round = 0;
-    while (v0 + 128 * (round + 1) < v1 && before + scratch[warp * (32768 / kThreads) + round + 1] <= index) ++round;
+    while (v0 + 32 * kRound * (round + 1) < v1 && before + scratch[warp * (32768 / kThreads) + round + 1] <= index) ++round;
     before += scratch[warp * (32768 / kThreads) + round];
-    uint4 x[4];
+    uint4 x[kRound];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = fetch(v0 + 128 * round + 32 * k + lane);
+    for (int k = 0; k < kRound; ++k) x[k] = fetch(v0 + 32 * kRound * round + 32 * k + lane);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kRound; ++k) {
         const uint32_t bits = bits_of(x[k]), n = __popc(bits);
         uint32_t upto = n;
 #pragma unroll
@@ -248,7 +254,7 @@ __device__ __forceinline__ void find_occurrence(const uint16_t* src, int begin, 
             if (lane >= o) upto += y;
         }
         if (index >= before + upto - n && index < before + upto)  // in this lane's vector
-            *token = base + 8 * (v0 + 128 * round + 32 * k + lane) +
+            *token = base + 8 * (v0 + 32 * kRound * round + 32 * k + lane) +
                      static_cast<int>(__fns(bits, 0, static_cast<int>(index - (before + upto - n)) + 1));
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
