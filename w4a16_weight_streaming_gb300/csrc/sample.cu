@@ -24,12 +24,12 @@
 // values and folds them into coarse bins of 32 values, count and mass. Every decision is a search in the
 // 2048 prefix sums followed by a look at the 32 values of one bin.
 //
-// Measured on one GB300, vocabulary 248,320: 1 row with top-k 20 and top-p 12.3 us, 16 rows with min-p 13.0 us:
-// latency, of two short passes and the barriers behind them. 256 rows with top-p alone 138 us (127 MB, 0.92
-// TB/s): the issue of 44 instructions a logit, most of them for the exponentials of those below the window (35
-// us) and the counts (22 us). 33 rows of 32,003 with settings of their own 24 us, rows of the second kernel
-// among them.
+// Measured on one GB300, vocabulary 248,320: 1 row with top-k 20 and top-p 12.1 us, 16 rows with min-p 12.0 us:
+// latency, of two short passes and the barriers behind them. 256 rows with top-p alone 112 us (127 MB, 1.13 TB/s):
+// the issue of some 40 instructions a logit, most of them for the exponentials of those below the window and
+// the counts. 33 rows of 32,003 with settings of their own 22.5 us: rank 0's weights and decisions.
 #include <cfloat>
+#include <cmath>
 
 #include "common.cuh"
 #include "internal.h"
@@ -389,11 +389,10 @@ __global__ void __launch_bounds__(kWindowThreads, 4)
         const uint32_t neg = static_cast<uint32_t>(static_cast<int>(bits << 16) >> 31);
         return kmax - ((bits ^ (neg | 0x8000u)) & 0xFFFFu);
     };
+    // Without a branch: what is not counted goes to a word of the thread's own (256 rows 120 us with a predicate)
+    const uint32_t aside = smem_u32(weights) + (kThreads + tid) * 4;
     auto count_one = [&](uint32_t d) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t@p red.shared::cta.add.u32 [%2], 1;\n\t}" ::"r"(d), "r"(size),
-            "r"(hist_s + d * 4)
-            : "memory");
+        asm volatile("red.shared::cta.add.u32 [%0], 1;" ::"r"(d < size ? hist_s + d * 4 : aside) : "memory");
     };
     auto half_of = [](uint32_t bits) { return __half2float(__ushort_as_half(static_cast<unsigned short>(bits))); };
     auto exponent = [&](float x) {  // weight of a logit below the window
@@ -440,9 +439,8 @@ __global__ void __launch_bounds__(kWindowThreads, 4)
                     const uint32_t b = clean(w[j]), d0 = below(b & 0xFFFFu), d1 = below(b >> 16);
                     count_one(d0);
                     count_one(d1);
-                    const uint32_t a0 = small_fixed_of(exponent(half_of(b & 0xFFFFu)), 1099511627776.f);
-                    const uint32_t a1 = small_fixed_of(exponent(half_of(b >> 16)), 1099511627776.f);
-                    part += (d0 < size ? 0u : a0) + (d1 < size ? 0u : a1);
+                    const float x0 = d0 < size ? -INFINITY : half_of(b & 0xFFFFu), x1 = d1 < size ? -INFINITY : half_of(b >> 16);
+                    part += small_fixed_of(exponent(x0), 1099511627776.f) + small_fixed_of(exponent(x1), 1099511627776.f);
                 }
             } else if (with_tail) {
 #pragma unroll
@@ -450,9 +448,9 @@ __global__ void __launch_bounds__(kWindowThreads, 4)
                     const uint32_t b = clean(w[j]), d0 = below(b & 0xFFFFu), d1 = below(b >> 16);
                     count_one(d0);
                     count_one(d1);
-                    const float e0 = exponent(half_of(b & 0xFFFFu)), e1 = exponent(half_of(b >> 16));
-                    add_fixed(d0 < size ? 0.f : e0, high, part);
-                    add_fixed(d1 < size ? 0.f : e1, high, part);
+                    const float x0 = d0 < size ? -INFINITY : half_of(b & 0xFFFFu), x1 = d1 < size ? -INFINITY : half_of(b >> 16);
+                    add_fixed(exponent(x0), high, part);
+                    add_fixed(exponent(x1), high, part);
                 }
             } else if (!sparse && top >= least) {
 #pragma unroll
@@ -991,9 +989,9 @@ cudaError_t launch_rows(F* f, const SampleParams& p, int C, int threads, size_t 
 
 cudaError_t launch_sample(const SampleParams& p, int sm_count, cudaStream_t s, unsigned* status) {
     // Window: 256 threads, four CTAs an SM (with 512 and two, and 8192 values: 256 rows of 248,320 153 us
-    // against 139, 33 mixed rows of 32,003 26.7 against 24.4). Few rows are spread over up to 16 CTAs (1 row
-    // 12.4 us, with 8 14.4), more over up to 8 (16 rows 12.5, with 16 13.4), many over as many as make two
-    // rounds (256 rows: 216 with 1, 167 with 2, 139 with 4, 149 with 8).
+    // against then 139, 33 mixed rows of 32,003 26.7 against then 24.4). Few rows are spread over up to 16 CTAs
+    // (1 row 12.2 us, with 8 14.0), more over up to 8 (16 rows 12.6, with 16 13.2), many over as many as make
+    // two rounds (256 rows, of then 122 us with 4: 187 with 1, 141 with 2, 140 with 8).
     int C = p.M <= 8 ? 16 : 8;
     while (C > 1 && static_cast<int64_t>(p.M) * C > 7LL * sm_count) C /= 2;
     cudaError_t e = launch_rows(sample_window_kernel, p, C, kWindowThreads, kWindowSmem, s, status);
