@@ -38,7 +38,7 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kRows = 128;     // query rows of a unit
+constexpr int kRows = 128;     // query rows of a CTA
 constexpr int kTok = 64;       // tokens of a tile
 constexpr int kSub = kTok / kKv4Tile;
 // What the start and end of a unit cost, in tiles (prompt chunk of 1024 x 20 heads behind 8192 tokens: 164.9 us
@@ -54,11 +54,14 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kJoinInPlace = 8;  // most parts of a unit that its last CTA adds to its own in TMEM
 constexpr int kNotes = 16;     // tiles whose page validity is kept
 
-template <int D>
+template <int D, bool Pair>
 struct Prompt {
+    static constexpr int kCtas = Pair ? 2 : 1;            // of a cluster, on one unit
+    static constexpr int kUnitRows = kRows * kCtas;
+    static constexpr int kTokCta = kTok / kCtas;          // tokens of K' in a CTA (of V' it has D / kCtas elements)
     static constexpr int kRaw = kSub * Kv4<D>::kTileBytes;
     static constexpr int kRawStages = D == 256 ? 3 : 4;
-    static constexpr int kBuf = kTok * D * 2;  // one K' or V' buffer
+    static constexpr int kBuf = kTok * D * 2 / kCtas;  // one K' or V' buffer
     static constexpr int kOffV = 2 * kBuf;
     // (where the tiles are, a unit's parts are added: four slots or more of 16 elements of a part for every
     // softmax thread, or what up to kKv4MaxPromptCtas parts are scaled by, under the raw tiles)
@@ -194,7 +197,8 @@ __device__ __forceinline__ void lds_params(uint32_t addr, uint32_t (&p)[G]) {
     }
 }
 
-struct PromptSeq {
+template <int kUnitRows>
+struct PromptSeqOf {
     int q0, q_len, n, grp, row_tiles;
     bool bad;  // (24 bytes)
     // tokens that query row r (within the sequence) sees
@@ -203,26 +207,27 @@ struct PromptSeq {
     }
     // tiles of a row tile (its last row sees most); at least one, so that empty rows are written
     __device__ __forceinline__ int tiles(int rt, int causal) const {
-        const int last = min(q_len * grp, (rt + 1) * kRows) - 1;
+        const int last = min(q_len * grp, (rt + 1) * kUnitRows) - 1;
         return max(1, (seen(last, causal) + kTok - 1) / kTok);
     }
     // The work list's unit is 1 / grp of a token: row tile rt takes a fixed cost, then no less than its
-    // tokens, grows by kRows from one row tile to the next (causal), and so has a sum in closed form. Its
+    // tokens, grows by kUnitRows from one row tile to the next (causal), and so has a sum in closed form. Its
     // tile t begins at fixed() + t * grp * kTok.
     __device__ __forceinline__ int64_t fixed() const { return static_cast<int64_t>(grp) * kTok * kUnitCost; }
     __device__ __forceinline__ int64_t flat(int causal) const {
         return fixed() + static_cast<int64_t>(grp) * (causal ? max(n - q_len, 0) + 1 : max(n, 1));
     }
     __device__ __forceinline__ int64_t length(int rt, int causal) const {
-        return flat(causal) + (causal ? static_cast<int64_t>(rt + 1) * kRows : 0);
+        return flat(causal) + (causal ? static_cast<int64_t>(rt + 1) * kUnitRows : 0);
     }
     __device__ __forceinline__ int64_t before(int rt, int causal) const {  // of row tiles 0 .. rt-1 of one head
-        return rt * flat(causal) + (causal ? static_cast<int64_t>(rt) * (rt + 1) / 2 * kRows : 0);
+        return rt * flat(causal) + (causal ? static_cast<int64_t>(rt) * (rt + 1) / 2 * kUnitRows : 0);
     }
 };
 
-__device__ __forceinline__ PromptSeq seq_of(const Kv4AttnParams& p, const Kv4View& c, int b) {
-    PromptSeq s;
+template <int kUnitRows>
+__device__ __forceinline__ PromptSeqOf<kUnitRows> prompt_seq(const Kv4AttnParams& p, const Kv4View& c, int b) {
+    PromptSeqOf<kUnitRows> s;
     const int q0 = p.q_start[b], q1 = p.q_start[b + 1], n = p.kv_len[b];
     s.q0 = min(max(q0, 0), p.M);
     const int end = min(max(q1, s.q0), p.M);
@@ -230,15 +235,61 @@ __device__ __forceinline__ PromptSeq seq_of(const Kv4AttnParams& p, const Kv4Vie
     s.n = min(max(n, 0), p.max_pages << c.page_shift);
     s.bad = s.q0 != q0 || end != q1 || s.n != n;
     s.grp = p.heads / c.kv_heads;
-    s.row_tiles = (s.q_len * s.grp + kRows - 1) / kRows;
+    s.row_tiles = (s.q_len * s.grp + kUnitRows - 1) / kUnitRows;
     return s;
 }
 
-template <int D>
+// The same for the two CTAs of a cluster: one product of 256 rows, A and D in the TMEM of both (128 rows each), B
+// half in each one's shared memory; issued by the cluster's first CTA.
+__device__ __forceinline__ void umma_pair_f16_ts(uint32_t d_taddr, uint32_t a_taddr, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_taddr),
+        "r"(a_taddr), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void umma_pair_commit(uint32_t bar) {  // arrives at the barrier of both
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"(static_cast<uint16_t>(3))
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_pair_alloc(uint32_t slot_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot_smem), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_pair_dealloc(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrive at the first CTA's barrier. What precedes it is this SM's own shared memory and TMEM, complete after a
+// proxy fence or wait::st, and read by this SM's part of a product: a release at the cluster's scope, which waits 900
+// cycles here, is not needed.
+__device__ __forceinline__ void mbar_arrive_first(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_peer(bar, 0)) : "memory");
+}
+// Wait for arrivals of the other CTA too (a suspended thread is not woken promptly by those: polled).
+__device__ __forceinline__ bool warp_poll_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns,
+                                                  unsigned* status) {
+    if (__all_sync(0xffffffffu, mbar_test_wait_cluster(bar, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t spin = 1;; ++spin) {
+        if (__all_sync(0xffffffffu, mbar_test_wait_cluster(bar, parity))) return true;
+        if ((spin & 255u) != 0u) continue;
+        bool over = *abort_flag != 0;
+        if (!over && global_timer_ns() - t0 > timeout_ns) {
+            record_error(status, kErrTimeout);
+            *abort_flag = 1;
+            over = true;
+        }
+        if (__any_sync(0xffffffffu, over)) return false;
+    }
+}
+
+template <int D, bool Pair>
 __global__ void __launch_bounds__(kThreads, 1)
     kv4_prompt_kernel(const Kv4AttnParams p, const Kv4View cache, uint64_t timeout_ns, unsigned* status) {
-    using C = Prompt<D>;
+    using C = Prompt<D, Pair>;
     using T = Kv4<D>;
+    using PromptSeq = PromptSeqOf<C::kUnitRows>;
+    auto seq_of = [](const Kv4AttnParams& p, const Kv4View& c, int b) { return prompt_seq<C::kUnitRows>(p, c, b); };
     constexpr int G = T::kGroups, R = C::kRawStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -266,6 +317,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto pv_done = [&](int s) { return bars + 8 * (2 * R + 8 + s); };  // O updated, V' and S/P free
     const uint32_t q_full = bars + 8 * (2 * R + 10);
     auto drained = [&](int i) { return bars + 8 * (2 * R + 11 + i); };  // the issuers' instructions, after a wait ran out
+    // A pair's barriers for what its products read are the first CTA's
+    const uint32_t rank = Pair ? cluster_ctarank() : 0u;
+    const int team = static_cast<int>(blockIdx.x) / C::kCtas, teams = static_cast<int>(gridDim.x) / C::kCtas;
+    auto arrive = [&](uint32_t bar) {
+        if constexpr (Pair) mbar_arrive_first(bar);
+        else mbar_arrive(bar);
+    };
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+        if constexpr (Pair) return warp_poll_cluster(bar, parity, s_abort, timeout_ns, status);
+        else return warp_suspend(bar, parity, s_abort, timeout_ns, status);
+    };
+    auto multiply = [&](uint32_t d, uint32_t a, uint64_t desc, uint32_t idesc, bool more) {
+        if constexpr (Pair) umma_pair_f16_ts(d, a, desc, idesc, more);
+        else umma_f16_ts(d, a, desc, idesc, more);
+    };
+    auto commit = [&](uint32_t bar) {
+        if constexpr (Pair) umma_pair_commit(bar);
+        else umma_commit(bar);
+    };
     auto wait = [&](uint32_t bar, uint32_t parity) { return warp_suspend(bar, parity, s_abort, timeout_ns, status); };
 
     if (warp == kProducer) {
@@ -275,21 +345,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(raw_empty(i), 8);
             }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(k_full(i), 4);
-                mbar_init(v_full(i), 4);
+                mbar_init(k_full(i), 4 * C::kCtas);
+                mbar_init(v_full(i), 4 * C::kCtas);
                 mbar_init(s_full(i), 1);
-                mbar_init(p_full(i), 16);
+                mbar_init(p_full(i), 16 * C::kCtas);
                 mbar_init(pv_done(i), 1);
             }
-            mbar_init(q_full, 16);
+            mbar_init(q_full, 16 * C::kCtas);
             mbar_init(drained(0), 1);
             mbar_init(drained(1), 1);
             *s_abort = 0;
             fence_barrier_init();
         }
         __syncwarp();
-        tmem_alloc(smem_u32(s_tmem), C::kCols);
-        tmem_relinquish();
+        if constexpr (Pair) {
+            tmem_pair_alloc(smem_u32(s_tmem), C::kCols);
+        } else {
+            tmem_alloc(smem_u32(s_tmem), C::kCols);
+            tmem_relinquish();
+        }
     }
     griddep_wait();
 
@@ -312,9 +386,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
             total += c;
         }
-        const int64_t per = max((total + gridDim.x - 1) / gridDim.x,
+        const int64_t per = max((total + teams - 1) / teams,
                                 static_cast<int64_t>(kMinRun + kUnitCost) * kTok * (p.heads / cache.kv_heads));
-        const int64_t w0 = min(total, per * blockIdx.x), w1 = min(total, w0 + per);
+        const int64_t w0 = min(total, per * team), w1 = min(total, w0 + per);
         int64_t at = 0;
         int first = p.B;
         for (int b0 = 0; b0 < p.B && w0 < w1; b0 += 32) {
@@ -360,7 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    if constexpr (Pair) cluster_sync_all();  // (the other's barriers are there too)
+    else __syncthreads();
     tc_fence_after();
     griddep_launch_dependents();  // (after the allocation: the next grid's cannot come before it)
     const uint32_t tmem = *s_tmem;
@@ -373,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     PromptSeq sq = {};
     if (b < p.B) sq = *s_seq;
 
-    // CTA c's part of the unit that begins in CTA cta0
+    // CTA c's part of the unit that begins in CTA cta0 (of a pair, every second CTA has the same rows)
     auto part_of = [&](int cta0, int c) {
         return reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + 4096) + static_cast<int64_t>(2 * c + (c == cta0 ? 1 : 0)) * C::kPart;
     };
@@ -388,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
         }
         // tiles of the unit whose places lie in the run
-        const int tiles = sq.tiles(rt, p.causal), row0 = rt * kRows;
+        const int tiles = sq.tiles(rt, p.causal), row0 = rt * C::kUnitRows + static_cast<int>(rank) * kRows;
         const int64_t first_at = at + sq.fixed(), each = static_cast<int64_t>(sq.grp) * kTok;
         const int t0 = static_cast<int>(min(static_cast<int64_t>(tiles), (max(w0 - first_at, static_cast<int64_t>(0)) + each - 1) / each));
         const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), (max(w1 - first_at, static_cast<int64_t>(0)) + each - 1) / each));
@@ -396,8 +472,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++rt;
         if (t0 >= t1) continue;
         const int nt = t1 - t0;
-        const int cta0 = static_cast<int>(first_at / per), cta1 = static_cast<int>((first_at + (tiles - 1) * each) / per);
-        const int rows = min(kRows, sq.q_len * sq.grp - row0);
+        const int cta0 = static_cast<int>(first_at / per) * C::kCtas + static_cast<int>(rank);
+        const int cta1 = static_cast<int>((first_at + (tiles - 1) * each) / per) * C::kCtas + static_cast<int>(rank);
+        const int parts = (cta1 - cta0) / C::kCtas + 1;
+        const int rows = max(0, min(kRows, sq.q_len * sq.grp - row0));  // (none: the second half of a pair's unit)
         const bool whole = t0 == 0 && t1 == tiles;
 
         if (warp < kDequant) {
@@ -426,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
+                if (lane == 0) arrive(q_full);
             }
             const float c1 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
             const int lim = sq.seen(in_seq, p.causal);
@@ -509,11 +587,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(buf));
+                if (lane == 0) arrive(p_full(buf));
             }
             // ---- the unit's rows, or this CTA's part of them: a quarter of the elements each. The last CTA adds
             // the others' parts to its own in TMEM, which is not written where they are all there by now.
-            const int n = cta1 - cta0 + 1, own = static_cast<int>(blockIdx.x) - cta0;
+            const int n = parts, own = (static_cast<int>(blockIdx.x) - cta0) / C::kCtas;
             bool join = false;
             if (!whole) {
                 if (tid == 0) {
@@ -601,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto fetch = [&]() {  // part `next` of the next chunk
                     if (to_come > 0) {
                         // (the parts of the unit's other CTAs: every second one from the first's neighbour on)
-                        const float4* from = rest + (next == 0 ? 0 : (2 * next - 1) * (C::kPart / 4)) + at_chunk;
+                        const float4* from = rest + (next == 0 ? 0 : (2 * C::kCtas * next - 1) * (C::kPart / 4)) + at_chunk;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) cp_async16(to_slot + k * (kSlot / 4), from + k * kRows);
                         --to_come;
@@ -619,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float mm[kJoinInPlace], ll[kJoinInPlace], top = -INFINITY, total = 0.f;
 #pragma unroll
                     for (int c = 0; c < kJoinInPlace; ++c) {
-                        const float* from = part_of(cta0, cta0 + min(c, n - 1)) + rr;
+                        const float* from = part_of(cta0, cta0 + C::kCtas * min(c, n - 1)) + rr;
                         mm[c] = c == own ? m : c < n ? __ldcg(from) : -INFINITY;
                         ll[c] = c == own ? l : c < n ? __ldcg(from + kRows) : 0.f;
                         top = fmaxf(top, mm[c]);
@@ -685,10 +763,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp < kProducer) {
             // ================= dequantise: keys or values of quarter `sub`
-            const int dw = warp - kDequant, sub = dw & 3;
+            // (a CTA of a pair has half of the tokens of K', a warp 8 of them, and half of the elements of V')
+            const int dw = warp - kDequant;
             const bool is_k = dw < 4;
+            const int sub = Pair && is_k ? 2 * static_cast<int>(rank) + (dw >> 1) : dw & 3;
             const int g = lane >> 2, t = lane & 3;
-            const uint32_t to_k0 = base + (sub * 16 + g) * 128;  // the row of token g
+            const uint32_t to_k0 = base + ((Pair ? sub & 1 : sub) * 16 + g) * 128;  // the row of token g
             // the 16 bytes that this lane addresses of the four 8 x 8 matrices of a V word: matrix lane / 8 (rows
             // 8 (m & 1) on, tokens 8 (m / 2) on), row lane % 8
             const uint32_t to_v0 = base + C::kOffV + (((lane >> 3) & 1) * 8 + (lane & 7)) * 128 +
@@ -702,7 +782,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(is_k ? s_full(buf) : pv_done(buf), (use & 1) ^ 1)) break;
                 if (is_k) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {  // tokens 8 h + g
+                    for (int half = 0; half < 2 / C::kCtas; ++half) {  // tokens 8 h + g
+                        const int h = Pair ? dw & 1 : half;
                         uint32_t pr[G], sc[G], mn[G];
                         lds_params<G>(tile + T::kKParams + (8 * h + g) * G * 4, pr);
                         if (there < 16) {
@@ -720,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             codes(word, q);
 #pragma unroll
                             for (int x = 0; x < 4; ++x) q[x] = hfma2(q[x], sc[y], mn[y]);
-                            sts128(to_k + h * 1024 + y * (kTok * 128) + (((2 * t + w) ^ g) << 4), q[0], q[1], q[2], q[3]);
+                            sts128(to_k + h * 1024 + y * (C::kTokCta * 128) + (((2 * t + w) ^ g) << 4), q[0], q[1], q[2], q[3]);
                         };
                         if constexpr (G == 1) {
                             const uint2 v = lds64(tile + (h * 32 + lane) * 8);
@@ -738,24 +819,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 } else {
-                    uint32_t pr[4][G];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+                    // groups y0 .. of the V codes, words x0 .. of each (heads of 64 have one group: half of its words)
+                    constexpr int kY = G == 1 ? 1 : G / C::kCtas, kX = Pair && G == 1 ? 2 : 4;
+                    const int y0 = G == 1 ? 0 : static_cast<int>(rank) * kY;
+                    uint32_t pr[4][kY];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int token = 2 * t + (k & 1) + 8 * (k >> 1);
-                        lds_params<G>(tile + T::kVParams + token * G * 4, pr[k]);
+                        lds_params<kY>(tile + T::kVParams + token * G * 4 + y0 * 4, pr[k]);
                         if (there < 16 && token >= there) {
 #pragma unroll
-                            for (int y = 0; y < G; ++y) pr[k][y] = 0;
+                            for (int y = 0; y < kY; ++y) pr[k][y] = 0;
                         }
                     }
 #pragma unroll
-                    for (int y = 0; y < G; ++y) {
+                    for (int y = 0; y < kY; ++y) {
                         const uint32_t sa = __byte_perm(pr[0][y], pr[1][y], 0x5410), ma = __byte_perm(pr[0][y], pr[1][y], 0x7632);
                         const uint32_t sb = __byte_perm(pr[2][y], pr[3][y], 0x5410), mb = __byte_perm(pr[2][y], pr[3][y], 0x7632);
-                        const uint4 v = lds128(tile + T::kV + y * 512 + lane * 16);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t w[4];
+                        if constexpr (kX == 4) {
+                            const uint4 v = lds128(tile + T::kV + (y0 + y) * 512 + lane * 16);
+                            w[0] = v.x;
+                            w[1] = v.y;
+                            w[2] = v.z;
+                            w[3] = v.w;
+                        } else {
+                            const uint2 v = lds64(tile + T::kV + lane * 16 + rank * 8);
+                            w[0] = v.x;
+                            w[1] = v.y;
+                        }
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
+                        for (int x = 0; x < kX; ++x) {
                             uint32_t q[4];
                             codes(w[x], q);
                             stmatrix4(to_v + (64 * y + 16 * x) * 128, hfma2(q[0], sa, ma), hfma2(q[1], sa, ma), hfma2(q[2], sb, mb),
@@ -766,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(is_k ? k_full(buf) : v_full(buf));
+                    arrive(is_k ? k_full(buf) : v_full(buf));
                     mbar_arrive(raw_empty(st));
                 }
             }
@@ -808,37 +902,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == kIssueS) {
             // ================= S = Q . K'^T
-            constexpr uint32_t idesc = idesc_f16_f32(128, kTok);
-            bool ok = wait(q_full, segment & 1);
+            constexpr uint32_t idesc = idesc_f16_f32(C::kUnitRows, kTok);
+            bool ok = rank == 0 && wait_all(q_full, segment & 1);
             for (int i = 0; i < nt && ok; ++i) {
                 const uint32_t it = done + i, buf = it & 1, use = it >> 1;
-                ok = wait(k_full(buf), use & 1) && wait(pv_done(buf), (use & 1) ^ 1);
+                ok = wait_all(k_full(buf), use & 1) && wait(pv_done(buf), (use & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t desc = smem_desc_sw128(base + buf * C::kBuf + (k / 4) * (kTok * 128)) + (k & 3) * 2;
-                        umma_f16_ts(tmem + C::kColS + buf * kTok, tmem + C::kColQ + 8 * k, desc, idesc, k > 0);
+                        const uint64_t desc = smem_desc_sw128(base + buf * C::kBuf + (k / 4) * (C::kTokCta * 128)) + (k & 3) * 2;
+                        multiply(tmem + C::kColS + buf * kTok, tmem + C::kColQ + 8 * k, desc, idesc, k > 0);
                     }
-                    umma_commit(s_full(buf));
+                    commit(s_full(buf));
                 }
                 __syncwarp();
             }
         } else {
             // ================= O += P . V'
-            constexpr uint32_t idesc = idesc_f16_f32(128, D);
-            for (int i = 0; i < nt; ++i) {
+            constexpr uint32_t idesc = idesc_f16_f32(C::kUnitRows, D);
+            for (int i = 0; i < nt && rank == 0; ++i) {
                 const uint32_t it = done + i, buf = it & 1, use = it >> 1;
-                if (!wait(v_full(buf), use & 1) || !wait(p_full(buf), use & 1)) break;
+                if (!wait_all(v_full(buf), use & 1) || !wait_all(p_full(buf), use & 1)) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k) {
                         const uint64_t desc = smem_desc_sw128(base + C::kOffV + buf * C::kBuf) + k * 2;
-                        umma_f16_ts(tmem, tmem + C::kColS + buf * kTok + 8 * k, desc, idesc, i > 0 || k > 0);
+                        multiply(tmem, tmem + C::kColS + buf * kTok + 8 * k, desc, idesc, i > 0 || k > 0);
                     }
-                    umma_commit(pv_done(buf));
+                    commit(pv_done(buf));
                 }
                 __syncwarp();
             }
@@ -846,15 +940,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         done += nt;
         ++segment;
 
-        if (cta1 - cta0 >= kJoinInPlace) {
+        if (parts > kJoinInPlace) {
             // ---- more parts than that: all threads of the last CTA add them from memory, in the same order
             __syncthreads();
-            if (*s_last && !*s_abort) {
+            if (*s_last && !*s_abort && rows > 0) {
                 __threadfence();
                 // What each part's rows are scaled by: six groups of threads, every sixth part each. (K' and V'
                 // are not in use: all their products are done.)
                 constexpr int kGroups = kThreads / kRows;
-                const int n = min(cta1, kKv4MaxPromptCtas - 1) - cta0 + 1;
+                const int n = parts;
                 float* s_f = reinterpret_cast<float*>(smem);  // [n][128]
                 // 8 elements of a row a thread, from four parts in one round of loads (the first one's before
                 // the factors are known)
@@ -864,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int c8 = x / rows, r = x - c8 * rows;
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
-                        const float4* from = reinterpret_cast<const float4*>(part_of(cta0, cta0 + min(c + h, n - 1)) + 2 * kRows) + r;
+                        const float4* from = reinterpret_cast<const float4*>(part_of(cta0, cta0 + C::kCtas * min(c + h, n - 1)) + 2 * kRows) + r;
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
                             a[h][k] = x < items && c + h < n ? __ldcg(from + (2 * c8 + k) * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -876,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float top = -INFINITY;
                     if (grp < kGroups) {
                         for (int c = grp; c < n; c += kGroups) {
-                            const float m = __ldcg(part_of(cta0, cta0 + c) + r);
+                            const float m = __ldcg(part_of(cta0, cta0 + C::kCtas * c) + r);
                             s_f[c * kRows + (tid & (kRows - 1))] = m;
                             top = fmaxf(top, m);
                         }
@@ -897,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < n; c += 4) {
                             float l[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) l[k] = c + k < n ? __ldcg(part_of(cta0, cta0 + c + k) + kRows + r) : 0.f;
+                            for (int k = 0; k < 4; ++k) l[k] = c + k < n ? __ldcg(part_of(cta0, cta0 + C::kCtas * (c + k)) + kRows + r) : 0.f;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) total = c + k < n ? fmaf(l[k], s_f[(c + k) * kRows + tid], total) : total;
                         }
@@ -949,33 +1043,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
         } else if (warp >= kIssueS) {
             const uint32_t bar = drained(warp - kIssueS);
-            if (elect_one()) umma_commit(bar);
+            if (rank == 0 && elect_one()) commit(bar);
             for (int n = 0; n < 65536 && !mbar_test_wait(bar, 0); ++n) {
             }
         }
     }
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    if constexpr (Pair) cluster_sync_all();  // (the other's products read this one's memory)
+    else __syncthreads();
     tc_fence_after();
-    if (warp == kProducer) tmem_dealloc(tmem, C::kCols);
+    if (warp == kProducer) {
+        if constexpr (Pair) tmem_pair_dealloc(tmem, C::kCols);
+        else tmem_dealloc(tmem, C::kCols);
+    }
 }
 
-template <int D>
+template <int D, bool Pair>
 cudaError_t launch_prompt(const Kv4AttnParams& p, const Kv4View& v, const LaunchCtx& ctx) {
-    using C = Prompt<D>;
-    cudaError_t e = cudaFuncSetAttribute(kv4_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    using C = Prompt<D, Pair>;
+    cudaError_t e = cudaFuncSetAttribute(kv4_prompt_kernel<D, Pair>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min(ctx.sm_count, kKv4MaxPromptCtas)), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min(ctx.sm_count, kKv4MaxPromptCtas) / C::kCtas * C::kCtas), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = ctx.stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C::kCtas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_prompt_kernel<D>, p, v, ctx.timeout_ns, ctx.status);
+    cfg.numAttrs = Pair ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kv4_prompt_kernel<D, Pair>, p, v, ctx.timeout_ns, ctx.status);
 }
 
 }  // namespace
@@ -985,10 +1088,11 @@ size_t kv4_prompt_workspace(int head_dim) {
 }
 
 cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4View& v, int head_dim, const LaunchCtx& ctx) {
+    const bool pair = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / v.kv_heads) > kRows;
     switch (head_dim) {
-        case 64: return launch_prompt<64>(p, v, ctx);
-        case 128: return launch_prompt<128>(p, v, ctx);
-        default: return launch_prompt<256>(p, v, ctx);
+        case 64: return pair ? launch_prompt<64, true>(p, v, ctx) : launch_prompt<64, false>(p, v, ctx);
+        case 128: return pair ? launch_prompt<128, true>(p, v, ctx) : launch_prompt<128, false>(p, v, ctx);
+        default: return pair ? launch_prompt<256, true>(p, v, ctx) : launch_prompt<256, false>(p, v, ctx);
     }
 }
 
