@@ -1,11 +1,15 @@
 // Attention over the 4-bit paged key/value cache for many query rows a sequence (prompt chunks, verify
 // steps of several positions): o = softmax(scale q k'^T) v' on the tcgen05 tensor cores.
 //
-// A work unit is 128 query rows of one key/value head of one sequence (row r: query r / group, head
+// A work unit is 128 or 256 query rows of one key/value head of one sequence (row r: query r / group, head
 // r % group, so that every head that shares the keys uses one read of them) against the sequence's tokens,
-// 64 at a time:
+// 64 at a time; for a CTA's 128 rows:
 //   S[128][64]  = Q[128][D] . K'[64][D]^T      A = Q in TMEM, B = K' in shared memory
 //   O[128][D]  += P[128][64] . V'[64][D]       A = P in TMEM (over S), B = V'^T in shared memory
+// 256 rows are two CTAs of a cluster (cta_group::2): each keeps its rows' Q, S, P and O, dequantises half of K' (32
+// tokens) and half of V' (D / 2 elements), and the first CTA issues the products of both. So a tile costs half the
+// dequantisation and half the shared-memory traffic a CTA (prompt chunk of 1024 queries x 20 heads behind 8192
+// tokens, 4 heads of 256: 163 us with one CTA, 141 with two).
 // K' and V' are the stored values rounded to fp16 once (fma(code, scale, min)), written by dequantisation
 // warps in the matrix instruction's 128-byte-swizzled layouts straight from the cache's lane order: a K
 // word is 16 bytes of one token's row, a V word four pairs of tokens in rows of elements. With Q in TMEM a
@@ -13,22 +17,22 @@
 // room for the dequantised stores; with Q in shared memory it would be 128 KB.
 //
 // Warps: 0-15 softmax, a quarter of a row a thread (the four warps of 32 rows meet at a barrier once a tile;
-// the row's reference moves, and O is rescaled in TMEM, only when a score exceeds it by 2^8); 16-23
-// dequantise a 16-token quarter of the tile's keys or values each; 24 fetches the cache's tiles by bulk
-// copies; 25 issues S, 26 issues PV. K', V' and S/P are double-buffered. What bounds a tile is the circle
-// S -> softmax -> PV -> S of its S/P buffer, so the softmax is spread over many warps for its latency
-// (a row in one thread: 283 us, in two 179, in four less; two groups of one-thread rows taking the even and
-// the odd tiles: 186).
+// the row's reference moves, and O is rescaled in TMEM, only when a score exceeds it by 2^8); then 8 (one CTA)
+// or 4 that dequantise a 16-token quarter of the tile's keys or values each, one that fetches the cache's tiles
+// by bulk copies, one that issues S and one that issues PV. K', V' and S/P are double-buffered. What bounds a
+// tile is the circle S -> softmax -> PV -> S of its S/P buffer and the softmax warps' own chain, 1500 cycles of
+// latencies, so the softmax is spread over many warps (a row in one thread: 283 us, in two 179, in four less; two
+// groups of one-thread rows taking the even and the odd tiles: 186, all then with one CTA).
 //
 // Work is a list of (unit, tile); every CTA takes an equal run. Units that a run's end cuts leave parts
 // (maximum, sum, unnormalised rows) in the workspace; the CTA that arrives last adds them, in CTA order, to
 // what it still has in TMEM. (Added from memory, its own part among them: 169 us for the chunk above, 163 so.
 // An SM reads parts at 45 to 60 GB/s, however many loads are under way.)
 //
-// Measured on one GB300: 1024 queries of 20 heads (4 of 256) behind 8192 tokens 162.6 us (183 GFLOP, 1,125 TFLOP/s,
-// 0.59 of the bf16 rate); 16 sequences of 1070 .. 8005 tokens with 8 .. 16 queries each 46.8 us (73.6 MB). A tile
-// of 64 tokens takes 1.05 us with full rows, of which its matrix instructions fill 0.55; 6000 warp instructions
-// at 2.8 a cycle are the rest: issue bounds the chunk, the dequantisation above all.
+// Measured on one GB300: 1024 queries of 20 heads (4 of 256) behind 8192 tokens 140.6 us (183 GFLOP, 1,298 TFLOP/s,
+// 0.68 of the bf16 rate); 16 sequences of 1070 .. 8005 tokens with 8 .. 16 queries each 46.8 us (73.6 MB). A tile
+// of 64 tokens takes 0.95 us with 256 rows on two CTAs, of which its matrix instructions fill 0.55, 0.85 with up
+// to 80 rows on one, where a tile's dequantisation (1400 cycles a warp) bounds it.
 #include <algorithm>
 
 #include "common.cuh"
@@ -47,10 +51,7 @@ constexpr int kUnitCost = 8;
 // Fewest tiles of a run: less makes more parts than it saves (24 queries of 20 heads behind 4096 tokens, 4 heads of
 // 256: 32.2 us with 4, 34.8 with 8, 37.3 with 12; behind 16384 53.4, 50.0, 50.9)
 constexpr int kMinRun = 6;
-constexpr int kDequant = 16;   // first warp of each role (softmax: 0)
-constexpr int kProducer = 24, kIssueS = 25;
-constexpr int kWarps = 27;     // (26: PV)
-constexpr int kThreads = kWarps * 32;
+constexpr int kDequant = 16;   // softmax warps; the dequantising ones follow, then the fetching one and the two issuers
 constexpr int kJoinInPlace = 8;  // most parts of a unit that its last CTA adds to its own in TMEM
 constexpr int kNotes = 16;     // tiles whose page validity is kept
 
@@ -59,6 +60,9 @@ struct Prompt {
     static constexpr int kCtas = Pair ? 2 : 1;            // of a cluster, on one unit
     static constexpr int kUnitRows = kRows * kCtas;
     static constexpr int kTokCta = kTok / kCtas;          // tokens of K' in a CTA (of V' it has D / kCtas elements)
+    // dequantising warps, half of them for keys (prompt chunk below, pair: 149 us with 8, 141 with 4)
+    static constexpr int kDeq = Pair ? 4 : 8;
+    static constexpr int kProducer = kDequant + kDeq, kIssueS = kProducer + 1, kThreads = (kProducer + 3) * 32;
     static constexpr int kRaw = kSub * Kv4<D>::kTileBytes;
     static constexpr int kRawStages = D == 256 ? 3 : 4;
     static constexpr int kBuf = kTok * D * 2 / kCtas;  // one K' or V' buffer
@@ -284,13 +288,13 @@ __device__ __forceinline__ bool warp_poll_cluster(uint32_t bar, uint32_t parity,
 }
 
 template <int D, bool Pair>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
     kv4_prompt_kernel(const Kv4AttnParams p, const Kv4View cache, uint64_t timeout_ns, unsigned* status) {
     using C = Prompt<D, Pair>;
     using T = Kv4<D>;
     using PromptSeq = PromptSeqOf<C::kUnitRows>;
     auto seq_of = [](const Kv4AttnParams& p, const Kv4View& c, int b) { return prompt_seq<C::kUnitRows>(p, c, b); };
-    constexpr int G = T::kGroups, R = C::kRawStages;
+    constexpr int G = T::kGroups, R = C::kRawStages, kProducer = C::kProducer, kIssueS = C::kIssueS, kThreads = C::kThreads;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
@@ -342,11 +346,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             for (int i = 0; i < R; ++i) {
                 mbar_init(raw_full(i), 1);
-                mbar_init(raw_empty(i), 8);
+                mbar_init(raw_empty(i), C::kDeq);
             }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(k_full(i), 4 * C::kCtas);
-                mbar_init(v_full(i), 4 * C::kCtas);
+                mbar_init(k_full(i), C::kDeq / 2 * C::kCtas);
+                mbar_init(v_full(i), C::kDeq / 2 * C::kCtas);
                 mbar_init(s_full(i), 1);
                 mbar_init(p_full(i), 16 * C::kCtas);
                 mbar_init(pv_done(i), 1);
@@ -762,28 +766,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
             }
         } else if (warp < kProducer) {
-            // ================= dequantise: keys or values of quarter `sub`
-            // (a CTA of a pair has half of the tokens of K', a warp 8 of them, and half of the elements of V')
+            // ================= dequantise: keys or values of a quarter of the tokens (of values, where a CTA has half
+            // of the elements, of two quarters)
             const int dw = warp - kDequant;
-            const bool is_k = dw < 4;
-            const int sub = Pair && is_k ? 2 * static_cast<int>(rank) + (dw >> 1) : dw & 3;
+            const bool is_k = dw < C::kDeq / 2;
+            constexpr int kValues = C::kCtas;
+            const int sub0 = is_k ? 2 * static_cast<int>(rank) + dw : (dw - C::kDeq / 2) * kValues;
             const int g = lane >> 2, t = lane & 3;
-            const uint32_t to_k0 = base + ((Pair ? sub & 1 : sub) * 16 + g) * 128;  // the row of token g
+            const uint32_t to_k0 = base + (dw * 16 + g) * 128;  // the row of token g
             // the 16 bytes that this lane addresses of the four 8 x 8 matrices of a V word: matrix lane / 8 (rows
             // 8 (m & 1) on, tokens 8 (m / 2) on), row lane % 8
             const uint32_t to_v0 = base + C::kOffV + (((lane >> 3) & 1) * 8 + (lane & 7)) * 128 +
-                                   (((2 * sub + (lane >> 4)) ^ (lane & 7)) << 4);
+                                   (((2 * sub0 + (lane >> 4)) ^ (lane & 7)) << 4);
+            const uint32_t to_v1 = to_v0 ^ 32u;  // of the quarter after an even one
             for (int i = 0; i < nt; ++i) {
                 const uint32_t it = done + i, st = it % R, buf = it & 1, use = it >> 1;
-                const uint32_t to_k = to_k0 + buf * C::kBuf, to_v = to_v0 + buf * C::kBuf;
+                const uint32_t to_k = to_k0 + buf * C::kBuf;
                 if (!wait(raw_full(st), (it / R) & 1)) break;
-                const uint32_t tile = base + C::kOffRaw + st * C::kRaw + sub * T::kTileBytes;
-                const int there = static_cast<int>((s_valid[it % kNotes] >> (8 * sub)) & 255u);
+                const uint32_t note = s_valid[it % kNotes];
                 if (!wait(is_k ? s_full(buf) : pv_done(buf), (use & 1) ^ 1)) break;
                 if (is_k) {
+                    const uint32_t tile = base + C::kOffRaw + st * C::kRaw + sub0 * T::kTileBytes;
+                    const int there = static_cast<int>((note >> (8 * sub0)) & 255u);
 #pragma unroll
-                    for (int half = 0; half < 2 / C::kCtas; ++half) {  // tokens 8 h + g
-                        const int h = Pair ? dw & 1 : half;
+                    for (int h = 0; h < 2; ++h) {  // tokens 8 h + g
                         uint32_t pr[G], sc[G], mn[G];
                         lds_params<G>(tile + T::kKParams + (8 * h + g) * G * 4, pr);
                         if (there < 16) {
@@ -819,41 +825,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 } else {
-                    // groups y0 .. of the V codes, words x0 .. of each (heads of 64 have one group: half of its words)
-                    constexpr int kY = G == 1 ? 1 : G / C::kCtas, kX = Pair && G == 1 ? 2 : 4;
-                    const int y0 = G == 1 ? 0 : static_cast<int>(rank) * kY;
-                    uint32_t pr[4][kY];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int token = 2 * t + (k & 1) + 8 * (k >> 1);
-                        lds_params<kY>(tile + T::kVParams + token * G * 4 + y0 * 4, pr[k]);
-                        if (there < 16 && token >= there) {
+                    for (int vs = 0; vs < kValues; ++vs) {
+                        const uint32_t tile = base + C::kOffRaw + st * C::kRaw + (sub0 + vs) * T::kTileBytes;
+                        const uint32_t to_v = (vs == 0 ? to_v0 : to_v1) + buf * C::kBuf;
+                        const int there = static_cast<int>((note >> (8 * (sub0 + vs))) & 255u);
+                        // groups y0 .. of the V codes, words x0 .. of each (heads of 64 have one group: half of its words)
+                        constexpr int kY = G == 1 ? 1 : G / C::kCtas, kX = Pair && G == 1 ? 2 : 4;
+                        const int y0 = G == 1 ? 0 : static_cast<int>(rank) * kY;
+                        uint32_t pr[4][kY];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-                            for (int y = 0; y < kY; ++y) pr[k][y] = 0;
-                        }
-                    }
+                        for (int k = 0; k < 4; ++k) {
+                            const int token = 2 * t + (k & 1) + 8 * (k >> 1);
+                            lds_params<kY>(tile + T::kVParams + token * G * 4 + y0 * 4, pr[k]);
+                            if (there < 16 && token >= there) {
 #pragma unroll
-                    for (int y = 0; y < kY; ++y) {
-                        const uint32_t sa = __byte_perm(pr[0][y], pr[1][y], 0x5410), ma = __byte_perm(pr[0][y], pr[1][y], 0x7632);
-                        const uint32_t sb = __byte_perm(pr[2][y], pr[3][y], 0x5410), mb = __byte_perm(pr[2][y], pr[3][y], 0x7632);
-                        uint32_t w[4];
-                        if constexpr (kX == 4) {
-                            const uint4 v = lds128(tile + T::kV + (y0 + y) * 512 + lane * 16);
-                            w[0] = v.x;
-                            w[1] = v.y;
-                            w[2] = v.z;
-                            w[3] = v.w;
-                        } else {
-                            const uint2 v = lds64(tile + T::kV + lane * 16 + rank * 8);
-                            w[0] = v.x;
-                            w[1] = v.y;
+                                for (int y = 0; y < kY; ++y) pr[k][y] = 0;
+                            }
                         }
 #pragma unroll
-                        for (int x = 0; x < kX; ++x) {
-                            uint32_t q[4];
-                            codes(w[x], q);
-                            stmatrix4(to_v + (64 * y + 16 * x) * 128, hfma2(q[0], sa, ma), hfma2(q[1], sa, ma), hfma2(q[2], sb, mb),
-                                      hfma2(q[3], sb, mb));
+                        for (int y = 0; y < kY; ++y) {
+                            const uint32_t sa = __byte_perm(pr[0][y], pr[1][y], 0x5410), ma = __byte_perm(pr[0][y], pr[1][y], 0x7632);
+                            const uint32_t sb = __byte_perm(pr[2][y], pr[3][y], 0x5410), mb = __byte_perm(pr[2][y], pr[3][y], 0x7632);
+                            uint32_t w[4];
+                            if constexpr (kX == 4) {
+                                const uint4 v = lds128(tile + T::kV + (y0 + y) * 512 + lane * 16);
+                                w[0] = v.x;
+                                w[1] = v.y;
+                                w[2] = v.z;
+                                w[3] = v.w;
+                            } else {
+                                const uint2 v = lds64(tile + T::kV + lane * 16 + rank * 8);
+                                w[0] = v.x;
+                                w[1] = v.y;
+                            }
+#pragma unroll
+                            for (int x = 0; x < kX; ++x) {
+                                uint32_t q[4];
+                                codes(w[x], q);
+                                stmatrix4(to_v + (64 * y + 16 * x) * 128, hfma2(q[0], sa, ma), hfma2(q[1], sa, ma), hfma2(q[2], sb, mb),
+                                          hfma2(q[3], sb, mb));
+                            }
                         }
                     }
                 }
@@ -1066,7 +1078,7 @@ cudaError_t launch_prompt(const Kv4AttnParams& p, const Kv4View& v, const Launch
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min(ctx.sm_count, kKv4MaxPromptCtas) / C::kCtas * C::kCtas), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = ctx.stream;
     cudaLaunchAttribute attr[2];
@@ -1088,7 +1100,13 @@ size_t kv4_prompt_workspace(int head_dim) {
 }
 
 cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4View& v, int head_dim, const LaunchCtx& ctx) {
-    const bool pair = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / v.kv_heads) > kRows;
+    // Two CTAs on 256 rows save 4 to 14 % of what one on 128 twice takes, and are worth no less for a half-empty last
+    // unit: an even number of 128-row units (one sequence of 4096, heads of 256, 4096 queries of 5 heads a key head:
+    // 189.9 us with one, 182.1 with two; 8 of 4096, 240 rows 48.3 | 45.7, heads of 64 95.1 | 91.4), or so many that
+    // the last does not count (300 rows, heads of 256: 36.0 | 33.1 one sequence, 63.4 | 64.6 eight; of 128 81.7 |
+    // 95.8, of 64 136.2 | 169.2).
+    const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / v.kv_heads), units = (rows + kRows - 1) / kRows;
+    const bool pair = units % 2 == 0 || units >= (head_dim == 256 ? 3 : 17);
     switch (head_dim) {
         case 64: return pair ? launch_prompt<64, true>(p, v, ctx) : launch_prompt<64, false>(p, v, ctx);
         case 128: return pair ? launch_prompt<128, true>(p, v, ctx) : launch_prompt<128, false>(p, v, ctx);
