@@ -287,8 +287,9 @@ def test_attention_repeats_bit_for_bit_and_on_another_stream(W, q_lens):
 
 
 @pytest.mark.parametrize("lens,q_lens,H,KV,D", [([14000], [3], 8, 1, 64), ([16000], [26], 5, 1, 256), ([12000], [17], 16, 2, 128),
-                                                ([5000, 4100, 70], [40, 9, 26], 10, 2, 256)],
-                         ids=["many64", "many256", "many128", "several"])
+                                                ([5000, 4100, 70], [40, 9, 26], 10, 2, 256), ([14000], [30], 5, 1, 256),
+                                                ([9000, 300], [20, 33], 16, 2, 64), ([4000, 4500], [50, 5], 8, 2, 128)],
+                         ids=["many64", "many256", "many128", "several", "pairs256", "pairs64", "pairs128"])
 def test_parts_of_long_units_are_added_alike_whoever_is_last(W, lens, q_lens, H, KV, D):
     """One unit's tokens in the hands of up to a dozen CTAs, which finish in any order."""
     b = Batch(W, 16, lens, q_lens, H, KV, D, 64)
