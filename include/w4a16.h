@@ -367,6 +367,16 @@ int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4
                         int B, int M, int max_q_len, int causal, float scale, uint16_t* out, float* lse,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* Failure reporting of the attention kernels, without a GPU fault. Both set W4A16_ERR_DEVICE_TIMEOUT in the
+ * device status word after the wait limit (w4a16_set_wait_timeout_ns) and leave the context usable.
+ * wait_timeout: one warp in a wait that nothing ends; mode 0: the kernels' suspending wait, 1: the one on
+ * arrivals of another CTA.
+ * withhold (debug-bounds build only, INVALID_ARG in the other): from now on every fetching warp of
+ * w4a16_kv4_attention leaves out its copy number `copy` (from 0; the tcgen05 kernel: of tile number `copy`)
+ * while the readers wait for it; -1: none. */
+int w4a16_kv4_selftest_wait_timeout(int mode, void* stream);
+int w4a16_kv4_selftest_withhold(int copy);
+
 /*
  * ---- After the output head: one token per row of fp16 logits, by a given uniform random number.
  * Tokens in the order of their logits, ties by lower index; NaN and -inf are never chosen.

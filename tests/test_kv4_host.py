@@ -177,3 +177,11 @@ def test_sampled_statement_refuses_wrong_tokens():
     s = ref.Sampled(x, 0.5, temperature=0.0)
     assert s.check(1, 1.0) and not s.check(4, 1.0)
     assert ref.Sampled(np.full(3, -np.inf, np.float16), 0.5).check(-1, 0)
+
+
+def test_selftest_refusals(W):
+    assert W.w4a16_kv4_selftest_wait_timeout(2) == W.ERR_INVALID_ARG and W.w4a16_kv4_selftest_wait_timeout(-1) == W.ERR_INVALID_ARG
+    assert W.w4a16_kv4_selftest_withhold(0) == W.ERR_INVALID_ARG  # only the index-checking build leaves copies out
+    debug = W.load_debug_bounds()
+    assert debug.w4a16_kv4_selftest_withhold(-2) == W.ERR_INVALID_ARG
+    assert debug.w4a16_kv4_selftest_withhold(3) == W.OK and debug.w4a16_kv4_selftest_withhold(-1) == W.OK

@@ -41,7 +41,8 @@ EXPORTED = [
     "w4a16_unrepack_nvfp4", "w4a16_gemm_nvfp4", "w4a16_gemm_nvfp4_ex", "w4a16_plan_for_nvfp4",
     "w4a16_quantize_x_int8", "w4a16_gemm_w4a8", "w4a16_gemm_w4a8_ex", "w4a16_plan_for_w4a8",
     "w4a16_quantize_gemm_w4a8", "w4a16_kv4_cache_bytes", "w4a16_kv4_append", "w4a16_kv4_load",
-    "w4a16_kv4_attention_workspace_bytes", "w4a16_kv4_attention", "w4a16_sample",
+    "w4a16_kv4_attention_workspace_bytes", "w4a16_kv4_attention", "w4a16_kv4_selftest_wait_timeout",
+    "w4a16_kv4_selftest_withhold", "w4a16_sample",
 ]
 
 
@@ -136,6 +137,10 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.w4a16_kv4_attention_workspace_bytes.argtypes = [I]
     lib.w4a16_kv4_attention.restype = I
     lib.w4a16_kv4_attention.argtypes = [P, L, I, C, P, I, P, P, I, I, I, I, F, P, P, P, S, P]
+    lib.w4a16_kv4_selftest_wait_timeout.restype = I
+    lib.w4a16_kv4_selftest_wait_timeout.argtypes = [I, P]
+    lib.w4a16_kv4_selftest_withhold.restype = I
+    lib.w4a16_kv4_selftest_withhold.argtypes = [I]
     lib.w4a16_sample.restype = I
     lib.w4a16_sample.argtypes = [P, L, I, I, P, P, P, P, P, P, P, P]
     return lib
@@ -459,6 +464,15 @@ def w4a16_kv4_attention(q: int, q_stride: int, heads: int, cache: KV4Desc, block
                         out: int, lse: int | None, workspace: int, workspace_bytes: int, stream: int | None) -> int:
     return lib.w4a16_kv4_attention(q, q_stride, heads, ctypes.byref(cache), block_table, max_pages, kv_len, q_start,
                                    B, M, max_q_len, causal, scale, out, lse, workspace, workspace_bytes, stream)
+
+
+def w4a16_kv4_selftest_wait_timeout(mode: int, stream: int | None = None) -> int:
+    return lib.w4a16_kv4_selftest_wait_timeout(int(mode), stream)
+
+
+def w4a16_kv4_selftest_withhold(copy: int) -> int:
+    """Of this build: INVALID_ARG but in the handle of load_debug_bounds()."""
+    return lib.w4a16_kv4_selftest_withhold(int(copy))
 
 
 def w4a16_sample(logits: int, stride: int, M: int, V: int, temperature: int | None, top_k: int | None,

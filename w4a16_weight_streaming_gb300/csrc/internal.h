@@ -136,6 +136,7 @@ struct Kv4AttnParams {
     int max_q_len;
     int causal;
     float scale;
+    int withhold;  // debug-bounds build: the copy that every warp which fetches leaves out, -1 for none
 };
 size_t kv4_attention_workspace(int head_dim);  // bytes; the same for every batch
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, const Kv4Cache& c, const LaunchCtx& ctx);

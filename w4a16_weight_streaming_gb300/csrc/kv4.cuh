@@ -90,6 +90,24 @@ __device__ __forceinline__ bool warp_suspend(uint32_t bar, uint32_t parity, vola
     }
 }
 
+// Wait for arrivals of the other CTA too (a suspended thread is not woken promptly by those: polled).
+__device__ __forceinline__ bool warp_poll_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns,
+                                                  unsigned* status) {
+    if (__all_sync(0xffffffffu, mbar_test_wait_cluster(bar, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t spin = 1;; ++spin) {
+        if (__all_sync(0xffffffffu, mbar_test_wait_cluster(bar, parity))) return true;
+        if ((spin & 255u) != 0u) continue;
+        bool over = *abort_flag != 0;
+        if (!over && global_timer_ns() - t0 > timeout_ns) {
+            record_error(status, kErrTimeout);
+            *abort_flag = 1;
+            over = true;
+        }
+        if (__any_sync(0xffffffffu, over)) return false;
+    }
+}
+
 // ---- kv4_prompt.cu: the tcgen05 kernel for many query rows a sequence.
 struct Kv4AttnParams;
 struct LaunchCtx;

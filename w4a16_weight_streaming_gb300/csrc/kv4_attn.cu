@@ -255,6 +255,7 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
     const int64_t per = s_plan[2];
     const bool chunked = s_first[3] != 0;
     uint32_t phase = 0;  // one bit per ring stage
+    int copies = 0;      // that the warp has asked for
     const uint64_t policy = policy_evict_first();
 
     const int first = *s_first;
@@ -323,7 +324,8 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
             there = from >= 0 ? there | (1u << st) : there & ~(1u << st);
             if (from >= 0 && lane == 0) {
                 mbar_arrive_expect_tx(bars + 8 * st, C::kTile);
-                bulk_g2s(ring + st * C::kTile, cache.pages + from, C::kTile, bars + 8 * st, policy);
+                if (!kDebugBounds || copies++ != p.withhold)
+                    bulk_g2s(ring + st * C::kTile, cache.pages + from, C::kTile, bars + 8 * st, policy);
             }
         };
         // ---- Q^T as the B operand (row g of the unit), times a power of two that brings the row's largest
@@ -408,10 +410,12 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
             const uint32_t tile_s = ring + st * C::kTile;
             if (have) {
                 if (!warp_suspend(bars + 8 * st, (phase >> st) & 1u, s_abort, timeout_ns, status)) {
-                    // give up: let the copies in flight land (bounded) before their memory is used again
-                    for (int k = 0; k < S; ++k)
-                        for (int n = 0; n < 65536 && !mbar_test_wait(bars + 8 * k, (phase >> k) & 1u); ++n) {
-                        }
+                    // Give up: let this warp's copies in flight (of tiles i .. i + S - 1) land, bounded, before their
+                    // memory is used for the parts or another CTA has it. The CTA ends with this unit.
+                    for (int j = 0, k = st; j < S && i + j < mine; ++j, k = k + 1 == S ? 0 : k + 1)
+                        if ((there >> k) & 1u)
+                            for (int n = 0; n < 65536 && !mbar_test_wait(bars + 8 * k, (phase >> k) & 1u); ++n) {
+                            }
                     break;
                 }
                 phase ^= 1u << st;
@@ -716,9 +720,12 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
                 }
             }
         }
+        // (waits run out before the warps join, so all threads read the same here; after one the ring's phases are
+        // those of the copies no longer: no further unit)
+        const bool over = chunked || *static_cast<volatile int*>(s_abort) != 0;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring is written by copies again
         __syncthreads();
-        if (chunked) break;
+        if (over) break;
     }
 }
 

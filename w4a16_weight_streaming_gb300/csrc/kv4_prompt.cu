@@ -269,24 +269,6 @@ __device__ __forceinline__ void tmem_pair_dealloc(uint32_t taddr, uint32_t ncols
 __device__ __forceinline__ void mbar_arrive_first(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_peer(bar, 0)) : "memory");
 }
-// Wait for arrivals of the other CTA too (a suspended thread is not woken promptly by those: polled).
-__device__ __forceinline__ bool warp_poll_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns,
-                                                  unsigned* status) {
-    if (__all_sync(0xffffffffu, mbar_test_wait_cluster(bar, parity))) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t spin = 1;; ++spin) {
-        if (__all_sync(0xffffffffu, mbar_test_wait_cluster(bar, parity))) return true;
-        if ((spin & 255u) != 0u) continue;
-        bool over = *abort_flag != 0;
-        if (!over && global_timer_ns() - t0 > timeout_ns) {
-            record_error(status, kErrTimeout);
-            *abort_flag = 1;
-            over = true;
-        }
-        if (__any_sync(0xffffffffu, over)) return false;
-    }
-}
-
 template <int D, bool Pair>
 __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
     kv4_prompt_kernel(const Kv4AttnParams p, const Kv4View cache, uint64_t timeout_ns, unsigned* status) {
@@ -907,7 +889,7 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
                     mbar_arrive_expect_tx(raw_full(st), static_cast<uint32_t>(__popc(have)) * T::kTileBytes);
                 }
                 __syncwarp();
-                if (mine)
+                if (mine && (!kDebugBounds || static_cast<int>(it) != p.withhold))
                     bulk_g2s(base + C::kOffRaw + st * C::kRaw + (lane % kSub) * T::kTileBytes, cache.pages + from, T::kTileBytes,
                              raw_full(st), policy);
                 issued = it + 1;
@@ -1045,8 +1027,8 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
                 }
             }
         }
-        __syncthreads();  // Q, O and the barriers' phases belong to the next segment from here on
-        if (*s_abort) break;
+        // Q, O and the barriers' phases belong to the next segment from here on (all threads leave, or none)
+        if (__syncthreads_or(*static_cast<volatile int*>(s_abort))) break;
     }
     if (*s_abort) {  // what is under way ends before the memory is given back (bounded)
         if (warp == kProducer) {

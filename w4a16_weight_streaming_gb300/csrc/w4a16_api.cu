@@ -15,6 +15,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "kv4.cuh"
 #include "w4a16.h"
 
 namespace w4a16 {
@@ -523,6 +524,24 @@ __global__ void wait_timeout_selftest_kernel(unsigned* status, uint64_t timeout_
     __syncwarp();
 }
 
+// The same for the attention kernels, in which whole warps wait: mode 0 their suspending wait, 1 the one on
+// arrivals of another CTA of the cluster.
+__global__ void kv4_wait_selftest_kernel(unsigned* status, uint64_t timeout_ns, int mode) {
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ int abort_flag;
+    const uint32_t b = smem_u32(&bar);
+    if (threadIdx.x == 0) {
+        mbar_init(b, 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncwarp();
+    if (mode == 0)
+        warp_suspend(b, 0, &abort_flag, timeout_ns, status);
+    else
+        warp_poll_cluster(b, 0, &abort_flag, timeout_ns, status);
+}
+
 // Moves the status word into `taken` and clears it in one atomic exchange, so that a timeout
 // recorded concurrently by a kernel on another stream is either taken now or left for the next read.
 __global__ void take_status_kernel(unsigned* status, unsigned* taken) { *taken = atomicExch(status, 0u); }
@@ -987,6 +1006,8 @@ size_t rows_bytes(int M, int64_t stride, int64_t width, size_t element) {
     return (static_cast<size_t>(M - 1) * static_cast<size_t>(stride) + static_cast<size_t>(width)) * element;
 }
 
+std::atomic<int> g_withhold{-1};  // of w4a16_kv4_selftest_withhold
+
 int launched(cudaError_t e) {
     if (e == cudaSuccess) return W4A16_OK;
     cudaGetLastError();
@@ -1103,13 +1124,27 @@ int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4
     DeviceInfo d;
     if (!device_info(&d)) return W4A16_ERR_CUDA;
     Kv4AttnParams p = {q, q_stride, block_table, kv_len, q_start, out, lse, workspace, B, M, heads, max_pages,
-                       max_q_len, causal, scale};
+                       max_q_len, causal, scale, g_withhold.load()};
     LaunchCtx ctx;
     ctx.stream = static_cast<cudaStream_t>(stream);
     ctx.status = d.status;
     ctx.timeout_ns = g_timeout_ns.load();
     ctx.sm_count = d.sm_count;
     return launched(launch_kv4_attention(p, c, ctx));
+}
+
+int w4a16_kv4_selftest_wait_timeout(int mode, void* stream) {
+    if (mode < 0 || mode > 1) return W4A16_ERR_INVALID_ARG;
+    DeviceInfo d;
+    if (!device_info(&d)) return W4A16_ERR_CUDA;
+    kv4_wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(d.status, g_timeout_ns.load(), mode);
+    return launched(cudaGetLastError());
+}
+
+int w4a16_kv4_selftest_withhold(int copy) {
+    if (!kDebugBounds || copy < -1) return W4A16_ERR_INVALID_ARG;
+    g_withhold.store(copy);
+    return W4A16_OK;
 }
 
 int w4a16_sample(const uint16_t* logits, int64_t stride, int M, int V, const float* temperature, const int32_t* top_k,
