@@ -444,3 +444,66 @@ def test_the_index_checking_build_runs_clean(W, wide):
     ok(W)
     assert torch.equal(out.view(torch.int16), normal.view(torch.int16))
     assert torch.equal(kv[0], k) and torch.equal(kv[1], v)
+
+
+class Sink:
+    """Sequences whose scores are exact: every key is 0 but that of one token, the same in all elements, and
+    every query is 1, so that one token stands `gap` powers of two above the others, which are alike. The
+    values' groups of 64 have gains of their own."""
+
+    def __init__(self, W, seed, lens, KV, D, gap, gains, sink_value=1.0, group=1):
+        rng = np.random.default_rng(seed)
+        self.scale = gap * np.log(2) / (0.25 * D)
+        need = [-(-n // 64) for n in lens]
+        self.cache = W.KV4Cache(sum(need), 64, KV, D)
+        self.cache.pages.fill_(0xFF)
+        self.table = np.full((len(lens), max(need)), -1, np.int32)
+        self.keys, self.values, self.magnitude, at = [], [], [], 0
+        gain = np.repeat(np.asarray(gains), 64)
+        for b, n in enumerate(lens):
+            self.table[b, :need[b]] = at + np.arange(need[b])
+            at += need[b]
+            one = rng.integers(0, n)
+            k = np.zeros((n, KV, D), np.float16)
+            k[one] = 0.25
+            v = ((rng.normal(size=(n, KV, D)) + 0.5 * rng.normal(size=(KV, D))) * gain).astype(np.float16)
+            v[one] = (v[one] * sink_value).astype(np.float16)
+            slots = self.table[b, np.arange(n) // 64] * 64 + np.arange(n) % 64
+            W.kv4_append(cuda(np.concatenate([k, v], axis=1).reshape(n, -1)), self.cache, cuda(slots.astype(np.int32)), heads=0)
+            self.keys.append(ref.store(k))
+            self.values.append(ref.store(v))
+            # |min| + 15 scale of each element's group: what the codes' and the minimums' parts are made of
+            g = self.values[-1].reshape(n, KV, D // 64, 64)
+            size = np.abs(g.min(-1, keepdims=True)) + (g.max(-1, keepdims=True) - g.min(-1, keepdims=True)) * 1.01
+            self.magnitude.append(np.broadcast_to(size, g.shape).reshape(n, KV, D))
+        self.lens, self.H = lens, KV * group
+        self.work = W.kv4_attention_workspace(self.cache)
+
+    def run(self, W, q_lens, pages=None):
+        q = np.ones((sum(q_lens), self.H, self.cache.head_dim), np.float16)
+        start = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+        table = self.table
+        if pages:
+            table = np.full((table.shape[0], pages), -1, np.int32)
+            table[:, :self.table.shape[1]] = self.table
+        out = W.kv4_attention(cuda(q), self.cache, cuda(table), cuda(np.array(self.lens, np.int32)), cuda(start), max(q_lens),
+                              self.work, scale=self.scale, causal=False)
+        ok(W)
+        one = [1] * len(self.lens)  # all queries of a sequence are alike
+        q1 = np.ones((len(self.lens), self.H, self.cache.head_dim), np.float16)
+        want, _, _ = ref.attention(q1, self.keys, self.values, one, self.scale, False)
+        size, _, _ = ref.attention(q1, self.keys, self.magnitude, one, self.scale, False)
+        plain, _, _ = ref.attention(q1, self.keys, [np.abs(v) for v in self.values], one, self.scale, False)
+        of = np.repeat(np.arange(len(self.lens)), q_lens)
+        return out, want[of], size[of], plain[of]
+
+
+@pytest.mark.parametrize("lens,KV,D,group", [([8192], 4, 256, 5), ([700], 1, 256, 8), ([777] * 40, 8, 128, 1), ([5000] * 3, 2, 128, 4),
+                                             ([1500] * 24, 4, 256, 2), ([3000], 2, 64, 4)])
+def test_one_query_keeps_groups_of_any_size_exact(W, lens, KV, D, group):
+    """One token has half of the weight. The decode kernel takes P times scale to 2^-18 of itself, a score of
+    13 in fp32 is off by 13 * 2^-22 or less and the exponential by 2^-22, sums by less: 2^-16 of what a group
+    of 64 is made of, beside the output's rounding to fp16. A group may be 2^12 times smaller than another."""
+    b = Sink(W, 40, lens, KV, D, 13, [1, 2.0 ** -8, 2.0 ** -12, 2.0 ** -4][:D // 64], group=group)
+    out, want, size, _ = b.run(W, [1] * len(lens))
+    close(out, want, 2.0 ** -11 * np.abs(want) + 2.0 ** -16 * size + 2.0 ** -25)

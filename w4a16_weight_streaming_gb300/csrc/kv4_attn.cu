@@ -7,14 +7,17 @@
 //   scores  S^T[16 tokens][8 rows]   = K codes [16 x D] . Q^T[D x 8]
 //   output  O^T[D][8 rows]          += V codes^T [D x 16] . P[16 x 8]
 // The codes go into the instruction as they are: a nibble in the low bits of an fp16 is the subnormal
-// code * 2^-24, exact, so a pair of operands costs one AND. (The nibbles one place up count 16 times: for
-// keys their elements of q are divided by 16, for values they are other rows of the output.) The
+// code * 2^-24, in those of a bf16 code * 2^-133, both exact, so a pair of operands costs one AND. (The
+// nibbles one place up count 16 times: for keys their elements of q are divided by 16, for values they are
+// other rows of the output. With them a bf16 leaves its subnormal numbers, at the same step.) The
 // parameters come in around the products, in fp32, per token t and group y of 64 elements:
 //   S_t  = sum_y scale_ty (sum_d q_d code_td) + min_ty (sum_d q_d)
 //   O_d  = sum_t (P_t scale_ty) code_td + sum_t P_t min_ty
-// P_t scale_ty goes into the instruction as two fp16 numbers, its rounding and what that left over: the
-// codes' part and the minimums' part of a value cancel where the value is small, so one rounding of P_t
-// scale_ty would be off by 2^-11 of the group's whole range. A power of two keeps both normal.
+// P_t scale_ty 2^100 goes into the instruction as two bf16 numbers, its rounding and what that left over, 2^-18
+// of itself or less: the codes' part and the minimums' part of a value cancel where the value is small, so one
+// rounding would be off by 2^-9 of the group's whole range. bf16, since its exponents reach every P times every
+// scale: with two fp16 numbers under a power of two of the warp's largest scale, what was below 2^-25 of that was
+// lost (the values of groups with 2^-12 of another group's scale were off by 9 %).
 //
 // Work is a list of (sequence, 8 rows, key/value head, 16-token tile); every CTA takes an equal share of
 // it, whatever the lengths, and its warps take the run's tiles in turn, each with a running maximum and
@@ -22,9 +25,9 @@
 // warp's own ring in shared memory. Runs that end inside a row group leave their part in the workspace;
 // the CTA that arrives last there adds the parts in CTA order.
 //
-// Measured on one GB300: one sequence of 131,072 tokens, 20 heads on 4 of 256, 41.3 us (151 MB, 3.7 TB/s, 0.54 of
-// the copy bandwidth); 64 sequences of up to 8192 tokens, 40 heads on 8 of 128, 79.1 us (304 MB, 3.8 TB/s, 0.57);
-// one sequence of 777 tokens 10.1 us, which is the kernel's start (4 us), a few tiles, and the adding of parts (3
+// Measured on one GB300: one sequence of 131,072 tokens, 20 heads on 4 of 256, 40.1 us (151 MB, 3.8 TB/s, 0.56 of
+// the copy bandwidth); 64 sequences of up to 8192 tokens, 40 heads on 8 of 128, 78.3 us (304 MB, 3.9 TB/s, 0.57);
+// one sequence of 777 tokens 9.9 us, which is the kernel's start (4 us), a few tiles, and the adding of parts (3
 // us). A tile is 380 warp instructions for D = 128 and 610 for 256; with the 16 warps that the registers leave room
 // for an SM issues 2.2 of 4 a cycle, its ALU busy half of the time: the issue of dependent instructions bounds
 // the long calls, not memory.
@@ -63,6 +66,11 @@ struct Decode {
     static constexpr int kPart = kRows * (D + 2);  // floats of one workspace part: m, l, then rows
 };
 
+// 2^100: P times scale, 2^22 at most, stays finite, and its product with a code of 2^-133 is a normal number down to
+// P scale = 2^-93
+constexpr float kUp = 1.2676506002282294e30f;
+constexpr float kDown = 8589934592.f;  // 2^33: 1 over what a code unit times kUp is
+
 constexpr int kMaxCtas = 640;
 constexpr size_t kCounterBytes = 4096;
 static_assert(kMaxCtas * 4 <= kCounterBytes, "a counter a CTA");
@@ -80,6 +88,20 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint3
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+__device__ __forceinline__ void mma16816_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// a, b as bf16, a in the low half
+__device__ __forceinline__ uint32_t pack_bf2(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ float lo_bf(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_bf(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -403,7 +425,6 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
 #pragma unroll
         for (int y = 0; y < G; ++y) om[y][0] = om[y][1] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-        float vmul = 1.f, vcap = 0.f;  // P scale is taken times vmul = 2^e; scales up to vcap fit
 
         for (int i = 0, st = 0; i < mine; ++i, st = st + 1 == S ? 0 : st + 1) {
             const bool have = (there >> st) & 1u;
@@ -490,23 +511,15 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
                     if (tok + g + 8 >= lim1) s[3] = -INFINITY;
                 }
                 // P may grow to 2^8 before the reference moves: most tiles rescale nothing. A score above that
-                // (or a scale that would not fit) anywhere in the warp: take the new maximum, rescale the sums.
-                __half2 big = __hmax2(*reinterpret_cast<const __half2*>(&vp[0][0]), *reinterpret_cast<const __half2*>(&vp[1][0]));
-#pragma unroll
-                for (int y = 1; y < G; ++y) {
-                    big = __hmax2(big, *reinterpret_cast<const __half2*>(&vp[0][y]));
-                    big = __hmax2(big, *reinterpret_cast<const __half2*>(&vp[1][y]));
-                }
-                float top = __low2float(big);
-                if (__any_sync(0xffffffffu, fmaxf(s[0], s[2]) > m0 + 8.f || fmaxf(s[1], s[3]) > m1 + 8.f || top > vcap)) {
+                // anywhere in the warp: take the new maximum, rescale the sums.
+                if (__any_sync(0xffffffffu, fmaxf(s[0], s[2]) > m0 + 8.f || fmaxf(s[1], s[3]) > m1 + 8.f)) {
                     float n0 = fmaxf(m0, fmaxf(s[0], s[2])), n1 = fmaxf(m1, fmaxf(s[1], s[3]));
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) {
                         n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
                         n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
                     }
-                    float r0 = m0 == n0 ? 1.f : ex2(m0 - n0), r1 = m1 == n1 ? 1.f : ex2(m1 - n1);
+                    const float r0 = m0 == n0 ? 1.f : ex2(m0 - n0), r1 = m1 == n1 ? 1.f : ex2(m1 - n1);
                     m0 = n0;
                     m1 = n1;
                     l0 *= r0;
@@ -515,17 +528,6 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
                     for (int y = 0; y < G; ++y) {
                         om[y][0] *= r0;
                         om[y][1] *= r1;
-                    }
-                    if (top > vcap) {
-                        // the largest scale becomes 1 .. 2: 2^8 P times scales up to 2^7 of it fit in fp16. Never
-                        // less than 2^-9, with which every finite scale does
-                        const int e = max(-(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127), -9);
-                        const float to = __uint_as_float(static_cast<uint32_t>(min(e, 100) + 127) << 23);
-                        const float f = to / vmul;
-                        vmul = to;
-                        vcap = 127.f / to;
-                        r0 *= f;
-                        r1 *= f;
                     }
 #pragma unroll
                     for (int x = 0; x < 4 * G; ++x) {
@@ -541,17 +543,15 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
                 l1 += p1 + p3;
 #pragma unroll
                 for (int y = 0; y < G; ++y) {
-                    const float sa = lo_f(vp[0][y]) * vmul, sb = lo_f(vp[1][y]) * vmul;
+                    const float sa = lo_f(vp[0][y]) * kUp, sb = lo_f(vp[1][y]) * kUp;
                     const float na = hi_f(vp[0][y]), nb = hi_f(vp[1][y]);
                     om[y][0] = fmaf(p0, na, fmaf(p2, nb, om[y][0]));
                     om[y][1] = fmaf(p1, na, fmaf(p3, nb, om[y][1]));
-                    const __half2 ha = __floats2half2_rn(p0 * sa, p1 * sa), hb = __floats2half2_rn(p2 * sb, p3 * sb);
-                    const __half2 la = __floats2half2_rn(fmaf(p0, sa, -__low2float(ha)), fmaf(p1, sa, -__high2float(ha)));
-                    const __half2 lb = __floats2half2_rn(fmaf(p2, sb, -__low2float(hb)), fmaf(p3, sb, -__high2float(hb)));
-                    const uint32_t b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&ha));
-                    const uint32_t b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&hb));
-                    const uint32_t e0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&la));
-                    const uint32_t e1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&lb));
+                    const uint32_t ha = pack_bf2(p0 * sa, p1 * sa), hb = pack_bf2(p2 * sb, p3 * sb);
+                    const uint32_t la = pack_bf2(fmaf(p0, sa, -lo_bf(ha)), fmaf(p1, sa, -hi_bf(ha)));
+                    const uint32_t lb = pack_bf2(fmaf(p2, sb, -lo_bf(hb)), fmaf(p3, sb, -hi_bf(hb)));
+                    const uint32_t b0 = transpose8x8(ha), b1 = transpose8x8(hb);
+                    const uint32_t e0 = transpose8x8(la), e1 = transpose8x8(lb);
                     const uint4 v = lds128(tile_s + T::kV + y * 512 + lane * 16);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -559,8 +559,8 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
                         // rows g: the low codes; rows g + 8: low + 16 high (the low ones are taken off at the end)
                         const uint32_t a1 = w[x] & 0x00FF00FFu, a3 = __byte_perm(w[x], 0u, 0x4341);
                         const uint32_t a0 = w[x] & 0x000F000Fu, a2 = a3 & 0x000F000Fu;
-                        mma16816(o[4 * y + x], a0, a1, a2, a3, b0, b1);
-                        mma16816(o[4 * y + x], a0, a1, a2, a3, e0, e1);
+                        mma16816_bf16(o[4 * y + x], a0, a1, a2, a3, b0, b1);
+                        mma16816_bf16(o[4 * y + x], a0, a1, a2, a3, e0, e1);
                     }
                 }
             }
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(Decode<D, Narrow>::kThreads, Decode<D, Narrow>
         }
         {
             const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - top0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - top1);
-            const float k0 = f0 * (16777216.f / vmul), k1 = f1 * (16777216.f / vmul);
+            const float k0 = f0 * kDown, k1 = f1 * kDown;
             float* part = reinterpret_cast<float*>(smem) + warp * kRows * C::kPitch;
 #pragma unroll
             for (int x = 0; x < 4 * G; ++x) {
