@@ -507,3 +507,15 @@ def test_one_query_keeps_groups_of_any_size_exact(W, lens, KV, D, group):
     b = Sink(W, 40, lens, KV, D, 13, [1, 2.0 ** -8, 2.0 ** -12, 2.0 ** -4][:D // 64], group=group)
     out, want, size, _ = b.run(W, [1] * len(lens))
     close(out, want, 2.0 ** -11 * np.abs(want) + 2.0 ** -16 * size + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("lens,q_lens,KV,D,group", [([16384], [20], 4, 256, 5), ([20000, 3000], [60, 60], 2, 256, 5), ([16000], [100], 1, 128, 4),
+                                                    ([9000] * 3, [300, 40, 2], 2, 64, 2), ([16384], [64], 2, 128, 4),
+                                                    ([2500] * 48, [20] * 48, 4, 256, 5), ([2000] * 80, [64] * 80, 2, 128, 4)])
+def test_many_queries_keep_the_weights_of_a_long_context(W, lens, q_lens, KV, D, group):
+    """One token whose value is 0 has nearly all of the weight, the others 2^-20.37 of it each. Keys are exact
+    in fp16; values, weights and the output are rounded to it once each, 2^-11 of themselves, and sums of up to
+    2000 products in fp32 are off by less than 2^-12."""
+    b = Sink(W, 41, lens, KV, D, 20.37, [1.0] * (D // 64), sink_value=0.0, group=group)
+    out, want, _, plain = b.run(W, q_lens, pages=2 ** 14)
+    close(out, want, 2.0 ** -11 * np.abs(want) + (2.0 ** -10 + 2.0 ** -12) * plain + 2.0 ** -25)

@@ -10,8 +10,9 @@
 // tokens) and half of V' (D / 2 elements), and the first CTA issues the products of both. So a tile costs half the
 // dequantisation and half the shared-memory traffic a CTA (prompt chunk of 1024 queries x 20 heads behind 8192
 // tokens, 4 heads of 256: 163 us with one CTA, 141 with two).
-// K' and V' are the stored values rounded to fp16 once (fma(code, scale, min)), written by dequantisation
-// warps in the matrix instruction's 128-byte-swizzled layouts straight from the cache's lane order: a K
+// K', V' and P are rounded to fp16 once each (2^-11 of themselves), which the decode kernel does not do: f16 is the
+// widest operand at this rate (tf32 has half of it and twice the shared memory, of which heads of 256 use all). The
+// row's sum takes P before its rounding. K' and V' are fma(code, scale, min), written by dequantisation warps in the matrix instruction's 128-byte-swizzled layouts straight from the cache's lane order: a K
 // word is 16 bytes of one token's row, a V word four pairs of tokens in rows of elements. With Q in TMEM a
 // tile reads 64 KB of operands from shared memory for 1077 cycles of tensor work (D = 256), which leaves
 // room for the dequantised stores; with Q in shared memory it would be 128 KB.
@@ -54,6 +55,9 @@ constexpr int kMinRun = 6;
 constexpr int kDequant = 16;   // softmax warps; the dequantising ones follow, then the fetching one and the two issuers
 constexpr int kJoinInPlace = 8;  // most parts of a unit that its last CTA adds to its own in TMEM
 constexpr int kNotes = 16;     // tiles whose page validity is kept
+// A weight of the row's reference is 2^kLift, so that with scores up to 2^8 above it fp16 is used to 2^15, and to
+// 2^-32 of the reference below (a long context beside one token that has nearly all of the weight).
+constexpr float kLift = 7.f;
 
 template <int D, bool Pair>
 struct Prompt {
@@ -551,7 +555,7 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
                         named_sync(1 + quad, 128);  // s_part may be written again
                         if (leave) break;
                     }
-                    const float sub = m == -INFINITY ? 0.f : m;
+                    const float sub = m == -INFINITY ? 0.f : m - kLift;
                     uint32_t pk[8];
                     uint64_t sum = 0;  // two fp32 sums
                     const uint64_t c2 = pair(c1, c1), sub2 = pair(-sub, -sub);
@@ -636,7 +640,7 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
                         __stcg(dst + r, m);
                         __stcg(dst + kRows + r, l);
                     } else if (p.lse != nullptr) {
-                        p.lse[q_row * p.heads + head] = l > 0.f ? 0.6931471805599453f * (m + log2f(l)) : -INFINITY;
+                        p.lse[q_row * p.heads + head] = l > 0.f ? 0.6931471805599453f * (m - kLift + log2f(l)) : -INFINITY;
                     }
                 }
                 tc_fence_before();
@@ -696,7 +700,7 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
                     }
                     s_join[kJoinInPlace * kRows + r] = total > 0.f ? 1.f / total : 0.f;
                     if (r < rows && p.lse != nullptr)
-                        p.lse[q_row * p.heads + head] = total > 0.f ? 0.6931471805599453f * (top + log2f(total)) : -INFINITY;
+                        p.lse[q_row * p.heads + head] = total > 0.f ? 0.6931471805599453f * (top - kLift + log2f(total)) : -INFINITY;
                 }
                 named_sync(1 + quad, 128);
                 tc_fence_after();
@@ -993,7 +997,7 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
                         if (p.lse != nullptr && tid < rows) {
                             const int in_seq = row0 + tid, pos = in_seq / sq.grp, hd = in_seq - pos * sq.grp;
                             p.lse[static_cast<int64_t>(sq.q0 + pos) * p.heads + kvh * sq.grp + hd] =
-                                total > 0.f ? 0.6931471805599453f * (top + log2f(total)) : -INFINITY;
+                                total > 0.f ? 0.6931471805599453f * (top - kLift + log2f(total)) : -INFINITY;
                         }
                     }
                     __syncthreads();
