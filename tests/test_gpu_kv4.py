@@ -519,3 +519,38 @@ def test_many_queries_keep_the_weights_of_a_long_context(W, lens, q_lens, KV, D,
     b = Sink(W, 41, lens, KV, D, 20.37, [1.0] * (D // 64), sink_value=0.0, group=group)
     out, want, _, plain = b.run(W, q_lens, pages=2 ** 14)
     close(out, want, 2.0 ** -11 * np.abs(want) + (2.0 ** -10 + 2.0 ** -12) * plain + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("q_len", [1, 40, 130], ids=["decode", "one_cta", "pair"])
+def test_a_sequence_of_nearly_2_31_tokens(W, q_len):
+    """The longest that a block table may hold: three pages, then one page again and again. Rows see 2^31 - 32
+    tokens or a few less, so what they see is known from four pages."""
+    KV, D, page = 1, 64, 32
+    rng = np.random.default_rng(42)
+    x = rng.normal(size=(4 * page, 2 * D)).astype(np.float16)
+    cache = W.KV4Cache(4, page, KV, D)
+    W.kv4_append(cuda(x), cache, cuda(np.arange(4 * page, dtype=np.int32)), heads=0)
+    k, v = ref.store(x[:, :D]).reshape(4, page, D), ref.store(x[:, D:]).reshape(4, page, D)
+    pages = 2 ** 31 // page - 1
+    n = pages * page
+    table = torch.zeros((1, pages), dtype=torch.int32, device="cuda")
+    table[0, :3] = torch.tensor([1, 2, 3], dtype=torch.int32)
+    q = rng.normal(size=(q_len, 1, D)).astype(np.float16)
+    lse = torch.empty((q_len, 1), device="cuda")
+    out = W.kv4_attention(cuda(q), cache, table, cuda(np.array([n], np.int32)), cuda(np.array([0, q_len], np.int32)), q_len,
+                          W.kv4_attention_workspace(cache), lse=lse)
+    ok(W)
+    p = np.exp(np.einsum("id,ptd->ipt", q[:, 0].astype(np.float64), k) / 8)
+    weight = np.ones((q_len, 4, page))
+    weight[:, 0] = pages - 3
+    for i in range(q_len):
+        for t in range(n - q_len + 1 + i, n):
+            weight[i, 0, t % page] -= 1
+    z = (weight * p).sum((1, 2))
+    want = np.einsum("ipt,ptd->id", weight * p, v) / z[:, None]
+    size = np.einsum("ipt,ptd->id", weight * p, np.abs(v)) / z[:, None]
+    # a thread's or accumulator's sum takes at most 2^25 tiles / 152 CTAs * 4 steps, 2^-24 of itself lost in each
+    lost = 2.0 ** 25 / 152 * 4 * 2.0 ** -24
+    scores = 2.0 ** -11 * 6.0 / 8 * np.abs(q[:, 0].astype(np.float64)).sum(-1)
+    assert (np.abs(lse[:, 0].cpu().numpy() - np.log(z)) <= scores + lost).all()
+    close(out[:, 0], want, 2.0 ** -10 * np.abs(want) + (2.0 ** -10 + 2 * scores[:, None] + lost) * size)

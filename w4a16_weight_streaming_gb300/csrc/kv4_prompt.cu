@@ -12,10 +12,11 @@
 // tokens, 4 heads of 256: 163 us with one CTA, 141 with two).
 // K', V' and P are rounded to fp16 once each (2^-11 of themselves), which the decode kernel does not do: f16 is the
 // widest operand at this rate (tf32 has half of it and twice the shared memory, of which heads of 256 use all). The
-// row's sum takes P before its rounding. K' and V' are fma(code, scale, min), written by dequantisation warps in the matrix instruction's 128-byte-swizzled layouts straight from the cache's lane order: a K
-// word is 16 bytes of one token's row, a V word four pairs of tokens in rows of elements. With Q in TMEM a
-// tile reads 64 KB of operands from shared memory for 1077 cycles of tensor work (D = 256), which leaves
-// room for the dequantised stores; with Q in shared memory it would be 128 KB.
+// row's sum takes P before its rounding. K' and V' are fma(code, scale, min), written by dequantisation warps in
+// the matrix instruction's 128-byte-swizzled layouts straight from the cache's lane order: a K word is 16 bytes of
+// one token's row, a V word four pairs of tokens in rows of elements. With Q in TMEM a tile reads 64 KB of
+// operands from shared memory for 1077 cycles of tensor work (D = 256), which leaves room for the dequantised
+// stores; with Q in shared memory it would be 128 KB.
 //
 // Warps: 0-15 softmax, a quarter of a row a thread (the four warps of 32 rows meet at a barrier once a tile;
 // the row's reference moves, and O is rescaled in TMEM, only when a score exceeds it by 2^8); then 8 (one CTA)
@@ -216,7 +217,8 @@ struct PromptSeqOf {
     // tiles of a row tile (its last row sees most); at least one, so that empty rows are written
     __device__ __forceinline__ int tiles(int rt, int causal) const {
         const int last = min(q_len * grp, (rt + 1) * kUnitRows) - 1;
-        return max(1, (seen(last, causal) + kTok - 1) / kTok);
+        const int most = seen(last, causal);
+        return most > 0 ? (most - 1) / kTok + 1 : 1;  // (no sum: a length may be next to 2^31)
     }
     // The work list's unit is 1 / grp of a token: row tile rt takes a fixed cost, then no less than its
     // tokens, grows by kUnitRows from one row tile to the next (causal), and so has a sum in closed form. Its
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
                     tmem_wait_ld();
                     const int tok = (t0 + i) * kTok + part * 16;
                     const int there = static_cast<int>((s_valid[it % kNotes] >> (8 * part)) & 255u);
-                    if (tok + 16 > lim_min || there != 16) {
+                    if (tok > lim_min - 16 || there != 16) {
                         const int most = min(there, lim - tok);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
@@ -870,13 +872,13 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
             for (int i = 0; i < nt; ++i) {
                 const uint32_t it = done + i, st = it % R;
                 if ((i & 7) == 0) {
-                    const int tok = (t0 + i) * kTok + lane * kKv4Tile;
-                    there = max(0, min(kKv4Tile, sq.n - tok));
+                    const int64_t tok = static_cast<int64_t>(t0 + i) * kTok + lane * kKv4Tile;
+                    there = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(kKv4Tile), sq.n - tok)));
                     from = -1;
                     if (there > 0 && i + lane / kSub < nt && in_bounds((tok >> cache.page_shift) < p.max_pages, status)) {
                         const int page = p.block_table[static_cast<int64_t>(b) * p.max_pages + (tok >> cache.page_shift)];
                         if (page >= 0 && page < cache.num_pages) {
-                            from = cache.tile_offset<D>(page, kvh, tok & ((1 << cache.page_shift) - 1));
+                            from = cache.tile_offset<D>(page, kvh, static_cast<int>(tok) & ((1 << cache.page_shift) - 1));
                             if (!in_bounds(from >= 0 && from + T::kTileBytes <= cache.bytes<D>(), status)) from = -1;
                         } else {
                             record_error(status, kErrBounds);
@@ -943,8 +945,8 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
             __syncthreads();
             if (*s_last && !*s_abort && rows > 0) {
                 __threadfence();
-                // What each part's rows are scaled by: six groups of threads, every sixth part each. (K' and V'
-                // are not in use: all their products are done.)
+                // What each part's rows are scaled by: kGroups groups of threads (6, of a pair 5), every kGroups-th
+                // part each. (K' and V' are not in use: all their products are done.)
                 constexpr int kGroups = kThreads / kRows;
                 const int n = parts;
                 float* s_f = reinterpret_cast<float*>(smem);  // [n][128]
