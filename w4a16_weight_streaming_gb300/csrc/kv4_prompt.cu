@@ -71,13 +71,16 @@ struct Prompt {
     static constexpr int kRaw = kSub * Kv4<D>::kTileBytes;
     static constexpr int kRawStages = D == 256 ? 3 : 4;
     static constexpr int kBuf = kTok * D * 2 / kCtas;  // one K' or V' buffer
-    static constexpr int kOffV = 2 * kBuf;
+    // K' (and V') buffers. A pair's take half of the memory, and four hide what handing one to the other CTA takes
+    // (prompt chunk below: 156 us with two)
+    static constexpr int kBufs = Pair ? 4 : 2;
+    static constexpr int kOffV = kBufs * kBuf;
     // (where the tiles are, a unit's parts are added: four slots or more of 16 elements of a part for every
     // softmax thread, or what up to kKv4MaxPromptCtas parts are scaled by, under the raw tiles)
     static constexpr int kOffRaw = 4 * 64 * kDequant * 32;
-    static_assert(4 * kBuf <= kOffRaw && kKv4MaxPromptCtas * kRows * 4 <= kOffRaw, "");
+    static_assert(2 * kBufs * kBuf <= kOffRaw && kKv4MaxPromptCtas * kRows * 4 <= kOffRaw, "");
     static constexpr int kOffBars = kOffRaw + kRawStages * kRaw;
-    static constexpr int kBars = 2 * kRawStages + 2 * 5 + 3;
+    static constexpr int kBars = 2 * kRawStages + 2 * 3 + 3 + (Pair ? 4 : 2) * kBufs;
     static constexpr int kOffMisc = kOffBars + kBars * 8;
     static constexpr int kJoin = (kJoinInPlace + 1) * kRows * 4;
     static constexpr int kSmem = kOffMisc + 256 + kJoin + 1024;  // + alignment
@@ -269,11 +272,10 @@ __device__ __forceinline__ void tmem_pair_alloc(uint32_t slot_smem, uint32_t nco
 __device__ __forceinline__ void tmem_pair_dealloc(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// Arrive at the first CTA's barrier. What precedes it is this SM's own shared memory and TMEM, complete after a
-// proxy fence or wait::st, and read by this SM's part of a product: a release at the cluster's scope, which waits 900
-// cycles here, is not needed.
+// Arrive at the first CTA's barrier after this thread's tcgen05 instructions (tcgen05.fence::before_thread_sync here,
+// after_thread_sync there order them; an arrival between the two need not release anything else).
 __device__ __forceinline__ void mbar_arrive_first(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_peer(bar, 0)) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_peer(bar, 0)) : "memory");
 }
 template <int D, bool Pair>
 __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
@@ -302,20 +304,28 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
     const uint32_t bars = base + C::kOffBars;
     auto raw_full = [&](int s) { return bars + 8 * s; };
     auto raw_empty = [&](int s) { return bars + 8 * (R + s); };
-    auto k_full = [&](int s) { return bars + 8 * (2 * R + s); };
-    auto v_full = [&](int s) { return bars + 8 * (2 * R + 2 + s); };
-    auto s_full = [&](int s) { return bars + 8 * (2 * R + 4 + s); };   // S in TMEM, K' free
-    auto p_full = [&](int s) { return bars + 8 * (2 * R + 6 + s); };
-    auto pv_done = [&](int s) { return bars + 8 * (2 * R + 8 + s); };  // O updated, V' and S/P free
-    const uint32_t q_full = bars + 8 * (2 * R + 10);
-    auto drained = [&](int i) { return bars + 8 * (2 * R + 11 + i); };  // the issuers' instructions, after a wait ran out
-    // A pair's barriers for what its products read are the first CTA's
+    auto s_full = [&](int s) { return bars + 8 * (2 * R + s); };       // S in TMEM
+    auto p_full = [&](int s) { return bars + 8 * (2 * R + 2 + s); };
+    auto pv_done = [&](int s) { return bars + 8 * (2 * R + 4 + s); };  // O updated, S/P free
+    const uint32_t q_full = bars + 8 * (2 * R + 6);
+    auto drained = [&](int i) { return bars + 8 * (2 * R + 7 + i); };  // the issuers' instructions, after a wait ran out
+    constexpr int KB = C::kBufs;
+    auto k_full = [&](int s) { return bars + 8 * (2 * R + 9 + s); };
+    auto v_full = [&](int s) { return bars + 8 * (2 * R + 9 + KB + s); };
+    // K' and V' are free again: with two buffers at the barriers of S and O
+    auto k_free = [&](int s) { return KB == 2 ? s_full(s) : bars + 8 * (2 * R + 9 + 2 * KB + s); };
+    auto v_free = [&](int s) { return KB == 2 ? pv_done(s) : bars + 8 * (2 * R + 9 + 3 * KB + s); };
+    // A pair's barriers for what its products read are the first CTA's. Of Q and P every warp arrives there itself. K'
+    // and V' are shared memory, which takes a release at the cluster's scope to be handed to another CTA's thread: that
+    // waits 900 cycles (with every warp's arrival a chunk took 186 us), so the second CTA's warps arrive at its own
+    // barrier, and its issuers, which have no products to issue, pass that on while the next tile is dequantised.
     const uint32_t rank = Pair ? cluster_ctarank() : 0u;
     const int team = static_cast<int>(blockIdx.x) / C::kCtas, teams = static_cast<int>(gridDim.x) / C::kCtas;
     auto arrive = [&](uint32_t bar) {
         if constexpr (Pair) mbar_arrive_first(bar);
         else mbar_arrive(bar);
     };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return warp_suspend(bar, parity, s_abort, timeout_ns, status); };
     auto wait_all = [&](uint32_t bar, uint32_t parity) {
         if constexpr (Pair) return warp_poll_cluster(bar, parity, s_abort, timeout_ns, status);
         else return warp_suspend(bar, parity, s_abort, timeout_ns, status);
@@ -324,11 +334,17 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
         if constexpr (Pair) umma_pair_f16_ts(d, a, desc, idesc, more);
         else umma_f16_ts(d, a, desc, idesc, more);
     };
+    // (the second CTA's issuers) the buffer is complete here: say so to the first CTA
+    auto pass_on = [&](uint32_t bar, uint32_t parity) {
+        if (!wait(bar, parity)) return false;
+        if (lane == 0) mbar_arrive_remote(bar, 0);
+        __syncwarp();
+        return true;
+    };
     auto commit = [&](uint32_t bar) {
         if constexpr (Pair) umma_pair_commit(bar);
         else umma_commit(bar);
     };
-    auto wait = [&](uint32_t bar, uint32_t parity) { return warp_suspend(bar, parity, s_abort, timeout_ns, status); };
 
     if (warp == kProducer) {
         if (lane == 0) {
@@ -337,11 +353,17 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
                 mbar_init(raw_empty(i), C::kDeq);
             }
             for (int i = 0; i < 2; ++i) {
-                mbar_init(k_full(i), C::kDeq / 2 * C::kCtas);
-                mbar_init(v_full(i), C::kDeq / 2 * C::kCtas);
                 mbar_init(s_full(i), 1);
                 mbar_init(p_full(i), 16 * C::kCtas);
                 mbar_init(pv_done(i), 1);
+            }
+            for (int i = 0; i < KB; ++i) {
+                mbar_init(k_full(i), C::kDeq / 2 + (Pair && rank == 0 ? 1 : 0));
+                mbar_init(v_full(i), C::kDeq / 2 + (Pair && rank == 0 ? 1 : 0));
+                if constexpr (KB > 2) {
+                    mbar_init(k_free(i), 1);
+                    mbar_init(v_free(i), 1);
+                }
             }
             mbar_init(q_full, 16 * C::kCtas);
             mbar_init(drained(0), 1);
@@ -768,11 +790,11 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
                                    (((2 * sub0 + (lane >> 4)) ^ (lane & 7)) << 4);
             const uint32_t to_v1 = to_v0 ^ 32u;  // of the quarter after an even one
             for (int i = 0; i < nt; ++i) {
-                const uint32_t it = done + i, st = it % R, buf = it & 1, use = it >> 1;
+                const uint32_t it = done + i, st = it % R, buf = it % KB, use = it / KB;
                 const uint32_t to_k = to_k0 + buf * C::kBuf;
                 if (!wait(raw_full(st), (it / R) & 1)) break;
                 const uint32_t note = s_valid[it % kNotes];
-                if (!wait(is_k ? s_full(buf) : pv_done(buf), (use & 1) ^ 1)) break;
+                if (!wait(is_k ? k_free(buf) : v_free(buf), (use & 1) ^ 1)) break;
                 if (is_k) {
                     const uint32_t tile = base + C::kOffRaw + st * C::kRaw + sub0 * T::kTileBytes;
                     const int there = static_cast<int>((note >> (8 * sub0)) & 255u);
@@ -860,7 +882,7 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-                    arrive(is_k ? k_full(buf) : v_full(buf));
+                    mbar_arrive(is_k ? k_full(buf) : v_full(buf));
                     mbar_arrive(raw_empty(st));
                 }
             }
@@ -903,36 +925,44 @@ __global__ void __launch_bounds__(Prompt<D, Pair>::kThreads, 1)
         } else if (warp == kIssueS) {
             // ================= S = Q . K'^T
             constexpr uint32_t idesc = idesc_f16_f32(C::kUnitRows, kTok);
+            if constexpr (Pair)
+                for (int i = 0; i < nt && rank != 0 && pass_on(k_full((done + i) % KB), (done + i) / KB & 1); ++i) {
+                }
             bool ok = rank == 0 && wait_all(q_full, segment & 1);
             for (int i = 0; i < nt && ok; ++i) {
-                const uint32_t it = done + i, buf = it & 1, use = it >> 1;
-                ok = wait_all(k_full(buf), use & 1) && wait(pv_done(buf), (use & 1) ^ 1);
+                const uint32_t it = done + i, buf = it & 1, use = it >> 1, kb = it % KB;
+                ok = wait_all(k_full(kb), it / KB & 1) && wait(pv_done(buf), (use & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t desc = smem_desc_sw128(base + buf * C::kBuf + (k / 4) * (C::kTokCta * 128)) + (k & 3) * 2;
+                        const uint64_t desc = smem_desc_sw128(base + kb * C::kBuf + (k / 4) * (C::kTokCta * 128)) + (k & 3) * 2;
                         multiply(tmem + C::kColS + buf * kTok, tmem + C::kColQ + 8 * k, desc, idesc, k > 0);
                     }
                     commit(s_full(buf));
+                    if constexpr (KB > 2) commit(k_free(kb));
                 }
                 __syncwarp();
             }
         } else {
             // ================= O += P . V'
             constexpr uint32_t idesc = idesc_f16_f32(C::kUnitRows, D);
+            if constexpr (Pair)
+                for (int i = 0; i < nt && rank != 0 && pass_on(v_full((done + i) % KB), (done + i) / KB & 1); ++i) {
+                }
             for (int i = 0; i < nt && rank == 0; ++i) {
-                const uint32_t it = done + i, buf = it & 1, use = it >> 1;
-                if (!wait_all(v_full(buf), use & 1) || !wait_all(p_full(buf), use & 1)) break;
+                const uint32_t it = done + i, buf = it & 1, use = it >> 1, kb = it % KB;
+                if (!wait_all(v_full(kb), it / KB & 1) || !wait_all(p_full(buf), use & 1)) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k) {
-                        const uint64_t desc = smem_desc_sw128(base + C::kOffV + buf * C::kBuf) + k * 2;
+                        const uint64_t desc = smem_desc_sw128(base + C::kOffV + kb * C::kBuf) + k * 2;
                         multiply(tmem, tmem + C::kColS + buf * kTok + 8 * k, desc, idesc, i > 0 || k > 0);
                     }
                     commit(pv_done(buf));
+                    if constexpr (KB > 2) commit(v_free(kb));
                 }
                 __syncwarp();
             }
