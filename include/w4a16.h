@@ -312,7 +312,7 @@ size_t w4a16_kv4_cache_bytes(int num_pages, int page_tokens, int kv_heads, int h
  * One pass over the rows of a fused qkv product: norms and rotation of each head, queries written out,
  * keys and values stored in the cache.
  *   qkv:       fp16 [M] rows of (heads + 2 kv_heads) * head_dim elements (query, key, value heads), rows
- *              qkv_stride elements apart (a multiple of 8)
+ *              qkv_stride elements apart (a multiple of 8; of one row anything)
  *   q_out:     fp16 [M][heads][head_dim], written in full; NULL when heads is 0 (rows of keys and values)
  *   slots:     int32 [M]; a negative slot stores nothing (a padding row); no slot twice
  *   positions: int32 [M], rows of the rotation table; NULL when rope is NULL
@@ -343,8 +343,8 @@ size_t w4a16_kv4_attention_workspace_bytes(int head_dim);
 
 /*
  * out = softmax(scale * q . k'^T) . v' over the cached tokens of each sequence.
- *   q:           fp16 [M][heads][head_dim], rows q_stride elements apart (a multiple of 8); head h
- *                attends with key/value head h / (heads / kv_heads)
+ *   q:           fp16 [M][heads][head_dim], rows q_stride elements apart (a multiple of 8; of one row
+ *                anything); head h attends with key/value head h / (heads / kv_heads)
  *   block_table: int32 [B][max_pages], page j of sequence b holds its tokens j * page_tokens and on
  *   kv_len:      int32 [B], cached tokens of each sequence (0 is allowed)
  *   q_start:     int32 [B + 1], not decreasing, within 0..M: sequence b's queries are rows

@@ -554,3 +554,20 @@ def test_a_sequence_of_nearly_2_31_tokens(W, q_len):
     scores = 2.0 ** -11 * 6.0 / 8 * np.abs(q[:, 0].astype(np.float64)).sum(-1)
     assert (np.abs(lse[:, 0].cpu().numpy() - np.log(z)) <= scores + lost).all()
     close(out[:, 0], want, 2.0 ** -10 * np.abs(want) + (2.0 ** -10 + 2 * scores[:, None] + lost) * size)
+
+
+def test_one_row_of_a_buffer_of_any_width(W):
+    b = Batch(W, 43, [50], [1], 4, 2, 64, 16)
+    rng = np.random.default_rng(44)
+    x = awkward(rng, 1, 8, 64)
+    slots = cuda(np.array([3], np.int32))
+    caches, outs = [W.KV4Cache(1, 16, 2, 64) for _ in range(2)], []
+    for cache, width in zip(caches, (512, 517)):
+        row = torch.zeros((1, width), dtype=torch.float16, device="cuda")
+        row[:, :512] = cuda(x)
+        q = W.kv4_append(row[:, :512], cache, slots, heads=4)
+        qrow = torch.zeros((1, width), dtype=torch.float16, device="cuda")
+        qrow[:, :256] = cuda(b.q.reshape(1, -1))
+        outs.append((q, *W.kv4_load(cache, slots), W.kv4_attention(qrow[:, :256].unflatten(1, (4, 64)), b.cache, **b.args())))
+    ok(W)
+    assert all(torch.equal(one, other) for one, other in zip(*outs))

@@ -1033,7 +1033,8 @@ int w4a16_kv4_append(const uint16_t* qkv, int64_t qkv_stride, int heads, uint16_
     if (rc != W4A16_OK) return rc;
     if (M > (1 << 20) || heads > 1024 || heads % c.kv_heads != 0) return W4A16_ERR_UNSUPPORTED_SHAPE;
     const int64_t width = static_cast<int64_t>(heads + 2 * c.kv_heads) * c.head_dim;
-    if (qkv_stride < width && M > 1) return W4A16_ERR_INVALID_ARG;
+    if (M == 1) qkv_stride = width;  // (of one row there is no distance)
+    if (qkv_stride < width) return W4A16_ERR_INVALID_ARG;
     if (qkv_stride % 8 != 0 || qkv_stride > (1LL << 32)) return W4A16_ERR_UNSUPPORTED_SHAPE;
     if (rope && (rot % 16 != 0 || rot > c.head_dim)) return W4A16_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(rope) || !aligned16(q_norm) || !aligned16(k_norm) ||
@@ -1094,7 +1095,8 @@ int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4
     if (static_cast<int64_t>(max_pages) * c.page_tokens >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED_SHAPE;
     if (static_cast<int64_t>(M) * heads > (1LL << 28)) return W4A16_ERR_UNSUPPORTED_SHAPE;
     const int64_t width = static_cast<int64_t>(heads) * c.head_dim;
-    if (q_stride < width && M > 1) return W4A16_ERR_INVALID_ARG;
+    if (M == 1) q_stride = width;
+    if (q_stride < width) return W4A16_ERR_INVALID_ARG;
     if (q_stride % 8 != 0 || q_stride > (1LL << 32)) return W4A16_ERR_UNSUPPORTED_SHAPE;
     if (workspace_bytes < kv4_attention_workspace(c.head_dim)) return W4A16_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned4(lse) || !aligned4(block_table) ||
