@@ -367,6 +367,17 @@ int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4
                         int B, int M, int max_q_len, int causal, float scale, uint16_t* out, float* lse,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* Which kernel w4a16_kv4_attention takes for these arguments (host only, lengths on the device play no part):
+ * the mma one in one CTA an SM (few work units) or several, the tcgen05 one with 128 rows a CTA or 256 a pair
+ * of CTAs. 0 for arguments that it would refuse. */
+typedef enum {
+    W4A16_KV4_DECODE_WIDE = 1,
+    W4A16_KV4_DECODE = 2,
+    W4A16_KV4_PROMPT = 3,
+    W4A16_KV4_PROMPT_PAIRS = 4
+} w4a16_kv4_kernel;
+int w4a16_kv4_attention_kernel(int heads, const w4a16_kv4_cache* cache, int max_pages, int B, int M, int max_q_len);
+
 /* Failure reporting of the attention kernels, without a GPU fault. Both set W4A16_ERR_DEVICE_TIMEOUT in the
  * device status word after the wait limit (w4a16_set_wait_timeout_ns) and leave the context usable.
  * wait_timeout: one warp in a wait that nothing ends; mode 0: the kernels' suspending wait, 1: the one on

@@ -571,3 +571,46 @@ def test_one_row_of_a_buffer_of_any_width(W):
         outs.append((q, *W.kv4_load(cache, slots), W.kv4_attention(qrow[:, :256].unflatten(1, (4, 64)), b.cache, **b.args())))
     ok(W)
     assert all(torch.equal(one, other) for one, other in zip(*outs))
+
+
+def batch_of(kind, B, rng, most_rows, most_tokens):
+    """(lens, q_lens) of a large batch. few: three sequences of rows, the others empty; gaps: runs of empty
+    sequences across the multiples of 32, sequences without rows and rows without tokens."""
+    lens, q_lens = [0] * B, [0] * B
+    for b in range(B):
+        if kind == "few":
+            busy = b in (3, 32, B - 1)
+            lens[b], q_lens[b] = (most_tokens - b, most_rows) if busy else (int(b % 5 == 0), 0)
+        elif not any(lo <= b < lo + 8 for lo in (28, 60, 92)):
+            lens[b] = int(rng.integers(0, most_tokens)) if b % 7 else 0
+            q_lens[b] = int(rng.integers(1, most_rows + 1)) if b % 5 else 0
+    q_lens[B - 1], lens[B - 1] = most_rows, most_tokens
+    return lens, q_lens
+
+
+# kernel (w4a16_kv4_kernel), kind, rows, tokens, H, KV, a table for longer sequences
+LARGE = {"decode-wide": (1, "few", 1, 3000, 8, 2, False), "decode": (2, "gaps", 1, 400, 16, 8, False),
+         "one-cta": (3, "gaps", 20, 300, 8, 2, True), "one-cta-few": (3, "few", 25, 3000, 4, 1, True),
+         "pairs": (4, "gaps", 40, 300, 8, 2, True), "pairs-few": (4, "few", 60, 3000, 4, 1, True)}
+
+
+@pytest.mark.parametrize("B,D", [(33, 64), (33, 128), (65, 256), (65, 64), (100, 128), (100, 256)])
+@pytest.mark.parametrize("case", LARGE)
+def test_batches_of_more_than_32_sequences(W, case, B, D):
+    kernel, kind, rows, tokens, H, KV, wide = LARGE[case]
+    rng = np.random.default_rng(B + D)
+    lens, q_lens = batch_of(kind, B, rng, rows, tokens)
+    b = Batch(W, B * D, lens, q_lens, H, KV, D, 16)
+    args = b.args(wide)
+    assert W.w4a16_kv4_attention_kernel(H, b.cache.desc, args["block_table"].shape[1], B, sum(q_lens), rows) == kernel
+    lse = torch.full((sum(q_lens), H), 7.0, device="cuda")
+    out = W.kv4_attention(cuda(b.q), b.cache, lse=lse, **args)
+    ok(W)
+    want, want_lse, bound = b.want(D ** -0.5)
+    close(out, want, bound)
+    got = lse.cpu().numpy().astype(np.float64)
+    empty = np.isneginf(want_lse)
+    assert np.array_equal(np.isneginf(got), empty)
+    tol = 2.0 ** -11 * D ** -0.5 * 6.0 * np.abs(b.q.astype(np.float64)).sum(-1) + 2.0 ** -18
+    assert (np.abs(got[~empty] - want_lse[~empty]) <= tol[~empty]).all()
+    assert int(b.work[:4096].sum()) == 0

@@ -185,3 +185,29 @@ def test_selftest_refusals(W):
     debug = W.load_debug_bounds()
     assert debug.w4a16_kv4_selftest_withhold(-2) == W.ERR_INVALID_ARG
     assert debug.w4a16_kv4_selftest_withhold(3) == W.OK and debug.w4a16_kv4_selftest_withhold(-1) == W.OK
+
+
+def test_choice_of_the_attention_kernel(W):
+    def choice(heads=20, pages=64, B=4, M=4, most=1, **kw):
+        return W.w4a16_kv4_attention_kernel(heads, desc(W, **kw), pages, B, M, most)
+
+    assert choice() == 1 and choice(B=64, M=64) == 2                       # one query: few units, many
+    assert choice(M=80, most=20, pages=4096) == 3                          # 100 rows a key head
+    assert choice(M=240, most=60, pages=4096, d=256) == 4                  # 300
+    assert choice(M=160, most=40, pages=4096) == 4 and choice(M=104, most=26, pages=4096) == 4
+    assert choice(M=100, most=25, pages=4096) == 3                         # 125 rows: one CTA's
+    for kw in (dict(heads=0), dict(heads=18), dict(heads=1028), dict(pages=0), dict(pages=1 << 28), dict(B=0), dict(M=0), dict(most=0),
+               dict(d=96), dict(t=24), dict(n=0), dict(h=0), dict(B=(1 << 20) + 1), dict(M=(1 << 20) + 1)):
+        assert choice(**kw) == 0, kw
+
+
+def test_every_attention_kernel_is_tested(W):
+    from test_gpu_kv4 import ATTENTION, LARGE
+
+    seen = set()
+    for lens, q_lens, H, KV, D, page in ATTENTION:
+        for wide in (0, 2 ** 20 // page):
+            pages = max(1, max(-(-n // page) for n in lens)) + wide
+            seen.add((W.w4a16_kv4_attention_kernel(H, desc(W, t=page, h=KV, d=D), pages, len(lens), sum(q_lens), max(1, max(q_lens))), D))
+    assert {k for k, _ in seen} == {1, 2, 3, 4}
+    assert {case[0] for case in LARGE.values()} == {1, 2, 3, 4}  # each with every head size; it asserts its kernel

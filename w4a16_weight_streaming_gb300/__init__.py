@@ -41,8 +41,8 @@ EXPORTED = [
     "w4a16_unrepack_nvfp4", "w4a16_gemm_nvfp4", "w4a16_gemm_nvfp4_ex", "w4a16_plan_for_nvfp4",
     "w4a16_quantize_x_int8", "w4a16_gemm_w4a8", "w4a16_gemm_w4a8_ex", "w4a16_plan_for_w4a8",
     "w4a16_quantize_gemm_w4a8", "w4a16_kv4_cache_bytes", "w4a16_kv4_append", "w4a16_kv4_load",
-    "w4a16_kv4_attention_workspace_bytes", "w4a16_kv4_attention", "w4a16_kv4_selftest_wait_timeout",
-    "w4a16_kv4_selftest_withhold", "w4a16_sample",
+    "w4a16_kv4_attention_workspace_bytes", "w4a16_kv4_attention", "w4a16_kv4_attention_kernel",
+    "w4a16_kv4_selftest_wait_timeout", "w4a16_kv4_selftest_withhold", "w4a16_sample",
 ]
 
 
@@ -137,6 +137,8 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.w4a16_kv4_attention_workspace_bytes.argtypes = [I]
     lib.w4a16_kv4_attention.restype = I
     lib.w4a16_kv4_attention.argtypes = [P, L, I, C, P, I, P, P, I, I, I, I, F, P, P, P, S, P]
+    lib.w4a16_kv4_attention_kernel.restype = I
+    lib.w4a16_kv4_attention_kernel.argtypes = [I, C, I, I, I, I]
     lib.w4a16_kv4_selftest_wait_timeout.restype = I
     lib.w4a16_kv4_selftest_wait_timeout.argtypes = [I, P]
     lib.w4a16_kv4_selftest_withhold.restype = I
@@ -464,6 +466,10 @@ def w4a16_kv4_attention(q: int, q_stride: int, heads: int, cache: KV4Desc, block
                         out: int, lse: int | None, workspace: int, workspace_bytes: int, stream: int | None) -> int:
     return lib.w4a16_kv4_attention(q, q_stride, heads, ctypes.byref(cache), block_table, max_pages, kv_len, q_start,
                                    B, M, max_q_len, causal, scale, out, lse, workspace, workspace_bytes, stream)
+
+
+def w4a16_kv4_attention_kernel(heads: int, cache: KV4Desc, max_pages: int, B: int, M: int, max_q_len: int) -> int:
+    return lib.w4a16_kv4_attention_kernel(heads, ctypes.byref(cache), max_pages, B, M, max_q_len)
 
 
 def w4a16_kv4_selftest_wait_timeout(mode: int, stream: int | None = None) -> int:

@@ -139,6 +139,8 @@ struct Kv4AttnParams {
     int withhold;  // debug-bounds build: the copy that every warp which fetches leaves out, -1 for none
 };
 size_t kv4_attention_workspace(int head_dim);  // bytes; the same for every batch
+// Which kernel takes the call (the pointers are not looked at): w4a16_kv4_attention_kernel's values.
+int kv4_attention_kernel(const Kv4AttnParams& p, const Kv4Cache& c, int sm_count);
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, const Kv4Cache& c, const LaunchCtx& ctx);
 
 // ---- sample.cu

@@ -113,6 +113,7 @@ struct Kv4AttnParams;
 struct LaunchCtx;
 constexpr int kKv4MaxPromptCtas = 160;
 size_t kv4_prompt_workspace(int head_dim);
-cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4View& v, int head_dim, const LaunchCtx& ctx);
+bool kv4_prompt_pairs(const Kv4AttnParams& p, int kv_heads, int head_dim);
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4View& v, int head_dim, bool pair, const LaunchCtx& ctx);
 
 }  // namespace w4a16

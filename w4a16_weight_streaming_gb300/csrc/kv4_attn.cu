@@ -36,6 +36,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "kv4.cuh"
+#include "w4a16.h"
 
 namespace w4a16 {
 namespace {
@@ -748,12 +749,14 @@ cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, const Launch
 }
 
 // Wide where half the SMs suffice for the work units, narrow otherwise.
+bool decode_is_wide(const Kv4AttnParams& p, int kv_heads, int sm_count) {
+    const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / kv_heads);
+    return 2 * std::min<int64_t>(p.B, p.M) * kv_heads * ((rows + kRows - 1) / kRows) <= sm_count;
+}
+
 template <int D>
-cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, const LaunchCtx& ctx) {
-    const int grp = p.heads / v.kv_heads;
-    const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * grp;
-    const int64_t units = std::min<int64_t>(p.B, p.M) * v.kv_heads * ((rows + kRows - 1) / kRows);
-    return 2 * units <= ctx.sm_count ? launch_decode<D, false>(p, v, ctx) : launch_decode<D, true>(p, v, ctx);
+cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, bool wide, const LaunchCtx& ctx) {
+    return wide ? launch_decode<D, false>(p, v, ctx) : launch_decode<D, true>(p, v, ctx);
 }
 
 // This kernel takes a pass over a sequence's tokens for every 8 query rows, the tcgen05 kernel one for every
@@ -764,7 +767,7 @@ cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, const Launch
 // 64, 20 rows 73.2 | 94.4, 40 rows 115.5 | 94.3; one sequence of 16384, heads of 256, 40 rows 31.5 | 34.4, 80 rows
 // 57.3 | 41.4. The choice costs 0.3 % over the better of the two on average, 17 % at most (1000 tokens, where both
 // take 20 to 35 us). The lengths are on the device: the block table's width stands for them.
-bool decode_is_faster(const Kv4AttnParams& p, const Kv4Cache& c) {
+bool decode_is_faster(const Kv4AttnParams& p, const Kv4Cache& c, int sm_count) {
     const double start_here = c.head_dim == 256 ? 11.2 : c.head_dim == 128 ? 10.0 : 8.5;
     const double start_there = c.head_dim == 256 ? 26.3 : c.head_dim == 128 ? 19.3 : 16.1;
     const double tile_here = c.head_dim == 256 ? 0.162 : c.head_dim == 128 ? 0.087 : 0.053;
@@ -772,8 +775,8 @@ bool decode_is_faster(const Kv4AttnParams& p, const Kv4Cache& c) {
     const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / c.kv_heads);
     const double heads = static_cast<double>(std::min(p.B, p.M)) * c.kv_heads;
     const double tokens = static_cast<double>(p.max_pages) * c.page_tokens;
-    const double here = start_here + tile_here / 152 * heads * static_cast<double>((rows + kRows - 1) / kRows) * (tokens / kKv4Tile);
-    const double there = start_there + tile_there / 152 * heads * static_cast<double>((rows + 127) / 128) * (tokens / 64);
+    const double here = start_here + tile_here / sm_count * heads * static_cast<double>((rows + kRows - 1) / kRows) * (tokens / kKv4Tile);
+    const double there = start_there + tile_there / sm_count * heads * static_cast<double>((rows + 127) / 128) * (tokens / 64);
     return here <= there;
 }
 
@@ -784,6 +787,11 @@ size_t kv4_attention_workspace(int head_dim) {
                     kCounterBytes + static_cast<size_t>(2 * kMaxCtas) * kRows * (head_dim + 2) * 4);
 }
 
+int kv4_attention_kernel(const Kv4AttnParams& p, const Kv4Cache& c, int sm_count) {
+    if (decode_is_faster(p, c, sm_count)) return decode_is_wide(p, c.kv_heads, sm_count) ? W4A16_KV4_DECODE_WIDE : W4A16_KV4_DECODE;
+    return kv4_prompt_pairs(p, c.kv_heads, c.head_dim) ? W4A16_KV4_PROMPT_PAIRS : W4A16_KV4_PROMPT;
+}
+
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, const Kv4Cache& c, const LaunchCtx& ctx) {
     Kv4View v;
     v.pages = static_cast<uint8_t*>(c.pages);
@@ -791,11 +799,14 @@ cudaError_t launch_kv4_attention(const Kv4AttnParams& p, const Kv4Cache& c, cons
     v.page_shift = 0;
     while ((1 << v.page_shift) < c.page_tokens) ++v.page_shift;
     v.kv_heads = c.kv_heads;
-    if (!decode_is_faster(p, c)) return launch_kv4_prompt(p, v, c.head_dim, ctx);
+    const int kernel = kv4_attention_kernel(p, c, ctx.sm_count);
+    if (kernel == W4A16_KV4_PROMPT || kernel == W4A16_KV4_PROMPT_PAIRS)
+        return launch_kv4_prompt(p, v, c.head_dim, kernel == W4A16_KV4_PROMPT_PAIRS, ctx);
+    const bool wide = kernel == W4A16_KV4_DECODE_WIDE;
     switch (c.head_dim) {
-        case 64: return launch_decode<64>(p, v, ctx);
-        case 128: return launch_decode<128>(p, v, ctx);
-        default: return launch_decode<256>(p, v, ctx);
+        case 64: return launch_decode<64>(p, v, wide, ctx);
+        case 128: return launch_decode<128>(p, v, wide, ctx);
+        default: return launch_decode<256>(p, v, wide, ctx);
     }
 }
 

@@ -1117,14 +1117,17 @@ size_t kv4_prompt_workspace(int head_dim) {
     return 4096 + static_cast<size_t>(2 * kKv4MaxPromptCtas) * kRows * (head_dim + 2) * 4;
 }
 
-cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4View& v, int head_dim, const LaunchCtx& ctx) {
-    // Two CTAs on 256 rows save 4 to 14 % of what one on 128 twice takes, and are worth no less for a half-empty last
-    // unit: an even number of 128-row units (one sequence of 4096, heads of 256, 4096 queries of 5 heads a key head:
-    // 189.9 us with one, 182.1 with two; 8 of 4096, 240 rows 48.3 | 45.7, heads of 64 95.1 | 91.4), or so many that
-    // the last does not count (300 rows, heads of 256: 36.0 | 33.1 one sequence, 63.4 | 64.6 eight; of 128 81.7 |
-    // 95.8, of 64 136.2 | 169.2).
-    const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / v.kv_heads), units = (rows + kRows - 1) / kRows;
-    const bool pair = units % 2 == 0 || units >= (head_dim == 256 ? 3 : 17);
+// Two CTAs on 256 rows save 4 to 14 % of what one on 128 twice takes, and are worth no less for a half-empty last
+// unit: an even number of 128-row units (one sequence of 4096, heads of 256, 4096 queries of 5 heads a key head:
+// 189.9 us with one, 182.1 with two; 8 of 4096, 240 rows 48.3 | 45.7, heads of 64 95.1 | 91.4), or so many that
+// the last does not count (300 rows, heads of 256: 36.0 | 33.1 one sequence, 63.4 | 64.6 eight; of 128 81.7 |
+// 95.8, of 64 136.2 | 169.2).
+bool kv4_prompt_pairs(const Kv4AttnParams& p, int kv_heads, int head_dim) {
+    const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / kv_heads), units = (rows + kRows - 1) / kRows;
+    return units % 2 == 0 || units >= (head_dim == 256 ? 3 : 17);
+}
+
+cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4View& v, int head_dim, bool pair, const LaunchCtx& ctx) {
     switch (head_dim) {
         case 64: return pair ? launch_prompt<64, true>(p, v, ctx) : launch_prompt<64, false>(p, v, ctx);
         case 128: return pair ? launch_prompt<128, true>(p, v, ctx) : launch_prompt<128, false>(p, v, ctx);

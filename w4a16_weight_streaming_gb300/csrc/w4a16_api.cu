@@ -999,6 +999,16 @@ int check_kv4_cache(const w4a16_kv4_cache* c, Kv4Cache* out) {
     return W4A16_OK;
 }
 
+int check_kv4_attention(int heads, const w4a16_kv4_cache* cache, int max_pages, int B, int M, int max_q_len, Kv4Cache* c) {
+    if (heads <= 0 || max_pages <= 0 || B <= 0 || M <= 0 || max_q_len <= 0) return W4A16_ERR_INVALID_ARG;
+    const int rc = check_kv4_cache(cache, c);
+    if (rc != W4A16_OK) return rc;
+    if (heads > 1024 || heads % c->kv_heads != 0 || B > (1 << 20) || M > (1 << 20)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<int64_t>(max_pages) * c->page_tokens >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (static_cast<int64_t>(M) * heads > (1LL << 28)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    return W4A16_OK;
+}
+
 size_t kv4_cache_size(const Kv4Cache& c) { return kv4_bytes(c.num_pages, c.page_tokens, c.kv_heads, c.head_dim); }
 
 // Bytes from the first element of the first row to the last of the last, rows `stride` elements apart.
@@ -1086,14 +1096,10 @@ int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4
                         int B, int M, int max_q_len, int causal, float scale, uint16_t* out, float* lse,
                         void* workspace, size_t workspace_bytes, void* stream) {
     if (!q || !block_table || !kv_len || !q_start || !out || !workspace) return W4A16_ERR_INVALID_ARG;
-    if (heads <= 0 || max_pages <= 0 || B <= 0 || M <= 0 || max_q_len <= 0) return W4A16_ERR_INVALID_ARG;
     if ((causal != 0 && causal != 1) || !std::isfinite(scale)) return W4A16_ERR_INVALID_ARG;
     Kv4Cache c;
-    const int rc = check_kv4_cache(cache, &c);
+    const int rc = check_kv4_attention(heads, cache, max_pages, B, M, max_q_len, &c);
     if (rc != W4A16_OK) return rc;
-    if (heads > 1024 || heads % c.kv_heads != 0 || B > (1 << 20) || M > (1 << 20)) return W4A16_ERR_UNSUPPORTED_SHAPE;
-    if (static_cast<int64_t>(max_pages) * c.page_tokens >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED_SHAPE;
-    if (static_cast<int64_t>(M) * heads > (1LL << 28)) return W4A16_ERR_UNSUPPORTED_SHAPE;
     const int64_t width = static_cast<int64_t>(heads) * c.head_dim;
     if (M == 1) q_stride = width;
     if (q_stride < width) return W4A16_ERR_INVALID_ARG;
@@ -1133,6 +1139,19 @@ int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4
     ctx.timeout_ns = g_timeout_ns.load();
     ctx.sm_count = d.sm_count;
     return launched(launch_kv4_attention(p, c, ctx));
+}
+
+int w4a16_kv4_attention_kernel(int heads, const w4a16_kv4_cache* cache, int max_pages, int B, int M, int max_q_len) {
+    Kv4Cache c;
+    if (check_kv4_attention(heads, cache, max_pages, B, M, max_q_len, &c) != W4A16_OK) return 0;
+    DeviceInfo d;
+    Kv4AttnParams p = {};
+    p.B = B;
+    p.M = M;
+    p.heads = heads;
+    p.max_pages = max_pages;
+    p.max_q_len = max_q_len;
+    return kv4_attention_kernel(p, c, device_info(&d) ? d.sm_count : 152);
 }
 
 int w4a16_kv4_selftest_wait_timeout(int mode, void* stream) {
