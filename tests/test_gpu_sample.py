@@ -226,3 +226,23 @@ def test_the_index_checking_build_gives_the_same(W):
     assert D.w4a16_device_status(s) == W.OK
     a, b = W.sample(x, u)
     assert torch.equal(a, tokens) and torch.equal(b, probs)
+
+
+@pytest.mark.parametrize("M,V", [(20, 262113), (19, 300000), (10, 600000), (19, 1000000)])
+def test_draws_from_below_the_window_of_long_rows(W, M, V):
+    """Vocabularies so long that four or eight CTAs a row could not count them in 16 bits, and draws far below
+    the largest logit, so that the counting kernel decides. A third of a row's tokens have one value: more than
+    65,536 of them, as many in a CTA's slice as it holds in the rows where they lie side by side."""
+    rng = np.random.default_rng(V)
+    x = np.clip(rng.normal(size=(M, V)), -3, 3).astype(np.float16) - np.float16(40)
+    for r in range(M):
+        if r % 2:
+            x[r, rng.choice(V, V // 3, replace=False)] = np.float16(-39.0)
+        else:
+            x[r, V // 3: 2 * (V // 3)] = np.float16(-39.0)
+        x[r, rng.integers(0, V)] = np.float16(30.0)  # the largest: the others are more than 4 octaves below
+    u = (1 - 2.0 ** -24 - rng.random(M) * 0.3).astype(np.float32)
+    for kw in (dict(temperature=50.0), dict(temperature=50.0, top_p=0.9), dict(temperature=80.0, top_k=V // 2)):
+        tokens, probs = draw(W, x, u, **kw)
+        for r in range(0, M, 3):  # (both kinds of rows; a row takes half a second)
+            assert Sampled(x[r], float(u[r]), **kw).check(tokens[r], probs[r]), (kw, r, tokens[r], probs[r])
