@@ -137,3 +137,63 @@ class Sampled:
         low = self.cdf[i] - p
         return self.w[i] > 0 and low - self.slack <= self.u <= self.cdf[i] + self.slack and \
             abs(prob - p) <= self.slack * p + 1e-12
+
+
+def rounded(x, bits):
+    """x to `bits` significant bits, to nearest even."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(np.ldexp(m, bits)), e - bits)
+
+
+class Pairs:
+    """Sequences of two tokens, in which a rounding of keys, values or weights shows: nothing averages it out.
+    kind "weights": keys are one number each, so scores are exact; "keys": all but two elements of a group of 64
+    are 7 steps of a full-width scale above 0, so that a rounding of k' is the same in all of them. Queries are
+    1 (a key head's `group` query heads alike)."""
+
+    D, SCALE = 128, 1.0 / 32
+
+    def __init__(self, kind, seed, B=96):
+        rng = np.random.default_rng(seed)
+        k = np.zeros((B, 2, self.D), F16)
+        if kind == "weights":
+            k[:, 1] = (rng.integers(4, 64, (B, 1)) / 64).astype(F16)
+        else:
+            scale = (rng.integers(1024, 2048, (B, 2)) / 2048).astype(F16)  # 11 significant bits
+            scale[:, 1] = (scale[:, 0].astype(np.float64) * (1 + rng.normal(size=B) / 64)).astype(F16)
+            k[..., 1::64] = (15 * scale.astype(np.float64)).astype(F16)[..., None]
+            # 7 steps of the scale that storage takes from a group's ends, 0 and its largest element
+            step = (k[..., 1].astype(F32) / F32(15)).astype(F16).astype(np.float64)
+            k[..., 2:64] = k[..., 66:128] = (7 * step).astype(F16)[..., None]
+        v = (rng.normal(size=(B, 2, self.D)) + rng.normal(size=(B, 1, self.D))).astype(F16)
+        self.k16, self.v16 = k, v
+        self.k, self.v = store(k), store(v)
+        g = self.v.reshape(B, 2, -1, 64)
+        self.low = np.broadcast_to(g.min(-1, keepdims=True), g.shape).reshape(self.v.shape)
+        size = np.abs(g.min(-1, keepdims=True)) + 1.01 * (g.max(-1, keepdims=True) - g.min(-1, keepdims=True))
+        self.p = self.weights(self.k)
+        self.want = self.mean(self.p, self.v)
+        plain, size = self.mean(self.p, np.abs(self.v)), self.mean(self.p, np.broadcast_to(size, g.shape).reshape(self.v.shape))
+        # what one rounding to fp16 of the output and of k', v' and the weights each may do (2^-11 of each; a score's
+        # error moves the output by no more than twice itself), and what the decode kernel's two numbers leave
+        e = self.SCALE * 2.0 ** -11 * np.abs(self.k).sum(-1).max(-1)[:, None] if kind == "keys" else 0.0
+        self.many = 2.0 ** -11 * np.abs(self.want) + 2.0 ** -25 + (2.0 ** -10 + 2 * e + 2.0 ** -18) * plain
+        self.one = 2.0 ** -11 * np.abs(self.want) + 2.0 ** -25 + 2.0 ** -16 * size
+
+    def weights(self, k):
+        s = self.SCALE * k.sum(-1)
+        return np.exp(s - s.max(-1, keepdims=True))
+
+    def mean(self, p, v, total=None):
+        return (p[..., None] * v).sum(1) / (p if total is None else total).sum(1)[:, None]
+
+    def many_with(self, keys, values, weights):
+        """The output of a kernel for many rows that rounds k', v' and the weights to so many bits."""
+        p = self.weights(rounded(self.k, keys))
+        return self.mean(rounded(p, weights), rounded(self.v, values), p).astype(F16).astype(np.float64)
+
+    def one_with(self, bits):
+        """The output of a kernel that rounds weights times scales to so many bits, beside the minimums in full."""
+        step = np.maximum(self.v - self.low, 0)
+        return (self.mean(self.p, self.low) + self.mean(rounded(self.p, bits), step)).astype(F16).astype(np.float64) \
+            if bits < 24 else self.want.astype(F16).astype(np.float64)

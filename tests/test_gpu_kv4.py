@@ -614,3 +614,25 @@ def test_batches_of_more_than_32_sequences(W, case, B, D):
     tol = 2.0 ** -11 * D ** -0.5 * 6.0 * np.abs(b.q.astype(np.float64)).sum(-1) + 2.0 ** -18
     assert (np.abs(got[~empty] - want_lse[~empty]) <= tol[~empty]).all()
     assert int(b.work[:4096].sum()) == 0
+
+
+@pytest.mark.parametrize("kind", ["weights", "keys"])
+@pytest.mark.parametrize("kernel,q_len", [(2, 1), (2, 30), (3, 10), (4, 40)])
+def test_no_bit_is_lost_that_the_kernels_say_they_keep(W, kernel, q_len, kind):
+    """Two tokens, so that nothing averages a rounding out; a test without a GPU shows what breaks the bounds."""
+    p, group = ref.Pairs(kind, 1), 4
+    B, D = p.k.shape[0], p.D
+    cache = W.KV4Cache(B, 16, 1, D)
+    slots = (np.arange(B)[:, None] * 16 + np.arange(2)).reshape(-1).astype(np.int32)
+    W.kv4_append(cuda(np.concatenate([p.k16, p.v16], axis=2).reshape(2 * B, 2 * D)), cache, cuda(slots), heads=0)
+    table = np.full((B, 2 ** 16 if kernel > 2 else 1), -1, np.int32)
+    table[:, 0] = np.arange(B)
+    rows = [q_len] + [1] * (B - 1)
+    start = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    q = np.ones((sum(rows), group, D), np.float16)
+    assert W.w4a16_kv4_attention_kernel(group, cache.desc, table.shape[1], B, sum(rows), q_len) == kernel
+    out = W.kv4_attention(cuda(q), cache, cuda(table), cuda(np.full(B, 2, np.int32)), cuda(start), q_len, W.kv4_attention_workspace(cache),
+                          scale=p.SCALE, causal=False)
+    ok(W)
+    of = np.repeat(np.arange(B), rows)
+    close(out, np.repeat(p.want[of][:, None], group, 1), np.repeat((p.one if kernel < 3 else p.many)[of][:, None], group, 1))

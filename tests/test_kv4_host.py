@@ -211,3 +211,16 @@ def test_every_attention_kernel_is_tested(W):
             seen.add((W.w4a16_kv4_attention_kernel(H, desc(W, t=page, h=KV, d=D), pages, len(lens), sum(q_lens), max(1, max(q_lens))), D))
     assert {k for k, _ in seen} == {1, 2, 3, 4}
     assert {case[0] for case in LARGE.values()} == {1, 2, 3, 4}  # each with every head size; it asserts its kernel
+
+
+def test_the_precision_bounds_see_a_lost_bit():
+    """Three bits fewer than fp16 has, of the keys, the values or the weights, and one rounding of the decode
+    kernel's products instead of two: each breaks its bound somewhere; what the kernels do keeps it."""
+    worst = lambda p, got, bound: float((np.abs(got - p.want) / bound).max())  # noqa: E731
+    weights, keys = ref.Pairs("weights", 1), ref.Pairs("keys", 1)
+    for p in (weights, keys):
+        assert worst(p, p.many_with(11, 11, 11), p.many) < 1 and worst(p, p.one_with(16), p.one) < 1
+        assert worst(p, p.one_with(11), p.one) > 1.5
+    assert worst(weights, weights.many_with(11, 8, 11), weights.many) > 2
+    assert worst(weights, weights.many_with(11, 11, 8), weights.many) > 2
+    assert worst(keys, keys.many_with(8, 11, 11), keys.many) > 2
