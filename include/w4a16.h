@@ -296,6 +296,7 @@ int w4a16_plan_for_w4a8(int M, int N, int K, int group, w4a16_plan* out);
  *
  * Supported: head_dim 64, 128, 256; page_tokens a power of two, 16..4096; num_pages * page_tokens < 2^31;
  * kv_heads <= 256; heads (of queries) a multiple of kv_heads, heads <= 1024; pages 16-byte aligned.
+ * These calls and w4a16_sample refuse memory of another GPU than the current one (INVALID_ARG).
  */
 typedef struct {
     void* pages;     /* device memory, w4a16_kv4_cache_bytes */

@@ -636,3 +636,17 @@ def test_no_bit_is_lost_that_the_kernels_say_they_keep(W, kernel, q_len, kind):
     ok(W)
     of = np.repeat(np.arange(B), rows)
     close(out, np.repeat(p.want[of][:, None], group, 1), np.repeat((p.one if kernel < 3 else p.many)[of][:, None], group, 1))
+
+
+def test_host_memory_is_refused(W):
+    b = Batch(W, 45, [20], [1], 4, 2, 64, 16)
+    args = b.args()
+    q, out = cuda(b.q), torch.empty((1, 4, 64), dtype=torch.float16, device="cuda")
+    base = dict(q=q, table=args["block_table"], kv=args["kv_len"], start=args["q_start"], out=out, work=b.work)
+    for name in base:
+        t = dict(base)
+        t[name] = base[name].cpu().pin_memory()
+        assert W.w4a16_kv4_attention(t["q"].data_ptr(), 256, 4, b.cache.desc, t["table"].data_ptr(), 2, t["kv"].data_ptr(),
+                                     t["start"].data_ptr(), 1, 1, 1, 1, 0.1, t["out"].data_ptr(), None, t["work"].data_ptr(),
+                                     t["work"].numel(), None) == W.ERR_INVALID_ARG, name
+    ok(W)

@@ -974,6 +974,17 @@ namespace {
 
 using namespace w4a16;
 
+// Host memory, or device memory of another GPU than the current one, on whose streams a call's kernels run.
+bool elsewhere(const void* p) {
+    cudaPointerAttributes a;
+    int dev = 0;
+    if (cudaPointerGetAttributes(&a, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return a.type == cudaMemoryTypeHost || (a.type == cudaMemoryTypeDevice && a.device != dev);
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int check_kv4_shape(int num_pages, int page_tokens, int kv_heads, int head_dim) {
@@ -1056,9 +1067,9 @@ int w4a16_kv4_append(const uint16_t* qkv, int64_t qkv_stride, int heads, uint16_
     if (heads > 0 && (overlaps(qkv, in_b, q_out, out_b) || overlaps(q_out, out_b, c.pages, kv_b) ||
                       overlaps(slots, row_b, q_out, out_b) || (positions && overlaps(positions, row_b, q_out, out_b))))
         return W4A16_ERR_INVALID_ARG;
-    if (is_host_pointer(qkv) || is_host_pointer(c.pages) || is_host_pointer(slots) ||
-        (heads > 0 && is_host_pointer(q_out)) || (rope && (is_host_pointer(rope) || is_host_pointer(positions))) ||
-        (q_norm && is_host_pointer(q_norm)) || (k_norm && is_host_pointer(k_norm)))
+    if (elsewhere(qkv) || elsewhere(c.pages) || elsewhere(slots) ||
+        (heads > 0 && elsewhere(q_out)) || (rope && (elsewhere(rope) || elsewhere(positions))) ||
+        (q_norm && elsewhere(q_norm)) || (k_norm && elsewhere(k_norm)))
         return W4A16_ERR_INVALID_ARG;
     DeviceInfo d;
     if (!device_info(&d)) return W4A16_ERR_CUDA;
@@ -1079,7 +1090,7 @@ int w4a16_kv4_load(const w4a16_kv4_cache* cache, const int32_t* slots, uint16_t*
     if (overlaps(k, b, v, b) || overlaps(k, b, c.pages, kv_b) || overlaps(v, b, c.pages, kv_b) ||
         overlaps(slots, row_b, k, b) || overlaps(slots, row_b, v, b))
         return W4A16_ERR_INVALID_ARG;
-    if (is_host_pointer(slots) || is_host_pointer(k) || is_host_pointer(v) || is_host_pointer(c.pages))
+    if (elsewhere(slots) || elsewhere(k) || elsewhere(v) || elsewhere(c.pages))
         return W4A16_ERR_INVALID_ARG;
     DeviceInfo d;
     if (!device_info(&d)) return W4A16_ERR_CUDA;
@@ -1121,14 +1132,14 @@ int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4
                             {q_start, (static_cast<size_t>(B) + 1) * 4}};
     for (int i = 0; i < 3; ++i) {
         if (!written[i].p) continue;
-        if (is_host_pointer(written[i].p)) return W4A16_ERR_INVALID_ARG;
+        if (elsewhere(written[i].p)) return W4A16_ERR_INVALID_ARG;
         for (int j = 0; j < i; ++j)
             if (overlaps(written[i].p, written[i].n, written[j].p, written[j].n)) return W4A16_ERR_INVALID_ARG;
         for (const Buffer& r : read)
             if (overlaps(written[i].p, written[i].n, r.p, r.n)) return W4A16_ERR_INVALID_ARG;
     }
     for (const Buffer& r : read)
-        if (is_host_pointer(r.p)) return W4A16_ERR_INVALID_ARG;
+        if (elsewhere(r.p)) return W4A16_ERR_INVALID_ARG;
     DeviceInfo d;
     if (!device_info(&d)) return W4A16_ERR_CUDA;
     Kv4AttnParams p = {q, q_stride, block_table, kv_len, q_start, out, lse, workspace, B, M, heads, max_pages,
@@ -1181,12 +1192,12 @@ int w4a16_sample(const uint16_t* logits, int64_t stride, int M, int V, const flo
     if (probs && overlaps(tokens, row_b, probs, row_b)) return W4A16_ERR_INVALID_ARG;
     for (int i = 0; i < 6; ++i) {
         if (!read[i]) continue;
-        if (is_host_pointer(read[i])) return W4A16_ERR_INVALID_ARG;
+        if (elsewhere(read[i])) return W4A16_ERR_INVALID_ARG;
         for (const void* w : written)
             if (w && overlaps(read[i], i == 0 ? in_b : row_b, w, row_b)) return W4A16_ERR_INVALID_ARG;
     }
     for (const void* w : written)
-        if (w && is_host_pointer(w)) return W4A16_ERR_INVALID_ARG;
+        if (w && elsewhere(w)) return W4A16_ERR_INVALID_ARG;
     DeviceInfo d;
     if (!device_info(&d)) return W4A16_ERR_CUDA;
     SampleParams p = {logits, stride, temperature, top_k, top_p, min_p, u, tokens, probs, M, V};
