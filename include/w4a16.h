@@ -368,15 +368,25 @@ int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4
                         int B, int M, int max_q_len, int causal, float scale, uint16_t* out, float* lse,
                         void* workspace, size_t workspace_bytes, void* stream);
 
-/* Which kernel w4a16_kv4_attention takes for these arguments (host only, lengths on the device play no part):
- * the mma one in one CTA an SM (few work units) or several, the tcgen05 one with 128 rows a CTA or 256 a pair
- * of CTAs. 0 for arguments that it would refuse. */
+/* The kernels of w4a16_kv4_attention: mma with exact codes, in one CTA an SM (few work units) or several;
+ * tcgen05 with k', v' and the weights in fp16, 128 rows a CTA or 256 a pair of CTAs. Each takes any call. */
 typedef enum {
+    W4A16_KV4_AUTO = 0,
     W4A16_KV4_DECODE_WIDE = 1,
     W4A16_KV4_DECODE = 2,
     W4A16_KV4_PROMPT = 3,
     W4A16_KV4_PROMPT_PAIRS = 4
 } w4a16_kv4_kernel;
+
+/* w4a16_kv4_attention by a kernel of the caller's choice: W4A16_KV4_DECODE for results that no rounding of keys,
+ * values or weights to fp16 bears on (a prompt chunk takes 9 times as long), W4A16_KV4_AUTO as the call above. */
+int w4a16_kv4_attention_ex(const uint16_t* q, int64_t q_stride, int heads, const w4a16_kv4_cache* cache,
+                           const int32_t* block_table, int max_pages, const int32_t* kv_len, const int32_t* q_start,
+                           int B, int M, int max_q_len, int causal, float scale, uint16_t* out, float* lse,
+                           void* workspace, size_t workspace_bytes, int kernel, void* stream);
+
+/* Which kernel w4a16_kv4_attention takes for these arguments (host only, lengths on the device play no part);
+ * 0 for arguments that it would refuse. */
 int w4a16_kv4_attention_kernel(int heads, const w4a16_kv4_cache* cache, int max_pages, int B, int M, int max_q_len);
 
 /* Failure reporting of the attention kernels, without a GPU fault. Both set W4A16_ERR_DEVICE_TIMEOUT in the

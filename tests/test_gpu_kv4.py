@@ -650,3 +650,39 @@ def test_host_memory_is_refused(W):
                                      t["start"].data_ptr(), 1, 1, 1, 1, 0.1, t["out"].data_ptr(), None, t["work"].data_ptr(),
                                      t["work"].numel(), None) == W.ERR_INVALID_ARG, name
     ok(W)
+
+
+@pytest.mark.parametrize("kernel", [1, 2, 3, 4])
+@pytest.mark.parametrize("case", [2, 4, 5, 6, 8, 9, 13])
+def test_any_kernel_takes_any_call(W, case, kernel):
+    lens, q_lens, H, KV, D, page = ATTENTION[case]
+    b = Batch(W, 50 + case, lens, q_lens, H, KV, D, page)
+    lse = torch.full((sum(q_lens), H), 7.0, device="cuda")
+    q, args = cuda(b.q), b.args()
+    out = W.kv4_attention(q, b.cache, lse=lse, kernel=kernel, **args)
+    ok(W)
+    want, want_lse, bound = b.want(D ** -0.5)
+    close(out, want, bound)
+    assert np.array_equal(np.isneginf(lse.cpu().numpy()), np.isneginf(want_lse))
+    chosen = W.w4a16_kv4_attention_kernel(H, b.cache.desc, args["block_table"].shape[1], len(lens), sum(q_lens), args["max_q_len"])
+    if kernel == chosen:
+        assert torch.equal(out.view(torch.int16), W.kv4_attention(q, b.cache, **args).view(torch.int16))
+    assert int(b.work[:4096].sum()) == 0
+
+
+@pytest.mark.parametrize("kernel", [1, 2])
+def test_many_rows_by_the_exact_kernel(W, kernel):
+    """A prompt at the decode kernel's bound: 2^-16 of what a group is made of, beside the output's rounding."""
+    p = ref.Pairs("keys", 3)
+    B, D = p.k.shape[0], p.D
+    cache = W.KV4Cache(B, 16, 1, D)
+    slots = (np.arange(B)[:, None] * 16 + np.arange(2)).reshape(-1).astype(np.int32)
+    W.kv4_append(cuda(np.concatenate([p.k16, p.v16], axis=2).reshape(2 * B, 2 * D)), cache, cuda(slots), heads=0)
+    rows = [150] + [2] * (B - 1)
+    start = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    out = W.kv4_attention(cuda(np.ones((sum(rows), 4, D), np.float16)), cache, cuda(np.arange(B, dtype=np.int32)[:, None]),
+                          cuda(np.full(B, 2, np.int32)), cuda(start), 150, W.kv4_attention_workspace(cache), scale=p.SCALE,
+                          causal=False, kernel=kernel)
+    ok(W)
+    of = np.repeat(np.arange(B), rows)
+    close(out, np.repeat(p.want[of][:, None], 4, 1), np.repeat(p.one[of][:, None], 4, 1))

@@ -224,3 +224,11 @@ def test_the_precision_bounds_see_a_lost_bit():
     assert worst(weights, weights.many_with(11, 8, 11), weights.many) > 2
     assert worst(weights, weights.many_with(11, 11, 8), weights.many) > 2
     assert worst(keys, keys.many_with(8, 11, 11), keys.many) > 2
+
+
+def test_kernels_that_do_not_exist_are_refused(W):
+    n = W.w4a16_kv4_attention_workspace_bytes(128)
+    for kernel in (-1, 5):
+        assert W.w4a16_kv4_attention_ex(FAKE, 2560, 20, desc(W), FAKE + GB, 8, FAKE + 2 * GB, FAKE + 3 * GB, 2, 5, 4, 1, 0.1, FAKE + 4 * GB,
+                                        None, FAKE + 6 * GB, n, kernel, None) == W.ERR_INVALID_ARG
+    assert [W.KV4_AUTO, W.KV4_DECODE_WIDE, W.KV4_DECODE, W.KV4_PROMPT, W.KV4_PROMPT_PAIRS] == list(range(5))

@@ -32,6 +32,13 @@ PATH_AUTO = 0
 PATH_GEMV = 1
 PATH_TC = 2
 
+# kernels of w4a16_kv4_attention_ex
+KV4_AUTO = 0
+KV4_DECODE_WIDE = 1
+KV4_DECODE = 2
+KV4_PROMPT = 3
+KV4_PROMPT_PAIRS = 4
+
 # every symbol include/w4a16.h declares
 EXPORTED = [
     "w4a16_version", "w4a16_status_string", "w4a16_repacked_qweight_bytes", "w4a16_repacked_scales_bytes",
@@ -41,8 +48,9 @@ EXPORTED = [
     "w4a16_unrepack_nvfp4", "w4a16_gemm_nvfp4", "w4a16_gemm_nvfp4_ex", "w4a16_plan_for_nvfp4",
     "w4a16_quantize_x_int8", "w4a16_gemm_w4a8", "w4a16_gemm_w4a8_ex", "w4a16_plan_for_w4a8",
     "w4a16_quantize_gemm_w4a8", "w4a16_kv4_cache_bytes", "w4a16_kv4_append", "w4a16_kv4_load",
-    "w4a16_kv4_attention_workspace_bytes", "w4a16_kv4_attention", "w4a16_kv4_attention_kernel",
-    "w4a16_kv4_selftest_wait_timeout", "w4a16_kv4_selftest_withhold", "w4a16_sample",
+    "w4a16_kv4_attention_workspace_bytes", "w4a16_kv4_attention", "w4a16_kv4_attention_ex",
+    "w4a16_kv4_attention_kernel", "w4a16_kv4_selftest_wait_timeout", "w4a16_kv4_selftest_withhold",
+    "w4a16_sample",
 ]
 
 
@@ -137,6 +145,8 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.w4a16_kv4_attention_workspace_bytes.argtypes = [I]
     lib.w4a16_kv4_attention.restype = I
     lib.w4a16_kv4_attention.argtypes = [P, L, I, C, P, I, P, P, I, I, I, I, F, P, P, P, S, P]
+    lib.w4a16_kv4_attention_ex.restype = I
+    lib.w4a16_kv4_attention_ex.argtypes = [P, L, I, C, P, I, P, P, I, I, I, I, F, P, P, P, S, I, P]
     lib.w4a16_kv4_attention_kernel.restype = I
     lib.w4a16_kv4_attention_kernel.argtypes = [I, C, I, I, I, I]
     lib.w4a16_kv4_selftest_wait_timeout.restype = I
@@ -468,6 +478,14 @@ def w4a16_kv4_attention(q: int, q_stride: int, heads: int, cache: KV4Desc, block
                                    B, M, max_q_len, causal, scale, out, lse, workspace, workspace_bytes, stream)
 
 
+def w4a16_kv4_attention_ex(q: int, q_stride: int, heads: int, cache: KV4Desc, block_table: int, max_pages: int,
+                           kv_len: int, q_start: int, B: int, M: int, max_q_len: int, causal: int, scale: float,
+                           out: int, lse: int | None, workspace: int, workspace_bytes: int, kernel: int,
+                           stream: int | None) -> int:
+    return lib.w4a16_kv4_attention_ex(q, q_stride, heads, ctypes.byref(cache), block_table, max_pages, kv_len, q_start,
+                                      B, M, max_q_len, causal, scale, out, lse, workspace, workspace_bytes, kernel, stream)
+
+
 def w4a16_kv4_attention_kernel(heads: int, cache: KV4Desc, max_pages: int, B: int, M: int, max_q_len: int) -> int:
     return lib.w4a16_kv4_attention_kernel(heads, ctypes.byref(cache), max_pages, B, M, max_q_len)
 
@@ -591,10 +609,11 @@ def kv4_attention_workspace(cache: KV4Cache) -> torch.Tensor:
 def kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, kv_len: torch.Tensor,
                   q_start: torch.Tensor, max_q_len: int, workspace: torch.Tensor, scale: float | None = None,
                   causal: bool = True, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-                  stream=None) -> torch.Tensor:
+                  stream=None, kernel: int = KV4_AUTO) -> torch.Tensor:
     """Attention of q [M, heads, head_dim] (float16) over the cached tokens of B sequences: block_table
     int32 [B, pages], kv_len int32 [B], q_start int32 [B + 1] (sequence b's rows of q). Queries are the last
-    tokens of their sequence (causal) or see all of them. scale: 1 / sqrt(head_dim) when None."""
+    tokens of their sequence (causal) or see all of them. scale: 1 / sqrt(head_dim) when None. kernel: KV4_DECODE
+    for exact codes and weights whatever the rows, else chosen by max_q_len, B and the block table's width."""
     half, i32, D = torch.float16, torch.int32, cache.head_dim
     if not (q.dtype is half and q.is_cuda and q.dim() == 3 and q.shape[2] == D and q.stride()[1:] == (D, 1)):
         _refuse("kv4_attention", "q must be a CUDA float16 tensor [M, heads, head_dim], dense in a row")
@@ -613,10 +632,10 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, k
         out = _new((M, heads, D), half, q.device, stream)
     elif not _dense(out, half, (M, heads, D)):
         _refuse("kv4_attention", "out must be a contiguous CUDA float16 tensor [M, heads, head_dim]")
-    rc = lib.w4a16_kv4_attention(q.data_ptr(), q.stride(0), heads, cache.ref, block_table.data_ptr(),
-                                 block_table.shape[1], kv_len.data_ptr(), q_start.data_ptr(), B, M, max_q_len,
-                                 int(causal), D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse),
-                                 workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
+    rc = lib.w4a16_kv4_attention_ex(q.data_ptr(), q.stride(0), heads, cache.ref, block_table.data_ptr(),
+                                    block_table.shape[1], kv_len.data_ptr(), q_start.data_ptr(), B, M, max_q_len,
+                                    int(causal), D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse),
+                                    workspace.data_ptr(), workspace.numel(), kernel, _stream_handle(stream))
     if rc != OK:
         raise W4A16Error(rc, "w4a16_kv4_attention")
     return out

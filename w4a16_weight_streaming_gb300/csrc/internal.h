@@ -136,6 +136,7 @@ struct Kv4AttnParams {
     int max_q_len;
     int causal;
     float scale;
+    int kernel;    // which one, 0: by the fitted costs
     int withhold;  // debug-bounds build: the copy that every warp which fetches leaves out, -1 for none
 };
 size_t kv4_attention_workspace(int head_dim);  // bytes; the same for every batch

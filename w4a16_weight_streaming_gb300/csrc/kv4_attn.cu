@@ -788,6 +788,7 @@ size_t kv4_attention_workspace(int head_dim) {
 }
 
 int kv4_attention_kernel(const Kv4AttnParams& p, const Kv4Cache& c, int sm_count) {
+    if (p.kernel != 0) return p.kernel;
     if (decode_is_faster(p, c, sm_count)) return decode_is_wide(p, c.kv_heads, sm_count) ? W4A16_KV4_DECODE_WIDE : W4A16_KV4_DECODE;
     return kv4_prompt_pairs(p, c.kv_heads, c.head_dim) ? W4A16_KV4_PROMPT_PAIRS : W4A16_KV4_PROMPT;
 }

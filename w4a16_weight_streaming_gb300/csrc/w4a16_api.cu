@@ -1102,12 +1102,13 @@ size_t w4a16_kv4_attention_workspace_bytes(int head_dim) {
     return kv4_attention_workspace(head_dim);
 }
 
-int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4a16_kv4_cache* cache,
+int w4a16_kv4_attention_ex(const uint16_t* q, int64_t q_stride, int heads, const w4a16_kv4_cache* cache,
                         const int32_t* block_table, int max_pages, const int32_t* kv_len, const int32_t* q_start,
                         int B, int M, int max_q_len, int causal, float scale, uint16_t* out, float* lse,
-                        void* workspace, size_t workspace_bytes, void* stream) {
+                        void* workspace, size_t workspace_bytes, int kernel, void* stream) {
     if (!q || !block_table || !kv_len || !q_start || !out || !workspace) return W4A16_ERR_INVALID_ARG;
     if ((causal != 0 && causal != 1) || !std::isfinite(scale)) return W4A16_ERR_INVALID_ARG;
+    if (kernel < 0 || kernel > W4A16_KV4_PROMPT_PAIRS) return W4A16_ERR_INVALID_ARG;
     Kv4Cache c;
     const int rc = check_kv4_attention(heads, cache, max_pages, B, M, max_q_len, &c);
     if (rc != W4A16_OK) return rc;
@@ -1143,13 +1144,21 @@ int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4
     DeviceInfo d;
     if (!device_info(&d)) return W4A16_ERR_CUDA;
     Kv4AttnParams p = {q, q_stride, block_table, kv_len, q_start, out, lse, workspace, B, M, heads, max_pages,
-                       max_q_len, causal, scale, g_withhold.load()};
+                       max_q_len, causal, scale, kernel, g_withhold.load()};
     LaunchCtx ctx;
     ctx.stream = static_cast<cudaStream_t>(stream);
     ctx.status = d.status;
     ctx.timeout_ns = g_timeout_ns.load();
     ctx.sm_count = d.sm_count;
     return launched(launch_kv4_attention(p, c, ctx));
+}
+
+int w4a16_kv4_attention(const uint16_t* q, int64_t q_stride, int heads, const w4a16_kv4_cache* cache,
+                        const int32_t* block_table, int max_pages, const int32_t* kv_len, const int32_t* q_start,
+                        int B, int M, int max_q_len, int causal, float scale, uint16_t* out, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+    return w4a16_kv4_attention_ex(q, q_stride, heads, cache, block_table, max_pages, kv_len, q_start, B, M, max_q_len, causal,
+                                  scale, out, lse, workspace, workspace_bytes, 0, stream);
 }
 
 int w4a16_kv4_attention_kernel(int heads, const w4a16_kv4_cache* cache, int max_pages, int B, int M, int max_q_len) {
