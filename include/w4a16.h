@@ -359,7 +359,7 @@ size_t w4a16_kv4_attention_workspace_bytes(int head_dim);
  * the cache, a kv_len or q_start outside its range is cut off (its tokens are not seen) and sets
  * W4A16_ERR_BOUNDS in the device status word. B, M <= 2^20, M * heads <= 2^28,
  * max_pages * page_tokens < 2^31. Two kernels (8 query rows a key/value head at a time on mma, exact codes;
- * 128 or 256 at a time on tcgen05, k', v' and the weights rounded to fp16): the choice is by max_q_len, B and the
+ * 128 or 256 at a time on tcgen05, k', v' and the weights rounded to fp16): the choice is by max_q_len, M, B and the
  * block table's width. Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
  * MISALIGNED, CUDA.
  */

@@ -602,9 +602,8 @@ def test_batches_of_more_than_32_sequences(W, case, B, D):
     lens, q_lens = batch_of(kind, B, rng, rows, tokens)
     b = Batch(W, B * D, lens, q_lens, H, KV, D, 16)
     args = b.args(wide)
-    assert W.w4a16_kv4_attention_kernel(H, b.cache.desc, args["block_table"].shape[1], B, sum(q_lens), rows) == kernel
     lse = torch.full((sum(q_lens), H), 7.0, device="cuda")
-    out = W.kv4_attention(cuda(b.q), b.cache, lse=lse, **args)
+    out = W.kv4_attention(cuda(b.q), b.cache, lse=lse, kernel=kernel, **args)
     ok(W)
     want, want_lse, bound = b.want(D ** -0.5)
     close(out, want, bound)
@@ -630,9 +629,8 @@ def test_no_bit_is_lost_that_the_kernels_say_they_keep(W, kernel, q_len, kind):
     rows = [q_len] + [1] * (B - 1)
     start = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
     q = np.ones((sum(rows), group, D), np.float16)
-    assert W.w4a16_kv4_attention_kernel(group, cache.desc, table.shape[1], B, sum(rows), q_len) == kernel
     out = W.kv4_attention(cuda(q), cache, cuda(table), cuda(np.full(B, 2, np.int32)), cuda(start), q_len, W.kv4_attention_workspace(cache),
-                          scale=p.SCALE, causal=False)
+                          scale=p.SCALE, causal=False, kernel=kernel)
     ok(W)
     of = np.repeat(np.arange(B), rows)
     close(out, np.repeat(p.want[of][:, None], group, 1), np.repeat((p.one if kernel < 3 else p.many)[of][:, None], group, 1))

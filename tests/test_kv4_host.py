@@ -210,7 +210,7 @@ def test_every_attention_kernel_is_tested(W):
             pages = max(1, max(-(-n // page) for n in lens)) + wide
             seen.add((W.w4a16_kv4_attention_kernel(H, desc(W, t=page, h=KV, d=D), pages, len(lens), sum(q_lens), max(1, max(q_lens))), D))
     assert {k for k, _ in seen} == {1, 2, 3, 4}
-    assert {case[0] for case in LARGE.values()} == {1, 2, 3, 4}  # each with every head size; it asserts its kernel
+    assert {case[0] for case in LARGE.values()} == {1, 2, 3, 4}  # each with every head size, by name
 
 
 def test_the_precision_bounds_see_a_lost_bit():
@@ -232,3 +232,28 @@ def test_kernels_that_do_not_exist_are_refused(W):
         assert W.w4a16_kv4_attention_ex(FAKE, 2560, 20, desc(W), FAKE + GB, 8, FAKE + 2 * GB, FAKE + 3 * GB, 2, 5, 4, 1, 0.1, FAKE + 4 * GB,
                                         None, FAKE + 6 * GB, n, kernel, None) == W.ERR_INVALID_ARG
     assert [W.KV4_AUTO, W.KV4_DECODE_WIDE, W.KV4_DECODE, W.KV4_PROMPT, W.KV4_PROMPT_PAIRS] == list(range(5))
+
+
+def test_the_choice_counts_the_rows_of_the_whole_batch(W):
+    """Sequences that are alike are counted as before (cost and pair rules of one sequence times the batch); a
+    prompt among streams of one query no longer counts as a prompt a stream."""
+    def one_by_one(H, KV, D, tokens, B, n):
+        rows = n * (H // KV)
+        here = {256: 11.2, 128: 10.0, 64: 8.5}[D] + {256: 0.162, 128: 0.087, 64: 0.053}[D] / 152 * B * KV * -(-rows // 8) * (tokens / 16)
+        there = {256: 26.3, 128: 19.3, 64: 16.1}[D] + {256: 0.73, 128: 0.69, 64: 0.74}[D] / 152 * B * KV * -(-rows // 128) * (tokens / 64)
+        if abs(here - there) < 1e-9 * here:
+            return None
+        if here < there:
+            return 1 if 2 * B * KV * -(-rows // 8) <= 152 else 2
+        units = -(-rows // 128)
+        return 4 if units % 2 == 0 or units >= (3 if D == 256 else 17) else 3
+
+    rng = np.random.default_rng(0)
+    for _ in range(3000):
+        KV, D, grp = int(rng.integers(1, 9)), int(rng.choice([64, 128, 256])), int(rng.integers(1, 17))
+        B, n, pages = int(np.exp(rng.uniform(0, 5))), int(np.exp(rng.uniform(0, 7))), int(np.exp(rng.uniform(0, 9)))
+        want = one_by_one(KV * grp, KV, D, pages * 16, B, n)
+        assert want in (None, W.w4a16_kv4_attention_kernel(KV * grp, desc(W, h=KV, d=D), pages, B, B * n, n)), (KV, D, grp, B, n, pages)
+    mixed = lambda streams, n, d: W.w4a16_kv4_attention_kernel(20, desc(W, h=4, d=d), 256, streams + 1, streams + n, n)  # noqa: E731
+    assert mixed(63, 512, 256) == mixed(15, 512, 256) == mixed(63, 512, 128) == 3
+    assert mixed(3, 1024, 256) == 4

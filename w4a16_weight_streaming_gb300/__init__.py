@@ -613,7 +613,7 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, k
     """Attention of q [M, heads, head_dim] (float16) over the cached tokens of B sequences: block_table
     int32 [B, pages], kv_len int32 [B], q_start int32 [B + 1] (sequence b's rows of q). Queries are the last
     tokens of their sequence (causal) or see all of them. scale: 1 / sqrt(head_dim) when None. kernel: KV4_DECODE
-    for exact codes and weights whatever the rows, else chosen by max_q_len, B and the block table's width."""
+    for exact codes and weights whatever the rows, else chosen by max_q_len, M, B and the block table's width."""
     half, i32, D = torch.float16, torch.int32, cache.head_dim
     if not (q.dtype is half and q.is_cuda and q.dim() == 3 and q.shape[2] == D and q.stride()[1:] == (D, 1)):
         _refuse("kv4_attention", "q must be a CUDA float16 tensor [M, heads, head_dim], dense in a row")

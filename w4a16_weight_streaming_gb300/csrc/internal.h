@@ -139,6 +139,15 @@ struct Kv4AttnParams {
     int kernel;    // which one, 0: by the fitted costs
     int withhold;  // debug-bounds build: the copy that every warp which fetches leaves out, -1 for none
 };
+// The most groups of `size` query rows of one key/value head that the call's sequences can have: each has no more
+// than max_q_len queries, all together M (one prompt among streams of one query has few groups, though each
+// sequence could have many).
+inline int64_t kv4_row_groups(const Kv4AttnParams& p, int kv_heads, int size) {
+    const int64_t grp = p.heads / kv_heads, sequences = p.B < p.M ? p.B : p.M;
+    const int64_t rows = (p.max_q_len < p.M ? p.max_q_len : p.M) * grp, each = (rows + size - 1) / size;
+    const int64_t all = sequences * each, total = p.M * grp / size + sequences;
+    return all < total ? all : total;
+}
 size_t kv4_attention_workspace(int head_dim);  // bytes; the same for every batch
 // Which kernel takes the call (the pointers are not looked at): w4a16_kv4_attention_kernel's values.
 int kv4_attention_kernel(const Kv4AttnParams& p, const Kv4Cache& c, int sm_count);

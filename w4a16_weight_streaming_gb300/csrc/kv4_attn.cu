@@ -750,8 +750,7 @@ cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, const Launch
 
 // Wide where half the SMs suffice for the work units, narrow otherwise.
 bool decode_is_wide(const Kv4AttnParams& p, int kv_heads, int sm_count) {
-    const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / kv_heads);
-    return 2 * std::min<int64_t>(p.B, p.M) * kv_heads * ((rows + kRows - 1) / kRows) <= sm_count;
+    return 2 * kv4_row_groups(p, kv_heads, kRows) * kv_heads <= sm_count;
 }
 
 template <int D>
@@ -766,17 +765,19 @@ cudaError_t launch_decode(const Kv4AttnParams& p, const Kv4View& v, bool wide, c
 // 10 rows 47.9 | 43.1, 20 rows 64.0 | 43.2; 8 heads of 128, 10 rows 48.7 | 57.5, 20 rows 61.0 | 57.5; 16 heads of
 // 64, 20 rows 73.2 | 94.4, 40 rows 115.5 | 94.3; one sequence of 16384, heads of 256, 40 rows 31.5 | 34.4, 80 rows
 // 57.3 | 41.4. The choice costs 0.3 % over the better of the two on average, 17 % at most (1000 tokens, where both
-// take 20 to 35 us). The lengths are on the device: the block table's width stands for them.
+// take 20 to 35 us), where the block table is as wide as the longest sequence. The lengths are on the device and the
+// table's width stands for them: with one allocated for far longer sequences several queries go to the other kernel too
+// early (777 tokens under a table of 131,072, 4 heads of 256, 2 to 16 queries of 20 heads: 11.4 to 13.0 | 23.0 to
+// 25.0, and the second is taken). A caller who knows the lengths names the kernel.
 bool decode_is_faster(const Kv4AttnParams& p, const Kv4Cache& c, int sm_count) {
     const double start_here = c.head_dim == 256 ? 11.2 : c.head_dim == 128 ? 10.0 : 8.5;
     const double start_there = c.head_dim == 256 ? 26.3 : c.head_dim == 128 ? 19.3 : 16.1;
     const double tile_here = c.head_dim == 256 ? 0.162 : c.head_dim == 128 ? 0.087 : 0.053;
     const double tile_there = c.head_dim == 256 ? 0.73 : c.head_dim == 128 ? 0.69 : 0.74;
-    const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / c.kv_heads);
-    const double heads = static_cast<double>(std::min(p.B, p.M)) * c.kv_heads;
+    const double groups = static_cast<double>(kv4_row_groups(p, c.kv_heads, kRows)), groups128 = static_cast<double>(kv4_row_groups(p, c.kv_heads, 128));
     const double tokens = static_cast<double>(p.max_pages) * c.page_tokens;
-    const double here = start_here + tile_here / sm_count * heads * static_cast<double>((rows + kRows - 1) / kRows) * (tokens / kKv4Tile);
-    const double there = start_there + tile_there / sm_count * heads * static_cast<double>((rows + 127) / 128) * (tokens / 64);
+    const double here = start_here + tile_here / sm_count * c.kv_heads * groups * (tokens / kKv4Tile);
+    const double there = start_there + tile_there / sm_count * c.kv_heads * groups128 * (tokens / 64);
     return here <= there;
 }
 

@@ -1118,13 +1118,15 @@ size_t kv4_prompt_workspace(int head_dim) {
 }
 
 // Two CTAs on 256 rows save 4 to 14 % of what one on 128 twice takes, and are worth no less for a half-empty last
-// unit: an even number of 128-row units (one sequence of 4096, heads of 256, 4096 queries of 5 heads a key head:
-// 189.9 us with one, 182.1 with two; 8 of 4096, 240 rows 48.3 | 45.7, heads of 64 95.1 | 91.4), or so many that
-// the last does not count (300 rows, heads of 256: 36.0 | 33.1 one sequence, 63.4 | 64.6 eight; of 128 81.7 |
-// 95.8, of 64 136.2 | 169.2).
+// unit: an even number of 128-row units a sequence (one sequence of 4096, heads of 256, 4096 queries of 5 heads a key
+// head: 189.9 us with one, 182.1 with two; 8 of 4096, 240 rows 48.3 | 45.7, heads of 64 95.1 | 91.4), or so many that
+// the last does not count, 3 of heads of 256 and 17 of others (300 rows, heads of 256: 36.0 | 33.1 one sequence, 63.4 |
+// 64.6 eight; of 128 81.7 | 95.8, of 64 136.2 | 169.2). So pairs may take a third, or a 17th, more CTAs for the whole
+// batch. (A prompt of 512 queries among 15 or 63 streams of one, all of 4096 tokens, 4 heads of 256: 79.1 | 96.6, 171.3
+// | 249.9.)
 bool kv4_prompt_pairs(const Kv4AttnParams& p, int kv_heads, int head_dim) {
-    const int64_t rows = static_cast<int64_t>(std::min(p.max_q_len, p.M)) * (p.heads / kv_heads), units = (rows + kRows - 1) / kRows;
-    return units % 2 == 0 || units >= (head_dim == 256 ? 3 : 17);
+    const int64_t units = kv4_row_groups(p, kv_heads, kRows), ctas = 2 * kv4_row_groups(p, kv_heads, 2 * kRows);
+    return head_dim == 256 ? 3 * ctas <= 4 * units : 17 * ctas <= 18 * units;
 }
 
 cudaError_t launch_kv4_prompt(const Kv4AttnParams& p, const Kv4View& v, int head_dim, bool pair, const LaunchCtx& ctx) {
