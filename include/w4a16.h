@@ -327,6 +327,8 @@ size_t w4a16_kv4_cache_bytes(int num_pages, int page_tokens, int kv_heads, int h
  * and then in pairs of neighbouring sums). x must be finite. A position outside the table makes the row's
  * queries 0 and stores nothing, a slot outside the cache stores nothing; both set W4A16_ERR_BOUNDS in the
  * device status word. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA.
+ * (An infinite or NaN x spoils its group of 64, and other queries' rows of a tile that holds it, seen or not. A
+ * value of |x| above 65,440 may be stored as one above 65,519, infinity to kv4_load and the tcgen05 kernel.)
  */
 int w4a16_kv4_append(const uint16_t* qkv, int64_t qkv_stride, int heads, uint16_t* q_out, const w4a16_kv4_cache* cache,
                      const int32_t* slots, const int32_t* positions, const float* rope, int rope_positions, int rot,

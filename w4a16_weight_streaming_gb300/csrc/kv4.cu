@@ -6,12 +6,13 @@
 //   - the rotation's partner element is in the same lane (adjacent pairs) or one exchange away (halves),
 //   - the minimum and maximum of the 64 elements that share a scale are 3 exchanges among 8 lanes,
 // and one pass takes a row from the product's output to rotated queries and stored codes. A decode row is
-// bound by latency (a load, three short exchange chains, a store), a prompt chunk by instruction issue: the
-// exact arithmetic below is some 200 instructions a warp for 256 elements. Rows are the grid's first
-// dimension, so no thread divides (1024 rows 15.2 us with one index over rows and heads, 13.0 so).
+// bound by latency (a load, three short exchange chains, a store). A prompt chunk is near no single limit: 318
+// instructions a warp for 256 elements at 2.6 of 4 a cycle, 46 % of the warps there, the first stall the first
+// wave's loads. Rows are the grid's first dimension, so no thread divides (1024 rows 15.2 us with one index over
+// rows and heads, 13.0 so).
 //
 // Measured with the reading kernel behind it, on one GB300, the data in L2: 1 row of 20 + 2 x 4 heads of 256
-// 3.7 us the pair, 64 rows of 40 + 2 x 8 heads of 128 4.2 us, 1024 rows of 20 + 2 x 4 heads of 256 13.0 us (32
+// 3.6 us the pair, 64 rows of 40 + 2 x 8 heads of 128 4.2 us, 1024 rows of 20 + 2 x 4 heads of 256 12.9 us (32
 // MB in and out: 2.5 TB/s, 0.36 of the copy bandwidth).
 //
 // The codes are decisions, so everything before them is defined to the bit, in binary32 without fused

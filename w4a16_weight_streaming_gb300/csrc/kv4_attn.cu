@@ -27,8 +27,8 @@
 //
 // Measured on one GB300: one sequence of 131,072 tokens, 20 heads on 4 of 256, 40.1 us (151 MB, 3.8 TB/s, 0.56 of
 // the copy bandwidth); 64 sequences of up to 8192 tokens, 40 heads on 8 of 128, 78.3 us (304 MB, 3.9 TB/s, 0.57);
-// one sequence of 777 tokens 9.9 us, which is the kernel's start (4 us), a few tiles, and the adding of parts (3
-// us). A tile is 380 warp instructions for D = 128 and 610 for 256; with the 16 warps that the registers leave room
+// one sequence of 777 tokens 10.0 us, which is the kernel's start (4 us), a few tiles, and the adding of parts (3
+// us). A tile is 371 warp instructions for D = 128 and 579 for 256; with the 16 warps that the registers leave room
 // for an SM issues 2.2 of 4 a cycle, its ALU busy half of the time: the issue of dependent instructions bounds
 // the long calls, not memory.
 #include <algorithm>

@@ -21,7 +21,8 @@
 // Warps: 0-15 softmax, a quarter of a row a thread (the four warps of 32 rows meet at a barrier once a tile;
 // the row's reference moves, and O is rescaled in TMEM, only when a score exceeds it by 2^8); then 8 (one CTA)
 // or 4 that dequantise a 16-token quarter of the tile's keys or values each, one that fetches the cache's tiles
-// by bulk copies, one that issues S and one that issues PV. K', V' and S/P are double-buffered. What bounds a
+// by bulk copies, one that issues S and one that issues PV. K', V' and S/P are double-buffered, K' and V' of
+// a pair four times. What bounds a
 // tile is the circle S -> softmax -> PV -> S of its S/P buffer and the softmax warps' own chain, 1500 cycles of
 // latencies, so the softmax is spread over many warps (a row in one thread: 283 us, in two 179, in four less; two
 // groups of one-thread rows taking the even and the odd tiles: 186, all then with one CTA).
@@ -31,8 +32,8 @@
 // what it still has in TMEM. (Added from memory, its own part among them: 169 us for the chunk above, 163 so.
 // An SM reads parts at 45 to 60 GB/s, however many loads are under way.)
 //
-// Measured on one GB300: 1024 queries of 20 heads (4 of 256) behind 8192 tokens 140.6 us (183 GFLOP, 1,298 TFLOP/s,
-// 0.68 of the bf16 rate); 16 sequences of 1070 .. 8005 tokens with 8 .. 16 queries each 46.8 us (73.6 MB). A tile
+// Measured on one GB300: 1024 queries of 20 heads (4 of 256) behind 8192 tokens 140.9 us (183 GFLOP, 1,299 TFLOP/s,
+// 0.68 of the bf16 rate); 16 sequences of 1070 .. 8005 tokens with 8 .. 16 queries each 47.0 us (73.6 MB). A tile
 // of 64 tokens takes 0.95 us with 256 rows on two CTAs, of which its matrix instructions fill 0.55, 0.85 with up
 // to 80 rows on one, where a tile's dequantisation (1400 cycles a warp) bounds it.
 #include <algorithm>
