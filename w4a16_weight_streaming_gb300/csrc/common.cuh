@@ -25,13 +25,11 @@ __device__ __forceinline__ void record_error(unsigned* status, unsigned code) { 
 // kErrBounds and the access is skipped (no trap: the context stays usable). In the normal build the
 // test compiles away.
 #ifdef W4A16_DEBUG_BOUNDS
-constexpr bool kDebugBounds = true;
 __device__ __forceinline__ bool in_bounds(bool ok, unsigned* status) {
     if (!ok) record_error(status, kErrBounds);
     return ok;
 }
 #else
-constexpr bool kDebugBounds = false;
 __device__ __forceinline__ bool in_bounds(bool, unsigned*) { return true; }
 #endif
 

@@ -23,6 +23,12 @@
 
 namespace w4a16 {
 
+#ifdef W4A16_DEBUG_BOUNDS
+constexpr bool kDebugBounds = true;
+#else
+constexpr bool kDebugBounds = false;
+#endif
+
 constexpr int kKv4Group = 64;  // elements per (scale, min) pair
 constexpr int kKv4Tile = 16;   // tokens per tile
 
