@@ -1,12 +1,13 @@
 #!/usr/bin/env python3
-"""Benchmark of the W4A16 weight-streaming GEMM on GB300 (one JSON line on stdout).
+"""Benchmark of the W4A16 weight-streaming GEMM on GB300 (one JSON line on stdout, short enough to be
+kept whole by whatever keeps the last 2000 characters; --details writes the whole record to a file).
 
 Default workload: the dense-layer sweep. The four matrices of one dense layer (K x N = 5120 x 7168
 fused qkv, 5120 x 5120 o, 5120 x 34816 fused gate+up, 17408 x 5120 down; group 128) at every M in
 {1, 2, 4, ..., 1024}. One step = one pass of the hot path over all 44 (M, matrix) GEMMs, in layer
 order (for each M: qkv, o, gate+up, down), each y = x . dequant(W) through the C ABI. `value` =
 weight bytes streamed per step / step time (effective weight-stream GB/s of the whole sweep);
-`tflops` likewise; `rows` gives every (matrix, M) launch on its own: mean us (plain CUDA graph),
+`tflops` likewise. In the record, `rows` gives every (matrix, M) launch on its own: mean us (plain CUDA graph),
 median / p10 / p90 us (per-launch event pairs), weight GB/s, TFLOP/s, roofline fraction, bound and
 plan.
 
@@ -15,7 +16,7 @@ bracketed by a barrier and torch.cuda.synchronize(), timed with CUDA events on t
 L2: every weight matrix exists in R device copies and consecutive uses of one copy are at least 4 x
 L2 bytes of other weights apart, so no launch finds its weights in L2. `e2e` repeats steps through
 w4a16_gemm_host with host buffers (x copied in from pinned host memory, y copied back, every GEMM of
-the step, the independent GEMMs spread over eight streams). More objects, outside the timed step:
+the step, the independent GEMMs spread over eight streams). More objects of the record, outside the timed step:
 `decode_step_chain` (64 dense layers in one CUDA graph per decode step, at B = 1 .. 64 streams),
 `nvfp4` (the same four matrices with NVFP4 weights at M = 1, 16, 256, and their chain) and `w4a8`
 (the same int4 weights with int8 activations at M = 1, 8, 16, 256, the quantisation timed beside
@@ -606,6 +607,26 @@ def measure_w4a8(W, dev, peaks, timed, capture, l2, n_launches=100, keep=None):
             "layer_step": layer, "rows": rows}
 
 
+# ------------------------------------------------------------------------------ the line
+TABLES = ("layer_step", "rows", "cold_launch_us", "decode_step_chain", "nvfp4", "w4a8", "value_is", "peaks")  # of the record only
+
+
+def short_line(record: dict) -> str:
+    """The JSON line: the record without its tables and explanations, numbers to 6 significant digits."""
+    def short(x):
+        if isinstance(x, float):
+            return float(f"{x:.6g}")
+        if isinstance(x, dict):
+            return {k: short(v) for k, v in x.items()}
+        return [short(v) for v in x] if isinstance(x, (list, tuple)) else x
+
+    line = {k: v for k, v in record.items() if k not in TABLES}
+    if line.get("cpu_baseline"):
+        line["cpu_baseline"] = {k: v for k, v in line["cpu_baseline"].items() if k != "single_thread"}
+    line["config"] = {k: v for k, v in line["config"].items() if not isinstance(v, list)}  # (they are in the workload's name)
+    return json.dumps(short(line))
+
+
 # ------------------------------------------------------------------------------ GPU arm
 def percentile(v, q):
     return float(np.percentile(np.asarray(v, dtype=np.float64), q))
@@ -624,6 +645,7 @@ def main():
                     help="streams the end-to-end step spreads its independent GEMMs over")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--cpu-seconds", type=float, default=12.0)
+    ap.add_argument("--details", default=None, help="file for the whole record (rows, chains, NVFP4 and int8 tables) as JSON")
     ap.add_argument("--table", action="store_true", help="also print the per-row table to stderr")
     ap.add_argument("--no-chain", action="store_true", help="skip the 64-layer decode-step chain")
     ap.add_argument("--no-nvfp4", action="store_true", help="skip the NVFP4-weight rows")
@@ -946,8 +968,8 @@ def main():
                 "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "f16",
                 "data": "synthetic",
                 "config": dict(cfg, **{
-                    "l2": "inputs larger than L2: every launch reads its own weight copy; a matrix's copies cycle "
-                          f"through more than 4x the {l2 / 1e6:.0f} MB L2 (no flush needed)",
+                    "l2": "inputs larger than L2: every launch reads its own weight copy, a matrix's copies "
+                          f"take more than 4x the {l2 / 1e6:.0f} MB L2",
                     "timing": "K replays of a CUDA graph of one step, CUDA events on the launching stream",
                     "parallelism": "replicas" if world > 1 else "single GPU"}),
                 "value_is": "weight bytes streamed per step / step time (all GEMMs of the step)",
@@ -959,7 +981,10 @@ def main():
                 "gpu_launches": args.steps * sum(2 if "tail_items=" in r["plan"] else 1 for r in rows),
                 "clocks": clocks,
                 "peaks": {k: v for k, v in peaks.items()}}
-        print(json.dumps(line), flush=True)
+        if args.details:
+            with open(args.details, "w") as f:
+                json.dump(line, f)
+        print(short_line(line), flush=True)
     if dist is not None:
         dist.destroy_process_group()
 
