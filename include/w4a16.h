@@ -419,6 +419,86 @@ int w4a16_kv4_selftest_withhold(int copy);
 int w4a16_sample(const uint16_t* logits, int64_t stride, int M, int V, const float* temperature, const int32_t* top_k,
                  const float* top_p, const float* min_p, const float* u, int32_t* tokens, float* probs, void* stream);
 
+/*
+ * ---- Of the logits that w4a16_sample draws from: log probabilities.
+ * p = exp((l - l_max) / T) / sum (NaN and -inf: 0; infinite logits share everything); the order is that of
+ * w4a16_sample: logits descending, ties by lower index, masked ones nowhere in it.
+ *   logits: fp16 [M] rows of V, stride elements apart (2-byte aligned: any part of a wider row)
+ *   tokens: int32 [M][given], the tokens whose log probability is asked for (NULL when given is 0). A negative one
+ *           (a padding entry) gives 0 and rank 0; so does one from V on, with W4A16_ERR_BOUNDS in the status word
+ *   temperature: fp32 [M] or NULL (1); not above 0: 1
+ *   logprob: fp32 [M][given] (-inf for a masked token); rank: int32 [M][given], place in the order from 1, 0 for a
+ *           masked token; entropy: fp32 [M], -sum p log p. Each may be NULL.
+ *   top_tokens int32, top_logprob fp32 [M][top]: the first `top` of the order; -1 and -inf where there are
+ *           fewer. NULL when top is 0.
+ * A row of nothing but masked logits: -inf, rank 0, entropy 0. fp32 sums; tokens and ranks are exact; repeats are
+ * bit-identical. given <= 8, top <= 32, V <= 1,000,000, M <= 65,536. Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
+ * MISALIGNED, CUDA.
+ */
+int w4a16_logprobs(const uint16_t* logits, int64_t stride, int M, int V, const int32_t* tokens, int given, int top,
+                   const float* temperature, float* logprob, int32_t* rank, float* entropy, int32_t* top_tokens,
+                   float* top_logprob, void* stream);
+
+/*
+ * ---- Between two blocks: the residual stream and the norms on both sides of it.
+ *   z  = y, or y * (1 / sqrt(mean(y^2) + eps)) * (offset + post_weight)      (a norm behind the block)
+ *   h' = h + scale * gate * z
+ *   x  = h' * (1 / sqrt(mean(h'^2) + eps)) * (offset + weight)                (the norm before the next block)
+ * in binary32 from the stored values; x is the norm of the sum before h' is rounded.
+ *   h:     fp16 (h_f32 0) or fp32 (1) [M] rows of H, h_stride elements apart (a multiple of 8; of one row anything)
+ *   y:     fp16 [M] rows, y_stride apart, or NULL: h' = h (post_weight and gate NULL too)
+ *   post_weight: fp16 [H], or NULL: no norm behind the block;  weight: fp16 [H], or NULL: a factor of 1
+ *   gate:  NULL: 1. fp16: rows of H gate_stride apart (0: one row for all; else a multiple of 8), or, when gate_per_row
+ *          is 1, one value a row, gate_stride apart (any)
+ *   h_out: [M][H] of h's type, or NULL; may be h itself where h is dense.  x: fp16 [M][H], or NULL. One of them at least.
+ * The weights must not be written by the kernel right before this call on its stream (they are read while it ends).
+ * H % 8 == 0, H <= 32768, M <= 2^20; all 16-byte aligned but a gate of one value a row (2). These two calls and
+ * w4a16_moe refuse memory of another GPU than the current one. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA.
+ */
+int w4a16_block_norm(const void* h, int64_t h_stride, int h_f32, const uint16_t* y, int64_t y_stride,
+                     const uint16_t* post_weight, const uint16_t* gate, int64_t gate_stride, int gate_per_row, float scale,
+                     const uint16_t* weight, float offset, float eps, void* h_out, uint16_t* x, int M, int H, void* stream);
+
+/*
+ * ---- A mixture-of-experts layer for a few tokens, where a dense layer has gate+up, w4a16_silu_mul and down.
+ *   l[t][e] = x[t] . router[e];  score = softmax over e of l, or 1 / (1 + e^-l)
+ *   chosen:  the top_k experts of a token with the largest l (sigmoid: score + bias); ties: the lower index, NaN last
+ *   r[t][e] = scale * score, with renormalize over the sum of the chosen ones' scores
+ *   a = fp16_rne(silu(x . Wg) * (x . Wu)), the products in fp32;  y[t] = fp16_rne(sum_e r * (a . Wd)), in order of e
+ * The experts' matrices are those of w4a16_repack (or w4a16_repack_nvfp4) one after another: gate_up [hidden, 2 inner]
+ * (gate columns first), down [inner, hidden]. A call reads each chosen expert's weights once, whatever the tokens (an
+ * expert with many more tokens than the average again).
+ */
+typedef struct {
+    const void* gate_up_q;      /* experts * w4a16_repacked_qweight_bytes(2 inner, hidden, group) */
+    const void* gate_up_s;      /* experts * w4a16_repacked_scales_bytes (NVFP4: w4a16_repacked_nvfp4_scales_bytes) */
+    const void* down_q;         /* of (hidden, inner) */
+    const void* down_s;
+    const float* gate_up_scale; /* NVFP4: the tensor scale of each expert's matrix, fp32 [experts] (device); int4: NULL */
+    const float* down_scale;
+    int experts;                /* <= 512 */
+    int hidden;                 /* a multiple of 64 and of group, <= 65,536; inner too */
+    int inner;
+    int group;                  /* a multiple of 32; ignored for NVFP4 */
+    int nvfp4;                  /* 0 or 1 */
+} w4a16_moe_experts;
+
+/* Device memory that w4a16_moe needs beside its operands, the same for every batch; 0 for an unsupported shape. To be
+ * zeroed once, before its first use; every call leaves it ready for the next. Calls that may run at the same time
+ * (captured ones that may be replayed at the same time too) need one each. */
+size_t w4a16_moe_workspace_bytes(int experts, int hidden, int inner);
+
+/*   x:       fp16 [tokens] rows of hidden, x_stride elements apart (a multiple of 8; of one row anything)
+ *   router:  fp16 [experts][hidden]; bias: fp32 [experts] (scoring 1 only) or NULL; scoring: 0 softmax, 1 sigmoid
+ *   y:       fp16 [tokens][hidden], written in full
+ *   ids:     int32 [tokens][top_k], the chosen experts in order, or NULL; weights: fp32 [tokens][top_k], r, or NULL
+ * No token bears on another's result but in the order of its sums (which follows the list of chosen experts): infinities
+ * and NaN stay in their row. Repeats of a batch are bit-identical.
+ * tokens <= 64, top_k <= 16 and <= experts. Three kernels. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
+int w4a16_moe(const uint16_t* x, int64_t x_stride, const w4a16_moe_experts* experts, const uint16_t* router, const float* bias,
+              int top_k, int scoring, int renormalize, float scale, uint16_t* y, int32_t* ids, float* weights, int tokens,
+              void* workspace, size_t workspace_bytes, void* stream);
+
 /* Describes the last GEMM this process launched (path, tile, split, grid) into buf (NUL
  * terminated, truncated to len). Host only. Returns W4A16_OK or INVALID_ARG. */
 int w4a16_last_dispatch(char* buf, size_t len);

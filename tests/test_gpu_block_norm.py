@@ -1,0 +1,144 @@
+"""block_norm against the formula in 64 bits.
+
+Bounds: a sum of squares goes through at most 24 roundings of 2^-24 (square, pairs, a thread's 8 vectors, warp, warps),
+half of that after the root, 6 more in root, division and factors: below 2^-19 of z and of x. The sum h + scale gate z
+adds 2^-22 of its terms. Outputs are rounded once: half a step, 2^-11 (fp16) or 2^-24 (fp32), 2^-25 among subnormals."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from gpu_util import lib
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def W():
+    return lib()
+
+
+def rms(v, w, eps, offset):
+    v = v * (v.square().mean(1, keepdim=True) + eps).rsqrt()
+    return v if w is None else v * (offset + w.double())
+
+
+def check(W, h, y=None, weight=None, post=None, gate=None, scale=1.0, eps=1e-6, offset=0.0, result=None, **kw):
+    before = h.clone()
+    h2, x = result if result is not None else W.block_norm(h, y, weight=weight, post_weight=post, gate=gate, scale=scale, eps=eps, offset=offset, **kw)
+    torch.cuda.synchronize()
+    assert W.w4a16_device_status() == W.OK
+    d = before.double()
+    branch = torch.zeros_like(d)
+    if y is not None:
+        z = y.double() if post is None else rms(y.double(), post, eps, offset)
+        branch = scale * z * (1.0 if gate is None else gate.double())
+    ref = d + branch
+    slack = 2.0 ** -19 * branch.abs() + 2.0 ** -22 * d.abs()
+    if h2 is not None:
+        half = 2.0 ** -11 if h.dtype is torch.float16 else 2.0 ** -24
+        assert bool(((h2.double() - ref).abs() <= half * ref.abs() * 1.001 + 2.0 ** -25 + slack).all())
+    if x is not None:
+        q = (ref.square().mean(1, keepdim=True) + eps).rsqrt()
+        f = torch.ones_like(ref) if weight is None else (offset + weight.double()).abs()
+        want = rms(ref, weight, eps, offset)
+        assert bool(((x.double() - want).abs() <= (2.0 ** -11 + 2.0 ** -19) * want.abs() * 1.001 + 2.0 ** -25 + slack * q * f
+                     + 2.0 ** -21 * want.abs()).all())
+    return h2, x
+
+
+def make(M, H, f32=False, seed=0):
+    g = torch.Generator("cuda").manual_seed(seed + M * 131 + H)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")
+    h = 2 * r(M, H)
+    return (h if f32 else h.half()), r(M, H).half(), (1 + 0.3 * r(H)).half(), (1 + 0.3 * r(H)).half(), r(M, H).half()
+
+
+# a warp a row (1, 2, 4 vectors), a CTA a row with 1, 2, 4, 8 vectors a thread, odd row and vector counts
+SIZES = [(1, 8), (5, 64), (3, 256), (7, 264), (2, 520), (400, 1000), (1, 1024), (1, 5120), (33, 5120), (400, 2048), (400, 4096),
+         (400, 5120), (400, 8200), (310, 16384), (1, 8200), (2, 16392), (3, 32768), (310, 32768), (1001, 40)]
+
+
+@pytest.mark.parametrize("f32", [False, True], ids=["f16", "f32"])
+@pytest.mark.parametrize("M,H", SIZES)
+def test_every_form_at_every_size(W, M, H, f32):
+    h, y, w, p, g = make(M, H, f32)
+    check(W, h, y, w)
+    check(W, h, y, w, post=p, gate=g, scale=0.7, offset=1.0)
+    check(W, h, y, None, post=p, gate=g[0].contiguous(), scale=-0.3)
+    check(W, h, y, w, gate=g[:, :1].contiguous(), scale=2.0)
+    check(W, h, y, w, gate=g[:, 3:4] if H > 8 else g[:, :1])  # one value a row of a wider tensor
+    a = check(W, h, None, w)
+    assert a[0] is h
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_rows_with_strides(W, f32):
+    M, H = 9, 1272
+    h, y, w, p, g = make(M, H + 64, f32)
+    check(W, h[:, 8:H + 8], y[:, 40:H + 40], w[:H].contiguous(), post=p[8:H + 8].contiguous(), gate=g[:, 16:H + 16])
+    check(W, h[::2, 8:H + 8], y[::2, :H], w[:H].contiguous(), gate=g[0, 8:H + 8])
+    check(W, h[:1, 8:H + 8], y[:1, 16:H + 16], w[:H].contiguous())
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_in_place_and_single_outputs(W, f32):
+    h, y, w, p, g = make(12, 1536, f32)
+    old = h.clone()
+    new, x = W.block_norm(h, y, weight=w, post_weight=p)
+    x2 = torch.empty_like(x)
+    assert W.block_norm(h, y, weight=w, post_weight=p, out=(h, x2))[0] is h
+    torch.cuda.synchronize()
+    assert torch.equal(h, new) and torch.equal(x, x2)
+    check(W, old, y, w, post=p, out=(None, x2))
+    check(W, old, y, w, post=p, out=(new, None))
+
+
+def test_extreme_values(W):
+    H = 2048
+    h, y, w, p, _ = make(6, H, True)
+    h[0] = 0
+    y[0] = 0          # a row of nothing: eps carries the division
+    y[1] *= 2.0 ** -14
+    h[2] = 1e15       # squares of 1e30
+    h[3, 0], y[3] = 60000.0, 0
+    y[4] = 60000.0    # the largest fp16 numbers, squares of 4e9
+    check(W, h, y, w, post=p)
+    out = W.block_norm(h, y, weight=w, post_weight=p)[1]
+    assert bool((out[0] == 0).all())
+    h2, y2 = h[:3].half(), y[:3].clone()
+    h2[2] = 1.0
+    y2[1, 7], h2[2, 9] = float("inf"), float("nan")  # stay in their rows
+    a, x = W.block_norm(h2, y2, weight=w)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(x[0]).all()) and bool(torch.isinf(a[1, 7])) and bool(torch.isnan(x[2]).any())
+
+
+def test_replayed_on_another_stream(W):
+    h, y, w, p, g = make(64, 5120)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    direct = W.block_norm(h, y, weight=w, post_weight=p, gate=g, stream=s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        captured = W.block_norm(h, y, weight=w, post_weight=p, gate=g)
+    y.mul_(0.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    again = W.block_norm(h, y, weight=w, post_weight=p, gate=g)
+    torch.cuda.synchronize()
+    assert torch.equal(captured[0], again[0]) and torch.equal(captured[1], again[1])
+    assert not torch.equal(direct[1], again[1])
+
+
+def test_the_index_checking_build_gives_the_same(W):
+    D = W.load_debug_bounds()
+    h, y, w, p, g = make(5, 1336)
+    a, x = torch.empty_like(h), torch.empty_like(h)
+    s = torch.cuda.current_stream().cuda_stream
+    assert D.w4a16_block_norm(h.data_ptr(), 1336, 0, y.data_ptr(), 1336, p.data_ptr(), g.data_ptr(), 1336, 0, 0.5, w.data_ptr(), 0.0, 1e-6,
+                              a.data_ptr(), x.data_ptr(), 5, 1336, s) == 0
+    torch.cuda.synchronize()
+    assert D.w4a16_device_status(s) == W.OK
+    b = W.block_norm(h, y, weight=w, post_weight=p, gate=g, scale=0.5)
+    assert torch.equal(a, b[0]) and torch.equal(x, b[1])

@@ -1,0 +1,281 @@
+"""The mixture-of-experts layer against 64 bits.
+
+Choice: logits are sums of exact fp16 products in fp32; a chain is H / 512 + 9 roundings long at most, so a logit is
+off by less than 2^-19 of sum|x router| for H <= 5120. A choice has to be one that logits within that bound allow;
+the rest is compared for the choice made.
+Products: an instruction adds 16 products to an fp32 sum, off by 2^-21 of sum|x w| at most; with up to 2^5 in a chain and
+the warps' sums, below 2^-16 of sum|x w|. a = silu(g) u is off by 1.1 |u| dg + |silu(g)| du, 2^-20 of itself for the
+fp32 exponential and division, and its rounding, 2^-11 (2^-25 among subnormals). y by sum r (da |Wd|), 2^-16 of
+sum r |a Wd|, the weights' own error (twice that of a logit, and 2^-20), and 2^-11 of itself."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import w4a16_inputs as inputs
+from gpu_util import lib
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def W():
+    return lib()
+
+
+def dequantised(q, s, group):
+    """float64 [E, K, N] of int4 codes [E, K / 8, N] (int32) and fp16 scales: one rounding to fp16."""
+    k = torch.arange(8, device=q.device) * 4
+    code = ((q[:, :, None, :] >> k[None, None, :, None]) & 15).flatten(1, 2) - 8
+    return (code.float() * s.float().repeat_interleave(group, 1)).half().double()
+
+
+E2M1 = [0, 0.5, 1, 1.5, 2, 3, 4, 6]
+
+
+def dequantised_nvfp4(q, s8, factor):
+    k = torch.arange(8, device=q.device) * 4
+    code = ((q[:, :, None, :] >> k[None, None, :, None]) & 15).flatten(1, 2).long()
+    value = torch.tensor(E2M1 + [-v for v in E2M1], dtype=torch.float64, device=q.device)[code]
+    scale = s8.view(torch.float8_e4m3fn).double().repeat_interleave(16, 1)
+    return value * scale * factor.double()[:, None, None]
+
+
+class Layer:
+    def __init__(self, W, E, H, I, group=64, seed=0, nvfp4=False):
+        g = torch.Generator("cuda").manual_seed(seed)
+        self.E, self.H, self.I = E, H, I
+
+        def codes(rows, cols):
+            return torch.randint(-2 ** 31, 2 ** 31, (E, rows // 8, cols), generator=g, device="cuda", dtype=torch.int32)
+
+        up, down = codes(H, 2 * I), codes(I, H)
+        if nvfp4:
+            s = [torch.randint(0x30, 0x40, (E, r // 16, c), generator=g, device="cuda").to(torch.uint8) for r, c in ((H, 2 * I), (I, H))]
+            f = [(1 + torch.rand(E, generator=g, device="cuda")) / 256 for _ in range(2)]
+            self.m = W.Experts(up, s[0], down, s[1], gate_up_scale=f[0], down_scale=f[1])
+            self.up, self.down = dequantised_nvfp4(up, s[0], f[0]), dequantised_nvfp4(down, s[1], f[1])
+        else:
+            s = [(0.004 * (1 + torch.rand((E, r // group, c), generator=g, device="cuda"))).half() for r, c in ((H, 2 * I), (I, H))]
+            self.m = W.Experts(up, s[0], down, s[1], group)
+            self.up, self.down = dequantised(up, s[0], group), dequantised(down, s[1], group)
+        self.router = (torch.randn((E, H), generator=g, device="cuda") * 1.5 / H ** 0.5).half()
+        self.bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+        self.work = W.moe_workspace(self.m)
+
+    def x(self, T, seed=0):
+        g = torch.Generator("cuda").manual_seed(seed + 7 * T)
+        return torch.randn((T, self.H), generator=g, device="cuda").half()
+
+
+def check(W, L, x, k, sigmoid=False, renormalize=True, scale=1.0, bias=None, result=None, work=None):
+    y, ids, w = result or W.moe(x, L.m, L.router, k, L.work if work is None else work, bias=bias, sigmoid=sigmoid,
+                                renormalize=renormalize, scale=scale)
+    torch.cuda.synchronize()
+    assert W.w4a16_device_status() == W.OK
+    T = x.shape[0]
+    xd, r = x.double(), L.router.double()
+    logits, off = xd @ r.T, 2.0 ** -19 * (xd.abs() @ r.abs().T)
+    score = torch.sigmoid(logits) if sigmoid else torch.softmax(logits, 1)
+    key = score + (0 if bias is None else bias.double()) if sigmoid else logits
+    key_off = off / 4 + 2.0 ** -22 if sigmoid else off
+    chosen = ids.long()
+    assert int(chosen.min()) >= 0 and int(chosen.max()) < L.E
+    picked = torch.zeros_like(key, dtype=torch.bool).scatter(1, chosen, True)
+    assert bool((picked.sum(1) == k).all())  # all different
+    worst_in = (key + key_off).gather(1, chosen).amin(1)
+    best_out = torch.where(picked, -torch.inf, key - key_off).amax(1)
+    assert bool((worst_in >= best_out).all())
+    got = key.gather(1, chosen)
+    slack = key_off.gather(1, chosen)
+    assert bool((got[:, :-1] + slack[:, :-1] >= got[:, 1:] - slack[:, 1:]).all())  # in order
+    s = score.gather(1, chosen)
+    s = s / s.sum(1, keepdim=True) if renormalize else s
+    rel = 2 * off.amax(1, keepdim=True) + 2.0 ** -20
+    assert bool(((w.double() - scale * s).abs() <= rel * scale * s).all())
+    ref, bound = torch.zeros_like(xd), torch.zeros_like(xd)
+    for e in range(L.E):
+        t, j = (chosen == e).nonzero(as_tuple=True)
+        if len(t) == 0:
+            continue
+        both, mass = xd[t] @ L.up[e], xd[t].abs() @ L.up[e].abs() * 2.0 ** -16
+        g, u, dg, du = both[:, :L.I], both[:, L.I:], mass[:, :L.I], mass[:, L.I:]
+        a = g * torch.sigmoid(g) * u
+        da = 1.1 * u.abs() * dg + (g * torch.sigmoid(g)).abs() * du + 1.1 * dg * du + (2.0 ** -11 + 2.0 ** -20) * a.abs() + 2.0 ** -25
+        weight = scale * s[t, j][:, None]
+        ref.index_add_(0, t, weight * (a @ L.down[e]))
+        sums = a.abs() @ L.down[e].abs()
+        bound.index_add_(0, t, weight * (da @ L.down[e].abs() + (2.0 ** -16 + rel[t]) * sums))
+    bound += 2.0 ** -11 * ref.abs() + 2.0 ** -25
+    assert bool(((y.double() - ref).abs() <= bound * 1.01).all()), float(((y.double() - ref).abs() / bound).max())
+    # the bound is a worst case; errors are independent, so a lost expert or token would still be far outside this
+    assert float((y.double() - ref).norm() / ref.norm()) < 2.0 ** -10
+    return y, ids, w
+
+
+# (experts, hidden, inner, group): odd counts, K not a multiple of 128, one group a row, a single column tile
+SHAPES = [(4, 128, 128, 128), (5, 192, 64, 64), (24, 1280, 448, 64), (16, 320, 320, 32), (7, 640, 960, 160), (40, 512, 192, 64), (3, 64, 576, 32)]
+
+
+@pytest.mark.parametrize("E,H,I,G", SHAPES)
+@pytest.mark.parametrize("T", [1, 2, 5, 8, 9, 17, 33, 64])
+def test_sizes(W, E, H, I, G, T):
+    L = Layer(W, E, H, I, G, seed=E)
+    x = L.x(T)
+    check(W, L, x, min(2, E))
+    check(W, L, x, min(6, E), sigmoid=True, bias=L.bias, scale=2.5)
+    check(W, L, x, 1, renormalize=False)
+    check(W, L, x, E if E <= 16 else 16, sigmoid=True, renormalize=False)
+
+
+@pytest.mark.parametrize("T", [1, 6, 20, 64])
+def test_nvfp4_experts(W, T):
+    for E, H, I in ((8, 256, 192), (5, 192, 448)):
+        L = Layer(W, E, H, I, nvfp4=True, seed=3)
+        check(W, L, L.x(T), 3)
+
+
+@pytest.mark.parametrize("T", [1, 16, 64])
+def test_the_dense_layers_width(W, T):
+    L = Layer(W, 12, 5120, 2176, 128, seed=1)
+    check(W, L, L.x(T), 8)
+
+
+def test_many_experts(W):
+    L = Layer(W, 512, 128, 64, 64, seed=2)
+    for T in (1, 64):
+        check(W, L, L.x(T), 16, sigmoid=True, bias=L.bias)
+        check(W, L, L.x(T), 8, renormalize=False)
+
+
+@pytest.mark.parametrize("T", [9, 64])
+def test_every_token_to_the_same_experts(W, T):
+    L = Layer(W, 16, 256, 192, 64, seed=4)
+    bias = torch.zeros(16, device="cuda")
+    bias[5], bias[11] = 10.0, 20.0
+    _, ids, _ = check(W, L, L.x(T), 2, sigmoid=True, bias=bias)
+    assert ids.tolist() == [[11, 5]] * T
+
+
+def test_ties_go_to_the_lower_index(W):
+    L = Layer(W, 40, 256, 64, 64, seed=5)
+    L.router[:] = L.router[7]
+    for sigmoid in (False, True):
+        _, ids, w = check(W, L, L.x(11), 5, sigmoid=sigmoid)
+        assert ids.tolist() == [[0, 1, 2, 3, 4]] * 11
+        assert torch.allclose(w, torch.full_like(w, 0.2), rtol=1e-6)
+    L.router[33] = 2 * L.router[33]
+    x = L.x(11)
+    _, ids, _ = W.moe(x, L.m, L.router, 3, L.work)
+    up = (x.double() @ L.router[33].double()) > 0
+    assert all(r == ([33, 0, 1] if u else [0, 1, 2]) for r, u in zip(ids.tolist(), up.tolist()))
+
+
+def test_infinities_and_nan_stay_in_their_row(W):
+    L = Layer(W, 12, 256, 128, 64, seed=6)
+    x = L.x(20)
+    want, ids, _ = W.moe(x, L.m, L.router, 4, L.work)
+    bad = x.clone()
+    bad[3, 17], bad[9] = float("nan"), float("inf")
+    got, got_ids, _ = W.moe(bad, L.m, L.router, 4, L.work)
+    torch.cuda.synchronize()
+    rest = [t for t in range(20) if t not in (3, 9)]
+    assert torch.equal(got_ids[rest], ids[rest])
+    # the list of experts may differ by the bad rows' choices, and with it the order of sums
+    assert bool(((got[rest].double() - want[rest].double()).abs() <= 2.0 ** -9 * want[rest].double().abs().amax()).all())
+    assert bool(torch.isnan(got[3]).all()) and int(got_ids.min()) >= 0 and int(got_ids.max()) < 12
+    assert got_ids[3].tolist() == [0, 1, 2, 3]
+
+
+def test_rows_with_a_stride_and_given_outputs(W):
+    L = Layer(W, 6, 192, 128, 64, seed=7)
+    wide = torch.randn((10, 264), device="cuda").half()
+    check(W, L, wide[:, 8:200], 2)
+    check(W, L, wide[4:5, 8:200], 2)
+    y = torch.full((10, 192), 7.0, device="cuda").half()
+    a = W.moe(wide[:, 8:200], L.m, L.router, 2, L.work, out=(y, None, None))
+    b = W.moe(wide[:, 8:200], L.m, L.router, 2, L.work)
+    torch.cuda.synchronize()
+    assert a[0] is y and torch.equal(y, b[0])
+
+
+def test_repeats_batches_and_a_shared_workspace(W):
+    L = Layer(W, 24, 512, 320, 64, seed=8)
+    x = L.x(48)
+    first = W.moe(x, L.m, L.router, 4, L.work)
+    for T in (1, 7, 48, 13, 48):  # the workspace is ready for any batch after any other
+        again = W.moe(x[:T], L.m, L.router, 4, L.work)
+        if T == 48:
+            assert all(torch.equal(a, b) for a, b in zip(first, again))
+        else:
+            check(W, L, x[:T], 4, result=again)
+
+
+def test_replayed_and_chained_calls(W):
+    L = Layer(W, 16, 512, 256, 128, seed=9)
+    x = L.x(5)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    W.moe(x, L.m, L.router, 2, L.work, stream=s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):  # the second layer takes the first one's output
+        a = W.moe(x, L.m, L.router, 2, L.work)
+        b = W.moe(a[0], L.m, L.router, 3, L.work, sigmoid=True)
+    x.copy_(L.x(5, seed=33))
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    check(W, L, x, 2, result=a)
+    check(W, L, a[0], 3, sigmoid=True, result=b)
+
+
+def test_two_calls_at_once_with_their_own_workspaces(W):
+    L = Layer(W, 16, 512, 256, 128, seed=10)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    work = [L.work, W.moe_workspace(L.m)]
+    xs = [L.x(8, seed=1), L.x(40, seed=2)]
+    torch.cuda.synchronize()
+    out = [None, None]
+    for _ in range(10):
+        for i in range(2):
+            out[i] = W.moe(xs[i], L.m, L.router, 3, work[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        check(W, L, xs[i], 3, result=out[i])
+
+
+@pytest.mark.parametrize("nvfp4", [False, True])
+def test_the_index_checking_build_gives_the_same(W, nvfp4):
+    D = W.load_debug_bounds()
+    L = Layer(W, 9, 320, 192, 64, seed=11, nvfp4=nvfp4)
+    s = torch.cuda.current_stream().cuda_stream
+    for T in (1, 21):
+        x = L.x(T)
+        want = W.moe(x, L.m, L.router, 3, L.work)
+        got = [torch.empty_like(v) for v in want]
+        assert D.w4a16_moe(x.data_ptr(), 320, L.m.ref, L.router.data_ptr(), None, 3, 0, 1, 1.0, *(v.data_ptr() for v in got), T,
+                           L.work.data_ptr(), L.work.numel(), s) == 0
+        torch.cuda.synchronize()
+        assert D.w4a16_device_status(s) == W.OK
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_one_expert_is_the_dense_layer(W):
+    """One expert that every token takes with weight 1: gemm, silu_mul and gemm of the same matrices, within the bounds."""
+    H, I, G, T = 512, 256, 128, 12
+    d = [inputs.generate_weights(H, 2 * I, G, seed=1), inputs.generate_weights(I, H, G, seed=2)]
+    t = [(torch.from_numpy(q).cuda(), torch.from_numpy(s.view(np.int16)).cuda().view(torch.float16)) for q, s in d]
+    m = W.Experts(t[0][0][None], t[0][1][None], t[1][0][None], t[1][1][None], G)
+    x = torch.randn((T, H), device="cuda").half()
+    y, ids, w = W.moe(x, m, torch.randn((1, H), device="cuda").half(), 1, W.moe_workspace(m))
+    up = [W.repack(q, s.view(torch.int16), G) for q, s in t]
+    act = W.silu_mul(W.gemm(x, *up[0], 2 * I, H, G))
+    dense = W.gemm(act, *up[1], H, I, G)
+    torch.cuda.synchronize()
+    assert bool((ids == 0).all()) and bool((w == 1).all())
+    y_ref, abs_ref = oracle.gemm(act.cpu().numpy().view(np.uint16), d[1][0], d[1][1], G)
+    # gate and up rounded to fp16 there: 2^-11 of each, so act by 2^-9 at most
+    assert bool((np.abs(y.double().cpu().numpy() - y_ref) <= 2.0 ** -10 * np.abs(y_ref) + 2.0 ** -8 * abs_ref).all())
+    assert bool(((y.double() - dense.double()).abs() <= 0.02 * dense.double().abs().amax()).all())

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -51,6 +52,7 @@ EXPORTED = [
     "w4a16_kv4_attention_workspace_bytes", "w4a16_kv4_attention", "w4a16_kv4_attention_ex",
     "w4a16_kv4_attention_kernel", "w4a16_kv4_selftest_wait_timeout", "w4a16_kv4_selftest_withhold",
     "w4a16_sample",
+    "w4a16_logprobs", "w4a16_block_norm", "w4a16_moe_workspace_bytes", "w4a16_moe",
 ]
 
 
@@ -71,6 +73,15 @@ class KV4Desc(ctypes.Structure):
 
     _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_tokens", ctypes.c_int),
                 ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class MoEDesc(ctypes.Structure):
+    """Mirror of ``w4a16_moe_experts``."""
+
+    _fields_ = [("gate_up_q", ctypes.c_void_p), ("gate_up_s", ctypes.c_void_p), ("down_q", ctypes.c_void_p),
+                ("down_s", ctypes.c_void_p), ("gate_up_scale", ctypes.c_void_p), ("down_scale", ctypes.c_void_p),
+                ("experts", ctypes.c_int), ("hidden", ctypes.c_int), ("inner", ctypes.c_int), ("group", ctypes.c_int),
+                ("nvfp4", ctypes.c_int)]
 
 
 class W4A16Error(RuntimeError):
@@ -155,6 +166,14 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.w4a16_kv4_selftest_withhold.argtypes = [I]
     lib.w4a16_sample.restype = I
     lib.w4a16_sample.argtypes = [P, L, I, I, P, P, P, P, P, P, P, P]
+    lib.w4a16_logprobs.restype = I
+    lib.w4a16_logprobs.argtypes = [P, L, I, I, P, I, I, P, P, P, P, P, P, P]
+    lib.w4a16_block_norm.restype = I
+    lib.w4a16_block_norm.argtypes = [P, L, I, P, L, P, P, L, I, F, P, F, F, P, P, I, I, P]
+    lib.w4a16_moe_workspace_bytes.restype = S
+    lib.w4a16_moe_workspace_bytes.argtypes = [I, I, I]
+    lib.w4a16_moe.restype = I
+    lib.w4a16_moe.argtypes = [P, L, ctypes.POINTER(MoEDesc), P, P, I, I, I, F, P, P, P, I, P, S, P]
     return lib
 
 
@@ -505,6 +524,31 @@ def w4a16_sample(logits: int, stride: int, M: int, V: int, temperature: int | No
     return lib.w4a16_sample(logits, stride, M, V, temperature, top_k, top_p, min_p, u, tokens, probs, stream)
 
 
+def w4a16_logprobs(logits: int, stride: int, M: int, V: int, tokens: int | None, given: int, top: int,
+                   temperature: int | None, logprob: int | None, rank: int | None, entropy: int | None,
+                   top_tokens: int | None, top_logprob: int | None, stream: int | None) -> int:
+    return lib.w4a16_logprobs(logits, stride, M, V, tokens, given, top, temperature, logprob, rank, entropy, top_tokens,
+                              top_logprob, stream)
+
+
+def w4a16_block_norm(h: int, h_stride: int, h_f32: int, y: int | None, y_stride: int, post_weight: int | None,
+                     gate: int | None, gate_stride: int, gate_per_row: int, scale: float, weight: int | None, offset: float,
+                     eps: float, h_out: int | None, x: int | None, M: int, H: int, stream: int | None) -> int:
+    return lib.w4a16_block_norm(h, h_stride, h_f32, y, y_stride, post_weight, gate, gate_stride, gate_per_row, scale, weight,
+                                offset, eps, h_out, x, M, H, stream)
+
+
+def w4a16_moe_workspace_bytes(experts: int, hidden: int, inner: int) -> int:
+    return lib.w4a16_moe_workspace_bytes(experts, hidden, inner)
+
+
+def w4a16_moe(x: int, x_stride: int, experts: MoEDesc, router: int, bias: int | None, top_k: int, scoring: int,
+              renormalize: int, scale: float, y: int, ids: int | None, weights: int | None, tokens: int, workspace: int,
+              workspace_bytes: int, stream: int | None) -> int:
+    return lib.w4a16_moe(x, x_stride, ctypes.byref(experts), router, bias, top_k, scoring, renormalize, scale, y, ids, weights,
+                         tokens, workspace, workspace_bytes, stream)
+
+
 def _ptr(t: torch.Tensor | None) -> int | None:
     return t.data_ptr() if t is not None else None
 
@@ -664,3 +708,173 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=None, top_k=None, 
     if rc != OK:
         raise W4A16Error(rc, "w4a16_sample")
     return tokens, probs
+
+
+class LogProbs(NamedTuple):
+    """What `logprobs` gives; None for what was not asked for."""
+
+    logprob: torch.Tensor | None       # float32, like `tokens`
+    rank: torch.Tensor | None          # int32, like `tokens`
+    entropy: torch.Tensor              # float32 [M]
+    top_tokens: torch.Tensor | None    # int32 [M, top]
+    top_logprob: torch.Tensor | None   # float32 [M, top]
+
+
+def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0, temperature=None, out: LogProbs | None = None,
+             stream=None) -> LogProbs:
+    """Of every row of logits [M, V] (float16, rows of any stride): log probabilities and ranks (from 1) of `tokens`
+    (int32 [M] or [M, up to 8]; a negative one: 0 and rank 0), the entropy, the first `top` (up to 32) tokens in the
+    order of `sample`. temperature float32 [M], or None for 1."""
+    f, i32 = torch.float32, torch.int32
+    if not (logits.dtype is torch.float16 and logits.is_cuda and logits.dim() == 2 and logits.stride(1) == 1):
+        _refuse("logprobs", "logits must be a CUDA float16 tensor [M, V], dense in a row")
+    M, V = logits.shape
+    shape, given = None, 0
+    if tokens is not None:
+        if not (tokens.dtype is i32 and tokens.is_cuda and tokens.dim() in (1, 2) and tokens.shape[0] == M and tokens.is_contiguous()):
+            _refuse("logprobs", "tokens must be a contiguous CUDA int32 tensor [M] or [M, n]")
+        shape, given = tuple(tokens.shape), 1 if tokens.dim() == 1 else tokens.shape[1]
+        if given == 0:
+            _refuse("logprobs", "tokens [M, n] must have an n above 0")
+    if not _vec(temperature, f, M):
+        _refuse("logprobs", "temperature must be a CUDA float32 vector of M elements")
+    if top < 0:
+        _refuse("logprobs", "top must not be negative")
+    if out is None:
+        def new(n, dtype):
+            return None if n is None else _new(n, dtype, logits.device, stream)
+        tops = (M, top) if top else None
+        out = LogProbs(new(shape, f), new(shape, i32), new((M,), f), new(tops, i32), new(tops, f))
+    elif not ((out.logprob is None or shape) and (out.rank is None or shape) and _dense(out.logprob, f, shape)
+              and _dense(out.rank, i32, shape) and _vec(out.entropy, f, M) and _dense(out.top_tokens, i32, (M, top))
+              and _dense(out.top_logprob, f, (M, top)) and (top > 0) == (out.top_tokens is not None) == (out.top_logprob is not None)):
+        _refuse("logprobs", "out must be LogProbs of contiguous CUDA tensors of the result's shapes")
+    rc = lib.w4a16_logprobs(logits.data_ptr(), logits.stride(0), M, V, _ptr(tokens), given, top, _ptr(temperature),
+                            _ptr(out.logprob), _ptr(out.rank), _ptr(out.entropy), _ptr(out.top_tokens), _ptr(out.top_logprob),
+                            _stream_handle(stream))
+    if rc != OK:
+        raise W4A16Error(rc, "w4a16_logprobs")
+    return out
+
+
+# ------------------------------------------------------------------------------ around a block
+def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, weight=None, post_weight=None, gate=None, scale: float = 1.0,
+               eps: float = 1e-6, offset: float = 0.0, out=None, stream=None):
+    """(h', x): h' = h + scale * gate * z on the residual stream h [M, H] (float16 or float32), z the block's output y
+    (float16) or, with post_weight, its norm; x (float16) the norm of h'. Norms multiply by offset + weight (float16 [H];
+    weight None: by 1). gate (float16): [H], [M, H] or [M, 1]. Without y: x is the norm of h, and h' is h. out: the pair to
+    write, where h' may be h itself and x None; an h' of None is not written."""
+    half = torch.float16
+    if not (h.dtype in (half, torch.float32) and h.is_cuda and h.dim() == 2 and h.stride(1) == 1):
+        _refuse("block_norm", "h must be a CUDA float16 or float32 tensor [M, H], dense in a row")
+    M, H = h.shape
+    if y is not None and not (y.dtype is half and y.is_cuda and y.shape == h.shape and y.stride(1) == 1):
+        _refuse("block_norm", "y must be a CUDA float16 tensor of h's shape, dense in a row")
+    if y is None and (post_weight is not None or gate is not None):
+        _refuse("block_norm", "post_weight and gate need y")
+    if not (_vec(weight, half, H) and _vec(post_weight, half, H)):
+        _refuse("block_norm", "weight and post_weight must be contiguous CUDA float16 vectors of H elements")
+    gate_stride = per_row = 0
+    if gate is not None:
+        wide = gate.dim() == 2 and gate.shape[0] == M and gate.shape[1] in (1, H)
+        if not (gate.dtype is half and gate.is_cuda and (wide or gate.shape == (H,)) and (gate.shape[-1] == 1 or gate.stride(-1) == 1)):
+            _refuse("block_norm", "gate must be a CUDA float16 tensor [H], [M, H] or [M, 1], dense in a row")
+        gate_stride = gate.stride(0) if wide else 0
+        per_row = int(wide and gate.shape[1] == 1 and H != 1)
+    if out is None:
+        h_out = h if y is None else _new((M, H), h.dtype, h.device, stream)
+        x = _new((M, H), half, h.device, stream)
+    else:
+        h_out, x = out
+        if not (_dense(h_out, h.dtype, (M, H)) and _dense(x, half, (M, H))):
+            _refuse("block_norm", "out must be contiguous CUDA tensors [M, H]: one of h's type, one float16")
+    write_h = h_out is not None and not (y is None and h_out is h)
+    rc = lib.w4a16_block_norm(h.data_ptr(), h.stride(0), int(h.dtype is torch.float32), _ptr(y), 0 if y is None else y.stride(0),
+                              _ptr(post_weight), _ptr(gate), gate_stride, per_row, scale, _ptr(weight), offset, eps,
+                              h_out.data_ptr() if write_h else None, _ptr(x), M, H, _stream_handle(stream))
+    if rc != OK:
+        raise W4A16Error(rc, "w4a16_block_norm")
+    return h_out, x
+
+
+# ------------------------------------------------------------------------------ experts
+class Experts:
+    """The matrices of a mixture-of-experts layer in the device layout, repacked once: gate_up int4 [E, hidden / 8,
+    2 inner] (gate columns first) and down [E, inner / 8, hidden] with their scales float16 [E, rows / group, columns].
+    With gate_up_scale and down_scale (float32 [E], the tensor scales) the codes are NVFP4 and the scales
+    uint8 [E, rows / 16, columns]."""
+
+    def __init__(self, gate_up: torch.Tensor, gate_up_scales: torch.Tensor, down: torch.Tensor, down_scales: torch.Tensor,
+                 group: int = 128, gate_up_scale: torch.Tensor | None = None, down_scale: torch.Tensor | None = None, stream=None):
+        nvfp4 = gate_up_scale is not None
+        E = gate_up.shape[0]
+        self.experts, self.hidden, self.inner = E, gate_up.shape[1] * 8, gate_up.shape[2] // 2
+        rows = 16 if nvfp4 else group
+        if group <= 0 or not all(t.is_cuda and t.dim() == 3 and t.is_contiguous() for t in (gate_up, gate_up_scales, down, down_scales)):
+            _refuse("Experts", "gate_up, down and their scales must be contiguous CUDA tensors [E, rows, columns]")
+        half = (torch.uint8,) if nvfp4 else (torch.float16, torch.int16)
+        if not (gate_up.dtype is torch.int32 and down.dtype is torch.int32 and gate_up_scales.dtype in half and down_scales.dtype in half
+                and gate_up.shape[2] == 2 * self.inner and tuple(down.shape) == (E, self.inner // 8, self.hidden)
+                and tuple(gate_up_scales.shape) == (E, self.hidden // rows, 2 * self.inner)
+                and tuple(down_scales.shape) == (E, self.inner // rows, self.hidden)):
+            _refuse("Experts", "codes must be int32 [E, rows / 8, columns], scales [E, rows / group, columns], of one hidden and inner size")
+        if nvfp4 != (down_scale is not None) or not (_vec(gate_up_scale, torch.float32, E) and _vec(down_scale, torch.float32, E)):
+            _refuse("Experts", "gate_up_scale and down_scale must be CUDA float32 vectors of E elements, or both None")
+        if w4a16_moe_workspace_bytes(E, self.hidden, self.inner) == 0:
+            raise W4A16Error(ERR_UNSUPPORTED_SHAPE, "Experts")
+
+        def stacked(codes, scales):
+            pairs = []
+            for e in range(E):
+                pairs.append(repack_nvfp4(codes[e], scales[e], stream) if nvfp4 else repack(codes[e], scales[e], group, stream))
+            if stream is None:
+                return torch.stack([q for q, _ in pairs]), torch.stack([s for _, s in pairs])
+            with torch.cuda.stream(stream):
+                return torch.stack([q for q, _ in pairs]), torch.stack([s for _, s in pairs])
+
+        self.group, self.nvfp4 = rows, nvfp4
+        self.gate_up, self.down = stacked(gate_up, gate_up_scales), stacked(down, down_scales)
+        self.scales = (gate_up_scale, down_scale)
+        self.desc = MoEDesc(*(t.data_ptr() for t in self.gate_up + self.down), _ptr(gate_up_scale), _ptr(down_scale), E,
+                            self.hidden, self.inner, rows, int(nvfp4))
+        self.ref = ctypes.byref(self.desc)
+
+
+def moe_workspace(experts: Experts) -> torch.Tensor:
+    """Device memory for moe calls on `experts` (or others of their shape) that follow one another on one stream;
+    calls that may overlap need one each."""
+    return torch.zeros(w4a16_moe_workspace_bytes(experts.experts, experts.hidden, experts.inner), dtype=torch.uint8,
+                       device=experts.gate_up[0].device)
+
+
+def moe(x: torch.Tensor, experts: Experts, router: torch.Tensor, top_k: int, workspace: torch.Tensor,
+        bias: torch.Tensor | None = None, sigmoid: bool = False, renormalize: bool = True, scale: float = 1.0, out=None, stream=None):
+    """(y, ids, weights) of a mixture-of-experts layer on x [T, hidden] (float16, up to 64 tokens): y float16 [T, hidden],
+    the chosen experts int32 [T, top_k] in order and their weights float32 [T, top_k]. router float16 [E, hidden]; scores by
+    softmax or sigmoid, bias float32 [E] for the choice only (sigmoid); renormalize: the chosen ones' scores add up to 1
+    before `scale`. out: the three tensors to write (ids and weights may be None)."""
+    half, E, H = torch.float16, experts.experts, experts.hidden
+    if not (x.dtype is half and x.is_cuda and x.dim() == 2 and x.shape[1] == H and x.stride(1) == 1):
+        _refuse("moe", "x must be a CUDA float16 tensor [T, hidden], dense in a row")
+    if not _dense(router, half, (E, H)) or router is None:
+        _refuse("moe", "router must be a contiguous CUDA float16 tensor [E, hidden]")
+    if not _vec(bias, torch.float32, E):
+        _refuse("moe", "bias must be a CUDA float32 vector of E elements")
+    if not (workspace.dtype is torch.uint8 and workspace.is_cuda and workspace.is_contiguous()):
+        _refuse("moe", "workspace must come from moe_workspace")
+    if not 1 <= top_k <= E:
+        _refuse("moe", "top_k must be from 1 to the number of experts")
+    T = x.shape[0]
+    if out is None:
+        y = _new((T, H), half, x.device, stream)
+        ids, weights = _new((T, top_k), torch.int32, x.device, stream), _new((T, top_k), torch.float32, x.device, stream)
+    else:
+        y, ids, weights = out
+        if y is None or not (_dense(y, half, (T, H)) and _dense(ids, torch.int32, (T, top_k)) and _dense(weights, torch.float32, (T, top_k))):
+            _refuse("moe", "out must be contiguous CUDA tensors: float16 [T, hidden], int32 and float32 [T, top_k]")
+    rc = lib.w4a16_moe(x.data_ptr(), x.stride(0), experts.ref, router.data_ptr(), _ptr(bias), top_k, int(sigmoid), int(renormalize),
+                       scale, y.data_ptr(), _ptr(ids), _ptr(weights), T, workspace.data_ptr(), workspace.numel(),
+                       _stream_handle(stream))
+    if rc != OK:
+        raise W4A16Error(rc, "w4a16_moe")
+    return y, ids, weights

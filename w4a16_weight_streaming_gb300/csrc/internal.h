@@ -169,4 +169,77 @@ struct SampleParams {
 };
 cudaError_t launch_sample(const SampleParams& p, int sm_count, cudaStream_t s, unsigned* status);
 
+// ---- norm.cu: residual stream and norms around a block
+struct BlockNormParams {
+    const void* h;  // fp16, or fp32 with h_f32
+    const uint16_t* y;
+    const uint16_t* post;
+    const uint16_t* gate;
+    const uint16_t* weight;
+    void* h_out;
+    uint16_t* x;
+    int64_t h_stride;
+    int64_t y_stride;
+    int64_t gate_stride;
+    int M;
+    int H;
+    int h_f32;
+    int gate_per_row;
+    float scale;
+    float offset;
+    float eps;
+};
+cudaError_t launch_block_norm(const BlockNormParams& p, int sm_count, cudaStream_t s, unsigned* status);
+
+// ---- logprobs.cu
+struct LogprobParams {
+    const uint16_t* logits;
+    int64_t stride;
+    int M;
+    int V;
+    const int32_t* tokens;
+    int given;  // tokens a row, 0..8
+    int top;    // 0..32
+    const float* temperature;
+    float* logprob;
+    int32_t* rank;
+    float* entropy;
+    int32_t* top_tokens;
+    float* top_logprob;
+};
+cudaError_t launch_logprobs(const LogprobParams& p, int sm_count, cudaStream_t s, unsigned* status);
+
+// ---- moe.cu: a mixture-of-experts layer for up to 64 tokens
+constexpr int kMoeMaxTokens = 64;
+constexpr int kMoeMaxTop = 16;
+constexpr int kMoeMaxExperts = 512;
+struct MoeParams {
+    const uint16_t* x;
+    int64_t x_stride;
+    const uint16_t* router;
+    const float* bias;
+    const void* gate_up_q;  // repacked [H, 2 I] of every expert, one after another
+    const uint16_t* gate_up_s;
+    const void* down_q;  // repacked [I, H]
+    const uint16_t* down_s;
+    const float* gate_up_factor;  // NVFP4: fp32 scale of each expert's matrix
+    const float* down_factor;
+    uint16_t* y;
+    int32_t* ids;
+    float* weights;
+    void* workspace;
+    int T;
+    int E;
+    int H;
+    int I;
+    int G;  // 16 for NVFP4
+    int k;
+    int nvfp4;
+    int sigmoid;
+    int renormalize;
+    float scale;
+};
+size_t moe_workspace_bytes(int E, int H, int I);
+cudaError_t launch_moe(const MoeParams& p, int sm_count, cudaStream_t s, unsigned* status);
+
 }  // namespace w4a16

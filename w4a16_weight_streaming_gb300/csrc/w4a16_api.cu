@@ -1213,6 +1213,141 @@ int w4a16_sample(const uint16_t* logits, int64_t stride, int M, int V, const flo
     return launched(launch_sample(p, d.sm_count, static_cast<cudaStream_t>(stream), d.status));
 }
 
+namespace {
+
+struct Span {
+    const void* p;  // NULL: not there
+    size_t n;
+};
+
+// INVALID_ARG where a written span overlaps another of them or a read one, or memory lies elsewhere; `same` is a
+// read span that written[0] may be.
+int check_spans(const Span* written, int nw, const Span* read, int nr, const void* same = nullptr) {
+    for (int i = 0; i < nw; ++i) {
+        if (!written[i].p) continue;
+        if (elsewhere(written[i].p)) return W4A16_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (written[j].p && overlaps(written[i].p, written[i].n, written[j].p, written[j].n)) return W4A16_ERR_INVALID_ARG;
+        for (int j = 0; j < nr; ++j) {
+            if (!read[j].p || (i == 0 && j == 0 && same != nullptr && written[0].p == same)) continue;
+            if (overlaps(written[i].p, written[i].n, read[j].p, read[j].n)) return W4A16_ERR_INVALID_ARG;
+        }
+    }
+    for (int j = 0; j < nr; ++j)
+        if (read[j].p && elsewhere(read[j].p)) return W4A16_ERR_INVALID_ARG;
+    return W4A16_OK;
+}
+
+}  // namespace
+
+int w4a16_logprobs(const uint16_t* logits, int64_t stride, int M, int V, const int32_t* tokens, int given, int top,
+                   const float* temperature, float* logprob, int32_t* rank, float* entropy, int32_t* top_tokens,
+                   float* top_logprob, void* stream) {
+    if (!logits || M <= 0 || V <= 0 || given < 0 || top < 0 || (stride < V && M > 1)) return W4A16_ERR_INVALID_ARG;
+    if ((given > 0) != (tokens != nullptr) || (top > 0) != (top_tokens != nullptr) || (top > 0) != (top_logprob != nullptr))
+        return W4A16_ERR_INVALID_ARG;
+    if (given == 0 && (logprob || rank)) return W4A16_ERR_INVALID_ARG;
+    if (!logprob && !rank && !entropy && !top_tokens) return W4A16_ERR_INVALID_ARG;
+    if (M > 65536 || V > 1000000 || given > 8 || top > 32 || stride > (1LL << 32)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if ((reinterpret_cast<uintptr_t>(logits) & 1u) != 0 || !aligned4(tokens) || !aligned4(temperature) || !aligned4(logprob) ||
+        !aligned4(rank) || !aligned4(entropy) || !aligned4(top_tokens) || !aligned4(top_logprob))
+        return W4A16_ERR_MISALIGNED;
+    if (M == 1) stride = V;
+    const size_t rows = static_cast<size_t>(M) * 4;
+    const Span written[5] = {{logprob, rows * given}, {rank, rows * given}, {entropy, rows}, {top_tokens, rows * top}, {top_logprob, rows * top}};
+    const Span read[3] = {{logits, rows_bytes(M, stride, V, 2)}, {tokens, rows * given}, {temperature, rows}};
+    const int rc = check_spans(written, 5, read, 3);
+    if (rc != W4A16_OK) return rc;
+    DeviceInfo d;
+    if (!device_info(&d)) return W4A16_ERR_CUDA;
+    const LogprobParams p = {logits, stride, M, V, tokens, given, top, temperature, logprob, rank, entropy, top_tokens, top_logprob};
+    return launched(launch_logprobs(p, d.sm_count, static_cast<cudaStream_t>(stream), d.status));
+}
+
+int w4a16_block_norm(const void* h, int64_t h_stride, int h_f32, const uint16_t* y, int64_t y_stride,
+                     const uint16_t* post_weight, const uint16_t* gate, int64_t gate_stride, int gate_per_row, float scale,
+                     const uint16_t* weight, float offset, float eps, void* h_out, uint16_t* x, int M, int H, void* stream) {
+    if (!h || (!h_out && !x) || M <= 0 || H <= 0) return W4A16_ERR_INVALID_ARG;
+    if ((h_f32 != 0 && h_f32 != 1) || (gate_per_row != 0 && gate_per_row != 1)) return W4A16_ERR_INVALID_ARG;
+    if (!y && (post_weight || gate)) return W4A16_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !std::isfinite(offset) || !std::isfinite(eps) || eps < 0.f) return W4A16_ERR_INVALID_ARG;
+    if (M == 1) h_stride = y_stride = H;
+    if (M == 1 && gate_per_row == 0) gate_stride = 0;
+    if (!y) y_stride = H;
+    if (!gate) gate_stride = gate_per_row = 0;
+    if (h_stride < H || y_stride < H || gate_stride < 0 || (gate && !gate_per_row && gate_stride != 0 && gate_stride < H))
+        return W4A16_ERR_INVALID_ARG;
+    if (H % 8 != 0 || H > 32768 || M > (1 << 20)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (h_stride % 8 != 0 || y_stride % 8 != 0 || (!gate_per_row && gate_stride % 8 != 0)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (h_stride > (1LL << 32) || y_stride > (1LL << 32) || gate_stride > (1LL << 32)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(h) || !aligned16(y) || !aligned16(post_weight) || !aligned16(weight) || !aligned16(h_out) || !aligned16(x) ||
+        (gate_per_row ? (reinterpret_cast<uintptr_t>(gate) & 1u) != 0 : !aligned16(gate)))
+        return W4A16_ERR_MISALIGNED;
+    const size_t dense = static_cast<size_t>(M) * H, element = h_f32 ? 4 : 2;
+    const Span written[2] = {{h_out, dense * element}, {x, dense * 2}};
+    const Span read[5] = {{h, rows_bytes(M, h_stride, H, element)},
+                          {y, rows_bytes(M, y_stride, H, 2)},
+                          {post_weight, static_cast<size_t>(H) * 2},
+                          {weight, static_cast<size_t>(H) * 2},
+                          {gate, rows_bytes(M, gate_stride, gate_per_row ? 1 : H, 2)}};
+    const int rc = check_spans(written, 2, read, 5, h_stride == H ? h : nullptr);
+    if (rc != W4A16_OK) return rc;
+    DeviceInfo d;
+    if (!device_info(&d)) return W4A16_ERR_CUDA;
+    const BlockNormParams p = {h, y, post_weight, gate, weight, h_out, x, h_stride, y_stride, gate_stride, M, H, h_f32, gate_per_row, scale, offset, eps};
+    return launched(launch_block_norm(p, d.sm_count, static_cast<cudaStream_t>(stream), d.status));
+}
+
+static bool moe_shape(int E, int H, int I) {
+    return E > 0 && E <= kMoeMaxExperts && H > 0 && H <= 65536 && H % 64 == 0 && I > 0 && I <= 65536 && I % 64 == 0;
+}
+
+size_t w4a16_moe_workspace_bytes(int experts, int hidden, int inner) {
+    return moe_shape(experts, hidden, inner) ? moe_workspace_bytes(experts, hidden, inner) : 0;
+}
+
+int w4a16_moe(const uint16_t* x, int64_t x_stride, const w4a16_moe_experts* m, const uint16_t* router, const float* bias,
+              int top_k, int scoring, int renormalize, float scale, uint16_t* y, int32_t* ids, float* weights, int tokens,
+              void* workspace, size_t workspace_bytes, void* stream) {
+    if (!x || !m || !router || !y || !workspace || tokens <= 0 || top_k <= 0) return W4A16_ERR_INVALID_ARG;
+    if (!m->gate_up_q || !m->gate_up_s || !m->down_q || !m->down_s || m->experts <= 0 || m->hidden <= 0 || m->inner <= 0)
+        return W4A16_ERR_INVALID_ARG;
+    if ((m->nvfp4 != 0 && m->nvfp4 != 1) || (m->nvfp4 == 1) != (m->gate_up_scale != nullptr) || (m->nvfp4 == 1) != (m->down_scale != nullptr))
+        return W4A16_ERR_INVALID_ARG;
+    if ((scoring != 0 && scoring != 1) || (renormalize != 0 && renormalize != 1) || !std::isfinite(scale)) return W4A16_ERR_INVALID_ARG;
+    if ((bias && scoring != 1) || top_k > m->experts) return W4A16_ERR_INVALID_ARG;
+    const int E = m->experts, H = m->hidden, I = m->inner, G = m->nvfp4 ? kNvfp4Block : m->group;
+    if (!moe_shape(E, H, I) || tokens > kMoeMaxTokens || top_k > kMoeMaxTop) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (!m->nvfp4 && (G <= 0 || G % 32 != 0 || H % G != 0 || I % G != 0)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (tokens == 1) x_stride = H;
+    if (x_stride < H) return W4A16_ERR_INVALID_ARG;
+    if (x_stride % 8 != 0 || x_stride > (1LL << 32)) return W4A16_ERR_UNSUPPORTED_SHAPE;
+    if (workspace_bytes < moe_workspace_bytes(E, H, I)) return W4A16_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(router) || !aligned16(y) || !aligned16(workspace) || !aligned16(m->gate_up_q) ||
+        !aligned16(m->gate_up_s) || !aligned16(m->down_q) || !aligned16(m->down_s) || !aligned4(bias) || !aligned4(ids) ||
+        !aligned4(weights) || !aligned4(m->gate_up_scale) || !aligned4(m->down_scale))
+        return W4A16_ERR_MISALIGNED;
+    const size_t e = E, h = H, i = I, pairs = static_cast<size_t>(tokens) * top_k * 4;
+    const Span written[4] = {{y, tokens * h * 2}, {workspace, workspace_bytes}, {ids, pairs}, {weights, pairs}};
+    const Span read[9] = {{x, rows_bytes(tokens, x_stride, H, 2)},
+                          {router, e * h * 2},
+                          {bias, e * 4},
+                          {m->gate_up_q, e * h * i},
+                          {m->gate_up_s, e * (h / G) * 2 * i * 2},
+                          {m->down_q, e * h * i / 2},
+                          {m->down_s, e * (i / G) * h * 2},
+                          {m->gate_up_scale, e * 4},
+                          {m->down_scale, e * 4}};
+    const int rc = check_spans(written, 4, read, 9);
+    if (rc != W4A16_OK) return rc;
+    DeviceInfo d;
+    if (!device_info(&d)) return W4A16_ERR_CUDA;
+    const MoeParams p = {x, x_stride, router, bias, m->gate_up_q, static_cast<const uint16_t*>(m->gate_up_s), m->down_q,
+                         static_cast<const uint16_t*>(m->down_s), m->gate_up_scale, m->down_scale, y, ids, weights, workspace,
+                         tokens, E, H, I, G, top_k, m->nvfp4, scoring, renormalize, scale};
+    return launched(launch_moe(p, d.sm_count, static_cast<cudaStream_t>(stream), d.status));
+}
+
 int w4a16_last_dispatch(char* buf, size_t len) {
     if (!buf || len == 0) return W4A16_ERR_INVALID_ARG;
     std::lock_guard<std::mutex> lock(g_mu);
