@@ -4,48 +4,64 @@
 //   score   = softmax_e(l) or sigmoid(l); chosen: the k experts with the largest l, or score + bias
 //             (ties: the lower index); r[t][e] = score, over the sum of the chosen ones' if asked, times `scale`
 //   a[t][e] = fp16(silu(x[t] . Wg[e]) * (x[t] . Wu[e]))            for the chosen e, products kept in fp32
-//   y[t]    = fp16(sum_e r[t][e] * (a[t][e] . Wd[e]))              summed in order of e, in fp32
+//   y[t]    = fp16(sum_e r[t][e] * (a[t][e] . Wd[e]))              summed in the order of choice, in fp32
 //
-// Three kernels on one stream, each scheduled while the one before it runs:
-//   route    a CTA per expert and 8 tokens; the last CTA of 8 tokens chooses their experts, the last of all
-//            lists the experts that were chosen, each with its tokens
-//   gate_up  a CTA per listed expert and 16 gate + 16 up columns over the whole of K
-//   down     a CTA (or cluster) per 32 output columns over all listed experts: so the sum over the experts of
-//            a token is made in one place and in one order, without atomics
+// Four kernels on one stream, each scheduled while the one before it runs:
+//   route    the logits: a CTA per expert and 8 tokens
+//   gate_up  every CTA chooses from the logits and lists the chosen experts in shared memory (cheaper than one CTA
+//            that does it and all others waiting for it), then streams the experts' gate and up columns
+//   down     the same list, the down columns, r * (a . Wd) of each (token, expert) pair in fp32
+//   combine  the sum over a token's k pairs: one order, no atomics
 //
 // What bounds it is the weights of the chosen experts, read once each whatever the tokens. They go from
-// global memory through registers into mma.m16n8k16 as the A operand (16 columns of W), tokens are its 8
+// global memory through shared memory into mma.m16n8k16 as the A operand (16 columns of W), tokens are its 8
 // columns: a lane (g, t) = (lane / 4, lane % 4) takes the whole 16-byte vector of column g and 32-k block t of
 // four adjacent blocks, so that of every 128 k a lane's loads are wide and dense and nothing is exchanged:
 // the instruction's k slots are simply numbered so that lane t's are the k of its own block. The B operand
 // must follow, so rows of x and of a are kept with their 16-byte units transposed within each 128 (unit w of
-// block t at place 4 w + t).
+// block t at place 4 w + t). A lane copies what it will read itself, so a warp's ring of stages needs no barrier.
+//
+// Work is a list of items, (listed expert, 32 columns) over all of K, in steps of 128 k. A cluster takes an equal
+// run of items, its warps equal runs of their steps, wherever that cuts an item: the warp that has an item's
+// beginning keeps its sums and adds the following warps' parts at the end. All of a warp's steps are one stream of
+// copies, whatever items they belong to. The runs are contiguous, so that a CTA meets few experts and finds the
+// rows of their tokens in L1.
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
 namespace w4a16 {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kRouteThreads = 256;
+constexpr int kStages = 3;    // of a warp's ring
+#ifndef MOE_CLUSTER
+#define MOE_CLUSTER 2
+#endif
+constexpr int kCluster = MOE_CLUSTER;
+
+// Warps of a gate_up or down CTA, one CTA an SM, by the tokens (8 NT) that they multiply at a time: the registers for
+// their sums.
+__host__ __device__ constexpr int warps_for(int nt) { return nt == 1 ? 16 : nt == 2 ? 12 : 8; }
+
+// How weights become operands.
+enum Form {
+    kInt4,       // groups of a multiple of 128 k: the codes themselves, a step's sums times the scale
+    kInt4Small,  // other groups: (code - 8) * scale rounded to fp16
+    kNvfp4       // code * block scale, exact in fp16
+};
+
+constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTop;
 
 // ------------------------------------------------------------------------------------ workspace
 // The same layout for every call with the same experts.
-struct Plan {  // what the router leaves to the other kernels
-    int active;                       // listed experts
-    int expert[kMoeMaxExperts];
-    int base[kMoeMaxExperts + 1];     // of a listed expert's first (token, weight) pair
-    int token[kMoeMaxTokens * kMoeMaxTop];
-    float weight[kMoeMaxTokens * kMoeMaxTop];
-};
 struct Space {
-    unsigned* arrived;  // 8 groups of 8 tokens, then the groups
-    Plan* plan;
-    int* chosen;        // [tokens][k]
-    float* share;       // [tokens][k]
     float* logits;      // [tokens][E]
+    int* place;         // [tokens][k]: of a pair in the list
     uint16_t* xp;       // [tokens][Hp], transposed units
     uint16_t* act;      // [pairs][Ip], transposed units
+    float* part;        // [pairs][H]
     size_t bytes;
 };
 
@@ -60,13 +76,11 @@ inline Space space_of(void* base, int E, int H, int I) {
         at += (n + 255) / 256 * 256;
         return q;
     };
-    s.arrived = reinterpret_cast<unsigned*>(take(64));
-    s.plan = reinterpret_cast<Plan*>(take(sizeof(Plan)));
-    s.chosen = reinterpret_cast<int*>(take(kMoeMaxTokens * kMoeMaxTop * 4));
-    s.share = reinterpret_cast<float*>(take(kMoeMaxTokens * kMoeMaxTop * 4));
     s.logits = reinterpret_cast<float*>(take(static_cast<size_t>(kMoeMaxTokens) * E * 4));
+    s.place = reinterpret_cast<int*>(take(kMaxPairs * 4));
     s.xp = reinterpret_cast<uint16_t*>(take(kMoeMaxTokens * padded(H) * 2));
-    s.act = reinterpret_cast<uint16_t*>(take(static_cast<size_t>(kMoeMaxTokens) * kMoeMaxTop * padded(I) * 2));
+    s.act = reinterpret_cast<uint16_t*>(take(kMaxPairs * padded(I) * 2));
+    s.part = reinterpret_cast<float*>(take(static_cast<size_t>(kMaxPairs) * H * 4));
     s.bytes = at;
     return s;
 }
@@ -74,12 +88,6 @@ inline Space space_of(void* base, int E, int H, int I) {
 // Place of element i of a row with transposed units.
 __device__ __forceinline__ int64_t unit_place(int i) {
     return (static_cast<int64_t>(i) & ~127LL) + ((((i >> 3) & 3) * 4 + ((i >> 5) & 3)) << 3) + (i & 7);
-}
-
-__device__ __forceinline__ uint4 ldg_weights(const uint4* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
 }
 
 // ------------------------------------------------------------------------------------ routing
@@ -95,6 +103,60 @@ struct RouteArgs {
     float scale;
 };
 
+// TB tokens a CTA (1 or 8), one expert.
+template <int TB>
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a, unsigned* status) {
+    constexpr int kW = kRouteThreads / 32;
+    __shared__ float part[kW][TB];
+    griddep_launch_dependents();
+    const int e = blockIdx.x, t0 = blockIdx.y * TB;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tokens = min(TB, a.T - t0), vecs = a.H / 8;
+    const uint16_t* wrow = a.router + static_cast<int64_t>(e) * a.H;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (static_cast<int>(threadIdx.x) < vecs) w = *reinterpret_cast<const uint4*>(wrow + 8 * threadIdx.x);
+    griddep_wait();
+    float acc[TB][2];
+#pragma unroll
+    for (int i = 0; i < TB; ++i) acc[i][0] = acc[i][1] = 0.f;
+    for (int v = threadIdx.x; v < vecs; v += kRouteThreads) {
+        uint4 x[TB];
+#pragma unroll
+        for (int i = 0; i < TB; ++i) {
+            const int64_t at = (t0 + i) * a.x_stride + 8 * static_cast<int64_t>(v);
+            x[i] = i < tokens && in_bounds(8 * v + 8 <= a.H, status) ? *reinterpret_cast<const uint4*>(a.x + at) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        const int next = v + kRouteThreads;
+        const uint4 wn = next < vecs ? *reinterpret_cast<const uint4*>(wrow + 8 * next) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < TB; ++i) {
+            fma2_mixed(acc[i][0], acc[i][1], w.x, x[i].x);
+            fma2_mixed(acc[i][0], acc[i][1], w.y, x[i].y);
+            fma2_mixed(acc[i][0], acc[i][1], w.z, x[i].z);
+            fma2_mixed(acc[i][0], acc[i][1], w.w, x[i].w);
+            if (e == 0 && i < tokens) {  // one expert's CTAs leave x as the products want it
+                uint16_t* to = a.w.xp + (t0 + i) * padded(a.H) + unit_place(8 * v);
+                *reinterpret_cast<uint4*>(to) = x[i];
+            }
+        }
+        w = wn;
+    }
+#pragma unroll
+    for (int i = 0; i < TB; ++i) {
+        float s = acc[i][0] + acc[i][1];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) part[warp][i] = s;
+    }
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < tokens) {
+        float s = part[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < kW; ++i) s += part[i][threadIdx.x];
+        a.w.logits[static_cast<int64_t>(t0 + threadIdx.x) * a.E + e] = s;
+    }
+}
+
 // A float as a whole number of the same order, above 1; NaN: 1 (below all).
 __device__ __forceinline__ uint32_t order_of(float f) {
     if (f != f) return 1u;
@@ -102,8 +164,23 @@ __device__ __forceinline__ uint32_t order_of(float f) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// The chosen experts with their tokens, in shared memory. An expert with more than `cap` tokens is listed several
+// times, each time with the next of them.
+struct List {
+    int entries;
+    uint16_t expert[kMoeMaxExperts + kMaxPairs / 8];
+    uint16_t base[kMoeMaxExperts + kMaxPairs / 8 + 1];  // of an entry's first (token, expert) pair
+    uint8_t token[kMaxPairs];
+    float weight[kMaxPairs];
+    // while it is made
+    uint16_t chosen[kMaxPairs];  // [T][k]
+    float share[kMaxPairs];
+    uint32_t mask[2][kMoeMaxExperts];  // tokens of an expert, one bit each
+    uint32_t sums[16];
+};
+
 // One warp chooses the experts of token t and their weights.
-__device__ __forceinline__ void choose(const RouteArgs& a, int t) {
+__device__ __forceinline__ void choose(const RouteArgs& a, List& list, int t) {
     constexpr int kEach = kMoeMaxExperts / 32;
     const int lane = threadIdx.x & 31;
     uint32_t key[kEach];
@@ -153,138 +230,69 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t) {
     }
     if (a.renormalize || !a.sigmoid) s = __fdiv_rn(s, fmaxf(all, 1e-30f));  // (sigmoids may all be 0)
     if (lane < a.k) {
-        const int64_t at = static_cast<int64_t>(t) * a.k + lane;
-        a.w.chosen[at] = mine;
-        a.w.share[at] = s * a.scale;
-        if (a.ids) a.ids[at] = mine;
-        if (a.weights) a.weights[at] = s * a.scale;
+        list.chosen[t * a.k + lane] = static_cast<uint16_t>(mine);
+        list.share[t * a.k + lane] = s * a.scale;
     }
 }
 
-// The list of chosen experts with their tokens, by one CTA.
-__device__ __forceinline__ void list_experts(const RouteArgs& a) {
-    __shared__ uint32_t mask[2][kMoeMaxExperts];  // tokens of an expert, one bit each
-    __shared__ uint32_t scan[kMoeMaxExperts];     // (listed experts << 16) + pairs, up to and with this one
-    const int pairs = a.T * a.k;
-    for (int e = threadIdx.x; e < kMoeMaxExperts; e += kThreads) mask[0][e] = mask[1][e] = 0;
+// The list, made by one CTA of WARPS warps. `results`: this CTA writes what the caller and the last kernel want of it.
+template <int WARPS>
+__device__ __forceinline__ void make_list(const RouteArgs& a, List& list, int cap, bool results, unsigned* status) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pairs = a.T * a.k;
+    for (int e = threadIdx.x; e < kMoeMaxExperts; e += WARPS * 32) list.mask[0][e] = list.mask[1][e] = 0;
+    for (int t = warp; t < a.T; t += WARPS) choose(a, list, t);
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += kThreads) {
+    for (int p = threadIdx.x; p < pairs; p += WARPS * 32) {
         const int t = p / a.k;
-        atomicOr(&mask[t >> 5][__ldcg(a.w.chosen + p)], 1u << (t & 31));
+        atomicOr(&list.mask[t >> 5][list.chosen[p]], 1u << (t & 31));
     }
-    __syncthreads();
-    for (int e = threadIdx.x; e < kMoeMaxExperts; e += kThreads) {
-        const uint32_t n = __popc(mask[0][e]) + __popc(mask[1][e]);
-        scan[e] = n == 0 ? 0u : (1u << 16) + n;
-    }
-    __syncthreads();
-    for (int o = 1; o < kMoeMaxExperts && o < a.E; o <<= 1) {
-        uint32_t add[kMoeMaxExperts / kThreads];
-#pragma unroll
-        for (int i = 0; i < kMoeMaxExperts / kThreads; ++i) {
-            const int e = static_cast<int>(threadIdx.x) + i * kThreads;
-            add[i] = e >= o ? scan[e - o] : 0u;
-        }
+    uint32_t carry = 0;  // (entries << 16) + pairs of the experts before
+    for (int e0 = 0; e0 < a.E; e0 += WARPS * 32) {
         __syncthreads();
+        const int e = e0 + static_cast<int>(threadIdx.x);
+        const uint32_t lo = e < a.E ? list.mask[0][e] : 0u, hi = e < a.E ? list.mask[1][e] : 0u;
+        const uint32_t n = __popc(lo) + __popc(hi), own = ((n + cap - 1) / cap << 16) + n;
+        uint32_t upto = own;
 #pragma unroll
-        for (int i = 0; i < kMoeMaxExperts / kThreads; ++i) scan[threadIdx.x + i * kThreads] += add[i];
-        __syncthreads();
-    }
-    Plan* plan = a.w.plan;
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
-        const uint32_t n = __popc(mask[0][e]) + __popc(mask[1][e]);
-        if (n == 0) continue;
-        const int at = static_cast<int>(scan[e] >> 16) - 1;
-        plan->expert[at] = e;
-        plan->base[at + 1] = static_cast<int>(scan[e] & 0xFFFFu);
-    }
-    if (threadIdx.x == 0) {
-        plan->base[0] = 0;
-        plan->active = static_cast<int>(scan[a.E - 1] >> 16);
-    }
-    for (int p = threadIdx.x; p < pairs; p += kThreads) {
-        const int t = p / a.k, e = __ldcg(a.w.chosen + p);
-        const uint32_t lo = mask[0][e], hi = mask[1][e], bit = 1u << (t & 31);
-        const int before = t < 32 ? __popc(lo & (bit - 1)) : __popc(lo) + __popc(hi & (bit - 1));
-        const int at = static_cast<int>(scan[e] & 0xFFFFu) - __popc(lo) - __popc(hi) + before;
-        plan->token[at] = t;
-        plan->weight[at] = __ldcg(a.w.share + p);
-    }
-}
-
-// TB tokens a CTA (1 or 8), one expert.
-template <int TB>
-__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a, unsigned* status) {
-    __shared__ float part[kWarps][TB];
-    __shared__ int last;
-    griddep_launch_dependents();
-    const int e = blockIdx.x, group = blockIdx.y, t0 = group * TB;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tokens = min(TB, a.T - t0), vecs = a.H / 8;
-    const uint16_t* wrow = a.router + static_cast<int64_t>(e) * a.H;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (static_cast<int>(threadIdx.x) < vecs) w = *reinterpret_cast<const uint4*>(wrow + 8 * threadIdx.x);
-    griddep_wait();
-    float acc[TB][2];
-#pragma unroll
-    for (int i = 0; i < TB; ++i) acc[i][0] = acc[i][1] = 0.f;
-    for (int v = threadIdx.x; v < vecs; v += kThreads) {
-        uint4 x[TB];
-#pragma unroll
-        for (int i = 0; i < TB; ++i) {
-            const int64_t at = (t0 + i) * a.x_stride + 8 * static_cast<int64_t>(v);
-            x[i] = i < tokens && in_bounds(8 * v + 8 <= a.H, status) ? *reinterpret_cast<const uint4*>(a.x + at) : make_uint4(0u, 0u, 0u, 0u);
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
         }
-        const int next = v + kThreads;
-        const uint4 wn = next < vecs ? *reinterpret_cast<const uint4*>(wrow + 8 * next) : make_uint4(0u, 0u, 0u, 0u);
+        if (lane == 31) list.sums[warp] = upto;
+        __syncthreads();
+        upto += carry;
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) upto += list.sums[w];
+            carry += list.sums[w];
+        }
+        const uint32_t before = upto - own;
+        int at = static_cast<int>(before >> 16), base = static_cast<int>(before & 0xFFFFu);
+        for (uint32_t i = 0; i < n; i += cap) {
+            list.expert[at] = static_cast<uint16_t>(e);
+            list.base[at++] = static_cast<uint16_t>(base + i);
+        }
+        // pairs of an expert by token
 #pragma unroll
-        for (int i = 0; i < TB; ++i) {
-            fma2_mixed(acc[i][0], acc[i][1], w.x, x[i].x);
-            fma2_mixed(acc[i][0], acc[i][1], w.y, x[i].y);
-            fma2_mixed(acc[i][0], acc[i][1], w.z, x[i].z);
-            fma2_mixed(acc[i][0], acc[i][1], w.w, x[i].w);
-            if (e == 0 && i < tokens) {  // one expert's CTAs leave x as the products want it
-                uint16_t* to = a.w.xp + (t0 + i) * padded(a.H) + unit_place(8 * v);
-                *reinterpret_cast<uint4*>(to) = x[i];
+        for (int h = 0; h < 2; ++h)
+            for (uint32_t left = h ? hi : lo; left != 0; left &= left - 1) {
+                const int t = 32 * h + __ffs(left) - 1;
+                int j = 0;
+                while (j + 1 < a.k && list.chosen[t * a.k + j] != e) ++j;
+                list.token[base] = static_cast<uint8_t>(t);
+                list.weight[base] = list.share[t * a.k + j];
+                if (results && in_bounds(base < pairs, status)) {
+                    a.w.place[t * a.k + j] = base;
+                    if (a.ids) a.ids[t * a.k + j] = e;
+                    if (a.weights) a.weights[t * a.k + j] = list.share[t * a.k + j];
+                }
+                ++base;
             }
-        }
-        w = wn;
     }
-#pragma unroll
-    for (int i = 0; i < TB; ++i) {
-        float s = acc[i][0] + acc[i][1];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) part[warp][i] = s;
-    }
-    __syncthreads();
-    if (static_cast<int>(threadIdx.x) < tokens) {
-        float s = part[0][threadIdx.x];
-#pragma unroll
-        for (int i = 1; i < kWarps; ++i) s += part[i][threadIdx.x];
-        a.w.logits[static_cast<int64_t>(t0 + threadIdx.x) * a.E + e] = s;
-        __threadfence();
-    }
-    __syncthreads();
     if (threadIdx.x == 0) {
-        __threadfence();
-        last = atomicAdd(a.w.arrived + group, 1u) == static_cast<unsigned>(a.E) - 1u;
-        if (last) a.w.arrived[group] = 0;  // ready for the next call
-        __threadfence();
+        list.entries = static_cast<int>(carry >> 16);
+        list.base[carry >> 16] = static_cast<uint16_t>(carry & 0xFFFFu);
     }
     __syncthreads();
-    if (!last) return;
-    for (int t = warp; t < tokens; t += kWarps) choose(a, t0 + t);
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        last = atomicAdd(a.w.arrived + 15, 1u) == gridDim.y - 1u;
-        if (last) a.w.arrived[15] = 0;
-        __threadfence();
-    }
-    __syncthreads();
-    if (last) list_experts(a);
 }
 
 // ------------------------------------------------------------------------------------ products
@@ -302,269 +310,376 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two bands of 16 columns of one expert's matrix, as a lane reads them: column g and g + 8 of each.
-template <bool FP4>
-struct Columns {
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A stage of a warp's ring: 128 k of 32 columns. Vectors: [band][half][32-k block][column, swizzled]; then scales
+// [row][32 columns]. Column g of block t lies at place g ^ 2 t of its 8, so that neither the copies (8 columns of
+// a block at a time) nor the reads (2 columns of 4 blocks) meet in a bank.
+template <Form F>
+struct Stage {
+    static constexpr int kRows = F == kInt4 ? 1 : F == kInt4Small ? 4 : 8;  // of scales
+    static constexpr int kScales = 2048;
+    static constexpr int kBytes = kScales + kRows * 64;
+};
+__device__ __forceinline__ uint32_t vector_place(int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    return static_cast<uint32_t>(t * 128 + ((g ^ (2 * t)) & 7) * 16);
+}
+
+// Where a lane's copies come from: an item's two bands of 16 columns.
+template <Form F>
+struct Source {
     const uint4* w[2];
     const uint16_t* s[2];
-    int wt[2];     // vectors from one 32-k block to the next
-    int blocks;    // 32-k blocks of K
-    int shift, per;  // 32-k blocks a scale row (int4), as a shift where that is a power of two
+    int wt[2];  // vectors from one 32-k block to the next
 
     __device__ __forceinline__ void set(const Matrices& m, int expert, int c0, int c1, int lane) {
-        blocks = m.K / 32;
-        per = FP4 ? 1 : m.G / 32;
-        shift = (per & (per - 1)) == 0 ? __ffs(per) - 1 : -1;
-        const int rows = FP4 ? 2 * blocks : m.K / m.G;
+        const int blocks = m.K / 32, rows = m.K / m.G;
         const int64_t codes = static_cast<int64_t>(expert) * m.N * blocks, scales = static_cast<int64_t>(expert) * m.N * rows;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const int c = b ? c1 : c0, tile = c >> 7;
             wt[b] = min(128, m.N - 128 * tile);
             w[b] = m.w + codes + static_cast<int64_t>(tile) * 128 * blocks + (c & 127) + (lane >> 2);
-            s[b] = m.s + scales + static_cast<int64_t>(tile) * 128 * rows + (c & 127) + (lane >> 2);
+            s[b] = m.s + scales + static_cast<int64_t>(tile) * 128 * rows + (c & 127);
         }
     }
-};
-
-template <bool FP4>
-struct Step {  // a lane's share of 128 k: 4 columns, 32 k each
-    uint4 v[4];
-    uint32_t s[4];  // int4: (scale, scale); NVFP4: (of the first 16 k, of the second)
-
-    __device__ __forceinline__ void load(const Columns<FP4>& c, int kb, int lane, bool any) {
+    // per: 32-k blocks a scale row (int4), shift its logarithm or -1
+    __device__ __forceinline__ void copy(uint32_t stage, int kb, int blocks, int per, int shift, int lane) const {
         const int blk = kb * 4 + (lane & 3);
-        const bool there = any && blk < c.blocks;
+        if (F == kInt4 || blk < blocks) {
+            const uint32_t vec = stage + vector_place(lane);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const uint4* p = c.w[b] + static_cast<int64_t>(blk) * c.wt[b];
-            v[2 * b] = there ? ldg_weights(p) : make_uint4(0u, 0u, 0u, 0u);
-            v[2 * b + 1] = there ? ldg_weights(p + 8) : make_uint4(0u, 0u, 0u, 0u);
-            if (FP4) {
-                const uint16_t* q = c.s[b] + static_cast<int64_t>(2 * blk) * c.wt[b];
-                s[2 * b] = there ? __ldg(q) | static_cast<uint32_t>(__ldg(q + c.wt[b])) << 16 : 0u;
-                s[2 * b + 1] = there ? __ldg(q + 8) | static_cast<uint32_t>(__ldg(q + c.wt[b] + 8)) << 16 : 0u;
-            } else {
-                const int row = c.shift >= 0 ? blk >> c.shift : blk / c.per;
-                const uint16_t* q = c.s[b] + static_cast<int64_t>(row) * c.wt[b];
-                s[2 * b] = there ? __ldg(q) : 0u;
-                s[2 * b + 1] = there ? __ldg(q + 8) : 0u;
+            for (int b = 0; b < 2; ++b) {
+                const uint4* p = w[b] + static_cast<int64_t>(blk) * wt[b];
+                copy16(vec + 1024u * b, p);
+                copy16(vec + 1024u * b + 512u, p + 8);
             }
         }
-    }
-
-    // acc[b][n] += the bands' columns times NT * 8 tokens; rows[n]: this lane's token of those 8, NULL for none.
-    template <int NT>
-    __device__ __forceinline__ void multiply(float (&acc)[2][NT][4], const uint16_t* const (&rows)[NT], int tiles, int blocks, int kb,
-                                             int lane) const {
-        const bool there = kb * 4 + (lane & 3) < blocks;
-        const int64_t at = (static_cast<int64_t>(kb) * 16 + (lane & 3)) * 8;
+        if (F == kInt4) {  // 16 pairs of one row
+            const int row = shift >= 0 ? (kb * 4) >> shift : kb * 4 / per, b = (lane >> 3) & 1;
+            if (lane < 16) copy4(stage + Stage<F>::kScales + 4u * lane, (b ? s[1] : s[0]) + static_cast<int64_t>(row) * (b ? wt[1] : wt[0]) + 2 * (lane & 7));
+        } else {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            uint32_t d[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t word = w == 0 ? v[i].x : w == 1 ? v[i].y : w == 2 ? v[i].z : v[i].w;
-                if (FP4) {
-                    const uint32_t h = w < 2 ? s[i] & 0xFFFFu : s[i] >> 16;
-                    dequant8_nvfp4(word, h * 0x10001u, d[i]);
-                } else {
-                    dequant8(word, s[i] * 0x10001u, d[i]);
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n >= tiles) break;
-                const uint4 x = there && rows[n] ? *reinterpret_cast<const uint4*>(rows[n] + at + w * 32) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    mma16816(acc[b][n], d[2 * b][0], d[2 * b + 1][0], d[2 * b][1], d[2 * b + 1][1], x.x, x.y);
-                    mma16816(acc[b][n], d[2 * b][2], d[2 * b + 1][2], d[2 * b][3], d[2 * b + 1][3], x.z, x.w);
-                }
+            for (int j = 0; j < Stage<F>::kRows / 2; ++j) {
+                const int i = lane + 32 * j, r = i >> 4, b = (i >> 3) & 1;
+                const int sblk = F == kNvfp4 ? kb * 4 + (r >> 1) : kb * 4 + r;
+                if (sblk >= blocks) continue;
+                const int row = F == kNvfp4 ? kb * 8 + r : shift >= 0 ? sblk >> shift : sblk / per;
+                copy4(stage + Stage<F>::kScales + 4u * i, (b ? s[1] : s[0]) + static_cast<int64_t>(row) * (b ? wt[1] : wt[0]) + 2 * (i & 7));
             }
         }
     }
 };
 
-// CTA: listed expert blockIdx.x / chunks, gate columns 16 j .. and up columns I + 16 j .. The warps take the
-// 128-k steps in turn and are added up through shared memory; SwiGLU on the sums.
-template <int NT, bool FP4>
-__global__ void __launch_bounds__(kThreads) gate_up_kernel(const Matrices m, const Space ws, int H, int I, unsigned* status) {
-    __shared__ float2 red[kWarps][NT][2][64];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    griddep_wait();
-    griddep_launch_dependents();  // (after the wait: the next kernel may read the plan before its own wait)
-    const int chunks = I / 16;
-    const int at = static_cast<int>(blockIdx.x) / chunks, j = static_cast<int>(blockIdx.x) % chunks;
-    if (at >= __ldcg(&ws.plan->active)) return;
-    const int expert = __ldcg(ws.plan->expert + at), base = __ldcg(ws.plan->base + at), count = __ldcg(ws.plan->base + at + 1) - base;
-    const int steps = static_cast<int>(padded(H) / 128);
-    Columns<FP4> cols;
-    cols.set(m, expert, 16 * j, I + 16 * j, lane);
-    for (int first = 0; first < count; first += 8 * NT) {
-        const int tiles = min(NT, (count - first + 7) / 8);
-        const uint16_t* rows[NT];
-        float acc[2][NT][4];
+// sum[b][n] += a stage's columns times NT * 8 tokens (the first `tiles` of NT); rows[n]: this lane's token of those 8, at
+// the step's unit.
+//
+// kInt4: a pair of codes q, taken out of a word by a mask, is a pair of fp16 numbers q 2^-24 or 16 q 2^-24 (subnormal,
+// exact in a product), so 5 instructions make the operands of 8 weights. Sums of either kind, and 8 sum x from a
+// constant operand, are kept for the step; (q - 8) s then costs three instructions a sum: w is not rounded to
+// fp16. (The other forms' 13 and 12 instructions for 8 weights are what bounds the products otherwise: 401 against
+// some 200 a step of 16 tokens, gate_up of 16 tokens 348 us against the figure at the launch.) Sums are 2^24 too small.
+template <int NT, Form F>
+__device__ __forceinline__ void multiply(float (&sum)[2][NT][4], uint32_t stage, const uint16_t* const (&rows)[NT], int tiles, bool there,
+                                         int lane) {
+    uint4 x[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int i = first + 8 * n + (lane >> 2);
-            rows[n] = i < count ? ws.xp + __ldcg(ws.plan->token + base + i) * padded(H) : nullptr;
+    for (int n = 0; n < NT; ++n)
+        if (n == 0 || n < tiles) x[n] = *reinterpret_cast<const uint4*>(rows[n]);
+    uint4 v[4];
+    const uint32_t vec = stage + vector_place(lane), sc = stage + Stage<F>::kScales + 2u * (lane >> 2);
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+    for (int i = 0; i < 4; ++i) v[i] = lds128(vec + 512u * i);
+    uint32_t s[4][F == kNvfp4 ? 2 : 1];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[b][n][r] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t row = F == kInt4 ? 0u : F == kInt4Small ? lane & 3u : 2u * (lane & 3u);
+        s[i][0] = lds16(sc + 64u * row + 16u * i);
+        if (F == kNvfp4) s[i][F == kNvfp4 ? 1 : 0] = lds16(sc + 64u * (row + 1) + 16u * i);
+        if (F != kInt4) {  // past K: what the stage holds is not of this step
+            s[i][0] = there ? s[i][0] * 0x10001u : 0u;
+            if (F == kNvfp4) s[i][F == kNvfp4 ? 1 : 0] = there ? s[i][F == kNvfp4 ? 1 : 0] * 0x10001u : 0u;
         }
-        Step<FP4> cur, next;
-        cur.load(cols, warp, lane, warp < steps);
-        for (int kb = warp; kb < steps; kb += kWarps) {
-            next.load(cols, kb + kWarps, lane, kb + kWarps < steps);
-            cur.template multiply<NT>(acc, rows, tiles, cols.blocks, kb, lane);
-            cur = next;
-        }
+    }
+    float one[2][NT][4], sixteen[2][NT][4], eight[NT][4];
+    if (F == kInt4) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {  // [column][token]
-                red[warp][n][b][lane] = make_float2(acc[b][n][0], acc[b][n][1]);
-                red[warp][n][b][32 + lane] = make_float2(acc[b][n][2], acc[b][n][3]);
-            }
-        __syncthreads();
-        const float factor = FP4 ? m.factor[expert] : 1.f;
-        for (int i = threadIdx.x; i < tiles * 128; i += kThreads) {
-            // unit of 8 columns as consecutive threads, so that a row's stores are 16 bytes wide
-            const int n = i >> 7, col = i & 15, tok = (i >> 4) & 7;
-            const int pair = first + 8 * n + tok;
-            if (pair >= count) continue;
-            float sum[2];
+            for (int i = 0; i < 4; ++i) one[0][n][i] = one[1][n][i] = sixteen[0][n][i] = sixteen[1][n][i] = eight[n][i] = 0.f;
+    }
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const float* p = reinterpret_cast<const float*>(&red[0][n][b][0]) + col * 8 + tok;
-                sum[b] = p[0];
+    for (int w = 0; w < 4; ++w) {
+        uint4 ahead[NT];
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) sum[b] += p[w * NT * 2 * 128];
-                sum[b] *= factor;
+        for (int n = 0; n < NT; ++n)
+            if (w < 3 && (n == 0 || n < tiles)) ahead[n] = *reinterpret_cast<const uint4*>(rows[n] + (w + 1) * 32);
+        uint32_t d[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t word = w == 0 ? v[i].x : w == 1 ? v[i].y : w == 2 ? v[i].z : v[i].w;
+            if (F == kNvfp4) {
+                dequant8_nvfp4(word, s[i][F == kNvfp4 && w >= 2 ? 1 : 0], d[i]);
+            } else if (F == kInt4Small) {
+                dequant8(word, s[i][0], d[i]);
+            } else {
+                d[i][0] = word & 0x000F000Fu;
+                d[i][1] = word & 0x00F000F0u;
+                d[i][2] = (word >> 8) & 0x000F000Fu;
+                d[i][3] = (word >> 8) & 0x00F000F0u;
             }
-            const float act = sum[0] / (1.0f + expf(-sum[0])) * sum[1];
-            if (in_bounds(base + pair < kMoeMaxTokens * kMoeMaxTop && 16 * j + col < I, status))
-                ws.act[(base + pair) * padded(I) + unit_place(16 * j + col)] = __half_as_ushort(__float2half_rn(act));
         }
-        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (n > 0 && n >= tiles) break;
+            if (F == kInt4) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    mma16816(one[b][n], d[2 * b][0], d[2 * b + 1][0], d[2 * b][2], d[2 * b + 1][2], x[n].x, x[n].z);
+                    mma16816(sixteen[b][n], d[2 * b][1], d[2 * b + 1][1], d[2 * b][3], d[2 * b + 1][3], x[n].y, x[n].w);
+                }
+                constexpr uint32_t k8 = 0x00080008u;
+                mma16816(eight[n], k8, k8, k8, k8, x[n].x, x[n].z);
+                mma16816(eight[n], k8, k8, k8, k8, x[n].y, x[n].w);
+            } else {
+                if (!there) x[n] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    mma16816(sum[b][n], d[2 * b][0], d[2 * b + 1][0], d[2 * b][1], d[2 * b + 1][1], x[n].x, x[n].y);
+                    mma16816(sum[b][n], d[2 * b][2], d[2 * b + 1][2], d[2 * b][3], d[2 * b + 1][3], x[n].z, x[n].w);
+                }
+            }
+            if (w < 3) x[n] = ahead[n];
+        }
+    }
+    if (F == kInt4) {
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(s[i][0])));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (n > 0 && n >= tiles) break;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum[b][n][i] = fmaf(f[2 * b + (i >> 1)], fmaf(0.0625f, sixteen[b][n][i], one[b][n][i]) - eight[n][i & 1], sum[b][n][i]);
+        }
     }
 }
 
-// CTA `rank` of a cluster of P: output columns 32 c .., the rank's share of all (listed expert, 128-k step) in
-// order, each warp a run of it. Sums of a token are kept a warp in shared memory and added up in order.
-template <int NT, bool FP4>
-__global__ void __launch_bounds__(kThreads) down_kernel(const Matrices m, const Space ws, uint16_t* __restrict__ y, int T, int H, int I,
-                                                        int P, unsigned* status) {
-    extern __shared__ float total[];  // [warps][T][32], then [T][32] of the CTA
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    griddep_launch_dependents();
-    const int rank = static_cast<int>(blockIdx.x) % P, chunk = static_cast<int>(blockIdx.x) / P;
-    // The plan is the work of the kernel before the last: complete, since every CTA of the last one passed its wait
-    // before this kernel could start.
-    const int active = __ldcg(&ws.plan->active);
-    const int steps = static_cast<int>(padded(I) / 128);
-    const int runs = P * kWarps, run = rank * kWarps + warp, all = active * steps;
-    int s = static_cast<int>(static_cast<int64_t>(all) * run / runs);
-    const int end = static_cast<int>(static_cast<int64_t>(all) * (run + 1) / runs);
-    float* mine = total + warp * T * 32;
-    for (int i = lane; i < T * 32; i += 32) mine[i] = 0.f;
-    int at = s / steps, kb = s % steps;
-    Columns<FP4> cols;
-    Step<FP4> cur, next;
-    if (s < end) {
-        cols.set(m, __ldcg(ws.plan->expert + at), 32 * chunk, 32 * chunk + 16, lane);
-        cur.load(cols, kb, lane, true);
+// DOWN false: gate and up (items of 16 gate and the same 16 up columns), true: down (32 columns).
+template <int NT, Form F, bool DOWN>
+__global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Matrices m, const RouteArgs r, int I, unsigned* status) {
+    constexpr int kWarps = warps_for(NT);
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ List list;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = r.H;
+    const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * kStages * Stage<F>::kBytes);
+    // parts of items that begin in an earlier warp: [warp][band][n][register][lane]
+    float* heads = reinterpret_cast<float*>(smem + kWarps * kStages * Stage<F>::kBytes);
+    if (!DOWN) {
+        griddep_wait();
+        griddep_launch_dependents();  // (after the wait: the next kernel may read the logits before its own)
+    } else {
+        griddep_launch_dependents();
+        // The logits are the work of the kernel before the last: complete, since every CTA of the last one had passed
+        // its wait before this kernel could start.
     }
-    griddep_wait();
-    __syncwarp();
-    while (s < end) {
-        const int base = __ldcg(ws.plan->base + at), count = __ldcg(ws.plan->base + at + 1) - base;
-        const int stop = min(steps, kb + end - s);  // this expert's steps kb .. stop - 1
-        const float factor = FP4 ? m.factor[__ldcg(ws.plan->expert + at)] : 1.f;
-        const bool more = s + stop - kb < end;
-        for (int first = 0; first < count; first += 8 * NT) {
-            const int tiles = min(NT, (count - first + 7) / 8);
-            const bool again = first + 8 * NT < count;
-            const uint16_t* rows[NT];
-            float acc[2][NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int i = first + 8 * n + (lane >> 2);
-                rows[n] = i < count ? ws.act + (base + i) * padded(I) : nullptr;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[b][n][r] = 0.f;
-            }
-            for (int k = kb; k < stop; ++k) {
-                if (k + 1 < stop) {
-                    next.load(cols, k + 1, lane, true);
-                } else if (again) {
-                    next.load(cols, kb, lane, true);
-                } else if (more) {
-                    Columns<FP4> after;
-                    after.set(m, __ldcg(ws.plan->expert + at + 1), 32 * chunk, 32 * chunk + 16, lane);
-                    next.load(after, 0, lane, true);
+    make_list<kWarps>(r, list, 8 * NT, !DOWN && blockIdx.x == 0, status);
+
+    const int rank = static_cast<int>(blockIdx.x) % kCluster, cluster = static_cast<int>(blockIdx.x) / kCluster;
+    const int clusters = static_cast<int>(gridDim.x) / kCluster;
+    const int chunks = DOWN ? H / 32 : I / 16;
+    const int steps = static_cast<int>(padded(m.K) / 128), blocks = m.K / 32;
+    const int per = F == kNvfp4 ? 1 : m.G / 32, shift = (per & (per - 1)) == 0 ? __ffs(per) - 1 : -1;
+    const int64_t items = static_cast<int64_t>(list.entries) * chunks;
+    const int64_t item0 = items * cluster / clusters;
+    const int run = static_cast<int>(items * (cluster + 1) / clusters - item0) * steps;  // the cluster's steps
+    const int workers = kCluster * kWarps, me = rank * kWarps + warp;
+    auto begin = [&](int worker) { return static_cast<int>(static_cast<int64_t>(run) * worker / workers); };
+    const int s0 = begin(me), s1 = begin(me + 1);
+
+    // the copying end of the stream
+    Source<F> src;
+    const int64_t first = item0 + s0 / steps;
+    int entry = static_cast<int>(first / chunks), chunk = static_cast<int>(first % chunks), kb = s0 % steps;
+    int c_entry = entry, c_chunk = chunk, c_kb = kb, c_left = s1 - s0;
+    auto aim = [&]() {
+        src.set(m, list.expert[c_entry], DOWN ? 32 * c_chunk : 16 * c_chunk, DOWN ? 32 * c_chunk + 16 : I + 16 * c_chunk, lane);
+    };
+    auto fetch = [&](int slot) {
+        if (c_left > 0) {
+            src.copy(ring + static_cast<uint32_t>(slot * Stage<F>::kBytes), c_kb, blocks, per, shift, lane);
+            --c_left;
+            if (++c_kb == steps && c_left > 0) {
+                c_kb = 0;
+                if (++c_chunk == chunks) {
+                    c_chunk = 0;
+                    ++c_entry;
                 }
-                cur.template multiply<NT>(acc, rows, tiles, cols.blocks, k, lane);
-                cur = next;
+                aim();
             }
+        }
+        copies_commit();
+    };
+    if (c_left > 0) aim();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    if (DOWN) griddep_wait();
+
+    const uint16_t* rows[NT];
+    float acc[2][NT][4];
+    int base = 0, count = 0, tiles = 0;
+    const int width = static_cast<int>(padded(m.K));
+    auto meet = [&]() {  // the rows of an entry's tokens at step kb; a place without a token reads the first one's
+        base = list.base[entry];
+        count = list.base[entry + 1] - base;
+        tiles = (count + 7) / 8;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int i = 8 * n + (lane >> 2), pair = base + (i < count ? i : 0);
+            rows[n] = (DOWN ? r.w.act + static_cast<int64_t>(pair) * width : r.w.xp + static_cast<int64_t>(list.token[pair]) * width) +
+                      kb * 128 + (lane & 3) * 8;
+        }
+    };
+    auto clear = [&]() {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int i = first + 8 * n + 2 * (lane & 3) + h;
-                    if (i >= count) continue;
-                    const int token = __ldcg(ws.plan->token + base + i);
-                    const float w = __ldcg(ws.plan->weight + base + i) * factor;
-                    if (!in_bounds(token >= 0 && token < T, status)) continue;
-                    float* to = mine + token * 32 + (lane >> 2);
-                    to[0] = fmaf(w, acc[0][n][h], to[0]);
-                    to[8] = fmaf(w, acc[0][n][2 + h], to[8]);
-                    to[16] = fmaf(w, acc[1][n][h], to[16]);
-                    to[24] = fmaf(w, acc[1][n][2 + h], to[24]);
-                }
-            __syncwarp();
-        }
-        s += stop - kb;
-        ++at;
-        kb = 0;
-        if (s < end) cols.set(m, __ldcg(ws.plan->expert + at), 32 * chunk, 32 * chunk + 16, lane);
-    }
-    __syncthreads();
-    float* part = total + kWarps * T * 32;
-    for (int i = threadIdx.x; i < T * 32; i += kThreads) {
-        float v = total[i];
+                for (int i = 0; i < 4; ++i) acc[b][n][i] = 0.f;
+    };
+    auto finish = [&]() {  // a lane's columns g, g + 8 of both bands for tokens 2 t, 2 t + 1 of 8
+        const float factor = F == kNvfp4 ? m.factor[list.expert[entry]] : F == kInt4 ? 16777216.f : 1.f;
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) v += total[w * T * 32 + i];
-        if (P > 1) {
-            part[i] = v;
-        } else {
-            const int64_t o = static_cast<int64_t>(i >> 5) * H + 32 * chunk + (i & 31);
-            if (in_bounds(o < static_cast<int64_t>(T) * H, status)) y[o] = __half_as_ushort(__float2half_rn(v));
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = 8 * n + 2 * (lane & 3) + h, pair = base + i;
+                if (i >= count || !in_bounds(pair < kMaxPairs, status)) continue;
+                if (DOWN) {
+                    const float w = list.weight[pair] * factor;
+                    float* to = r.w.part + static_cast<int64_t>(pair) * H + 32 * chunk + (lane >> 2);
+                    to[0] = w * acc[0][n][h];
+                    to[8] = w * acc[0][n][2 + h];
+                    to[16] = w * acc[1][n][h];
+                    to[24] = w * acc[1][n][2 + h];
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float g = acc[0][n][2 * q + h] * factor, u = acc[1][n][2 * q + h] * factor;
+                        r.w.act[pair * padded(I) + unit_place(16 * chunk + 8 * q + (lane >> 2))] =
+                            __half_as_ushort(__float2half_rn(g / (1.0f + expf(-g)) * u));
+                    }
+                }
+            }
+    };
+    float* mine = heads + (warp * 2 * NT * 4) * 32 + lane;
+    auto leave = [&]() {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mine[((b * NT + n) * 4 + i) * 32] = acc[b][n][i];
+    };
+
+    bool whole = kb == 0;  // the item's beginning is this warp's
+    clear();
+    if (s0 < s1) meet();
+    int slot = 0;
+    for (int s = s0; s < s1; ++s) {
+        copies_wait<kStages - 2>();
+        __syncwarp();  // (scales are copied for each other; and the slot that is filled next has been read)
+        fetch(slot == 0 ? kStages - 1 : slot - 1);
+        multiply<NT, F>(acc, ring + static_cast<uint32_t>(slot * Stage<F>::kBytes), rows, tiles, kb * 4 + (lane & 3) < blocks, lane);
+        if (++slot == kStages) slot = 0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) rows[n] += 128;
+        if (++kb == steps) {
+            if (whole)
+                finish();
+            else
+                leave();
+            clear();
+            whole = true;
+            kb = 0;
+            if (++chunk == chunks) {
+                chunk = 0;
+                ++entry;
+                if (s + 1 < s1) meet();
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) rows[n] -= width;
+            }
         }
     }
-    if (P == 1) return;
+    copies_wait<0>();
+    const bool open = s0 < s1 && kb != 0;
+    if (open && !whole) leave();
     cluster_sync_all();
-    for (int i = static_cast<int>(threadIdx.x) + rank * kThreads; i < T * 32; i += P * kThreads) {
-        const float v = cluster_sum_f1(smem_u32(part + i), P);
-        const int64_t o = static_cast<int64_t>(i >> 5) * H + 32 * chunk + (i & 31);
-        if (in_bounds(o < static_cast<int64_t>(T) * H, status)) y[o] = __half_as_ushort(__float2half_rn(v));
+    if (open && whole) {
+        const int end = s1 - kb + steps;  // of the item, in the cluster's steps
+        for (int other = me + 1; other < workers && begin(other) < end; ++other) {
+            if (begin(other) == begin(other + 1)) continue;
+            const uint32_t from = map_peer(smem_u32(heads + ((other % kWarps) * 2 * NT * 4) * 32 + lane), static_cast<uint32_t>(other / kWarps));
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[b][n][i] += ld_dsmem_f1(from + ((b * NT + n) * 4 + i) * 128);
+        }
+        finish();
     }
     cluster_sync_all();
 }
 
+// y of a token: its pairs' sums in the order of choice. Four columns a thread.
+__global__ void __launch_bounds__(256) combine_kernel(const Space ws, uint16_t* __restrict__ y, int T, int H, int k, unsigned* status) {
+    griddep_launch_dependents();
+    const int64_t i = blockIdx.x * 256LL + threadIdx.x;
+    const int quads = H / 4;
+    griddep_wait();
+    if (i >= static_cast<int64_t>(T) * quads) return;
+    const int t = static_cast<int>(i / quads), c = static_cast<int>(i % quads) * 4;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < k; ++j) {
+        const int pair = ws.place[t * k + j];
+        if (!in_bounds(pair >= 0 && pair < T * k, status)) continue;
+        const float4 v = *reinterpret_cast<const float4*>(ws.part + static_cast<int64_t>(pair) * H + c);
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+    }
+    const __half2 lo = __floats2half2_rn(sum.x, sum.y), hi = __floats2half2_rn(sum.z, sum.w);
+    *reinterpret_cast<uint2*>(y + static_cast<int64_t>(t) * H + c) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
 template <typename Kern, typename... Args>
-cudaError_t launch(Kern kern, dim3 grid, size_t smem, int cluster, cudaStream_t s, Args... args) {
-    if (smem > 48 * 1024) {
+cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, Args... args) {
+    if (smem > 0) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -584,19 +699,53 @@ cudaError_t launch(Kern kern, dim3 grid, size_t smem, int cluster, cudaStream_t 
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int NT, bool FP4>
-cudaError_t launch_products(const MoeParams& p, const Space& ws, int sm_count, cudaStream_t s, unsigned* status) {
-    const int most = p.E < p.T * p.k ? p.E : p.T * p.k;  // experts that can be chosen
+// Clusters of experts_kernel that the device holds at once (asked once a device): clusters lie within a part of the
+// GPU, so there may be fewer than a quarter of its SMs.
+template <int NT, Form F, bool DOWN>
+int resident_clusters(size_t smem, int sm_count) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count / kCluster;
+    int n = known[dev].load();
+    if (n > 0) return n;
+    auto kern = experts_kernel<NT, F, DOWN>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(warps_for(NT) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        return sm_count / kCluster;
+    }
+    known[dev].store(n);
+    return n;
+}
+
+template <int NT, Form F>
+cudaError_t launch_form(const MoeParams& p, const RouteArgs& r, int sm_count, cudaStream_t s, unsigned* status) {
     const Matrices up = {static_cast<const uint4*>(p.gate_up_q), p.gate_up_s, p.gate_up_factor, 2 * p.I, p.H, p.G};
     const Matrices down = {static_cast<const uint4*>(p.down_q), p.down_s, p.down_factor, p.H, p.I, p.G};
-    const cudaError_t e = launch(gate_up_kernel<NT, FP4>, dim3(static_cast<unsigned>(most * (p.I / 16))), 0, 1, s, up, ws, p.H, p.I, status);
+    constexpr int kThreads = warps_for(NT) * 32;
+    constexpr size_t smem = warps_for(NT) * (kStages * Stage<F>::kBytes + 2 * NT * 4 * 32 * 4);
+    const dim3 grid_up(static_cast<unsigned>(resident_clusters<NT, F, false>(smem, sm_count) * kCluster));
+    const cudaError_t e = launch(experts_kernel<NT, F, false>, grid_up, kThreads, smem, kCluster, s, up, r, p.I, status);
     if (e != cudaSuccess) return e;
-    const int chunks = p.H / 32;
-    const int64_t steps = most * (padded(p.I) / 128);
-    int P = 1;
-    while (P < 8 && chunks * P * 2 <= 4 * sm_count && steps / (2 * P * kWarps) >= 2) P *= 2;
-    const size_t smem = static_cast<size_t>(kWarps + 1) * p.T * 32 * 4;
-    return launch(down_kernel<NT, FP4>, dim3(static_cast<unsigned>(chunks * P)), smem, P, s, down, ws, p.y, p.T, p.H, p.I, P, status);
+    const dim3 grid_down(static_cast<unsigned>(resident_clusters<NT, F, true>(smem, sm_count) * kCluster));
+    return launch(experts_kernel<NT, F, true>, grid_down, kThreads, smem, kCluster, s, down, r, p.I, status);
+}
+
+template <int NT>
+cudaError_t launch_products(const MoeParams& p, const RouteArgs& r, int sm_count, cudaStream_t s, unsigned* status) {
+    if (p.nvfp4) return launch_form<NT, kNvfp4>(p, r, sm_count, s, status);
+    return p.G % 128 == 0 ? launch_form<NT, kInt4>(p, r, sm_count, s, status) : launch_form<NT, kInt4Small>(p, r, sm_count, s, status);
 }
 
 }  // namespace
@@ -606,18 +755,17 @@ size_t moe_workspace_bytes(int E, int H, int I) { return space_of(nullptr, E, H,
 cudaError_t launch_moe(const MoeParams& p, int sm_count, cudaStream_t s, unsigned* status) {
     const Space ws = space_of(p.workspace, p.E, p.H, p.I);
     const RouteArgs r = {p.x, p.x_stride, p.router, p.bias, p.ids, p.weights, ws, p.T, p.E, p.H, p.k, p.sigmoid, p.renormalize, p.scale};
-    const cudaError_t e = p.T == 1 ? launch(route_kernel<1>, dim3(static_cast<unsigned>(p.E), 1), 0, 1, s, r, status)
-                                   : launch(route_kernel<8>, dim3(static_cast<unsigned>(p.E), static_cast<unsigned>((p.T + 7) / 8)), 0, 1, s, r, status);
+    cudaError_t e = p.T == 1 ? launch(route_kernel<1>, dim3(static_cast<unsigned>(p.E), 1), kRouteThreads, 0, 1, s, r, status)
+                             : launch(route_kernel<8>, dim3(static_cast<unsigned>(p.E), static_cast<unsigned>((p.T + 7) / 8)), kRouteThreads, 0, 1, s, r, status);
     if (e != cudaSuccess) return e;
-    // Tokens an expert's weights are multiplied by at a time: as many as it has on average when the batch is
-    // spread evenly, at least 8; an expert with more reads its weights again.
-    const int mean = (p.T * p.k + p.E - 1) / p.E;
-    const int nt = p.T <= 8 ? 1 : mean <= 12 ? 2 : 4;
-#define W4A16_MOE(NT_) \
-    if (nt == NT_) return p.nvfp4 ? launch_products<NT_, true>(p, ws, sm_count, s, status) : launch_products<NT_, false>(p, ws, sm_count, s, status);
-    W4A16_MOE(1) W4A16_MOE(2) W4A16_MOE(4)
-#undef W4A16_MOE
-    return cudaErrorInvalidValue;
+    // Tokens that an expert's weights are multiplied by at a time: 8 where there are no more, 16 where the average
+    // expert has up to 10 (one with more is streamed again), else 32.
+    const int nt = p.T <= 8 ? 1 : p.T * p.k <= 10 * p.E || p.T <= 16 ? 2 : 4;
+    e = nt == 1 ? launch_products<1>(p, r, sm_count, s, status)
+        : nt == 2 ? launch_products<2>(p, r, sm_count, s, status)
+                  : launch_products<4>(p, r, sm_count, s, status);
+    if (e != cudaSuccess) return e;
+    return launch(combine_kernel, dim3(static_cast<unsigned>((static_cast<int64_t>(p.T) * p.H / 4 + 255) / 256)), 256, 0, 1, s, ws, p.y, p.T, p.H, p.k, status);
 }
 
 }  // namespace w4a16
