@@ -61,9 +61,13 @@ struct Space {
     int* place;         // [tokens][k]: of a pair in the list
     uint16_t* xp;       // [tokens][Hp], transposed units
     uint16_t* act;      // [pairs][Ip], transposed units
+    float* xsum;        // [tokens][Hp / 128]: 8 * 2^-24 times the sums of 128 elements of x
+    float* asum;        // [pairs][I / 16]: of 16 elements of a
     float* part;        // [pairs][H]
     size_t bytes;
 };
+
+constexpr float kEight = 8.f / 16777216.f;  // 8 * 2^-24
 
 __host__ __device__ inline int64_t padded(int k) { return (static_cast<int64_t>(k) + 127) / 128 * 128; }
 
@@ -80,14 +84,17 @@ inline Space space_of(void* base, int E, int H, int I) {
     s.place = reinterpret_cast<int*>(take(kMaxPairs * 4));
     s.xp = reinterpret_cast<uint16_t*>(take(kMoeMaxTokens * padded(H) * 2));
     s.act = reinterpret_cast<uint16_t*>(take(kMaxPairs * padded(I) * 2));
+    s.xsum = reinterpret_cast<float*>(take(kMoeMaxTokens * padded(H) / 128 * 4));
+    s.asum = reinterpret_cast<float*>(take(static_cast<size_t>(kMaxPairs) * (I / 16) * 4));
     s.part = reinterpret_cast<float*>(take(static_cast<size_t>(kMaxPairs) * H * 4));
     s.bytes = at;
     return s;
 }
 
-// Place of element i of a row with transposed units.
+// Place of element i of a row with transposed units. Within a unit the pairs lie in the order 0, 2, 1, 3: pairs 0 and 2
+// of a word's codes are taken out by one mask, 1 and 3 by another, and each two are the operand of one instruction.
 __device__ __forceinline__ int64_t unit_place(int i) {
-    return (static_cast<int64_t>(i) & ~127LL) + ((((i >> 3) & 3) * 4 + ((i >> 5) & 3)) << 3) + (i & 7);
+    return (static_cast<int64_t>(i) & ~127LL) + ((((i >> 3) & 3) * 4 + ((i >> 5) & 3)) << 3) + ((i & 2) << 1) + ((i & 4) >> 1) + (i & 1);
 }
 
 // ------------------------------------------------------------------------------------ routing
@@ -136,10 +143,30 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
             fma2_mixed(acc[i][0], acc[i][1], w.w, x[i].w);
             if (e == 0 && i < tokens) {  // one expert's CTAs leave x as the products want it
                 uint16_t* to = a.w.xp + (t0 + i) * padded(a.H) + unit_place(8 * v);
-                *reinterpret_cast<uint4*>(to) = x[i];
+                *reinterpret_cast<uint4*>(to) = make_uint4(x[i].x, x[i].z, x[i].y, x[i].w);
             }
         }
         w = wn;
+    }
+    if (e == 0) {  // sums of 128 elements, a half-warp each
+        for (int v0 = 0; v0 < (vecs + 15) / 16 * 16; v0 += kRouteThreads) {
+            const int v = v0 + static_cast<int>(threadIdx.x);
+            for (int i = 0; i < tokens; ++i) {
+                float s = 0.f;
+                if (v < vecs) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(a.x + (t0 + i) * a.x_stride + 8 * static_cast<int64_t>(v));
+                    const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+                        s += f.x + f.y;
+                    }
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if ((threadIdx.x & 15) == 0 && v < vecs) a.w.xsum[(t0 + i) * (padded(a.H) / 128) + (v >> 4)] = kEight * s;
+            }
+        }
     }
 #pragma unroll
     for (int i = 0; i < TB; ++i) {
@@ -310,6 +337,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
@@ -336,39 +369,50 @@ __device__ __forceinline__ uint32_t vector_place(int lane) {
     return static_cast<uint32_t>(t * 128 + ((g ^ (2 * t)) & 7) * 16);
 }
 
-// Where a lane's copies come from: an item's two bands of 16 columns.
+// Where a lane's copies come from: an item's two bands of 16 columns, at the next step to be copied.
 template <Form F>
 struct Source {
     const uint4* w[2];
-    const uint16_t* s[2];
-    int wt[2];  // vectors from one 32-k block to the next
+    int wt[2];          // vectors from one 32-k block to the next
+    const uint16_t* s[2];  // scales; of kInt4: s[0], this lane's pair
+    int kb, row_left;   // kInt4: steps until the next row of scales
 
-    __device__ __forceinline__ void set(const Matrices& m, int expert, int c0, int c1, int lane) {
+    __device__ __forceinline__ void set(const Matrices& m, int expert, int c0, int c1, int first, int lane) {
         const int blocks = m.K / 32, rows = m.K / m.G;
         const int64_t codes = static_cast<int64_t>(expert) * m.N * blocks, scales = static_cast<int64_t>(expert) * m.N * rows;
+        kb = first;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const int c = b ? c1 : c0, tile = c >> 7;
             wt[b] = min(128, m.N - 128 * tile);
-            w[b] = m.w + codes + static_cast<int64_t>(tile) * 128 * blocks + (c & 127) + (lane >> 2);
+            w[b] = m.w + codes + static_cast<int64_t>(tile) * 128 * blocks + (c & 127) + (lane >> 2) +
+                   static_cast<int64_t>(4 * first + (lane & 3)) * wt[b];
             s[b] = m.s + scales + static_cast<int64_t>(tile) * 128 * rows + (c & 127);
         }
+        if (F == kInt4) {
+            const int q = m.G / 128, row = first / q, b = (lane >> 3) & 1;
+            s[0] = (b ? s[1] : s[0]) + static_cast<int64_t>(row) * (b ? wt[1] : wt[0]) + 2 * (lane & 7);
+            row_left = q - (first - row * q);
+        }
     }
-    // per: 32-k blocks a scale row (int4), shift its logarithm or -1
-    __device__ __forceinline__ void copy(uint32_t stage, int kb, int blocks, int per, int shift, int lane) const {
-        const int blk = kb * 4 + (lane & 3);
-        if (F == kInt4 || blk < blocks) {
-            const uint32_t vec = stage + vector_place(lane);
+    // per: 32-k blocks a scale row, shift its logarithm or -1
+    __device__ __forceinline__ void copy(uint32_t stage, int blocks, int per, int shift, int lane) {
+        const uint32_t vec = stage + vector_place(lane);
+        if (F == kInt4 || kb * 4 + (lane & 3) < blocks) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const uint4* p = w[b] + static_cast<int64_t>(blk) * wt[b];
-                copy16(vec + 1024u * b, p);
-                copy16(vec + 1024u * b + 512u, p + 8);
+                copy16(vec + 1024u * b, w[b]);
+                copy16(vec + 1024u * b + 512u, w[b] + 8);
             }
         }
+        w[0] += 4 * wt[0];
+        w[1] += 4 * wt[1];
         if (F == kInt4) {  // 16 pairs of one row
-            const int row = shift >= 0 ? (kb * 4) >> shift : kb * 4 / per, b = (lane >> 3) & 1;
-            if (lane < 16) copy4(stage + Stage<F>::kScales + 4u * lane, (b ? s[1] : s[0]) + static_cast<int64_t>(row) * (b ? wt[1] : wt[0]) + 2 * (lane & 7));
+            if (lane < 16) copy4(stage + Stage<F>::kScales + 4u * lane, s[0]);
+            if (--row_left == 0) {
+                row_left = per >> 2;
+                s[0] += (lane >> 3) & 1 ? wt[1] : wt[0];
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < Stage<F>::kRows / 2; ++j) {
@@ -379,24 +423,29 @@ struct Source {
                 copy4(stage + Stage<F>::kScales + 4u * i, (b ? s[1] : s[0]) + static_cast<int64_t>(row) * (b ? wt[1] : wt[0]) + 2 * (i & 7));
             }
         }
+        ++kb;
     }
 };
 
-// sum[b][n] += a stage's columns times NT * 8 tokens (the first `tiles` of NT); rows[n]: this lane's token of those 8, at
-// the step's unit.
+// sum[b][n] += a stage's columns times TILES * 8 tokens; rows[n]: where this lane's token of those 8 has the step's unit;
+// sums[n] (kInt4): where it has what adds up, over the quad with DOWN, to 8 * 2^-24 times the sum of its 128 elements.
 //
 // kInt4: a pair of codes q, taken out of a word by a mask, is a pair of fp16 numbers q 2^-24 or 16 q 2^-24 (subnormal,
-// exact in a product), so 5 instructions make the operands of 8 weights. Sums of either kind, and 8 sum x from a
-// constant operand, are kept for the step; (q - 8) s then costs three instructions a sum: w is not rounded to
-// fp16. (The other forms' 13 and 12 instructions for 8 weights are what bounds the products otherwise: 401 against
-// some 200 a step of 16 tokens, gate_up of 16 tokens 348 us against the figure at the launch.) Sums are 2^24 too small.
-template <int NT, Form F>
-__device__ __forceinline__ void multiply(float (&sum)[2][NT][4], uint32_t stage, const uint16_t* const (&rows)[NT], int tiles, bool there,
-                                         int lane) {
-    uint4 x[NT];
+// exact in a product), so 5 instructions make the operands of 8 weights. Sums of either kind are kept for the step,
+// sums of x come with it, and (q - 8) s then costs three instructions a sum: w is not rounded to fp16. (The other
+// forms' 13 and 12 instructions for 8 weights bound the products otherwise: gate_up of 16 tokens 348 us.) Sums are
+// 2^24 too small.
+template <int NT, int TILES, Form F, bool DOWN>
+__device__ __forceinline__ void multiply(float (&sum)[2][NT][4], uint32_t stage, const uint16_t* base, const uint32_t (&rows)[NT],
+                                         const float* sums_base, const uint32_t (&sums)[NT], bool there, int lane) {
+    uint4 x[TILES];
+    float2 less[TILES];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-        if (n == 0 || n < tiles) x[n] = *reinterpret_cast<const uint4*>(rows[n]);
+    for (int n = 0; n < TILES; ++n) {
+        x[n] = *reinterpret_cast<const uint4*>(base + rows[n]);
+        if (F == kInt4 && DOWN) less[n] = *reinterpret_cast<const float2*>(sums_base + sums[n]);
+        if (F == kInt4 && !DOWN) less[n].x = sums_base[sums[n]];
+    }
     uint4 v[4];
     const uint32_t vec = stage + vector_place(lane), sc = stage + Stage<F>::kScales + 2u * (lane >> 2);
 #pragma unroll
@@ -412,19 +461,13 @@ __device__ __forceinline__ void multiply(float (&sum)[2][NT][4], uint32_t stage,
             if (F == kNvfp4) s[i][F == kNvfp4 ? 1 : 0] = there ? s[i][F == kNvfp4 ? 1 : 0] * 0x10001u : 0u;
         }
     }
-    float one[2][NT][4], sixteen[2][NT][4], eight[NT][4];
-    if (F == kInt4) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) one[0][n][i] = one[1][n][i] = sixteen[0][n][i] = sixteen[1][n][i] = eight[n][i] = 0.f;
-    }
+    float one[2][TILES][4], sixteen[2][TILES][4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        uint4 ahead[NT];
+        uint4 ahead[TILES];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            if (w < 3 && (n == 0 || n < tiles)) ahead[n] = *reinterpret_cast<const uint4*>(rows[n] + (w + 1) * 32);
+        for (int n = 0; n < TILES; ++n)
+            if (w < 3) ahead[n] = *reinterpret_cast<const uint4*>(base + rows[n] + (w + 1) * 32);
         uint32_t d[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -441,23 +484,24 @@ __device__ __forceinline__ void multiply(float (&sum)[2][NT][4], uint32_t stage,
             }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (n > 0 && n >= tiles) break;
+        for (int n = 0; n < TILES; ++n) {
             if (F == kInt4) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    mma16816(one[b][n], d[2 * b][0], d[2 * b + 1][0], d[2 * b][2], d[2 * b + 1][2], x[n].x, x[n].z);
-                    mma16816(sixteen[b][n], d[2 * b][1], d[2 * b + 1][1], d[2 * b][3], d[2 * b + 1][3], x[n].y, x[n].w);
+                    if (w == 0) {
+                        mma16816_first(one[b][n], d[2 * b][0], d[2 * b + 1][0], d[2 * b][2], d[2 * b + 1][2], x[n].x, x[n].y);
+                        mma16816_first(sixteen[b][n], d[2 * b][1], d[2 * b + 1][1], d[2 * b][3], d[2 * b + 1][3], x[n].z, x[n].w);
+                    } else {
+                        mma16816(one[b][n], d[2 * b][0], d[2 * b + 1][0], d[2 * b][2], d[2 * b + 1][2], x[n].x, x[n].y);
+                        mma16816(sixteen[b][n], d[2 * b][1], d[2 * b + 1][1], d[2 * b][3], d[2 * b + 1][3], x[n].z, x[n].w);
+                    }
                 }
-                constexpr uint32_t k8 = 0x00080008u;
-                mma16816(eight[n], k8, k8, k8, k8, x[n].x, x[n].z);
-                mma16816(eight[n], k8, k8, k8, k8, x[n].y, x[n].w);
             } else {
                 if (!there) x[n] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    mma16816(sum[b][n], d[2 * b][0], d[2 * b + 1][0], d[2 * b][1], d[2 * b + 1][1], x[n].x, x[n].y);
-                    mma16816(sum[b][n], d[2 * b][2], d[2 * b + 1][2], d[2 * b][3], d[2 * b + 1][3], x[n].z, x[n].w);
+                    mma16816(sum[b][n], d[2 * b][0], d[2 * b + 1][0], d[2 * b][2], d[2 * b + 1][2], x[n].x, x[n].y);
+                    mma16816(sum[b][n], d[2 * b][1], d[2 * b + 1][1], d[2 * b][3], d[2 * b + 1][3], x[n].z, x[n].w);
                 }
             }
             if (w < 3) x[n] = ahead[n];
@@ -468,13 +512,20 @@ __device__ __forceinline__ void multiply(float (&sum)[2][NT][4], uint32_t stage,
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(s[i][0])));
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (n > 0 && n >= tiles) break;
+        for (int n = 0; n < TILES; ++n) {
+            // from the lanes of tokens 2 t, 2 t + 1
+            float total = less[n].x;
+            if (DOWN) {
+                total += less[n].y;
+                total += __shfl_xor_sync(0xffffffffu, total, 1);
+                total += __shfl_xor_sync(0xffffffffu, total, 2);
+            }
+            const float off[2] = {__shfl_sync(0xffffffffu, total, (lane & 3) * 8), __shfl_sync(0xffffffffu, total, (lane & 3) * 8 + 4)};
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    sum[b][n][i] = fmaf(f[2 * b + (i >> 1)], fmaf(0.0625f, sixteen[b][n][i], one[b][n][i]) - eight[n][i & 1], sum[b][n][i]);
+                    sum[b][n][i] = fmaf(f[2 * b + (i >> 1)], fmaf(0.0625f, sixteen[b][n][i], one[b][n][i]) - off[i & 1], sum[b][n][i]);
         }
     }
 }
@@ -515,15 +566,14 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     Source<F> src;
     const int64_t first = item0 + s0 / steps;
     int entry = static_cast<int>(first / chunks), chunk = static_cast<int>(first % chunks), kb = s0 % steps;
-    int c_entry = entry, c_chunk = chunk, c_kb = kb, c_left = s1 - s0;
+    int c_entry = entry, c_chunk = chunk, c_kb = kb, c_left = s1 - s0;  // (c_kb: of an item's first step only)
     auto aim = [&]() {
-        src.set(m, list.expert[c_entry], DOWN ? 32 * c_chunk : 16 * c_chunk, DOWN ? 32 * c_chunk + 16 : I + 16 * c_chunk, lane);
+        src.set(m, list.expert[c_entry], DOWN ? 32 * c_chunk : 16 * c_chunk, DOWN ? 32 * c_chunk + 16 : I + 16 * c_chunk, c_kb, lane);
     };
     auto fetch = [&](int slot) {
         if (c_left > 0) {
-            src.copy(ring + static_cast<uint32_t>(slot * Stage<F>::kBytes), c_kb, blocks, per, shift, lane);
-            --c_left;
-            if (++c_kb == steps && c_left > 0) {
+            src.copy(ring + static_cast<uint32_t>(slot * Stage<F>::kBytes), blocks, per, shift, lane);
+            if (--c_left > 0 && src.kb == steps) {
                 c_kb = 0;
                 if (++c_chunk == chunks) {
                     c_chunk = 0;
@@ -539,9 +589,12 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     for (int i = 0; i < kStages - 1; ++i) fetch(i);
     if (DOWN) griddep_wait();
 
-    const uint16_t* rows[NT];
+    const uint16_t* const rows_of = DOWN ? r.w.act : r.w.xp;
+    const float* const sums_of = DOWN ? r.w.asum : r.w.xsum;
+    uint32_t rows[NT], sums[NT];  // of this lane's tokens, at step kb (below 2^32: 1024 rows of 65,536 at most)
     float acc[2][NT][4];
-    int base = 0, count = 0, tiles = 0;
+    constexpr int kSums = DOWN ? 8 : 1;  // a step
+    int base = 0, count = 0, tiles = 1;
     const int width = static_cast<int>(padded(m.K));
     auto meet = [&]() {  // the rows of an entry's tokens at step kb; a place without a token reads the first one's
         base = list.base[entry];
@@ -550,8 +603,9 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int i = 8 * n + (lane >> 2), pair = base + (i < count ? i : 0);
-            rows[n] = (DOWN ? r.w.act + static_cast<int64_t>(pair) * width : r.w.xp + static_cast<int64_t>(list.token[pair]) * width) +
-                      kb * 128 + (lane & 3) * 8;
+            const int row = DOWN ? pair : list.token[pair];
+            rows[n] = static_cast<uint32_t>(row * width + kb * 128 + (lane & 3) * 8);
+            sums[n] = static_cast<uint32_t>(DOWN ? row * (I / 16) + kb * 8 + 2 * (lane & 3) : row * (width / 128) + kb);
         }
     };
     auto clear = [&]() {
@@ -568,9 +622,11 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                if (n > 0 && n >= tiles) break;
                 const int i = 8 * n + 2 * (lane & 3) + h, pair = base + i;
-                if (i >= count || !in_bounds(pair < kMaxPairs, status)) continue;
+                const bool there = i < count && in_bounds(i >= count || pair < kMaxPairs, status);
                 if (DOWN) {
+                    if (!there) continue;
                     const float w = list.weight[pair] * factor;
                     float* to = r.w.part + static_cast<int64_t>(pair) * H + 32 * chunk + (lane >> 2);
                     to[0] = w * acc[0][n][h];
@@ -578,11 +634,18 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
                     to[16] = w * acc[1][n][h];
                     to[24] = w * acc[1][n][2 + h];
                 } else {
+                    float both = 0.f;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         const float g = acc[0][n][2 * q + h] * factor, u = acc[1][n][2 * q + h] * factor;
-                        r.w.act[pair * padded(I) + unit_place(16 * chunk + 8 * q + (lane >> 2))] =
-                            __half_as_ushort(__float2half_rn(g / (1.0f + expf(-g)) * u));
+                        const __half a = __float2half_rn(g / (1.0f + expf(-g)) * u);
+                        both += __half2float(a);
+                        if (there) r.w.act[pair * padded(I) + unit_place(16 * chunk + 8 * q + (lane >> 2))] = __half_as_ushort(a);
+                    }
+                    if (F == kInt4) {
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) both += __shfl_xor_sync(0xffffffffu, both, o);
+                        if (there && lane < 4) r.w.asum[static_cast<int64_t>(pair) * (I / 16) + chunk] = kEight * both;
                     }
                 }
             }
@@ -605,10 +668,20 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
         copies_wait<kStages - 2>();
         __syncwarp();  // (scales are copied for each other; and the slot that is filled next has been read)
         fetch(slot == 0 ? kStages - 1 : slot - 1);
-        multiply<NT, F>(acc, ring + static_cast<uint32_t>(slot * Stage<F>::kBytes), rows, tiles, kb * 4 + (lane & 3) < blocks, lane);
+        const uint32_t stage = ring + static_cast<uint32_t>(slot * Stage<F>::kBytes);
+        const bool there = F == kInt4 || kb * 4 + (lane & 3) < blocks;
+        if (NT == 1 || tiles == 1)
+            multiply<NT, 1, F, DOWN>(acc, stage, rows_of, rows, sums_of, sums, there, lane);
+        else if (NT == 2 || tiles == 2)
+            multiply<NT, NT < 2 ? 1 : 2, F, DOWN>(acc, stage, rows_of, rows, sums_of, sums, there, lane);
+        else
+            multiply<NT, NT, F, DOWN>(acc, stage, rows_of, rows, sums_of, sums, there, lane);
         if (++slot == kStages) slot = 0;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) rows[n] += 128;
+        for (int n = 0; n < NT; ++n) {
+            rows[n] += 128;
+            sums[n] += kSums;
+        }
         if (++kb == steps) {
             if (whole)
                 finish();
@@ -623,7 +696,10 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
                 if (s + 1 < s1) meet();
             } else {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) rows[n] -= width;
+                for (int n = 0; n < NT; ++n) {
+                    rows[n] -= width;
+                    sums[n] -= kSums * steps;
+                }
             }
         }
     }
@@ -657,6 +733,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const Space ws, uint16_t* 
     if (i >= static_cast<int64_t>(T) * quads) return;
     const int t = static_cast<int>(i / quads), c = static_cast<int>(i % quads) * 4;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int j = 0; j < k; ++j) {
         const int pair = ws.place[t * k + j];
         if (!in_bounds(pair >= 0 && pair < T * k, status)) continue;
