@@ -7,10 +7,10 @@
 //   y[t]    = fp16(sum_e r[t][e] * (a[t][e] . Wd[e]))              summed in the order of choice, in fp32
 //
 // Four kernels on one stream, each scheduled while the one before it runs:
-//   route    the logits: a CTA per expert and 8 tokens
-//   gate_up  every CTA chooses from the logits and lists the chosen experts in shared memory (cheaper than one CTA
-//            that does it and all others waiting for it), then streams the experts' gate and up columns
-//   down     the same list, the down columns, r * (a . Wd) of each (token, expert) pair in fp32
+//   route    the logits, a CTA per expert and 8 tokens; the last CTA of 8 tokens chooses their experts, the last of all
+//            lists the chosen experts with their tokens
+//   gate_up  the listed experts' gate and up columns
+//   down     their down columns, r * (a . Wd) of each (token, expert) pair in fp32
 //   combine  the sum over a token's k pairs: one order, no atomics
 //
 // What bounds it is the weights of the chosen experts, read once each whatever the tokens. They go from
@@ -56,7 +56,22 @@ constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTop;
 
 // ------------------------------------------------------------------------------------ workspace
 // The same layout for every call with the same experts.
+
+// The chosen experts with their tokens. An expert with more than the products take at a time is listed several times,
+// each time with the next of them.
+struct List {
+    int entries;
+    uint16_t expert[kMoeMaxExperts + kMaxPairs / 8];
+    uint16_t base[kMoeMaxExperts + kMaxPairs / 8 + 1];  // of an entry's first (token, expert) pair
+    uint8_t token[kMaxPairs];
+    float weight[kMaxPairs];
+};
+
 struct Space {
+    unsigned* arrived;  // CTAs of each 8 tokens, then the groups
+    List* list;
+    uint16_t* chosen;   // [tokens][k]
+    float* share;       // [tokens][k]
     float* logits;      // [tokens][E]
     int* place;         // [tokens][k]: of a pair in the list
     uint16_t* xp;       // [tokens][Hp], transposed units
@@ -80,6 +95,10 @@ inline Space space_of(void* base, int E, int H, int I) {
         at += (n + 255) / 256 * 256;
         return q;
     };
+    s.arrived = reinterpret_cast<unsigned*>(take(64));
+    s.list = reinterpret_cast<List*>(take(sizeof(List)));
+    s.chosen = reinterpret_cast<uint16_t*>(take(kMaxPairs * 2));
+    s.share = reinterpret_cast<float*>(take(kMaxPairs * 4));
     s.logits = reinterpret_cast<float*>(take(static_cast<size_t>(kMoeMaxTokens) * E * 4));
     s.place = reinterpret_cast<int*>(take(kMaxPairs * 4));
     s.xp = reinterpret_cast<uint16_t*>(take(kMoeMaxTokens * padded(H) * 2));
@@ -108,7 +127,151 @@ struct RouteArgs {
     Space w;
     int T, E, H, k, sigmoid, renormalize;
     float scale;
+    int cap;  // tokens of a list entry
 };
+
+// A float as a whole number of the same order, above 1; NaN: 1 (below all).
+__device__ __forceinline__ uint32_t order_of(float f) {
+    if (f != f) return 1u;
+    const uint32_t b = __float_as_uint(f + 0.f);  // -0 and 0 are one value
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// One warp chooses the experts of token t and their weights, of kEach * 32 at most.
+template <int kEach>
+__device__ __forceinline__ void choose(const RouteArgs& a, int t) {
+    const int lane = threadIdx.x & 31;
+    uint32_t key[kEach];
+    float l[kEach], most = -INFINITY, all = 0.f;
+    const float* row = a.w.logits + static_cast<int64_t>(t) * a.E;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) l[i] = i * 32 + lane < a.E ? __ldcg(row + i * 32 + lane) : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int e = i * 32 + lane;
+        most = fmaxf(most, l[i]);
+        key[i] = e < a.E ? order_of(a.sigmoid ? 1.f / (1.f + expf(-l[i])) + (a.bias ? __ldg(a.bias + e) : 0.f) : l[i]) : 0u;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (!a.sigmoid && !a.renormalize) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (i * 32 + lane < a.E) all += expf(l[i] - most);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    int mine = 0;
+    float value = 0.f;  // of the expert in place `lane`
+    for (int r = 0; r < a.k; ++r) {  // the largest left
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < kEach; ++i) best = max(best, key[i]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        uint32_t at = 0xFFFFFFFFu;
+        float v = 0.f;
+#pragma unroll
+        for (int i = kEach - 1; i >= 0; --i)
+            if (key[i] == best) {
+                at = static_cast<uint32_t>(i * 32 + lane);
+                v = l[i];
+            }
+        at = __reduce_min_sync(0xffffffffu, at);
+        v = __shfl_sync(0xffffffffu, v, at & 31u);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (static_cast<uint32_t>(i * 32 + lane) == at) key[i] = 0;
+        if (lane == r) {
+            mine = static_cast<int>(at);
+            value = v;
+        }
+    }
+    float s = lane < a.k ? (a.sigmoid ? 1.f / (1.f + expf(-value)) : expf(value - most)) : 0.f;
+    if (a.renormalize) {
+        all = s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    if (a.renormalize || !a.sigmoid) s = __fdiv_rn(s, fmaxf(all, 1e-30f));  // (sigmoids may all be 0)
+    if (lane < a.k) {
+        const int p = t * a.k + lane;
+        a.w.chosen[p] = static_cast<uint16_t>(mine);
+        a.w.share[p] = s * a.scale;
+        if (a.ids) a.ids[p] = mine;
+        if (a.weights) a.weights[p] = s * a.scale;
+    }
+}
+
+// The list, made by one CTA.
+__device__ __forceinline__ void make_list(const RouteArgs& a, unsigned* status) {
+    constexpr int kW = kRouteThreads / 32;
+    __shared__ uint32_t mask[2][kMoeMaxExperts];  // tokens of an expert, one bit each
+    __shared__ uint16_t start[kMoeMaxExperts];    // of its pairs
+    __shared__ uint32_t sums[kW];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pairs = a.T * a.k;
+    List& list = *a.w.list;
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) mask[0][e] = mask[1][e] = 0;
+    __syncthreads();
+    for (int p = threadIdx.x; p < pairs; p += kRouteThreads) {
+        const int t = p / a.k;
+        atomicOr(&mask[t >> 5][__ldcg(a.w.chosen + p)], 1u << (t & 31));
+    }
+    uint32_t carry = 0;  // (entries << 16) + pairs of the experts before
+    for (int e0 = 0; e0 < a.E; e0 += kRouteThreads) {
+        __syncthreads();
+        const int e = e0 + static_cast<int>(threadIdx.x);
+        const uint32_t n = e < a.E ? __popc(mask[0][e]) + __popc(mask[1][e]) : 0u, own = ((n + a.cap - 1) / a.cap << 16) + n;
+        uint32_t upto = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) sums[warp] = upto;
+        __syncthreads();
+        upto += carry;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            if (w < warp) upto += sums[w];
+            carry += sums[w];
+        }
+        const uint32_t before = upto - own;
+        int at = static_cast<int>(before >> 16);
+        for (uint32_t i = 0; i < n; i += a.cap) {
+            list.expert[at] = static_cast<uint16_t>(e);
+            list.base[at++] = static_cast<uint16_t>((before & 0xFFFFu) + i);
+        }
+        if (e < a.E) start[e] = static_cast<uint16_t>(before & 0xFFFFu);
+    }
+    if (threadIdx.x == 0) {
+        list.entries = static_cast<int>(carry >> 16);
+        list.base[carry >> 16] = static_cast<uint16_t>(carry & 0xFFFFu);
+    }
+    __syncthreads();
+    for (int p = threadIdx.x; p < pairs; p += kRouteThreads) {  // an expert's pairs by token
+        const int t = p / a.k, e = __ldcg(a.w.chosen + p);
+        const uint32_t lo = mask[0][e], hi = mask[1][e], bit = 1u << (t & 31);
+        const int at = start[e] + (t < 32 ? __popc(lo & (bit - 1)) : __popc(lo) + __popc(hi & (bit - 1)));
+        if (!in_bounds(at < pairs, status)) continue;
+        list.token[at] = static_cast<uint8_t>(t);
+        list.weight[at] = __ldcg(a.w.share + p);
+        a.w.place[p] = at;
+    }
+}
+
+// Whether this CTA is the last of `of` that arrive at `counter`, which is then ready for the next call.
+__device__ __forceinline__ bool last_of(unsigned* counter, unsigned of) {
+    __shared__ int last;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(counter, 1u) == of - 1u;
+        if (last) *counter = 0;
+        __threadfence();
+    }
+    __syncthreads();
+    return last != 0;
+}
 
 // TB tokens a CTA (1 or 8), one expert.
 template <int TB>
@@ -141,31 +304,27 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
             fma2_mixed(acc[i][0], acc[i][1], w.y, x[i].y);
             fma2_mixed(acc[i][0], acc[i][1], w.z, x[i].z);
             fma2_mixed(acc[i][0], acc[i][1], w.w, x[i].w);
-            if (e == 0 && i < tokens) {  // one expert's CTAs leave x as the products want it
-                uint16_t* to = a.w.xp + (t0 + i) * padded(a.H) + unit_place(8 * v);
-                *reinterpret_cast<uint4*>(to) = make_uint4(x[i].x, x[i].z, x[i].y, x[i].w);
-            }
         }
         w = wn;
     }
-    if (e == 0) {  // sums of 128 elements, a half-warp each
-        for (int v0 = 0; v0 < (vecs + 15) / 16 * 16; v0 += kRouteThreads) {
+    for (int i = e; i < tokens; i += a.E) {  // a token's row as the products want it, and the sums of 128 elements: a half-warp each
+        for (int v0 = 0; v0 < vecs; v0 += kRouteThreads) {
             const int v = v0 + static_cast<int>(threadIdx.x);
-            for (int i = 0; i < tokens; ++i) {
-                float s = 0.f;
-                if (v < vecs) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(a.x + (t0 + i) * a.x_stride + 8 * static_cast<int64_t>(v));
-                    const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+            const int64_t row = padded(a.H) * (t0 + i);
+            float s = 0.f;
+            if (v < vecs) {
+                const uint4 q = *reinterpret_cast<const uint4*>(a.x + (t0 + i) * a.x_stride + 8 * static_cast<int64_t>(v));
+                *reinterpret_cast<uint4*>(a.w.xp + row + unit_place(8 * v)) = make_uint4(q.x, q.z, q.y, q.w);
+                const uint32_t h[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-                        s += f.x + f.y;
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+                    s += f.x + f.y;
                 }
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if ((threadIdx.x & 15) == 0 && v < vecs) a.w.xsum[(t0 + i) * (padded(a.H) / 128) + (v >> 4)] = kEight * s;
             }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if ((threadIdx.x & 15) == 0 && v < vecs) a.w.xsum[(row >> 7) + (v >> 4)] = kEight * s;
         }
     }
 #pragma unroll
@@ -182,144 +341,18 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
         for (int i = 1; i < kW; ++i) s += part[i][threadIdx.x];
         a.w.logits[static_cast<int64_t>(t0 + threadIdx.x) * a.E + e] = s;
     }
-}
-
-// A float as a whole number of the same order, above 1; NaN: 1 (below all).
-__device__ __forceinline__ uint32_t order_of(float f) {
-    if (f != f) return 1u;
-    const uint32_t b = __float_as_uint(f + 0.f);  // -0 and 0 are one value
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-
-// The chosen experts with their tokens, in shared memory. An expert with more than `cap` tokens is listed several
-// times, each time with the next of them.
-struct List {
-    int entries;
-    uint16_t expert[kMoeMaxExperts + kMaxPairs / 8];
-    uint16_t base[kMoeMaxExperts + kMaxPairs / 8 + 1];  // of an entry's first (token, expert) pair
-    uint8_t token[kMaxPairs];
-    float weight[kMaxPairs];
-    // while it is made
-    uint16_t chosen[kMaxPairs];  // [T][k]
-    float share[kMaxPairs];
-    uint32_t mask[2][kMoeMaxExperts];  // tokens of an expert, one bit each
-    uint32_t sums[16];
-};
-
-// One warp chooses the experts of token t and their weights.
-__device__ __forceinline__ void choose(const RouteArgs& a, List& list, int t) {
-    constexpr int kEach = kMoeMaxExperts / 32;
-    const int lane = threadIdx.x & 31;
-    uint32_t key[kEach];
-    float most = -INFINITY, all = 0.f;
-    const float* row = a.w.logits + static_cast<int64_t>(t) * a.E;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        key[i] = 0;
-        const int e = i * 32 + lane;
-        if (i * 32 >= a.E || e >= a.E) continue;
-        const float l = __ldcg(row + e);
-        most = fmaxf(most, l);
-        key[i] = order_of(a.sigmoid ? 1.f / (1.f + expf(-l)) + (a.bias ? a.bias[e] : 0.f) : l);
+    if (!last_of(a.w.arrived + blockIdx.y, gridDim.x)) return;
+    if (warp < tokens) {
+        if (a.E <= 64)
+            choose<2>(a, t0 + warp);
+        else if (a.E <= 256)
+            choose<8>(a, t0 + warp);
+        else
+            choose<kMoeMaxExperts / 32>(a, t0 + warp);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if (!a.sigmoid && !a.renormalize) {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (i * 32 < a.E && i * 32 + lane < a.E) all += expf(__ldcg(row + i * 32 + lane) - most);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    }
-    int mine = 0;
-    for (int r = 0; r < a.k; ++r) {
-        uint32_t best = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (i * 32 < a.E) best = max(best, key[i]);
-        best = __reduce_max_sync(0xffffffffu, best);
-        uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-        for (int i = kEach - 1; i >= 0; --i)
-            if (i * 32 < a.E && key[i] == best) at = static_cast<uint32_t>(i * 32 + lane);
-        at = __reduce_min_sync(0xffffffffu, at);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (static_cast<uint32_t>(i * 32 + lane) == at) key[i] = 0;
-        if (lane == r) mine = static_cast<int>(at);
-    }
-    const float l = lane < a.k ? __ldcg(row + mine) : 0.f;
-    float s = lane < a.k ? (a.sigmoid ? 1.f / (1.f + expf(-l)) : expf(l - most)) : 0.f;
-    if (a.renormalize) {
-        all = s;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    }
-    if (a.renormalize || !a.sigmoid) s = __fdiv_rn(s, fmaxf(all, 1e-30f));  // (sigmoids may all be 0)
-    if (lane < a.k) {
-        list.chosen[t * a.k + lane] = static_cast<uint16_t>(mine);
-        list.share[t * a.k + lane] = s * a.scale;
-    }
-}
-
-// The list, made by one CTA of WARPS warps. `results`: this CTA writes what the caller and the last kernel want of it.
-template <int WARPS>
-__device__ __forceinline__ void make_list(const RouteArgs& a, List& list, int cap, bool results, unsigned* status) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pairs = a.T * a.k;
-    for (int e = threadIdx.x; e < kMoeMaxExperts; e += WARPS * 32) list.mask[0][e] = list.mask[1][e] = 0;
-    for (int t = warp; t < a.T; t += WARPS) choose(a, list, t);
+    if (gridDim.y > 1 && !last_of(a.w.arrived + 15, gridDim.y)) return;
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += WARPS * 32) {
-        const int t = p / a.k;
-        atomicOr(&list.mask[t >> 5][list.chosen[p]], 1u << (t & 31));
-    }
-    uint32_t carry = 0;  // (entries << 16) + pairs of the experts before
-    for (int e0 = 0; e0 < a.E; e0 += WARPS * 32) {
-        __syncthreads();
-        const int e = e0 + static_cast<int>(threadIdx.x);
-        const uint32_t lo = e < a.E ? list.mask[0][e] : 0u, hi = e < a.E ? list.mask[1][e] : 0u;
-        const uint32_t n = __popc(lo) + __popc(hi), own = ((n + cap - 1) / cap << 16) + n;
-        uint32_t upto = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
-        if (lane == 31) list.sums[warp] = upto;
-        __syncthreads();
-        upto += carry;
-        for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) upto += list.sums[w];
-            carry += list.sums[w];
-        }
-        const uint32_t before = upto - own;
-        int at = static_cast<int>(before >> 16), base = static_cast<int>(before & 0xFFFFu);
-        for (uint32_t i = 0; i < n; i += cap) {
-            list.expert[at] = static_cast<uint16_t>(e);
-            list.base[at++] = static_cast<uint16_t>(base + i);
-        }
-        // pairs of an expert by token
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            for (uint32_t left = h ? hi : lo; left != 0; left &= left - 1) {
-                const int t = 32 * h + __ffs(left) - 1;
-                int j = 0;
-                while (j + 1 < a.k && list.chosen[t * a.k + j] != e) ++j;
-                list.token[base] = static_cast<uint8_t>(t);
-                list.weight[base] = list.share[t * a.k + j];
-                if (results && in_bounds(base < pairs, status)) {
-                    a.w.place[t * a.k + j] = base;
-                    if (a.ids) a.ids[t * a.k + j] = e;
-                    if (a.weights) a.weights[t * a.k + j] = list.share[t * a.k + j];
-                }
-                ++base;
-            }
-    }
-    if (threadIdx.x == 0) {
-        list.entries = static_cast<int>(carry >> 16);
-        list.base[carry >> 16] = static_cast<uint16_t>(carry & 0xFFFFu);
-    }
-    __syncthreads();
+    make_list(a, status);
 }
 
 // ------------------------------------------------------------------------------------ products
@@ -542,13 +575,31 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     float* heads = reinterpret_cast<float*>(smem + kWarps * kStages * Stage<F>::kBytes);
     if (!DOWN) {
         griddep_wait();
-        griddep_launch_dependents();  // (after the wait: the next kernel may read the logits before its own)
+        griddep_launch_dependents();  // (after the wait: the next kernel may read the list before its own)
     } else {
         griddep_launch_dependents();
-        // The logits are the work of the kernel before the last: complete, since every CTA of the last one had passed
-        // its wait before this kernel could start.
+        // The list is the work of the kernel before the last: complete, since every CTA of the last one had passed its
+        // wait before this kernel could start.
     }
-    make_list<kWarps>(r, list, 8 * NT, !DOWN && blockIdx.x == 0, status);
+    {
+        const List* from = r.w.list;
+        const int entries = __ldcg(&from->entries), pairs = r.T * r.k;
+        for (int i = threadIdx.x; i < entries; i += kWarps * 32) {
+            list.expert[i] = __ldcg(from->expert + i);
+            list.base[i] = __ldcg(from->base + i);
+        }
+        for (int i = threadIdx.x; i < pairs; i += kWarps * 32) {
+            if (DOWN)
+                list.weight[i] = __ldcg(from->weight + i);
+            else
+                list.token[i] = __ldcg(from->token + i);
+        }
+        if (threadIdx.x == 0) {
+            list.entries = entries;
+            list.base[entries] = static_cast<uint16_t>(pairs);
+        }
+        __syncthreads();
+    }
 
     const int rank = static_cast<int>(blockIdx.x) % kCluster, cluster = static_cast<int>(blockIdx.x) / kCluster;
     const int clusters = static_cast<int>(gridDim.x) / kCluster;
@@ -831,13 +882,13 @@ size_t moe_workspace_bytes(int E, int H, int I) { return space_of(nullptr, E, H,
 
 cudaError_t launch_moe(const MoeParams& p, int sm_count, cudaStream_t s, unsigned* status) {
     const Space ws = space_of(p.workspace, p.E, p.H, p.I);
-    const RouteArgs r = {p.x, p.x_stride, p.router, p.bias, p.ids, p.weights, ws, p.T, p.E, p.H, p.k, p.sigmoid, p.renormalize, p.scale};
+    // Tokens that an expert's weights are multiplied by at a time: 8 where the average expert has few (the kernel with
+    // the most warps), 16, or 32; an expert with more is streamed again.
+    const int nt = p.T <= 8 || p.T * p.k <= 3 * p.E ? 1 : p.T * p.k <= 10 * p.E || p.T <= 16 ? 2 : 4;
+    const RouteArgs r = {p.x, p.x_stride, p.router, p.bias, p.ids, p.weights, ws, p.T, p.E, p.H, p.k, p.sigmoid, p.renormalize, p.scale, 8 * nt};
     cudaError_t e = p.T == 1 ? launch(route_kernel<1>, dim3(static_cast<unsigned>(p.E), 1), kRouteThreads, 0, 1, s, r, status)
                              : launch(route_kernel<8>, dim3(static_cast<unsigned>(p.E), static_cast<unsigned>((p.T + 7) / 8)), kRouteThreads, 0, 1, s, r, status);
     if (e != cudaSuccess) return e;
-    // Tokens that an expert's weights are multiplied by at a time: 8 where there are no more, 16 where the average
-    // expert has up to 10 (one with more is streamed again), else 32.
-    const int nt = p.T <= 8 ? 1 : p.T * p.k <= 10 * p.E || p.T <= 16 ? 2 : 4;
     e = nt == 1 ? launch_products<1>(p, r, sm_count, s, status)
         : nt == 2 ? launch_products<2>(p, r, sm_count, s, status)
                   : launch_products<4>(p, r, sm_count, s, status);
