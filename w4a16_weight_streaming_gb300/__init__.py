@@ -823,17 +823,23 @@ class Experts:
         if w4a16_moe_workspace_bytes(E, self.hidden, self.inner) == 0:
             raise W4A16Error(ERR_UNSUPPORTED_SHAPE, "Experts")
 
-        def stacked(codes, scales):
-            pairs = []
+        def in_turns(t):  # 16 columns of gate, the same 16 of up, and on
+            return t.unflatten(-1, (2, -1, 16)).transpose(-3, -2).flatten(-3).contiguous()
+
+        def packed(codes, scales, turns):
+            K, N = codes.shape[1] * 8, codes.shape[2]
+            q = torch.empty((E, K // 8 * N), dtype=torch.int32, device=codes.device)
+            s = torch.empty((E, K // rows * N), dtype=torch.int16, device=codes.device)
+            call = lib.w4a16_repack_nvfp4 if nvfp4 else lib.w4a16_repack
+            shape = (N, K) if nvfp4 else (N, K, group)
             for e in range(E):
-                pairs.append(repack_nvfp4(codes[e], scales[e], stream) if nvfp4 else repack(codes[e], scales[e], group, stream))
-            if stream is None:
-                return torch.stack([q for q, _ in pairs]), torch.stack([s for _, s in pairs])
-            with torch.cuda.stream(stream):
-                return torch.stack([q for q, _ in pairs]), torch.stack([s for _, s in pairs])
+                a, b = (in_turns(codes[e]), in_turns(scales[e])) if turns else (codes[e], scales[e])
+                _check(call(a.data_ptr(), b.data_ptr(), q[e].data_ptr(), s[e].data_ptr(), *shape, _stream_handle(stream)), "Experts")
+            return q, s
 
         self.group, self.nvfp4 = rows, nvfp4
-        self.gate_up, self.down = stacked(gate_up, gate_up_scales), stacked(down, down_scales)
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(gate_up.device)):
+            self.gate_up, self.down = packed(gate_up, gate_up_scales, True), packed(down, down_scales, False)
         self.scales = (gate_up_scale, down_scale)
         self.desc = MoEDesc(*(t.data_ptr() for t in self.gate_up + self.down), _ptr(gate_up_scale), _ptr(down_scale), E,
                             self.hidden, self.inner, rows, int(nvfp4))

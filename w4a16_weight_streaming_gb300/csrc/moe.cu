@@ -21,7 +21,7 @@
 // must follow, so rows of x and of a are kept with their 16-byte units transposed within each 128 (unit w of
 // block t at place 4 w + t). A lane copies what it will read itself, so a warp's ring of stages needs no barrier.
 //
-// Work is a list of items, (listed expert, 32 columns) over all of K, in steps of 128 k. A cluster takes an equal
+// Work is a list of items, (listed expert, 64 columns) over all of K, in steps of 128 k. A cluster takes an equal
 // run of items, its warps equal runs of their steps, wherever that cuts an item: the warp that has an item's
 // beginning keeps its sums and adds the following warps' parts at the end. All of a warp's steps are one stream of
 // copies, whatever items they belong to. The runs are contiguous, so that a CTA meets few experts and finds the
@@ -35,7 +35,7 @@ namespace w4a16 {
 namespace {
 
 constexpr int kRouteThreads = 256;
-constexpr int kStages = 3;    // of a warp's ring
+constexpr int kStages = 2;    // of a warp's ring
 #ifndef MOE_CLUSTER
 #define MOE_CLUSTER 2
 #endif
@@ -77,7 +77,7 @@ struct Space {
     uint16_t* xp;       // [tokens][Hp], transposed units
     uint16_t* act;      // [pairs][Ip], transposed units
     float* xsum;        // [tokens][Hp / 128]: 8 * 2^-24 times the sums of 128 elements of x
-    float* asum;        // [pairs][I / 16]: of 16 elements of a
+    float* asum;        // [pairs][I / 32]: of 32 elements of a
     float* part;        // [pairs][H]
     size_t bytes;
 };
@@ -104,7 +104,7 @@ inline Space space_of(void* base, int E, int H, int I) {
     s.xp = reinterpret_cast<uint16_t*>(take(kMoeMaxTokens * padded(H) * 2));
     s.act = reinterpret_cast<uint16_t*>(take(kMaxPairs * padded(I) * 2));
     s.xsum = reinterpret_cast<float*>(take(kMoeMaxTokens * padded(H) / 128 * 4));
-    s.asum = reinterpret_cast<float*>(take(static_cast<size_t>(kMaxPairs) * (I / 16) * 4));
+    s.asum = reinterpret_cast<float*>(take(static_cast<size_t>(kMaxPairs) * (I / 32) * 4));
     s.part = reinterpret_cast<float*>(take(static_cast<size_t>(kMaxPairs) * H * 4));
     s.bytes = at;
     return s;
@@ -388,43 +388,39 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A stage of a warp's ring: 128 k of 32 columns. Vectors: [band][half][32-k block][column, swizzled]; then scales
-// [row][32 columns]. Column g of block t lies at place g ^ 2 t of its 8, so that neither the copies (8 columns of
+// A stage of a warp's ring: 128 k of 64 columns. Vectors: [16 columns][half][32-k block][column, swizzled]; then scales
+// [row][64 columns]. Column g of block t lies at place g ^ 2 t of its 8, so that neither the copies (8 columns of
 // a block at a time) nor the reads (2 columns of 4 blocks) meet in a bank.
 template <Form F>
 struct Stage {
     static constexpr int kRows = F == kInt4 ? 1 : F == kInt4Small ? 4 : 8;  // of scales
-    static constexpr int kScales = 2048;
-    static constexpr int kBytes = kScales + kRows * 64;
+    static constexpr int kScales = 4096;
+    static constexpr int kBytes = kScales + kRows * 128;
 };
 __device__ __forceinline__ uint32_t vector_place(int lane) {
     const int g = lane >> 2, t = lane & 3;
     return static_cast<uint32_t>(t * 128 + ((g ^ (2 * t)) & 7) * 16);
 }
 
-// Where a lane's copies come from: an item's two bands of 16 columns, at the next step to be copied.
+// Where a lane's copies come from: an item's 64 columns, at the next step to be copied. A block's 64 vectors are 1 KB
+// side by side. (Items of 2 x 16 columns, 256 bytes a block, streamed at 5.0 TB/s with the products left out.)
 template <Form F>
 struct Source {
-    const uint4* w[2];
-    int wt[2];          // vectors from one 32-k block to the next
-    const uint16_t* s[2];  // scales; of kInt4: s[0], this lane's pair
+    const uint4* w;
+    const uint16_t* s;  // kInt4: of this lane's pair
+    int wt;             // vectors from one 32-k block to the next
     int kb, row_left;   // kInt4: steps until the next row of scales
 
-    __device__ __forceinline__ void set(const Matrices& m, int expert, int c0, int c1, int first, int lane) {
-        const int blocks = m.K / 32, rows = m.K / m.G;
-        const int64_t codes = static_cast<int64_t>(expert) * m.N * blocks, scales = static_cast<int64_t>(expert) * m.N * rows;
+    __device__ __forceinline__ void set(const Matrices& m, int expert, int column, int first, int lane) {
+        const int blocks = m.K / 32, rows = m.K / m.G, tile = column >> 7;
         kb = first;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int c = b ? c1 : c0, tile = c >> 7;
-            wt[b] = min(128, m.N - 128 * tile);
-            w[b] = m.w + codes + static_cast<int64_t>(tile) * 128 * blocks + (c & 127) + (lane >> 2) +
-                   static_cast<int64_t>(4 * first + (lane & 3)) * wt[b];
-            s[b] = m.s + scales + static_cast<int64_t>(tile) * 128 * rows + (c & 127);
-        }
+        wt = min(128, m.N - 128 * tile);
+        w = m.w + static_cast<int64_t>(expert) * m.N * blocks + static_cast<int64_t>(tile) * 128 * blocks + (column & 127) + (lane >> 2) +
+            static_cast<int64_t>(4 * first + (lane & 3)) * wt;
+        s = m.s + static_cast<int64_t>(expert) * m.N * rows + static_cast<int64_t>(tile) * 128 * rows + (column & 127);
         if (F == kInt4) {
-            const int q = m.G / 128, row = first / q, b = (lane >> 3) & 1;
-            s[0] = (b ? s[1] : s[0]) + static_cast<int64_t>(row) * (b ? wt[1] : wt[0]) + 2 * (lane & 7);
+            const int q = m.G / 128, row = first / q;
+            s += static_cast<int64_t>(row) * wt + 2 * lane;
             row_left = q - (first - row * q);
         }
     }
@@ -433,137 +429,122 @@ struct Source {
         const uint32_t vec = stage + vector_place(lane);
         if (F == kInt4 || kb * 4 + (lane & 3) < blocks) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                copy16(vec + 1024u * b, w[b]);
-                copy16(vec + 1024u * b + 512u, w[b] + 8);
-            }
+            for (int i = 0; i < 8; ++i) copy16(vec + 512u * i, w + 8 * i);
         }
-        w[0] += 4 * wt[0];
-        w[1] += 4 * wt[1];
-        if (F == kInt4) {  // 16 pairs of one row
-            if (lane < 16) copy4(stage + Stage<F>::kScales + 4u * lane, s[0]);
+        w += 4 * wt;
+        const uint32_t to = stage + Stage<F>::kScales + 4u * lane;
+        if (F == kInt4) {
+            copy4(to, s);
             if (--row_left == 0) {
                 row_left = per >> 2;
-                s[0] += (lane >> 3) & 1 ? wt[1] : wt[0];
+                s += wt;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < Stage<F>::kRows / 2; ++j) {
-                const int i = lane + 32 * j, r = i >> 4, b = (i >> 3) & 1;
-                const int sblk = F == kNvfp4 ? kb * 4 + (r >> 1) : kb * 4 + r;
-                if (sblk >= blocks) continue;
-                const int row = F == kNvfp4 ? kb * 8 + r : shift >= 0 ? sblk >> shift : sblk / per;
-                copy4(stage + Stage<F>::kScales + 4u * i, (b ? s[1] : s[0]) + static_cast<int64_t>(row) * (b ? wt[1] : wt[0]) + 2 * (i & 7));
+            for (int r = 0; r < Stage<F>::kRows; ++r) {
+                const int blk = F == kNvfp4 ? kb * 4 + (r >> 1) : kb * 4 + r;
+                if (blk >= blocks) continue;
+                const int row = F == kNvfp4 ? kb * 8 + r : shift >= 0 ? blk >> shift : blk / per;
+                copy4(to + 128u * r, s + static_cast<int64_t>(row) * wt + 2 * lane);
             }
         }
         ++kb;
     }
 };
 
-// sum[b][n] += a stage's columns times TILES * 8 tokens; rows[n]: where this lane's token of those 8 has the step's unit;
-// sums[n] (kInt4): where it has what adds up, over the quad with DOWN, to 8 * 2^-24 times the sum of its 128 elements.
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int w) { return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w; }
+
+// sum[c][n] += 16 columns c of a stage times 8 tokens n, TILES * 8 tokens; rows[n]: where this lane's token of those 8 has
+// the step's unit; sums[n] (kInt4): where it has 8 * 2^-24 times the sum of its 128 elements, or, with DOWN, one of four
+// parts of it a lane of the quad.
 //
 // kInt4: a pair of codes q, taken out of a word by a mask, is a pair of fp16 numbers q 2^-24 or 16 q 2^-24 (subnormal,
 // exact in a product), so 5 instructions make the operands of 8 weights. Sums of either kind are kept for the step,
 // sums of x come with it, and (q - 8) s then costs three instructions a sum: w is not rounded to fp16. (The other
-// forms' 13 and 12 instructions for 8 weights bound the products otherwise: gate_up of 16 tokens 348 us.) Sums are
-// 2^24 too small.
+// forms' 13 and 12 instructions for 8 weights bound the products otherwise.) Sums are 2^24 too small.
 template <int NT, int TILES, Form F, bool DOWN>
-__device__ __forceinline__ void multiply(float (&sum)[2][NT][4], uint32_t stage, const uint16_t* base, const uint32_t (&rows)[NT],
+__device__ __forceinline__ void multiply(float (&sum)[4][NT][4], uint32_t stage, const uint16_t* base, const uint32_t (&rows)[NT],
                                          const float* sums_base, const uint32_t (&sums)[NT], bool there, int lane) {
-    uint4 x[TILES];
-    float2 less[TILES];
+    uint4 x[TILES][4];
+    float less[TILES];
 #pragma unroll
     for (int n = 0; n < TILES; ++n) {
-        x[n] = *reinterpret_cast<const uint4*>(base + rows[n]);
-        if (F == kInt4 && DOWN) less[n] = *reinterpret_cast<const float2*>(sums_base + sums[n]);
-        if (F == kInt4 && !DOWN) less[n].x = sums_base[sums[n]];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) x[n][w] = *reinterpret_cast<const uint4*>(base + rows[n] + 32 * w);
+        if (F == kInt4) less[n] = sums_base[sums[n]];
     }
-    uint4 v[4];
     const uint32_t vec = stage + vector_place(lane), sc = stage + Stage<F>::kScales + 2u * (lane >> 2);
+    float off[TILES][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lds128(vec + 512u * i);
-    uint32_t s[4][F == kNvfp4 ? 2 : 1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int c = 0; c < 4; ++c) {
+        const uint4 v[2] = {lds128(vec + 1024u * c), lds128(vec + 1024u * c + 512u)};
+        uint32_t s[2][2];  // of columns g, g + 8; NVFP4: of a block's halves
         const uint32_t row = F == kInt4 ? 0u : F == kInt4Small ? lane & 3u : 2u * (lane & 3u);
-        s[i][0] = lds16(sc + 64u * row + 16u * i);
-        if (F == kNvfp4) s[i][F == kNvfp4 ? 1 : 0] = lds16(sc + 64u * (row + 1) + 16u * i);
-        if (F != kInt4) {  // past K: what the stage holds is not of this step
-            s[i][0] = there ? s[i][0] * 0x10001u : 0u;
-            if (F == kNvfp4) s[i][F == kNvfp4 ? 1 : 0] = there ? s[i][F == kNvfp4 ? 1 : 0] * 0x10001u : 0u;
-        }
-    }
-    float one[2][TILES][4], sixteen[2][TILES][4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        uint4 ahead[TILES];
-#pragma unroll
-        for (int n = 0; n < TILES; ++n)
-            if (w < 3) ahead[n] = *reinterpret_cast<const uint4*>(base + rows[n] + (w + 1) * 32);
-        uint32_t d[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t word = w == 0 ? v[i].x : w == 1 ? v[i].y : w == 2 ? v[i].z : v[i].w;
-            if (F == kNvfp4) {
-                dequant8_nvfp4(word, s[i][F == kNvfp4 && w >= 2 ? 1 : 0], d[i]);
-            } else if (F == kInt4Small) {
-                dequant8(word, s[i][0], d[i]);
-            } else {
-                d[i][0] = word & 0x000F000Fu;
-                d[i][1] = word & 0x00F000F0u;
-                d[i][2] = (word >> 8) & 0x000F000Fu;
-                d[i][3] = (word >> 8) & 0x00F000F0u;
+        for (int i = 0; i < 2; ++i) {
+            s[i][0] = lds16(sc + 128u * row + 32u * c + 16u * i);
+            if (F == kNvfp4) s[i][1] = lds16(sc + 128u * (row + 1) + 32u * c + 16u * i);
+            if (F != kInt4) {  // past K: what the stage holds is not of this step
+                s[i][0] = there ? s[i][0] * 0x10001u : 0u;
+                if (F == kNvfp4) s[i][1] = there ? s[i][1] * 0x10001u : 0u;
             }
         }
+        float one[TILES][4], sixteen[TILES][4];
 #pragma unroll
-        for (int n = 0; n < TILES; ++n) {
-            if (F == kInt4) {
+        for (int w = 0; w < 4; ++w) {
+            uint32_t d[2][4];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    if (w == 0) {
-                        mma16816_first(one[b][n], d[2 * b][0], d[2 * b + 1][0], d[2 * b][2], d[2 * b + 1][2], x[n].x, x[n].y);
-                        mma16816_first(sixteen[b][n], d[2 * b][1], d[2 * b + 1][1], d[2 * b][3], d[2 * b + 1][3], x[n].z, x[n].w);
-                    } else {
-                        mma16816(one[b][n], d[2 * b][0], d[2 * b + 1][0], d[2 * b][2], d[2 * b + 1][2], x[n].x, x[n].y);
-                        mma16816(sixteen[b][n], d[2 * b][1], d[2 * b + 1][1], d[2 * b][3], d[2 * b + 1][3], x[n].z, x[n].w);
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t word = word_of(v[i], w);
+                if (F == kNvfp4) {
+                    dequant8_nvfp4(word, s[i][w >> 1], d[i]);
+                } else if (F == kInt4Small) {
+                    dequant8(word, s[i][0], d[i]);
+                } else {
+                    d[i][0] = word & 0x000F000Fu;
+                    d[i][1] = word & 0x00F000F0u;
+                    d[i][2] = (word >> 8) & 0x000F000Fu;
+                    d[i][3] = (word >> 8) & 0x00F000F0u;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < TILES; ++n) {
+                if (F == kInt4 && w == 0) {
+                    mma16816_first(one[n], d[0][0], d[1][0], d[0][2], d[1][2], x[n][w].x, x[n][w].y);
+                    mma16816_first(sixteen[n], d[0][1], d[1][1], d[0][3], d[1][3], x[n][w].z, x[n][w].w);
+                } else if (F == kInt4) {
+                    mma16816(one[n], d[0][0], d[1][0], d[0][2], d[1][2], x[n][w].x, x[n][w].y);
+                    mma16816(sixteen[n], d[0][1], d[1][1], d[0][3], d[1][3], x[n][w].z, x[n][w].w);
+                } else {
+                    if (c == 0 && !there) x[n][w] = make_uint4(0u, 0u, 0u, 0u);
+                    mma16816(sum[c][n], d[0][0], d[1][0], d[0][2], d[1][2], x[n][w].x, x[n][w].y);
+                    mma16816(sum[c][n], d[0][1], d[1][1], d[0][3], d[1][3], x[n][w].z, x[n][w].w);
+                }
+            }
+        }
+        if (F == kInt4) {
+            const float f[2] = {__half2float(__ushort_as_half(static_cast<unsigned short>(s[0][0]))),
+                                __half2float(__ushort_as_half(static_cast<unsigned short>(s[1][0])))};
+#pragma unroll
+            for (int n = 0; n < TILES; ++n) {
+                if (c == 0) {  // from the lanes of tokens 2 t, 2 t + 1
+                    float total = less[n];
+                    if (DOWN) {
+                        total += __shfl_xor_sync(0xffffffffu, total, 1);
+                        total += __shfl_xor_sync(0xffffffffu, total, 2);
                     }
+                    off[n][0] = __shfl_sync(0xffffffffu, total, (lane & 3) * 8);
+                    off[n][1] = __shfl_sync(0xffffffffu, total, (lane & 3) * 8 + 4);
                 }
-            } else {
-                if (!there) x[n] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    mma16816(sum[b][n], d[2 * b][0], d[2 * b + 1][0], d[2 * b][2], d[2 * b + 1][2], x[n].x, x[n].y);
-                    mma16816(sum[b][n], d[2 * b][1], d[2 * b + 1][1], d[2 * b][3], d[2 * b + 1][3], x[n].z, x[n].w);
-                }
-            }
-            if (w < 3) x[n] = ahead[n];
-        }
-    }
-    if (F == kInt4) {
-        float f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(s[i][0])));
-#pragma unroll
-        for (int n = 0; n < TILES; ++n) {
-            // from the lanes of tokens 2 t, 2 t + 1
-            float total = less[n].x;
-            if (DOWN) {
-                total += less[n].y;
-                total += __shfl_xor_sync(0xffffffffu, total, 1);
-                total += __shfl_xor_sync(0xffffffffu, total, 2);
-            }
-            const float off[2] = {__shfl_sync(0xffffffffu, total, (lane & 3) * 8), __shfl_sync(0xffffffffu, total, (lane & 3) * 8 + 4)};
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    sum[b][n][i] = fmaf(f[2 * b + (i >> 1)], fmaf(0.0625f, sixteen[b][n][i], one[b][n][i]) - off[i & 1], sum[b][n][i]);
+                    sum[c][n][i] = fmaf(f[i >> 1], fmaf(0.0625f, sixteen[n][i], one[n][i]) - off[n][i & 1], sum[c][n][i]);
+            }
         }
     }
 }
 
-// DOWN false: gate and up (items of 16 gate and the same 16 up columns), true: down (32 columns).
+// DOWN false: gate and up (16 columns of gate, the 16 of up, twice an item), true: down.
 template <int NT, Form F, bool DOWN>
 __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Matrices m, const RouteArgs r, int I, unsigned* status) {
     constexpr int kWarps = warps_for(NT);
@@ -571,7 +552,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     __shared__ List list;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = r.H;
     const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * kStages * Stage<F>::kBytes);
-    // parts of items that begin in an earlier warp: [warp][band][n][register][lane]
+    // parts of items that begin in an earlier warp: [warp][16 columns][n][register][lane]
     float* heads = reinterpret_cast<float*>(smem + kWarps * kStages * Stage<F>::kBytes);
     if (!DOWN) {
         griddep_wait();
@@ -603,7 +584,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
 
     const int rank = static_cast<int>(blockIdx.x) % kCluster, cluster = static_cast<int>(blockIdx.x) / kCluster;
     const int clusters = static_cast<int>(gridDim.x) / kCluster;
-    const int chunks = DOWN ? H / 32 : I / 16;
+    const int chunks = m.N / 64;
     const int steps = static_cast<int>(padded(m.K) / 128), blocks = m.K / 32;
     const int per = F == kNvfp4 ? 1 : m.G / 32, shift = (per & (per - 1)) == 0 ? __ffs(per) - 1 : -1;
     const int64_t items = static_cast<int64_t>(list.entries) * chunks;
@@ -617,25 +598,21 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     Source<F> src;
     const int64_t first = item0 + s0 / steps;
     int entry = static_cast<int>(first / chunks), chunk = static_cast<int>(first % chunks), kb = s0 % steps;
-    int c_entry = entry, c_chunk = chunk, c_kb = kb, c_left = s1 - s0;  // (c_kb: of an item's first step only)
-    auto aim = [&]() {
-        src.set(m, list.expert[c_entry], DOWN ? 32 * c_chunk : 16 * c_chunk, DOWN ? 32 * c_chunk + 16 : I + 16 * c_chunk, c_kb, lane);
-    };
+    int c_entry = entry, c_chunk = chunk, c_left = s1 - s0;
     auto fetch = [&](int slot) {
         if (c_left > 0) {
             src.copy(ring + static_cast<uint32_t>(slot * Stage<F>::kBytes), blocks, per, shift, lane);
             if (--c_left > 0 && src.kb == steps) {
-                c_kb = 0;
                 if (++c_chunk == chunks) {
                     c_chunk = 0;
                     ++c_entry;
                 }
-                aim();
+                src.set(m, list.expert[c_entry], 64 * c_chunk, 0, lane);
             }
         }
         copies_commit();
     };
-    if (c_left > 0) aim();
+    if (c_left > 0) src.set(m, list.expert[c_entry], 64 * c_chunk, kb, lane);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(i);
     if (DOWN) griddep_wait();
@@ -643,8 +620,8 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     const uint16_t* const rows_of = DOWN ? r.w.act : r.w.xp;
     const float* const sums_of = DOWN ? r.w.asum : r.w.xsum;
     uint32_t rows[NT], sums[NT];  // of this lane's tokens, at step kb (below 2^32: 1024 rows of 65,536 at most)
-    float acc[2][NT][4];
-    constexpr int kSums = DOWN ? 8 : 1;  // a step
+    float acc[4][NT][4];
+    constexpr int kSums = DOWN ? 4 : 1;  // a step
     int base = 0, count = 0, tiles = 1;
     const int width = static_cast<int>(padded(m.K));
     auto meet = [&]() {  // the rows of an entry's tokens at step kb; a place without a token reads the first one's
@@ -656,18 +633,18 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
             const int i = 8 * n + (lane >> 2), pair = base + (i < count ? i : 0);
             const int row = DOWN ? pair : list.token[pair];
             rows[n] = static_cast<uint32_t>(row * width + kb * 128 + (lane & 3) * 8);
-            sums[n] = static_cast<uint32_t>(DOWN ? row * (I / 16) + kb * 8 + 2 * (lane & 3) : row * (width / 128) + kb);
+            sums[n] = static_cast<uint32_t>(DOWN ? row * (I / 32) + kb * 4 + (lane & 3) : row * (width / 128) + kb);
         }
     };
     auto clear = [&]() {
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[b][n][i] = 0.f;
+                for (int i = 0; i < 4; ++i) acc[c][n][i] = 0.f;
     };
-    auto finish = [&]() {  // a lane's columns g, g + 8 of both bands for tokens 2 t, 2 t + 1 of 8
+    auto finish = [&]() {  // a lane's columns g, g + 8 of each 16 for tokens 2 t, 2 t + 1 of 8
         const float factor = F == kNvfp4 ? m.factor[list.expert[entry]] : F == kInt4 ? 16777216.f : 1.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -679,36 +656,37 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
                 if (DOWN) {
                     if (!there) continue;
                     const float w = list.weight[pair] * factor;
-                    float* to = r.w.part + static_cast<int64_t>(pair) * H + 32 * chunk + (lane >> 2);
-                    to[0] = w * acc[0][n][h];
-                    to[8] = w * acc[0][n][2 + h];
-                    to[16] = w * acc[1][n][h];
-                    to[24] = w * acc[1][n][2 + h];
-                } else {
-                    float both = 0.f;
+                    float* to = r.w.part + static_cast<int64_t>(pair) * H + 64 * chunk + (lane >> 2);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float g = acc[0][n][2 * q + h] * factor, u = acc[1][n][2 * q + h] * factor;
+                    for (int c = 0; c < 4; ++c) {
+                        to[16 * c] = w * acc[c][n][h];
+                        to[16 * c + 8] = w * acc[c][n][2 + h];
+                    }
+                } else {
+                    float all = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float g = acc[q & 2][n][2 * (q & 1) + h] * factor, u = acc[(q & 2) + 1][n][2 * (q & 1) + h] * factor;
                         const __half a = __float2half_rn(g / (1.0f + expf(-g)) * u);
-                        both += __half2float(a);
-                        if (there) r.w.act[pair * padded(I) + unit_place(16 * chunk + 8 * q + (lane >> 2))] = __half_as_ushort(a);
+                        all += __half2float(a);
+                        if (there) r.w.act[pair * padded(I) + unit_place(32 * chunk + 8 * q + (lane >> 2))] = __half_as_ushort(a);
                     }
                     if (F == kInt4) {
 #pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) both += __shfl_xor_sync(0xffffffffu, both, o);
-                        if (there && lane < 4) r.w.asum[static_cast<int64_t>(pair) * (I / 16) + chunk] = kEight * both;
+                        for (int o = 4; o < 32; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+                        if (there && lane < 4) r.w.asum[static_cast<int64_t>(pair) * (I / 32) + chunk] = kEight * all;
                     }
                 }
             }
     };
-    float* mine = heads + (warp * 2 * NT * 4) * 32 + lane;
+    float* mine = heads + (warp * 4 * NT * 4) * 32 + lane;
     auto leave = [&]() {
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mine[((b * NT + n) * 4 + i) * 32] = acc[b][n][i];
+                for (int i = 0; i < 4; ++i) mine[((c * NT + n) * 4 + i) * 32] = acc[c][n][i];
     };
 
     bool whole = kb == 0;  // the item's beginning is this warp's
@@ -762,13 +740,13 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
         const int end = s1 - kb + steps;  // of the item, in the cluster's steps
         for (int other = me + 1; other < workers && begin(other) < end; ++other) {
             if (begin(other) == begin(other + 1)) continue;
-            const uint32_t from = map_peer(smem_u32(heads + ((other % kWarps) * 2 * NT * 4) * 32 + lane), static_cast<uint32_t>(other / kWarps));
+            const uint32_t from = map_peer(smem_u32(heads + ((other % kWarps) * 4 * NT * 4) * 32 + lane), static_cast<uint32_t>(other / kWarps));
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[b][n][i] += ld_dsmem_f1(from + ((b * NT + n) * 4 + i) * 128);
+                    for (int i = 0; i < 4; ++i) acc[c][n][i] += ld_dsmem_f1(from + ((c * NT + n) * 4 + i) * 128);
         }
         finish();
     }
@@ -862,7 +840,7 @@ cudaError_t launch_form(const MoeParams& p, const RouteArgs& r, int sm_count, cu
     const Matrices up = {static_cast<const uint4*>(p.gate_up_q), p.gate_up_s, p.gate_up_factor, 2 * p.I, p.H, p.G};
     const Matrices down = {static_cast<const uint4*>(p.down_q), p.down_s, p.down_factor, p.H, p.I, p.G};
     constexpr int kThreads = warps_for(NT) * 32;
-    constexpr size_t smem = warps_for(NT) * (kStages * Stage<F>::kBytes + 2 * NT * 4 * 32 * 4);
+    constexpr size_t smem = warps_for(NT) * (kStages * Stage<F>::kBytes + 4 * NT * 4 * 32 * 4);
     const dim3 grid_up(static_cast<unsigned>(resident_clusters<NT, F, false>(smem, sm_count) * kCluster));
     const cudaError_t e = launch(experts_kernel<NT, F, false>, grid_up, kThreads, smem, kCluster, s, up, r, p.I, status);
     if (e != cudaSuccess) return e;
