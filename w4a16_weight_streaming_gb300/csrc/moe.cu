@@ -21,13 +21,11 @@
 // must follow, so rows of x and of a are kept with their 16-byte units transposed within each 128 (unit w of
 // block t at place 4 w + t). A lane copies what it will read itself, so a warp's ring of stages needs no barrier.
 //
-// Work is a list of items, (listed expert, 64 columns) over all of K, in steps of 128 k. A cluster takes an equal
+// Work is a list of items, (listed expert, 64 columns) over all of K, in steps of 128 k. A CTA takes an equal
 // run of items, its warps equal runs of their steps, wherever that cuts an item: the warp that has an item's
 // beginning keeps its sums and adds the following warps' parts at the end. All of a warp's steps are one stream of
 // copies, whatever items they belong to. The runs are contiguous, so that a CTA meets few experts and finds the
 // rows of their tokens in L1.
-#include <atomic>
-
 #include "common.cuh"
 #include "internal.h"
 
@@ -36,14 +34,10 @@ namespace {
 
 constexpr int kRouteThreads = 256;
 constexpr int kStages = 2;    // of a warp's ring
-#ifndef MOE_CLUSTER
-#define MOE_CLUSTER 2
-#endif
-constexpr int kCluster = MOE_CLUSTER;
 
 // Warps of a gate_up or down CTA, one CTA an SM, by the tokens (8 NT) that they multiply at a time: the registers for
 // their sums.
-__host__ __device__ constexpr int warps_for(int nt) { return nt == 1 ? 16 : nt == 2 ? 12 : 8; }
+__host__ __device__ constexpr int warps_for(int nt) { return nt <= 2 ? 12 : 8; }
 
 // How weights become operands.
 enum Form {
@@ -200,6 +194,19 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t) {
         if (a.ids) a.ids[p] = mine;
         if (a.weights) a.weights[p] = s * a.scale;
     }
+    if (a.T == 1) {  // the list at once: an entry a lane
+        int at = 0;
+        for (int o = 0; o < a.k; ++o) at += __shfl_sync(0xffffffffu, mine, o) < mine;
+        if (lane < a.k) {
+            List& list = *a.w.list;
+            list.expert[at] = static_cast<uint16_t>(mine);
+            list.base[at] = static_cast<uint16_t>(at);
+            list.token[at] = 0;
+            list.weight[at] = s * a.scale;
+            a.w.place[lane] = at;
+            if (lane == 0) list.entries = a.k;
+        }
+    }
 }
 
 // The list, made by one CTA.
@@ -350,6 +357,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
         else
             choose<kMoeMaxExperts / 32>(a, t0 + warp);
     }
+    if (TB == 1) return;
     if (gridDim.y > 1 && !last_of(a.w.arrived + 15, gridDim.y)) return;
     __syncthreads();
     make_list(a, status);
@@ -565,7 +573,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     {
         const List* from = r.w.list;
         const int entries = __ldcg(&from->entries), pairs = r.T * r.k;
-        for (int i = threadIdx.x; i < entries; i += kWarps * 32) {
+        for (int i = threadIdx.x; i < min(pairs, kMoeMaxExperts + kMaxPairs / 8); i += kWarps * 32) {  // (no more entries than pairs)
             list.expert[i] = __ldcg(from->expert + i);
             list.base[i] = __ldcg(from->base + i);
         }
@@ -575,6 +583,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
             else
                 list.token[i] = __ldcg(from->token + i);
         }
+        __syncthreads();
         if (threadIdx.x == 0) {
             list.entries = entries;
             list.base[entries] = static_cast<uint16_t>(pairs);
@@ -582,17 +591,14 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
         __syncthreads();
     }
 
-    const int rank = static_cast<int>(blockIdx.x) % kCluster, cluster = static_cast<int>(blockIdx.x) / kCluster;
-    const int clusters = static_cast<int>(gridDim.x) / kCluster;
     const int chunks = m.N / 64;
     const int steps = static_cast<int>(padded(m.K) / 128), blocks = m.K / 32;
     const int per = F == kNvfp4 ? 1 : m.G / 32, shift = (per & (per - 1)) == 0 ? __ffs(per) - 1 : -1;
     const int64_t items = static_cast<int64_t>(list.entries) * chunks;
-    const int64_t item0 = items * cluster / clusters;
-    const int run = static_cast<int>(items * (cluster + 1) / clusters - item0) * steps;  // the cluster's steps
-    const int workers = kCluster * kWarps, me = rank * kWarps + warp;
-    auto begin = [&](int worker) { return static_cast<int>(static_cast<int64_t>(run) * worker / workers); };
-    const int s0 = begin(me), s1 = begin(me + 1);
+    const int64_t item0 = items * blockIdx.x / gridDim.x;
+    const int run = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x - item0) * steps;  // this CTA's steps
+    auto begin = [&](int w) { return static_cast<int>(static_cast<int64_t>(run) * w / kWarps); };
+    const int s0 = begin(warp), s1 = begin(warp + 1);
 
     // the copying end of the stream
     Source<F> src;
@@ -735,22 +741,28 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     copies_wait<0>();
     const bool open = s0 < s1 && kb != 0;
     if (open && !whole) leave();
-    cluster_sync_all();
+    __syncthreads();
     if (open && whole) {
-        const int end = s1 - kb + steps;  // of the item, in the cluster's steps
-        for (int other = me + 1; other < workers && begin(other) < end; ++other) {
-            if (begin(other) == begin(other + 1)) continue;
-            const uint32_t from = map_peer(smem_u32(heads + ((other % kWarps) * 4 * NT * 4) * 32 + lane), static_cast<uint32_t>(other / kWarps));
+        const int end = s1 - kb + steps;  // of the item, in the CTA's steps
+        constexpr int kBatch = NT == 1 ? 4 : NT == 2 ? 2 : 1, kValues = 16 * NT;
+        for (int other = warp + 1; other < kWarps && begin(other) < end; other += kBatch) {
+            float v[kBatch][kValues];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int o = 0; o < kBatch; ++o) {
+                const int w = other + o;
+                const bool part = w < kWarps && begin(w) < end && begin(w) < begin(w + 1);
+                const float* from = heads + w * kValues * 32 + lane;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int i = 0; i < kValues; ++i)
+                    v[o][i] = part ? from[32 * i] : 0.f;
+            }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[c][n][i] += ld_dsmem_f1(from + ((c * NT + n) * 4 + i) * 128);
+            for (int o = 0; o < kBatch; ++o)
+#pragma unroll
+                for (int i = 0; i < kValues; ++i) acc[i / (4 * NT)][i / 4 % NT][i % 4] += v[o][i];
         }
         finish();
     }
-    cluster_sync_all();
 }
 
 // y of a token: its pairs' sums in the order of choice. Four columns a thread.
@@ -758,19 +770,31 @@ __global__ void __launch_bounds__(256) combine_kernel(const Space ws, uint16_t* 
     griddep_launch_dependents();
     const int64_t i = blockIdx.x * 256LL + threadIdx.x;
     const int quads = H / 4;
-    griddep_wait();
-    if (i >= static_cast<int64_t>(T) * quads) return;
     const int t = static_cast<int>(i / quads), c = static_cast<int>(i % quads) * 4;
+    const bool there = t < T;
+    // (the places are route's work: complete before down could start, and so before this kernel could)
+    int pair[kMoeMaxTop];
+#pragma unroll
+    for (int j = 0; j < kMoeMaxTop; ++j) pair[j] = there && j < k ? __ldcg(ws.place + t * k + j) : 0;
+    griddep_wait();
+    if (!there) return;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int j = 0; j < k; ++j) {
-        const int pair = ws.place[t * k + j];
-        if (!in_bounds(pair >= 0 && pair < T * k, status)) continue;
-        const float4 v = *reinterpret_cast<const float4*>(ws.part + static_cast<int64_t>(pair) * H + c);
-        sum.x += v.x;
-        sum.y += v.y;
-        sum.z += v.z;
-        sum.w += v.w;
+#pragma unroll
+    for (int j0 = 0; j0 < kMoeMaxTop; j0 += 8) {
+        if (j0 >= k) break;
+        float4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = j0 + j < k && in_bounds(pair[j0 + j] >= 0 && pair[j0 + j] < T * k, status)
+                       ? __ldcg(reinterpret_cast<const float4*>(ws.part + static_cast<int64_t>(pair[j0 + j]) * H + c))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sum.x += v[j].x;
+            sum.y += v[j].y;
+            sum.z += v[j].z;
+            sum.w += v[j].w;
+        }
     }
     const __half2 lo = __floats2half2_rn(sum.x, sum.y), hi = __floats2half2_rn(sum.z, sum.w);
     *reinterpret_cast<uint2*>(y + static_cast<int64_t>(t) * H + c) =
@@ -778,7 +802,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const Space ws, uint16_t* 
 }
 
 template <typename Kern, typename... Args>
-cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, Args... args) {
+cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
     if (smem > 0) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
@@ -788,51 +812,12 @@ cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, int cluster, 
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    int n = 0;
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-    if (cluster > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
-        attr[n].val.clusterDim.y = 1;
-        attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
-// Clusters of experts_kernel that the device holds at once (asked once a device): clusters lie within a part of the
-// GPU, so there may be fewer than a quarter of its SMs.
-template <int NT, Form F, bool DOWN>
-int resident_clusters(size_t smem, int sm_count) {
-    static std::atomic<int> known[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count / kCluster;
-    int n = known[dev].load();
-    if (n > 0) return n;
-    auto kern = experts_kernel<NT, F, DOWN>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCluster);
-    cfg.blockDim = dim3(warps_for(NT) * 32);
-    cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
-        cudaGetLastError();
-        return sm_count / kCluster;
-    }
-    known[dev].store(n);
-    return n;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int NT, Form F>
@@ -841,11 +826,10 @@ cudaError_t launch_form(const MoeParams& p, const RouteArgs& r, int sm_count, cu
     const Matrices down = {static_cast<const uint4*>(p.down_q), p.down_s, p.down_factor, p.H, p.I, p.G};
     constexpr int kThreads = warps_for(NT) * 32;
     constexpr size_t smem = warps_for(NT) * (kStages * Stage<F>::kBytes + 4 * NT * 4 * 32 * 4);
-    const dim3 grid_up(static_cast<unsigned>(resident_clusters<NT, F, false>(smem, sm_count) * kCluster));
-    const cudaError_t e = launch(experts_kernel<NT, F, false>, grid_up, kThreads, smem, kCluster, s, up, r, p.I, status);
+    const dim3 grid(static_cast<unsigned>(sm_count));
+    const cudaError_t e = launch(experts_kernel<NT, F, false>, grid, kThreads, smem, s, up, r, p.I, status);
     if (e != cudaSuccess) return e;
-    const dim3 grid_down(static_cast<unsigned>(resident_clusters<NT, F, true>(smem, sm_count) * kCluster));
-    return launch(experts_kernel<NT, F, true>, grid_down, kThreads, smem, kCluster, s, down, r, p.I, status);
+    return launch(experts_kernel<NT, F, true>, grid, kThreads, smem, s, down, r, p.I, status);
 }
 
 template <int NT>
@@ -864,14 +848,14 @@ cudaError_t launch_moe(const MoeParams& p, int sm_count, cudaStream_t s, unsigne
     // the most warps), 16, or 32; an expert with more is streamed again.
     const int nt = p.T <= 8 || p.T * p.k <= 3 * p.E ? 1 : p.T * p.k <= 10 * p.E || p.T <= 16 ? 2 : 4;
     const RouteArgs r = {p.x, p.x_stride, p.router, p.bias, p.ids, p.weights, ws, p.T, p.E, p.H, p.k, p.sigmoid, p.renormalize, p.scale, 8 * nt};
-    cudaError_t e = p.T == 1 ? launch(route_kernel<1>, dim3(static_cast<unsigned>(p.E), 1), kRouteThreads, 0, 1, s, r, status)
-                             : launch(route_kernel<8>, dim3(static_cast<unsigned>(p.E), static_cast<unsigned>((p.T + 7) / 8)), kRouteThreads, 0, 1, s, r, status);
+    cudaError_t e = p.T == 1 ? launch(route_kernel<1>, dim3(static_cast<unsigned>(p.E), 1), kRouteThreads, 0, s, r, status)
+                             : launch(route_kernel<8>, dim3(static_cast<unsigned>(p.E), static_cast<unsigned>((p.T + 7) / 8)), kRouteThreads, 0, s, r, status);
     if (e != cudaSuccess) return e;
     e = nt == 1 ? launch_products<1>(p, r, sm_count, s, status)
         : nt == 2 ? launch_products<2>(p, r, sm_count, s, status)
                   : launch_products<4>(p, r, sm_count, s, status);
     if (e != cudaSuccess) return e;
-    return launch(combine_kernel, dim3(static_cast<unsigned>((static_cast<int64_t>(p.T) * p.H / 4 + 255) / 256)), 256, 0, 1, s, ws, p.y, p.T, p.H, p.k, status);
+    return launch(combine_kernel, dim3(static_cast<unsigned>((static_cast<int64_t>(p.T) * p.H / 4 + 255) / 256)), 256, 0, s, ws, p.y, p.T, p.H, p.k, status);
 }
 
 }  // namespace w4a16
