@@ -6,14 +6,18 @@
 //            of one sign, nothing cancels
 //   the first n of the order
 //
-// A thread keeps the largest logit so far, S and sum w d relative to it, and rescales both when a larger
-// one turns up. A place is a count: logits above the given one, and equal ones before it; "equal or above"
-// is "above the next smaller fp16 number", so either is one packed comparison.
+// A thread takes 32 neighbouring logits (a chunk, 64 bytes in two loads) at a time; it keeps the largest logit
+// so far, S and sum w d relative to it, and rescales both when a larger one turns up. A masked logit is read
+// as -65504, whose weight is 0 where the largest is not as low itself or T is below hundreds; elsewhere, and
+// for infinite ones, a chunk goes the slow way, logit by logit.
 //
-// The first n: each 32 neighbours (a chunk, four lanes' vectors) leave their maximum in shared memory. The
-// first n of a row lie in the n chunks that come first in the order (maximum, then lower chunk): a chunk
-// before another has an element before each of the other's. So a search among the maxima names n chunks,
-// and only their n * 32 elements are read a second time.
+// A place is a count: logits above the given one, and equal ones before it; "equal or above" is "above the
+// next smaller fp16 number", so either is one packed comparison, and a warp with no logit above skips it.
+//
+// The first n: each chunk leaves its maximum in shared memory. The first n of a row lie in the n chunks that
+// come first in the order (maximum, then lower chunk): a chunk before another has an element before each of
+// the other's. So a search among the maxima names n chunks, and only their n * 32 elements are read a
+// second time.
 //
 // A row is a CTA or a cluster, whose parts rank 0 brings together in a fixed order.
 #include <cmath>
@@ -24,9 +28,7 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = 32;       // elements: 4 vectors of 8
+constexpr int kChunk = 32;       // elements, 64 bytes and on their boundary
 constexpr int kCandidates = 1024;
 constexpr int kMaxTop = 32;
 constexpr uint32_t kMasked2 = 0xFC00FC00u;  // (-inf, -inf)
@@ -49,19 +51,22 @@ struct Sums {
     float m, s, d;  // largest logit, sum of weights, sum of weight * exponent (in powers of 2)
 };
 
-template <int NG>
+template <int NG, int kThreads>
 struct __align__(16) Shared {
+    static constexpr int kWarps = kThreads / 32;
     unsigned long long best[kMaxTop];          // this CTA's first tokens
     unsigned long long cand[kCandidates];      // (value key, ~index)
     uint32_t keys[kCandidates];                // (value key of a chunk's maximum, ~chunk)
-    uint32_t group[32];
+    uint32_t first[kThreads];                  // the first of each thread's maxima
+    uint32_t least;
     uint32_t chunk[kMaxTop];
     uint32_t last;                             // value key of the n-th chunk
-    int count;
+    int count, found;
     Sums part[kWarps];
     uint32_t above[kWarps][NG == 0 ? 1 : NG];
     Sums whole;                                // of this CTA
     uint32_t above_whole[NG == 0 ? 1 : NG];
+    uint32_t given[NG == 0 ? 1 : NG];  // bits of a given token's logit, with how many of its chunk before it equal it << 16
 };
 
 // Order of the numbers as 16 bits, above 0; 0 for a masked one. -0 and 0 are one value.
@@ -78,19 +83,14 @@ __device__ __forceinline__ uint32_t below(uint32_t bits) {  // the next smaller 
     return (bits & 0x7FFFu) == 0 ? 0x8001u : (bits & 0x8000u) ? bits + 1 : bits - 1;
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const uint4* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
+__device__ __forceinline__ void ldg_stream(uint32_t* v, const void* p) {  // 32 bytes, aligned to them
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
 }
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -142,103 +142,114 @@ __device__ __forceinline__ Sums joined(Sums a, Sums b, float c) {
     return {m, a.s + b.s, a.d + b.d};
 }
 
-template <int NG, bool TOP>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a, int C, int64_t total, unsigned* status) {
-    extern __shared__ uint16_t chunk_max[];  // fp16 maxima of this CTA's chunks
-    __shared__ Shared<NG> sh;
+__device__ __forceinline__ Sums shuffled(const Sums& a, int o) {
+    return {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.d, o)};
+}
+
+// How many of n sorted keys (descending) are above k.
+__device__ __forceinline__ int above_in(const unsigned long long* sorted, int n, unsigned long long k) {
+    int at = 0;
+#pragma unroll
+    for (int step = 32; step > 0; step >>= 1)
+        if (at + step <= n && sorted[at + step - 1] > k) at += step;
+    return at;
+}
+
+template <int NG, bool TOP, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(const LogprobArgs a, int C, int64_t total, unsigned* status) {
+    extern __shared__ __align__(16) uint16_t chunk_max[];  // fp16 maxima of this CTA's chunks
+    constexpr int kWarps = kThreads / 32;
+    __shared__ Shared<NG, kThreads> sh;
+    constexpr int kG = NG == 0 ? 1 : NG;
     griddep_launch_dependents();
     const int rank = static_cast<int>(blockIdx.x) % C, m = static_cast<int>(blockIdx.x) / C;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint16_t* row = a.logits + static_cast<int64_t>(m) * a.stride;
-    // Vectors are the 16-byte aligned ones that cover the row: vector v holds elements 8 v - off and on.
-    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 7u);
-    const uint4* vec = reinterpret_cast<const uint4*>(row - off);
-    const int NV = (off + a.V + 7) / 8;
-    const int per = ((NV + 3) / 4 + C - 1) / C * 4;
-    const int v0 = min(NV, rank * per), v1 = min(NV, v0 + per);
+    // Chunk i holds elements 32 i - off and on, 64-byte aligned; the first and last may lie outside the row in part.
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 31u);
+    const unsigned char* chunk0 = reinterpret_cast<const unsigned char*>(row - off);
+    const int chunks_all = (off + a.V + 31) / 32, per = (chunks_all + C - 1) / C;
+    const int c0 = min(chunks_all, rank * per), c1 = min(chunks_all, c0 + per);
+    const int inner0 = off == 0 ? 0 : 1, inner1 = (off + a.V) / 32;  // whole chunks
+    uint32_t x[16];
+    auto load = [&](int i) {
+        if (i >= inner0 && i < min(c1, inner1) && in_bounds(m * a.stride + 32LL * i - off + 32 <= total, status)) {
+            ldg_stream(x, chunk0 + static_cast<int64_t>(i) * 64);
+            ldg_stream(x + 8, chunk0 + static_cast<int64_t>(i) * 64 + 32);
+        } else {  // an end of the row, or past this CTA's part
+            const int first = 32 * i - off;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int e = first + 2 * j;
+                const uint32_t lo = i < c1 && e >= 0 && e < a.V ? row[e] : 0xFC00u, hi = i < c1 && e + 1 >= 0 && e + 1 < a.V ? row[e + 1] : 0xFC00u;
+                x[j] = lo | hi << 16;
+            }
+        }
+    };
     griddep_wait();
+    int base = c0 + warp * 32;
+    if (base < c1) load(base + lane);
     float temp = a.temperature ? a.temperature[m] : 1.f;
     if (!(temp > 0.f)) temp = 1.f;
     const float c = fminf(1.44269504088896341f / temp, 1e30f);
 
-    int tok[NG == 0 ? 1 : NG], tvec[NG == 0 ? 1 : NG];
-    uint32_t gt[NG == 0 ? 1 : NG], ge[NG == 0 ? 1 : NG];
-    uint32_t above[NG == 0 ? 1 : NG];
+    int tchunk[kG];
+    uint32_t gt[kG], ge[kG], above[kG];
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
-        tok[j] = j < a.given ? a.tokens[static_cast<int64_t>(m) * a.given + j] : -1;
-        const bool there = tok[j] >= 0 && tok[j] < a.V;
-        const uint32_t bits = there ? row[tok[j]] : 0x7C00u;
+        const int tok = j < a.given ? a.tokens[static_cast<int64_t>(m) * a.given + j] : -1;
+        const bool there = tok >= 0 && tok < a.V;
+        const uint32_t bits = there ? row[tok] : 0x7C00u;
         gt[j] = bits * 0x10001u;
         ge[j] = below(bits) * 0x10001u;
-        tvec[j] = there ? (tok[j] + off) / 8 : 0;
+        tchunk[j] = there ? (tok + off) / 32 : 0;
         above[j] = 0;
+        if (rank == 0 && warp == j % kWarps) {  // equal ones before it in its own chunk, which the counts leave out
+            const int e = 32 * tchunk[j] - off + lane;
+            const bool equal = there && e >= 0 && e < tok && key_of(row[e]) == key_of(bits);
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, equal));
+            if (lane == 0) sh.given[j] = bits | n << 16;
+        }
     }
 
     Sums run = {-INFINITY, 0.f, 0.f};
+    float best = -INFINITY;  // of this thread's chunks, and the first that has it
+    int best_chunk = -1;
     const unsigned long long c2 = pack(c, c);
-    for (int base = v0 + warp * 128; base < v1; base += kWarps * 128) {
-        uint32_t x[4][4];
+    for (; base < c1; base += kThreads) {
+        const int i = base + lane;
+        if (base != c0 + warp * 32) load(i);
+        uint32_t hi = max2(x[0], x[1]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int v = base + u * 32 + lane;
-            uint4 q = make_uint4(kMasked2, kMasked2, kMasked2, kMasked2);
-            const int first = 8 * v - off;
-            if (v < v1) {
-                if (first >= 0 && first + 8 <= a.V) {
-                    if (in_bounds(m * a.stride + first + 8 <= total, status)) q = ldg_stream(vec + v);
-                } else {  // the vectors at the ends of the row: only what is inside
-                    uint32_t e[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) e[i] = first + i >= 0 && first + i < a.V ? row[first + i] : 0xFC00u;
-                    q = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-                }
-            }
-            x[u][0] = q.x;
-            x[u][1] = q.y;
-            x[u][2] = q.z;
-            x[u][3] = q.w;
-        }
-        uint32_t hi = kMasked2;
-        bool plain[4], all_plain = true;  // no masked logit in the vector
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            uint32_t h = max2(max2(x[u][0], x[u][1]), max2(x[u][2], x[u][3]));
-            const uint32_t lo = min2_nan(min2_nan(x[u][0], x[u][1]), min2_nan(x[u][2], x[u][3]));
-            const __half2 lo2 = *reinterpret_cast<const __half2*>(&lo);
-            plain[u] = __low2float(lo2) > -INFINITY && __high2float(lo2) > -INFINITY;
-            all_plain = all_plain && plain[u];
-            hi = max2(hi, h);
-            if (TOP) {
-                h = max2(h, kMasked2);  // (a chunk of NaN alone)
-                h = max2(h, __byte_perm(h, h, 0x1032));
-                h = max2(h, __shfl_xor_sync(0xffffffffu, h, 1));
-                h = max2(h, __shfl_xor_sync(0xffffffffu, h, 2));
-                const int v = base + u * 32 + lane;
-                if ((lane & 3) == 0 && v < v1) chunk_max[(v - v0) >> 2] = static_cast<uint16_t>(h & 0xFFFFu);
-            }
+        for (int j = 2; j < 16; ++j) hi = max2(hi, x[j]);
+        hi = max2(hi, kMasked2);  // (NaN alone)
+        hi = max2(hi, __byte_perm(hi, hi, 0x1032));
+        if (TOP && i < c1) chunk_max[i - c0] = static_cast<uint16_t>(hi & 0xFFFFu);
+        const __half2 hi2 = *reinterpret_cast<const __half2*>(&hi);
+        const float most = __low2float(hi2);
+        if (TOP && most > best) {
+            best = most;
+            best_chunk = i - c0;
         }
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-            __half2 n = __float2half2_rn(0.f);
+            const uint32_t t = i < tchunk[j] ? ge[j] : gt[j];
+            const __half2 t2 = *reinterpret_cast<const __half2*>(&t);
+            if (__any_sync(0xffffffffu, most > __low2float(t2))) {
+                __half2 n = __float2half2_rn(0.f);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const uint32_t t = base + u * 32 + lane < tvec[j] ? ge[j] : gt[j];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    n = __hadd2(n, __hgt2(*reinterpret_cast<const __half2*>(&x[u][i]), *reinterpret_cast<const __half2*>(&t)));
+                for (int q = 0; q < 16; ++q) n = __hadd2(n, __hgt2(*reinterpret_cast<const __half2*>(&x[q]), t2));
+                above[j] += static_cast<uint32_t>(__low2float(n) + __high2float(n));
             }
-            above[j] += static_cast<uint32_t>(__low2float(n) + __high2float(n));
         }
-        const __half2 hi2 = *reinterpret_cast<const __half2*>(&hi);
-        const float most = fmaxf(__low2float(hi2), __high2float(hi2));
         if (most > run.m) rescale(run, most, c);
-        unsigned long long s = pack(0.f, 0.f), d = s;
-        const unsigned long long nm = pack(-run.m, -run.m);
-        auto plain_vector = [&](const uint32_t (&v)[4]) {
+        if (run.m < INFINITY && (run.m + 65504.f) * c > 160.f) {
+            unsigned long long s = pack(0.f, 0.f), d = s;
+            const unsigned long long nm = pack(-run.m, -run.m);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
+            for (int q = 0; q < 16; ++q) {
+                const uint32_t v = max2(x[q], 0xFBFFFBFFu);  // (-65504, -65504)
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
                 const unsigned long long e = mul2(add2(pack(f.x, f.y), nm), c2);
                 float e0, e1;
                 unpack(e, e0, e1);
@@ -246,95 +257,104 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
                 s = add2(s, w);
                 d = fma2(w, e, d);
             }
-        };
-        if (all_plain && run.m < INFINITY) {
+            float p, q;
+            unpack(s, p, q);
+            run.s += p + q;
+            unpack(d, p, q);
+            run.d += p + q;
+        } else if (run.m > -INFINITY) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) plain_vector(x[u]);
-        } else {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (base + u * 32 + lane >= v1) continue;
-                if (plain[u] && run.m < INFINITY) {
-                    plain_vector(x[u]);
-                    continue;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {  // masked or infinite logits among them
-                    const uint32_t w = i & 1 ? x[u][i >> 1] >> 16 : x[u][i >> 1] & 0xFFFFu;
-                    const float l = __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
-                    if (!(l > -INFINITY)) continue;
-                    const float e = run.m == INFINITY ? (l == run.m ? 0.f : -200.f) : (l - run.m) * c, y = ex2(e);
-                    run.s += y;
-                    run.d = y > 0.f ? fmaf(y, e, run.d) : run.d;
-                }
+            for (int q = 0; q < 32; ++q) {
+                const uint32_t w = q & 1 ? x[q >> 1] >> 16 : x[q >> 1] & 0xFFFFu;
+                const float l = __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
+                const float e = run.m == INFINITY ? (l == run.m ? 0.f : -200.f) : (l - run.m) * c;
+                const float y = l > -INFINITY ? ex2(e) : 0.f;
+                run.s += y;
+                run.d = y > 0.f ? fmaf(y, e, run.d) : run.d;
             }
         }
-        float p, q;
-        unpack(s, p, q);
-        run.s += p + q;
-        unpack(d, p, q);
-        run.d += p + q;
     }
 
-    // ---- the CTA's sums and counts, then the cluster's, in a fixed order
+    // ---- the CTA's sums and counts
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const Sums b = {__shfl_xor_sync(0xffffffffu, run.m, o), __shfl_xor_sync(0xffffffffu, run.s, o), __shfl_xor_sync(0xffffffffu, run.d, o)};
-        run = joined(run, b, c);
-    }
+    for (int o = 16; o > 0; o >>= 1) run = joined(run, shuffled(run, o), c);
     if (lane == 0) sh.part[warp] = run;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
         const uint32_t n = __reduce_add_sync(0xffffffffu, above[j]);
         if (lane == 0) sh.above[warp][j] = n;
     }
-    if (threadIdx.x == 0) sh.count = 0;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        Sums all = sh.part[0];
-        for (int w = 1; w < kWarps; ++w) all = joined(all, sh.part[w], c);
-        sh.whole = all;
+    const int n = a.top, chunks = c1 - c0;
+    uint32_t mine = 0;
+    if (TOP) {
+        auto key_with = [](uint32_t bits, int i) {  // 0 for a chunk of masked logits
+            const uint32_t k = key_of(bits);
+            return k == 0 ? 0u : k << 16 | (0xFFFFu - static_cast<uint32_t>(i));
+        };
+        mine = best_chunk < 0 ? 0u : key_with(__half_as_ushort(__float2half_rn(best)), best_chunk);
+        sh.first[threadIdx.x] = mine;
+        for (int i = chunks + threadIdx.x; i < (chunks + 7) / 8 * 8; i += kThreads) chunk_max[i] = 0xFC00u;
+        if (threadIdx.x == 0) {
+            sh.count = sh.found = 0;
+            sh.least = 1;
+        }
+        if (threadIdx.x < kMaxTop) sh.best[threadIdx.x] = 0;
     }
-    if (threadIdx.x < NG) {
-        uint32_t n = 0;
-        for (int w = 0; w < kWarps; ++w) n += sh.above[w][threadIdx.x];
-        sh.above_whole[threadIdx.x] = n;
+    __syncthreads();
+    if (warp == 0) {
+        run = lane < kWarps ? sh.part[lane] : Sums{-INFINITY, 0.f, 0.f};
+#pragma unroll
+        for (int o = kWarps / 2; o > 0; o >>= 1) run = joined(run, shuffled(run, o), c);
+        if (lane == 0) sh.whole = run;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            const uint32_t all = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.above[lane][j] : 0u);
+            if (lane == 0) sh.above_whole[j] = all;
+        }
     }
 
     if (TOP) {
-        const int n = a.top, chunks = (v1 - v0 + 3) / 4;
-        auto chunk_key = [&](int i) {  // 0 for a chunk of masked logits
-            const uint32_t k = key_of(chunk_max[i]);
+        auto key_with = [](uint32_t bits, int i) {
+            const uint32_t k = key_of(bits);
             return k == 0 ? 0u : k << 16 | (0xFFFFu - static_cast<uint32_t>(i));
         };
-        // A lower bound of the n-th largest maximum: the n-th largest of 32 groups'. Few maxima are above it.
-        uint32_t g = 0;
-        for (int i = threadIdx.x; i < chunks; i += kThreads) g = max(g, chunk_key(i));
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
-        if ((threadIdx.x & 7) == 0) sh.group[threadIdx.x >> 3] = g;
-        __syncthreads();
-        g = sh.group[lane];
-        int before = 0;
-        for (int o = 1; o < 32; ++o) {
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, g, o);
-            before += other > g || (other == g && (lane ^ o) < lane);  // (only empty groups are equal)
+        // A lower bound of the n-th largest maximum: the n-th largest of the threads'. Few maxima are above it.
+        if (mine != 0) {
+            int before = 0;
+#pragma unroll 8
+            for (int i = 0; i < kThreads; i += 4) {
+                const uint4 q = *reinterpret_cast<const uint4*>(sh.first + i);
+                before += (q.x > mine) + (q.y > mine) + (q.z > mine) + (q.w > mine);
+            }
+            if (before == n - 1) sh.least = mine;
         }
-        uint32_t least = max(1u, __reduce_min_sync(0xffffffffu, before < n ? g : 0xFFFFFFFFu));
+        __syncthreads();
+        uint32_t least = sh.least;
+        int found;
         for (;;) {  // (once, but for rows made to have hundreds of maxima above the bound)
-            for (int i = threadIdx.x; i < chunks; i += kThreads) {
-                const uint32_t k = chunk_key(i);
-                if (k >= least) {
-                    const int at = atomicAdd(&sh.count, 1);
-                    if (at < kCandidates) sh.keys[at] = k;
+            const __half2 bound = __half2half2(__float2half_rn(value_of(max(least >> 16, 0x0400u))));  // (at the lowest: all finite ones)
+            for (int i = 8 * threadIdx.x; i < chunks; i += 8 * kThreads) {
+                const uint4 q = *reinterpret_cast<const uint4*>(chunk_max + i);
+                const uint32_t h[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (__hbeq2(__hge2(*reinterpret_cast<const __half2*>(&h[j]), bound), __float2half2_rn(0.f))) continue;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t k = key_with(e ? h[j] >> 16 : h[j] & 0xFFFFu, i + 2 * j + e);
+                        if (k < least) continue;
+                        const int at = atomicAdd(&sh.count, 1);
+                        if (at < kCandidates) sh.keys[at] = k;
+                    }
                 }
             }
             __syncthreads();
-            const int found = min(sh.count, kCandidates);
+            found = min(sh.count, kCandidates);
             const bool more = sh.count > kCandidates;
             for (int i = threadIdx.x; i < found; i += kThreads) {
                 const uint32_t k = sh.keys[i];
                 int place = 0;
+#pragma unroll 8
                 for (int j = 0; j < found; ++j) place += sh.keys[j] > k;
                 if (place < n) sh.chunk[place] = 0xFFFFu - (k & 0xFFFFu);
                 if (place == min(n, found) - 1) sh.last = more ? k : k >> 16;
@@ -342,28 +362,23 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
             __syncthreads();
             if (!more) break;
             least = sh.last;  // at least n of the maxima in the list: the others go
-            __syncthreads();
             if (threadIdx.x == 0) sh.count = 0;
             __syncthreads();
         }
-        const int named = min(n, sh.count);
+        const int named = min(n, found);
         const uint32_t enough = named == n ? sh.last : 1u;
-        __syncthreads();
-        if (threadIdx.x == 0) sh.count = 0;
-        if (threadIdx.x < kMaxTop) sh.best[threadIdx.x] = 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < named * kChunk; i += kThreads) {
-            const int el = (v0 + static_cast<int>(sh.chunk[i / kChunk]) * 4) * 8 - off + i % kChunk;
-            if (el < 0 || el >= a.V || el >= 8 * v1 - off) continue;
-            if (!in_bounds(m * a.stride + el < total, status)) continue;
-            const uint32_t k = key_of(row[el]);
-            if (k >= enough) sh.cand[atomicAdd(&sh.count, 1)] = static_cast<unsigned long long>(k) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(el));
+        for (int i = warp; i < named; i += kWarps) {
+            const int el = (c0 + static_cast<int>(sh.chunk[i])) * kChunk - off + lane;
+            const bool there = el >= 0 && el < a.V && in_bounds(el < 0 || el >= a.V || m * a.stride + el < total, status);
+            const uint32_t k = there ? key_of(row[el]) : 0u;
+            if (k >= enough) sh.cand[atomicAdd(&sh.found, 1)] = static_cast<unsigned long long>(k) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(el));
         }
         __syncthreads();
-        const int found = sh.count;
+        found = sh.found;
         for (int i = threadIdx.x; i < found; i += kThreads) {
             const unsigned long long k = sh.cand[i];
             int place = 0;
+#pragma unroll 8
             for (int j = 0; j < found; ++j) place += sh.cand[j] > k;
             if (place < n) sh.best[place] = k;
         }
@@ -372,11 +387,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
     if (C > 1) {
         cluster_sync_all();
         if (rank == 0) {
-            if (TOP) {  // the others' first tokens: C * top <= 16 * 32 candidates
-                const int n = a.top;
-                unsigned long long k = 0;
+            if (TOP) {  // every CTA's first tokens in order: a place is what all of them have above
                 for (int i = threadIdx.x; i < C * n; i += kThreads) {
                     const uint32_t at = map_peer(smem_u32(&sh.best[i % n]), static_cast<uint32_t>(i / n));
+                    unsigned long long k;
                     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(at) : "memory");
                     sh.cand[i] = k;
                 }
@@ -384,25 +398,32 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
                 if (threadIdx.x < kMaxTop) sh.best[threadIdx.x] = 0;
                 __syncthreads();
                 for (int i = threadIdx.x; i < C * n; i += kThreads) {
-                    k = sh.cand[i];
+                    const unsigned long long k = sh.cand[i];
                     int place = 0;
-                    for (int j = 0; j < C * n; ++j) place += sh.cand[j] > k;
+#pragma unroll 4
+                    for (int p = 0; p < C; ++p) place += above_in(sh.cand + p * n, n, k);
                     if (k != 0 && place < n) sh.best[place] = k;
                 }
             }
-            if (threadIdx.x == 0) {
-                Sums all = sh.whole;
-                for (int p = 1; p < C; ++p) {
-                    const uint32_t at = map_peer(smem_u32(&sh.whole), static_cast<uint32_t>(p));
-                    all = joined(all, {ld_dsmem_f1(at), ld_dsmem_f1(at + 4), ld_dsmem_f1(at + 8)}, c);
+            if (warp == 0) {
+                run = {-INFINITY, 0.f, 0.f};
+                if (lane < C) {
+                    const uint32_t at = map_peer(smem_u32(&sh.whole), static_cast<uint32_t>(lane));
+                    run = {ld_dsmem_f1(at), ld_dsmem_f1(at + 4), ld_dsmem_f1(at + 8)};
                 }
-                sh.whole = all;
-            }
-            if (threadIdx.x < NG) {
-                uint32_t n = sh.above_whole[threadIdx.x];
-                for (int p = 1; p < C; ++p)
-                    n += __float_as_uint(ld_dsmem_f1(map_peer(smem_u32(&sh.above_whole[threadIdx.x]), static_cast<uint32_t>(p))));
-                sh.above_whole[threadIdx.x] = n;
+                uint32_t counts[kG];
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+                    counts[j] = lane < C ? __float_as_uint(ld_dsmem_f1(map_peer(smem_u32(&sh.above_whole[j]), static_cast<uint32_t>(lane)))) : 0u;
+                __syncwarp();  // (every lane has read before rank 0's own are replaced)
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) run = joined(run, shuffled(run, o), c);
+                if (lane == 0) sh.whole = run;
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    const uint32_t all = __reduce_add_sync(0xffffffffu, counts[j]);
+                    if (lane == 0) sh.above_whole[j] = all;
+                }
             }
         }
         cluster_sync_all();
@@ -417,25 +438,22 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
         return (l == all.m ? 0.f : __fdiv_rn(l - all.m, temp)) - log_s;
     };
     if (threadIdx.x == 0 && a.entropy) a.entropy[m] = all.s > 0.f ? log_s - all.d * 0.693147180559945309f / all.s : 0.f;
-    if (threadIdx.x < NG && threadIdx.x < a.given) {
+    if (static_cast<int>(threadIdx.x) < NG && static_cast<int>(threadIdx.x) < a.given) {
         const int64_t at = static_cast<int64_t>(m) * a.given + threadIdx.x;
         const int t = a.tokens[at];
         float lp = 0.f;
         int place = 0;
         if (t >= 0 && t < a.V) {
-            const uint32_t bits = row[t], key = key_of(bits);
+            const uint32_t bits = sh.given[threadIdx.x] & 0xFFFFu;
             lp = logprob(__half2float(__ushort_as_half(static_cast<unsigned short>(bits))));
-            if (key != 0) {
-                place = 1 + static_cast<int>(sh.above_whole[threadIdx.x]);
-                for (int i = max(0, (t + off) / 8 * 8 - off); i < t; ++i) place += key_of(row[i]) == key;  // equal ones in its own vector
-            }
+            if (key_of(bits) != 0) place = 1 + static_cast<int>(sh.above_whole[threadIdx.x] + (sh.given[threadIdx.x] >> 16));
         } else if (t >= a.V) {
             record_error(status, kErrBounds);
         }
         if (a.logprob) a.logprob[at] = lp;
         if (a.rank) a.rank[at] = place;
     }
-    if (TOP && threadIdx.x < a.top) {
+    if (TOP && static_cast<int>(threadIdx.x) < a.top) {
         const int64_t at = static_cast<int64_t>(m) * a.top + threadIdx.x;
         const unsigned long long k = sh.best[threadIdx.x];
         a.top_tokens[at] = k == 0 ? -1 : static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k));
@@ -443,12 +461,12 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs a,
     }
 }
 
-template <int NG>
-cudaError_t launch_ng(const LogprobArgs& a, int M, int C, cudaStream_t s, unsigned* status) {
+template <int NG, int kThreads>
+cudaError_t launch_with(const LogprobArgs& a, int M, int C, cudaStream_t s, unsigned* status) {
     const bool top = a.top > 0;
-    auto kern = top ? logprobs_kernel<NG, true> : logprobs_kernel<NG, false>;
-    const int chunks = (((a.V + 14) / 8 + 3) / 4 + C - 1) / C;
-    const size_t smem = top ? (static_cast<size_t>(chunks) * 2 + 15) / 16 * 16 : 0;
+    auto kern = top ? logprobs_kernel<NG, true, kThreads> : logprobs_kernel<NG, false, kThreads>;
+    const int chunks = ((a.V + 31 + 31) / 32 + C - 1) / C;
+    const size_t smem = top ? (static_cast<size_t>(chunks) * 2 + 31) / 16 * 16 : 0;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     if (C > 8) {
@@ -478,18 +496,24 @@ cudaError_t launch_ng(const LogprobArgs& a, int M, int C, cudaStream_t s, unsign
     return cudaLaunchKernelEx(&cfg, kern, a, C, total, status);
 }
 
+template <int NG>
+cudaError_t launch_ng(const LogprobArgs& a, int M, int C, bool wide, cudaStream_t s, unsigned* status) {
+    return wide ? launch_with<NG, 256>(a, M, C, s, status) : launch_with<NG, 128>(a, M, C, s, status);
+}
+
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobParams& p, int sm_count, cudaStream_t s, unsigned* status) {
     const LogprobArgs a = {p.logits, p.stride, p.V, p.tokens, p.given, p.top, p.temperature, p.logprob, p.rank, p.entropy, p.top_tokens, p.top_logprob};
     // Few rows: CTAs until every SM has two, each with 4096 logits at least; many: as many as even out the waves.
     int C = 1;
-    while (C < 16 && static_cast<int64_t>(p.M) * C * 2 <= 2 * sm_count && p.V / (2 * C) >= 4096) C *= 2;
-    if (p.given <= 0) return launch_ng<0>(a, p.M, C, s, status);
-    if (p.given <= 1) return launch_ng<1>(a, p.M, C, s, status);
-    if (p.given <= 2) return launch_ng<2>(a, p.M, C, s, status);
-    if (p.given <= 4) return launch_ng<4>(a, p.M, C, s, status);
-    return launch_ng<8>(a, p.M, C, s, status);
+    while (C < 8 && static_cast<int64_t>(p.M) * C * 2 <= 2 * sm_count && p.V / (2 * C) >= 4096) C *= 2;
+    const bool wide = p.M < 4 * sm_count;
+    if (p.given <= 0) return launch_ng<0>(a, p.M, C, wide, s, status);
+    if (p.given <= 1) return launch_ng<1>(a, p.M, C, wide, s, status);
+    if (p.given <= 2) return launch_ng<2>(a, p.M, C, wide, s, status);
+    if (p.given <= 4) return launch_ng<4>(a, p.M, C, wide, s, status);
+    return launch_ng<8>(a, p.M, C, wide, s, status);
 }
 
 }  // namespace w4a16
