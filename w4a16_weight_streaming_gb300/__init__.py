@@ -764,34 +764,45 @@ def block_norm(h: torch.Tensor, y: torch.Tensor | None = None, weight=None, post
     (float16) or, with post_weight, its norm; x (float16) the norm of h'. Norms multiply by offset + weight (float16 [H];
     weight None: by 1). gate (float16): [H], [M, H] or [M, 1]. Without y: x is the norm of h, and h' is h. out: the pair to
     write, where h' may be h itself and x None; an h' of None is not written."""
-    half = torch.float16
-    if not (h.dtype in (half, torch.float32) and h.is_cuda and h.dim() == 2 and h.stride(1) == 1):
+    half, f32 = torch.float16, h.dtype is torch.float32
+    if not ((f32 or h.dtype is half) and h.is_cuda and h.dim() == 2 and h.stride(1) == 1):
         _refuse("block_norm", "h must be a CUDA float16 or float32 tensor [M, H], dense in a row")
-    M, H = h.shape
-    if y is not None and not (y.dtype is half and y.is_cuda and y.shape == h.shape and y.stride(1) == 1):
-        _refuse("block_norm", "y must be a CUDA float16 tensor of h's shape, dense in a row")
-    if y is None and (post_weight is not None or gate is not None):
+    shape = M, H = h.shape
+    h_stride = h.stride(0)
+    y_p = w_p = post_p = gate_p = None
+    y_stride = gate_stride = per_row = 0
+    if y is not None:
+        if not (y.dtype is half and y.is_cuda and y.shape == shape and y.stride(1) == 1):
+            _refuse("block_norm", "y must be a CUDA float16 tensor of h's shape, dense in a row")
+        y_p, y_stride = y.data_ptr(), y.stride(0)
+    elif post_weight is not None or gate is not None:
         _refuse("block_norm", "post_weight and gate need y")
     if not (_vec(weight, half, H) and _vec(post_weight, half, H)):
         _refuse("block_norm", "weight and post_weight must be contiguous CUDA float16 vectors of H elements")
-    gate_stride = per_row = 0
+    if weight is not None:
+        w_p = weight.data_ptr()
+    if post_weight is not None:
+        post_p = post_weight.data_ptr()
     if gate is not None:
         wide = gate.dim() == 2 and gate.shape[0] == M and gate.shape[1] in (1, H)
         if not (gate.dtype is half and gate.is_cuda and (wide or gate.shape == (H,)) and (gate.shape[-1] == 1 or gate.stride(-1) == 1)):
             _refuse("block_norm", "gate must be a CUDA float16 tensor [H], [M, H] or [M, 1], dense in a row")
+        gate_p = gate.data_ptr()
         gate_stride = gate.stride(0) if wide else 0
-        per_row = int(wide and gate.shape[1] == 1 and H != 1)
-    if out is None:
-        h_out = h if y is None else _new((M, H), h.dtype, h.device, stream)
-        x = _new((M, H), half, h.device, stream)
-    else:
+        per_row = int(wide and gate.shape[1] == 1)
+    if out is not None:
         h_out, x = out
-        if not (_dense(h_out, h.dtype, (M, H)) and _dense(x, half, (M, H))):
+        if not (_dense(h_out, h.dtype, shape) and _dense(x, half, shape)):
             _refuse("block_norm", "out must be contiguous CUDA tensors [M, H]: one of h's type, one float16")
-    write_h = h_out is not None and not (y is None and h_out is h)
-    rc = lib.w4a16_block_norm(h.data_ptr(), h.stride(0), int(h.dtype is torch.float32), _ptr(y), 0 if y is None else y.stride(0),
-                              _ptr(post_weight), _ptr(gate), gate_stride, per_row, scale, _ptr(weight), offset, eps,
-                              h_out.data_ptr() if write_h else None, _ptr(x), M, H, _stream_handle(stream))
+    elif stream is None:
+        h_out = h if y is None else torch.empty_like(h)
+        x = torch.empty_like(h, dtype=half) if f32 else torch.empty_like(h)
+    else:
+        h_out = h if y is None else _new(shape, h.dtype, h.device, stream)
+        x = _new(shape, half, h.device, stream)
+    rc = lib.w4a16_block_norm(h.data_ptr(), h_stride, f32, y_p, y_stride, post_p, gate_p, gate_stride, per_row, scale, w_p, offset, eps,
+                              None if h_out is None or h_out is h and y is None else h_out.data_ptr(),
+                              None if x is None else x.data_ptr(), M, H, _stream_handle(stream))
     if rc != OK:
         raise W4A16Error(rc, "w4a16_block_norm")
     return h_out, x

@@ -26,6 +26,8 @@
 // beginning keeps its sums and adds the following warps' parts at the end. All of a warp's steps are one stream of
 // copies, whatever items they belong to. The runs are contiguous, so that a CTA meets few experts and finds the
 // rows of their tokens in L1.
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -803,10 +805,6 @@ __global__ void __launch_bounds__(256) combine_kernel(const Space ws, uint16_t* 
 
 template <typename Kern, typename... Args>
 cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
-    if (smem > 0) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
@@ -827,7 +825,18 @@ cudaError_t launch_form(const MoeParams& p, const RouteArgs& r, int sm_count, cu
     constexpr int kThreads = warps_for(NT) * 32;
     constexpr size_t smem = warps_for(NT) * (kStages * Stage<F>::kBytes + 4 * NT * 4 * 32 * 4);
     const dim3 grid(static_cast<unsigned>(sm_count));
-    const cudaError_t e = launch(experts_kernel<NT, F, false>, grid, kThreads, smem, s, up, r, p.I, status);
+    static std::atomic<uint64_t> allowed{0};  // devices that know these kernels' shared memory
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || (allowed.load() >> dev & 1) == 0) {
+        e = cudaFuncSetAttribute(experts_kernel<NT, F, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(experts_kernel<NT, F, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) allowed.fetch_or(uint64_t{1} << dev);
+    }
+    e = launch(experts_kernel<NT, F, false>, grid, kThreads, smem, s, up, r, p.I, status);
     if (e != cudaSuccess) return e;
     return launch(experts_kernel<NT, F, true>, grid, kThreads, smem, s, down, r, p.I, status);
 }

@@ -1223,9 +1223,18 @@ struct Span {
 // INVALID_ARG where a written span overlaps another of them or a read one, or memory lies elsewhere; `same` is a
 // read span that written[0] may be.
 int check_spans(const Span* written, int nw, const Span* read, int nr, const void* same = nullptr) {
+    int dev = 0;
+    const bool known = cudaGetDevice(&dev) == cudaSuccess;
+    auto wrong = [&](const void* p) {  // as elsewhere()
+        cudaPointerAttributes a;
+        if (!known || cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        return a.type == cudaMemoryTypeHost || (a.type == cudaMemoryTypeDevice && a.device != dev);
+    };
     for (int i = 0; i < nw; ++i) {
         if (!written[i].p) continue;
-        if (elsewhere(written[i].p)) return W4A16_ERR_INVALID_ARG;
         for (int j = 0; j < i; ++j)
             if (written[j].p && overlaps(written[i].p, written[i].n, written[j].p, written[j].n)) return W4A16_ERR_INVALID_ARG;
         for (int j = 0; j < nr; ++j) {
@@ -1233,8 +1242,10 @@ int check_spans(const Span* written, int nw, const Span* read, int nr, const voi
             if (overlaps(written[i].p, written[i].n, read[j].p, read[j].n)) return W4A16_ERR_INVALID_ARG;
         }
     }
+    for (int i = 0; i < nw; ++i)
+        if (written[i].p && wrong(written[i].p)) return W4A16_ERR_INVALID_ARG;
     for (int j = 0; j < nr; ++j)
-        if (read[j].p && elsewhere(read[j].p)) return W4A16_ERR_INVALID_ARG;
+        if (read[j].p && wrong(read[j].p)) return W4A16_ERR_INVALID_ARG;
     return W4A16_OK;
 }
 
