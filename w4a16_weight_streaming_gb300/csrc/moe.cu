@@ -371,6 +371,7 @@ struct Matrices {
     const uint16_t* s;    // repacked scales
     const float* factor;  // NVFP4: fp32 scale of each expert's matrix
     int N, K, G;          // of one expert
+    int E;
 };
 
 // D (16 columns x 8 tokens) += A (16 columns x 16 k) . B (16 k x 8 tokens)
@@ -435,16 +436,17 @@ struct Source {
         }
     }
     // per: 32-k blocks a scale row, shift its logarithm or -1
-    __device__ __forceinline__ void copy(uint32_t stage, int blocks, int per, int shift, int lane) {
+    __device__ __forceinline__ void copy(const Matrices& m, uint32_t stage, int blocks, int per, int shift, int lane, unsigned* status) {
         const uint32_t vec = stage + vector_place(lane);
-        if (F == kInt4 || kb * 4 + (lane & 3) < blocks) {
+        const int64_t all = static_cast<int64_t>(m.E) * m.N, scales = all * (m.K / m.G);  // (index checks)
+        if ((F == kInt4 || kb * 4 + (lane & 3) < blocks) && in_bounds(w - m.w + 56 < all * blocks, status)) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) copy16(vec + 512u * i, w + 8 * i);
         }
         w += 4 * wt;
         const uint32_t to = stage + Stage<F>::kScales + 4u * lane;
         if (F == kInt4) {
-            copy4(to, s);
+            if (in_bounds(s - m.s + 2 <= scales, status)) copy4(to, s);
             if (--row_left == 0) {
                 row_left = per >> 2;
                 s += wt;
@@ -455,7 +457,8 @@ struct Source {
                 const int blk = F == kNvfp4 ? kb * 4 + (r >> 1) : kb * 4 + r;
                 if (blk >= blocks) continue;
                 const int row = F == kNvfp4 ? kb * 8 + r : shift >= 0 ? blk >> shift : blk / per;
-                copy4(to + 128u * r, s + static_cast<int64_t>(row) * wt + 2 * lane);
+                const uint16_t* q = s + static_cast<int64_t>(row) * wt + 2 * lane;
+                if (in_bounds(q - m.s + 2 <= scales, status)) copy4(to + 128u * r, q);
             }
         }
         ++kb;
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     int c_entry = entry, c_chunk = chunk, c_left = s1 - s0;
     auto fetch = [&](int slot) {
         if (c_left > 0) {
-            src.copy(ring + static_cast<uint32_t>(slot * Stage<F>::kBytes), blocks, per, shift, lane);
+            src.copy(m, ring + static_cast<uint32_t>(slot * Stage<F>::kBytes), blocks, per, shift, lane, status);
             if (--c_left > 0 && src.kb == steps) {
                 if (++c_chunk == chunks) {
                     c_chunk = 0;
@@ -639,7 +642,8 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int i = 8 * n + (lane >> 2), pair = base + (i < count ? i : 0);
-            const int row = DOWN ? pair : list.token[pair];
+            int row = DOWN ? pair : list.token[pair];
+            if (!in_bounds(row >= 0 && row < (DOWN ? r.T * r.k : r.T), status)) row = 0;
             rows[n] = static_cast<uint32_t>(row * width + kb * 128 + (lane & 3) * 8);
             sums[n] = static_cast<uint32_t>(DOWN ? row * (I / 32) + kb * 4 + (lane & 3) : row * (width / 128) + kb);
         }
@@ -820,8 +824,8 @@ cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t 
 
 template <int NT, Form F>
 cudaError_t launch_form(const MoeParams& p, const RouteArgs& r, int sm_count, cudaStream_t s, unsigned* status) {
-    const Matrices up = {static_cast<const uint4*>(p.gate_up_q), p.gate_up_s, p.gate_up_factor, 2 * p.I, p.H, p.G};
-    const Matrices down = {static_cast<const uint4*>(p.down_q), p.down_s, p.down_factor, p.H, p.I, p.G};
+    const Matrices up = {static_cast<const uint4*>(p.gate_up_q), p.gate_up_s, p.gate_up_factor, 2 * p.I, p.H, p.G, p.E};
+    const Matrices down = {static_cast<const uint4*>(p.down_q), p.down_s, p.down_factor, p.H, p.I, p.G, p.E};
     constexpr int kThreads = warps_for(NT) * 32;
     constexpr size_t smem = warps_for(NT) * (kStages * Stage<F>::kBytes + 4 * NT * 4 * 32 * 4);
     const dim3 grid(static_cast<unsigned>(sm_count));

@@ -634,7 +634,7 @@ int launch_gemm(const Choice& ch, const uint16_t* x, const void* qweight_r, cons
 
 extern "C" {
 
-int w4a16_version(void) { return 400; }
+int w4a16_version(void) { return 500; }
 
 int w4a16_debug_bounds(void) {
 #ifdef W4A16_DEBUG_BOUNDS
