@@ -467,25 +467,25 @@ struct Source {
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int w) { return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w; }
 
-// sum[c][n] += 16 columns c of a stage times 8 tokens n, TILES * 8 tokens; rows[n]: where this lane's token of those 8 has
-// the step's unit; sums[n] (kInt4): where it has 8 * 2^-24 times the sum of its 128 elements, or, with DOWN, one of four
-// parts of it a lane of the quad.
+// A lane's tokens, one of each 8: where its row has the step's unit; kInt4: where it has 8 * 2^-24 times the sum of its 128
+// elements, or, with DOWN, one of four parts of it a lane of the quad; and what was read there.
+template <int NT>
+struct Tokens {
+    uint32_t row[NT], sum[NT];  // (below 2^32: 1024 rows of 65,536 at most)
+    uint4 unit[NT][4];
+    float less[NT];
+};
+
+// sum[c][n] += 16 columns c of a stage times 8 tokens n, TILES * 8 tokens. The units of the next step, `on` elements on,
+// are asked for as soon as this step's are done with (`ahead`: there is one of the same tokens).
 //
 // kInt4: a pair of codes q, taken out of a word by a mask, is a pair of fp16 numbers q 2^-24 or 16 q 2^-24 (subnormal,
 // exact in a product), so 5 instructions make the operands of 8 weights. Sums of either kind are kept for the step,
 // sums of x come with it, and (q - 8) s then costs three instructions a sum: w is not rounded to fp16. (The other
 // forms' 13 and 12 instructions for 8 weights bound the products otherwise.) Sums are 2^24 too small.
 template <int NT, int TILES, Form F, bool DOWN>
-__device__ __forceinline__ void multiply(float (&sum)[4][NT][4], uint32_t stage, const uint16_t* base, const uint32_t (&rows)[NT],
-                                         const float* sums_base, const uint32_t (&sums)[NT], bool there, int lane) {
-    uint4 x[TILES][4];
-    float less[TILES];
-#pragma unroll
-    for (int n = 0; n < TILES; ++n) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) x[n][w] = *reinterpret_cast<const uint4*>(base + rows[n] + 32 * w);
-        if (F == kInt4) less[n] = sums_base[sums[n]];
-    }
+__device__ __forceinline__ void multiply(float (&sum)[4][NT][4], uint32_t stage, Tokens<NT>& x, const uint16_t* rows, const float* sums,
+                                         int on, bool ahead, bool there, int lane) {
     const uint32_t vec = stage + vector_place(lane), sc = stage + Stage<F>::kScales + 2u * (lane >> 2);
     float off[TILES][2];
 #pragma unroll
@@ -523,16 +523,17 @@ __device__ __forceinline__ void multiply(float (&sum)[4][NT][4], uint32_t stage,
 #pragma unroll
             for (int n = 0; n < TILES; ++n) {
                 if (F == kInt4 && w == 0) {
-                    mma16816_first(one[n], d[0][0], d[1][0], d[0][2], d[1][2], x[n][w].x, x[n][w].y);
-                    mma16816_first(sixteen[n], d[0][1], d[1][1], d[0][3], d[1][3], x[n][w].z, x[n][w].w);
+                    mma16816_first(one[n], d[0][0], d[1][0], d[0][2], d[1][2], x.unit[n][w].x, x.unit[n][w].y);
+                    mma16816_first(sixteen[n], d[0][1], d[1][1], d[0][3], d[1][3], x.unit[n][w].z, x.unit[n][w].w);
                 } else if (F == kInt4) {
-                    mma16816(one[n], d[0][0], d[1][0], d[0][2], d[1][2], x[n][w].x, x[n][w].y);
-                    mma16816(sixteen[n], d[0][1], d[1][1], d[0][3], d[1][3], x[n][w].z, x[n][w].w);
+                    mma16816(one[n], d[0][0], d[1][0], d[0][2], d[1][2], x.unit[n][w].x, x.unit[n][w].y);
+                    mma16816(sixteen[n], d[0][1], d[1][1], d[0][3], d[1][3], x.unit[n][w].z, x.unit[n][w].w);
                 } else {
-                    if (c == 0 && !there) x[n][w] = make_uint4(0u, 0u, 0u, 0u);
-                    mma16816(sum[c][n], d[0][0], d[1][0], d[0][2], d[1][2], x[n][w].x, x[n][w].y);
-                    mma16816(sum[c][n], d[0][1], d[1][1], d[0][3], d[1][3], x[n][w].z, x[n][w].w);
+                    if (c == 0 && !there) x.unit[n][w] = make_uint4(0u, 0u, 0u, 0u);
+                    mma16816(sum[c][n], d[0][0], d[1][0], d[0][2], d[1][2], x.unit[n][w].x, x.unit[n][w].y);
+                    mma16816(sum[c][n], d[0][1], d[1][1], d[0][3], d[1][3], x.unit[n][w].z, x.unit[n][w].w);
                 }
+                if (c == 3 && ahead) x.unit[n][w] = *reinterpret_cast<const uint4*>(rows + x.row[n] + on + 32 * w);
             }
         }
         if (F == kInt4) {
@@ -541,7 +542,8 @@ __device__ __forceinline__ void multiply(float (&sum)[4][NT][4], uint32_t stage,
 #pragma unroll
             for (int n = 0; n < TILES; ++n) {
                 if (c == 0) {  // from the lanes of tokens 2 t, 2 t + 1
-                    float total = less[n];
+                    float total = x.less[n];
+                    if (ahead) x.less[n] = sums[x.sum[n] + on / 128 * (DOWN ? 4 : 1)];
                     if (DOWN) {
                         total += __shfl_xor_sync(0xffffffffu, total, 1);
                         total += __shfl_xor_sync(0xffffffffu, total, 2);
@@ -630,7 +632,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
 
     const uint16_t* const rows_of = DOWN ? r.w.act : r.w.xp;
     const float* const sums_of = DOWN ? r.w.asum : r.w.xsum;
-    uint32_t rows[NT], sums[NT];  // of this lane's tokens, at step kb (below 2^32: 1024 rows of 65,536 at most)
+    Tokens<NT> x;  // at step kb
     float acc[4][NT][4];
     constexpr int kSums = DOWN ? 4 : 1;  // a step
     int base = 0, count = 0, tiles = 1;
@@ -644,8 +646,12 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
             const int i = 8 * n + (lane >> 2), pair = base + (i < count ? i : 0);
             int row = DOWN ? pair : list.token[pair];
             if (!in_bounds(row >= 0 && row < (DOWN ? r.T * r.k : r.T), status)) row = 0;
-            rows[n] = static_cast<uint32_t>(row * width + kb * 128 + (lane & 3) * 8);
-            sums[n] = static_cast<uint32_t>(DOWN ? row * (I / 32) + kb * 4 + (lane & 3) : row * (width / 128) + kb);
+            x.row[n] = static_cast<uint32_t>(row * width + kb * 128 + (lane & 3) * 8);
+            x.sum[n] = static_cast<uint32_t>(DOWN ? row * (I / 32) + kb * 4 + (lane & 3) : row * (width / 128) + kb);
+            if (n > 0 && n >= tiles) continue;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) x.unit[n][w] = *reinterpret_cast<const uint4*>(rows_of + x.row[n] + 32 * w);
+            if (F == kInt4) x.less[n] = sums_of[x.sum[n]];
         }
     };
     auto clear = [&]() {
@@ -711,17 +717,19 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
         fetch(slot == 0 ? kStages - 1 : slot - 1);
         const uint32_t stage = ring + static_cast<uint32_t>(slot * Stage<F>::kBytes);
         const bool there = F == kInt4 || kb * 4 + (lane & 3) < blocks;
+        const bool last = kb + 1 == steps, ahead = s + 1 < s1 && !(last && chunk + 1 == chunks);
+        const int on = last ? 128 - width : 128;  // the next item's first step, of the same tokens
         if (NT == 1 || tiles == 1)
-            multiply<NT, 1, F, DOWN>(acc, stage, rows_of, rows, sums_of, sums, there, lane);
+            multiply<NT, 1, F, DOWN>(acc, stage, x, rows_of, sums_of, on, ahead, there, lane);
         else if (NT == 2 || tiles == 2)
-            multiply<NT, NT < 2 ? 1 : 2, F, DOWN>(acc, stage, rows_of, rows, sums_of, sums, there, lane);
+            multiply<NT, NT < 2 ? 1 : 2, F, DOWN>(acc, stage, x, rows_of, sums_of, on, ahead, there, lane);
         else
-            multiply<NT, NT, F, DOWN>(acc, stage, rows_of, rows, sums_of, sums, there, lane);
+            multiply<NT, NT, F, DOWN>(acc, stage, x, rows_of, sums_of, on, ahead, there, lane);
         if (++slot == kStages) slot = 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            rows[n] += 128;
-            sums[n] += kSums;
+            x.row[n] += static_cast<uint32_t>(on);
+            x.sum[n] += static_cast<uint32_t>(on / 128 * kSums);
         }
         if (++kb == steps) {
             if (whole)
@@ -735,12 +743,6 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
                 chunk = 0;
                 ++entry;
                 if (s + 1 < s1) meet();
-            } else {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    rows[n] -= width;
-                    sums[n] -= kSums * steps;
-                }
             }
         }
     }
