@@ -467,8 +467,7 @@ int w4a16_block_norm(const void* h, int64_t h_stride, int h_f32, const uint16_t*
  *   a = fp16_rne(silu(x . Wg) * (x . Wu)), the products in fp32;  y[t] = fp16_rne(sum_e r * (a . Wd)), in order of e
  * The experts' matrices are those of w4a16_repack (or w4a16_repack_nvfp4) one after another: gate_up [hidden, 2 inner]
  * with its columns in turns, 16 of gate and then the same 16 of up; down [inner, hidden]. A call reads each chosen expert's weights once, whatever the tokens (an
- * expert with many more tokens than the average again). Products are within the bound of w4a16_gemm; where group is a
- * multiple of 128 a weight is (q - 8) s itself, not rounded to fp16.
+ * expert with many more tokens than the average again). Products are within the bound of w4a16_gemm.
  */
 typedef struct {
     const void* gate_up_q;      /* experts * w4a16_repacked_qweight_bytes(2 inner, hidden, group) */

@@ -4,9 +4,7 @@ Choice: logits are sums of exact fp16 products in fp32; a chain is H / 512 + 9 r
 off by less than 2^-19 of sum|x router| for H <= 5120. A choice has to be one that logits within that bound allow;
 the rest is compared for the choice made.
 Products: an instruction adds 16 products to an fp32 sum, off by 2^-21 of sum|x w| at most; with up to 2^5 in a chain and
-the warps' sums, below 2^-16 of sum|x w|. Where the group is a multiple of 128 weights are not rounded to fp16, which
-the reference does: 2^-11 of each, so 2^-11 of sum|x w| (sums of codes 0..15 less 8 sum x lose no more than that of a code
-by itself: 15 against an average |q - 8| of 4). a = silu(g) u is off by 1.1 |u| dg + |silu(g)| du, 2^-20 of itself for the
+the warps' sums, below 2^-16 of sum|x w|. a = silu(g) u is off by 1.1 |u| dg + |silu(g)| du, 2^-20 of itself for the
 fp32 exponential and division, and its rounding, 2^-11 (2^-25 among subnormals). y by sum r (da |Wd|), as much of
 sum r |a Wd|, the weights' own error (twice that of a logit, and 2^-20), and 2^-11 of itself."""
 from __future__ import annotations
@@ -49,7 +47,6 @@ class Layer:
     def __init__(self, W, E, H, I, group=64, seed=0, nvfp4=False):
         g = torch.Generator("cuda").manual_seed(seed)
         self.E, self.H, self.I = E, H, I
-        self.products = 2.0 ** -16 + (2.0 ** -11 if group % 128 == 0 and not nvfp4 else 0.0)
 
         def codes(rows, cols):
             return torch.randint(-2 ** 31, 2 ** 31, (E, rows // 8, cols), generator=g, device="cuda", dtype=torch.int32)
@@ -103,14 +100,14 @@ def check(W, L, x, k, sigmoid=False, renormalize=True, scale=1.0, bias=None, res
         t, j = (chosen == e).nonzero(as_tuple=True)
         if len(t) == 0:
             continue
-        both, mass = xd[t] @ L.up[e], xd[t].abs() @ L.up[e].abs() * L.products
+        both, mass = xd[t] @ L.up[e], xd[t].abs() @ L.up[e].abs() * 2.0 ** -16
         g, u, dg, du = both[:, :L.I], both[:, L.I:], mass[:, :L.I], mass[:, L.I:]
         a = g * torch.sigmoid(g) * u
         da = 1.1 * u.abs() * dg + (g * torch.sigmoid(g)).abs() * du + 1.1 * dg * du + (2.0 ** -11 + 2.0 ** -20) * a.abs() + 2.0 ** -25
         weight = scale * s[t, j][:, None]
         ref.index_add_(0, t, weight * (a @ L.down[e]))
         sums = a.abs() @ L.down[e].abs()
-        bound.index_add_(0, t, weight * (da @ L.down[e].abs() + (L.products + rel[t]) * sums))
+        bound.index_add_(0, t, weight * (da @ L.down[e].abs() + (2.0 ** -16 + rel[t]) * sums))
     bound += 2.0 ** -11 * ref.abs() + 2.0 ** -25
     assert bool(((y.double() - ref).abs() <= bound * 1.01).all()), float(((y.double() - ref).abs() / bound).max())
     # the bound is a worst case; errors are independent, so a lost expert or token would still be far outside this
@@ -131,6 +128,48 @@ def test_sizes(W, E, H, I, G, T):
     check(W, L, x, min(6, E), sigmoid=True, bias=L.bias, scale=2.5)
     check(W, L, x, 1, renormalize=False)
     check(W, L, x, E if E <= 16 else 16, sigmoid=True, renormalize=False)
+
+
+# scales within 2^-10 .. 2^-4, where codes become weights in one step, on the borders, and outside of them
+SCALES = {"usual": lambda u: 0.002 + 0.01 * u, "wide": lambda u: 2.0 ** (-16 + 18 * u), "borders": lambda u: 2.0 ** (-10 - (u > 0.5) * 2.0 ** -10),
+          "top": lambda u: 0.0625 * (1 - 2.0 ** -11 * (u > 0.3).float()), "odd": lambda u: torch.where(u < 0.1, -0.01, torch.where(u < 0.2, 0.0, torch.where(u < 0.3, 3e-7, 0.01)))}
+
+
+@pytest.mark.parametrize("T", [1, 12, 60])  # 8, 16 and 32 tokens at a time
+@pytest.mark.parametrize("G", [32, 64, 128, 192, 384])
+@pytest.mark.parametrize("kind", SCALES)
+def test_weights_are_the_formats_own(W, kind, G, T):
+    """Rows with a single 1, and a down matrix of one power of two a column: y is a itself, of weights rounded once, times
+    2^-7. silu and the product in fp32 are off by 2^-20, so a by half a step and that."""
+    H = I = 384
+    if T == 60 and G == 64:
+        H = I = 320  # K not a multiple of 128
+    if H % G:
+        pytest.skip("the group does not divide K")
+    g = torch.Generator("cuda").manual_seed(G)
+    up = torch.randint(-2 ** 31, 2 ** 31, (1, H // 8, 2 * I), generator=g, device="cuda", dtype=torch.int32)
+    scales = SCALES[kind](torch.rand((1, H // G, 2 * I), generator=g, device="cuda")).half()
+    code = torch.full((I, H), 8, dtype=torch.int32, device="cuda")
+    code.fill_diagonal_(9)
+    down = torch.zeros((I // 8, H), dtype=torch.int32, device="cuda")
+    for j in range(8):
+        down |= code[j::8] << (4 * j)
+    m = W.Experts(up, scales, down[None].contiguous(), torch.full((1, I // G, H), 2.0 ** -7, device="cuda").half(), G)
+    at = torch.randint(0, H, (T,), generator=g, device="cuda")
+    big = 64.0 if kind != "wide" else 1.0  # so that a is no subnormal number
+    x = (torch.nn.functional.one_hot(at, H) * big).half()
+    y, _, _ = W.moe(x, m, torch.zeros((1, H), device="cuda").half(), 1, W.moe_workspace(m))
+    torch.cuda.synchronize()
+    assert W.w4a16_device_status() == W.OK
+    both = big * dequantised(up, scales, G)[0][at]
+    gate, upper = both[:, :I], both[:, I:]
+    a = gate * torch.sigmoid(gate) * upper
+    a16 = a.half().double()
+    got = y.double() * 128.0
+    near = 2.0 ** -20 * a.abs() + 2.0 ** -11 * a.abs() * 1.01 + 2.0 ** -24 * 65
+    assert bool(((got - a).abs() <= near).all()), float(((got - a).abs() / near).max())
+    if kind == "usual":  # half a step off at most, and nearly always the nearest
+        assert float((got != a16).double().mean()) < 0.01
 
 
 @pytest.mark.parametrize("T", [1, 6, 20, 64])

@@ -27,6 +27,7 @@
 // copies, whatever items they belong to. The runs are contiguous, so that a CTA meets few experts and finds the
 // rows of their tokens in L1.
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -41,11 +42,11 @@ constexpr int kStages = 2;    // of a warp's ring
 // their sums.
 __host__ __device__ constexpr int warps_for(int nt) { return nt <= 2 ? 12 : 8; }
 
-// How weights become operands.
+// The weights' formats: how many rows of scales 128 k have.
 enum Form {
-    kInt4,       // groups of a multiple of 128 k: the codes themselves, a step's sums times the scale
-    kInt4Small,  // other groups: (code - 8) * scale rounded to fp16
-    kNvfp4       // code * block scale, exact in fp16
+    kInt4,       // one: groups of a multiple of 128 k
+    kInt4Small,  // up to 4: other groups
+    kNvfp4       // 8
 };
 
 constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTop;
@@ -72,13 +73,9 @@ struct Space {
     int* place;         // [tokens][k]: of a pair in the list
     uint16_t* xp;       // [tokens][Hp], transposed units
     uint16_t* act;      // [pairs][Ip], transposed units
-    float* xsum;        // [tokens][Hp / 128]: 8 * 2^-24 times the sums of 128 elements of x
-    float* asum;        // [pairs][I / 32]: of 32 elements of a
     float* part;        // [pairs][H]
     size_t bytes;
 };
-
-constexpr float kEight = 8.f / 16777216.f;  // 8 * 2^-24
 
 __host__ __device__ inline int64_t padded(int k) { return (static_cast<int64_t>(k) + 127) / 128 * 128; }
 
@@ -99,8 +96,6 @@ inline Space space_of(void* base, int E, int H, int I) {
     s.place = reinterpret_cast<int*>(take(kMaxPairs * 4));
     s.xp = reinterpret_cast<uint16_t*>(take(kMoeMaxTokens * padded(H) * 2));
     s.act = reinterpret_cast<uint16_t*>(take(kMaxPairs * padded(I) * 2));
-    s.xsum = reinterpret_cast<float*>(take(kMoeMaxTokens * padded(H) / 128 * 4));
-    s.asum = reinterpret_cast<float*>(take(static_cast<size_t>(kMaxPairs) * (I / 32) * 4));
     s.part = reinterpret_cast<float*>(take(static_cast<size_t>(kMaxPairs) * H * 4));
     s.bytes = at;
     return s;
@@ -316,26 +311,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
         }
         w = wn;
     }
-    for (int i = e; i < tokens; i += a.E) {  // a token's row as the products want it, and the sums of 128 elements: a half-warp each
-        for (int v0 = 0; v0 < vecs; v0 += kRouteThreads) {
-            const int v = v0 + static_cast<int>(threadIdx.x);
-            const int64_t row = padded(a.H) * (t0 + i);
-            float s = 0.f;
-            if (v < vecs) {
-                const uint4 q = *reinterpret_cast<const uint4*>(a.x + (t0 + i) * a.x_stride + 8 * static_cast<int64_t>(v));
-                *reinterpret_cast<uint4*>(a.w.xp + row + unit_place(8 * v)) = make_uint4(q.x, q.z, q.y, q.w);
-                const uint32_t h[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-                    s += f.x + f.y;
-                }
-            }
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if ((threadIdx.x & 15) == 0 && v < vecs) a.w.xsum[(row >> 7) + (v >> 4)] = kEight * s;
+    for (int i = e; i < tokens; i += a.E)  // a token's row as the products want it
+        for (int v = threadIdx.x; v < vecs; v += kRouteThreads) {
+            const uint4 q = *reinterpret_cast<const uint4*>(a.x + (t0 + i) * a.x_stride + 8 * static_cast<int64_t>(v));
+            *reinterpret_cast<uint4*>(a.w.xp + padded(a.H) * (t0 + i) + unit_place(8 * v)) = make_uint4(q.x, q.z, q.y, q.w);
         }
-    }
 #pragma unroll
     for (int i = 0; i < TB; ++i) {
         float s = acc[i][0] + acc[i][1];
@@ -379,12 +359,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
@@ -465,44 +439,43 @@ struct Source {
     }
 };
 
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int w) { return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w; }
 
-// A lane's tokens, one of each 8: where its row has the step's unit; kInt4: where it has 8 * 2^-24 times the sum of its 128
-// elements, or, with DOWN, one of four parts of it a lane of the quad; and what was read there.
+// A lane's tokens, one of each 8: where its row has the step's units, and what was read there.
 template <int NT>
 struct Tokens {
-    uint32_t row[NT], sum[NT];  // (below 2^32: 1024 rows of 65,536 at most)
+    uint32_t row[NT];  // (below 2^32: 1024 rows of 65,536 at most)
     uint4 unit[NT][4];
-    float less[NT];
 };
 
 // sum[c][n] += 16 columns c of a stage times 8 tokens n, TILES * 8 tokens. The units of the next step, `on` elements on,
 // are asked for as soon as this step's are done with (`ahead`: there is one of the same tokens).
 //
-// kInt4: a pair of codes q, taken out of a word by a mask, is a pair of fp16 numbers q 2^-24 or 16 q 2^-24 (subnormal,
-// exact in a product), so 5 instructions make the operands of 8 weights. Sums of either kind are kept for the step,
-// sums of x come with it, and (q - 8) s then costs three instructions a sum: w is not rounded to fp16. (The other
-// forms' 13 and 12 instructions for 8 weights bound the products otherwise.) Sums are 2^24 too small.
-template <int NT, int TILES, Form F, bool DOWN>
-__device__ __forceinline__ void multiply(float (&sum)[4][NT][4], uint32_t stage, Tokens<NT>& x, const uint16_t* rows, const float* sums,
-                                         int on, bool ahead, bool there, int lane) {
+// FAST (int4): the pairs of codes that a mask takes out of a word are, as fp16 numbers, q 2^-24 (bits 0..3) or q 2^-20
+// (bits 4..7): subnormal and exact. One fused multiply-add with s 2^20 and -s / 2 or -8 s gives (q - 8) s / 16 or
+// (q - 8) s with its one rounding, which is the format's: 9 instructions for 8 weights instead of dequant8's 13. It needs
+// every number normal, a scale in 2^-10 .. 2^-4; other steps go the long way. Sixteenths are summed apart.
+template <int NT, int TILES, Form F, bool FAST>
+__device__ __forceinline__ void multiply(float (&sum)[4][NT][4], float (&sixteenth)[4][NT][4], uint32_t stage, Tokens<NT>& x,
+                                         const uint16_t* rows, int on, bool ahead, bool there, int lane) {
     const uint32_t vec = stage + vector_place(lane), sc = stage + Stage<F>::kScales + 2u * (lane >> 2);
-    float off[TILES][2];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const uint4 v[2] = {lds128(vec + 1024u * c), lds128(vec + 1024u * c + 512u)};
-        uint32_t s[2][2];  // of columns g, g + 8; NVFP4: of a block's halves
+        uint32_t s[2][2];  // of columns g, g + 8, twice in a register; NVFP4: of a block's halves
         const uint32_t row = F == kInt4 ? 0u : F == kInt4Small ? lane & 3u : 2u * (lane & 3u);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            s[i][0] = lds16(sc + 128u * row + 32u * c + 16u * i);
-            if (F == kNvfp4) s[i][1] = lds16(sc + 128u * (row + 1) + 32u * c + 16u * i);
-            if (F != kInt4) {  // past K: what the stage holds is not of this step
-                s[i][0] = there ? s[i][0] * 0x10001u : 0u;
-                if (F == kNvfp4) s[i][1] = there ? s[i][1] * 0x10001u : 0u;
-            }
+            s[i][0] = lds16(sc + 128u * row + 32u * c + 16u * i) * 0x10001u;
+            if (F == kNvfp4) s[i][1] = lds16(sc + 128u * (row + 1) + 32u * c + 16u * i) * 0x10001u;
+            if (F != kInt4 && !there) s[i][0] = s[i][1] = 0x1C001C00u;  // past K: what the stage holds is not of this step
         }
-        float one[TILES][4], sixteen[TILES][4];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             uint32_t d[2][4];
@@ -511,52 +484,39 @@ __device__ __forceinline__ void multiply(float (&sum)[4][NT][4], uint32_t stage,
                 const uint32_t word = word_of(v[i], w);
                 if (F == kNvfp4) {
                     dequant8_nvfp4(word, s[i][w >> 1], d[i]);
-                } else if (F == kInt4Small) {
+                } else if (!FAST) {
                     dequant8(word, s[i][0], d[i]);
                 } else {
-                    d[i][0] = word & 0x000F000Fu;
-                    d[i][1] = word & 0x00F000F0u;
-                    d[i][2] = (word >> 8) & 0x000F000Fu;
-                    d[i][3] = (word >> 8) & 0x00F000F0u;
+                    const uint32_t up = s[i][0] + 0x50005000u, less_half = s[i][0] + 0x7C007C00u, less_8 = s[i][0] + 0x8C008C00u;
+                    d[i][0] = hfma2(word & 0x000F000Fu, up, less_half);
+                    d[i][1] = hfma2(word & 0x00F000F0u, up, less_8);
+                    d[i][2] = hfma2((word >> 8) & 0x000F000Fu, up, less_half);
+                    d[i][3] = hfma2((word >> 8) & 0x00F000F0u, up, less_8);
                 }
             }
 #pragma unroll
             for (int n = 0; n < TILES; ++n) {
-                if (F == kInt4 && w == 0) {
-                    mma16816_first(one[n], d[0][0], d[1][0], d[0][2], d[1][2], x.unit[n][w].x, x.unit[n][w].y);
-                    mma16816_first(sixteen[n], d[0][1], d[1][1], d[0][3], d[1][3], x.unit[n][w].z, x.unit[n][w].w);
-                } else if (F == kInt4) {
-                    mma16816(one[n], d[0][0], d[1][0], d[0][2], d[1][2], x.unit[n][w].x, x.unit[n][w].y);
-                    mma16816(sixteen[n], d[0][1], d[1][1], d[0][3], d[1][3], x.unit[n][w].z, x.unit[n][w].w);
-                } else {
-                    if (c == 0 && !there) x.unit[n][w] = make_uint4(0u, 0u, 0u, 0u);
-                    mma16816(sum[c][n], d[0][0], d[1][0], d[0][2], d[1][2], x.unit[n][w].x, x.unit[n][w].y);
-                    mma16816(sum[c][n], d[0][1], d[1][1], d[0][3], d[1][3], x.unit[n][w].z, x.unit[n][w].w);
-                }
+                if (F != kInt4 && c == 0 && !there) x.unit[n][w] = make_uint4(0u, 0u, 0u, 0u);
+                const uint4& u = x.unit[n][w];
+                mma16816(FAST ? sixteenth[c][n] : sum[c][n], d[0][0], d[1][0], d[0][2], d[1][2], u.x, u.y);
+                mma16816(sum[c][n], d[0][1], d[1][1], d[0][3], d[1][3], u.z, u.w);
                 if (c == 3 && ahead) x.unit[n][w] = *reinterpret_cast<const uint4*>(rows + x.row[n] + on + 32 * w);
             }
         }
-        if (F == kInt4) {
-            const float f[2] = {__half2float(__ushort_as_half(static_cast<unsigned short>(s[0][0]))),
-                                __half2float(__ushort_as_half(static_cast<unsigned short>(s[1][0])))};
-#pragma unroll
-            for (int n = 0; n < TILES; ++n) {
-                if (c == 0) {  // from the lanes of tokens 2 t, 2 t + 1
-                    float total = x.less[n];
-                    if (ahead) x.less[n] = sums[x.sum[n] + on / 128 * (DOWN ? 4 : 1)];
-                    if (DOWN) {
-                        total += __shfl_xor_sync(0xffffffffu, total, 1);
-                        total += __shfl_xor_sync(0xffffffffu, total, 2);
-                    }
-                    off[n][0] = __shfl_sync(0xffffffffu, total, (lane & 3) * 8);
-                    off[n][1] = __shfl_sync(0xffffffffu, total, (lane & 3) * 8 + 4);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sum[c][n][i] = fmaf(f[i >> 1], fmaf(0.0625f, sixteen[n][i], one[n][i]) - off[n][i & 1], sum[c][n][i]);
-            }
-        }
     }
+}
+
+// Whether all scales of a step are normal enough for the fast way: 2^-10 <= s < 2^-4. (A row past K is not looked at.)
+template <Form F>
+__device__ __forceinline__ bool scales_fit(uint32_t stage, int kb, int blocks, int lane) {
+    bool fit = true;
+#pragma unroll
+    for (int r = 0; r < Stage<F>::kRows; ++r) {
+        if (F != kInt4 && kb * 4 + r >= blocks) continue;
+        const uint32_t p = lds32(stage + Stage<F>::kScales + 128u * r + 4u * lane);
+        fit = fit && (p & 0xFFFFu) - 0x1400u < 0x1800u && (p >> 16) - 0x1400u < 0x1800u;
+    }
+    return __all_sync(0xffffffffu, fit);
 }
 
 // DOWN false: gate and up (16 columns of gate, the 16 of up, twice an item), true: down.
@@ -631,10 +591,9 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     if (DOWN) griddep_wait();
 
     const uint16_t* const rows_of = DOWN ? r.w.act : r.w.xp;
-    const float* const sums_of = DOWN ? r.w.asum : r.w.xsum;
     Tokens<NT> x;  // at step kb
-    float acc[4][NT][4];
-    constexpr int kSums = DOWN ? 4 : 1;  // a step
+    float acc[4][NT][4], sixteenth[4][NT][4];
+    constexpr bool kFast = F != kNvfp4 && NT <= 2;  // (32 tokens at a time leave no registers for a second set of sums)
     int base = 0, count = 0, tiles = 1;
     const int width = static_cast<int>(padded(m.K));
     auto meet = [&]() {  // the rows of an entry's tokens at step kb; a place without a token reads the first one's
@@ -647,11 +606,9 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
             int row = DOWN ? pair : list.token[pair];
             if (!in_bounds(row >= 0 && row < (DOWN ? r.T * r.k : r.T), status)) row = 0;
             x.row[n] = static_cast<uint32_t>(row * width + kb * 128 + (lane & 3) * 8);
-            x.sum[n] = static_cast<uint32_t>(DOWN ? row * (I / 32) + kb * 4 + (lane & 3) : row * (width / 128) + kb);
             if (n > 0 && n >= tiles) continue;
 #pragma unroll
             for (int w = 0; w < 4; ++w) x.unit[n][w] = *reinterpret_cast<const uint4*>(rows_of + x.row[n] + 32 * w);
-            if (F == kInt4) x.less[n] = sums_of[x.sum[n]];
         }
     };
     auto clear = [&]() {
@@ -660,10 +617,20 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[c][n][i] = 0.f;
+                for (int i = 0; i < 4; ++i) acc[c][n][i] = sixteenth[c][n][i] = 0.f;
+    };
+    auto fold = [&]() {
+        if constexpr (kFast) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[c][n][i] = fmaf(16.f, sixteenth[c][n][i], acc[c][n][i]);
+        }
     };
     auto finish = [&]() {  // a lane's columns g, g + 8 of each 16 for tokens 2 t, 2 t + 1 of 8
-        const float factor = F == kNvfp4 ? m.factor[list.expert[entry]] : F == kInt4 ? 16777216.f : 1.f;
+        const float factor = F == kNvfp4 ? m.factor[list.expert[entry]] : 1.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -681,18 +648,12 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
                         to[16 * c + 8] = w * acc[c][n][2 + h];
                     }
                 } else {
-                    float all = 0.f;
+                    if (!there) continue;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float g = acc[q & 2][n][2 * (q & 1) + h] * factor, u = acc[(q & 2) + 1][n][2 * (q & 1) + h] * factor;
-                        const __half a = __float2half_rn(g / (1.0f + expf(-g)) * u);
-                        all += __half2float(a);
-                        if (there) r.w.act[pair * padded(I) + unit_place(32 * chunk + 8 * q + (lane >> 2))] = __half_as_ushort(a);
-                    }
-                    if (F == kInt4) {
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-                        if (there && lane < 4) r.w.asum[static_cast<int64_t>(pair) * (I / 32) + chunk] = kEight * all;
+                        r.w.act[pair * padded(I) + unit_place(32 * chunk + 8 * q + (lane >> 2))] =
+                            __half_as_ushort(__float2half_rn(g / (1.0f + expf(-g)) * u));
                     }
                 }
             }
@@ -719,19 +680,24 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
         const bool there = F == kInt4 || kb * 4 + (lane & 3) < blocks;
         const bool last = kb + 1 == steps, ahead = s + 1 < s1 && !(last && chunk + 1 == chunks);
         const int on = last ? 128 - width : 128;  // the next item's first step, of the same tokens
-        if (NT == 1 || tiles == 1)
-            multiply<NT, 1, F, DOWN>(acc, stage, x, rows_of, sums_of, on, ahead, there, lane);
-        else if (NT == 2 || tiles == 2)
-            multiply<NT, NT < 2 ? 1 : 2, F, DOWN>(acc, stage, x, rows_of, sums_of, on, ahead, there, lane);
+        auto go = [&](auto fast) {
+            constexpr bool kGo = decltype(fast)::value;
+            if (NT == 1 || tiles == 1)
+                multiply<NT, 1, F, kGo>(acc, sixteenth, stage, x, rows_of, on, ahead, there, lane);
+            else if (NT == 2 || tiles == 2)
+                multiply<NT, NT < 2 ? 1 : 2, F, kGo>(acc, sixteenth, stage, x, rows_of, on, ahead, there, lane);
+            else
+                multiply<NT, NT, F, kGo>(acc, sixteenth, stage, x, rows_of, on, ahead, there, lane);
+        };
+        if (kFast && scales_fit<F>(stage, kb, blocks, lane))
+            go(std::integral_constant<bool, kFast>());
         else
-            multiply<NT, NT, F, DOWN>(acc, stage, x, rows_of, sums_of, on, ahead, there, lane);
+            go(std::false_type());
         if (++slot == kStages) slot = 0;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            x.row[n] += static_cast<uint32_t>(on);
-            x.sum[n] += static_cast<uint32_t>(on / 128 * kSums);
-        }
+        for (int n = 0; n < NT; ++n) x.row[n] += static_cast<uint32_t>(on);
         if (++kb == steps) {
+            fold();
             if (whole)
                 finish();
             else
@@ -748,6 +714,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     }
     copies_wait<0>();
     const bool open = s0 < s1 && kb != 0;
+    if (open) fold();
     if (open && !whole) leave();
     __syncthreads();
     if (open && whole) {
