@@ -460,10 +460,16 @@ struct Tokens {
 // FAST (int4): the pairs of codes that a mask takes out of a word are, as fp16 numbers, q 2^-24 (bits 0..3) or q 2^-20
 // (bits 4..7): subnormal and exact. One fused multiply-add with s 2^20 and -s / 2 or -8 s gives (q - 8) s / 16 or
 // (q - 8) s with its one rounding, which is the format's: 9 instructions for 8 weights instead of dequant8's 13. It needs
-// every number normal, a scale in 2^-10 .. 2^-4; other steps go the long way. Sixteenths are summed apart.
+// every number normal, a scale in 2^-10 .. 2^-4; other steps go the long way (all of them: one token 57 us instead of 47,
+// 64 tokens 323 instead of 272). Sixteenths are summed apart, or, where there are registers for one set of sums only,
+// codes are multiplied by 16 first, 11 instructions (16 tokens 199 us that way, 189 apart; 64 tokens 272, 304 apart).
+__host__ __device__ constexpr bool apart(int nt) { return nt == 1; }
+
 template <int NT, int TILES, Form F, bool FAST>
 __device__ __forceinline__ void multiply(float (&sum)[4][NT][4], float (&sixteenth)[4][NT][4], uint32_t stage, Tokens<NT>& x,
                                          const uint16_t* rows, int on, bool ahead, bool there, int lane) {
+    constexpr bool kApart = apart(NT);
+    constexpr uint32_t k16 = 0x4C004C00u;  // (16, 16)
     const uint32_t vec = stage + vector_place(lane), sc = stage + Stage<F>::kScales + 2u * (lane >> 2);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -488,9 +494,9 @@ __device__ __forceinline__ void multiply(float (&sum)[4][NT][4], float (&sixteen
                     dequant8(word, s[i][0], d[i]);
                 } else {
                     const uint32_t up = s[i][0] + 0x50005000u, less_half = s[i][0] + 0x7C007C00u, less_8 = s[i][0] + 0x8C008C00u;
-                    d[i][0] = hfma2(word & 0x000F000Fu, up, less_half);
+                    d[i][0] = kApart ? hfma2(word & 0x000F000Fu, up, less_half) : hfma2(hmul2(word & 0x000F000Fu, k16), up, less_8);
                     d[i][1] = hfma2(word & 0x00F000F0u, up, less_8);
-                    d[i][2] = hfma2((word >> 8) & 0x000F000Fu, up, less_half);
+                    d[i][2] = kApart ? hfma2((word >> 8) & 0x000F000Fu, up, less_half) : hfma2(hmul2((word >> 8) & 0x000F000Fu, k16), up, less_8);
                     d[i][3] = hfma2((word >> 8) & 0x00F000F0u, up, less_8);
                 }
             }
@@ -498,7 +504,7 @@ __device__ __forceinline__ void multiply(float (&sum)[4][NT][4], float (&sixteen
             for (int n = 0; n < TILES; ++n) {
                 if (F != kInt4 && c == 0 && !there) x.unit[n][w] = make_uint4(0u, 0u, 0u, 0u);
                 const uint4& u = x.unit[n][w];
-                mma16816(FAST ? sixteenth[c][n] : sum[c][n], d[0][0], d[1][0], d[0][2], d[1][2], u.x, u.y);
+                mma16816(FAST && kApart ? sixteenth[c][n] : sum[c][n], d[0][0], d[1][0], d[0][2], d[1][2], u.x, u.y);
                 mma16816(sum[c][n], d[0][1], d[1][1], d[0][3], d[1][3], u.z, u.w);
                 if (c == 3 && ahead) x.unit[n][w] = *reinterpret_cast<const uint4*>(rows + x.row[n] + on + 32 * w);
             }
@@ -593,7 +599,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     const uint16_t* const rows_of = DOWN ? r.w.act : r.w.xp;
     Tokens<NT> x;  // at step kb
     float acc[4][NT][4], sixteenth[4][NT][4];
-    constexpr bool kFast = F != kNvfp4 && NT <= 2;  // (32 tokens at a time leave no registers for a second set of sums)
+    constexpr bool kFast = F != kNvfp4;
     int base = 0, count = 0, tiles = 1;
     const int width = static_cast<int>(padded(m.K));
     auto meet = [&]() {  // the rows of an entry's tokens at step kb; a place without a token reads the first one's
@@ -620,7 +626,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
                 for (int i = 0; i < 4; ++i) acc[c][n][i] = sixteenth[c][n][i] = 0.f;
     };
     auto fold = [&]() {
-        if constexpr (kFast) {
+        if constexpr (kFast && apart(NT)) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
