@@ -740,18 +740,30 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int 
         _refuse("logprobs", "temperature must be a CUDA float32 vector of M elements")
     if top < 0:
         _refuse("logprobs", "top must not be negative")
+    logprob = rank = top_tokens = top_logprob = None
     if out is None:
-        def new(n, dtype):
-            return None if n is None else _new(n, dtype, logits.device, stream)
-        tops = (M, top) if top else None
-        out = LogProbs(new(shape, f), new(shape, i32), new((M,), f), new(tops, i32), new(tops, f))
+        dev = logits.device
+        if stream is None:
+            if shape is not None:
+                logprob, rank = torch.empty(shape, dtype=f, device=dev), torch.empty_like(tokens)
+            entropy = torch.empty(M, dtype=f, device=dev)
+            if top:
+                top_tokens, top_logprob = torch.empty((M, top), dtype=i32, device=dev), torch.empty((M, top), dtype=f, device=dev)
+        else:
+            if shape is not None:
+                logprob, rank = _new(shape, f, dev, stream), _new(shape, i32, dev, stream)
+            entropy = _new(M, f, dev, stream)
+            if top:
+                top_tokens, top_logprob = _new((M, top), i32, dev, stream), _new((M, top), f, dev, stream)
+        out = LogProbs(logprob, rank, entropy, top_tokens, top_logprob)
     elif not ((out.logprob is None or shape) and (out.rank is None or shape) and _dense(out.logprob, f, shape)
               and _dense(out.rank, i32, shape) and _vec(out.entropy, f, M) and _dense(out.top_tokens, i32, (M, top))
               and _dense(out.top_logprob, f, (M, top)) and (top > 0) == (out.top_tokens is not None) == (out.top_logprob is not None)):
         _refuse("logprobs", "out must be LogProbs of contiguous CUDA tensors of the result's shapes")
+    else:
+        logprob, rank, entropy, top_tokens, top_logprob = out
     rc = lib.w4a16_logprobs(logits.data_ptr(), logits.stride(0), M, V, _ptr(tokens), given, top, _ptr(temperature),
-                            _ptr(out.logprob), _ptr(out.rank), _ptr(out.entropy), _ptr(out.top_tokens), _ptr(out.top_logprob),
-                            _stream_handle(stream))
+                            _ptr(logprob), _ptr(rank), _ptr(entropy), _ptr(top_tokens), _ptr(top_logprob), _stream_handle(stream))
     if rc != OK:
         raise W4A16Error(rc, "w4a16_logprobs")
     return out
@@ -883,8 +895,12 @@ def moe(x: torch.Tensor, experts: Experts, router: torch.Tensor, top_k: int, wor
         _refuse("moe", "top_k must be from 1 to the number of experts")
     T = x.shape[0]
     if out is None:
-        y = _new((T, H), half, x.device, stream)
-        ids, weights = _new((T, top_k), torch.int32, x.device, stream), _new((T, top_k), torch.float32, x.device, stream)
+        dev = x.device
+        if stream is None:
+            y, ids = torch.empty_like(x), torch.empty((T, top_k), dtype=torch.int32, device=dev)
+            weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        else:
+            y, ids, weights = _new((T, H), half, dev, stream), _new((T, top_k), torch.int32, dev, stream), _new((T, top_k), torch.float32, dev, stream)
     else:
         y, ids, weights = out
         if y is None or not (_dense(y, half, (T, H)) and _dense(ids, torch.int32, (T, top_k)) and _dense(weights, torch.float32, (T, top_k))):
