@@ -19,7 +19,14 @@
 // the other's. So a search among the maxima names n chunks, and only their n * 32 elements are read a
 // second time.
 //
-// A row is a CTA or a cluster, whose parts rank 0 brings together in a fixed order.
+// A row is a CTA or a cluster, whose parts rank 0 brings together in a fixed order. Many rows are a CTA of 128 threads
+// each, seven an SM, so that 1024 rows run at once (256 threads, four an SM, 110 us: a second, partial round).
+//
+// Measured on one GB300, vocabulary 248,320, in a CUDA graph: 1024 rows, a token and the first alternative each, 101 us
+// (509 MB, 5.0 TB/s, 0.74 of the measured copy): 8 instructions a logit, and loads that a thread waits for a chunk at a
+// time (the next chunk's by halves, as the one before is worked on: 140 us). One row with 20 alternatives 14.6 us, 16 rows
+// with two tokens each 8.5, 33 rows of 32,003 with 5 alternatives 10.5: latency, of the launch, the token's
+// logit, one chunk or two a thread, the search's six barriers and the cluster's two.
 #include <cmath>
 
 #include "common.cuh"
@@ -219,6 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
     for (; base < c1; base += kThreads) {
         const int i = base + lane;
         if (base != c0 + warp * 32) load(i);
+        if (i + kThreads < min(c1, inner1))  // the next chunk into L2 (1024 rows 103 -> 101 us; two ahead 102, four 107)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(chunk0 + static_cast<int64_t>(i + kThreads) * 64));
         uint32_t hi = max2(x[0], x[1]);
 #pragma unroll
         for (int j = 2; j < 16; ++j) hi = max2(hi, x[j]);

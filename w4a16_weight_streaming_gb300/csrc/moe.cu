@@ -26,6 +26,15 @@
 // beginning keeps its sums and adds the following warps' parts at the end. All of a warp's steps are one stream of
 // copies, whatever items they belong to. The runs are contiguous, so that a CTA meets few experts and finds the
 // rows of their tokens in L1.
+//
+// Measured on one GB300 (hidden 5120, 64 experts of 2176, 8 a token, group 128, in a CUDA graph): 1 token 47 us (139 MB,
+// 2.96 TB/s, 0.44 of the measured copy): 9 us of routing, list, starts and ends, then 12 warps an SM that wait for
+// their first stages and for one another's items (3.6 items a CTA). 16 tokens 190 us (974 MB, 5.1 TB/s, 0.76; gate_up
+// alone 115 us, 5.7 TB/s): the stream without its products takes 181. 64 tokens 272 us (1.1 GB, 4.1 TB/s, 0.60): a step's
+// chain of loads, conversions and products at 3 warps a scheduler, with rows of tokens from L2 (all tokens' rows the same
+// one, in L1: 215; without the weights' stream 230). A cluster of 2 or 4 CTAs with runs of steps in
+// common was slower (46 us for one token where one CTA took 41), as were runs cut at any step (48) and rows of tokens
+// copied to shared memory with the weights (94).
 #include <atomic>
 #include <type_traits>
 

@@ -9,6 +9,10 @@
 // sum before its rounding. A row stays in the registers of the threads that loaded it: one read of y, h
 // and the gate, one write of h' and x, two sums over the row between them. Sums: 8 neighbours of a vector
 // in pairs, a thread's vectors in turn, then the warp and the warps in a fixed order.
+//
+// Measured on one GB300 (rows of 5120, in a CUDA graph): 8192 rows with a norm behind the block and a gate for every
+// element 71.8 us (419 MB, 5.84 TB/s, 0.86 of the measured copy), 1024 rows with an fp32 residual stream 10.2 us
+// (6.2 TB/s, 0.91): memory. 64 rows 2.85 us, one row 2.6: the latency of a launch, a round of loads and two sums.
 #include "common.cuh"
 #include "internal.h"
 
