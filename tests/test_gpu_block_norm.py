@@ -142,3 +142,13 @@ def test_the_index_checking_build_gives_the_same(W):
     assert D.w4a16_device_status(s) == W.OK
     b = W.block_norm(h, y, weight=w, post_weight=p, gate=g, scale=0.5)
     assert torch.equal(a, b[0]) and torch.equal(x, b[1])
+
+
+def test_rows_further_apart_than_32_bits(W):
+    H, step = 1024, 2 ** 31 + 8
+    wide = torch.zeros(2 * step + H, dtype=torch.float16, device="cuda")
+    h = wide.as_strided((3, H), (step, 1))
+    h.copy_(make(3, H)[0])
+    _, y, w, p, _ = make(3, H, seed=5)
+    check(W, h, y, w, post=p)
+    check(W, y, h, w, post=p, gate=h)

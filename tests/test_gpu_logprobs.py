@@ -227,3 +227,28 @@ def test_the_index_checking_build_gives_the_same(W):
     torch.cuda.synchronize()
     assert D.w4a16_device_status(s) == W.OK
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_rows_further_apart_than_32_bits(W):
+    V, step = 5003, 2 ** 31 + 7
+    wide = torch.zeros(2 * step + V, dtype=torch.float16, device="cuda")
+    x = wide.as_strided((3, V), (step, 1))
+    rng = np.random.default_rng(11)
+    x.copy_(torch.from_numpy(peaked(rng, 3, V)).cuda())
+    check(W, x, rng.integers(0, V, (3, 2)), 6)
+
+
+def test_many_rows(W):
+    g = torch.Generator("cuda").manual_seed(12)
+    x = (3 * torch.randn((65536, 300), generator=g, device="cuda")).half()
+    t = torch.randint(0, 300, (65536, 1), generator=g, device="cuda").int()
+    r = W.logprobs(x, t, top=2)
+    torch.cuda.synchronize()
+    lp = torch.log_softmax(x.double(), 1)
+    assert float((r.logprob.double() - lp.gather(1, t.long())).abs().max()) < 1e-5
+    best = torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :2]
+    assert torch.equal(r.top_tokens.long(), best)
+    at = x.gather(1, t.long())
+    index = torch.arange(300, device="cuda")[None]
+    assert torch.equal(r.rank[:, 0].long(), 1 + ((x > at) | ((x == at) & (index < t))).sum(1))
+    assert float((r.entropy.double() + (lp.exp() * lp).sum(1)).abs().max()) < 1e-5

@@ -321,3 +321,42 @@ def test_one_expert_is_the_dense_layer(W):
     # gate and up rounded to fp16 there: 2^-11 of each, so act by 2^-9 at most
     assert bool((np.abs(y.double().cpu().numpy() - y_ref) <= 2.0 ** -10 * np.abs(y_ref) + 2.0 ** -8 * abs_ref).all())
     assert bool(((y.double() - dense.double()).abs() <= 0.02 * dense.double().abs().amax()).all())
+
+
+def test_experts_and_rows_further_apart_than_32_bits(W):
+    """300 experts of 2560 x 12288 and 6144 x 2560: 4.7 and 2.4 GB of codes. Only the chosen ones are looked at."""
+    E, H, I, G = 300, 2560, 6144, 128
+    g = torch.Generator("cuda").manual_seed(13)
+    up = torch.randint(-2 ** 31, 2 ** 31, (E, H // 8, 2 * I), generator=g, device="cuda", dtype=torch.int32)
+    down = torch.randint(-2 ** 31, 2 ** 31, (E, I // 8, H), generator=g, device="cuda", dtype=torch.int32)
+    su = (0.004 * (1 + torch.rand((E, H // G, 2 * I), generator=g, device="cuda"))).half()
+    sd = (0.004 * (1 + torch.rand((E, I // G, H), generator=g, device="cuda"))).half()
+    m = W.Experts(up, su, down, sd, G)
+    assert up.numel() * 4 > 2 ** 32
+    step = 2 ** 31 + 8
+    wide = torch.zeros(2 * step + H, dtype=torch.float16, device="cuda")
+    x = wide.as_strided((3, H), (step, 1))
+    x.copy_(torch.randn((3, H), generator=g, device="cuda").half())
+    bias = torch.zeros(E, device="cuda")
+    bias[[299, 150, 1]] = 5.0
+    y, ids, w = W.moe(x, m, (torch.randn((E, H), generator=g, device="cuda") / H ** 0.5).half(), 3, W.moe_workspace(m), bias=bias, sigmoid=True)
+    torch.cuda.synchronize()
+    assert all(sorted(r) == [1, 150, 299] for r in ids.tolist())
+    ref = torch.zeros((3, H), dtype=torch.float64, device="cuda")
+    for e in (1, 150, 299):
+        both = x.double() @ dequantised(up[e:e + 1], su[e:e + 1], G)[0]
+        a = both[:, :I] * torch.sigmoid(both[:, :I]) * both[:, I:]
+        share = torch.where(ids == e, w, 0.0).sum(1, keepdim=True).double()
+        ref += share * (a @ dequantised(down[e:e + 1], sd[e:e + 1], G)[0])
+    assert float((y.double() - ref).norm() / ref.norm()) < 2.0 ** -10
+
+
+@pytest.mark.parametrize("T", [5, 24, 64])
+def test_experts_with_every_load(W, T):
+    """One expert that every token takes, some that a few take, some that none does; tokens in every place of 8."""
+    L = Layer(W, 20, 384, 256, 128, seed=14)
+    g = torch.Generator("cuda").manual_seed(T)
+    for _ in range(4):
+        bias = torch.randn(20, generator=g, device="cuda")
+        bias[int(torch.randint(0, 20, (1,), generator=g, device="cuda"))] = 9.0
+        check(W, L, L.x(T, seed=int(torch.randint(0, 99, (1,), generator=g, device="cuda"))), 5, sigmoid=True, bias=bias)
