@@ -464,10 +464,12 @@ int w4a16_block_norm(const void* h, int64_t h_stride, int h_f32, const uint16_t*
  *   l[t][e] = x[t] . router[e];  score = softmax over e of l, or 1 / (1 + e^-l)
  *   chosen:  the top_k experts of a token with the largest l (sigmoid: score + bias); ties: the lower index, NaN last
  *   r[t][e] = scale * score, with renormalize over the sum of the chosen ones' scores
- *   a = fp16_rne(silu(x . Wg) * (x . Wu)), the products in fp32;  y[t] = fp16_rne(sum_e r * (a . Wd)), in order of e
+ *   a = fp16_rne(silu(x . Wg) * (x . Wu)), the products in fp32;  y[t] = fp16_rne(sum_e r * (a . Wd)), summed in
+ *   the order of choice
  * The experts' matrices are those of w4a16_repack (or w4a16_repack_nvfp4) one after another: gate_up [hidden, 2 inner]
- * with its columns in turns, 16 of gate and then the same 16 of up; down [inner, hidden]. A call reads each chosen expert's weights once, whatever the tokens (an
- * expert with many more tokens than the average again). Products are within the bound of w4a16_gemm.
+ * with its columns in turns, 16 of gate and then the same 16 of up; down [inner, hidden]. A call reads each chosen
+ * expert's weights once, whatever the tokens (an expert with many more tokens than the average again). Products are
+ * within the bound of w4a16_gemm.
  */
 typedef struct {
     const void* gate_up_q;      /* experts * w4a16_repacked_qweight_bytes(2 inner, hidden, group) */
@@ -494,7 +496,7 @@ size_t w4a16_moe_workspace_bytes(int experts, int hidden, int inner);
  *   ids:     int32 [tokens][top_k], the chosen experts in order, or NULL; weights: fp32 [tokens][top_k], r, or NULL
  * No token bears on another's result but in the order of its sums (which follows the list of chosen experts): infinities
  * and NaN stay in their row. Repeats of a batch are bit-identical.
- * tokens <= 64, top_k <= 16 and <= experts. Three kernels. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
+ * tokens <= 64, top_k <= 16 and <= experts. Four kernels. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
 int w4a16_moe(const uint16_t* x, int64_t x_stride, const w4a16_moe_experts* experts, const uint16_t* router, const float* bias,
               int top_k, int scoring, int renormalize, float scale, uint16_t* y, int32_t* ids, float* weights, int tokens,
               void* workspace, size_t workspace_bytes, void* stream);

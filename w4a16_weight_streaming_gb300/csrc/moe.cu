@@ -21,20 +21,21 @@
 // must follow, so rows of x and of a are kept with their 16-byte units transposed within each 128 (unit w of
 // block t at place 4 w + t). A lane copies what it will read itself, so a warp's ring of stages needs no barrier.
 //
-// Work is a list of items, (listed expert, 64 columns) over all of K, in steps of 128 k. A CTA takes an equal
+// Work is a list of items, (listed expert, 32 or 64 columns) over all of K, in steps of 128 k. A CTA takes an equal
 // run of items, its warps equal runs of their steps, wherever that cuts an item: the warp that has an item's
 // beginning keeps its sums and adds the following warps' parts at the end. All of a warp's steps are one stream of
 // copies, whatever items they belong to. The runs are contiguous, so that a CTA meets few experts and finds the
 // rows of their tokens in L1.
 //
-// Measured on one GB300 (hidden 5120, 64 experts of 2176, 8 a token, group 128, in a CUDA graph): 1 token 47 us (139 MB,
-// 2.96 TB/s, 0.44 of the measured copy): 9 us of routing, list, starts and ends, then 12 warps an SM that wait for
-// their first stages and for one another's items (3.6 items a CTA). 16 tokens 190 us (974 MB, 5.1 TB/s, 0.76; gate_up
-// alone 115 us, 5.7 TB/s): the stream without its products takes 181. 64 tokens 272 us (1.1 GB, 4.1 TB/s, 0.60): a step's
-// chain of loads, conversions and products at 3 warps a scheduler, with rows of tokens from L2 (all tokens' rows the same
-// one, in L1: 215; without the weights' stream 230). A cluster of 2 or 4 CTAs with runs of steps in
-// common was slower (46 us for one token where one CTA took 41), as were runs cut at any step (48) and rows of tokens
-// copied to shared memory with the weights (94).
+// Measured on one GB300 (hidden 5120, 64 experts of 2176, 8 a token, group 128, in a CUDA graph): 1 token 42.5 us (139 MB,
+// 3.26 TB/s, 0.48 of the measured copy): 9 us of routing, list, starts and ends, then 20 warps an SM that wait for
+// their first stages and for one another's items (7.2 items a CTA in gate_up, 8.4 in down: some have 8 and 9). 16 tokens
+// 191 us (974 MB, 5.1 TB/s, 0.75; gate_up alone 115 us, 5.7 TB/s): the stream without its products takes 181. 64 tokens
+// 272 us (1.1 GB, 4.1 TB/s, 0.60): a step's chain of loads, conversions and products at 3 warps a scheduler, with rows of
+// tokens from L2 (all tokens' rows the same one, in L1: 215; without the weights' stream 230); items of 128 columns at 8
+// warps, which read the tokens half as often, 284. A cluster of 2 or 4 CTAs with runs of steps in common was slower (46 us
+// for one token where one CTA took 41), as were runs cut at any step (48), rows of tokens copied to shared memory with
+// the weights (94) and tokens in loads of 32 bytes (43.1 for one, 195 for 16).
 #include <atomic>
 #include <type_traits>
 
@@ -47,9 +48,12 @@ namespace {
 constexpr int kRouteThreads = 256;
 constexpr int kStages = 2;    // of a warp's ring
 
-// Warps of a gate_up or down CTA, one CTA an SM, by the tokens (8 NT) that they multiply at a time: the registers for
-// their sums.
-__host__ __device__ constexpr int warps_for(int nt) { return nt <= 2 ? 12 : 8; }
+// Groups of 16 columns of an item, and warps of a gate_up or down CTA, one CTA an SM, by the tokens (8 NT) that are
+// multiplied at a time: as many warps as have the registers for their sums. For 8 tokens, narrow items and many warps:
+// one token 42.5 us, 45 with 64 columns and 12 warps, 43.4, 43.7 and 51 with 16, 18 and 22 warps of 32 columns (16 tokens
+// 191, 191, 196, 202, 243). For 16, 64 tokens take 272 us, with 32 columns and 12, 16 or 20 warps 307, 279, 424.
+__host__ __device__ constexpr int groups_for(int nt) { return nt == 1 ? 2 : 4; }
+__host__ __device__ constexpr int warps_for(int nt) { return nt == 1 ? 20 : nt == 2 ? 12 : 8; }
 
 // The weights' formats: how many rows of scales 128 k have.
 enum Form {
@@ -382,29 +386,29 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A stage of a warp's ring: 128 k of 64 columns. Vectors: [16 columns][half][32-k block][column, swizzled]; then scales
-// [row][64 columns]. Column g of block t lies at place g ^ 2 t of its 8, so that neither the copies (8 columns of
+// A stage of a warp's ring: 128 k of C * 16 columns. Vectors: [16 columns][half][32-k block][column, swizzled]; then scales
+// [row][columns]. Column g of block t lies at place g ^ 2 t of its 8, so that neither the copies (8 columns of
 // a block at a time) nor the reads (2 columns of 4 blocks) meet in a bank.
-template <Form F>
+template <Form F, int C>
 struct Stage {
     static constexpr int kRows = F == kInt4 ? 1 : F == kInt4Small ? 4 : 8;  // of scales
-    static constexpr int kScales = 4096;
-    static constexpr int kBytes = kScales + kRows * 128;
+    static constexpr int kScales = 1024 * C;
+    static constexpr int kBytes = kScales + kRows * 32 * C;
 };
 __device__ __forceinline__ uint32_t vector_place(int lane) {
     const int g = lane >> 2, t = lane & 3;
     return static_cast<uint32_t>(t * 128 + ((g ^ (2 * t)) & 7) * 16);
 }
 
-// Where a lane's copies come from: an item's 64 columns, at the next step to be copied. A block's 64 vectors are 1 KB
-// side by side. (Items of 2 x 16 columns, 256 bytes a block, streamed at 5.0 TB/s with the products left out.)
-template <Form F>
+// Where a lane's copies come from: an item's columns, at the next step to be copied. A block's vectors lie side by side.
+template <Form F, int C>
 struct Source {
     const uint4* w;
-    const uint16_t* s;  // kInt4: of this lane's pair
+    const uint16_t* s;  // kInt4: of this lane's pair (of 32 columns: of the first 16 lanes')
     int wt;             // vectors from one 32-k block to the next
     int kb, row_left;   // kInt4: steps until the next row of scales
 
+    static __device__ __forceinline__ int pair_of(int lane) { return 2 * (lane % (8 * C)); }
     __device__ __forceinline__ void set(const Matrices& m, int expert, int column, int first, int lane) {
         const int blocks = m.K / 32, rows = m.K / m.G, tile = column >> 7;
         kb = first;
@@ -414,7 +418,7 @@ struct Source {
         s = m.s + static_cast<int64_t>(expert) * m.N * rows + static_cast<int64_t>(tile) * 128 * rows + (column & 127);
         if (F == kInt4) {
             const int q = m.G / 128, row = first / q;
-            s += static_cast<int64_t>(row) * wt + 2 * lane;
+            s += static_cast<int64_t>(row) * wt + pair_of(lane);
             row_left = q - (first - row * q);
         }
     }
@@ -422,26 +426,27 @@ struct Source {
     __device__ __forceinline__ void copy(const Matrices& m, uint32_t stage, int blocks, int per, int shift, int lane, unsigned* status) {
         const uint32_t vec = stage + vector_place(lane);
         const int64_t all = static_cast<int64_t>(m.E) * m.N, scales = all * (m.K / m.G);  // (index checks)
-        if ((F == kInt4 || kb * 4 + (lane & 3) < blocks) && in_bounds(w - m.w + 56 < all * blocks, status)) {
+        if ((F == kInt4 || kb * 4 + (lane & 3) < blocks) && in_bounds(w - m.w + 16 * C - 8 < all * blocks, status)) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) copy16(vec + 512u * i, w + 8 * i);
+            for (int i = 0; i < 2 * C; ++i) copy16(vec + 512u * i, w + 8 * i);
         }
         w += 4 * wt;
-        const uint32_t to = stage + Stage<F>::kScales + 4u * lane;
+        const uint32_t to = stage + Stage<F, C>::kScales + 2u * pair_of(lane);
+        const bool one = 2 * lane < 16 * C;  // of the lanes that copy scales
         if (F == kInt4) {
-            if (in_bounds(s - m.s + 2 <= scales, status)) copy4(to, s);
+            if (one && in_bounds(s - m.s + 2 <= scales, status)) copy4(to, s);
             if (--row_left == 0) {
                 row_left = per >> 2;
                 s += wt;
             }
         } else {
 #pragma unroll
-            for (int r = 0; r < Stage<F>::kRows; ++r) {
+            for (int r = 0; r < Stage<F, C>::kRows; ++r) {
                 const int blk = F == kNvfp4 ? kb * 4 + (r >> 1) : kb * 4 + r;
                 if (blk >= blocks) continue;
                 const int row = F == kNvfp4 ? kb * 8 + r : shift >= 0 ? blk >> shift : blk / per;
-                const uint16_t* q = s + static_cast<int64_t>(row) * wt + 2 * lane;
-                if (in_bounds(q - m.s + 2 <= scales, status)) copy4(to + 128u * r, q);
+                const uint16_t* q = s + static_cast<int64_t>(row) * wt + pair_of(lane);
+                if (one && in_bounds(q - m.s + 2 <= scales, status)) copy4(to + 32u * C * r, q);
             }
         }
         ++kb;
@@ -469,26 +474,26 @@ struct Tokens {
 // FAST (int4): the pairs of codes that a mask takes out of a word are, as fp16 numbers, q 2^-24 (bits 0..3) or q 2^-20
 // (bits 4..7): subnormal and exact. One fused multiply-add with s 2^20 and -s / 2 or -8 s gives (q - 8) s / 16 or
 // (q - 8) s with its one rounding, which is the format's: 9 instructions for 8 weights instead of dequant8's 13. It needs
-// every number normal, a scale in 2^-10 .. 2^-4; other steps go the long way (all of them: one token 57 us instead of 47,
-// 64 tokens 323 instead of 272). Sixteenths are summed apart, or, where there are registers for one set of sums only,
-// codes are multiplied by 16 first, 11 instructions (16 tokens 199 us that way, 189 apart; 64 tokens 272, 304 apart).
+// every number normal, a scale in 2^-10 .. 2^-4; other steps go the long way (all of them: one token 45.4 us instead of 42.5,
+// 64 tokens 292 instead of 272; without the question 41.7 and 276). Sixteenths are summed apart, or, where there are registers for one set of sums only,
+// codes are multiplied by 16 first, 11 instructions (one token 43.7 us that way, 16 tokens 199; 64 tokens 304 apart).
 __host__ __device__ constexpr bool apart(int nt) { return nt == 1; }
 
-template <int NT, int TILES, Form F, bool FAST>
-__device__ __forceinline__ void multiply(float (&sum)[4][NT][4], float (&sixteenth)[4][NT][4], uint32_t stage, Tokens<NT>& x,
+template <int NT, int TILES, Form F, bool FAST, int C = groups_for(NT)>
+__device__ __forceinline__ void multiply(float (&sum)[C][NT][4], float (&sixteenth)[C][NT][4], uint32_t stage, Tokens<NT>& x,
                                          const uint16_t* rows, int on, bool ahead, bool there, int lane) {
     constexpr bool kApart = apart(NT);
     constexpr uint32_t k16 = 0x4C004C00u;  // (16, 16)
-    const uint32_t vec = stage + vector_place(lane), sc = stage + Stage<F>::kScales + 2u * (lane >> 2);
+    const uint32_t vec = stage + vector_place(lane), sc = stage + Stage<F, C>::kScales + 2u * (lane >> 2);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < C; ++c) {
         const uint4 v[2] = {lds128(vec + 1024u * c), lds128(vec + 1024u * c + 512u)};
         uint32_t s[2][2];  // of columns g, g + 8, twice in a register; NVFP4: of a block's halves
         const uint32_t row = F == kInt4 ? 0u : F == kInt4Small ? lane & 3u : 2u * (lane & 3u);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            s[i][0] = lds16(sc + 128u * row + 32u * c + 16u * i) * 0x10001u;
-            if (F == kNvfp4) s[i][1] = lds16(sc + 128u * (row + 1) + 32u * c + 16u * i) * 0x10001u;
+            s[i][0] = lds16(sc + 32u * C * row + 32u * c + 16u * i) * 0x10001u;
+            if (F == kNvfp4) s[i][1] = lds16(sc + 32u * C * (row + 1) + 32u * c + 16u * i) * 0x10001u;
             if (F != kInt4 && !there) s[i][0] = s[i][1] = 0x1C001C00u;  // past K: what the stage holds is not of this step
         }
 #pragma unroll
@@ -515,20 +520,20 @@ __device__ __forceinline__ void multiply(float (&sum)[4][NT][4], float (&sixteen
                 const uint4& u = x.unit[n][w];
                 mma16816(FAST && kApart ? sixteenth[c][n] : sum[c][n], d[0][0], d[1][0], d[0][2], d[1][2], u.x, u.y);
                 mma16816(sum[c][n], d[0][1], d[1][1], d[0][3], d[1][3], u.z, u.w);
-                if (c == 3 && ahead) x.unit[n][w] = *reinterpret_cast<const uint4*>(rows + x.row[n] + on + 32 * w);
+                if (c == C - 1 && ahead) x.unit[n][w] = *reinterpret_cast<const uint4*>(rows + x.row[n] + on + 32 * w);
             }
         }
     }
 }
 
 // Whether all scales of a step are normal enough for the fast way: 2^-10 <= s < 2^-4. (A row past K is not looked at.)
-template <Form F>
+template <Form F, int C>
 __device__ __forceinline__ bool scales_fit(uint32_t stage, int kb, int blocks, int lane) {
     bool fit = true;
 #pragma unroll
-    for (int r = 0; r < Stage<F>::kRows; ++r) {
+    for (int r = 0; r < Stage<F, C>::kRows; ++r) {
         if (F != kInt4 && kb * 4 + r >= blocks) continue;
-        const uint32_t p = lds32(stage + Stage<F>::kScales + 128u * r + 4u * lane);
+        const uint32_t p = lds32(stage + Stage<F, C>::kScales + 32u * C * r + 4u * (lane % (8 * C)));
         fit = fit && (p & 0xFFFFu) - 0x1400u < 0x1800u && (p >> 16) - 0x1400u < 0x1800u;
     }
     return __all_sync(0xffffffffu, fit);
@@ -537,13 +542,13 @@ __device__ __forceinline__ bool scales_fit(uint32_t stage, int kb, int blocks, i
 // DOWN false: gate and up (16 columns of gate, the 16 of up, twice an item), true: down.
 template <int NT, Form F, bool DOWN>
 __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Matrices m, const RouteArgs r, int I, unsigned* status) {
-    constexpr int kWarps = warps_for(NT);
+    constexpr int kWarps = warps_for(NT), C = groups_for(NT);
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ List list;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = r.H;
-    const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * kStages * Stage<F>::kBytes);
-    // parts of items that begin in an earlier warp: [warp][16 columns][n][register][lane]
-    float* heads = reinterpret_cast<float*>(smem + kWarps * kStages * Stage<F>::kBytes);
+    const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * kStages * Stage<F, C>::kBytes);
+    // parts of items that begin in an earlier warp: [warp][16 columns][8 tokens][register][lane]
+    float* heads = reinterpret_cast<float*>(smem + kWarps * kStages * Stage<F, C>::kBytes);
     if (!DOWN) {
         griddep_wait();
         griddep_launch_dependents();  // (after the wait: the next kernel may read the list before its own)
@@ -573,7 +578,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
         __syncthreads();
     }
 
-    const int chunks = m.N / 64;
+    const int chunks = m.N / (16 * C);
     const int steps = static_cast<int>(padded(m.K) / 128), blocks = m.K / 32;
     const int per = F == kNvfp4 ? 1 : m.G / 32, shift = (per & (per - 1)) == 0 ? __ffs(per) - 1 : -1;
     const int64_t items = static_cast<int64_t>(list.entries) * chunks;
@@ -583,31 +588,31 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     const int s0 = begin(warp), s1 = begin(warp + 1);
 
     // the copying end of the stream
-    Source<F> src;
+    Source<F, C> src;
     const int64_t first = item0 + s0 / steps;
     int entry = static_cast<int>(first / chunks), chunk = static_cast<int>(first % chunks), kb = s0 % steps;
     int c_entry = entry, c_chunk = chunk, c_left = s1 - s0;
     auto fetch = [&](int slot) {
         if (c_left > 0) {
-            src.copy(m, ring + static_cast<uint32_t>(slot * Stage<F>::kBytes), blocks, per, shift, lane, status);
+            src.copy(m, ring + static_cast<uint32_t>(slot * Stage<F, C>::kBytes), blocks, per, shift, lane, status);
             if (--c_left > 0 && src.kb == steps) {
                 if (++c_chunk == chunks) {
                     c_chunk = 0;
                     ++c_entry;
                 }
-                src.set(m, list.expert[c_entry], 64 * c_chunk, 0, lane);
+                src.set(m, list.expert[c_entry], 16 * C * c_chunk, 0, lane);
             }
         }
         copies_commit();
     };
-    if (c_left > 0) src.set(m, list.expert[c_entry], 64 * c_chunk, kb, lane);
+    if (c_left > 0) src.set(m, list.expert[c_entry], 16 * C * c_chunk, kb, lane);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(i);
     if (DOWN) griddep_wait();
 
     const uint16_t* const rows_of = DOWN ? r.w.act : r.w.xp;
     Tokens<NT> x;  // at step kb
-    float acc[4][NT][4], sixteenth[4][NT][4];
+    float acc[C][NT][4], sixteenth[C][NT][4];
     constexpr bool kFast = F != kNvfp4;
     int base = 0, count = 0, tiles = 1;
     const int width = static_cast<int>(padded(m.K));
@@ -628,7 +633,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     };
     auto clear = [&]() {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -637,7 +642,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     auto fold = [&]() {
         if constexpr (kFast && apart(NT)) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -656,27 +661,27 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
                 if (DOWN) {
                     if (!there) continue;
                     const float w = list.weight[pair] * factor;
-                    float* to = r.w.part + static_cast<int64_t>(pair) * H + 64 * chunk + (lane >> 2);
+                    float* to = r.w.part + static_cast<int64_t>(pair) * H + 16 * C * chunk + (lane >> 2);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < C; ++c) {
                         to[16 * c] = w * acc[c][n][h];
                         to[16 * c + 8] = w * acc[c][n][2 + h];
                     }
                 } else {
                     if (!there) continue;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float g = acc[q & 2][n][2 * (q & 1) + h] * factor, u = acc[(q & 2) + 1][n][2 * (q & 1) + h] * factor;
-                        r.w.act[pair * padded(I) + unit_place(32 * chunk + 8 * q + (lane >> 2))] =
+                    for (int q = 0; q < C; ++q) {
+                        const float g = acc[q & ~1][n][2 * (q & 1) + h] * factor, u = acc[(q & ~1) + 1][n][2 * (q & 1) + h] * factor;
+                        r.w.act[pair * padded(I) + unit_place(8 * C * chunk + 8 * q + (lane >> 2))] =
                             __half_as_ushort(__float2half_rn(g / (1.0f + expf(-g)) * u));
                     }
                 }
             }
     };
-    float* mine = heads + (warp * 4 * NT * 4) * 32 + lane;
+    float* mine = heads + (warp * C * NT * 4) * 32 + lane;
     auto leave = [&]() {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -691,7 +696,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
         copies_wait<kStages - 2>();
         __syncwarp();  // (scales are copied for each other; and the slot that is filled next has been read)
         fetch(slot == 0 ? kStages - 1 : slot - 1);
-        const uint32_t stage = ring + static_cast<uint32_t>(slot * Stage<F>::kBytes);
+        const uint32_t stage = ring + static_cast<uint32_t>(slot * Stage<F, C>::kBytes);
         const bool there = F == kInt4 || kb * 4 + (lane & 3) < blocks;
         const bool last = kb + 1 == steps, ahead = s + 1 < s1 && !(last && chunk + 1 == chunks);
         const int on = last ? 128 - width : 128;  // the next item's first step, of the same tokens
@@ -704,7 +709,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
             else
                 multiply<NT, NT, F, kGo>(acc, sixteenth, stage, x, rows_of, on, ahead, there, lane);
         };
-        if (kFast && scales_fit<F>(stage, kb, blocks, lane))
+        if (kFast && scales_fit<F, C>(stage, kb, blocks, lane))
             go(std::integral_constant<bool, kFast>());
         else
             go(std::false_type());
@@ -734,7 +739,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     __syncthreads();
     if (open && whole) {
         const int end = s1 - kb + steps;  // of the item, in the CTA's steps
-        constexpr int kBatch = NT == 1 ? 4 : NT == 2 ? 2 : 1, kValues = 16 * NT;
+        constexpr int kBatch = NT == 2 ? 2 : 1, kValues = 4 * C * NT;
         for (int other = warp + 1; other < kWarps && begin(other) < end; other += kBatch) {
             float v[kBatch][kValues];
 #pragma unroll
@@ -811,7 +816,8 @@ cudaError_t launch_form(const MoeParams& p, const RouteArgs& r, int sm_count, cu
     const Matrices up = {static_cast<const uint4*>(p.gate_up_q), p.gate_up_s, p.gate_up_factor, 2 * p.I, p.H, p.G, p.E};
     const Matrices down = {static_cast<const uint4*>(p.down_q), p.down_s, p.down_factor, p.H, p.I, p.G, p.E};
     constexpr int kThreads = warps_for(NT) * 32;
-    constexpr size_t smem = warps_for(NT) * (kStages * Stage<F>::kBytes + 4 * NT * 4 * 32 * 4);
+    constexpr int C = groups_for(NT);
+    constexpr size_t smem = warps_for(NT) * (kStages * Stage<F, C>::kBytes + C * NT * 4 * 32 * 4);
     const dim3 grid(static_cast<unsigned>(sm_count));
     static std::atomic<uint64_t> allowed{0};  // devices that know these kernels' shared memory
     int dev = 0;
