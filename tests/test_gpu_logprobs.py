@@ -252,3 +252,31 @@ def test_many_rows(W):
     index = torch.arange(300, device="cuda")[None]
     assert torch.equal(r.rank[:, 0].long(), 1 + ((x > at) | ((x == at) & (index < t))).sum(1))
     assert float((r.entropy.double() + (lp.exp() * lp).sum(1)).abs().max()) < 1e-5
+
+
+def test_two_host_threads(W):
+    """Calls of one kernel with much and with little shared memory, at the same time."""
+    import threading
+
+    rows = {v: torch.randn((320, v), device="cuda").half() for v in (1000000, 1000)}
+    wanted = {v: W.logprobs(x, top=3) for v, x in rows.items()}
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def work(v):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(100 if v < 10000 else 25):
+                got[v] = W.logprobs(rows[v], top=3, stream=s)
+            s.synchronize()
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(v,)) for v in rows]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for v in rows:
+        assert torch.equal(got[v].top_tokens, wanted[v].top_tokens) and torch.equal(got[v].entropy, wanted[v].entropy)

@@ -476,10 +476,9 @@ cudaError_t launch_with(const LogprobArgs& a, int M, int C, cudaStream_t s, unsi
     auto kern = top ? logprobs_kernel<NG, true, kThreads> : logprobs_kernel<NG, false, kThreads>;
     const int chunks = ((a.V + 31 + 31) / 32 + C - 1) / C;
     const size_t smem = top ? (static_cast<size_t>(chunks) * 2 + 31) / 16 * 16 : 0;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    if (C > 8) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (top) {  // the most that a call can need: another thread's call may be between here and its launch
+        constexpr int most = ((1000000 + 62) / 32 * 2 + 31) / 16 * 16;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
