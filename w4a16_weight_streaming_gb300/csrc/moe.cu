@@ -231,7 +231,7 @@ __device__ __forceinline__ void make_list(const RouteArgs& a, unsigned* status) 
     __syncthreads();
     for (int p = threadIdx.x; p < pairs; p += kRouteThreads) {
         const int t = p / a.k;
-        atomicOr(&mask[t >> 5][__ldcg(a.w.chosen + p)], 1u << (t & 31));
+        atomicOr(&mask[t >> 5][min(static_cast<int>(__ldcg(a.w.chosen + p)), a.E - 1)], 1u << (t & 31));
     }
     uint32_t carry = 0;  // (entries << 16) + pairs of the experts before
     for (int e0 = 0; e0 < a.E; e0 += kRouteThreads) {
@@ -266,7 +266,7 @@ __device__ __forceinline__ void make_list(const RouteArgs& a, unsigned* status) 
     }
     __syncthreads();
     for (int p = threadIdx.x; p < pairs; p += kRouteThreads) {  // an expert's pairs by token
-        const int t = p / a.k, e = __ldcg(a.w.chosen + p);
+        const int t = p / a.k, e = min(static_cast<int>(__ldcg(a.w.chosen + p)), a.E - 1);
         const uint32_t lo = mask[0][e], hi = mask[1][e], bit = 1u << (t & 31);
         const int at = start[e] + (t < 32 ? __popc(lo & (bit - 1)) : __popc(lo) + __popc(hi & (bit - 1)));
         if (!in_bounds(at < pairs, status)) continue;
@@ -557,18 +557,19 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
         // The list is the work of the kernel before the last: complete, since every CTA of the last one had passed its
         // wait before this kernel could start.
     }
-    {
+    {  // Every number within its limits: a workspace that was not zeroed, or that two calls share, gives wrong results only.
         const List* from = r.w.list;
-        const int entries = __ldcg(&from->entries), pairs = r.T * r.k;
-        for (int i = threadIdx.x; i < min(pairs, kMoeMaxExperts + kMaxPairs / 8); i += kWarps * 32) {  // (no more entries than pairs)
-            list.expert[i] = __ldcg(from->expert + i);
-            list.base[i] = __ldcg(from->base + i);
+        const int pairs = r.T * r.k, most = min(pairs, kMoeMaxExperts + kMaxPairs / 8);  // (no more entries than pairs)
+        const int entries = max(1, min(__ldcg(&from->entries), most));
+        for (int i = threadIdx.x; i < most; i += kWarps * 32) {
+            list.expert[i] = static_cast<uint16_t>(min(static_cast<int>(__ldcg(from->expert + i)), m.E - 1));
+            list.base[i] = static_cast<uint16_t>(min(static_cast<int>(__ldcg(from->base + i)), pairs - 1));
         }
         for (int i = threadIdx.x; i < pairs; i += kWarps * 32) {
             if (DOWN)
                 list.weight[i] = __ldcg(from->weight + i);
             else
-                list.token[i] = __ldcg(from->token + i);
+                list.token[i] = static_cast<uint8_t>(min(static_cast<int>(__ldcg(from->token + i)), r.T - 1));
         }
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     const int width = static_cast<int>(padded(m.K));
     auto meet = [&]() {  // the rows of an entry's tokens at step kb; a place without a token reads the first one's
         base = list.base[entry];
-        count = list.base[entry + 1] - base;
+        count = max(1, min(list.base[entry + 1] - base, 8 * NT));
         tiles = (count + 7) / 8;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -770,7 +771,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const Space ws, uint16_t* 
     // (the places are route's work: complete before down could start, and so before this kernel could)
     int pair[kMoeMaxTop];
 #pragma unroll
-    for (int j = 0; j < kMoeMaxTop; ++j) pair[j] = there && j < k ? __ldcg(ws.place + t * k + j) : 0;
+    for (int j = 0; j < kMoeMaxTop; ++j) pair[j] = there && j < k ? max(0, min(__ldcg(ws.place + t * k + j), T * k - 1)) : 0;
     griddep_wait();
     if (!there) return;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
