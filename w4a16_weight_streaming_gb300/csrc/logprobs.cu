@@ -6,13 +6,14 @@
 //            of one sign, nothing cancels
 //   the first n of the order
 //
-// A thread takes 32 neighbouring logits (a chunk, 64 bytes in two loads) at a time; it keeps the largest logit
+// A thread takes 32 neighbouring logits (a chunk, 64 bytes) at a time; it keeps the largest logit
 // so far, S and sum w d relative to it, and rescales both when a larger one turns up. A masked logit is read
 // as -65504, whose weight is 0 where the largest is not as low itself or T is below hundreds; elsewhere, and
 // for infinite ones, a chunk goes the slow way, logit by logit.
 //
 // A place is a count: logits above the given one, and equal ones before it; "equal or above" is "above the
-// next smaller fp16 number", so either is one packed comparison, and a warp with no logit above skips it.
+// next smaller fp16 number", so either is one packed comparison, its masks added up as whole numbers (3 instructions for
+// 4 logits; 4 with fp16 counts: 1024 rows 5 us more), and a warp with no logit above skips it.
 //
 // The first n: each chunk leaves its maximum in shared memory. The first n of a row lie in the n chunks that
 // come first in the order (maximum, then lower chunk): a chunk before another has an element before each of
@@ -20,14 +21,17 @@
 // second time.
 //
 // A row is a CTA or a cluster, whose parts rank 0 brings together in a fixed order. Many rows are a CTA of 128 threads
-// each, seven an SM, so that 1024 rows run at once (256 threads, four an SM, 110 us: a second, partial round).
+// each, seven an SM, so that 1024 rows run at once (256 threads, four an SM: a second, partial round, 110 us where 128
+// took 103). While a warp works on its 32 chunks, its next ones are on their way into shared memory.
 //
-// Measured on one GB300, vocabulary 248,320, in a CUDA graph: 1024 rows, a token and the first alternative each, 101 us
-// (509 MB, 5.0 TB/s, 0.74 of the measured copy): 8 instructions a logit, and loads that a thread waits for a chunk at a
-// time (the next chunk's by halves, as the one before is worked on: 140 us). One row with 20 alternatives 14.6 us, 16 rows
-// with two tokens each 8.5, 33 rows of 32,003 with 5 alternatives 10.5: latency, of the launch, the token's
-// logit, one chunk or two a thread, the search's six barriers and the cluster's two.
+// Measured on one GB300, vocabulary 248,320, in a CUDA graph: 1024 rows, a token and the first alternative each, 89.5 us
+// (509 MB, 5.7 TB/s, 0.84 of the measured copy) where some rows' tokens are unlikely, 84 where all are likely (no counting),
+// 80 without token and alternatives: instructions beside the stream, 8 a logit with all of it (with the next chunk prefetched
+// into L2 only 91.3; with (l - m) c in two instructions 97, with counts in fp16 and that 101). One row with 20
+// alternatives 14.7 us, 16 rows with two tokens each 8.75, 33 rows of 32,003 with 5 alternatives 10.8: latency, of the
+// launch, the token's logit, one chunk or two a thread, the search's six barriers and the cluster's two.
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -62,7 +66,10 @@ template <int NG, int kThreads>
 struct __align__(16) Shared {
     static constexpr int kWarps = kThreads / 32;
     unsigned long long best[kMaxTop];          // this CTA's first tokens
-    unsigned long long cand[kCandidates];      // (value key, ~index)
+    union {
+        unsigned long long cand[kCandidates];  // (value key, ~index)
+        uint4 next[kWarps][128];               // before: each warp's next 32 chunks
+    };
     uint32_t keys[kCandidates];                // (value key of a chunk's maximum, ~chunk)
     uint32_t first[kThreads];                  // the first of each thread's maxima
     uint32_t least;
@@ -94,6 +101,9 @@ __device__ __forceinline__ void ldg_stream(uint32_t* v, const void* p) {  // 32 
     asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "l"(p));
+}
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -129,20 +139,32 @@ __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigne
     return d;
 }
 
+// Exponents are those of 2, relative to the largest logit m: l c - k with k = m c rounded, one fused multiply-add a logit; what
+// the rounding of k makes of all weights is taken out at the end. Where k may be too large for that (`far`: T below 0.09),
+// (l - m) c.
+struct Scale {
+    float c;
+    bool far;
+    __device__ __forceinline__ float from(float l, float m) const { return far ? (l - m) * c : fmaf(l, c, -__fmul_rn(m, c)); }
+    __device__ __forceinline__ float between(float m0, float m1) const {
+        return far ? (m0 - m1) * c : __fsub_rn(__fmul_rn(m0, c), __fmul_rn(m1, c));
+    }
+};
+
 // `a` seen from the larger maximum m.
-__device__ __forceinline__ void rescale(Sums& a, float m, float c) {
+__device__ __forceinline__ void rescale(Sums& a, float m, const Scale& c) {
     if (a.s == 0.f) {
         a.d = 0.f;
     } else if (m == INFINITY) {
         if (a.m != m) a.s = a.d = 0.f;
     } else {
-        const float x = (a.m - m) * c, e = ex2(x);
+        const float x = c.between(a.m, m), e = ex2(x);
         a.d = e == 0.f ? 0.f : e * fmaf(x, a.s, a.d);
         a.s *= e;
     }
     a.m = m;
 }
-__device__ __forceinline__ Sums joined(Sums a, Sums b, float c) {
+__device__ __forceinline__ Sums joined(Sums a, Sums b, const Scale& c) {
     const float m = fmaxf(a.m, b.m);
     rescale(a, m, c);
     rescale(b, m, c);
@@ -198,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
     if (base < c1) load(base + lane);
     float temp = a.temperature ? a.temperature[m] : 1.f;
     if (!(temp > 0.f)) temp = 1.f;
-    const float c = fminf(1.44269504088896341f / temp, 1e30f);
+    const float factor = fminf(1.44269504088896341f / temp, 1e30f);
+    const Scale c = {factor, factor > 16.f};
 
     int tchunk[kG];
     uint32_t gt[kG], ge[kG], above[kG];
@@ -222,12 +245,32 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
     Sums run = {-INFINITY, 0.f, 0.f};
     float best = -INFINITY;  // of this thread's chunks, and the first that has it
     int best_chunk = -1;
-    const unsigned long long c2 = pack(c, c);
+    const unsigned long long c2 = pack(factor, factor);
+    const uint32_t slot = smem_u32(sh.next[warp]);
+    bool copied = false;  // this step's chunks
     for (; base < c1; base += kThreads) {
-        const int i = base + lane;
-        if (base != c0 + warp * 32) load(i);
-        if (i + kThreads < min(c1, inner1))  // the next chunk into L2 (1024 rows 103 -> 101 us; two ahead 102, four 107)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(chunk0 + static_cast<int64_t>(i + kThreads) * 64));
+        const int i = base + lane, after = base + kThreads;
+        if (copied) {  // a lane's 16-byte units in an order of its own: 8 lanes, 8 places in the banks
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint4 v = lds128(slot + 64u * lane + 16u * (q ^ (lane >> 1 & 3)));
+                x[4 * q] = v.x;
+                x[4 * q + 1] = v.y;
+                x[4 * q + 2] = v.z;
+                x[4 * q + 3] = v.w;
+            }
+            __syncwarp();
+        } else if (base != c0 + warp * 32) {
+            load(i);
+        }
+        copied = after >= inner0 && after + 32 <= min(c1, inner1) && in_bounds(m * a.stride + 32LL * (after + 32) - off <= total, status);
+        if (copied) {
+            const unsigned char* from = chunk0 + static_cast<int64_t>(after) * 64 + 16 * lane;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) copy16(slot + 512u * q + 16u * lane, from + 512 * q);
+        }
         uint32_t hi = max2(x[0], x[1]);
 #pragma unroll
         for (int j = 2; j < 16; ++j) hi = max2(hi, x[j]);
@@ -245,27 +288,36 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
             const uint32_t t = i < tchunk[j] ? ge[j] : gt[j];
             const __half2 t2 = *reinterpret_cast<const __half2*>(&t);
             if (__any_sync(0xffffffffu, most > __low2float(t2))) {
-                __half2 n = __float2half2_rn(0.f);
+                uint32_t n = 0;  // -1 for a logit above, in 16 bits: -2^16 hi + (2^16 - 1) lo
 #pragma unroll
-                for (int q = 0; q < 16; ++q) n = __hadd2(n, __hgt2(*reinterpret_cast<const __half2*>(&x[q]), t2));
-                above[j] += static_cast<uint32_t>(__low2float(n) + __high2float(n));
+                for (int q = 0; q < 16; q += 2)
+                    n += __hgt2_mask(*reinterpret_cast<const __half2*>(&x[q]), t2) + __hgt2_mask(*reinterpret_cast<const __half2*>(&x[q + 1]), t2);
+                const int lo = static_cast<int>((0u - n) & 0xFFFFu);
+                above[j] += static_cast<uint32_t>(2 * lo - (static_cast<int>(n + lo) >> 16));
             }
         }
         if (most > run.m) rescale(run, most, c);
-        if (run.m < INFINITY && (run.m + 65504.f) * c > 160.f) {
+        if (run.m < INFINITY && (run.m + 65504.f) * factor > 160.f) {
             unsigned long long s = pack(0.f, 0.f), d = s;
-            const unsigned long long nm = pack(-run.m, -run.m);
+            const float k = c.far ? run.m : __fmul_rn(run.m, factor);
+            const unsigned long long less = pack(-k, -k);
+            auto add = [&](auto far) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                const uint32_t v = max2(x[q], 0xFBFFFBFFu);  // (-65504, -65504)
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
-                const unsigned long long e = mul2(add2(pack(f.x, f.y), nm), c2);
-                float e0, e1;
-                unpack(e, e0, e1);
-                const unsigned long long w = pack(ex2(e0), ex2(e1));
-                s = add2(s, w);
-                d = fma2(w, e, d);
-            }
+                for (int q = 0; q < 16; ++q) {
+                    const uint32_t v = max2(x[q], 0xFBFFFBFFu);  // (-65504, -65504)
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+                    const unsigned long long l = pack(f.x, f.y), e = decltype(far)::value ? mul2(add2(l, less), c2) : fma2(l, c2, less);
+                    float e0, e1;
+                    unpack(e, e0, e1);
+                    const unsigned long long w = pack(ex2(e0), ex2(e1));
+                    s = add2(s, w);
+                    d = fma2(w, e, d);
+                }
+            };
+            if (c.far)
+                add(std::true_type());
+            else
+                add(std::false_type());
             float p, q;
             unpack(s, p, q);
             run.s += p + q;
@@ -276,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
             for (int q = 0; q < 32; ++q) {
                 const uint32_t w = q & 1 ? x[q >> 1] >> 16 : x[q >> 1] & 0xFFFFu;
                 const float l = __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
-                const float e = run.m == INFINITY ? (l == run.m ? 0.f : -200.f) : (l - run.m) * c;
+                const float e = run.m == INFINITY ? (l == run.m ? 0.f : -200.f) : c.from(l, run.m);
                 const float y = l > -INFINITY ? ex2(e) : 0.f;
                 run.s += y;
                 run.d = y > 0.f ? fmaf(y, e, run.d) : run.d;
@@ -441,12 +493,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
     __syncthreads();
 
     const Sums all = sh.whole;
-    const float log_s = logf(all.s);  // (s = 0: nothing but masked logits)
+    const bool exact = c.far || !(fabsf(all.m) < INFINITY);
+    const float log_k = logf(all.s);  // (s = 0: nothing but masked logits)
+    const float log_s = exact ? log_k : log_k - 0.693147180559945309f * fmaf(all.m, factor, -__fmul_rn(all.m, factor));
     auto logprob = [&](float l) {
         if (!(l > -INFINITY) || (all.m == INFINITY && l != all.m)) return -INFINITY;  // (whatever the temperature)
         return (l == all.m ? 0.f : __fdiv_rn(l - all.m, temp)) - log_s;
     };
-    if (threadIdx.x == 0 && a.entropy) a.entropy[m] = all.s > 0.f ? log_s - all.d * 0.693147180559945309f / all.s : 0.f;
+    if (threadIdx.x == 0 && a.entropy) a.entropy[m] = all.s > 0.f ? log_k - all.d * 0.693147180559945309f / all.s : 0.f;
     if (static_cast<int>(threadIdx.x) < NG && static_cast<int>(threadIdx.x) < a.given) {
         const int64_t at = static_cast<int64_t>(m) * a.given + threadIdx.x;
         const int t = a.tokens[at];
