@@ -280,3 +280,26 @@ def test_two_host_threads(W):
     assert not errors
     for v in rows:
         assert torch.equal(got[v].top_tokens, wanted[v].top_tokens) and torch.equal(got[v].entropy, wanted[v].entropy)
+
+
+@pytest.mark.parametrize("M", [3, 700])
+@pytest.mark.parametrize("temperature", [0.0001, 0.0901, 0.0902, 0.5, 1.0, 20.0, 32.0, 150.0])
+def test_logits_far_from_zero(W, temperature, M):
+    """l / T up to millions, of which the differences are what counts: 60000 / 32 in fp32 is off by 2^-14 or so."""
+    rng = np.random.default_rng(15)
+    V = 4099
+    x = np.empty((M, V), np.float16)
+    x[0::3] = 60000 - 32.0 * rng.integers(0, 40, (len(x[0::3]), V))
+    x[1::3] = -33000 - 32.0 * rng.integers(0, 40, (len(x[1::3]), V))
+    x[2::3] = 2000 + 1.0 * rng.integers(0, 40, (len(x[2::3]), V))
+    check(W, x, rng.integers(0, V, (M, 2)), 5, [temperature] * M, rows=range(min(M, 9)))
+
+
+def test_rows_of_rising_logits(W):
+    """Every step brings a new largest one."""
+    x = torch.linspace(-40, 40, 40000, device="cuda").half().repeat(3, 1)
+    x[1] = x[1].flip(0)
+    x[2] = -65504 + 0.8 * 131008 * torch.linspace(0, 1, 40000, device="cuda")
+    t = np.array([[0, 39999, 20000]] * 3)
+    check(W, x, t, 8, [1.0, 0.8, 300.0])
+    check(W, x.repeat(250, 1), np.tile(t, (250, 1)), 8, [1.0, 0.8, 300.0] * 250, rows=[0, 1, 2, 749])
