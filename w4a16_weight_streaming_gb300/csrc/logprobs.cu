@@ -115,30 +115,6 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ unsigned long long pack(float lo, float hi) {
-    unsigned long long v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-    return v;
-}
-__device__ __forceinline__ void unpack(unsigned long long v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
-    unsigned long long d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
 // Exponents are those of 2, relative to the largest logit m: l c - k with k = m c rounded, one fused multiply-add a logit; what
 // the rounding of k makes of all weights is taken out at the end. Where k may be too large for that (`far`: T below 0.09),
 // (l - m) c.
@@ -245,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
     Sums run = {-INFINITY, 0.f, 0.f};
     float best = -INFINITY;  // of this thread's chunks, and the first that has it
     int best_chunk = -1;
-    const unsigned long long c2 = pack(factor, factor);
+    const unsigned long long c2 = pack_f2(factor, factor);
     const uint32_t slot = smem_u32(sh.next[warp]);
     bool copied = false;  // this step's chunks
     for (; base < c1; base += kThreads) {
@@ -298,20 +274,20 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
         }
         if (most > run.m) rescale(run, most, c);
         if (run.m < INFINITY && (run.m + 65504.f) * factor > 160.f) {
-            unsigned long long s = pack(0.f, 0.f), d = s;
+            unsigned long long s = pack_f2(0.f, 0.f), d = s;
             const float k = c.far ? run.m : __fmul_rn(run.m, factor);
-            const unsigned long long less = pack(-k, -k);
+            const unsigned long long less = pack_f2(-k, -k);
             auto add = [&](auto far) {
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const uint32_t v = max2(x[q], 0xFBFFFBFFu);  // (-65504, -65504)
                     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
-                    const unsigned long long l = pack(f.x, f.y), e = decltype(far)::value ? mul2(add2(l, less), c2) : fma2(l, c2, less);
+                    const unsigned long long l = pack_f2(f.x, f.y), e = decltype(far)::value ? mul_f2(add_f2(l, less), c2) : fma_f2(l, c2, less);
                     float e0, e1;
-                    unpack(e, e0, e1);
-                    const unsigned long long w = pack(ex2(e0), ex2(e1));
-                    s = add2(s, w);
-                    d = fma2(w, e, d);
+                    unpack_f2(e, e0, e1);
+                    const unsigned long long w = pack_f2(ex2(e0), ex2(e1));
+                    s = add_f2(s, w);
+                    d = fma_f2(w, e, d);
                 }
             };
             if (c.far)
@@ -319,9 +295,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
             else
                 add(std::false_type());
             float p, q;
-            unpack(s, p, q);
+            unpack_f2(s, p, q);
             run.s += p + q;
-            unpack(d, p, q);
+            unpack_f2(d, p, q);
             run.d += p + q;
         } else if (run.m > -INFINITY) {
 #pragma unroll
