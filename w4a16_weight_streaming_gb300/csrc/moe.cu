@@ -27,10 +27,10 @@
 // copies, whatever items they belong to. The runs are contiguous, so that a CTA meets few experts and finds the
 // rows of their tokens in L1.
 //
-// Measured on one GB300 (hidden 5120, 64 experts of 2176, 8 a token, group 128, in a CUDA graph): 1 token 42.5 us (139 MB,
-// 3.26 TB/s, 0.48 of the measured copy): 9 us of routing, list, starts and ends, then 20 warps an SM that wait for
+// Measured on one GB300 (hidden 5120, 64 experts of 2176, 8 a token, group 128, in a CUDA graph): 1 token 43 us (139 MB,
+// 3.23 TB/s, 0.48 of the measured copy): 9 us of routing, list, starts and ends, then 20 warps an SM that wait for
 // their first stages and for one another's items (7.2 items a CTA in gate_up, 8.4 in down: some have 8 and 9). 16 tokens
-// 191 us (974 MB, 5.1 TB/s, 0.75; gate_up alone 115 us, 5.7 TB/s): the stream without its products takes 181. 64 tokens
+// 193 us (974 MB, 5.0 TB/s, 0.75; gate_up alone 115 us, 5.7 TB/s): the stream without its products takes 181. 64 tokens
 // 272 us (1.1 GB, 4.1 TB/s, 0.60): a step's chain of loads, conversions and products at 3 warps a scheduler, with rows of
 // tokens from L2 (all tokens' rows the same one, in L1: 215; without the weights' stream 230); items of 128 columns at 8
 // warps, which read the tokens half as often, 284. A cluster of 2 or 4 CTAs with runs of steps in common was slower (46 us
@@ -557,7 +557,8 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
         // The list is the work of the kernel before the last: complete, since every CTA of the last one had passed its
         // wait before this kernel could start.
     }
-    {  // Every number within its limits: a workspace that was not zeroed, or that two calls share, gives wrong results only.
+    {  // Every number within its limits: a workspace that was not zeroed, or that two calls
+       // share, gives wrong results only (one token 0.7 us more, 16 tokens 2).
         const List* from = r.w.list;
         const int pairs = r.T * r.k, most = min(pairs, kMoeMaxExperts + kMaxPairs / 8);  // (no more entries than pairs)
         const int entries = max(1, min(__ldcg(&from->entries), most));
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(warps_for(NT) * 32, 1) experts_kernel(const Ma
     const int width = static_cast<int>(padded(m.K));
     auto meet = [&]() {  // the rows of an entry's tokens at step kb; a place without a token reads the first one's
         base = list.base[entry];
-        count = max(1, min(list.base[entry + 1] - base, 8 * NT));
+        count = list.base[entry + 1] - base;
         tiles = (count + 7) / 8;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
