@@ -451,7 +451,6 @@ int w4a16_logprobs(const uint16_t* logits, int64_t stride, int M, int V, const i
  *   gate:  NULL: 1. fp16: rows of H gate_stride apart (0: one row for all; else a multiple of 8), or, when gate_per_row
  *          is 1, one value a row, gate_stride apart (any)
  *   h_out: [M][H] of h's type, or NULL; may be h itself where h is dense.  x: fp16 [M][H], or NULL. One of them at least.
- * The weights must not be written by the kernel right before this call on its stream (they are read while it ends).
  * H % 8 == 0, H <= 32768, M <= 2^20; all 16-byte aligned but a gate of one value a row (2). These two calls and
  * w4a16_moe refuse memory of another GPU than the current one. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA.
  */

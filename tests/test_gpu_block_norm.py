@@ -152,3 +152,43 @@ def test_rows_further_apart_than_32_bits(W):
     _, y, w, p, _ = make(3, H, seed=5)
     check(W, h, y, w, post=p)
     check(W, y, h, w, post=p, gate=h)
+
+
+@pytest.mark.parametrize("H", [512, 5120])
+def test_weights_that_earlier_calls_write(W, H):
+    """Norm weights out of gemm, with a call of something else in between: every kernel here may start while the ones
+    before it still run, the weights are those of their own step all the same. check()'s bounds."""
+    K, steps = 8192, 24
+    g = torch.Generator("cuda").manual_seed(H)
+    codes = torch.randint(-2 ** 31, 2 ** 31, (K // 8, 2 * H), generator=g, device="cuda", dtype=torch.int32)
+    matrix = W.repack(codes, (0.002 * (1 + torch.rand((K // 128, 2 * H), generator=g, device="cuda"))).half().view(torch.int16))
+    inputs = torch.randn((steps, 1, K), generator=g, device="cuda").half()
+    h, y, *_ = make(3, H)
+    small = torch.randn((1, 64), generator=g, device="cuda").half()
+    both = torch.zeros((1, 2 * H), dtype=torch.float16, device="cuda")  # post_weight and weight, written anew every step
+    kept = torch.empty((steps, 2 * H), dtype=torch.float16, device="cuda")
+    outs = [(torch.empty_like(h), torch.empty_like(h)) for _ in range(steps)]
+    spare = (torch.empty_like(small), torch.empty_like(small))
+
+    def run():
+        for i in range(steps):
+            W.gemm(inputs[i], *matrix, 2 * H, K, y=both)
+            for _ in range(1 + i % 3):
+                W.block_norm(small, small, out=spare)
+            W.block_norm(h, y, weight=both[0, H:], post_weight=both[0, :H], offset=1.0, out=outs[i])
+            kept[i] = both[0]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        run()
+    both.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert W.w4a16_device_status() == W.OK
+    for i, out in enumerate(outs):
+        assert i == 0 or not torch.equal(kept[i], kept[i - 1])
+        check(W, h, y, kept[i, H:], post=kept[i, :H], offset=1.0, result=out)

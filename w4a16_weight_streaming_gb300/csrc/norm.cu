@@ -103,7 +103,7 @@ __global__ void __maxnreg__((registers_for<V, THREADS, F32>())) block_norm_kerne
     if (m >= a.M) return;
     constexpr bool kLate = THREADS == 512 && !F32;  // the next norm's weights when the sums' registers are free
     const int vecs = a.H / 8;
-    // the norms' weights do not come from the kernel before this one
+    griddep_wait();  // before any load: a norm's weights may be an earlier kernel's output as well
     uint4 pw[V], nw[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -112,7 +112,6 @@ __global__ void __maxnreg__((registers_for<V, THREADS, F32>())) block_norm_kerne
         if (v < vecs && a.post) pw[i] = *reinterpret_cast<const uint4*>(a.post + 8 * v);
         if (!kLate && v < vecs && a.weight) nw[i] = *reinterpret_cast<const uint4*>(a.weight + 8 * v);
     }
-    griddep_wait();
     uint4 hv[V][F32 ? 2 : 1], yv[V], gv[V];
     const unsigned char* hrow = a.h + m * a.h_stride * (F32 ? 4 : 2);
     float per_row = a.scale;
