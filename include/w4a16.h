@@ -494,8 +494,7 @@ size_t w4a16_moe_workspace_bytes(int experts, int hidden, int inner);
  *   y:       fp16 [tokens][hidden], written in full
  *   ids:     int32 [tokens][top_k], the chosen experts in order, or NULL; weights: fp32 [tokens][top_k], r, or NULL
  * No token bears on another's result but in the order of its sums (which follows the list of chosen experts): infinities
- * and NaN stay in their row. Repeats of a batch are bit-identical. The router and the experts' matrices must not be written
- * by the kernel right before this call on its stream (they are read while it ends).
+ * and NaN stay in their row. Repeats of a batch are bit-identical.
  * tokens <= 64, top_k <= 16 and <= experts. Four kernels. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
 int w4a16_moe(const uint16_t* x, int64_t x_stride, const w4a16_moe_experts* experts, const uint16_t* router, const float* bias,
               int top_k, int scoring, int renormalize, float scale, uint16_t* y, int32_t* ids, float* weights, int tokens,

@@ -360,3 +360,43 @@ def test_experts_with_every_load(W, T):
         bias = torch.randn(20, generator=g, device="cuda")
         bias[int(torch.randint(0, 20, (1,), generator=g, device="cuda"))] = 9.0
         check(W, L, L.x(T, seed=int(torch.randint(0, 99, (1,), generator=g, device="cuda"))), 5, sigmoid=True, bias=bias)
+
+
+@pytest.mark.parametrize("T", [1, 9])
+def test_a_router_that_earlier_calls_write(W, T):
+    """The router out of gemm, with a norm of something else in between: every kernel here may start while the ones before
+    it still run, the choice is that of its own step's router all the same."""
+    E, K, steps = 16, 8192, 24
+    L = Layer(W, E, 512, 128, 128, seed=15)
+    g = torch.Generator("cuda").manual_seed(15)
+    codes = torch.randint(-2 ** 31, 2 ** 31, (K // 8, 512), generator=g, device="cuda", dtype=torch.int32)
+    matrix = W.repack(codes, (0.0002 * (1 + torch.rand((K // 128, 512), generator=g, device="cuda"))).half().view(torch.int16))
+    rows = torch.randn((steps, E, K), generator=g, device="cuda").half()
+    x = L.x(T)
+    small = torch.randn((1, 64), generator=g, device="cuda").half()
+    spare = (torch.empty_like(small), torch.empty_like(small))
+    kept = torch.empty((steps, E, 512), dtype=torch.float16, device="cuda")
+    outs = [(torch.empty_like(x), torch.empty((T, 3), dtype=torch.int32, device="cuda"), torch.empty((T, 3), device="cuda")) for _ in range(steps)]
+
+    def run():
+        for i in range(steps):
+            W.gemm(rows[i], *matrix, 512, K, y=L.router)
+            for _ in range(1 + i % 3):
+                W.block_norm(small, small, out=spare)
+            W.moe(x, L.m, L.router, 3, L.work, out=outs[i])
+            kept[i] = L.router
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        run()
+    L.router.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert i == 0 or not torch.equal(kept[i], kept[i - 1])
+        L.router = kept[i]
+        check(W, L, x, 3, result=out)

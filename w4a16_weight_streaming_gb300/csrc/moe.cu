@@ -300,9 +300,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tokens = min(TB, a.T - t0), vecs = a.H / 8;
     const uint16_t* wrow = a.router + static_cast<int64_t>(e) * a.H;
+    griddep_wait();  // before any load: the router may be an earlier kernel's output as well
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
     if (static_cast<int>(threadIdx.x) < vecs) w = *reinterpret_cast<const uint4*>(wrow + 8 * threadIdx.x);
-    griddep_wait();
     float acc[TB][2];
 #pragma unroll
     for (int i = 0; i < TB; ++i) acc[i][0] = acc[i][1] = 0.f;
