@@ -400,3 +400,25 @@ def test_a_router_that_earlier_calls_write(W, T):
         assert i == 0 or not torch.equal(kept[i], kept[i - 1])
         L.router = kept[i]
         check(W, L, x, 3, result=out)
+
+
+@pytest.mark.parametrize("T", [1, 9])
+def test_a_nan_score_reaches_every_weight_that_it_is_summed_into(W, T):
+    L = Layer(W, 4, 128, 64, 64, seed=16)
+    x = L.x(T)
+    for value in (float("nan"), float("inf")):
+        L.router[2] = 0
+        L.router[2, 5] = value  # logits: NaN, or infinities of x's sign
+        for k, sigmoid, renormalize in ((4, False, True), (2, False, False), (4, True, True), (4, True, False)):
+            y, ids, w = W.moe(x, L.m, L.router, k, L.work, sigmoid=sigmoid, renormalize=renormalize)
+            torch.cuda.synchronize()
+            logits = x.double() @ L.router.double().T
+            score = torch.sigmoid(logits) if sigmoid else torch.softmax(logits, 1)
+            want = score.gather(1, ids.long())
+            if renormalize:  # (softmax over the chosen ones: all of them here)
+                want = want / want.sum(1, keepdim=True)
+            assert torch.equal(torch.isnan(w), torch.isnan(want)), (value, k, sigmoid, renormalize)
+            fine = ~torch.isnan(want)
+            # a logit of 128 products off by 2^-19 of sum|x router| (below 32 here): 2^-14; scores and weights by four times that at most
+            assert bool(((w.double() - want)[fine].abs() <= 2.0 ** -12 * want[fine]).all())
+            assert bool(torch.isnan(y).all(1)[torch.isnan(want).any(1)].all())

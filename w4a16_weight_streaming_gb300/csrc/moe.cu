@@ -196,7 +196,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     }
-    if (a.renormalize || !a.sigmoid) s = __fdiv_rn(s, fmaxf(all, 1e-30f));  // (sigmoids may all be 0)
+    if (a.renormalize || !a.sigmoid) s = all == 0.f ? 0.f : __fdiv_rn(s, all);  // (sigmoids may all be 0; a NaN goes on to all)
     if (lane < a.k) {
         const int p = t * a.k + lane;
         a.w.chosen[p] = static_cast<uint16_t>(mine);
