@@ -422,3 +422,29 @@ def test_a_nan_score_reaches_every_weight_that_it_is_summed_into(W, T):
             # a logit of 128 products off by 2^-19 of sum|x router| (below 32 here): 2^-14; scores and weights by four times that at most
             assert bool(((w.double() - want)[fine].abs() <= 2.0 ** -12 * want[fine]).all())
             assert bool(torch.isnan(y).all(1)[torch.isnan(want).any(1)].all())
+
+
+@pytest.mark.parametrize("highest", [0.0, -16.0, -24.0, -64.0, -80.0, -96.0, -256.0, -1280.0])
+def test_sigmoids_far_below_zero_share_what_there_is(W, highest):
+    """Logits are exact here (64 products of one number). Scores are within 2^-22 of themselves, their sum within 2^-20, so a
+    weight within 2^-19; scores below fp32's numbers beside one of e^-20 or more are 0: 2^-96 of the sum."""
+    L = Layer(W, 6, 64, 64, 64, seed=17)
+    x = torch.ones((9, 64), device="cuda").half()
+    logits = torch.tensor([highest - 16, highest, highest - 1, highest - 80, highest, -torch.inf], device="cuda")
+    L.router[:] = (logits / 64).half()[:, None]
+    L.router[5] = 0
+    L.router[5, 3] = -torch.inf
+    order = [1, 4, 2, 0, 3, 5]
+    for T in (1, 9):
+        for k in range(1, 7):
+            y, ids, w = W.moe(x[:T], L.m, L.router, k, L.work, sigmoid=True, scale=1.5, bias=torch.arange(0, -60, -10, device="cuda").float()[torch.tensor(order).argsort()])
+            torch.cuda.synchronize()
+            assert ids.tolist() == [order[:k]] * T
+            log_score = torch.nn.functional.logsigmoid(logits.double())[order[:k]]
+            want = 1.5 * torch.softmax(log_score, 0)
+            assert bool(((w.double() - want).abs() <= 2.0 ** -19 * want + 2.0 ** -95).all()), (k, w[0], want)
+            assert bool(torch.isfinite(y).all())
+    L.router[:] = L.router[5]  # nothing but -inf
+    y, ids, w = W.moe(x, L.m, L.router, 3, L.work, sigmoid=True)
+    torch.cuda.synchronize()
+    assert bool((w == 0).all()) and bool((y == 0).all())

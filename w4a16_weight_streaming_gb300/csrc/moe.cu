@@ -192,11 +192,17 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t) {
     }
     float s = lane < a.k ? (a.sigmoid ? 1.f / (1.f + expf(-value)) : expf(value - most)) : 0.f;
     if (a.renormalize) {
+        if (a.sigmoid) {  // far below 0 a sigmoid is e^l, and its share is the same relative to the largest chosen: no sum of tiny numbers
+            float top = lane < a.k ? value : -INFINITY;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (top < -20.f && top > -INFINITY) s = lane < a.k ? expf(value - top) : 0.f;  // (1 + e^l is 1 in fp32)
+        }
         all = s;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     }
-    if (a.renormalize || !a.sigmoid) s = all == 0.f ? 0.f : __fdiv_rn(s, all);  // (sigmoids may all be 0; a NaN goes on to all)
+    if (a.renormalize || !a.sigmoid) s = all == 0.f ? 0.f : __fdiv_rn(s, all);  // (sigmoids of -inf are 0; a NaN goes on to all)
     if (lane < a.k) {
         const int p = t * a.k + lane;
         a.w.chosen[p] = static_cast<uint16_t>(mine);
