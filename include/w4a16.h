@@ -461,7 +461,8 @@ int w4a16_block_norm(const void* h, int64_t h_stride, int h_f32, const uint16_t*
 /*
  * ---- A mixture-of-experts layer for a few tokens, where a dense layer has gate+up, w4a16_silu_mul and down.
  *   l[t][e] = x[t] . router[e];  score = softmax over e of l, or 1 / (1 + e^-l)
- *   chosen:  the top_k experts of a token with the largest l (sigmoid: score + bias); ties: the lower index, NaN last
+ *   chosen:  the top_k experts of a token with the largest l (sigmoid with a bias: score + bias in fp32); ties: the lower
+ *   index, NaN last
  *   r[t][e] = scale * score, with renormalize over the sum of the chosen ones' scores (a NaN among the scores that are summed
  *   makes all of the token's weights NaN; a sum of 0, from logits of -inf, makes them 0)
  *   a = fp16_rne(silu(x . Wg) * (x . Wu)), the products in fp32;  y[t] = fp16_rne(sum_e r * (a . Wd)), summed in

@@ -448,3 +448,22 @@ def test_sigmoids_far_below_zero_share_what_there_is(W, highest):
     y, ids, w = W.moe(x, L.m, L.router, 3, L.work, sigmoid=True)
     torch.cuda.synchronize()
     assert bool((w == 0).all()) and bool((y == 0).all())
+
+
+@pytest.mark.parametrize("logits", [[17.5, 18, 30, 100, 25, 18], [-90, -100, -96, -200, -89, -96], [200, -200, 90, -90, 17, -17]])
+def test_sigmoids_that_are_alike_in_fp32_are_chosen_by_their_logits(W, logits):
+    """Logits are exact here (64 products of one number)."""
+    L = Layer(W, 6, 64, 64, 64, seed=18)
+    x = torch.ones((9, 64), device="cuda").half()
+    L.router[:] = (torch.tensor(logits, device="cuda") / 64).half()[:, None]
+    order = sorted(range(6), key=lambda e: (-logits[e], e))
+    for T in (1, 9):
+        for k in (1, 2, 3, 6):
+            for renormalize in (False, True):
+                _, ids, w = W.moe(x[:T], L.m, L.router, k, L.work, sigmoid=True, renormalize=renormalize)
+                torch.cuda.synchronize()
+                assert ids.tolist() == [order[:k]] * T
+                log_score = torch.nn.functional.logsigmoid(torch.tensor(logits, dtype=torch.float64))[order[:k]]
+                want = torch.softmax(log_score, 0) if renormalize else log_score.exp()
+                # as above; a score itself below 2^-126 may be 0
+                assert bool(((w.double().cpu() - want).abs() <= 2.0 ** -19 * want + 2.0 ** -95).all())

@@ -1,7 +1,7 @@
 // A mixture-of-experts layer for a few tokens (T <= 64), its experts' weights in 4 bits:
 //
 //   l[t][e] = x[t] . router[e]                                     fp16 products, fp32 sums
-//   score   = softmax_e(l) or sigmoid(l); chosen: the k experts with the largest l, or score + bias
+//   score   = softmax_e(l) or sigmoid(l); chosen: the k experts with the largest l, or score + bias (sigmoid with a bias)
 //             (ties: the lower index); r[t][e] = score, over the sum of the chosen ones' if asked, times `scale`
 //   a[t][e] = fp16(silu(x[t] . Wg[e]) * (x[t] . Wu[e]))            for the chosen e, products kept in fp32
 //   y[t]    = fp16(sum_e r[t][e] * (a[t][e] . Wd[e]))              summed in the order of choice, in fp32
@@ -154,7 +154,8 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t) {
     for (int i = 0; i < kEach; ++i) {
         const int e = i * 32 + lane;
         most = fmaxf(most, l[i]);
-        key[i] = e < a.E ? order_of(a.sigmoid ? 1.f / (1.f + expf(-l[i])) + (a.bias ? __ldg(a.bias + e) : 0.f) : l[i]) : 0u;
+        // (without a bias the logits' own order: sigmoids above 17 are all 1 in fp32, below -88 all 0)
+        key[i] = e < a.E ? order_of(a.bias ? 1.f / (1.f + expf(-l[i])) + __ldg(a.bias + e) : l[i]) : 0u;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
