@@ -236,9 +236,15 @@ __device__ __forceinline__ void make_list(const RouteArgs& a, unsigned* status) 
     List& list = *a.w.list;
     for (int e = threadIdx.x; e < a.E; e += kRouteThreads) mask[0][e] = mask[1][e] = 0;
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += kRouteThreads) {
-        const int t = p / a.k;
-        atomicOr(&mask[t >> 5][min(static_cast<int>(__ldcg(a.w.chosen + p)), a.E - 1)], 1u << (t & 31));
+    // Read once: that every token's bit is set in its expert's mask is what keeps the places below within the list, also
+    // where another call on the same workspace changes `chosen` meanwhile (which is not allowed, and gives wrong results only).
+    int expert[kMaxPairs / kRouteThreads];
+#pragma unroll
+    for (int i = 0; i < kMaxPairs / kRouteThreads; ++i) {
+        const int p = i * kRouteThreads + static_cast<int>(threadIdx.x), t = p / a.k;
+        if (p >= pairs) continue;
+        expert[i] = min(static_cast<int>(__ldcg(a.w.chosen + p)), a.E - 1);
+        atomicOr(&mask[t >> 5][expert[i]], 1u << (t & 31));
     }
     uint32_t carry = 0;  // (entries << 16) + pairs of the experts before
     for (int e0 = 0; e0 < a.E; e0 += kRouteThreads) {
@@ -272,8 +278,10 @@ __device__ __forceinline__ void make_list(const RouteArgs& a, unsigned* status) 
         list.base[carry >> 16] = static_cast<uint16_t>(carry & 0xFFFFu);
     }
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += kRouteThreads) {  // an expert's pairs by token
-        const int t = p / a.k, e = min(static_cast<int>(__ldcg(a.w.chosen + p)), a.E - 1);
+#pragma unroll
+    for (int i = 0; i < kMaxPairs / kRouteThreads; ++i) {  // an expert's pairs by token
+        const int p = i * kRouteThreads + static_cast<int>(threadIdx.x), t = p / a.k, e = expert[i];
+        if (p >= pairs) continue;
         const uint32_t lo = mask[0][e], hi = mask[1][e], bit = 1u << (t & 31);
         const int at = start[e] + (t < 32 ? __popc(lo & (bit - 1)) : __popc(lo) + __popc(hi & (bit - 1)));
         if (!in_bounds(at < pairs, status)) continue;
