@@ -303,3 +303,41 @@ def test_rows_of_rising_logits(W):
     t = np.array([[0, 39999, 20000]] * 3)
     check(W, x, t, 8, [1.0, 0.8, 300.0])
     check(W, x.repeat(250, 1), np.tile(t, (250, 1)), 8, [1.0, 0.8, 300.0] * 250, rows=[0, 1, 2, 749])
+
+
+def listed_maxima(row, threads, parts, top):
+    """How many maxima of chunks of 32 each CTA of a row lists at first: those not below the top-th largest of its
+    threads' largest ones (a row on a 64-byte boundary; chunk i of a CTA is thread i % threads')."""
+    chunks = row.astype(np.float64).reshape(-1, 32).max(1)
+    per, counts = -(-len(chunks) // parts), []
+    for part in range(parts):
+        own = chunks[part * per:(part + 1) * per]
+        place = np.empty(len(own), np.int64)
+        place[np.argsort(-own, kind="stable")] = np.arange(len(own))
+        counts.append(int(np.sort([place[t::threads].min() for t in range(threads)])[top - 1]) + 1)
+    return counts
+
+
+@pytest.mark.parametrize("M,V,threads,parts", [(160, 1000000, 256, 1), (90, 1000000, 256, 2), (700, 248320, 128, 1)])
+@pytest.mark.parametrize("top", [32, 27])
+def test_rows_with_more_maxima_than_the_list_holds(W, M, V, threads, parts, top):
+    """top - 1 threads own every high chunk, so that the bound is a low one's and thousands of maxima pass it; the list of
+    1024 is filled and cut again, once or (values rising along the row) several times."""
+    chunk = np.arange(V // 32)
+    own = chunk % -(-len(chunk) // parts)  # within its CTA's part
+    high = own % threads < top - 1
+    n = np.cumsum(high)
+    rng = np.random.default_rng(V + top)
+    values = [8 + (n * 7919 % 1021) / 128, np.full(len(chunk), 12.5), 8 + 24 * n / n[-1], 32 - 24 * n / n[-1], np.where(n % 9 == 4, 20.0, 11 + (n % 4) / 4)]
+    rows = np.empty((len(values), V), np.float16)
+    for i, v in enumerate(values):
+        x = rng.normal(size=(len(chunk), 32)) - 4
+        x[high] = v[high, None] - 0.25 * rng.integers(0, 5, (high.sum(), 32))
+        x[high, rng.integers(0, 32, high.sum())] = v[high]
+        rows[i] = x.reshape(-1)
+        assert min(listed_maxima(rows[i], threads, parts, top)) > 1024
+    which = np.arange(M) % len(values)
+    x = torch.from_numpy(rows).cuda()[torch.from_numpy(which).cuda()]
+    tokens = rng.integers(0, V, (M, 2))
+    tokens[:, 0] = 32 * np.flatnonzero(high)[rng.integers(0, high.sum(), M)]
+    check(W, x, tokens, top, rows=[0, 1, 2, 3, 4, M - 1])
