@@ -98,3 +98,11 @@ def test_tensors_that_are_refused(W):
         W.block_norm(x, x)
     with pytest.raises(ValueError):
         W.Experts(torch.zeros((2, 8, 128), dtype=torch.int32), x, x, x)
+
+
+@pytest.mark.parametrize("shape", [(), (8,), (8, 128), (1, 2, 8, 128)])
+def test_experts_of_other_ranks_are_refused(W, shape):
+    m, s = torch.zeros(shape, dtype=torch.int32), torch.zeros((2, 1, 128), dtype=torch.float16)
+    for codes in ((m, m), (m, torch.zeros((2, 8, 64), dtype=torch.int32)), (torch.zeros((2, 8, 128), dtype=torch.int32), m)):
+        with pytest.raises(ValueError):
+            W.Experts(codes[0], s, codes[1], s)

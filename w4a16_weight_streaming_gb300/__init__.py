@@ -829,12 +829,12 @@ class Experts:
 
     def __init__(self, gate_up: torch.Tensor, gate_up_scales: torch.Tensor, down: torch.Tensor, down_scales: torch.Tensor,
                  group: int = 128, gate_up_scale: torch.Tensor | None = None, down_scale: torch.Tensor | None = None, stream=None):
+        if group <= 0 or not all(t.is_cuda and t.dim() == 3 and t.is_contiguous() for t in (gate_up, gate_up_scales, down, down_scales)):
+            _refuse("Experts", "gate_up, down and their scales must be contiguous CUDA tensors [E, rows, columns]")
         nvfp4 = gate_up_scale is not None
         E = gate_up.shape[0]
         self.experts, self.hidden, self.inner = E, gate_up.shape[1] * 8, gate_up.shape[2] // 2
         rows = 16 if nvfp4 else group
-        if group <= 0 or not all(t.is_cuda and t.dim() == 3 and t.is_contiguous() for t in (gate_up, gate_up_scales, down, down_scales)):
-            _refuse("Experts", "gate_up, down and their scales must be contiguous CUDA tensors [E, rows, columns]")
         half = (torch.uint8,) if nvfp4 else (torch.float16, torch.int16)
         if not (gate_up.dtype is torch.int32 and down.dtype is torch.int32 and gate_up_scales.dtype in half and down_scales.dtype in half
                 and gate_up.shape[2] == 2 * self.inner and tuple(down.shape) == (E, self.inner // 8, self.hidden)
