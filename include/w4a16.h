@@ -468,9 +468,9 @@ int w4a16_block_norm(const void* h, int64_t h_stride, int h_f32, const uint16_t*
  *   a = fp16_rne(silu(x . Wg) * (x . Wu)), the products in fp32;  y[t] = fp16_rne(sum_e r * (a . Wd)), summed in
  *   the order of choice
  * The experts' matrices are those of w4a16_repack (or w4a16_repack_nvfp4) one after another: gate_up [hidden, 2 inner]
- * with its columns in turns, 16 of gate and then the same 16 of up; down [inner, hidden]. A call reads each chosen
- * expert's weights once, whatever the tokens (an expert with many more tokens than the average again). Products are
- * within the bound of w4a16_gemm.
+ * with its columns in turns, 16 of gate and then the same 16 of up; down [inner, hidden]. A call reads an
+ * expert's weights once for every 8, 16 or 32 of its tokens (8 where the tokens' top_k choices are 3 an expert or fewer, 16
+ * up to 10). Products are within the bound of w4a16_gemm.
  */
 typedef struct {
     const void* gate_up_q;      /* experts * w4a16_repacked_qweight_bytes(2 inner, hidden, group) */

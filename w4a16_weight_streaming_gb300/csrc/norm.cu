@@ -11,9 +11,13 @@
 // neighbours of a vector in pairs, a thread's vectors in turn, then the warp and the warps in a fixed order.
 //
 // Measured on one GB300 (rows of 5120, in a CUDA graph): 8192 rows with a norm behind the block and a gate for every
-// element 65.0 us (419 MB, 6.45 TB/s, 0.95 of the measured copy), 1024 rows with an fp32 residual stream 9.8 us
-// (6.4 TB/s, 0.95): memory. 64 rows 2.6 us, one row 2.3: the latency of a launch, a round of loads and two sums. In scalar
-// fp32 with divisions and square roots for the two factors they took 71.8, 10.2, 2.85 and 2.6.
+// element 65.0 us (419 MB, 6.45 TB/s, 0.95 of the measured copy), 1024 rows with an fp32 residual stream 9.7 us
+// (6.5 TB/s, 0.96): memory. 64 rows 2.8 us, one row 2.6: the latency of a launch, a round of loads and two sums (0.2 of it
+// the norms' weights, which are loaded with the rest: a call before the last may still be writing them when this one
+// starts). Scalar fp32 with divisions and square roots for the two factors took 71.8 us for 8192 rows, 10.2 for 1024.
+//
+// Error of a factor: a sum of squares goes through 20 roundings of 2^-24 at most (4 in a vector's pairs and 1 to join them, 3 more
+// vectors, 5 in the warp, 5 among warps, 2 for mean and eps), half of that after the root, rsqrtf 2^-22, 4 in the products: below 2^-19.
 #include "common.cuh"
 #include "internal.h"
 
@@ -86,6 +90,7 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
 // Registers a thread. Where a CTA has one of many rows, more CTAs an SM are worth a few spilled registers (8192 rows of 5120,
 // fp16: 40 65.0 us, 48 64.1, 56 67.7; 4096 rows of 7168: 43.0, 48.5, 47.1; four vectors, 2048 rows of 16384: 64 52.7, 128
 // 59.4; with an fp32 stream two vectors, 8192 rows of 5120: 48 109, 64 78.3; four, 2048 rows of 16384: 64 105, 128 82.9).
+// Wider rows take 1024 threads and spill: 2048 rows of 32768 136.5 us (fp16, 3.9 TB/s) and 226 (fp32, 3.6 TB/s).
 template <int V, int THREADS, bool F32>
 constexpr int registers_for() {
     return THREADS == 1024 ? 64 : THREADS == 512 ? (V == 2 ? (F32 ? 64 : 40) : (F32 ? 128 : 64)) : 128;
