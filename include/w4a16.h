@@ -464,7 +464,7 @@ int w4a16_block_norm(const void* h, int64_t h_stride, int h_f32, const uint16_t*
  *   chosen:  the top_k experts of a token with the largest l (sigmoid with a bias: score + bias in fp32); ties: the lower
  *   index, NaN last
  *   r[t][e] = scale * score, with renormalize over the sum of the chosen ones' scores (a NaN among the scores that are summed
- *   makes all of the token's weights NaN; a sum of 0, from logits of -inf, makes them 0)
+ *   makes all of the token's weights NaN, as a logit of +inf does by softmax; sigmoids whose sum is 0, all of -inf, give 0)
  *   a = fp16_rne(silu(x . Wg) * (x . Wu)), the products in fp32;  y[t] = fp16_rne(sum_e r * (a . Wd)), summed in
  *   the order of choice
  * The experts' matrices are those of w4a16_repack (or w4a16_repack_nvfp4) one after another: gate_up [hidden, 2 inner]
